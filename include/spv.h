@@ -43,7 +43,9 @@ typedef enum {
     SPV_ERR_TIMEOUT = 5      /* a bounded device-side wait gave up (workspace word) */
 } spv_status;
 
-typedef enum { SPV_F32 = 0, SPV_BF16 = 1 } spv_dtype;
+/* Logits are SPV_F32 or SPV_BF16; the attention-side calls take SPV_BF16 or
+ * SPV_F16 activations and a cache of the same type or of SPV_E4M3. */
+typedef enum { SPV_F32 = 0, SPV_BF16 = 1, SPV_F16 = 2, SPV_E4M3 = 3 } spv_dtype;
 
 /* Limits of the library. */
 #define SPV_MAX_GAMMA 32     /* draft tokens per sequence */
@@ -54,6 +56,9 @@ typedef enum { SPV_F32 = 0, SPV_BF16 = 1 } spv_dtype;
 #define SPV_MAX_TRIALS 64    /* residual rejection trials before the direct draw */
 #define SPV_MAX_TOP_K 64     /* top_k of spv_verify_chain_filtered */
 #define SPV_MAX_TREE_NODES 64 /* nodes of a spv_verify_tree draft tree (root included) */
+#define SPV_MAX_NEW_TOKENS 64 /* T of spv_paged_attention and spv_attention_mass */
+#define SPV_MAX_EVICT_SLOTS 524288 /* budget and mass_stride of spv_kv_evict */
+#define SPV_MAX_GROUP 64      /* query heads per key head of spv_paged_attention and spv_attention_mass */
 
 /*
  * spv_verify_chain -- [SD] steps 3 and 4 for B independent sequences.
@@ -370,6 +375,179 @@ double spv_fanout_size(int F0, double a, double r, int k);
  * passed to spv_fanout_topk when every F_k <= SPV_MAX_FANOUT.
  */
 spv_status spv_fanout_sizes(int F0, double a, double r, int K, int V, int32_t *out);
+
+/* ------------------------------------------------------------------------
+ * The target model's attention layer around a verify step.  Per layer and
+ * step: spv_rope_append (rotary positions; keys and values into the paged
+ * cache), spv_paged_attention (the new tokens over the cache: T = 1 plain
+ * decode, gamma + 1 tokens of a chain, the nodes of a draft tree), then the
+ * verify call on the resulting logits, then spv_attention_mass (what each
+ * cached key received from the accepted tokens) and, when a cache has outgrown
+ * its budget, spv_kv_evict.  The pages have no counterpart.
+ *
+ * Paged cache: K and V are pools of `num_pages` pages of `page_size` slots (a
+ * power of two), each slot holding kv_heads rows of head_dim elements; the
+ * strides (in elements) of page, slot and head are free, a row's elements are
+ * contiguous.  Sequence b's slot j lies on page page_table[b, j / page_size]
+ * at j % page_size.  Entries of the table that no call needs may hold
+ * anything.  An e4m3 row stands for its elements times k_scale[h] /
+ * v_scale[h] (NULL: 1).  Sequence b has ctx_lens[b] cached slots and
+ * new_lens[b] new tokens (NULL: T each) at slots ctx_lens[b] + t.
+ *
+ * Sequences whose lengths are negative or beyond the table or T, or that need
+ * a page id outside [0, num_pages), do not stop a call: nothing outside the
+ * buffers is read or written, row_status[b] (optional) is SPV_ERR_BAD_ROW and
+ * each call says what its outputs then hold.
+ *
+ * All pointers of these calls are device memory but for the spv_kv_cache
+ * struct itself and what is marked HOST.  16-byte alignment: the pools, q, k,
+ * v and the outputs of their kind, and every stride in bytes.
+ */
+typedef struct {
+    void *k, *v;                /* device pools */
+    spv_dtype dtype;            /* SPV_BF16, SPV_F16 or SPV_E4M3 */
+    int32_t num_pages, page_size, kv_heads, head_dim;
+    int64_t k_page_stride, k_slot_stride, k_head_stride;
+    int64_t v_page_stride, v_slot_stride, v_head_stride;
+    const float *k_scale, *v_scale; /* [kv_heads], SPV_E4M3 only; NULL: 1 */
+} spv_kv_cache;
+
+/* Scalings of the rotary frequencies f_i = base^(-2 i / rotary_dim). */
+typedef enum {
+    SPV_ROPE_PLAIN = 0,
+    SPV_ROPE_LINEAR = 1,  /* f_i / factor */
+    SPV_ROPE_BASE = 2,    /* base * factor^(rotary_dim / (rotary_dim - 2)) */
+    SPV_ROPE_BY_PARTS = 3 /* g f_i + (1 - g) f_i / factor, g = clamp((n_i - low) / (high - low), 0, 1),
+                             n_i = original_len f_i / 2 pi (turns over the original length) */
+} spv_rope_scaling;
+
+/*
+ * spv_rope_frequencies -- the frequency table of spv_rope_append: entry i is
+ * f_i as a 64-bit fraction of a turn per position, round(f_i / (2 pi) 2^64)
+ * mod 2^64.  A position times an entry, wrapped at 64 bits, is the angle in
+ * turns reduced to one turn; the entry's own rounding is all that is off (at
+ * position p by p 2^-65 turns and the rounding of f_i in double), so angles
+ * of far positions lose nothing.
+ * Host function, no CUDA call.
+ *   rotary_dim   even, 2..1024; base > 0; factor > 0; BY_PARTS: low < high,
+ *                original_len > 0; BASE: rotary_dim > 2
+ *   out          rotary_dim / 2 uint64, HOST array
+ */
+spv_status spv_rope_frequencies(int rotary_dim, double base, int scaling, double factor, double low, double high,
+                                double original_len, uint64_t *out);
+
+/*
+ * spv_rope_append -- rotary positions for q and k, and k, v into the cache.
+ * With p = positions[b, t] (NULL: ctx_lens[b] + t), theta_i = p f_i:
+ *   (x_a, x_b) -> mscale (x_a cos theta_i - x_b sin theta_i, x_b cos theta_i + x_a sin theta_i),
+ * i < rotary_dim / 2, on the elements (i, i + rotary_dim / 2) of a head, or
+ * (2i, 2i + 1) if `interleaved`; elements from rotary_dim on pass unchanged.
+ * q goes to q_out, k (rotated) and v to slot ctx_lens[b] + t; for e4m3 divided
+ * by the head's scale, rounded to nearest even and saturated at +-448.
+ *   q [B, T, q_heads, D], k, v [B, T, kv_heads, D]: heads contiguous, strides
+ *   HOST array {q batch, q token, k batch, k token, v batch, v token} in
+ *   elements (NULL: contiguous); dtype SPV_BF16 or SPV_F16; the cache's dtype
+ *   the same or SPV_E4M3; D = head_dim, a multiple of 8 up to 512
+ *   freqs        [rotary_dim / 2] uint64 (spv_rope_frequencies), 0 <= rotary_dim <= D even
+ *   slot_pos     optional [B, kv_heads, pos_stride] int32: entry ctx_lens[b] + t
+ *                of every head is set to p (spv_kv_evict's pos)
+ *   q_out        [B, T, q_heads, D] contiguous; may be q itself when that is
+ *                contiguous
+ *   row_status   [B] optional
+ * Tokens t >= new_lens[b], and all of a bad sequence: q_out 0, nothing cached.
+ * Tokens on a bad page: q_out as usual, not cached.
+ */
+spv_status spv_rope_append(const void *q, const void *k, const void *v, spv_dtype dtype, const int64_t *strides, int B,
+                           int T, int q_heads, const uint64_t *freqs, int rotary_dim, int interleaved, float mscale,
+                           const int32_t *positions, const int32_t *ctx_lens, const int32_t *new_lens,
+                           const int32_t *page_table, int max_pages, const spv_kv_cache *cache, int32_t *slot_pos,
+                           int64_t pos_stride, void *q_out, int32_t *row_status, void *stream);
+
+/*
+ * spv_paged_attention -- attention of the new tokens over the paged cache,
+ * which already holds their own keys and values (spv_rope_append).  Token t
+ * of sequence b sees the slots j < ctx_lens[b] and, among the new tokens u at
+ * slot ctx_lens[b] + u: u <= t (parent NULL: a chain), or u = t and the
+ * ancestors of t in the tree parent[b, :], the array that spv_verify_tree
+ * takes (parent[b, 0] is not read).  Query head g belongs to key head
+ * g / (q_heads / kv_heads).  With s_j = scale k_scale[h] q . k_j over the
+ * visible slots:
+ *   out = v_scale[h] sum_j exp(s_j - m) v_j / sum_j exp(s_j - m),  lse = m + ln sum_j exp(s_j - m).
+ * A row that sees nothing, or only scores of minus infinity: out 0, lse minus
+ * infinity.  What lies in slots that a row does not see (NaN and infinities
+ * included) has no effect on it.
+ *   q, out       [B, T, q_heads, D] contiguous, SPV_BF16 or SPV_F16; D = head_dim 64, 128 or 256
+ *   parent       [B, T] int32, optional
+ *   1 <= T <= SPV_MAX_NEW_TOKENS; q_heads / kv_heads <= SPV_MAX_GROUP
+ *   lse          [B, T, q_heads] fp32, optional; row_status [B], optional
+ *   workspace    >= spv_attention_workspace_bytes(...) bytes, 256-byte
+ *                aligned, zero-filled once, as for spv_verify_chain; it does
+ *                not depend on the cached lengths
+ * Tokens t >= new_lens[b], and tree nodes whose path to the root has a parent
+ * outside [0, node): rows that see nothing.  Bad sequences: out and lse NaN.
+ * The result does not depend on the order in which the GPU runs the blocks.
+ */
+spv_status spv_paged_attention(const void *q, spv_dtype dtype, int B, int T, int q_heads, const spv_kv_cache *cache,
+                               const int32_t *page_table, int max_pages, const int32_t *ctx_lens,
+                               const int32_t *new_lens, const int32_t *parent, float scale, void *out, float *lse,
+                               int32_t *row_status, void *workspace, size_t workspace_bytes, void *stream);
+
+size_t spv_attention_workspace_bytes(int B, int T, int q_heads, int kv_heads, int head_dim);
+
+/*
+ * spv_attention_mass -- the attention weight that each cached key received
+ * from the tokens that stand after the verify step, added up over them and
+ * over the query heads of its key head:
+ *   mass_out[b, h, j] = decay mass_in[b, h, j] [j < ctx_lens[b]] + sum_{t counted, g in h} exp(s_j - lse[b, t, g])
+ * for j < ctx_lens[b] + new_lens[b]; further entries are not written.
+ * Counted tokens: t = 0 (the last emitted token) and the accepted ones,
+ * t = 1..accept_count[b] (chain), or nodes[b, 0..accept_count[b]-1] (tree);
+ * accept_count -1: none.  accept_count and nodes are what spv_verify_chain /
+ * spv_verify_tree wrote for drafts of T - 1 tokens / T nodes.
+ *   q, cache, page_table, ctx_lens, new_lens, parent, scale: as the
+ *   spv_paged_attention call that gave lse [B, T, q_heads]
+ *   nodes        [B, T] int32, optional
+ *   mass_in      [B, kv_heads, mass_stride] fp32, optional (NULL: 0);
+ *                may be mass_out; mass_stride >= the longest ctx + new
+ *   row_status   [B] optional
+ * Bad sequences (also: accept_count outside [-1, T - 1], a counted node
+ * outside [0, T), ctx + new > mass_stride): nothing is written; slots of a bad page: neither.
+ */
+spv_status spv_attention_mass(const void *q, spv_dtype dtype, int B, int T, int q_heads, const float *lse,
+                              const spv_kv_cache *cache, const int32_t *page_table, int max_pages,
+                              const int32_t *ctx_lens, const int32_t *new_lens, const int32_t *parent, float scale,
+                              const int32_t *accept_count, const int32_t *nodes, float decay, const float *mass_in,
+                              float *mass_out, int64_t mass_stride, int32_t *row_status, void *stream);
+
+/*
+ * spv_kv_evict -- cuts every sequence with lens[b] > budget back to `budget`
+ * slots, in place and for each key head by itself: kept are the entries with
+ * pos < sinks, the entries with pos > (largest pos) - recent, then those with
+ * the largest mass; among equals the lower slot (-0 equals 0, NaN is below
+ * everything).  The i-th evicted slot below `budget`, in ascending order,
+ * receives the i-th kept entry at or above it (K and V rows, mass, pos); the
+ * other kept entries stay where they are.  Attention does not depend on the
+ * order of the slots.  Pages shared with other sequences must be copied first.
+ *   lens         [B] int32; 1 <= budget
+ *   mass         [B, kv_heads, mass_stride] fp32
+ *   pos          same shape int32 (NULL: the slot is the position); >= 0 and
+ *                distinct within a head, else at least still memory-safe
+ *   sinks, recent >= 0, sinks + recent <= budget
+ *   mass_out     [B, kv_heads, out_stride] fp32, out_stride >= min(budget, mass_stride): the
+ *                kept entries' mass in their new slots; may be `mass` itself (same stride)
+ *   pos_out      likewise int32, optional
+ *   new_lens     [B] out: min(lens[b], budget)
+ *   slot_src     [B, kv_heads, budget] out: the slot that the entry came from, -1 from new_lens[b] on
+ *   row_status   [B] optional
+ * Entries of mass_out and pos_out from new_lens[b] on are not written.
+ * Bad sequences (lens[b] > mass_stride too): nothing moves, new_lens[b] is
+ * lens[b], slot_src -1; a row on a bad page is not copied.  Of the cache only the pools, sizes, strides and
+ * dtype are used (rows are copied as they are).
+ */
+spv_status spv_kv_evict(const spv_kv_cache *cache, const int32_t *page_table, int max_pages, int B,
+                        const int32_t *lens, int budget, int sinks, int recent, const float *mass, const int32_t *pos,
+                        int64_t mass_stride, float *mass_out, int32_t *pos_out, int64_t out_stride, int32_t *new_lens,
+                        int32_t *slot_src, int32_t *row_status, void *stream);
 
 /* Reads the device error word of a workspace (synchronises `stream`):
  * SPV_OK, or SPV_ERR_TIMEOUT if a bounded wait in an earlier call gave up. */

@@ -19,7 +19,7 @@ _PKG = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_PKG, "libspv.so")
 
 SPV_OK, SPV_ERR_INVALID_ARG, SPV_ERR_CUDA, SPV_ERR_UNSUPPORTED, SPV_ERR_BAD_ROW, SPV_ERR_TIMEOUT = range(6)
-SPV_F32, SPV_BF16 = 0, 1
+SPV_F32, SPV_BF16, SPV_F16, SPV_E4M3 = 0, 1, 2, 3
 SPV_MAX_GAMMA = 32
 SPV_MAX_FANOUT = 64
 SPV_MAX_FANOUT_ROWS = 64
@@ -28,6 +28,9 @@ SPV_SAMPLER_SUB = 32
 SPV_MAX_TRIALS = 64
 SPV_MAX_TOP_K = 64
 SPV_MAX_TREE_NODES = 64
+SPV_MAX_NEW_TOKENS = 64
+SPV_MAX_EVICT_SLOTS = 524288
+SPV_MAX_GROUP = 64
 SPV_NOALLOC_SCRATCH_BYTES = 4 * 1024 * 1024
 
 _lib = None
@@ -86,6 +89,19 @@ def load_library():
     lib.spv_workspace_status.restype = I
     lib.spv_status_string.argtypes = [I]
     lib.spv_status_string.restype = ctypes.c_char_p
+    L, F, Dbl = ctypes.c_int64, ctypes.c_float, ctypes.c_double
+    lib.spv_rope_frequencies.argtypes = [I, Dbl, I, Dbl, Dbl, Dbl, Dbl, P]
+    lib.spv_rope_frequencies.restype = I
+    lib.spv_rope_append.argtypes = [P, P, P, I, P, I, I, I, P, I, I, F, P, P, P, P, I, P, P, L, P, P, P]
+    lib.spv_rope_append.restype = I
+    lib.spv_attention_workspace_bytes.argtypes = [I, I, I, I, I]
+    lib.spv_attention_workspace_bytes.restype = S
+    lib.spv_paged_attention.argtypes = [P, I, I, I, I, P, P, I, P, P, P, F, P, P, P, P, S, P]
+    lib.spv_paged_attention.restype = I
+    lib.spv_attention_mass.argtypes = [P, I, I, I, I, P, P, P, I, P, P, P, F, P, P, F, P, P, L, P, P]
+    lib.spv_attention_mass.restype = I
+    lib.spv_kv_evict.argtypes = [P, P, I, I, P, I, I, I, P, P, L, P, P, L, P, P, P, P]
+    lib.spv_kv_evict.restype = I
     _lib = lib
     return lib
 
@@ -425,3 +441,7 @@ def spv_fanout_sizes(F0: int, a: float, r: float, K: int, V: int) -> list:
 
 
 fanout_sizes = spv_fanout_sizes
+
+from .kv import (  # noqa: E402  (the calls around the verify step; they use the helpers above)
+    KVCache, ROPE_SCALINGS, spv_attention_mass, spv_attention_workspace_bytes, spv_kv_evict, spv_paged_attention,
+    spv_rope_append, spv_rope_frequencies)

@@ -94,6 +94,65 @@ ChainLaunch chain_launch(const ChainArgs &a, void *ws);
 // Enqueues the call: the greedy kernels at T == 0, else the chain kernels.
 cudaError_t launch_chain_or_greedy(const ChainLaunch &L, cudaStream_t st);
 
+// The calls around the verify step (checked arguments, see spv.h).
+struct KvLaunch {
+    spv_kv_cache cache;
+    const int32_t *page_table;
+    int max_pages;
+    int B, T, q_heads;
+    spv_dtype dtype;
+    const int32_t *ctx_lens, *new_lens, *parent;
+    float scale;
+    int32_t *row_status;
+};
+struct RopeLaunch {
+    KvLaunch kv;
+    const void *q, *k, *v;
+    int64_t strides[6];
+    const uint64_t *freqs;
+    int rotary_dim, interleaved;
+    float mscale;
+    const int32_t *positions;
+    int32_t *slot_pos;
+    int64_t pos_stride;
+    void *q_out;
+};
+struct AttentionLaunch {
+    KvLaunch kv;
+    const void *q;
+    void *out;
+    float *lse;
+    void *ws;
+};
+struct MassLaunch {
+    KvLaunch kv;
+    const void *q;
+    const float *lse;
+    const int32_t *accept_count, *nodes;
+    float decay;
+    const float *mass_in;
+    float *mass_out;
+    int64_t mass_stride;
+};
+struct EvictLaunch {
+    KvLaunch kv;
+    const int32_t *lens;
+    int budget, sinks, recent;
+    const float *mass;
+    const int32_t *pos;
+    int64_t mass_stride;
+    float *mass_out;
+    int32_t *pos_out;
+    int64_t out_stride;
+    int32_t *new_lens, *slot_src;
+};
+inline int log2_of(int pow2)
+{
+    int s = 0;
+    while ((1 << s) < pow2) ++s;
+    return s;
+}
+
 size_t chain_ws_bytes(int B, int gamma, int V);
 size_t greedy_ws_bytes(int B, int gamma, int V);
 size_t fanout_ws_bytes(int B, int K1, int V, int Fmax);
@@ -106,5 +165,12 @@ cudaError_t launch_fanout(const FanoutLaunch &L, cudaStream_t st);
 cudaError_t launch_filtered(const ChainLaunch &L, cudaStream_t st);
 cudaError_t launch_selftest_wait(void *ws, unsigned polls, cudaStream_t st);
 cudaError_t launch_tree(const TreeLaunch &L, cudaStream_t st);
+
+size_t attention_ws_bytes(int B, int T, int q_heads, int kv_heads, int head_dim);
+struct PagedView paged_view(const KvLaunch &L);
+cudaError_t launch_rope(const RopeLaunch &L, cudaStream_t st);
+cudaError_t launch_attention(const AttentionLaunch &L, cudaStream_t st);
+cudaError_t launch_mass(const MassLaunch &L, cudaStream_t st);
+cudaError_t launch_evict(const EvictLaunch &L, cudaStream_t st);
 
 }  // namespace spv
