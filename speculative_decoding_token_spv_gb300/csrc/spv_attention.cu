@@ -24,22 +24,22 @@ struct AttParams {
     float *lse;
     const int32_t *parent;
     int32_t *row_status;
-    unsigned *arrived;  // per item, zero between calls
+    // Pieces of the item that begins in block i and ends in a later one (there is at most one) that are done; zero
+    // between calls.
+    unsigned *arrived;
     float *parts;       // [block][2] pieces: ATT_ROWS m, ATT_ROWS l, ATT_ROWS x D o
     int q_heads, group, rows;
     float scale_log2;
 };
 
 static int att_row_tiles(int T, int group) { return (T * group + ATT_ROWS - 1) / ATT_ROWS; }
-static size_t att_counter_bytes(int B, int T, int q_heads, int kv_heads)
-{
-    return align256(static_cast<size_t>(B) * kv_heads * att_row_tiles(T, q_heads / kv_heads) * sizeof(unsigned));
-}
+// Workspace: header, arrival counters, pieces.  The counters' place is the
+// same for every shape, so calls of different shapes can share a workspace.
+constexpr size_t ATT_PARTS_AT = (WS_HEADER + ATT_BLOCKS * sizeof(unsigned) + 255) / 256 * 256;
 
-size_t attention_ws_bytes(int B, int T, int q_heads, int kv_heads, int head_dim)
+size_t attention_ws_bytes(int, int, int, int, int head_dim)
 {
-    return WS_HEADER + att_counter_bytes(B, T, q_heads, kv_heads) +
-           static_cast<size_t>(ATT_BLOCKS) * 2 * ATT_ROWS * (head_dim + 2) * sizeof(float);
+    return ATT_PARTS_AT + static_cast<size_t>(ATT_BLOCKS) * 2 * ATT_ROWS * (head_dim + 2) * sizeof(float);
 }
 
 template <typename T, typename C, int D> __global__ void __launch_bounds__(ATT_THREADS) attention_kernel(const AttParams p)
@@ -156,7 +156,6 @@ template <typename T, typename C, int D> __global__ void __launch_bounds__(ATT_T
         __syncthreads();
         const bool any_bad = flag != 0;
         const bool whole = t0 == 0 && t1 == c.tiles;
-        const int item = (c.b * p.w.row_tiles + c.row_tile) * p.c.kv_heads + c.h;
         if (!whole) {
             float *part = p.parts + (static_cast<int64_t>(blockIdx.x) * 2 + (c.first < begin ? 0 : 1)) * PART;
             if (tid < R) {
@@ -172,11 +171,11 @@ template <typename T, typename C, int D> __global__ void __launch_bounds__(ATT_T
             __threadfence();
             __syncthreads();
             const int b0 = range_owner(c, c.first), b1 = range_owner(c, item_end - 1);
-            if (tid == 0) flag = atomicAdd(p.arrived + item, 1u) == static_cast<unsigned>(b1 - b0);
+            if (tid == 0) flag = atomicAdd(p.arrived + b0, 1u) == static_cast<unsigned>(b1 - b0);
             __syncthreads();
             if (!flag) continue;
             __threadfence();
-            if (tid == 0) p.arrived[item] = 0;
+            if (tid == 0) p.arrived[b0] = 0;
             // join the pieces in order
             if (tid < R) {
                 float m = -CUDART_INF_F;
@@ -258,9 +257,9 @@ cudaError_t launch_attention(const AttentionLaunch &L, cudaStream_t st)
     p.q_heads = k.q_heads;
     p.rows = k.T * p.group;
     p.scale_log2 = k.scale * LOG2E;
-    char *ws = static_cast<char *>(L.ws) + WS_HEADER;
-    p.arrived = reinterpret_cast<unsigned *>(ws);
-    p.parts = reinterpret_cast<float *>(ws + att_counter_bytes(k.B, k.T, k.q_heads, k.cache.kv_heads));
+    char *ws = static_cast<char *>(L.ws);
+    p.arrived = reinterpret_cast<unsigned *>(ws + WS_HEADER);
+    p.parts = reinterpret_cast<float *>(ws + ATT_PARTS_AT);
     const bool eight = k.cache.dtype == SPV_E4M3;
     const int D = k.cache.head_dim;
     if (k.dtype == SPV_BF16)

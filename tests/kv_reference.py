@@ -41,11 +41,16 @@ def make_cache(gen, lens, page, Hkv, D, kv, order="nhd", spare=2, width=None, ga
     return pools[0], pools[1], scales[0], scales[1], table
 
 
+def bits(pool):
+    """The pool's elements as integers (8-bit floats cannot be indexed on the CPU)."""
+    return pool.view(torch.int8 if pool.element_size() == 1 else torch.int16)
+
+
 def rows(pool, table_row, n):
     """Slots 0..n-1 of a sequence as float64 [n, Hkv, D]."""
     page = pool.shape[1]
     j = torch.arange(n)
-    return pool[table_row.long()[j // page], j % page].double()
+    return bits(pool)[table_row.long()[j // page], j % page].view(pool.dtype).double()
 
 
 def visible(t, ctx, n, parent):
