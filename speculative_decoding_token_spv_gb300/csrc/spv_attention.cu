@@ -1,20 +1,31 @@
 // spv_attention.cu -- attention of a sequence's new tokens over its paged
 // cache, in one pass over K and V.
 //
-// Mathematics: with scores in powers of two, s = q.k scale log2 e, a block
+// Mathematics: with scores in powers of two, s = q.k scale log2 e, a warp
 // keeps for each of its rows the running maximum m, l = sum 2^(s - m) and
-// o = sum 2^(s - m) v over the keys of its piece; pieces of one item join as
-// M = max m_i, l = sum l_i 2^(m_i - M), o likewise, out = o / l.  The last
-// block of an item to finish joins its pieces in their order along the
-// sequence, so the result does not depend on which block that is.
-#include "spv_kv.cuh"
+// o = sum 2^(s - m) v over the keys it takes; partial results join as
+// M = max m_i, l = sum l_i 2^(m_i - M), o likewise, out = o / l.
+//
+// What bounds it is reading K and V once.  The work is cut along the cache
+// (Work, Cursor), so the grid is the same for any lengths.  A block's four
+// warps take 16 keys each of a 64-key tile and share nothing until the end of
+// the piece: each has its own ring of K and V slices filled by asynchronous
+// copies, so that no warp waits for another and up to 190 KB an SM are on
+// their way.  All rows of a key head (new tokens x query heads of its group)
+// go through the tensor cores against the slice together, 16 or 32 of them.
+// Blocks leave what they have of an item in the workspace, and the last one
+// to do so joins the pieces in their order along the sequence: the result
+// does not depend on which block that is.
+#include "spv_mma.cuh"
 
 namespace spv {
 
-constexpr int ATT_BLOCKS = 4 * 152;  // blocks of the grid
-constexpr int ATT_ROWS = 16;         // query rows of a block's tile
-constexpr int ATT_KEYS = 64;         // keys of a tile
-constexpr int ATT_THREADS = 128;
+constexpr int ATT_WARPS = 4;
+constexpr int ATT_THREADS = 32 * ATT_WARPS;
+constexpr int ATT_KEYS = 16 * ATT_WARPS;  // keys of a tile: a slice for each warp
+constexpr int ATT_SMS = 152;
+constexpr int ATT_MAX_BLOCKS = 3 * ATT_SMS;
+constexpr int ATT_MAX_ROWS = 32;
 
 struct AttParams {
     PagedView c;
@@ -27,32 +38,73 @@ struct AttParams {
     // Pieces of the item that begins in block i and ends in a later one (there is at most one) that are done; zero
     // between calls.
     unsigned *arrived;
-    float *parts;       // [block][2] pieces: ATT_ROWS m, ATT_ROWS l, ATT_ROWS x D o
+    float *parts;  // [block][2] pieces: m and l of each row, then o
     int q_heads, group, rows;
     float scale_log2;
 };
 
-static int att_row_tiles(int T, int group) { return (T * group + ATT_ROWS - 1) / ATT_ROWS; }
 // Workspace: header, arrival counters, pieces.  The counters' place is the
 // same for every shape, so calls of different shapes can share a workspace.
-constexpr size_t ATT_PARTS_AT = (WS_HEADER + ATT_BLOCKS * sizeof(unsigned) + 255) / 256 * 256;
+constexpr size_t ATT_PARTS_AT = (WS_HEADER + ATT_MAX_BLOCKS * sizeof(unsigned) + 255) / 256 * 256;
 
 size_t attention_ws_bytes(int, int, int, int, int head_dim)
 {
-    return ATT_PARTS_AT + static_cast<size_t>(ATT_BLOCKS) * 2 * ATT_ROWS * (head_dim + 2) * sizeof(float);
+    return ATT_PARTS_AT + static_cast<size_t>(ATT_MAX_BLOCKS) * 2 * ATT_MAX_ROWS * (head_dim + 2) * sizeof(float);
 }
 
-template <typename T, typename C, int D> __global__ void __launch_bounds__(ATT_THREADS) attention_kernel(const AttParams p)
+// Sizes of a variant: MT tiles of 16 rows.
+template <typename C, int D, int MT> struct AttShape {
+    static constexpr int R = 16 * MT;
+    static constexpr int ROW_BYTES = D * static_cast<int>(sizeof(C));
+    static constexpr int SLICE = 16 * ROW_BYTES;
+    static constexpr int STAGES = SLICE >= 4096 ? 2 : 4;
+    static constexpr int RING = ATT_WARPS * STAGES * 2 * SLICE;
+    static constexpr int PAD = D + 8;  // row of the merge buffer: 8 rows on different banks
+    static constexpr int MERGE = ATT_WARPS * R * PAD * 4;
+    static constexpr int Q = R * D * 2;
+    static constexpr int SMEM = Q + (RING > MERGE ? RING : MERGE);
+    static constexpr int BLOCKS_PER_SM = SMEM * 3 <= 216 * 1024 ? 3 : SMEM * 2 <= 216 * 1024 ? 2 : 1;
+    static constexpr bool Q_IN_REGISTERS = MT == 1 && D <= 128;
+};
+
+template <typename T> __device__ __forceinline__ bool not_finite16(uint32_t two)
 {
-    constexpr int R = ATT_ROWS, KT = ATT_KEYS, PART = R * (D + 2);
-    constexpr int DPT = (D + ATT_THREADS - 1) / ATT_THREADS;  // output columns of a thread
-    __shared__ float qs[R][D];
-    __shared__ float ps[R][KT];
-    __shared__ float ms[R], ls[R], as[R];
-    __shared__ unsigned long long sees[64];
+    const uint32_t e = sizeof(T) == 1 ? 0 : std::is_same<T, __half>::value ? 0x7c00u : 0x7f80u;
+    return (two & e) == e || ((two >> 16) & e) == e;
+}
+// Whether a 16-byte chunk of the cache holds an infinity or NaN.
+template <typename C> __device__ __forceinline__ bool chunk_not_finite(uint4 x)
+{
+    const uint32_t w[4] = {x.x, x.y, x.z, x.w};
+    bool odd = false;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        if (sizeof(C) == 1) {  // e4m3 has no infinities; NaN is 0x7f and 0xff
+#pragma unroll
+            for (int k = 0; k < 4; ++k) odd |= ((w[i] >> (8 * k)) & 0x7fu) == 0x7fu;
+        } else {
+            odd |= not_finite16<C>(w[i]);
+        }
+    }
+    return odd;
+}
+
+template <typename T, typename C, int D, int MT>
+__global__ void __launch_bounds__(ATT_THREADS, AttShape<C, D, MT>::BLOCKS_PER_SM) attention_kernel(const AttParams p)
+{
+    using S = AttShape<C, D, MT>;
+    using M = typename MmaOf<T, C>::type;
+    constexpr int R = S::R, PART = R * (D + 2), NST = S::STAGES;
+    extern __shared__ __align__(1024) char smem[];
+    __shared__ float ms[ATT_WARPS][R], ls[ATT_WARPS][R];
+    __shared__ float q_unit[R];                // what a unit of the stored q row stands for
+    __shared__ unsigned long long sees[R];     // new tokens that each row sees; 0: a row that sees nothing
     __shared__ Cursor cur0;
     __shared__ int flag;
-    const int tid = threadIdx.x;
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    char *qs = smem;
+    float *merge = reinterpret_cast<float *>(smem + S::Q);
+    const uint32_t qs32 = smem_u32(qs), ring = smem_u32(smem + S::Q) + warp * (NST * 2 * S::SLICE);
     if (tid < 32) {
         const Cursor c = find_range(p.w, p.c, blockIdx.x, gridDim.x, tid);
         if (tid == 0) cur0 = c;
@@ -61,185 +113,361 @@ template <typename T, typename C, int D> __global__ void __launch_bounds__(ATT_T
     Cursor c = cur0;
     const long long begin = c.at;
     for (; c.at < c.end; next_item(c, p.w, p.c)) {
-        const int row0 = c.row_tile * R;
+        const int row0 = c.row_tile * R, live = min(R, p.rows - row0);
         const long long item_end = c.first + c.tiles;
         const int t0 = static_cast<int>(c.at - c.first);
-        const int t1 = static_cast<int>((c.end < item_end ? c.end : item_end) - c.first);
+        const int t1 = c.s.total > 0 ? static_cast<int>((c.end < item_end ? c.end : item_end) - c.first) : t0;
         const int32_t *table = p.c.table + static_cast<int64_t>(c.b) * p.c.max_pages;
-        __syncthreads();
-        if (tid == 0) flag = 0;
-        for (int t = tid; t < p.w.T; t += ATT_THREADS) sees[t] = visible_mask(p.parent ? p.parent + static_cast<int64_t>(c.b) * p.w.T : nullptr, t);
-        for (int i = tid; i < R * D; i += ATT_THREADS) {
-            const int r = i / D, d = i - r * D, t = (row0 + r) / p.group, g = (row0 + r) - t * p.group;
-            float x = 0.0f;
-            if (row0 + r < p.rows && t < c.s.fresh)
-                x = Num<T>::up(static_cast<const T *>(p.q)[((static_cast<int64_t>(c.b) * p.w.T + t) * p.q_heads + c.h * p.group + g) * D + d]);
-            qs[r][d] = x;
+        bool bad = c.s.bad;
+
+        // the first slices, as early as the page table allows
+        SliceSource src = find_slice(p.c, table, t0 * ATT_KEYS + warp * 16, t0 < t1 ? c.s.total : 0, lane, &bad);
+        auto issue = [&](int tile) {
+            if (tile < t1) {
+                const int j0 = tile * ATT_KEYS + warp * 16;
+                const uint32_t dst = ring + ((tile - t0) % NST) * (2 * S::SLICE);
+                copy_slice<S::ROW_BYTES>(p.c, p.c.k, src, j0, c.h, dst, lane);
+                copy_slice<S::ROW_BYTES>(p.c, p.c.v, src, j0, c.h, dst + S::SLICE, lane);
+                src = find_slice(p.c, table, j0 + ATT_KEYS, tile + 1 < t1 ? c.s.total : 0, lane, &bad);
+            }
+            cp_async_commit();
+        };
+#pragma unroll
+        for (int i = 0; i < NST - 1; ++i) issue(t0 + i);
+
+        // q of the tile's rows; for an e4m3 cache each row by a power of two into f16's range
+        for (int i = tid; i < R * (D / 8); i += ATT_THREADS) {
+            const int r = i / (D / 8), d = (i - r * (D / 8)) * 8, t = (row0 + r) / p.group, g = (row0 + r) - t * p.group;
+            float x[8];
+#pragma unroll
+            for (int e = 0; e < 8; ++e) x[e] = 0.0f;
+            if (r < live && t < c.s.fresh && !c.s.bad) {
+                const T *q = static_cast<const T *>(p.q) +
+                             ((static_cast<int64_t>(c.b) * p.w.T + t) * p.q_heads + c.h * p.group + g) * D + d;
+                const uint4 raw = *reinterpret_cast<const uint4 *>(q);
+                const T *y = reinterpret_cast<const T *>(&raw);
+#pragma unroll
+                for (int e = 0; e < 8; ++e) x[e] = Num<T>::up(y[e]);
+            }
+            if (sizeof(C) == 1) {
+                float top = 0.0f;
+#pragma unroll
+                for (int e = 0; e < 8; ++e) top = fabsf(x[e]) < CUDART_INF_F ? fmaxf(top, fabsf(x[e])) : top;
+#pragma unroll
+                for (int o = D / 16; o; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+                int e2 = 0;
+                if (top > 0.0f) e2 = 14 - ilogbf(top);  // the largest below 2^15
+                e2 = max(-120, min(120, e2));           // both scales normal numbers
+                const float up = exp2f(static_cast<float>(e2));
+#pragma unroll
+                for (int e = 0; e < 8; ++e) x[e] *= up;
+                if (d == 0) q_unit[r] = exp2f(static_cast<float>(-e2));
+            }
+            put_q8<M, C, D>(qs, r, d, x);
         }
         if (tid < R) {
-            ms[tid] = -CUDART_INF_F;
-            ls[tid] = 0.0f;
+            const int t = (row0 + tid) / p.group;
+            sees[tid] = tid < live && t < c.s.fresh && !c.s.bad
+                            ? visible_mask(p.parent ? p.parent + static_cast<int64_t>(c.b) * p.w.T : nullptr, t)
+                            : 0ull;
         }
-        float o[R][DPT];
-#pragma unroll
-        for (int r = 0; r < R; ++r)
-#pragma unroll
-            for (int e = 0; e < DPT; ++e) o[r][e] = 0.0f;
-        const float factor = p.scale_log2 * (p.c.k_scale ? __ldg(p.c.k_scale + c.h) : 1.0f);
-        bool bad = c.s.bad;
+        if (tid == 0) flag = 0;
         __syncthreads();
-        for (int tile = t0; tile < t1 && c.s.total > 0; ++tile) {
-            const int j0 = tile * KT;
-            const int j = j0 + tid % KT;
-            int page = -1;
-            if (j < c.s.total) {
-                page = page_of(p.c, table, j);
-                bad |= page < 0;
+
+        uint32_t qr[S::Q_IN_REGISTERS ? D / 16 : 1][4];
+        if (S::Q_IN_REGISTERS) {
+#pragma unroll
+            for (int ks = 0; ks < D / 16; ++ks) get_q<D>(qr[S::Q_IN_REGISTERS ? ks : 0], qs32, 0, ks, lane);
+        }
+        auto q_fragment = [&](int mt, int ks, uint32_t (&a)[4]) {
+            if (S::Q_IN_REGISTERS) {
+#pragma unroll
+                for (int i = 0; i < 4; ++i) a[i] = qr[S::Q_IN_REGISTERS ? ks : 0][i];
+            } else {
+                get_q<D>(a, qs32, mt, ks, lane);
             }
-            float acc[R / 2];
+        };
+        const float unit = p.scale_log2 * (p.c.k_scale ? __ldg(p.c.k_scale + c.h) : 1.0f);
+        float factor[MT][2], m[MT][2], l[MT][2], o[MT][D / 8][4];
 #pragma unroll
-            for (int r = 0; r < R / 2; ++r) acc[r] = 0.0f;
-            if (page >= 0) {
-                const C *k = reinterpret_cast<const C *>(row_ptr(p.c, p.c.k, page, j, c.h));
-                for (int d = 0; d < D; d += 4) {
-                    float x[4];
+        for (int mt = 0; mt < MT; ++mt) {
 #pragma unroll
-                    for (int e = 0; e < 4; ++e) x[e] = Num<C>::up(k[d + e]);
-#pragma unroll
-                    for (int r = 0; r < R / 2; ++r)
-#pragma unroll
-                        for (int e = 0; e < 4; ++e) acc[r] += x[e] * qs[(tid / KT) * (R / 2) + r][d + e];
-                }
+            for (int i = 0; i < 2; ++i) {
+                factor[mt][i] = sizeof(C) == 1 ? unit * q_unit[mt * 16 + i * 8 + (lane >> 2)] : unit;
+                m[mt][i] = -CUDART_INF_F;
+                l[mt][i] = 0.0f;
             }
 #pragma unroll
-            for (int r = 0; r < R / 2; ++r) {
-                const int row = (tid / KT) * (R / 2) + r, t = (row0 + row) / p.group;
-                bool seen = page >= 0 && row0 + row < p.rows && t < c.s.fresh;
-                if (seen) seen = sees[t] != 0 && (j < c.s.ctx || (sees[t] >> (j - c.s.ctx) & 1));
-                ps[row][tid % KT] = seen ? acc[r] * factor : -CUDART_INF_F;
-            }
-            __syncthreads();
-            if (tid < R) {
-                float m = ms[tid];
-                for (int i = 0; i < KT; ++i) m = fmaxf(m, ps[tid][i]);
-                const float m0 = m == -CUDART_INF_F ? 0.0f : m;
-                as[tid] = exp2f(ms[tid] - m0);
-                float l = ls[tid] * as[tid];
-                for (int i = 0; i < KT; ++i) {
-                    const float e = exp2f(ps[tid][i] - m0);
-                    ps[tid][i] = e;
-                    l += e;
-                }
-                ms[tid] = m;
-                ls[tid] = l;
-            }
-            __syncthreads();
+            for (int i = 0; i < D / 8; ++i)
 #pragma unroll
-            for (int e = 0; e < DPT; ++e) {
-                const int d = tid + e * ATT_THREADS;
-                if (d < D) {
+                for (int e = 0; e < 4; ++e) o[mt][i][e] = 0.0f;
+        }
+        for (int tile = t0; tile < t1; ++tile) {
+            __syncwarp();
+            issue(tile + NST - 1);
+            cp_async_wait<NST - 1>();
+            __syncwarp();
+            const int j0 = tile * ATT_KEYS + warp * 16;
+            if (j0 >= c.s.total) break;
+            const uint32_t stage = ring + ((tile - t0) % NST) * (2 * S::SLICE);
+            float s[MT][2][4];
+            slice_scores<M, C, D, MT>(s, stage, lane, q_fragment);
+            const bool tail = j0 + 16 > c.s.ctx;
+            uint32_t pf[MT][4];
 #pragma unroll
-                    for (int r = 0; r < R; ++r) o[r][e] *= as[r];
-                    for (int i = 0; i < KT && j0 + i < c.s.total; ++i) {
-                        const int pg = page_of(p.c, table, j0 + i);
-                        if (pg < 0) continue;
-                        const float v = Num<C>::up(reinterpret_cast<const C *>(row_ptr(p.c, p.c.v, pg, j0 + i, c.h))[d]);
+            for (int mt = 0; mt < MT; ++mt) {
 #pragma unroll
-                        for (int r = 0; r < R; ++r)
-                            if (ps[r][i] != 0.0f) o[r][e] += ps[r][i] * v;
+                for (int i = 0; i < 2; ++i)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) s[mt][i][e] *= factor[mt][e >> 1];
+                if (tail) {
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        const unsigned long long see = sees[mt * 16 + (e >> 1) * 8 + (lane >> 2)];
+#pragma unroll
+                        for (int i = 0; i < 2; ++i) {
+                            const int j = j0 + 8 * i + 2 * (lane & 3) + (e & 1);
+                            if (!(j < c.s.ctx || (j < c.s.total && (see >> (j - c.s.ctx) & 1)))) s[mt][i][e] = -CUDART_INF_F;
+                        }
                     }
                 }
-            }
-            __syncthreads();
-        }
-        if (bad) flag = 1;
-        __syncthreads();
-        const bool any_bad = flag != 0;
-        const bool whole = t0 == 0 && t1 == c.tiles;
-        if (!whole) {
-            float *part = p.parts + (static_cast<int64_t>(blockIdx.x) * 2 + (c.first < begin ? 0 : 1)) * PART;
-            if (tid < R) {
-                part[tid] = any_bad ? CUDART_NAN_F : ms[tid];
-                part[R + tid] = ls[tid];
-            }
+                float top[2];
+                bool moved = false;
 #pragma unroll
-            for (int e = 0; e < DPT; ++e) {
-                const int d = tid + e * ATT_THREADS;
-                if (d < D)
-                    for (int r = 0; r < R; ++r) part[2 * R + r * D + d] = o[r][e];
+                for (int i = 0; i < 2; ++i) {
+                    float x = fmaxf(fmaxf(s[mt][0][2 * i], s[mt][0][2 * i + 1]), fmaxf(s[mt][1][2 * i], s[mt][1][2 * i + 1]));
+                    x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 1));
+                    x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 2));
+                    top[i] = fmaxf(m[mt][i], x);
+                    moved |= top[i] > m[mt][i];
+                }
+                if (__any_sync(0xffffffffu, moved)) {
+#pragma unroll
+                    for (int i = 0; i < 2; ++i) {
+                        const float a = top[i] == -CUDART_INF_F ? 0.0f : fast_exp2(m[mt][i] - top[i]);
+                        m[mt][i] = top[i];
+                        l[mt][i] *= a;
+#pragma unroll
+                        for (int k = 0; k < D / 8; ++k) {
+                            o[mt][k][2 * i] *= a;
+                            o[mt][k][2 * i + 1] *= a;
+                        }
+                    }
+                }
+#pragma unroll
+                for (int i = 0; i < 2; ++i) {
+                    const float base = m[mt][i] == -CUDART_INF_F ? 0.0f : m[mt][i];
+#pragma unroll
+                    for (int k = 0; k < 2; ++k)
+#pragma unroll
+                        for (int e = 2 * i; e < 2 * i + 2; ++e) s[mt][k][e] = fast_exp2(s[mt][k][e] - base);
+                    l[mt][i] += (s[mt][0][2 * i] + s[mt][0][2 * i + 1]) + (s[mt][1][2 * i] + s[mt][1][2 * i + 1]);
+                }
+                // rounded to the cache's 16-bit type for the product (half a step of it each); l keeps 32 bits
+                pf[mt][0] = pack_mma<M>(s[mt][0][0], s[mt][0][1]);
+                pf[mt][1] = pack_mma<M>(s[mt][0][2], s[mt][0][3]);
+                pf[mt][2] = pack_mma<M>(s[mt][1][0], s[mt][1][1]);
+                pf[mt][3] = pack_mma<M>(s[mt][1][2], s[mt][1][3]);
             }
+            if (tail) {
+                // A new token's v may hold infinities or NaN that rows that do not see it must not meet as 0 x inf:
+                // such a key is added to the rows that see it here, and its v cleared before the product.
+                char *v = smem + S::Q + (stage - smem_u32(smem + S::Q)) + S::SLICE;
+                constexpr int CHUNKS = S::ROW_BYTES / 16;
+                unsigned odd = 0;
+                for (int i = lane; i < 16 * CHUNKS; i += 32) {
+                    const int row = i / CHUNKS;
+                    if (j0 + row >= c.s.ctx &&
+                        chunk_not_finite<C>(*reinterpret_cast<const uint4 *>(v + chunk_at<S::ROW_BYTES>(row, i % CHUNKS))))
+                        odd |= 1u << row;
+                }
+                odd = __reduce_or_sync(0xffffffffu, odd);
+                for (; odd; odd &= odd - 1) {
+                    const int row = __ffs(odd) - 1;
+#pragma unroll
+                    for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+                        for (int i = 0; i < 2; ++i) {
+                            // p of (row 8 i + lane / 4, key row): the quad's lane that holds column row % 8
+                            const float lo = __shfl_sync(0xffffffffu, row < 8 ? s[mt][0][2 * i] : s[mt][1][2 * i], (lane & ~3) | ((row & 7) >> 1));
+                            const float hi = __shfl_sync(0xffffffffu, row < 8 ? s[mt][0][2 * i + 1] : s[mt][1][2 * i + 1], (lane & ~3) | ((row & 7) >> 1));
+                            const float w = (row & 1) ? hi : lo;
+                            if (w != 0.0f) {
+#pragma unroll
+                                for (int k = 0; k < D / 8; ++k)
+#pragma unroll
+                                    for (int e = 0; e < 2; ++e) {
+                                        const int d = value_column<C>(k, e, lane) * static_cast<int>(sizeof(C));
+                                        o[mt][k][2 * i + e] += w * Num<C>::up(*reinterpret_cast<const C *>(
+                                                                       v + chunk_at<S::ROW_BYTES>(row, d >> 4) + (d & 15)));
+                                    }
+                            }
+                        }
+                    __syncwarp();
+                    for (int i = lane; i < CHUNKS; i += 32)
+                        *reinterpret_cast<uint4 *>(v + chunk_at<S::ROW_BYTES>(row, i)) = make_uint4(0, 0, 0, 0);
+                }
+                __syncwarp();
+            }
+            slice_values<M, C, D, MT>(o, pf, stage + S::SLICE, lane);
+        }
+        cp_async_wait<0>();
+
+        // the four warps' parts into one
+#pragma unroll
+        for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                float x = l[mt][i];
+                x += __shfl_xor_sync(0xffffffffu, x, 1);
+                x += __shfl_xor_sync(0xffffffffu, x, 2);
+                const int r = mt * 16 + i * 8 + (lane >> 2);
+                if ((lane & 3) == 0) {
+                    ms[warp][r] = sees[r] ? m[mt][i] : -CUDART_INF_F;
+                    ls[warp][r] = sees[r] ? x : 0.0f;
+                }
+            }
+        if (bad) flag = 1;
+        __syncthreads();  // the rings are free
+#pragma unroll
+        for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                const int r = mt * 16 + i * 8 + (lane >> 2);
+                if (r < live) {
+                    float *row = merge + (warp * R + r) * S::PAD;
+#pragma unroll
+                    for (int k = 0; k < D / 8; ++k)
+#pragma unroll
+                        for (int e = 0; e < 2; ++e) row[value_column<C>(k, e, lane)] = o[mt][k][2 * i + e];
+                }
+            }
+        const bool any_bad = flag != 0;
+        __syncthreads();
+        const bool whole = c.s.total == 0 || (t0 == 0 && t1 == c.tiles);
+        const float v_scale = p.c.v_scale ? __ldg(p.c.v_scale + c.h) : 1.0f;
+        float *part = p.parts + (static_cast<int64_t>(blockIdx.x) * 2 + (c.first < begin ? 0 : 1)) * PART;
+
+        // Row r's result: out = x / l, or what stands for it.
+        auto write_row = [&](int r, int d, float4 x, float mr, float lr) {
+            const int t = (row0 + r) / p.group, g = (row0 + r) - t * p.group;
+            const int64_t at = (static_cast<int64_t>(c.b) * p.w.T + t) * p.q_heads + c.h * p.group + g;
+            const bool nan = mr != mr, none = mr == -CUDART_INF_F && lr == 0.0f;
+            const float inv = v_scale / lr;
+            x.x *= inv, x.y *= inv, x.z *= inv, x.w *= inv;
+            if (none) x = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+            if (nan) x = make_float4(mr, mr, mr, mr);
+            *reinterpret_cast<uint2 *>(static_cast<T *>(p.out) + at * D + d) =
+                make_uint2(pack_mma<T>(x.x, x.y), pack_mma<T>(x.z, x.w));
+            if (d == 0 && p.lse) p.lse[at] = nan ? mr : none ? -CUDART_INF_F : LN2 * (mr + log2f(lr));
+        };
+        for (int i = tid; i < live * (D / 4); i += ATT_THREADS) {
+            const int r = i / (D / 4), d = (i - r * (D / 4)) * 4;
+            float mr = ms[0][r];
+#pragma unroll
+            for (int w = 1; w < ATT_WARPS; ++w) mr = fmaxf(mr, ms[w][r]);
+            const float base = mr == -CUDART_INF_F ? 0.0f : mr;
+            float lr = 0.0f;
+            float4 x = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+#pragma unroll
+            for (int w = 0; w < ATT_WARPS; ++w) {
+                const float a = fast_exp2(ms[w][r] - base);
+                const float4 y = *reinterpret_cast<const float4 *>(merge + (w * R + r) * S::PAD + d);
+                if (ls[w][r] != 0.0f) {  // a warp without keys has nothing to add
+                    lr += a * ls[w][r];
+                    x.x += a * y.x, x.y += a * y.y, x.z += a * y.z, x.w += a * y.w;
+                }
+            }
+            if (any_bad) mr = CUDART_NAN_F;
+            if (whole) {
+                write_row(r, d, x, mr, lr);
+            } else {
+                if (d == 0) {
+                    part[r] = mr;
+                    part[R + r] = lr;
+                }
+                *reinterpret_cast<float4 *>(part + 2 * R + r * D + d) = x;
+            }
+        }
+        bool seq_bad = any_bad;
+        if (!whole) {
             __threadfence();
             __syncthreads();
             const int b0 = range_owner(c, c.first), b1 = range_owner(c, item_end - 1);
-            if (tid == 0) flag = atomicAdd(p.arrived + b0, 1u) == static_cast<unsigned>(b1 - b0);
+            if (tid == 0) {
+                const bool last = atomicAdd(p.arrived + b0, 1u) == static_cast<unsigned>(b1 - b0);
+                if (last) p.arrived[b0] = 0;
+                flag = last;
+            }
             __syncthreads();
-            if (!flag) continue;
+            if (!flag) {
+                __syncthreads();
+                continue;
+            }
             __threadfence();
-            if (tid == 0) p.arrived[b0] = 0;
-            // join the pieces in order
-            if (tid < R) {
-                float m = -CUDART_INF_F;
+            // piece b0 lies in its block's second place, the others in their first
+            auto piece = [&](int i) { return p.parts + (static_cast<int64_t>(i) * 2 + (i == b0 ? 1 : 0)) * PART; };
+            for (int r = warp; r < live; r += ATT_WARPS) {
+                float mr = -CUDART_INF_F, lr = 0.0f;
                 bool nan = false;
-                for (int i = b0; i <= b1; ++i) {
-                    const float x = p.parts[(static_cast<int64_t>(i) * 2 + (c.first < range_begin(c, i) ? 0 : 1)) * PART + tid];
+                for (int i = b0 + lane; i <= b1; i += 32) {
+                    const float x = __ldcg(piece(i) + r);
                     nan |= x != x;
-                    m = fmaxf(m, x);
+                    mr = fmaxf(mr, x);
                 }
-                const float m0 = m == -CUDART_INF_F ? 0.0f : m;
-                float l = 0.0f;
-                for (int i = b0; i <= b1; ++i) {
-                    const float *x = p.parts + (static_cast<int64_t>(i) * 2 + (c.first < range_begin(c, i) ? 0 : 1)) * PART;
-                    l += x[R + tid] * exp2f(x[tid] - m0);
+                mr = warp_max(mr);
+                nan = __any_sync(0xffffffffu, nan);
+                const float base = mr == -CUDART_INF_F ? 0.0f : mr;
+                for (int i = b0 + lane; i <= b1; i += 32) lr += __ldcg(piece(i) + R + r) * fast_exp2(__ldcg(piece(i) + r) - base);
+                lr = warp_sum(lr);
+                if (lane == 0) {
+                    ms[0][r] = nan ? CUDART_NAN_F : mr;
+                    ls[0][r] = lr;
                 }
-                ms[tid] = nan ? CUDART_NAN_F : m;
-                ls[tid] = l;
             }
             __syncthreads();
-#pragma unroll
-            for (int e = 0; e < DPT; ++e) {
-                const int d = tid + e * ATT_THREADS;
-                if (d < D)
-                    for (int r = 0; r < R; ++r) {
-                        const float m0 = ms[r] == -CUDART_INF_F ? 0.0f : ms[r];
-                        float x = 0.0f;
-                        for (int i = b0; i <= b1; ++i) {
-                            const float *y = p.parts + (static_cast<int64_t>(i) * 2 + (c.first < range_begin(c, i) ? 0 : 1)) * PART;
-                            x += y[2 * R + r * D + d] * exp2f(y[r] - m0);
-                        }
-                        o[r][e] = x;
-                    }
+            for (int i = tid; i < live * (D / 4); i += ATT_THREADS) {
+                const int r = i / (D / 4), d = (i - r * (D / 4)) * 4;
+                const float mr = ms[0][r], base = mr == -CUDART_INF_F ? 0.0f : mr;
+                float4 x = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+#pragma unroll 4
+                for (int k = b0; k <= b1; ++k) {
+                    const float a = fast_exp2(__ldcg(piece(k) + r) - base);
+                    const float4 y = __ldcg(reinterpret_cast<const float4 *>(piece(k) + 2 * R + r * D + d));
+                    x.x += a * y.x, x.y += a * y.y, x.z += a * y.z, x.w += a * y.w;
+                }
+                write_row(r, d, x, mr, ls[0][r]);
             }
-        } else {
-            if (any_bad && tid < R) ms[tid] = CUDART_NAN_F;
-            __syncthreads();
+            seq_bad = ms[0][0] != ms[0][0];
         }
-        const float v_scale = p.c.v_scale ? __ldg(p.c.v_scale + c.h) : 1.0f;
-        for (int r = 0; r < R; ++r) {
-            if (row0 + r >= p.rows) break;
-            const int t = (row0 + r) / p.group, g = (row0 + r) - t * p.group;
-            const int64_t at = (static_cast<int64_t>(c.b) * p.w.T + t) * p.q_heads + c.h * p.group + g;
-            const float m = ms[r], l = ls[r];
-            const bool nan = m != m, none = m == -CUDART_INF_F && l == 0.0f;
-#pragma unroll
-            for (int e = 0; e < DPT; ++e) {
-                const int d = tid + e * ATT_THREADS;
-                if (d < D) static_cast<T *>(p.out)[at * D + d] = Num<T>::down(nan ? CUDART_NAN_F : none ? 0.0f : o[r][e] / l * v_scale);
-            }
-            if (tid == 0 && p.lse) p.lse[at] = nan ? CUDART_NAN_F : none ? -CUDART_INF_F : LN2 * (m + log2f(l));
-        }
-        if (tid == 0 && p.row_status && c.h == 0 && c.row_tile == 0) p.row_status[c.b] = ms[0] != ms[0] ? KV_STATUS_BAD : 0;
+        if (tid == 0 && p.row_status && c.h == 0 && c.row_tile == 0) p.row_status[c.b] = seq_bad ? KV_STATUS_BAD : 0;
+        __syncthreads();
     }
 }
 
-template <typename T, typename C> static cudaError_t launch_dim(const AttParams &p, int D, cudaStream_t st)
+template <typename T, typename C, int D, int MT> static cudaError_t launch_rows(const AttParams &p, cudaStream_t st)
 {
-    if (D == 64)
-        attention_kernel<T, C, 64><<<ATT_BLOCKS, ATT_THREADS, 0, st>>>(p);
-    else if (D == 128)
-        attention_kernel<T, C, 128><<<ATT_BLOCKS, ATT_THREADS, 0, st>>>(p);
-    else
-        attention_kernel<T, C, 256><<<ATT_BLOCKS, ATT_THREADS, 0, st>>>(p);
+    using S = AttShape<C, D, MT>;
+    auto kernel = attention_kernel<T, C, D, MT>;
+    const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, S::SMEM);
+    if (e != cudaSuccess) return e;
+    kernel<<<ATT_SMS * S::BLOCKS_PER_SM, ATT_THREADS, S::SMEM, st>>>(p);
     return cudaGetLastError();
+}
+template <typename T, typename C, int D> static cudaError_t launch_dim(AttParams &p, cudaStream_t st)
+{
+    // 32 rows at a time halve the re-reading of K and V where there are more than 16; at D = 256 their sums would
+    // not fit the registers
+    const bool two = p.rows > 16 && D <= 128;
+    p.w.row_tiles = (p.rows + (two ? 31 : 15)) / (two ? 32 : 16);
+    if (two) return launch_rows<T, C, D, D <= 128 ? 2 : 1>(p, st);
+    return launch_rows<T, C, D, 1>(p, st);
+}
+template <typename T, typename C> static cudaError_t launch_types(AttParams &p, int D, cudaStream_t st)
+{
+    if (D == 64) return launch_dim<T, C, 64>(p, st);
+    if (D == 128) return launch_dim<T, C, 128>(p, st);
+    return launch_dim<T, C, 256>(p, st);
 }
 
 cudaError_t launch_attention(const AttentionLaunch &L, cudaStream_t st)
@@ -248,7 +476,7 @@ cudaError_t launch_attention(const AttentionLaunch &L, cudaStream_t st)
     AttParams p{};
     p.c = paged_view(k);
     p.group = k.q_heads / k.cache.kv_heads;
-    p.w = Work{k.B, k.T, att_row_tiles(k.T, p.group), ATT_KEYS, k.ctx_lens, k.new_lens, false};
+    p.w = Work{k.B, k.T, 1, ATT_KEYS, k.ctx_lens, k.new_lens, false};
     p.q = L.q;
     p.out = L.out;
     p.lse = L.lse;
@@ -263,8 +491,9 @@ cudaError_t launch_attention(const AttentionLaunch &L, cudaStream_t st)
     const bool eight = k.cache.dtype == SPV_E4M3;
     const int D = k.cache.head_dim;
     if (k.dtype == SPV_BF16)
-        return eight ? launch_dim<__nv_bfloat16, __nv_fp8_e4m3>(p, D, st) : launch_dim<__nv_bfloat16, __nv_bfloat16>(p, D, st);
-    return eight ? launch_dim<__half, __nv_fp8_e4m3>(p, D, st) : launch_dim<__half, __half>(p, D, st);
+        return eight ? launch_types<__nv_bfloat16, __nv_fp8_e4m3>(p, D, st)
+                     : launch_types<__nv_bfloat16, __nv_bfloat16>(p, D, st);
+    return eight ? launch_types<__half, __nv_fp8_e4m3>(p, D, st) : launch_types<__half, __half>(p, D, st);
 }
 
 }  // namespace spv
