@@ -16,32 +16,14 @@
 // Blocks leave what they have of an item in the workspace, and the last one
 // to do so joins the pieces in their order along the sequence: the result
 // does not depend on which block that is.
-#include "spv_mma.cuh"
+#include "spv_attention.cuh"
 
 namespace spv {
 
 constexpr int ATT_WARPS = 4;
 constexpr int ATT_THREADS = 32 * ATT_WARPS;
 constexpr int ATT_KEYS = 16 * ATT_WARPS;  // keys of a tile: a slice for each warp
-constexpr int ATT_SMS = 152;
-constexpr int ATT_MAX_BLOCKS = 3 * ATT_SMS;
 constexpr int ATT_MAX_ROWS = 32;
-
-struct AttParams {
-    PagedView c;
-    Work w;
-    const void *q;
-    void *out;
-    float *lse;
-    const int32_t *parent;
-    int32_t *row_status;
-    // Pieces of the item that begins in block i and ends in a later one (there is at most one) that are done; zero
-    // between calls.
-    unsigned *arrived;
-    float *parts;  // [block][2] pieces: m and l of each row, then o
-    int q_heads, group, rows;
-    float scale_log2;
-};
 
 // Workspace: header, arrival counters, pieces.  The counters' place is the
 // same for every shape, so calls of different shapes can share a workspace.
@@ -49,7 +31,9 @@ constexpr size_t ATT_PARTS_AT = (WS_HEADER + ATT_MAX_BLOCKS * sizeof(unsigned) +
 
 size_t attention_ws_bytes(int, int, int, int, int head_dim)
 {
-    return ATT_PARTS_AT + static_cast<size_t>(ATT_MAX_BLOCKS) * 2 * ATT_MAX_ROWS * (head_dim + 2) * sizeof(float);
+    const size_t few = static_cast<size_t>(ATT_MAX_BLOCKS) * 2 * ATT_MAX_ROWS * (head_dim + 2);
+    const size_t many = attention_rows_part_floats(head_dim);
+    return ATT_PARTS_AT + (few > many ? few : many) * sizeof(float);
 }
 
 // Sizes of a variant: MT tiles of 16 rows.
@@ -66,28 +50,6 @@ template <typename C, int D, int MT> struct AttShape {
     static constexpr int BLOCKS_PER_SM = SMEM * 3 <= 216 * 1024 ? 3 : SMEM * 2 <= 216 * 1024 ? 2 : 1;
     static constexpr bool Q_IN_REGISTERS = MT == 1 && D <= 128;
 };
-
-template <typename T> __device__ __forceinline__ bool not_finite16(uint32_t two)
-{
-    const uint32_t e = sizeof(T) == 1 ? 0 : std::is_same<T, __half>::value ? 0x7c00u : 0x7f80u;
-    return (two & e) == e || ((two >> 16) & e) == e;
-}
-// Whether a 16-byte chunk of the cache holds an infinity or NaN.
-template <typename C> __device__ __forceinline__ bool chunk_not_finite(uint4 x)
-{
-    const uint32_t w[4] = {x.x, x.y, x.z, x.w};
-    bool odd = false;
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        if (sizeof(C) == 1) {  // e4m3 has no infinities; NaN is 0x7f and 0xff
-#pragma unroll
-            for (int k = 0; k < 4; ++k) odd |= ((w[i] >> (8 * k)) & 0x7fu) == 0x7fu;
-        } else {
-            odd |= not_finite16<C>(w[i]);
-        }
-    }
-    return odd;
-}
 
 template <typename T, typename C, int D, int MT>
 __global__ void __launch_bounds__(ATT_THREADS, AttShape<C, D, MT>::BLOCKS_PER_SM) attention_kernel(const AttParams p)
@@ -348,19 +310,7 @@ __global__ void __launch_bounds__(ATT_THREADS, AttShape<C, D, MT>::BLOCKS_PER_SM
         const float v_scale = p.c.v_scale ? __ldg(p.c.v_scale + c.h) : 1.0f;
         float *part = p.parts + (static_cast<int64_t>(blockIdx.x) * 2 + (c.first < begin ? 0 : 1)) * PART;
 
-        // Row r's result: out = x / l, or what stands for it.
-        auto write_row = [&](int r, int d, float4 x, float mr, float lr) {
-            const int t = (row0 + r) / p.group, g = (row0 + r) - t * p.group;
-            const int64_t at = (static_cast<int64_t>(c.b) * p.w.T + t) * p.q_heads + c.h * p.group + g;
-            const bool nan = mr != mr, none = mr == -CUDART_INF_F && lr == 0.0f;
-            const float inv = v_scale / lr;
-            x.x *= inv, x.y *= inv, x.z *= inv, x.w *= inv;
-            if (none) x = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-            if (nan) x = make_float4(mr, mr, mr, mr);
-            *reinterpret_cast<uint2 *>(static_cast<T *>(p.out) + at * D + d) =
-                make_uint2(pack_mma<T>(x.x, x.y), pack_mma<T>(x.z, x.w));
-            if (d == 0 && p.lse) p.lse[at] = nan ? mr : none ? -CUDART_INF_F : LN2 * (mr + log2f(lr));
-        };
+        const AttRows rows{c.b, c.h, row0, live};
         for (int i = tid; i < live * (D / 4); i += ATT_THREADS) {
             const int r = i / (D / 4), d = (i - r * (D / 4)) * 4;
             float mr = ms[0][r];
@@ -380,7 +330,7 @@ __global__ void __launch_bounds__(ATT_THREADS, AttShape<C, D, MT>::BLOCKS_PER_SM
             }
             if (any_bad) mr = CUDART_NAN_F;
             if (whole) {
-                write_row(r, d, x, mr, lr);
+                write_row<T, D>(p, rows, r, d, x, mr, lr, v_scale);
             } else {
                 if (d == 0) {
                     part[r] = mr;
@@ -391,53 +341,8 @@ __global__ void __launch_bounds__(ATT_THREADS, AttShape<C, D, MT>::BLOCKS_PER_SM
         }
         bool seq_bad = any_bad;
         if (!whole) {
-            __threadfence();
-            __syncthreads();
-            const int b0 = range_owner(c, c.first), b1 = range_owner(c, item_end - 1);
-            if (tid == 0) {
-                const bool last = atomicAdd(p.arrived + b0, 1u) == static_cast<unsigned>(b1 - b0);
-                if (last) p.arrived[b0] = 0;
-                flag = last;
-            }
-            __syncthreads();
-            if (!flag) {
-                __syncthreads();
+            if (!join_pieces<T, D, R, ATT_THREADS>(p, rows, c, tid, ms[0], ls[0], &flag, v_scale, [] { __syncthreads(); }))
                 continue;
-            }
-            __threadfence();
-            // piece b0 lies in its block's second place, the others in their first
-            auto piece = [&](int i) { return p.parts + (static_cast<int64_t>(i) * 2 + (i == b0 ? 1 : 0)) * PART; };
-            for (int r = warp; r < live; r += ATT_WARPS) {
-                float mr = -CUDART_INF_F, lr = 0.0f;
-                bool nan = false;
-                for (int i = b0 + lane; i <= b1; i += 32) {
-                    const float x = __ldcg(piece(i) + r);
-                    nan |= x != x;
-                    mr = fmaxf(mr, x);
-                }
-                mr = warp_max(mr);
-                nan = __any_sync(0xffffffffu, nan);
-                const float base = mr == -CUDART_INF_F ? 0.0f : mr;
-                for (int i = b0 + lane; i <= b1; i += 32) lr += __ldcg(piece(i) + R + r) * fast_exp2(__ldcg(piece(i) + r) - base);
-                lr = warp_sum(lr);
-                if (lane == 0) {
-                    ms[0][r] = nan ? CUDART_NAN_F : mr;
-                    ls[0][r] = lr;
-                }
-            }
-            __syncthreads();
-            for (int i = tid; i < live * (D / 4); i += ATT_THREADS) {
-                const int r = i / (D / 4), d = (i - r * (D / 4)) * 4;
-                const float mr = ms[0][r], base = mr == -CUDART_INF_F ? 0.0f : mr;
-                float4 x = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-#pragma unroll 4
-                for (int k = b0; k <= b1; ++k) {
-                    const float a = fast_exp2(__ldcg(piece(k) + r) - base);
-                    const float4 y = __ldcg(reinterpret_cast<const float4 *>(piece(k) + 2 * R + r * D + d));
-                    x.x += a * y.x, x.y += a * y.y, x.z += a * y.z, x.w += a * y.w;
-                }
-                write_row(r, d, x, mr, ls[0][r]);
-            }
             seq_bad = ms[0][0] != ms[0][0];
         }
         if (tid == 0 && p.row_status && c.h == 0 && c.row_tile == 0) p.row_status[c.b] = seq_bad ? KV_STATUS_BAD : 0;
@@ -486,10 +391,12 @@ cudaError_t launch_attention(const AttentionLaunch &L, cudaStream_t st)
     p.rows = k.T * p.group;
     p.scale_log2 = k.scale * LOG2E;
     char *ws = static_cast<char *>(L.ws);
+    p.error = reinterpret_cast<unsigned *>(ws);
     p.arrived = reinterpret_cast<unsigned *>(ws + WS_HEADER);
     p.parts = reinterpret_cast<float *>(ws + ATT_PARTS_AT);
     const bool eight = k.cache.dtype == SPV_E4M3;
     const int D = k.cache.head_dim;
+    if (p.rows > 16 && D <= 128) return launch_attention_rows(p, k.dtype, k.cache.dtype, D, st);
     if (k.dtype == SPV_BF16)
         return eight ? launch_types<__nv_bfloat16, __nv_fp8_e4m3>(p, D, st)
                      : launch_types<__nv_bfloat16, __nv_bfloat16>(p, D, st);

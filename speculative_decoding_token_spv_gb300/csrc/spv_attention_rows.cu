@@ -1,0 +1,615 @@
+// spv_attention_rows.cu -- attention over the paged cache for many query rows
+// a key head (drafted chains with wide groups, draft trees): 5th-generation
+// tensor cores, up to 128 rows at a time against tiles of 128 keys.
+//
+// One block an SM, with its equal range of all tiles (Work, Cursor), in three
+// roles that follow one another over shared and tensor memory:
+//   * four loader warps gather K and V rows through the page table with
+//     asynchronous copies, in the permuted layout the tensor cores read; an
+//     e4m3 cache lands as it is and is widened to f16 by the threads that
+//     loaded it (f16 holds every e4m3 value);
+//   * one thread issues S = Q K^T of the next tile, then O += P V of this one,
+//     P from tensor memory, both sums in 32 bits in tensor memory;
+//   * four warps hold a row a thread: running maximum, exponentials, sum, P
+//     back to tensor memory.  O is only rescaled when a maximum has grown by
+//     more than 2^8, so p stays below 2^8 and the 32-bit sums lose nothing.
+// With 64 rows or fewer the rows stand in tensor memory two or four times,
+// each copy taking half or a quarter of every tile's keys (its P is zero
+// elsewhere): all four warps work whatever the number of rows, and the
+// copies join at the end like pieces.
+//
+// Every wait is bounded; one that gives up records SPV_ERR_TIMEOUT in the
+// workspace, ends the block in order and leaves NaN in what it had to write.
+#include "spv_attention.cuh"
+#include "spv_tcgen.cuh"
+
+namespace spv {
+
+constexpr int AR_KEYS = 128;
+constexpr int AR_THREADS = 9 * 32;
+constexpr int AR_ROWS = 128;
+constexpr int AR_ITEMS = 8;           // items whose flags can be in use at once
+constexpr float AR_GROWTH = 8.0f;     // growth of a maximum (powers of two) that O waits for
+
+template <typename C, int D> struct RowsShape {
+    static constexpr bool WIDEN = sizeof(C) == 1;
+    static constexpr int TILE = AR_KEYS * D * 2;                             // K or V as multiplied
+    static constexpr int RAW = AR_KEYS * D;                                  // e4m3 K or V
+    static constexpr int STAGES = WIDEN ? 4 : (D == 128 ? 3 : 5);
+    static constexpr int Q_AT = 0, KV_AT = AR_ROWS * D * 2;
+    static constexpr int RAW_AT = KV_AT + 2 * TILE;
+    static constexpr int CTL_AT = WIDEN ? RAW_AT + STAGES * 2 * RAW : KV_AT + STAGES * 2 * TILE;
+};
+
+struct RowsCtl {
+    uint64_t kv_full[5], kv_empty[5];  // 16-bit cache: K and V of a stage
+    uint64_t k_full, k_empty, v_full, v_empty;  // e4m3: the widened tiles
+    uint64_t s_full[2], p_full[2], o_done[2], q_full, spare;
+    unsigned long long odd[AR_ITEMS];  // new tokens whose v has infinities or NaN
+    int bad[AR_ITEMS];                 // a page id outside the pool
+    // What handing a tile on needs to know of it, per loader warp and stage: the row of its first new token (128:
+    // none), that token's number, the item's flags.
+    int tail[4][5][3];
+    uint32_t tmem;
+    int dead, stop, flag;
+    float ms[AR_ROWS], ls[AR_ROWS];
+};
+
+// Bounded wait; false once a wait of the block has given up.
+__device__ __forceinline__ bool rows_wait1(RowsCtl *ctl, uint64_t *bar, uint32_t parity, unsigned *err)
+{
+    for (uint32_t i = 0; i < WAIT_LIMIT; ++i) {
+        if (mbar_try_wait(bar, parity)) return true;
+        if ((i & 63) == 63 && *reinterpret_cast<volatile int *>(&ctl->dead)) return false;
+    }
+    *reinterpret_cast<volatile int *>(&ctl->dead) = 1;
+    atomicExch(err, static_cast<unsigned>(STATUS_TIMEOUT));
+    return false;
+}
+// The same of a whole warp, with one answer for all its lanes.
+__device__ __forceinline__ bool rows_wait(RowsCtl *ctl, uint64_t *bar, uint32_t parity, unsigned *err)
+{
+    return __all_sync(0xffffffffu, rows_wait1(ctl, bar, parity, err));
+}
+
+// Tiles of the cursor's item that this block has: [t0, t1); none for an item without keys.
+__device__ __forceinline__ int first_tile(const Cursor &c) { return static_cast<int>(c.at - c.first); }
+__device__ __forceinline__ int last_tile(const Cursor &c)
+{
+    if (c.s.total == 0) return first_tile(c);
+    const long long e = c.first + c.tiles;
+    return static_cast<int>((c.end < e ? c.end : e) - c.first);
+}
+
+__device__ __forceinline__ uint32_t panel_at(int row, int chunk)  // 16-byte chunk of a 16-bit row in an operand tile
+{
+    return (chunk >> 3) * (AR_KEYS * 128) + row * 128 + (((chunk & 7) ^ (row & 7)) << 4);
+}
+
+// Clears infinities and NaN in 8 16-bit values.
+template <typename C> __device__ __forceinline__ uint4 finite_only(uint4 x)
+{
+    const uint32_t e = std::is_same<C, __half>::value ? 0x7c00u : 0x7f80u;
+    uint32_t *w = &x.x;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        if ((w[i] & e) == e) w[i] &= 0xffff0000u;
+        if (((w[i] >> 16) & e) == e) w[i] &= 0x0000ffffu;
+    }
+    return x;
+}
+
+// ------------------------------------------------------------------ loaders
+template <typename C, int D>
+__device__ void rows_load(const AttParams &p, Cursor c, char *smem, RowsCtl *ctl, unsigned *err, int lt)
+{
+    using S = RowsShape<C, D>;
+    constexpr int CH = D * static_cast<int>(sizeof(C)) / 16, RPI = 32 / CH, NST = S::STAGES;
+    const int lane = lt & 31, w = lt >> 5, chunk = lane % CH, sub = lane / CH;
+    const uint32_t base = smem_u32(smem);
+    const int mask = (1 << p.c.page_shift) - 1;
+    int n = 0, done = 0, item = 0;  // tiles issued, tiles handed on, items with tiles
+
+    // Hands on the oldest tile, whose copies have landed.
+    auto hand_on = [&]() -> bool {
+        const int st = done % NST;
+        const int row0 = ctl->tail[w][st][0], token0 = ctl->tail[w][st][1], slot_item = ctl->tail[w][st][2];
+        if (!S::WIDEN) {
+            if (row0 < AR_KEYS) {
+                const uint32_t v = base + S::KV_AT + st * 2 * S::TILE + S::TILE;
+#pragma unroll 1
+                for (int i = 0; i < CH; ++i) {
+                    const int row = 32 * w + i * RPI + sub;
+                    if (row < row0) continue;
+                    uint4 *at = reinterpret_cast<uint4 *>(smem + (v - base) + panel_at(row, chunk));
+                    const uint4 x = *at;
+                    if (chunk_not_finite<C>(x)) {
+                        *at = finite_only<C>(x);
+                        atomicOr(&ctl->odd[slot_item], 1ull << ((token0 + row - row0) & 63));
+                    }
+                }
+            }
+            fence_async_shared();
+            mbar_arrive(&ctl->kv_full[st]);
+        } else {
+#pragma unroll
+            for (int kv = 0; kv < 2; ++kv) {
+                const char *raw = smem + S::RAW_AT + (st * 2 + kv) * S::RAW;
+                char *to = smem + S::KV_AT + kv * S::TILE;
+                if (done > 0 && !rows_wait(ctl, kv ? &ctl->v_empty : &ctl->k_empty, (done - 1) & 1, err)) return false;
+#pragma unroll 4
+                for (int i = 0; i < CH; ++i) {
+                    const int row = 32 * w + i * RPI + sub;
+                    const uint4 x = *reinterpret_cast<const uint4 *>(raw + row * D + chunk * 16);
+                    uint32_t b[4] = {x.x, x.y, x.z, x.w};
+                    if (kv && row >= row0 && chunk_not_finite<C>(x)) {
+#pragma unroll
+                        for (int k = 0; k < 4; ++k)
+#pragma unroll
+                            for (int e = 0; e < 32; e += 8)
+                                if (((b[k] >> e) & 0x7fu) == 0x7fu) b[k] &= ~(0xffu << e);
+                        atomicOr(&ctl->odd[slot_item], 1ull << ((token0 + row - row0) & 63));
+                    }
+                    uint32_t y[8];
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) {
+                        y[2 * k] = e4m3x2_to_f16x2(b[k] & 0xffffu);
+                        y[2 * k + 1] = e4m3x2_to_f16x2(b[k] >> 16);
+                    }
+                    *reinterpret_cast<uint4 *>(to + panel_at(row, 2 * chunk)) = make_uint4(y[0], y[1], y[2], y[3]);
+                    *reinterpret_cast<uint4 *>(to + panel_at(row, 2 * chunk + 1)) = make_uint4(y[4], y[5], y[6], y[7]);
+                }
+                fence_async_shared();
+                mbar_arrive(kv ? &ctl->v_full : &ctl->k_full);
+            }
+        }
+        ++done;
+        return true;
+    };
+    bool ok = true;
+    for (; ok && c.at < c.end; next_item(c, p.w, p.c)) {
+        const int t0 = first_tile(c), t1 = last_tile(c);
+        if (t0 == t1) continue;
+        const int32_t *table = p.c.table + static_cast<int64_t>(c.b) * p.c.max_pages;
+        const int slot_item = item++ % AR_ITEMS;
+        auto lookup = [&](int tile) {  // this lane's row of a tile
+            const int j = tile * AR_KEYS + 32 * w + lane;
+            if (tile >= t1 || j >= c.s.total) return -1;
+            const int pg = page_of(p.c, table, j);
+            if (pg < 0) *reinterpret_cast<volatile int *>(&ctl->bad[slot_item]) = 1;
+            return pg;
+        };
+        int pg = lookup(t0);
+        for (int tile = t0; tile < t1; ++tile, ++n) {
+            if (n >= NST - 1) {
+                cp_async_wait<NST - 2>();
+                if (!(ok = hand_on())) break;
+            }
+            if (!S::WIDEN && n >= NST && !(ok = rows_wait(ctl, &ctl->kv_empty[n % NST], (n / NST - 1) & 1, err))) break;
+            const int j0 = tile * AR_KEYS;
+            if (lane == 0) {
+                ctl->tail[w][n % NST][0] = min(max(0, c.s.ctx - j0), AR_KEYS);
+                ctl->tail[w][n % NST][1] = max(0, j0 - c.s.ctx);
+                ctl->tail[w][n % NST][2] = slot_item;
+            }
+            __syncwarp();
+            const uint32_t dk = base + (S::WIDEN ? S::RAW_AT + (n % NST) * 2 * S::RAW : S::KV_AT + (n % NST) * 2 * S::TILE);
+            const uint32_t dv = dk + (S::WIDEN ? S::RAW : S::TILE);
+            const char *kb = p.c.k.base + c.h * p.c.k.head_stride + chunk * 16;
+            const char *vb = p.c.v.base + c.h * p.c.v.head_stride + chunk * 16;
+#pragma unroll 4
+            for (int i = 0; i < CH; ++i) {
+                const int row = 32 * w + i * RPI + sub;
+                const int page = __shfl_sync(0xffffffffu, pg, i * RPI + sub);
+                const uint32_t at = S::WIDEN ? row * D + chunk * 16 : panel_at(row, chunk);
+                const int64_t in = (j0 + row) & mask;
+                const bool there = page >= 0;
+                cp_async16_zfill(dk + at, there ? kb + page * p.c.k.page_stride + in * p.c.k.slot_stride : p.c.k.base, there ? 16 : 0);
+                cp_async16_zfill(dv + at, there ? vb + page * p.c.v.page_stride + in * p.c.v.slot_stride : p.c.v.base, there ? 16 : 0);
+            }
+            cp_async_commit();
+            pg = lookup(tile + 1);
+        }
+        if (!ok) break;
+    }
+    // the tiles still on their way, oldest first
+    cp_async_wait<0>();
+    while (ok && done < n) ok = hand_on();
+}
+
+// ------------------------------------------------------------------ products
+template <typename T, typename C, int D>
+__device__ void rows_multiply(const AttParams &p, Cursor c, char *smem, RowsCtl *ctl, unsigned *err)
+{
+    using S = RowsShape<C, D>;
+    using M = typename MmaOf<T, C>::type;
+    constexpr bool BF = std::is_same<M, __nv_bfloat16>::value;
+    constexpr uint32_t SHAPE_S = mma_shape(BF, false, AR_KEYS), SHAPE_O = mma_shape(BF, true, D);
+    constexpr int NST = S::STAGES;
+    const uint32_t base = smem_u32(smem), tmem = ctl->tmem;
+    const uint32_t tm_s = tmem, tm_p = tmem + 256, tm_o = tmem + 384;
+    auto scores = [&](int n) -> bool {  // S of tile n
+        const uint32_t k = base + S::KV_AT + (S::WIDEN ? 0 : (n % NST) * 2 * S::TILE);
+        if (!rows_wait1(ctl, S::WIDEN ? &ctl->k_full : &ctl->kv_full[n % NST], S::WIDEN ? n & 1 : (n / NST) & 1, err)) return false;
+        tc_fence_after();
+        fence_async_shared();
+#pragma unroll
+        for (int ks = 0; ks < D / 16; ++ks) {
+            const uint32_t off = (ks >> 2) * (AR_KEYS * 128) + (ks & 3) * 32;
+            tc_mma(tm_s + (n & 1) * AR_KEYS, desc_k_major(base + S::Q_AT + off), desc_k_major(k + off), SHAPE_S, ks > 0);
+        }
+        tc_commit(&ctl->s_full[n & 1]);
+        if (S::WIDEN) tc_commit(&ctl->k_empty);
+        return true;
+    };
+    int n = 0, item = 0;
+    for (; c.at < c.end; next_item(c, p.w, p.c)) {
+        const int tiles = last_tile(c) - first_tile(c);
+        if (tiles == 0) continue;
+        if (!rows_wait1(ctl, &ctl->q_full, item++ & 1, err)) return;
+        if (!scores(n)) return;
+        for (int i = 0; i < tiles; ++i, ++n) {
+            if (i + 1 < tiles && !scores(n + 1)) return;
+            if (!rows_wait1(ctl, &ctl->p_full[n & 1], (n >> 1) & 1, err)) return;
+            if (S::WIDEN && !rows_wait1(ctl, &ctl->v_full, n & 1, err)) return;
+            tc_fence_after();
+            fence_async_shared();
+            const uint32_t v = base + S::KV_AT + S::TILE + (S::WIDEN ? 0 : (n % NST) * 2 * S::TILE);
+#pragma unroll
+            for (int ks = 0; ks < AR_KEYS / 16; ++ks)
+                tc_mma_ta(tm_o, tm_p + (n & 1) * (AR_KEYS / 2) + ks * 8, desc_n_major(v + ks * 2048, AR_KEYS * 128), SHAPE_O,
+                          i > 0 || ks > 0);
+            tc_commit(&ctl->o_done[n & 1]);
+            tc_commit(S::WIDEN ? &ctl->v_empty : &ctl->kv_empty[n % NST]);
+        }
+    }
+}
+
+// ------------------------------------------------------------------ rows
+__device__ __forceinline__ void rows_sync() { asm volatile("bar.sync 1, 128;" ::: "memory"); }
+
+// COLS: keys of a tile that a thread takes, and rows of a copy.
+template <typename T, typename C, int D, int COLS>
+__device__ void rows_softmax(const AttParams &p, Cursor c, char *smem, RowsCtl *ctl, unsigned *err, int tid)
+{
+    using S = RowsShape<C, D>;
+    using M = typename MmaOf<T, C>::type;
+    constexpr int COPIES = AR_ROWS / COLS, PART = AR_ROWS * (D + 2);
+    const int lane = tid & 31, warp = tid >> 5, copy = tid / COLS, r = tid % COLS;
+    const uint32_t quarter = static_cast<uint32_t>(warp * 32) << 16;
+    const uint32_t tm_s = ctl->tmem + quarter + copy * COLS, tm_p = ctl->tmem + quarter + 256 + copy * (COLS / 2),
+                   tm_o = ctl->tmem + quarter + 384;
+    const long long begin = c.at;
+    float *merge = reinterpret_cast<float *>(smem + S::Q_AT);  // q's place, once a piece's scores are done
+    // the keys of other copies never get a probability
+    if (COPIES > 1) {
+        uint32_t zero[32];
+#pragma unroll
+        for (int i = 0; i < 32; ++i) zero[i] = 0;
+#pragma unroll
+        for (int i = 0; i < 128; i += 32) tc_st32(ctl->tmem + quarter + 256 + i, zero);
+        tc_wait_st();
+    }
+    int n = 0, item = 0;
+    for (; c.at < c.end; next_item(c, p.w, p.c)) {
+        const int t0 = first_tile(c), t1 = last_tile(c), row0 = c.row_tile * COLS, live = min(COLS, p.rows - row0);
+        const AttRows rows{c.b, c.h, row0, live};
+        const float v_scale = p.c.v_scale ? __ldg(p.c.v_scale + c.h) : 1.0f;
+        const bool mine = r < live;
+        const int token = (row0 + r) / p.group;
+        const unsigned long long see =
+            mine && token < c.s.fresh && !c.s.bad
+                ? visible_mask(p.parent ? p.parent + static_cast<int64_t>(c.b) * p.w.T : nullptr, token)
+                : 0ull;
+        float m = -CUDART_INF_F, l = 0.0f;
+        float factor = p.scale_log2 * (p.c.k_scale ? __ldg(p.c.k_scale + c.h) : 1.0f);
+        unsigned long long odd = 0;
+        bool any_bad = c.s.bad;
+        if (t0 < t1) {
+            // q of every copy's rows; for an e4m3 cache each row by a power of two into f16's range
+            for (int i = tid; i < AR_ROWS * (D / 8); i += 128) {
+                const int tr = i / (D / 8), ch = i - tr * (D / 8), rr = tr % COLS, t = (row0 + rr) / p.group,
+                          g = (row0 + rr) - t * p.group;
+                uint4 raw = make_uint4(0, 0, 0, 0);
+                if (rr < live && t < c.s.fresh)
+                    raw = *reinterpret_cast<const uint4 *>(
+                        static_cast<const T *>(p.q) +
+                        ((static_cast<int64_t>(c.b) * p.w.T + t) * p.q_heads + c.h * p.group + g) * D + ch * 8);
+                if (S::WIDEN) {
+                    const T *y = reinterpret_cast<const T *>(&raw);
+                    float x[8], top = 0.0f;
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) {
+                        x[e] = Num<T>::up(y[e]);
+                        top = fabsf(x[e]) < CUDART_INF_F ? fmaxf(top, fabsf(x[e])) : top;
+                    }
+#pragma unroll
+                    for (int o = D / 16; o; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+                    const int e2 = top > 0.0f ? max(-120, min(120, 14 - ilogbf(top))) : 0;
+                    const float up = exp2f(static_cast<float>(e2));
+                    if (ch == 0) ctl->ms[tr] = exp2f(static_cast<float>(-e2));
+                    raw = make_uint4(pack_mma<M>(x[0] * up, x[1] * up), pack_mma<M>(x[2] * up, x[3] * up),
+                                     pack_mma<M>(x[4] * up, x[5] * up), pack_mma<M>(x[6] * up, x[7] * up));
+                }
+                *reinterpret_cast<uint4 *>(smem + S::Q_AT + panel_at(tr, ch)) = raw;
+            }
+            fence_async_shared();
+            mbar_arrive(&ctl->q_full);
+            if (S::WIDEN) {
+                rows_sync();
+                factor *= ctl->ms[tid];
+            }
+            const bool works = __any_sync(0xffffffffu, mine);
+            bool ok = true;
+            for (int tile = t0; tile < t1; ++tile, ++n) {
+                if (!(ok = rows_wait(ctl, &ctl->s_full[n & 1], (n >> 1) & 1, err))) break;
+                tc_fence_after();
+                __syncwarp();
+                if (works) {
+                    float x[COLS];
+#pragma unroll
+                    for (int i = 0; i < COLS; i += 32) {
+                        uint32_t y[32];
+                        tc_ld32(y, tm_s + (n & 1) * AR_KEYS + i);
+#pragma unroll
+                        for (int k = 0; k < 32; ++k) x[i + k] = __uint_as_float(y[k]) * factor;
+                    }
+                    const int j0 = tile * AR_KEYS + copy * COLS;
+                    if (j0 + COLS > c.s.ctx) {
+#pragma unroll
+                        for (int i = 0; i < COLS; ++i) {
+                            const int j = j0 + i;
+                            if (!(j < c.s.ctx || (j < c.s.total && (see >> (j - c.s.ctx) & 1)))) x[i] = -CUDART_INF_F;
+                        }
+                    }
+                    float top = x[0];
+#pragma unroll
+                    for (int i = 1; i + 1 < COLS; i += 2) top = fmax3(top, x[i], x[i + 1]);
+                    top = fmaxf(top, x[COLS - 1]);
+                    if (tile == t0) {
+                        m = fmaxf(m, top);
+                    } else if (__any_sync(0xffffffffu, top > m + AR_GROWTH || (m == -CUDART_INF_F && top > m))) {
+                        const float grown = fmaxf(m, top), a = grown == -CUDART_INF_F ? 0.0f : fast_exp2(m - grown);
+                        m = grown;
+                        l *= a;
+                        if (!(ok = rows_wait(ctl, &ctl->o_done[(n - 1) & 1], ((n - 1) >> 1) & 1, err))) break;
+                        tc_fence_after();
+#pragma unroll 1
+                        for (int i = 0; i < D; i += 32) {
+                            uint32_t y[32];
+                            tc_ld32(y, tm_o + i);
+#pragma unroll
+                            for (int k = 0; k < 32; ++k) y[k] = __float_as_uint(__uint_as_float(y[k]) * a);
+                            tc_st32(tm_o + i, y);
+                        }
+                    }
+                    const float base = m == -CUDART_INF_F ? 0.0f : m;
+                    float s0 = 0.0f, s1 = 0.0f;
+                    uint32_t pk[COLS / 2];
+#pragma unroll
+                    for (int i = 0; i < COLS; i += 2) {
+                        const float a = fast_exp2(x[i] - base), b = fast_exp2(x[i + 1] - base);
+                        s0 += a;
+                        s1 += b;
+                        // rounded to 16 bits for the product (half a step of the type each); l keeps 32 bits
+                        pk[i / 2] = pack_mma<M>(a, b);
+                    }
+                    l += s0 + s1;
+                    // its place was read by the product two tiles ago
+                    if (n >= 2 && !(ok = rows_wait(ctl, &ctl->o_done[n & 1], ((n - 2) >> 1) & 1, err))) break;
+                    tc_fence_after();
+                    if (COLS == 32) {
+                        tc_st16(tm_p + (n & 1) * (AR_KEYS / 2), *reinterpret_cast<uint32_t(*)[16]>(pk));
+                    } else {
+#pragma unroll
+                        for (int i = 0; i < COLS / 2; i += 32)
+                            tc_st32(tm_p + (n & 1) * (AR_KEYS / 2) + i, *reinterpret_cast<uint32_t(*)[32]>(pk + i));
+                    }
+                    tc_wait_st();
+                }
+                tc_fence_before();
+                mbar_arrive(&ctl->p_full[n & 1]);
+            }
+            if (ok) ok = rows_wait(ctl, &ctl->o_done[(n - 1) & 1], ((n - 1) >> 1) & 1, err);
+            tc_fence_after();
+            odd = *reinterpret_cast<volatile unsigned long long *>(&ctl->odd[item % AR_ITEMS]);
+            any_bad |= *reinterpret_cast<volatile int *>(&ctl->bad[item % AR_ITEMS]) != 0;
+        }
+        if (see == 0) {
+            m = -CUDART_INF_F;
+            l = 0.0f;
+        }
+        rows_sync();  // the scale factors in ms are read
+        ctl->ms[tid] = m;
+        ctl->ls[tid] = l;
+        if (tid == 0) {
+            ctl->stop = *reinterpret_cast<volatile int *>(&ctl->dead);
+            if (t0 < t1) {
+                ctl->odd[item % AR_ITEMS] = 0;
+                ctl->bad[item % AR_ITEMS] = 0;
+            }
+        }
+        rows_sync();
+        if (t0 < t1) ++item;
+        const bool stop = *reinterpret_cast<volatile int *>(&ctl->stop) != 0;
+        any_bad |= stop;
+        float all_m = -CUDART_INF_F, all_l = 0.0f;
+#pragma unroll
+        for (int k = 0; k < COPIES; ++k) all_m = fmaxf(all_m, ctl->ms[k * COLS + r]);
+        const float base = all_m == -CUDART_INF_F ? 0.0f : all_m, mine_a = l == 0.0f ? 0.0f : fast_exp2(m - base);
+#pragma unroll
+        for (int k = 0; k < COPIES; ++k) {
+            const float lk = ctl->ls[k * COLS + r];
+            if (lk != 0.0f) all_l += lk * fast_exp2(ctl->ms[k * COLS + r] - base);
+        }
+        const bool whole = c.s.total == 0 || (t0 == 0 && t1 == c.tiles);
+        float *part = p.parts + (static_cast<int64_t>(blockIdx.x) * 2 + (c.first < begin ? 0 : 1)) * PART;
+        const float out_m = any_bad ? CUDART_NAN_F : all_m;
+        if (!whole && copy == 0 && mine) {
+            part[r] = out_m;
+            part[AR_ROWS + r] = all_l;
+        }
+#pragma unroll 1
+        for (int d0 = 0; d0 < D; d0 += 32) {
+            float x[32];
+            __syncwarp();
+            if (t0 < t1 && !stop) {
+                uint32_t y[32];
+                tc_ld32(y, tm_o + d0);
+#pragma unroll
+                for (int k = 0; k < 32; ++k) x[k] = mine_a == 0.0f ? 0.0f : __uint_as_float(y[k]) * mine_a;
+            } else {
+#pragma unroll
+                for (int k = 0; k < 32; ++k) x[k] = 0.0f;
+            }
+            if (COPIES > 1) {
+                if (copy > 0) {
+#pragma unroll
+                    for (int k = 0; k < 32; ++k) merge[((copy - 1) * COLS + r) * 33 + k] = x[k];
+                }
+                rows_sync();
+                if (copy == 0) {
+#pragma unroll
+                    for (int q = 1; q < COPIES; ++q)
+#pragma unroll
+                        for (int k = 0; k < 32; ++k) x[k] += merge[((q - 1) * COLS + r) * 33 + k];
+                }
+                rows_sync();
+            }
+            if (copy != 0 || !mine) continue;
+            if (odd) {
+                // New tokens whose v has infinities or NaN (cleared for the product): for the rows that see them.
+                for (unsigned long long left = odd & see; left; left &= left - 1) {
+                    const int j = c.s.ctx + __ffsll(left) - 1;
+                    const int page = page_of(p.c, p.c.table + static_cast<int64_t>(c.b) * p.c.max_pages, j);
+                    if (page < 0) continue;
+                    const C *k = reinterpret_cast<const C *>(row_ptr(p.c, p.c.k, page, j, c.h));
+                    const C *v = reinterpret_cast<const C *>(row_ptr(p.c, p.c.v, page, j, c.h));
+                    const T *q = static_cast<const T *>(p.q) +
+                                 ((static_cast<int64_t>(c.b) * p.w.T + token) * p.q_heads + c.h * p.group + (row0 + r) % p.group) * D;
+                    float s = 0.0f;
+                    for (int d = 0; d < D; ++d) s += Num<T>::up(q[d]) * Num<C>::up(k[d]);
+                    const float w = fast_exp2(s * p.scale_log2 * (p.c.k_scale ? __ldg(p.c.k_scale + c.h) : 1.0f) - base);
+                    if (w == 0.0f) continue;
+#pragma unroll
+                    for (int e = 0; e < 32; ++e) {
+                        const float y = Num<C>::up(v[d0 + e]);
+                        if (!(fabsf(y) < CUDART_INF_F)) x[e] += w * y;
+                    }
+                }
+            }
+#pragma unroll
+            for (int k = 0; k < 32; k += 4) {
+                const float4 y = make_float4(x[k], x[k + 1], x[k + 2], x[k + 3]);
+                if (whole)
+                    write_row<T, D>(p, rows, r, d0 + k, y, out_m, all_l, v_scale);
+                else
+                    *reinterpret_cast<float4 *>(part + 2 * AR_ROWS + r * D + d0 + k) = y;
+            }
+        }
+        tc_fence_before();
+        bool seq_bad = any_bad, wrote = whole;
+        if (!whole) {
+            rows_sync();  // ms and ls are free
+            wrote = join_pieces<T, D, AR_ROWS, 128>(p, rows, c, tid, ctl->ms, ctl->ls, &ctl->flag, v_scale, rows_sync);
+            if (wrote) seq_bad = ctl->ms[0] != ctl->ms[0];
+        }
+        if (wrote && tid == 0 && p.row_status && c.h == 0 && c.row_tile == 0) p.row_status[c.b] = seq_bad ? KV_STATUS_BAD : 0;
+        rows_sync();
+        if (stop) break;
+    }
+}
+
+template <typename T, typename C, int D, int COLS>
+__global__ void __launch_bounds__(AR_THREADS, 1) attention_rows_kernel(const AttParams p)
+{
+    using S = RowsShape<C, D>;
+    extern __shared__ char raw_smem[];
+    char *smem = raw_smem + ((1024u - (smem_u32(raw_smem) & 1023u)) & 1023u);
+    RowsCtl *ctl = reinterpret_cast<RowsCtl *>(smem + S::CTL_AT);
+    const int tid = threadIdx.x, warp = tid >> 5;
+    unsigned *err = p.error;
+    const Cursor c = find_range(p.w, p.c, blockIdx.x, gridDim.x, tid & 31);
+    if (c.at == c.end) return;  // the whole block
+    if (tid == 0) {
+        for (int i = 0; i < 5; ++i) {
+            mbar_init(&ctl->kv_full[i], 128);
+            mbar_init(&ctl->kv_empty[i], 1);
+        }
+        mbar_init(&ctl->k_full, 128);
+        mbar_init(&ctl->v_full, 128);
+        mbar_init(&ctl->k_empty, 1);
+        mbar_init(&ctl->v_empty, 1);
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(&ctl->s_full[i], 1);
+            mbar_init(&ctl->p_full[i], 128);
+            mbar_init(&ctl->o_done[i], 1);
+        }
+        mbar_init(&ctl->q_full, 128);
+        mbar_init(&ctl->spare, 1);
+        for (int i = 0; i < AR_ITEMS; ++i) ctl->odd[i] = 0, ctl->bad[i] = 0;
+        ctl->dead = ctl->stop = 0;
+        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    }
+    if (warp == 4) tmem_alloc(&ctl->tmem, 512);
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    if (warp < 4) {
+        rows_softmax<T, C, D, COLS>(p, c, smem, ctl, err, tid);
+    } else if (warp == 4) {
+        if ((tid & 31) == 0) {
+            rows_multiply<T, C, D>(p, c, smem, ctl, err);
+            if (*reinterpret_cast<volatile int *>(&ctl->dead)) {  // let what was issued end
+                tc_commit(&ctl->spare);
+                mbar_wait(&ctl->spare, 0);
+            }
+        }
+        __syncwarp();
+    } else {
+        rows_load<C, D>(p, c, smem, ctl, err, tid - 160);
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    if (warp == 4) tmem_free(ctl->tmem, 512);
+}
+
+template <typename T, typename C, int D, int COLS> static cudaError_t launch_cols(AttParams p, cudaStream_t st)
+{
+    using S = RowsShape<C, D>;
+    constexpr int SMEM = S::CTL_AT + static_cast<int>(sizeof(RowsCtl)) + 1024;
+    static_assert(SMEM <= 232448, "shared memory of a block");
+    auto kernel = attention_rows_kernel<T, C, D, COLS>;
+    const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, SMEM);
+    if (e != cudaSuccess) return e;
+    p.w.tile = AR_KEYS;
+    p.w.row_tiles = (p.rows + COLS - 1) / COLS;
+    kernel<<<ATT_SMS, AR_THREADS, SMEM, st>>>(p);
+    return cudaGetLastError();
+}
+template <typename T, typename C, int D> static cudaError_t launch_dim(const AttParams &p, cudaStream_t st)
+{
+    if (p.rows <= 32) return launch_cols<T, C, D, 32>(p, st);
+    if (p.rows <= 64) return launch_cols<T, C, D, 64>(p, st);
+    return launch_cols<T, C, D, 128>(p, st);
+}
+template <typename T, typename C> static cudaError_t launch_types(const AttParams &p, int D, cudaStream_t st)
+{
+    return D == 64 ? launch_dim<T, C, 64>(p, st) : launch_dim<T, C, 128>(p, st);
+}
+
+size_t attention_rows_part_floats(int head_dim)
+{
+    return static_cast<size_t>(ATT_SMS) * 2 * AR_ROWS * (head_dim + 2);
+}
+
+cudaError_t launch_attention_rows(const AttParams &p, spv_dtype q, spv_dtype cache, int D, cudaStream_t st)
+{
+    const bool eight = cache == SPV_E4M3;
+    if (q == SPV_BF16)
+        return eight ? launch_types<__nv_bfloat16, __nv_fp8_e4m3>(p, D, st) : launch_types<__nv_bfloat16, __nv_bfloat16>(p, D, st);
+    return eight ? launch_types<__half, __nv_fp8_e4m3>(p, D, st) : launch_types<__half, __half>(p, D, st);
+}
+
+}  // namespace spv
