@@ -42,12 +42,11 @@ template <typename C, int D> struct RowsShape {
 };
 
 struct RowsCtl {
-    uint64_t kv_full[5], kv_empty[5];  // 16-bit cache: K and V of a stage
-    uint64_t k_full, k_empty, v_full, v_empty;  // e4m3: the widened tiles
+    uint64_t k_full[5], k_empty[5], v_full[5], v_empty[5];  // of a stage (e4m3: the one widened tile)
     uint64_t s_full[2], p_full[2], o_done[2], q_full, spare;
     unsigned long long odd[AR_ITEMS];  // new tokens whose v has infinities or NaN
     int bad[AR_ITEMS];                 // a page id outside the pool
-    // What handing a tile on needs to know of it, per loader warp and stage: the row of its first new token (128:
+    // e4m3: what widening a tile needs to know of it, per loader warp and stage: the row of its first new token (128:
     // none), that token's number, the item's flags.
     int tail[4][5][3];
     uint32_t tmem;
@@ -99,7 +98,17 @@ template <typename C> __device__ __forceinline__ uint4 finite_only(uint4 x)
     return x;
 }
 
+// The block's item that a loader or the multiplying thread is at, by number of
+// items with tiles: the place of its flags.
+__device__ __forceinline__ int item_flags(int item) { return item % AR_ITEMS; }
+
 // ------------------------------------------------------------------ loaders
+// Arrives on `bar` once this thread's asynchronous copies so far have landed.
+__device__ __forceinline__ void cp_async_arrive(uint64_t *bar)
+{
+    asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(smem_u32(bar)) : "memory");
+}
+
 template <typename C, int D>
 __device__ void rows_load(const AttParams &p, Cursor c, char *smem, RowsCtl *ctl, unsigned *err, int lt)
 {
@@ -108,62 +117,39 @@ __device__ void rows_load(const AttParams &p, Cursor c, char *smem, RowsCtl *ctl
     const int lane = lt & 31, w = lt >> 5, chunk = lane % CH, sub = lane / CH;
     const uint32_t base = smem_u32(smem);
     const int mask = (1 << p.c.page_shift) - 1;
-    int n = 0, done = 0, item = 0;  // tiles issued, tiles handed on, items with tiles
+    int n = 0, item = 0;  // tiles issued, items with tiles
 
-    // Hands on the oldest tile, whose copies have landed.
-    auto hand_on = [&]() -> bool {
-        const int st = done % NST;
-        const int row0 = ctl->tail[w][st][0], token0 = ctl->tail[w][st][1], slot_item = ctl->tail[w][st][2];
-        if (!S::WIDEN) {
-            if (row0 < AR_KEYS) {
-                const uint32_t v = base + S::KV_AT + st * 2 * S::TILE + S::TILE;
-#pragma unroll 1
-                for (int i = 0; i < CH; ++i) {
-                    const int row = 32 * w + i * RPI + sub;
-                    if (row < row0) continue;
-                    uint4 *at = reinterpret_cast<uint4 *>(smem + (v - base) + panel_at(row, chunk));
-                    const uint4 x = *at;
-                    if (chunk_not_finite<C>(x)) {
-                        *at = finite_only<C>(x);
-                        atomicOr(&ctl->odd[slot_item], 1ull << ((token0 + row - row0) & 63));
-                    }
-                }
-            }
-            fence_async_shared();
-            mbar_arrive(&ctl->kv_full[st]);
-        } else {
-#pragma unroll
-            for (int kv = 0; kv < 2; ++kv) {
-                const char *raw = smem + S::RAW_AT + (st * 2 + kv) * S::RAW;
-                char *to = smem + S::KV_AT + kv * S::TILE;
-                if (done > 0 && !rows_wait(ctl, kv ? &ctl->v_empty : &ctl->k_empty, (done - 1) & 1, err)) return false;
+    // e4m3: widens K (kv = 0) or V of tile t, whose copies have landed; each thread what it has loaded.
+    auto widen = [&](int t, int kv) -> bool {
+        const int st = t % NST;
+        const int row0 = ctl->tail[w][st][0], token0 = ctl->tail[w][st][1], flags = ctl->tail[w][st][2];
+        const char *raw = smem + S::RAW_AT + (st * 2 + kv) * S::RAW;
+        char *to = smem + S::KV_AT + kv * S::TILE;
+        if (t > 0 && !rows_wait(ctl, kv ? &ctl->v_empty[0] : &ctl->k_empty[0], (t - 1) & 1, err)) return false;
 #pragma unroll 4
-                for (int i = 0; i < CH; ++i) {
-                    const int row = 32 * w + i * RPI + sub;
-                    const uint4 x = *reinterpret_cast<const uint4 *>(raw + row * D + chunk * 16);
-                    uint32_t b[4] = {x.x, x.y, x.z, x.w};
-                    if (kv && row >= row0 && chunk_not_finite<C>(x)) {
+        for (int i = 0; i < CH; ++i) {
+            const int row = 32 * w + i * RPI + sub;
+            const uint4 x = *reinterpret_cast<const uint4 *>(raw + row * D + chunk * 16);
+            uint32_t b[4] = {x.x, x.y, x.z, x.w};
+            if (kv && row >= row0 && chunk_not_finite<C>(x)) {
 #pragma unroll
-                        for (int k = 0; k < 4; ++k)
+                for (int k = 0; k < 4; ++k)
 #pragma unroll
-                            for (int e = 0; e < 32; e += 8)
-                                if (((b[k] >> e) & 0x7fu) == 0x7fu) b[k] &= ~(0xffu << e);
-                        atomicOr(&ctl->odd[slot_item], 1ull << ((token0 + row - row0) & 63));
-                    }
-                    uint32_t y[8];
-#pragma unroll
-                    for (int k = 0; k < 4; ++k) {
-                        y[2 * k] = e4m3x2_to_f16x2(b[k] & 0xffffu);
-                        y[2 * k + 1] = e4m3x2_to_f16x2(b[k] >> 16);
-                    }
-                    *reinterpret_cast<uint4 *>(to + panel_at(row, 2 * chunk)) = make_uint4(y[0], y[1], y[2], y[3]);
-                    *reinterpret_cast<uint4 *>(to + panel_at(row, 2 * chunk + 1)) = make_uint4(y[4], y[5], y[6], y[7]);
-                }
-                fence_async_shared();
-                mbar_arrive(kv ? &ctl->v_full : &ctl->k_full);
+                    for (int e = 0; e < 32; e += 8)
+                        if (((b[k] >> e) & 0x7fu) == 0x7fu) b[k] &= ~(0xffu << e);
+                atomicOr(&ctl->odd[flags], 1ull << ((token0 + row - row0) & 63));
             }
+            uint32_t y[8];
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                y[2 * k] = e4m3x2_to_f16x2(b[k] & 0xffffu);
+                y[2 * k + 1] = e4m3x2_to_f16x2(b[k] >> 16);
+            }
+            *reinterpret_cast<uint4 *>(to + panel_at(row, 2 * chunk)) = make_uint4(y[0], y[1], y[2], y[3]);
+            *reinterpret_cast<uint4 *>(to + panel_at(row, 2 * chunk + 1)) = make_uint4(y[4], y[5], y[6], y[7]);
         }
-        ++done;
+        fence_async_shared();
+        mbar_arrive(kv ? &ctl->v_full[0] : &ctl->k_full[0]);
         return true;
     };
     bool ok = true;
@@ -171,53 +157,101 @@ __device__ void rows_load(const AttParams &p, Cursor c, char *smem, RowsCtl *ctl
         const int t0 = first_tile(c), t1 = last_tile(c);
         if (t0 == t1) continue;
         const int32_t *table = p.c.table + static_cast<int64_t>(c.b) * p.c.max_pages;
-        const int slot_item = item++ % AR_ITEMS;
+        const int flags = item_flags(item++);
         auto lookup = [&](int tile) {  // this lane's row of a tile
             const int j = tile * AR_KEYS + 32 * w + lane;
             if (tile >= t1 || j >= c.s.total) return -1;
             const int pg = page_of(p.c, table, j);
-            if (pg < 0) *reinterpret_cast<volatile int *>(&ctl->bad[slot_item]) = 1;
+            if (pg < 0) *reinterpret_cast<volatile int *>(&ctl->bad[flags]) = 1;
             return pg;
         };
         int pg = lookup(t0);
-        for (int tile = t0; tile < t1; ++tile, ++n) {
-            if (n >= NST - 1) {
-                cp_async_wait<NST - 2>();
-                if (!(ok = hand_on())) break;
+        for (int tile = t0; ok && tile < t1; ++tile, ++n) {
+            const int st = n % NST, j0 = tile * AR_KEYS;
+            const int row0 = min(max(0, c.s.ctx - j0), AR_KEYS), token0 = max(0, j0 - c.s.ctx);  // the first new token
+            if (S::WIDEN) {
+                if (lane == 0) {
+                    ctl->tail[w][st][0] = row0;
+                    ctl->tail[w][st][1] = token0;
+                    ctl->tail[w][st][2] = flags;
+                }
+                __syncwarp();
             }
-            if (!S::WIDEN && n >= NST && !(ok = rows_wait(ctl, &ctl->kv_empty[n % NST], (n / NST - 1) & 1, err))) break;
-            const int j0 = tile * AR_KEYS;
-            if (lane == 0) {
-                ctl->tail[w][n % NST][0] = min(max(0, c.s.ctx - j0), AR_KEYS);
-                ctl->tail[w][n % NST][1] = max(0, j0 - c.s.ctx);
-                ctl->tail[w][n % NST][2] = slot_item;
+#pragma unroll
+            for (int kv = 0; kv < 2; ++kv) {
+                const PoolView &pool = kv ? p.c.v : p.c.k;
+                uint32_t to;
+                if (S::WIDEN) {  // the raw stages are each thread's own
+                    to = base + S::RAW_AT + (st * 2 + kv) * S::RAW;
+                } else {
+                    if (ok && n >= NST) ok = rows_wait(ctl, kv ? &ctl->v_empty[st] : &ctl->k_empty[st], (n / NST - 1) & 1, err);
+                    if (!ok) break;
+                    to = base + S::KV_AT + (st * 2 + kv) * S::TILE;
+                }
+                const int64_t mine = pg < 0 ? -1 : pg * pool.page_stride + ((j0 + 32 * w + lane) & mask) * pool.slot_stride;
+                const char *from = pool.base + c.h * pool.head_stride + chunk * 16;
+#pragma unroll 8
+                for (int i = 0; i < CH; ++i) {
+                    const int row = 32 * w + i * RPI + sub;
+                    const int64_t at = __shfl_sync(0xffffffffu, mine, i * RPI + sub);
+                    cp_async16_zfill(to + (S::WIDEN ? row * D + chunk * 16 : panel_at(row, chunk)), at < 0 ? pool.base : from + at,
+                                     at < 0 ? 0 : 16);
+                }
+                if (S::WIDEN) {
+                    cp_async_commit();
+                } else if (kv && row0 < AR_KEYS) {
+                    // Infinities and NaN in a new token's v: cleared here, as 0 x inf would reach rows that do not see
+                    // it; the rows that do get them at the end.
+                    asm volatile("cp.async.wait_all;" ::: "memory");
+#pragma unroll 1
+                    for (int i = 0; i < CH; ++i) {
+                        const int row = 32 * w + i * RPI + sub;
+                        if (row < row0) continue;
+                        uint4 *v = reinterpret_cast<uint4 *>(smem + (to - base) + panel_at(row, chunk));
+                        const uint4 x = *v;
+                        if (chunk_not_finite<C>(x)) {
+                            *v = finite_only<C>(x);
+                            atomicOr(&ctl->odd[flags], 1ull << ((token0 + row - row0) & 63));
+                        }
+                    }
+                    fence_async_shared();
+                    mbar_arrive(&ctl->v_full[st]);
+                } else {
+                    cp_async_arrive(kv ? &ctl->v_full[st] : &ctl->k_full[st]);
+                }
             }
-            __syncwarp();
-            const uint32_t dk = base + (S::WIDEN ? S::RAW_AT + (n % NST) * 2 * S::RAW : S::KV_AT + (n % NST) * 2 * S::TILE);
-            const uint32_t dv = dk + (S::WIDEN ? S::RAW : S::TILE);
-            const char *kb = p.c.k.base + c.h * p.c.k.head_stride + chunk * 16;
-            const char *vb = p.c.v.base + c.h * p.c.v.head_stride + chunk * 16;
-#pragma unroll 4
-            for (int i = 0; i < CH; ++i) {
-                const int row = 32 * w + i * RPI + sub;
-                const int page = __shfl_sync(0xffffffffu, pg, i * RPI + sub);
-                const uint32_t at = S::WIDEN ? row * D + chunk * 16 : panel_at(row, chunk);
-                const int64_t in = (j0 + row) & mask;
-                const bool there = page >= 0;
-                cp_async16_zfill(dk + at, there ? kb + page * p.c.k.page_stride + in * p.c.k.slot_stride : p.c.k.base, there ? 16 : 0);
-                cp_async16_zfill(dv + at, there ? vb + page * p.c.v.page_stride + in * p.c.v.slot_stride : p.c.v.base, there ? 16 : 0);
-            }
-            cp_async_commit();
+            if (!ok) break;
             pg = lookup(tile + 1);
+            if (S::WIDEN && n >= NST - 1) {  // K one tile ahead of V
+                const int t = n - (NST - 1);
+                cp_async_wait<2 * NST - 3>();
+                if (t == 0) ok = widen(0, 0);
+                ok = ok && widen(t + 1, 0) && widen(t, 1);
+            }
         }
-        if (!ok) break;
     }
-    // the tiles still on their way, oldest first
-    cp_async_wait<0>();
-    while (ok && done < n) ok = hand_on();
+    asm volatile("cp.async.wait_all;" ::: "memory");
+    if (S::WIDEN) {  // the tiles still on their way
+        int t = n >= NST ? n - (NST - 1) : 0;
+        if (ok && t == 0 && n > 0) ok = widen(0, 0);
+        for (; ok && t < n; ++t) ok = (t + 1 >= n || widen(t + 1, 0)) && widen(t, 1);
+    }
 }
 
 // ------------------------------------------------------------------ products
+__device__ __forceinline__ bool mbar_test(uint64_t *bar, uint32_t parity)
+{
+    uint32_t ok;
+    asm volatile("{\n\t.reg .pred p;\n\tmbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\tselp.u32 %0, 1, 0, p;\n\t}"
+                 : "=r"(ok)
+                 : "r"(smem_u32(bar)), "r"(parity)
+                 : "memory");
+    return ok != 0;
+}
+
+// One thread.  Issues whatever is ready: the scores of the next tile, up to
+// two ahead of the last tile whose probabilities were multiplied, and the
+// probabilities' product; neither waits for the other's operands.
 template <typename T, typename C, int D>
 __device__ void rows_multiply(const AttParams &p, Cursor c, char *smem, RowsCtl *ctl, unsigned *err)
 {
@@ -225,42 +259,50 @@ __device__ void rows_multiply(const AttParams &p, Cursor c, char *smem, RowsCtl 
     using M = typename MmaOf<T, C>::type;
     constexpr bool BF = std::is_same<M, __nv_bfloat16>::value;
     constexpr uint32_t SHAPE_S = mma_shape(BF, false, AR_KEYS), SHAPE_O = mma_shape(BF, true, D);
-    constexpr int NST = S::STAGES;
+    constexpr int NST = S::WIDEN ? 1 : S::STAGES;  // of the multiplied tiles
     const uint32_t base = smem_u32(smem), tmem = ctl->tmem;
     const uint32_t tm_s = tmem, tm_p = tmem + 256, tm_o = tmem + 384;
-    auto scores = [&](int n) -> bool {  // S of tile n
-        const uint32_t k = base + S::KV_AT + (S::WIDEN ? 0 : (n % NST) * 2 * S::TILE);
-        if (!rows_wait1(ctl, S::WIDEN ? &ctl->k_full : &ctl->kv_full[n % NST], S::WIDEN ? n & 1 : (n / NST) & 1, err)) return false;
-        tc_fence_after();
-        fence_async_shared();
-#pragma unroll
-        for (int ks = 0; ks < D / 16; ++ks) {
-            const uint32_t off = (ks >> 2) * (AR_KEYS * 128) + (ks & 3) * 32;
-            tc_mma(tm_s + (n & 1) * AR_KEYS, desc_k_major(base + S::Q_AT + off), desc_k_major(k + off), SHAPE_S, ks > 0);
-        }
-        tc_commit(&ctl->s_full[n & 1]);
-        if (S::WIDEN) tc_commit(&ctl->k_empty);
-        return true;
-    };
-    int n = 0, item = 0;
+    int ns = 0, no = 0, item = 0;  // tiles whose scores, whose outputs were issued
     for (; c.at < c.end; next_item(c, p.w, p.c)) {
         const int tiles = last_tile(c) - first_tile(c);
         if (tiles == 0) continue;
         if (!rows_wait1(ctl, &ctl->q_full, item++ & 1, err)) return;
-        if (!scores(n)) return;
-        for (int i = 0; i < tiles; ++i, ++n) {
-            if (i + 1 < tiles && !scores(n + 1)) return;
-            if (!rows_wait1(ctl, &ctl->p_full[n & 1], (n >> 1) & 1, err)) return;
-            if (S::WIDEN && !rows_wait1(ctl, &ctl->v_full, n & 1, err)) return;
-            tc_fence_after();
-            fence_async_shared();
-            const uint32_t v = base + S::KV_AT + S::TILE + (S::WIDEN ? 0 : (n % NST) * 2 * S::TILE);
+        const int start = no, end = no + tiles;
+        uint32_t idle = 0;
+        while (no < end) {
+            if (ns < end && ns <= no + 1 && mbar_test(&ctl->k_full[ns % NST], (ns / NST) & 1)) {
+                tc_fence_after();
+                fence_async_shared();  // K was written by ordinary and asynchronous copies
+                const uint32_t k = base + S::KV_AT + (ns % NST) * 2 * S::TILE;
 #pragma unroll
-            for (int ks = 0; ks < AR_KEYS / 16; ++ks)
-                tc_mma_ta(tm_o, tm_p + (n & 1) * (AR_KEYS / 2) + ks * 8, desc_n_major(v + ks * 2048, AR_KEYS * 128), SHAPE_O,
-                          i > 0 || ks > 0);
-            tc_commit(&ctl->o_done[n & 1]);
-            tc_commit(S::WIDEN ? &ctl->v_empty : &ctl->kv_empty[n % NST]);
+                for (int ks = 0; ks < D / 16; ++ks) {
+                    const uint32_t off = (ks >> 2) * (AR_KEYS * 128) + (ks & 3) * 32;
+                    tc_mma(tm_s + (ns & 1) * AR_KEYS, desc_k_major(base + S::Q_AT + off), desc_k_major(k + off), SHAPE_S, ks > 0);
+                }
+                tc_commit(&ctl->s_full[ns & 1]);
+                tc_commit(&ctl->k_empty[ns % NST]);
+                ++ns;
+                idle = 0;
+            } else if (no < ns && mbar_test(&ctl->p_full[no & 1], (no >> 1) & 1) &&
+                       mbar_test(&ctl->v_full[no % NST], (no / NST) & 1)) {
+                tc_fence_after();
+                fence_async_shared();
+                const uint32_t v = base + S::KV_AT + S::TILE + (no % NST) * 2 * S::TILE;
+#pragma unroll
+                for (int ks = 0; ks < AR_KEYS / 16; ++ks)
+                    tc_mma_ta(tm_o, tm_p + (no & 1) * (AR_KEYS / 2) + ks * 8, desc_n_major(v + ks * 2048, AR_KEYS * 128), SHAPE_O,
+                              no > start || ks > 0);
+                tc_commit(&ctl->o_done[no & 1]);
+                tc_commit(&ctl->v_empty[no % NST]);
+                ++no;
+                idle = 0;
+            } else if (++idle == 4 * WAIT_LIMIT) {
+                *reinterpret_cast<volatile int *>(&ctl->dead) = 1;
+                atomicExch(err, static_cast<unsigned>(STATUS_TIMEOUT));
+                return;
+            } else if ((idle & 63) == 63 && *reinterpret_cast<volatile int *>(&ctl->dead)) {
+                return;
+            }
         }
     }
 }
@@ -533,13 +575,11 @@ __global__ void __launch_bounds__(AR_THREADS, 1) attention_rows_kernel(const Att
     if (c.at == c.end) return;  // the whole block
     if (tid == 0) {
         for (int i = 0; i < 5; ++i) {
-            mbar_init(&ctl->kv_full[i], 128);
-            mbar_init(&ctl->kv_empty[i], 1);
+            mbar_init(&ctl->k_full[i], 128);
+            mbar_init(&ctl->v_full[i], 128);
+            mbar_init(&ctl->k_empty[i], 1);
+            mbar_init(&ctl->v_empty[i], 1);
         }
-        mbar_init(&ctl->k_full, 128);
-        mbar_init(&ctl->v_full, 128);
-        mbar_init(&ctl->k_empty, 1);
-        mbar_init(&ctl->v_empty, 1);
         for (int i = 0; i < 2; ++i) {
             mbar_init(&ctl->s_full[i], 1);
             mbar_init(&ctl->p_full[i], 128);
