@@ -26,7 +26,7 @@
 namespace spv {
 
 constexpr int AR_KEYS = 128;
-constexpr int AR_THREADS = 9 * 32;
+constexpr int AR_THREADS = 512;  // warps 0-3 rows, 4 products, 8-11 K, 12-15 V
 constexpr int AR_ROWS = 128;
 constexpr int AR_ITEMS = 8;           // items whose flags can be in use at once
 constexpr float AR_GROWTH = 8.0f;     // growth of a maximum (powers of two) that O waits for
@@ -48,7 +48,7 @@ struct RowsCtl {
     int bad[AR_ITEMS];                 // a page id outside the pool
     // e4m3: what widening a tile needs to know of it, per loader warp and stage: the row of its first new token (128:
     // none), that token's number, the item's flags.
-    int tail[4][5][3];
+    int tail[8][5][3];
     uint32_t tmem;
     int dead, stop, flag;
     float ms[AR_ROWS], ls[AR_ROWS];
@@ -109,23 +109,26 @@ __device__ __forceinline__ void cp_async_arrive(uint64_t *bar)
     asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(smem_u32(bar)) : "memory");
 }
 
+// One of two groups of four warps: K (kv = 0) or V.
 template <typename C, int D>
-__device__ void rows_load(const AttParams &p, Cursor c, char *smem, RowsCtl *ctl, unsigned *err, int lt)
+__device__ void rows_load(const AttParams &p, Cursor c, char *smem, RowsCtl *ctl, unsigned *err, int lt, int kv)
 {
     using S = RowsShape<C, D>;
     constexpr int CH = D * static_cast<int>(sizeof(C)) / 16, RPI = 32 / CH, NST = S::STAGES;
     const int lane = lt & 31, w = lt >> 5, chunk = lane % CH, sub = lane / CH;
     const uint32_t base = smem_u32(smem);
+    const PoolView pool = kv ? p.c.v : p.c.k;
+    uint64_t *full = kv ? ctl->v_full : ctl->k_full, *empty = kv ? ctl->v_empty : ctl->k_empty;
     const int mask = (1 << p.c.page_shift) - 1;
     int n = 0, item = 0;  // tiles issued, items with tiles
 
-    // e4m3: widens K (kv = 0) or V of tile t, whose copies have landed; each thread what it has loaded.
-    auto widen = [&](int t, int kv) -> bool {
+    // e4m3: widens tile t, whose copies have landed; each thread what it has loaded.
+    auto widen = [&](int t) -> bool {
         const int st = t % NST;
-        const int row0 = ctl->tail[w][st][0], token0 = ctl->tail[w][st][1], flags = ctl->tail[w][st][2];
+        const int row0 = ctl->tail[4 * kv + w][st][0], token0 = ctl->tail[4 * kv + w][st][1], flags = ctl->tail[4 * kv + w][st][2];
         const char *raw = smem + S::RAW_AT + (st * 2 + kv) * S::RAW;
         char *to = smem + S::KV_AT + kv * S::TILE;
-        if (t > 0 && !rows_wait(ctl, kv ? &ctl->v_empty[0] : &ctl->k_empty[0], (t - 1) & 1, err)) return false;
+        if (t > 0 && !rows_wait(ctl, empty, (t - 1) & 1, err)) return false;
 #pragma unroll 4
         for (int i = 0; i < CH; ++i) {
             const int row = 32 * w + i * RPI + sub;
@@ -145,11 +148,14 @@ __device__ void rows_load(const AttParams &p, Cursor c, char *smem, RowsCtl *ctl
                 y[2 * k] = e4m3x2_to_f16x2(b[k] & 0xffffu);
                 y[2 * k + 1] = e4m3x2_to_f16x2(b[k] >> 16);
             }
-            *reinterpret_cast<uint4 *>(to + panel_at(row, 2 * chunk)) = make_uint4(y[0], y[1], y[2], y[3]);
-            *reinterpret_cast<uint4 *>(to + panel_at(row, 2 * chunk + 1)) = make_uint4(y[4], y[5], y[6], y[7]);
+            // lanes of the two panels store their halves in opposite order: no two on one bank
+            const bool swap = (chunk >> 2) & 1;
+            const uint4 lo = make_uint4(y[0], y[1], y[2], y[3]), hi = make_uint4(y[4], y[5], y[6], y[7]);
+            *reinterpret_cast<uint4 *>(to + panel_at(row, 2 * chunk + swap)) = swap ? hi : lo;
+            *reinterpret_cast<uint4 *>(to + panel_at(row, 2 * chunk + !swap)) = swap ? lo : hi;
         }
         fence_async_shared();
-        mbar_arrive(kv ? &ctl->v_full[0] : &ctl->k_full[0]);
+        mbar_arrive(full);
         return true;
     };
     bool ok = true;
@@ -158,84 +164,73 @@ __device__ void rows_load(const AttParams &p, Cursor c, char *smem, RowsCtl *ctl
         if (t0 == t1) continue;
         const int32_t *table = p.c.table + static_cast<int64_t>(c.b) * p.c.max_pages;
         const int flags = item_flags(item++);
-        auto lookup = [&](int tile) {  // this lane's row of a tile
+        const char *from = pool.base + c.h * pool.head_stride + chunk * 16;
+        auto lookup = [&](int tile) {  // the page id of this lane's row of a tile, unchecked; -1: no such row
             const int j = tile * AR_KEYS + 32 * w + lane;
-            if (tile >= t1 || j >= c.s.total) return -1;
-            const int pg = page_of(p.c, table, j);
-            if (pg < 0) *reinterpret_cast<volatile int *>(&ctl->bad[flags]) = 1;
-            return pg;
+            return tile < t1 && j < c.s.total ? __ldg(table + (j >> p.c.page_shift)) : -1;
         };
-        int pg = lookup(t0);
-        for (int tile = t0; ok && tile < t1; ++tile, ++n) {
+        int pg = lookup(t0), next = lookup(t0 + 1);
+        for (int tile = t0; tile < t1; ++tile, ++n) {
             const int st = n % NST, j0 = tile * AR_KEYS;
             const int row0 = min(max(0, c.s.ctx - j0), AR_KEYS), token0 = max(0, j0 - c.s.ctx);  // the first new token
-            if (S::WIDEN) {
+            if (static_cast<unsigned>(pg) >= static_cast<unsigned>(p.c.num_pages)) {
+                if (j0 + 32 * w + lane < c.s.total) *reinterpret_cast<volatile int *>(&ctl->bad[flags]) = 1;
+                pg = -1;
+            }
+            const int64_t mine = pg < 0 ? -1 : pg * pool.page_stride + ((j0 + 32 * w + lane) & mask) * pool.slot_stride;
+            pg = next;
+            next = lookup(tile + 2);  // two tiles ahead: its latency is behind that of the rows
+            uint32_t to;
+            if (S::WIDEN) {  // the raw stages are each thread's own
                 if (lane == 0) {
-                    ctl->tail[w][st][0] = row0;
-                    ctl->tail[w][st][1] = token0;
-                    ctl->tail[w][st][2] = flags;
+                    ctl->tail[4 * kv + w][st][0] = row0;
+                    ctl->tail[4 * kv + w][st][1] = token0;
+                    ctl->tail[4 * kv + w][st][2] = flags;
                 }
                 __syncwarp();
+                to = base + S::RAW_AT + (st * 2 + kv) * S::RAW;
+            } else {
+                if (n >= NST && !(ok = rows_wait(ctl, &empty[st], (n / NST - 1) & 1, err))) break;
+                to = base + S::KV_AT + (st * 2 + kv) * S::TILE;
             }
-#pragma unroll
-            for (int kv = 0; kv < 2; ++kv) {
-                const PoolView &pool = kv ? p.c.v : p.c.k;
-                uint32_t to;
-                if (S::WIDEN) {  // the raw stages are each thread's own
-                    to = base + S::RAW_AT + (st * 2 + kv) * S::RAW;
-                } else {
-                    if (ok && n >= NST) ok = rows_wait(ctl, kv ? &ctl->v_empty[st] : &ctl->k_empty[st], (n / NST - 1) & 1, err);
-                    if (!ok) break;
-                    to = base + S::KV_AT + (st * 2 + kv) * S::TILE;
-                }
-                const int64_t mine = pg < 0 ? -1 : pg * pool.page_stride + ((j0 + 32 * w + lane) & mask) * pool.slot_stride;
-                const char *from = pool.base + c.h * pool.head_stride + chunk * 16;
 #pragma unroll 8
+            for (int i = 0; i < CH; ++i) {
+                const int row = 32 * w + i * RPI + sub;
+                const int64_t at = __shfl_sync(0xffffffffu, mine, i * RPI + sub);
+                cp_async16_zfill(to + (S::WIDEN ? row * D + chunk * 16 : panel_at(row, chunk)), at < 0 ? pool.base : from + at,
+                                 at < 0 ? 0 : 16);
+            }
+            if (S::WIDEN) {
+                cp_async_commit();
+                if (n >= NST - 1) {
+                    cp_async_wait<NST - 1>();
+                    if (!(ok = widen(n - (NST - 1)))) break;
+                }
+            } else if (kv && row0 < AR_KEYS) {
+                // Infinities and NaN in a new token's v: cleared here, as 0 x inf would reach rows that do not see it;
+                // the rows that do get them at the end.
+                asm volatile("cp.async.wait_all;" ::: "memory");
+#pragma unroll 1
                 for (int i = 0; i < CH; ++i) {
                     const int row = 32 * w + i * RPI + sub;
-                    const int64_t at = __shfl_sync(0xffffffffu, mine, i * RPI + sub);
-                    cp_async16_zfill(to + (S::WIDEN ? row * D + chunk * 16 : panel_at(row, chunk)), at < 0 ? pool.base : from + at,
-                                     at < 0 ? 0 : 16);
-                }
-                if (S::WIDEN) {
-                    cp_async_commit();
-                } else if (kv && row0 < AR_KEYS) {
-                    // Infinities and NaN in a new token's v: cleared here, as 0 x inf would reach rows that do not see
-                    // it; the rows that do get them at the end.
-                    asm volatile("cp.async.wait_all;" ::: "memory");
-#pragma unroll 1
-                    for (int i = 0; i < CH; ++i) {
-                        const int row = 32 * w + i * RPI + sub;
-                        if (row < row0) continue;
-                        uint4 *v = reinterpret_cast<uint4 *>(smem + (to - base) + panel_at(row, chunk));
-                        const uint4 x = *v;
-                        if (chunk_not_finite<C>(x)) {
-                            *v = finite_only<C>(x);
-                            atomicOr(&ctl->odd[flags], 1ull << ((token0 + row - row0) & 63));
-                        }
+                    if (row < row0) continue;
+                    uint4 *v = reinterpret_cast<uint4 *>(smem + (to - base) + panel_at(row, chunk));
+                    const uint4 x = *v;
+                    if (chunk_not_finite<C>(x)) {
+                        *v = finite_only<C>(x);
+                        atomicOr(&ctl->odd[flags], 1ull << ((token0 + row - row0) & 63));
                     }
-                    fence_async_shared();
-                    mbar_arrive(&ctl->v_full[st]);
-                } else {
-                    cp_async_arrive(kv ? &ctl->v_full[st] : &ctl->k_full[st]);
                 }
-            }
-            if (!ok) break;
-            pg = lookup(tile + 1);
-            if (S::WIDEN && n >= NST - 1) {  // K one tile ahead of V
-                const int t = n - (NST - 1);
-                cp_async_wait<2 * NST - 3>();
-                if (t == 0) ok = widen(0, 0);
-                ok = ok && widen(t + 1, 0) && widen(t, 1);
+                fence_async_shared();
+                mbar_arrive(&full[st]);
+            } else {
+                cp_async_arrive(&full[st]);
             }
         }
     }
     asm volatile("cp.async.wait_all;" ::: "memory");
-    if (S::WIDEN) {  // the tiles still on their way
-        int t = n >= NST ? n - (NST - 1) : 0;
-        if (ok && t == 0 && n > 0) ok = widen(0, 0);
-        for (; ok && t < n; ++t) ok = (t + 1 >= n || widen(t + 1, 0)) && widen(t, 1);
-    }
+    if (S::WIDEN)  // the tiles still on their way
+        for (int t = n >= NST - 1 ? n - (NST - 1) : 0; ok && t < n; ++t) ok = widen(t);
 }
 
 // ------------------------------------------------------------------ products
@@ -399,9 +394,12 @@ __device__ void rows_softmax(const AttParams &p, Cursor c, char *smem, RowsCtl *
                     const int j0 = tile * AR_KEYS + copy * COLS;
                     if (j0 + COLS > c.s.ctx) {
 #pragma unroll
-                        for (int i = 0; i < COLS; ++i) {
-                            const int j = j0 + i;
-                            if (!(j < c.s.ctx || (j < c.s.total && (see >> (j - c.s.ctx) & 1)))) x[i] = -CUDART_INF_F;
+                        for (int i = 0; i < COLS; i += 32) {
+                            const int o = c.s.ctx - (j0 + i);  // the first new token's column, from here
+                            unsigned bits = o >= 32 ? 0xffffffffu : o > 0 && see ? (1u << o) - 1u : 0u;
+                            if (o < 32 && o > -64) bits |= static_cast<unsigned>(o >= 0 ? see << o : see >> -o);
+#pragma unroll
+                            for (int k = 0; k < 32; ++k) x[i + k] = bits >> k & 1 ? x[i + k] : -CUDART_INF_F;
                         }
                     }
                     float top = x[0];
@@ -487,9 +485,17 @@ __device__ void rows_softmax(const AttParams &p, Cursor c, char *smem, RowsCtl *
         const bool whole = c.s.total == 0 || (t0 == 0 && t1 == c.tiles);
         float *part = p.parts + (static_cast<int64_t>(blockIdx.x) * 2 + (c.first < begin ? 0 : 1)) * PART;
         const float out_m = any_bad ? CUDART_NAN_F : all_m;
-        if (!whole && copy == 0 && mine) {
-            part[r] = out_m;
-            part[AR_ROWS + r] = all_l;
+        // the row's place, and what is written where there is no sum (0) or a bad sequence (NaN)
+        const int64_t row_at = (static_cast<int64_t>(c.b) * p.w.T + token) * p.q_heads + c.h * p.group + (row0 + r) - token * p.group;
+        const bool none = all_m == -CUDART_INF_F && all_l == 0.0f, fixed = none || any_bad;
+        const float instead = any_bad ? CUDART_NAN_F : 0.0f, out_scale = v_scale / all_l;
+        if (copy == 0 && mine) {
+            if (!whole) {
+                part[r] = out_m;
+                part[AR_ROWS + r] = all_l;
+            } else if (p.lse) {
+                p.lse[row_at] = any_bad ? CUDART_NAN_F : none ? -CUDART_INF_F : LN2 * (all_m + log2f(all_l));
+            }
         }
 #pragma unroll 1
         for (int d0 = 0; d0 < D; d0 += 32) {
@@ -543,10 +549,13 @@ __device__ void rows_softmax(const AttParams &p, Cursor c, char *smem, RowsCtl *
 #pragma unroll
             for (int k = 0; k < 32; k += 4) {
                 const float4 y = make_float4(x[k], x[k + 1], x[k + 2], x[k + 3]);
-                if (whole)
-                    write_row<T, D>(p, rows, r, d0 + k, y, out_m, all_l, v_scale);
-                else
+                if (!whole) {
                     *reinterpret_cast<float4 *>(part + 2 * AR_ROWS + r * D + d0 + k) = y;
+                } else {
+                    uint2 z = make_uint2(pack_mma<T>(y.x * out_scale, y.y * out_scale), pack_mma<T>(y.z * out_scale, y.w * out_scale));
+                    if (fixed) z = make_uint2(pack_mma<T>(instead, instead), pack_mma<T>(instead, instead));
+                    *reinterpret_cast<uint2 *>(static_cast<T *>(p.out) + row_at * D + d0 + k) = z;
+                }
             }
         }
         tc_fence_before();
@@ -595,10 +604,13 @@ __global__ void __launch_bounds__(AR_THREADS, 1) attention_rows_kernel(const Att
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
+    // registers: launched with 128 a thread, 4 x 128 = 208 + 80 + 2 x 112
     if (warp < 4) {
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 208;");
         rows_softmax<T, C, D, COLS>(p, c, smem, ctl, err, tid);
-    } else if (warp == 4) {
-        if ((tid & 31) == 0) {
+    } else if (warp < 8) {
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 80;");
+        if (tid == 128) {
             rows_multiply<T, C, D>(p, c, smem, ctl, err);
             if (*reinterpret_cast<volatile int *>(&ctl->dead)) {  // let what was issued end
                 tc_commit(&ctl->spare);
@@ -607,7 +619,8 @@ __global__ void __launch_bounds__(AR_THREADS, 1) attention_rows_kernel(const Att
         }
         __syncwarp();
     } else {
-        rows_load<C, D>(p, c, smem, ctl, err, tid - 160);
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 112;");
+        rows_load<C, D>(p, c, smem, ctl, err, tid & 127, warp >= 12);
     }
     tc_fence_before();
     __syncthreads();
