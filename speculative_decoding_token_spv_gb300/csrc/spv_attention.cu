@@ -13,9 +13,8 @@
 // copies, so that no warp waits for another and up to 190 KB an SM are on
 // their way.  All rows of a key head (new tokens x query heads of its group)
 // go through the tensor cores against the slice together, 16 or 32 of them.
-// Blocks leave what they have of an item in the workspace, and the last one
-// to do so joins the pieces in their order along the sequence: the result
-// does not depend on which block that is.
+// Blocks leave what they have of a shared item in the workspace; a dependent
+// launch joins the pieces in their order along the sequence.
 #include "spv_attention.cuh"
 
 namespace spv {
@@ -25,9 +24,8 @@ constexpr int ATT_THREADS = 32 * ATT_WARPS;
 constexpr int ATT_KEYS = 16 * ATT_WARPS;  // keys of a tile: a slice for each warp
 constexpr int ATT_MAX_ROWS = 32;
 
-// Workspace: header, arrival counters, pieces.  The counters' place is the
-// same for every shape, so calls of different shapes can share a workspace.
-constexpr size_t ATT_PARTS_AT = (WS_HEADER + ATT_MAX_BLOCKS * sizeof(unsigned) + 255) / 256 * 256;
+// Workspace: header, the blocks' split items, their pieces.
+constexpr size_t ATT_PARTS_AT = WS_HEADER + split_bytes(ATT_MAX_BLOCKS);
 
 size_t attention_ws_bytes(int, int, int, int, int head_dim)
 {
@@ -74,6 +72,8 @@ __global__ void __launch_bounds__(ATT_THREADS, AttShape<C, D, MT>::BLOCKS_PER_SM
     __syncthreads();
     Cursor c = cur0;
     const long long begin = c.at;
+    dependents_launch();
+    if (tid < 2) p.split[blockIdx.x * 2 + tid].n = 0;
     for (; c.at < c.end; next_item(c, p.w, p.c)) {
         const int row0 = c.row_tile * R, live = min(R, p.rows - row0);
         const long long item_end = c.first + c.tiles;
@@ -339,13 +339,8 @@ __global__ void __launch_bounds__(ATT_THREADS, AttShape<C, D, MT>::BLOCKS_PER_SM
                 *reinterpret_cast<float4 *>(part + 2 * R + r * D + d) = x;
             }
         }
-        bool seq_bad = any_bad;
-        if (!whole) {
-            if (!join_pieces<T, D, R, ATT_THREADS>(p, rows, c, tid, ms[0], ls[0], &flag, v_scale, [] { __syncthreads(); }))
-                continue;
-            seq_bad = ms[0][0] != ms[0][0];
-        }
-        if (tid == 0 && p.row_status && c.h == 0 && c.row_tile == 0) p.row_status[c.b] = seq_bad ? KV_STATUS_BAD : 0;
+        if (!whole) note_split(p, c, rows, begin, tid);
+        if (whole && tid == 0 && p.row_status && c.h == 0 && c.row_tile == 0) p.row_status[c.b] = any_bad ? KV_STATUS_BAD : 0;
         __syncthreads();
     }
 }
@@ -354,10 +349,12 @@ template <typename T, typename C, int D, int MT> static cudaError_t launch_rows(
 {
     using S = AttShape<C, D, MT>;
     auto kernel = attention_kernel<T, C, D, MT>;
-    const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, S::SMEM);
+    cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, S::SMEM);
     if (e != cudaSuccess) return e;
-    kernel<<<ATT_SMS * S::BLOCKS_PER_SM, ATT_THREADS, S::SMEM, st>>>(p);
-    return cudaGetLastError();
+    constexpr int BLOCKS = ATT_SMS * S::BLOCKS_PER_SM;
+    kernel<<<BLOCKS, ATT_THREADS, S::SMEM, st>>>(p);
+    e = cudaGetLastError();
+    return e != cudaSuccess ? e : launch_join(p, std::is_same<T, __half>::value ? SPV_F16 : SPV_BF16, D, S::R, BLOCKS, st);
 }
 template <typename T, typename C, int D> static cudaError_t launch_dim(AttParams &p, cudaStream_t st)
 {
@@ -392,7 +389,7 @@ cudaError_t launch_attention(const AttentionLaunch &L, cudaStream_t st)
     p.scale_log2 = k.scale * LOG2E;
     char *ws = static_cast<char *>(L.ws);
     p.error = reinterpret_cast<unsigned *>(ws);
-    p.arrived = reinterpret_cast<unsigned *>(ws + WS_HEADER);
+    p.split = reinterpret_cast<SplitItem *>(ws + WS_HEADER);
     p.parts = reinterpret_cast<float *>(ws + ATT_PARTS_AT);
     const bool eight = k.cache.dtype == SPV_E4M3;
     const int D = k.cache.head_dim;

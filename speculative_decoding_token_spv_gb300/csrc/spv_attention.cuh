@@ -17,11 +17,9 @@ struct AttParams {
     float *lse;
     const int32_t *parent;
     int32_t *row_status;
-    // Pieces of the item that begins in block i and ends in a later one (there is at most one) that are done; zero
-    // between calls.
-    unsigned *arrived;
     unsigned *error;  // the workspace's error word
-    float *parts;  // [block][2] pieces: m and l of each row, then o
+    struct SplitItem *split;  // [block][2]: the items that the block has pieces of
+    float *parts;             // [block][2] pieces: m and l of each row, then o
     int q_heads, group, rows;
     float scale_log2;
 };
@@ -54,6 +52,32 @@ struct AttRows {
     int b, h, row0, live;  // rows row0 .. row0 + live - 1 of key head h
 };
 
+// An item whose tiles more than one block has: blocks b0 .. b1.  Each of them
+// leaves its piece in the workspace -- b0, where the item begins, in its
+// second place, the others in their first -- and the join kernel puts them
+// together.  A block's two entries are written by every call; n = 0: none.
+struct SplitItem {
+    int b0, n;  // n = b1 - b0 + 1
+    AttRows rows;
+};
+
+__device__ __forceinline__ float *piece_of(const AttParams &p, int i, int b0, int size)
+{
+    return p.parts + (static_cast<int64_t>(i) * 2 + (i == b0 ? 1 : 0)) * size;
+}
+
+// Notes that this block has a piece of the cursor's item; `begin` is the start
+// of its range.
+__device__ __forceinline__ void note_split(const AttParams &p, const Cursor &c, const AttRows &rows, long long begin, int tid)
+{
+    if (tid != 0) return;
+    SplitItem s;
+    s.b0 = range_owner(c, c.first);
+    s.n = range_owner(c, c.first + c.tiles - 1) - s.b0 + 1;
+    s.rows = rows;
+    p.split[blockIdx.x * 2 + (c.first < begin ? 0 : 1)] = s;
+}
+
 // Result of row r of the tile, columns d .. d + 3: out = x v_scale / l, or what
 // stands for it (mr NaN: a bad sequence; no sum at all: 0 and minus infinity).
 template <typename T, int D>
@@ -71,72 +95,18 @@ __device__ __forceinline__ void write_row(const AttParams &p, const AttRows &w, 
     if (d == 0 && p.lse) p.lse[at] = nan ? mr : none ? -CUDART_INF_F : LN2 * (mr + log2f(lr));
 }
 
-// Block i's piece of the item that begins in block b0: there it lies in the
-// second place, in the later blocks in the first.
-__device__ __forceinline__ float *piece_of(const AttParams &p, int i, int b0, int size)
-{
-    return p.parts + (static_cast<int64_t>(i) * 2 + (i == b0 ? 1 : 0)) * size;
-}
+// Joins the pieces of the items that blocks share, after the kernel that wrote
+// them (a programmatic dependent launch of as many blocks as that had).  R:
+// rows of a piece.
+cudaError_t launch_join(const AttParams &p, spv_dtype q, int D, int R, int blocks, cudaStream_t st);
 
-// Called by all THREADS threads (whole warps) once their block's piece of the
-// item is in the workspace; `sync` is their barrier.  True for the block that
-// came last: it has joined the pieces, in their order, and written the rows.
-// ms and ls hold R floats each.
-template <typename T, int D, int R, int THREADS, typename Sync>
-__device__ __forceinline__ bool join_pieces(const AttParams &p, const AttRows &w, const Cursor &c, int tid, float *ms,
-                                            float *ls, int *flag, float v_scale, Sync &&sync)
-{
-    constexpr int PART = R * (D + 2);
-    const int b0 = range_owner(c, c.first), b1 = range_owner(c, c.first + c.tiles - 1);
-    __threadfence();
-    sync();
-    if (tid == 0) {
-        const bool last = atomicAdd(p.arrived + b0, 1u) == static_cast<unsigned>(b1 - b0);
-        if (last) p.arrived[b0] = 0;
-        *flag = last;
-    }
-    sync();
-    const bool last = *reinterpret_cast<volatile int *>(flag) != 0;
-    sync();
-    if (!last) return false;
-    __threadfence();
-    for (int r = tid >> 5; r < w.live; r += THREADS / 32) {
-        float mr = -CUDART_INF_F, lr = 0.0f;
-        bool nan = false;
-        for (int i = b0 + (tid & 31); i <= b1; i += 32) {
-            const float x = __ldcg(piece_of(p, i, b0, PART) + r);
-            nan |= x != x;
-            mr = fmaxf(mr, x);
-        }
-        mr = warp_max(mr);
-        nan = __any_sync(0xffffffffu, nan);
-        const float base = mr == -CUDART_INF_F ? 0.0f : mr;
-        for (int i = b0 + (tid & 31); i <= b1; i += 32) {
-            const float *x = piece_of(p, i, b0, PART);
-            lr += __ldcg(x + R + r) * fast_exp2(__ldcg(x + r) - base);
-        }
-        lr = warp_sum(lr);
-        if ((tid & 31) == 0) {
-            ms[r] = nan ? CUDART_NAN_F : mr;
-            ls[r] = lr;
-        }
-    }
-    sync();
-    for (int i = tid; i < w.live * (D / 4); i += THREADS) {
-        const int r = i / (D / 4), d = (i - r * (D / 4)) * 4;
-        const float mr = ms[r], base = mr == -CUDART_INF_F ? 0.0f : mr;
-        float4 x = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-#pragma unroll 4
-        for (int k = b0; k <= b1; ++k) {
-            const float *y0 = piece_of(p, k, b0, PART);
-            const float a = fast_exp2(__ldcg(y0 + r) - base);
-            const float4 y = __ldcg(reinterpret_cast<const float4 *>(y0 + 2 * R + r * D + d));
-            x.x += a * y.x, x.y += a * y.y, x.z += a * y.z, x.w += a * y.w;
-        }
-        write_row<T, D>(p, w, r, d, x, mr, ls[r], v_scale);
-    }
-    return true;
-}
+// Room for the entries of `blocks` blocks.
+constexpr size_t split_bytes(int blocks) { return (static_cast<size_t>(blocks) * 2 * sizeof(SplitItem) + 255) / 256 * 256; }
+
+// Lets a dependent launch start; a kernel's last use of what its predecessor
+// wrote lies behind dependents_wait.
+__device__ __forceinline__ void dependents_launch() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+__device__ __forceinline__ void dependents_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 
 cudaError_t launch_attention_rows(const AttParams &p, spv_dtype q, spv_dtype cache, int D, cudaStream_t st);
 size_t attention_rows_part_floats(int head_dim);  // of all blocks' pieces

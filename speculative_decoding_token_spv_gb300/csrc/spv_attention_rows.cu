@@ -9,7 +9,8 @@
 //     e4m3 cache lands as it is and is widened to f16 by the threads that
 //     loaded it (f16 holds every e4m3 value);
 //   * one thread issues S = Q K^T of the next tile, then O += P V of this one,
-//     P from tensor memory, both sums in 32 bits in tensor memory;
+//     P from tensor memory, both sums in 32 bits in tensor memory; three more
+//     warps bring q of the next item;
 //   * four warps hold a row a thread: running maximum, exponentials, sum, P
 //     back to tensor memory.  O is only rescaled when a maximum has grown by
 //     more than 2^8, so p stays below 2^8 and the 32-bit sums lose nothing.
@@ -28,30 +29,40 @@ namespace spv {
 constexpr int AR_KEYS = 128;
 constexpr int AR_THREADS = 512;  // warps 0-3 rows, 4 products, 8-11 K, 12-15 V
 constexpr int AR_ROWS = 128;
-constexpr int AR_ITEMS = 8;           // items whose flags can be in use at once
+constexpr int AR_ITEMS = 16;          // items whose flags can be in use at once
 constexpr float AR_GROWTH = 8.0f;     // growth of a maximum (powers of two) that O waits for
 
 template <typename C, int D> struct RowsShape {
     static constexpr bool WIDEN = sizeof(C) == 1;
-    static constexpr int TILE = AR_KEYS * D * 2;                             // K or V as multiplied
+    static constexpr int TILE = AR_KEYS * D * 2;                             // q, K or V as multiplied
     static constexpr int RAW = AR_KEYS * D;                                  // e4m3 K or V
-    static constexpr int STAGES = WIDEN ? 4 : (D == 128 ? 3 : 5);
-    static constexpr int Q_AT = 0, KV_AT = AR_ROWS * D * 2;
-    static constexpr int RAW_AT = KV_AT + 2 * TILE;
-    static constexpr int CTL_AT = WIDEN ? RAW_AT + STAGES * 2 * RAW : KV_AT + STAGES * 2 * TILE;
+    // K's place is free once the scores are there, V's only after the outputs: at D = 128 there is room for two and
+    // three. e4m3: one widened tile each, and stages of raw ones.
+    static constexpr int K_STAGES = WIDEN ? 1 : D == 128 ? 2 : 5, V_STAGES = WIDEN ? 1 : D == 128 ? 3 : 5;
+    static constexpr int RAW_STAGES = WIDEN ? (D == 128 ? 3 : 5) : 0;
+    static constexpr int Q_AT = 0, K_AT = 2 * TILE, V_AT = K_AT + K_STAGES * TILE, RAW_AT = V_AT + V_STAGES * TILE;
+    static constexpr int CTL_AT = RAW_AT + RAW_STAGES * 2 * RAW;
 };
 
 struct RowsCtl {
     uint64_t k_full[5], k_empty[5], v_full[5], v_empty[5];  // of a stage (e4m3: the one widened tile)
-    uint64_t s_full[2], p_full[2], o_done[2], q_full, spare;
+    uint64_t s_full[2], p_full[2], o_done[2], q_full[2], q_empty[2], spare;
     unsigned long long odd[AR_ITEMS];  // new tokens whose v has infinities or NaN
+    unsigned long long sees[2][64];    // per place of q: what each new token sees
     int bad[AR_ITEMS];                 // a page id outside the pool
     // e4m3: what widening a tile needs to know of it, per loader warp and stage: the row of its first new token (128:
     // none), that token's number, the item's flags.
-    int tail[8][5][3];
+    short tail[8][5][3];
+    signed char q_power[2][AR_ROWS];   // e4m3: the rows of q are stored times 2^q_power
     uint32_t tmem;
-    int dead, stop, flag;
+    int dead, stop;
+};
+
+// What the warps of the rows exchange at the end of a piece, in the place of its q.
+template <int D> struct RowsMerge {
+    static constexpr int ROUNDS = D == 128 ? 2 : 1;  // buffers in turn, as many as fit
     float ms[AR_ROWS], ls[AR_ROWS];
+    float x[ROUNDS][96 * 33];
 };
 
 // Bounded wait; false once a wait of the block has given up.
@@ -110,14 +121,15 @@ __device__ __forceinline__ void cp_async_arrive(uint64_t *bar)
 }
 
 // One of two groups of four warps: K (kv = 0) or V.
-template <typename C, int D>
-__device__ void rows_load(const AttParams &p, Cursor c, char *smem, RowsCtl *ctl, unsigned *err, int lt, int kv)
+template <typename C, int D, int kv>
+__device__ void rows_load(const AttParams &p, Cursor c, char *smem, RowsCtl *ctl, unsigned *err, int lt)
 {
     using S = RowsShape<C, D>;
-    constexpr int CH = D * static_cast<int>(sizeof(C)) / 16, RPI = 32 / CH, NST = S::STAGES;
+    constexpr int CH = D * static_cast<int>(sizeof(C)) / 16, RPI = 32 / CH;
+    constexpr int NST = S::WIDEN ? S::RAW_STAGES : kv ? S::V_STAGES : S::K_STAGES, AT = kv ? S::V_AT : S::K_AT;
     const int lane = lt & 31, w = lt >> 5, chunk = lane % CH, sub = lane / CH;
     const uint32_t base = smem_u32(smem);
-    const PoolView pool = kv ? p.c.v : p.c.k;
+    const PoolView &pool = kv ? p.c.v : p.c.k;
     uint64_t *full = kv ? ctl->v_full : ctl->k_full, *empty = kv ? ctl->v_empty : ctl->k_empty;
     const int mask = (1 << p.c.page_shift) - 1;
     int n = 0, item = 0;  // tiles issued, items with tiles
@@ -127,12 +139,15 @@ __device__ void rows_load(const AttParams &p, Cursor c, char *smem, RowsCtl *ctl
         const int st = t % NST;
         const int row0 = ctl->tail[4 * kv + w][st][0], token0 = ctl->tail[4 * kv + w][st][1], flags = ctl->tail[4 * kv + w][st][2];
         const char *raw = smem + S::RAW_AT + (st * 2 + kv) * S::RAW;
-        char *to = smem + S::KV_AT + kv * S::TILE;
+        char *to = smem + AT;
         if (t > 0 && !rows_wait(ctl, empty, (t - 1) & 1, err)) return false;
-#pragma unroll 4
+        uint4 in[CH];
+#pragma unroll
+        for (int i = 0; i < CH; ++i) in[i] = *reinterpret_cast<const uint4 *>(raw + (32 * w + i * RPI + sub) * D + chunk * 16);
+#pragma unroll
         for (int i = 0; i < CH; ++i) {
             const int row = 32 * w + i * RPI + sub;
-            const uint4 x = *reinterpret_cast<const uint4 *>(raw + row * D + chunk * 16);
+            const uint4 x = in[i];
             uint32_t b[4] = {x.x, x.y, x.z, x.w};
             if (kv && row >= row0 && chunk_not_finite<C>(x)) {
 #pragma unroll
@@ -182,6 +197,11 @@ __device__ void rows_load(const AttParams &p, Cursor c, char *smem, RowsCtl *ctl
             next = lookup(tile + 2);  // two tiles ahead: its latency is behind that of the rows
             uint32_t to;
             if (S::WIDEN) {  // the raw stages are each thread's own
+                if (n >= NST) {
+                    cp_async_wait<NST - 1>();
+                    if (!(ok = widen(n - NST))) break;
+                }
+                __syncwarp();
                 if (lane == 0) {
                     ctl->tail[4 * kv + w][st][0] = row0;
                     ctl->tail[4 * kv + w][st][1] = token0;
@@ -191,7 +211,7 @@ __device__ void rows_load(const AttParams &p, Cursor c, char *smem, RowsCtl *ctl
                 to = base + S::RAW_AT + (st * 2 + kv) * S::RAW;
             } else {
                 if (n >= NST && !(ok = rows_wait(ctl, &empty[st], (n / NST - 1) & 1, err))) break;
-                to = base + S::KV_AT + (st * 2 + kv) * S::TILE;
+                to = base + AT + st * S::TILE;
             }
 #pragma unroll 8
             for (int i = 0; i < CH; ++i) {
@@ -202,10 +222,6 @@ __device__ void rows_load(const AttParams &p, Cursor c, char *smem, RowsCtl *ctl
             }
             if (S::WIDEN) {
                 cp_async_commit();
-                if (n >= NST - 1) {
-                    cp_async_wait<NST - 1>();
-                    if (!(ok = widen(n - (NST - 1)))) break;
-                }
             } else if (kv && row0 < AR_KEYS) {
                 // Infinities and NaN in a new token's v: cleared here, as 0 x inf would reach rows that do not see it;
                 // the rows that do get them at the end.
@@ -230,7 +246,7 @@ __device__ void rows_load(const AttParams &p, Cursor c, char *smem, RowsCtl *ctl
     }
     asm volatile("cp.async.wait_all;" ::: "memory");
     if (S::WIDEN)  // the tiles still on their way
-        for (int t = n >= NST - 1 ? n - (NST - 1) : 0; ok && t < n; ++t) ok = widen(t);
+        for (int t = n >= NST ? n - NST : 0; ok && t < n; ++t) ok = widen(t);
 }
 
 // ------------------------------------------------------------------ products
@@ -248,57 +264,123 @@ __device__ __forceinline__ bool mbar_test(uint64_t *bar, uint32_t parity)
 // two ahead of the last tile whose probabilities were multiplied, and the
 // probabilities' product; neither waits for the other's operands.
 template <typename T, typename C, int D>
-__device__ void rows_multiply(const AttParams &p, Cursor c, char *smem, RowsCtl *ctl, unsigned *err)
+__device__ void rows_multiply(const AttParams &p, const Cursor &c0, char *smem, RowsCtl *ctl, unsigned *err)
 {
     using S = RowsShape<C, D>;
     using M = typename MmaOf<T, C>::type;
     constexpr bool BF = std::is_same<M, __nv_bfloat16>::value;
     constexpr uint32_t SHAPE_S = mma_shape(BF, false, AR_KEYS), SHAPE_O = mma_shape(BF, true, D);
-    constexpr int NST = S::WIDEN ? 1 : S::STAGES;  // of the multiplied tiles
+    constexpr int KST = S::K_STAGES, VST = S::V_STAGES;
     const uint32_t base = smem_u32(smem), tmem = ctl->tmem;
     const uint32_t tm_s = tmem, tm_p = tmem + 256, tm_o = tmem + 384;
-    int ns = 0, no = 0, item = 0;  // tiles whose scores, whose outputs were issued
-    for (; c.at < c.end; next_item(c, p.w, p.c)) {
-        const int tiles = last_tile(c) - first_tile(c);
-        if (tiles == 0) continue;
-        if (!rows_wait1(ctl, &ctl->q_full, item++ & 1, err)) return;
-        const int start = no, end = no + tiles;
-        uint32_t idle = 0;
-        while (no < end) {
-            if (ns < end && ns <= no + 1 && mbar_test(&ctl->k_full[ns % NST], (ns / NST) & 1)) {
-                tc_fence_after();
-                fence_async_shared();  // K was written by ordinary and asynchronous copies
-                const uint32_t k = base + S::KV_AT + (ns % NST) * 2 * S::TILE;
+    // the item of the next scores and that of the next outputs: where its tiles begin and end, its number
+    struct Side {
+        Cursor c;
+        int begin, end, item;
+    };
+    auto to_item_with_tiles = [&](Side &x) {
+        while (x.c.at < x.c.end && last_tile(x.c) == first_tile(x.c)) next_item(x.c, p.w, p.c);
+        x.begin = x.end;
+        if (x.c.at < x.c.end) x.end += last_tile(x.c) - first_tile(x.c);
+    };
+    Side sc{c0, 0, 0, 0}, ou{c0, 0, 0, 0};
+    to_item_with_tiles(sc);
+    to_item_with_tiles(ou);
+    int ns = 0, no = 0;  // tiles whose scores, whose outputs were issued
+    uint32_t idle = 0;
+    while (no < ou.end) {
+        if (ns < sc.end && ns <= no + 1 && mbar_test(&ctl->k_full[ns % KST], (ns / KST) & 1) &&
+            (ns > sc.begin || mbar_test(&ctl->q_full[sc.item & 1], (sc.item >> 1) & 1))) {
+            tc_fence_after();
+            fence_async_shared();  // K was written by asynchronous copies of threads, q by threads
+            const uint32_t k = base + S::K_AT + (ns % KST) * S::TILE, q = base + S::Q_AT + (sc.item & 1) * S::TILE;
 #pragma unroll
-                for (int ks = 0; ks < D / 16; ++ks) {
-                    const uint32_t off = (ks >> 2) * (AR_KEYS * 128) + (ks & 3) * 32;
-                    tc_mma(tm_s + (ns & 1) * AR_KEYS, desc_k_major(base + S::Q_AT + off), desc_k_major(k + off), SHAPE_S, ks > 0);
-                }
-                tc_commit(&ctl->s_full[ns & 1]);
-                tc_commit(&ctl->k_empty[ns % NST]);
-                ++ns;
-                idle = 0;
-            } else if (no < ns && mbar_test(&ctl->p_full[no & 1], (no >> 1) & 1) &&
-                       mbar_test(&ctl->v_full[no % NST], (no / NST) & 1)) {
-                tc_fence_after();
-                fence_async_shared();
-                const uint32_t v = base + S::KV_AT + S::TILE + (no % NST) * 2 * S::TILE;
-#pragma unroll
-                for (int ks = 0; ks < AR_KEYS / 16; ++ks)
-                    tc_mma_ta(tm_o, tm_p + (no & 1) * (AR_KEYS / 2) + ks * 8, desc_n_major(v + ks * 2048, AR_KEYS * 128), SHAPE_O,
-                              no > start || ks > 0);
-                tc_commit(&ctl->o_done[no & 1]);
-                tc_commit(&ctl->v_empty[no % NST]);
-                ++no;
-                idle = 0;
-            } else if (++idle == 4 * WAIT_LIMIT) {
-                *reinterpret_cast<volatile int *>(&ctl->dead) = 1;
-                atomicExch(err, static_cast<unsigned>(STATUS_TIMEOUT));
-                return;
-            } else if ((idle & 63) == 63 && *reinterpret_cast<volatile int *>(&ctl->dead)) {
-                return;
+            for (int ks = 0; ks < D / 16; ++ks) {
+                const uint32_t off = (ks >> 2) * (AR_KEYS * 128) + (ks & 3) * 32;
+                tc_mma(tm_s + (ns & 1) * AR_KEYS, desc_k_major(q + off), desc_k_major(k + off), SHAPE_S, ks > 0);
             }
+            tc_commit(&ctl->s_full[ns & 1]);
+            tc_commit(&ctl->k_empty[ns % KST]);
+            if (++ns == sc.end) {
+                next_item(sc.c, p.w, p.c);
+                ++sc.item;
+                to_item_with_tiles(sc);
+            }
+            idle = 0;
+        } else if (no < ns && mbar_test(&ctl->p_full[no & 1], (no >> 1) & 1) && mbar_test(&ctl->v_full[no % VST], (no / VST) & 1)) {
+            tc_fence_after();
+            fence_async_shared();
+            const uint32_t v = base + S::V_AT + (no % VST) * S::TILE;
+#pragma unroll
+            for (int ks = 0; ks < AR_KEYS / 16; ++ks)
+                tc_mma_ta(tm_o, tm_p + (no & 1) * (AR_KEYS / 2) + ks * 8, desc_n_major(v + ks * 2048, AR_KEYS * 128), SHAPE_O,
+                          no > ou.begin || ks > 0);
+            tc_commit(&ctl->o_done[no & 1]);
+            tc_commit(&ctl->v_empty[no % VST]);
+            if (++no == ou.end) {
+                next_item(ou.c, p.w, p.c);
+                to_item_with_tiles(ou);
+            }
+            idle = 0;
+        } else if (++idle == 4 * WAIT_LIMIT) {
+            *reinterpret_cast<volatile int *>(&ctl->dead) = 1;
+            atomicExch(err, static_cast<unsigned>(STATUS_TIMEOUT));
+            return;
+        } else if ((idle & 63) == 63 && *reinterpret_cast<volatile int *>(&ctl->dead)) {
+            return;
         }
+    }
+}
+
+// ------------------------------------------------------------------ q
+// Three warps, an item ahead of the others: q of every copy's rows, and what
+// the new tokens see.  For an e4m3 cache each row by a power of two into f16's
+// range.
+template <typename T, typename C, int D, int COLS>
+__device__ void rows_prepare(const AttParams &p, Cursor c, char *smem, RowsCtl *ctl, unsigned *err, int lt)
+{
+    using S = RowsShape<C, D>;
+    using M = typename MmaOf<T, C>::type;
+    int item = 0;
+    for (; c.at < c.end; next_item(c, p.w, p.c)) {
+        if (first_tile(c) == last_tile(c)) continue;
+        const int place = item & 1, row0 = c.row_tile * COLS, live = min(COLS, p.rows - row0);
+        char *qs = smem + S::Q_AT + place * S::TILE;
+        if (item >= 2 && !rows_wait(ctl, &ctl->q_empty[place], ((item >> 1) - 1) & 1, err)) return;
+        for (int t = lt; t < p.w.T; t += 96)
+            ctl->sees[place][t] = t < c.s.fresh ? visible_mask(p.parent ? p.parent + static_cast<int64_t>(c.b) * p.w.T : nullptr, t) : 0ull;
+        constexpr int CH = D / 8, STEP = 96 / CH;  // rows at a time: 6 or 12
+        for (int r0 = 0; r0 < COLS; r0 += STEP) {
+            const int r = r0 + lt / CH, ch = lt % CH, t = (row0 + r) / p.group, g = (row0 + r) - t * p.group;
+            uint4 raw = make_uint4(0, 0, 0, 0);
+            if (r < live && t < c.s.fresh)
+                raw = *reinterpret_cast<const uint4 *>(static_cast<const T *>(p.q) +
+                                                       ((static_cast<int64_t>(c.b) * p.w.T + t) * p.q_heads + c.h * p.group + g) * D + ch * 8);
+            if (S::WIDEN) {
+                const T *y = reinterpret_cast<const T *>(&raw);
+                float x[8], top = 0.0f;
+#pragma unroll
+                for (int e = 0; e < 8; ++e) {
+                    x[e] = Num<T>::up(y[e]);
+                    top = fabsf(x[e]) < CUDART_INF_F ? fmaxf(top, fabsf(x[e])) : top;
+                }
+#pragma unroll
+                for (int o = CH / 2; o; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+                const int e2 = top > 0.0f ? max(-120, min(120, 14 - ilogbf(top))) : 0;
+                const float up = exp2f(static_cast<float>(e2));
+                if (ch == 0 && r < COLS)
+#pragma unroll
+                    for (int k = 0; k < AR_ROWS; k += COLS) ctl->q_power[place][k + r] = static_cast<signed char>(e2);
+                raw = make_uint4(pack_mma<M>(x[0] * up, x[1] * up), pack_mma<M>(x[2] * up, x[3] * up),
+                                 pack_mma<M>(x[4] * up, x[5] * up), pack_mma<M>(x[6] * up, x[7] * up));
+            }
+            if (r < COLS)
+#pragma unroll
+                for (int k = 0; k < AR_ROWS; k += COLS) *reinterpret_cast<uint4 *>(qs + panel_at(k + r, ch)) = raw;
+        }
+        fence_async_shared();
+        mbar_arrive(&ctl->q_full[place]);
+        ++item;
     }
 }
 
@@ -317,7 +399,6 @@ __device__ void rows_softmax(const AttParams &p, Cursor c, char *smem, RowsCtl *
     const uint32_t tm_s = ctl->tmem + quarter + copy * COLS, tm_p = ctl->tmem + quarter + 256 + copy * (COLS / 2),
                    tm_o = ctl->tmem + quarter + 384;
     const long long begin = c.at;
-    float *merge = reinterpret_cast<float *>(smem + S::Q_AT);  // q's place, once a piece's scores are done
     // the keys of other copies never get a probability
     if (COPIES > 1) {
         uint32_t zero[32];
@@ -334,51 +415,21 @@ __device__ void rows_softmax(const AttParams &p, Cursor c, char *smem, RowsCtl *
         const float v_scale = p.c.v_scale ? __ldg(p.c.v_scale + c.h) : 1.0f;
         const bool mine = r < live;
         const int token = (row0 + r) / p.group;
-        const unsigned long long see =
-            mine && token < c.s.fresh && !c.s.bad
-                ? visible_mask(p.parent ? p.parent + static_cast<int64_t>(c.b) * p.w.T : nullptr, token)
-                : 0ull;
+        unsigned long long see = 0;
         float m = -CUDART_INF_F, l = 0.0f;
         float factor = p.scale_log2 * (p.c.k_scale ? __ldg(p.c.k_scale + c.h) : 1.0f);
         unsigned long long odd = 0;
-        bool any_bad = c.s.bad;
+        bool any_bad = c.s.bad, ok = true;
+        const int place = item & 1;
+        using Merge = RowsMerge<D>;
+        static_assert(sizeof(Merge) <= S::TILE, "the exchange fits q's place");
+        Merge *merge = reinterpret_cast<Merge *>(smem + S::Q_AT + place * S::TILE);  // once all scores are there
         if (t0 < t1) {
-            // q of every copy's rows; for an e4m3 cache each row by a power of two into f16's range
-            for (int i = tid; i < AR_ROWS * (D / 8); i += 128) {
-                const int tr = i / (D / 8), ch = i - tr * (D / 8), rr = tr % COLS, t = (row0 + rr) / p.group,
-                          g = (row0 + rr) - t * p.group;
-                uint4 raw = make_uint4(0, 0, 0, 0);
-                if (rr < live && t < c.s.fresh)
-                    raw = *reinterpret_cast<const uint4 *>(
-                        static_cast<const T *>(p.q) +
-                        ((static_cast<int64_t>(c.b) * p.w.T + t) * p.q_heads + c.h * p.group + g) * D + ch * 8);
-                if (S::WIDEN) {
-                    const T *y = reinterpret_cast<const T *>(&raw);
-                    float x[8], top = 0.0f;
-#pragma unroll
-                    for (int e = 0; e < 8; ++e) {
-                        x[e] = Num<T>::up(y[e]);
-                        top = fabsf(x[e]) < CUDART_INF_F ? fmaxf(top, fabsf(x[e])) : top;
-                    }
-#pragma unroll
-                    for (int o = D / 16; o; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
-                    const int e2 = top > 0.0f ? max(-120, min(120, 14 - ilogbf(top))) : 0;
-                    const float up = exp2f(static_cast<float>(e2));
-                    if (ch == 0) ctl->ms[tr] = exp2f(static_cast<float>(-e2));
-                    raw = make_uint4(pack_mma<M>(x[0] * up, x[1] * up), pack_mma<M>(x[2] * up, x[3] * up),
-                                     pack_mma<M>(x[4] * up, x[5] * up), pack_mma<M>(x[6] * up, x[7] * up));
-                }
-                *reinterpret_cast<uint4 *>(smem + S::Q_AT + panel_at(tr, ch)) = raw;
-            }
-            fence_async_shared();
-            mbar_arrive(&ctl->q_full);
-            if (S::WIDEN) {
-                rows_sync();
-                factor *= ctl->ms[tid];
-            }
+            ok = rows_wait(ctl, &ctl->q_full[place], (item >> 1) & 1, err);
+            if (mine && token < c.s.fresh) see = ctl->sees[place][token];
+            if (S::WIDEN) factor *= exp2f(-static_cast<float>(ctl->q_power[place][tid]));
             const bool works = __any_sync(0xffffffffu, mine);
-            bool ok = true;
-            for (int tile = t0; tile < t1; ++tile, ++n) {
+            for (int tile = t0; ok && tile < t1; ++tile, ++n) {
                 if (!(ok = rows_wait(ctl, &ctl->s_full[n & 1], (n >> 1) & 1, err))) break;
                 tc_fence_after();
                 __syncwarp();
@@ -452,35 +503,41 @@ __device__ void rows_softmax(const AttParams &p, Cursor c, char *smem, RowsCtl *
             }
             if (ok) ok = rows_wait(ctl, &ctl->o_done[(n - 1) & 1], ((n - 1) >> 1) & 1, err);
             tc_fence_after();
-            odd = *reinterpret_cast<volatile unsigned long long *>(&ctl->odd[item % AR_ITEMS]);
-            any_bad |= *reinterpret_cast<volatile int *>(&ctl->bad[item % AR_ITEMS]) != 0;
+            odd = *reinterpret_cast<volatile unsigned long long *>(&ctl->odd[item_flags(item)]);
+            any_bad |= *reinterpret_cast<volatile int *>(&ctl->bad[item_flags(item)]) != 0;
+            rows_sync();  // all have read them, and all scores
         }
         if (see == 0) {
             m = -CUDART_INF_F;
             l = 0.0f;
         }
-        rows_sync();  // the scale factors in ms are read
-        ctl->ms[tid] = m;
-        ctl->ls[tid] = l;
+        const bool tiles = t0 < t1;
+        if (tiles) {
+            merge->ms[tid] = m;
+            merge->ls[tid] = l;
+        }
         if (tid == 0) {
             ctl->stop = *reinterpret_cast<volatile int *>(&ctl->dead);
-            if (t0 < t1) {
-                ctl->odd[item % AR_ITEMS] = 0;
-                ctl->bad[item % AR_ITEMS] = 0;
+            if (tiles) {
+                ctl->odd[item_flags(item)] = 0;
+                ctl->bad[item_flags(item)] = 0;
             }
         }
         rows_sync();
-        if (t0 < t1) ++item;
         const bool stop = *reinterpret_cast<volatile int *>(&ctl->stop) != 0;
         any_bad |= stop;
         float all_m = -CUDART_INF_F, all_l = 0.0f;
+        if (tiles) {
 #pragma unroll
-        for (int k = 0; k < COPIES; ++k) all_m = fmaxf(all_m, ctl->ms[k * COLS + r]);
+            for (int k = 0; k < COPIES; ++k) all_m = fmaxf(all_m, merge->ms[k * COLS + r]);
+        }
         const float base = all_m == -CUDART_INF_F ? 0.0f : all_m, mine_a = l == 0.0f ? 0.0f : fast_exp2(m - base);
+        if (tiles) {
 #pragma unroll
-        for (int k = 0; k < COPIES; ++k) {
-            const float lk = ctl->ls[k * COLS + r];
-            if (lk != 0.0f) all_l += lk * fast_exp2(ctl->ms[k * COLS + r] - base);
+            for (int k = 0; k < COPIES; ++k) {
+                const float lk = merge->ls[k * COLS + r];
+                if (lk != 0.0f) all_l += lk * fast_exp2(merge->ms[k * COLS + r] - base);
+            }
         }
         const bool whole = c.s.total == 0 || (t0 == 0 && t1 == c.tiles);
         float *part = p.parts + (static_cast<int64_t>(blockIdx.x) * 2 + (c.first < begin ? 0 : 1)) * PART;
@@ -499,9 +556,11 @@ __device__ void rows_softmax(const AttParams &p, Cursor c, char *smem, RowsCtl *
         }
 #pragma unroll 1
         for (int d0 = 0; d0 < D; d0 += 32) {
+            // each 32 columns are put together by another copy
+            const int keeper = (d0 >> 5) % COPIES;
             float x[32];
             __syncwarp();
-            if (t0 < t1 && !stop) {
+            if (tiles && !stop) {
                 uint32_t y[32];
                 tc_ld32(y, tm_o + d0);
 #pragma unroll
@@ -510,21 +569,23 @@ __device__ void rows_softmax(const AttParams &p, Cursor c, char *smem, RowsCtl *
 #pragma unroll
                 for (int k = 0; k < 32; ++k) x[k] = 0.0f;
             }
-            if (COPIES > 1) {
-                if (copy > 0) {
+            if (COPIES > 1 && tiles) {
+                float *buf = merge->x[(d0 >> 5) % Merge::ROUNDS];
+                if (Merge::ROUNDS == 1 && d0 > 0) rows_sync();
+                if (copy != keeper) {
+                    float *to = buf + (((copy - keeper + COPIES) % COPIES - 1) * COLS + r) * 33;
 #pragma unroll
-                    for (int k = 0; k < 32; ++k) merge[((copy - 1) * COLS + r) * 33 + k] = x[k];
+                    for (int k = 0; k < 32; ++k) to[k] = x[k];
                 }
                 rows_sync();
-                if (copy == 0) {
+                if (copy == keeper) {
 #pragma unroll
-                    for (int q = 1; q < COPIES; ++q)
+                    for (int q = 0; q < COPIES - 1; ++q)
 #pragma unroll
-                        for (int k = 0; k < 32; ++k) x[k] += merge[((q - 1) * COLS + r) * 33 + k];
+                        for (int k = 0; k < 32; ++k) x[k] += buf[(q * COLS + r) * 33 + k];
                 }
-                rows_sync();
             }
-            if (copy != 0 || !mine) continue;
+            if (copy != keeper || !mine) continue;
             if (odd) {
                 // New tokens whose v has infinities or NaN (cleared for the product): for the rows that see them.
                 for (unsigned long long left = odd & see; left; left &= left - 1) {
@@ -546,26 +607,29 @@ __device__ void rows_softmax(const AttParams &p, Cursor c, char *smem, RowsCtl *
                     }
                 }
             }
+            if (!whole) {
 #pragma unroll
-            for (int k = 0; k < 32; k += 4) {
-                const float4 y = make_float4(x[k], x[k + 1], x[k + 2], x[k + 3]);
-                if (!whole) {
-                    *reinterpret_cast<float4 *>(part + 2 * AR_ROWS + r * D + d0 + k) = y;
-                } else {
-                    uint2 z = make_uint2(pack_mma<T>(y.x * out_scale, y.y * out_scale), pack_mma<T>(y.z * out_scale, y.w * out_scale));
-                    if (fixed) z = make_uint2(pack_mma<T>(instead, instead), pack_mma<T>(instead, instead));
-                    *reinterpret_cast<uint2 *>(static_cast<T *>(p.out) + row_at * D + d0 + k) = z;
-                }
+                for (int k = 0; k < 32; k += 4)
+                    *reinterpret_cast<float4 *>(part + 2 * AR_ROWS + r * D + d0 + k) = make_float4(x[k], x[k + 1], x[k + 2], x[k + 3]);
+            } else {
+#pragma unroll
+                for (int k = 0; k < 32; ++k) x[k] = fixed ? instead : x[k] * out_scale;
+#pragma unroll
+                for (int k = 0; k < 32; k += 8)
+                    *reinterpret_cast<uint4 *>(static_cast<T *>(p.out) + row_at * D + d0 + k) =
+                        make_uint4(pack_mma<T>(x[k], x[k + 1]), pack_mma<T>(x[k + 2], x[k + 3]), pack_mma<T>(x[k + 4], x[k + 5]),
+                                   pack_mma<T>(x[k + 6], x[k + 7]));
             }
         }
         tc_fence_before();
-        bool seq_bad = any_bad, wrote = whole;
-        if (!whole) {
-            rows_sync();  // ms and ls are free
-            wrote = join_pieces<T, D, AR_ROWS, 128>(p, rows, c, tid, ctl->ms, ctl->ls, &ctl->flag, v_scale, rows_sync);
-            if (wrote) seq_bad = ctl->ms[0] != ctl->ms[0];
+        if (!whole)
+            note_split(p, c, rows, begin, tid);
+        else if (tid == 0 && p.row_status && c.h == 0 && c.row_tile == 0)
+            p.row_status[c.b] = any_bad ? KV_STATUS_BAD : 0;
+        if (tiles) {
+            mbar_arrive(&ctl->q_empty[place]);
+            ++item;
         }
-        if (wrote && tid == 0 && p.row_status && c.h == 0 && c.row_tile == 0) p.row_status[c.b] = seq_bad ? KV_STATUS_BAD : 0;
         rows_sync();
         if (stop) break;
     }
@@ -581,6 +645,8 @@ __global__ void __launch_bounds__(AR_THREADS, 1) attention_rows_kernel(const Att
     const int tid = threadIdx.x, warp = tid >> 5;
     unsigned *err = p.error;
     const Cursor c = find_range(p.w, p.c, blockIdx.x, gridDim.x, tid & 31);
+    dependents_launch();
+    if (tid < 2) p.split[blockIdx.x * 2 + tid].n = 0;
     if (c.at == c.end) return;  // the whole block
     if (tid == 0) {
         for (int i = 0; i < 5; ++i) {
@@ -594,7 +660,10 @@ __global__ void __launch_bounds__(AR_THREADS, 1) attention_rows_kernel(const Att
             mbar_init(&ctl->p_full[i], 128);
             mbar_init(&ctl->o_done[i], 1);
         }
-        mbar_init(&ctl->q_full, 128);
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(&ctl->q_full[i], 96);
+            mbar_init(&ctl->q_empty[i], 128);
+        }
         mbar_init(&ctl->spare, 1);
         for (int i = 0; i < AR_ITEMS; ++i) ctl->odd[i] = 0, ctl->bad[i] = 0;
         ctl->dead = ctl->stop = 0;
@@ -618,9 +687,13 @@ __global__ void __launch_bounds__(AR_THREADS, 1) attention_rows_kernel(const Att
             }
         }
         __syncwarp();
+        if (warp > 4) rows_prepare<T, C, D, COLS>(p, c, smem, ctl, err, tid - 160);
     } else {
         asm volatile("setmaxnreg.dec.sync.aligned.u32 112;");
-        rows_load<C, D>(p, c, smem, ctl, err, tid & 127, warp >= 12);
+        if (warp < 12)
+            rows_load<C, D, 0>(p, c, smem, ctl, err, tid & 127);
+        else
+            rows_load<C, D, 1>(p, c, smem, ctl, err, tid & 127);
     }
     tc_fence_before();
     __syncthreads();
@@ -634,12 +707,13 @@ template <typename T, typename C, int D, int COLS> static cudaError_t launch_col
     constexpr int SMEM = S::CTL_AT + static_cast<int>(sizeof(RowsCtl)) + 1024;
     static_assert(SMEM <= 232448, "shared memory of a block");
     auto kernel = attention_rows_kernel<T, C, D, COLS>;
-    const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, SMEM);
+    cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, SMEM);
     if (e != cudaSuccess) return e;
     p.w.tile = AR_KEYS;
     p.w.row_tiles = (p.rows + COLS - 1) / COLS;
     kernel<<<ATT_SMS, AR_THREADS, SMEM, st>>>(p);
-    return cudaGetLastError();
+    e = cudaGetLastError();
+    return e != cudaSuccess ? e : launch_join(p, std::is_same<T, __half>::value ? SPV_F16 : SPV_BF16, D, AR_ROWS, ATT_SMS, st);
 }
 template <typename T, typename C, int D> static cudaError_t launch_dim(const AttParams &p, cudaStream_t st)
 {

@@ -116,11 +116,21 @@ __device__ __forceinline__ int range_owner(const Cursor &c, long long x)
 __device__ __forceinline__ Cursor find_range(const Work &w, const PagedView &v, int block, int grid, int lane)
 {
     const int per = w.row_tiles * v.kv_heads;
+    // Tiles of sequences lane, lane + 32, ...: the first KEEP of them stay in registers, their loads all under way
+    // at once (a load is about a microsecond when the lengths come from memory).
+    constexpr int KEEP = 8;
+    int tiles[KEEP];
     long long sum = 0;
-    for (int b = lane; b < w.B; b += 32)
-        sum += static_cast<long long>(tiles_of(w, seq_lens(w.ctx_lens, w.new_lens, b, w.T, v, w.idle))) * per;
+#pragma unroll
+    for (int i = 0; i < KEEP; ++i) {
+        const int b = 32 * i + lane;
+        tiles[i] = b < w.B ? tiles_of(w, seq_lens(w.ctx_lens, w.new_lens, b, w.T, v, w.idle)) : 0;
+        sum += tiles[i];
+    }
+    for (int b = 32 * KEEP + lane; b < w.B; b += 32) sum += tiles_of(w, seq_lens(w.ctx_lens, w.new_lens, b, w.T, v, w.idle));
 #pragma unroll
     for (int o = 16; o; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+    sum *= per;
     Cursor c{};
     c.all = sum;
     c.blocks = sum < grid ? static_cast<int>(sum) : grid;
@@ -128,10 +138,9 @@ __device__ __forceinline__ Cursor find_range(const Work &w, const PagedView &v, 
     c.at = range_begin(c, block);
     c.end = range_begin(c, block + 1);
     long long before = 0;
-    for (int b0 = 0; b0 < w.B; b0 += 32) {
-        const int b = b0 + lane;
-        long long n = 0;
-        if (b < w.B) n = static_cast<long long>(tiles_of(w, seq_lens(w.ctx_lens, w.new_lens, b, w.T, v, w.idle))) * per;
+    bool found = false;
+    auto look = [&](int b0, int mine) {  // among sequences b0 .. b0 + 31, whose tiles the lanes have
+        const long long n = static_cast<long long>(mine) * per;
         long long upto = n;
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
@@ -143,9 +152,17 @@ __device__ __forceinline__ Cursor find_range(const Work &w, const PagedView &v, 
             const int l = __ffs(here) - 1;
             c.b = b0 + l;
             before += __shfl_sync(0xffffffffu, upto - n, l);
-            break;
+            found = true;
+        } else {
+            before += __shfl_sync(0xffffffffu, upto, 31);
         }
-        before += __shfl_sync(0xffffffffu, upto, 31);
+    };
+#pragma unroll
+    for (int i = 0; i < KEEP; ++i)
+        if (!found && 32 * i < w.B) look(32 * i, tiles[i]);
+    for (int b0 = 32 * KEEP; !found && b0 < w.B; b0 += 32) {
+        const int b = b0 + lane;
+        look(b0, b < w.B ? tiles_of(w, seq_lens(w.ctx_lens, w.new_lens, b, w.T, v, w.idle)) : 0);
     }
     c.s = seq_lens(w.ctx_lens, w.new_lens, c.b, w.T, v, w.idle);
     c.tiles = tiles_of(w, c.s);
