@@ -717,7 +717,9 @@ template <typename T, typename C, int D, int COLS> static cudaError_t launch_col
 }
 template <typename T, typename C, int D> static cudaError_t launch_dim(const AttParams &p, cudaStream_t st)
 {
-    if (p.rows <= 32) return launch_cols<T, C, D, 32>(p, st);
+    if constexpr (sizeof(C) == 2) {  // an e4m3 cache comes here with more than 32 rows
+        if (p.rows <= 32) return launch_cols<T, C, D, 32>(p, st);
+    }
     if (p.rows <= 64) return launch_cols<T, C, D, 64>(p, st);
     return launch_cols<T, C, D, 128>(p, st);
 }
