@@ -168,23 +168,43 @@ __global__ void __launch_bounds__(MASS_THREADS, MassShape<C, D>::BLOCKS_PER_SM) 
                 if (r0 > 0) return p.mass_out[out_row + j];
                 return p.mass_in && j < c.s.ctx ? p.decay * p.mass_in[out_row + j] : 0.0f;
             };
+            // lanes 0..15: the page (-1: nothing is written) and the old mass of this lane's key of a tile, asked for
+            // a tile ahead
+            auto page_for = [&](int tile) {
+                const int j = tile * MASS_KEYS + warp * 16 + lane;
+                return lane < 16 && tile < t_end && j < c.s.total ? __ldg(table + (j >> p.c.page_shift)) : -1;
+            };
+            auto mass_for = [&](int tile) {
+                const int j = tile * MASS_KEYS + warp * 16 + lane;
+                return lane < 16 && tile < t_end && j < c.s.total ? carried(j) : 0.0f;
+            };
+            int next_page = page_for(t0);
+            float next_mass = mass_for(t0);
             for (int tile = t0; tile < t_end; ++tile) {
                 __syncwarp();
                 issue(tile + NST - 1);
-                // the slice's page again, for who writes: bad ones are left alone
                 const int j0 = tile * MASS_KEYS + warp * 16;
                 if (j0 >= c.s.total) break;
-                const int j = j0 + (lane & 15);
-                const bool writes = lane < 16 && j < c.s.total && page_of(p.c, table, j) >= 0;
-                const float old = writes ? carried(j) : 0.0f;
+                const int j = j0 + lane, page = next_page;
+                const float old = next_mass;
+                next_page = page_for(tile + 1);
+                next_mass = mass_for(tile + 1);
                 cp_async_wait<NST - 1>();
                 __syncwarp();
                 const uint32_t slice = ring + ((tile - t0) % NST) * S::SLICE;
+                uint32_t kf[D / 16][4];
+                get_k<C, D>(kf, slice, lane);
                 const bool tail = j0 + 16 > c.s.ctx;
                 float sum[2][2] = {{0.0f, 0.0f}, {0.0f, 0.0f}};  // [key tile][column]
                 for (int g = 0; g < groups; ++g) {
-                    float s[1][2][4];
-                    slice_scores<M, C, D, 1>(s, slice, lane, [&](int, int ks, uint32_t (&a)[4]) { get_q<D>(a, qs32, g, ks, lane); });
+                    float s[2][4] = {{0.0f, 0.0f, 0.0f, 0.0f}, {0.0f, 0.0f, 0.0f, 0.0f}};
+#pragma unroll
+                    for (int ks = 0; ks < D / 16; ++ks) {
+                        uint32_t a[4];
+                        get_q<D>(a, qs32, g, ks, lane);
+                        mma16816<M>(s[0], a, kf[ks][0], kf[ks][1]);
+                        mma16816<M>(s[1], a, kf[ks][2], kf[ks][3]);
+                    }
 #pragma unroll
                     for (int i = 0; i < 2; ++i) {
                         const int r = g * 16 + i * 8 + (lane >> 2);
@@ -193,7 +213,7 @@ __global__ void __launch_bounds__(MASS_THREADS, MassShape<C, D>::BLOCKS_PER_SM) 
                         for (int k = 0; k < 2; ++k)
 #pragma unroll
                             for (int e = 0; e < 2; ++e) {
-                                float w = fast_exp2(s[0][k][2 * i + e] * f - z);
+                                float w = fast_exp2(s[k][2 * i + e] * f - z);
                                 if (tail) {
                                     const int key = j0 + 8 * k + 2 * (lane & 3) + e;
                                     if (!(key < c.s.ctx || (key < c.s.total && (sees[r] >> (key - c.s.ctx) & 1)))) w = 0.0f;
@@ -215,7 +235,7 @@ __global__ void __launch_bounds__(MASS_THREADS, MassShape<C, D>::BLOCKS_PER_SM) 
                 const float a = __shfl_sync(0xffffffffu, sum[0][0], from), b = __shfl_sync(0xffffffffu, sum[0][1], from);
                 const float d = __shfl_sync(0xffffffffu, sum[1][0], from), e = __shfl_sync(0xffffffffu, sum[1][1], from);
                 const float mine = (lane & 8) ? ((lane & 1) ? e : d) : ((lane & 1) ? b : a);
-                if (writes) p.mass_out[out_row + j] = old + mine;
+                if (static_cast<unsigned>(page) < static_cast<unsigned>(p.c.num_pages)) p.mass_out[out_row + j] = old + mine;
             }
             cp_async_wait<0>();
             if (rows == 0)
