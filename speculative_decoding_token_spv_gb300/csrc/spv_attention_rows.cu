@@ -114,12 +114,6 @@ template <typename C> __device__ __forceinline__ uint4 finite_only(uint4 x)
 __device__ __forceinline__ int item_flags(int item) { return item % AR_ITEMS; }
 
 // ------------------------------------------------------------------ loaders
-// Arrives on `bar` once this thread's asynchronous copies so far have landed.
-__device__ __forceinline__ void cp_async_arrive(uint64_t *bar)
-{
-    asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(smem_u32(bar)) : "memory");
-}
-
 // One of two groups of four warps: K (kv = 0) or V.
 template <typename C, int D, int kv>
 __device__ void rows_load(const AttParams &p, Cursor c, char *smem, RowsCtl *ctl, unsigned *err, int lt)

@@ -3,21 +3,30 @@
 //
 // The weights are recomputed from q, K and the attention's log-sum-exp:
 // exp(s - lse) needs no second pass and no maximum, so K is read once, no
-// score is kept between the calls and no piece has to be joined.  The work is
-// cut along the cache as in the attention (Work, Cursor); each warp has its own
-// ring of 16-key slices, filled by asynchronous copies, and takes a slice's
-// fragments through the tensor cores against the counted rows, 16 at a time
-// from shared memory.  What a slice's 16 keys received is a sum over rows: a
-// thread's two rows, then a butterfly over the eight threads that share its
-// columns.
+// score is kept between the calls and no piece has to be joined.  Per 128-key
+// tile the 5th-generation tensor cores give the transposed scores, a key a
+// lane and a counted row a column of tensor memory: the sum over the rows is
+// then a thread's own, with no exchange between threads.  (On warp-level tensor
+// cores, whose lanes share a key's column, masks, exchanges and fragments came
+// to 750 instructions per 16 keys: 329 us for the case below.)
+//
+// One block an SM has an equal range of all tiles (Work, Cursor).  Two groups
+// of four loader warps take turns at the tiles, gathering K through the page
+// table with asynchronous copies (e4m3 is widened to f16 by the thread that
+// loaded it); three warps bring q and the rows' constants an item ahead; one
+// thread issues the products; four warps, a key a thread, sum and write.
+//
+// Every wait is bounded; one that gives up ends the block in order and leaves
+// SPV_ERR_TIMEOUT in the row_status of the sequence that it was at.
 #include "spv_mma.cuh"
+#include "spv_tcgen.cuh"
 
 namespace spv {
 
-constexpr int MASS_WARPS = 4;
-constexpr int MASS_THREADS = 32 * MASS_WARPS;
-constexpr int MASS_KEYS = 16 * MASS_WARPS;
 constexpr int MASS_SMS = 152;
+constexpr int MASS_KEYS = 128;
+constexpr int MASS_THREADS = 512;  // warps 0-3 keys, 4 products, 5-7 q, 8-11 and 12-15 K
+constexpr int MASS_BUFFERS = 4;    // of scores in tensor memory, 128 columns each
 
 struct MassParams {
     PagedView c;
@@ -54,204 +63,425 @@ __device__ __forceinline__ unsigned long long counted_tokens(const MassParams &p
     return m;
 }
 
-// Rows that a block holds in shared memory at once; more go in several passes
-// over the slices (from the L2, for the second time).
-template <typename C, int D> struct MassShape {
-    static constexpr int ROW_BYTES = D * static_cast<int>(sizeof(C));
-    static constexpr int SLICE = 16 * ROW_BYTES;
-    static constexpr int STAGES = 16384 / SLICE < 2 ? 2 : 16384 / SLICE > 8 ? 8 : 16384 / SLICE;
-    static constexpr int ROWS = D == 256 ? 32 : 64;
-    static constexpr int Q = ROWS * D * 2;
-    static constexpr int SMEM = Q + MASS_WARPS * STAGES * SLICE;
-    static constexpr int BLOCKS_PER_SM = SMEM * 3 <= 216 * 1024 ? 3 : 2;
+// The tokens that count and the rows that they make, of the item's sequence;
+// no rows where they are out of range (`bad`).  Kept while the heads of a
+// sequence pass by.
+struct Counted {
+    int b = -1, rows = 0;
+    unsigned long long tokens = 0;
+    bool bad = false;
+    __device__ __forceinline__ void at(const MassParams &p, const Cursor &c)
+    {
+        if (c.b == b) return;
+        b = c.b;
+        bad = c.s.bad || c.s.total > p.stride;
+        tokens = counted_tokens(p, b, &bad);
+        if (c.s.fresh < 64) tokens &= (1ull << (c.s.fresh < 0 ? 0 : c.s.fresh)) - 1ull;
+        rows = bad || c.s.total == 0 ? 0 : __popcll(tokens) * p.group;
+    }
 };
 
-template <typename T, typename C, int D>
-__global__ void __launch_bounds__(MASS_THREADS, MassShape<C, D>::BLOCKS_PER_SM) mass_kernel(const MassParams p)
+// ROWS rows at once; more go in several passes over the item's tiles.
+template <typename C, int D> struct MassShape {
+    static constexpr bool WIDEN = sizeof(C) == 1;
+    static constexpr int ROWS = D == 256 ? (WIDEN ? 32 : 64) : 128;
+    static constexpr int Q = ROWS * D * 2, TILE = MASS_KEYS * D * 2, RAW = MASS_KEYS * D;
+    // Both even: a stage is always the same group's, which so meets its barrier's phases one by one.
+    static constexpr int K_STAGES = WIDEN ? (D == 64 ? 4 : 2) : (D == 64 ? 8 : D == 128 ? 4 : 2);
+    static constexpr int RAW_STAGES = WIDEN ? (D == 64 ? 8 : D == 128 ? 4 : 2) : 0;
+    static constexpr int Q_AT = 0, K_AT = 2 * Q, RAW_AT = K_AT + K_STAGES * TILE, CTL_AT = RAW_AT + RAW_STAGES * RAW;
+};
+
+template <int ROWS> struct MassCtl {
+    uint64_t k_full[8], k_empty[8], s_full[MASS_BUFFERS], s_empty[MASS_BUFFERS], q_full[2], q_empty[2], spare;
+    unsigned long long sees[2][ROWS];
+    alignas(16) float2 row[2][ROWS];  // (read in pairs) what a unit of the stored q.k stands for, and the log-sum-exp, in powers of two
+    int careful[2];       // number (from 1) of the last pass in which some row gives nothing: masks are then looked at everywhere
+    uint32_t tmem;
+    int dead;
+};
+
+template <typename Ctl> __device__ __forceinline__ bool mass_wait1(Ctl *ctl, uint64_t *bar, uint32_t parity)
+{
+    for (uint32_t i = 0; i < WAIT_LIMIT; ++i) {
+        if (mbar_try_wait(bar, parity)) return true;
+        if ((i & 63) == 63 && *reinterpret_cast<volatile int *>(&ctl->dead)) return false;
+    }
+    *reinterpret_cast<volatile int *>(&ctl->dead) = 1;
+    return false;
+}
+template <typename Ctl> __device__ __forceinline__ bool mass_wait(Ctl *ctl, uint64_t *bar, uint32_t parity)
+{
+    return __all_sync(0xffffffffu, mass_wait1(ctl, bar, parity));
+}
+
+__device__ __forceinline__ int mass_first(const Cursor &c) { return static_cast<int>(c.at - c.first); }
+__device__ __forceinline__ int mass_last(const Cursor &c)
+{
+    if (c.s.total == 0) return mass_first(c);
+    const long long e = c.first + c.tiles;
+    return static_cast<int>((c.end < e ? c.end : e) - c.first);
+}
+// Byte of 16-byte chunk `chunk` of row `row` in an operand of ROWS rows.
+template <int ROWS> __device__ __forceinline__ uint32_t mass_panel(int row, int chunk)
+{
+    return (chunk >> 3) * (ROWS * 128) + row * 128 + (((chunk & 7) ^ (row & 7)) << 4);
+}
+
+// One of the two groups of loader warps: the tiles of its parity.
+template <typename C, int D, typename Ctl>
+__device__ void mass_load(const MassParams &p, Cursor c, char *smem, Ctl *ctl, int lt, int turn)
+{
+    using S = MassShape<C, D>;
+    constexpr int CH = D * static_cast<int>(sizeof(C)) / 16, CPL = CH > 32 ? 32 : CH, RPI = 32 / CPL, KST = S::K_STAGES;
+    constexpr int RST = S::RAW_STAGES > 0 ? S::RAW_STAGES / 2 : 1;
+    const int lane = lt & 31, w = lt >> 5, chunk = lane % CPL, sub = lane / CPL;
+    const uint32_t base = smem_u32(smem);
+    const int mask = (1 << p.c.page_shift) - 1;
+    Counted count;
+    int n = 0, mine_n = 0;  // tiles so far, and those of this group
+    // e4m3: widens this group's tile number t (tile 2 t + turn of all), whose copies have landed.
+    auto widen = [&](int t) -> bool {
+        const int all = 2 * t + turn, st = all % KST;
+        if (all >= KST && !mass_wait(ctl, &ctl->k_empty[st], (all / KST - 1) & 1)) return false;
+        const char *raw = smem + S::RAW_AT + (turn * RST + t % RST) * S::RAW;
+        char *to = smem + S::K_AT + st * S::TILE;
+#pragma unroll 8
+        for (int i = 0; i < 32 / RPI; ++i) {
+            const int row = 32 * w + i * RPI + sub;
+            const uint4 x = *reinterpret_cast<const uint4 *>(raw + row * D + chunk * 16);
+            const uint32_t b[4] = {x.x, x.y, x.z, x.w};
+            uint32_t y[8];
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                y[2 * k] = e4m3x2_to_f16x2(b[k] & 0xffffu);
+                y[2 * k + 1] = e4m3x2_to_f16x2(b[k] >> 16);
+            }
+            const bool swap = (chunk >> 2) & 1;  // lanes of two panels store their halves in opposite order
+            const uint4 lo = make_uint4(y[0], y[1], y[2], y[3]), hi = make_uint4(y[4], y[5], y[6], y[7]);
+            *reinterpret_cast<uint4 *>(to + mass_panel<MASS_KEYS>(row, 2 * chunk + swap)) = swap ? hi : lo;
+            *reinterpret_cast<uint4 *>(to + mass_panel<MASS_KEYS>(row, 2 * chunk + !swap)) = swap ? lo : hi;
+        }
+        fence_async_shared();
+        mbar_arrive(&ctl->k_full[st]);
+        return true;
+    };
+    bool ok = true;
+    for (; ok && c.at < c.end; next_item(c, p.w, p.c)) {
+        count.at(p, c);
+        const int t0 = mass_first(c), t1 = mass_last(c);
+        if (count.rows == 0 || t0 == t1) continue;
+        const int32_t *table = p.c.table + static_cast<int64_t>(c.b) * p.c.max_pages;
+        const char *from = p.c.k.base + c.h * p.c.k.head_stride + chunk * 16;
+        auto lookup = [&](int tile) {  // page id of this lane's row of a tile; -1: no such row
+            const int j = tile * MASS_KEYS + 32 * w + lane;
+            return tile < t1 && j < c.s.total ? __ldg(table + (j >> p.c.page_shift)) : -1;
+        };
+        for (int r0 = 0; ok && r0 < count.rows; r0 += S::ROWS) {
+            int tile = t0 + ((n ^ turn) & 1);  // this group's next
+            int pg = lookup(tile), next = lookup(tile + 2);
+            for (; ok && tile < t1; tile += 2, ++mine_n) {
+                const int all = 2 * mine_n + turn, j0 = tile * MASS_KEYS;
+                int64_t mine = -1;
+                if (static_cast<unsigned>(pg) < static_cast<unsigned>(p.c.num_pages))
+                    mine = pg * p.c.k.page_stride + ((j0 + 32 * w + lane) & mask) * p.c.k.slot_stride;
+                pg = next;
+                next = lookup(tile + 4);
+                uint32_t to;
+                if (S::WIDEN) {
+                    if (mine_n >= RST) {
+                        cp_async_wait<RST - 1>();
+                        if (!(ok = widen(mine_n - RST))) break;
+                    }
+                    to = base + S::RAW_AT + (turn * RST + mine_n % RST) * S::RAW;
+                } else {
+                    const int st = all % KST;
+                    if (all >= KST && !(ok = mass_wait(ctl, &ctl->k_empty[st], (all / KST - 1) & 1))) break;
+                    to = base + S::K_AT + st * S::TILE;
+                }
+#pragma unroll 8
+                for (int i = 0; i < 32 / RPI; ++i) {
+                    const int row = 32 * w + i * RPI + sub;
+                    const int64_t at = __shfl_sync(0xffffffffu, mine, i * RPI + sub);
+                    cp_async16_zfill(to + (S::WIDEN ? row * D + chunk * 16 : mass_panel<MASS_KEYS>(row, chunk)),
+                                     at < 0 ? p.c.k.base : from + at, at < 0 ? 0 : 16);
+                }
+                if (S::WIDEN)
+                    cp_async_commit();
+                else
+                    cp_async_arrive(&ctl->k_full[all % KST]);
+            }
+            n += t1 - t0;
+        }
+    }
+    asm volatile("cp.async.wait_all;" ::: "memory");
+    if (S::WIDEN)
+        for (int t = mine_n >= RST ? mine_n - RST : 0; ok && t < mine_n; ++t) ok = widen(t);
+}
+
+// Three warps, an item ahead of the others: the counted rows of q and their
+// constants.  For an e4m3 cache each row by a power of two into f16's range.
+template <typename T, typename C, int D, typename Ctl>
+__device__ void mass_prepare(const MassParams &p, Cursor c, char *smem, Ctl *ctl, int lt)
 {
     using S = MassShape<C, D>;
     using M = typename MmaOf<T, C>::type;
-    constexpr int NST = S::STAGES, ROWS = S::ROWS;
-    extern __shared__ __align__(1024) char smem[];
-    __shared__ float q_unit[ROWS], zs[ROWS];    // log-sum-exp in powers of two; infinity: a row that gives nothing
-    __shared__ unsigned long long sees[ROWS];
-    __shared__ Cursor cur0;
-    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    const uint32_t qs32 = smem_u32(smem), ring = smem_u32(smem + S::Q) + warp * (NST * S::SLICE);
-    if (tid < 32) {
-        const Cursor c = find_range(p.w, p.c, blockIdx.x, gridDim.x, tid);
-        if (tid == 0) cur0 = c;
-    }
-    __syncthreads();
-    Cursor c = cur0;
+    constexpr int CH = D / 8, STEP = 96 / CH;  // rows at a time
+    Counted count;
+    int unit_no = 0;
     for (; c.at < c.end; next_item(c, p.w, p.c)) {
-        bool bad = c.s.bad || c.s.total > p.stride;
-        unsigned long long counted = counted_tokens(p, c.b, &bad);
-        const int32_t *table = p.c.table + static_cast<int64_t>(c.b) * p.c.max_pages;
-        const long long item_end = c.first + c.tiles;
-        const int t0 = static_cast<int>(c.at - c.first);
-        const int t1 = c.s.total > 0 ? static_cast<int>((c.end < item_end ? c.end : item_end) - c.first) : t0;
-        if (p.row_status && t0 == 0 && c.h == 0) {
-            int any = bad;
-            for (int g = tid; c.s.total > 0 && g <= (c.s.total - 1) >> p.c.page_shift; g += MASS_THREADS)
-                any |= page_of(p.c, table, g << p.c.page_shift) < 0;
-            any = __syncthreads_or(any);
-            if (tid == 0) p.row_status[c.b] = any ? KV_STATUS_BAD : 0;
-        }
-        if (bad) continue;
-        if (c.s.fresh < 64) counted &= (1ull << c.s.fresh) - 1ull;
-        const int rows = __popcll(counted) * p.group;
+        count.at(p, c);
+        if (count.rows == 0 || mass_first(c) == mass_last(c)) continue;
         const float unit = p.scale_log2 * (p.c.k_scale ? __ldg(p.c.k_scale + c.h) : 1.0f);
-        const int64_t out_row = (static_cast<int64_t>(c.b) * p.c.kv_heads + c.h) * p.stride;
-        // at least one pass: without counted rows the old mass is carried over
-        for (int r0 = 0; r0 == 0 || r0 < rows; r0 += ROWS) {
-            const int live = min(ROWS, rows - r0), groups = (live + 15) >> 4;
-            const int t_end = rows > 0 ? t1 : t0;
-            bool unused = false;
-            SliceSource src = find_slice(p.c, table, t0 * MASS_KEYS + warp * 16, t0 < t_end ? c.s.total : 0, lane, &unused);
-            auto issue = [&](int tile) {
-                if (tile < t_end) {
-                    const int j0 = tile * MASS_KEYS + warp * 16;
-                    copy_slice<S::ROW_BYTES>(p.c, p.c.k, src, j0, c.h, ring + ((tile - t0) % NST) * S::SLICE, lane);
-                    src = find_slice(p.c, table, j0 + MASS_KEYS, tile + 1 < t_end ? c.s.total : 0, lane, &unused);
-                }
-                cp_async_commit();
-            };
-            __syncthreads();  // q and the rings of the pass before are no longer read
-#pragma unroll
-            for (int i = 0; i < NST - 1; ++i) issue(t0 + i);
-            for (int i = tid; i < groups * 16 * (D / 8); i += MASS_THREADS) {
-                const int r = i / (D / 8), d = (i - r * (D / 8)) * 8;
-                float x[8];
-#pragma unroll
-                for (int e = 0; e < 8; ++e) x[e] = 0.0f;
-                float z = CUDART_INF_F;
-                unsigned long long see = 0;
-                if (r < live) {
+        for (int r0 = 0; r0 < count.rows; r0 += S::ROWS, ++unit_no) {
+            const int place = unit_no & 1, live = min(S::ROWS, count.rows - r0), padded = (live + 15) & ~15;
+            char *qs = smem + S::Q_AT + place * S::Q;
+            if (unit_no >= 2 && !mass_wait(ctl, &ctl->q_empty[place], ((unit_no >> 1) - 1) & 1)) return;
+            for (int b0 = 0; b0 < padded; b0 += STEP) {
+                const int r = b0 + lt / CH, ch = lt % CH;
+                const bool there = lt < STEP * CH && r < live;
+                uint4 raw = make_uint4(0, 0, 0, 0);
+                int64_t at = 0;
+                int t = 0;
+                if (there) {
                     const int nth = (r0 + r) / p.group, g = r0 + r - nth * p.group;
-                    unsigned long long m = counted;
+                    unsigned long long m = count.tokens;
                     for (int e = 0; e < nth; ++e) m &= m - 1;
-                    const int t = __ffsll(m) - 1;
-                    const int64_t at = (static_cast<int64_t>(c.b) * p.w.T + t) * p.q_heads + c.h * p.group + g;
-                    const uint4 raw = *reinterpret_cast<const uint4 *>(static_cast<const T *>(p.q) + at * D + d);
-                    const T *y = reinterpret_cast<const T *>(&raw);
-#pragma unroll
-                    for (int e = 0; e < 8; ++e) x[e] = Num<T>::up(y[e]);
-                    if (d == 0) {
-                        see = visible_mask(p.parent ? p.parent + static_cast<int64_t>(c.b) * p.w.T : nullptr, t);
-                        z = __ldg(p.lse + at) * LOG2E;
-                        if (z == -CUDART_INF_F || see == 0) z = CUDART_INF_F;
-                    }
+                    t = __ffsll(m) - 1;
+                    at = (static_cast<int64_t>(c.b) * p.w.T + t) * p.q_heads + c.h * p.group + g;
+                    raw = *reinterpret_cast<const uint4 *>(static_cast<const T *>(p.q) + at * D + ch * 8);
                 }
                 float down = 1.0f;
-                if (sizeof(C) == 1) {
-                    float top = 0.0f;
+                if (S::WIDEN) {
+                    const T *y = reinterpret_cast<const T *>(&raw);
+                    float x[8], top = 0.0f;
 #pragma unroll
-                    for (int e = 0; e < 8; ++e) top = fabsf(x[e]) < CUDART_INF_F ? fmaxf(top, fabsf(x[e])) : top;
+                    for (int e = 0; e < 8; ++e) {
+                        x[e] = Num<T>::up(y[e]);
+                        top = fabsf(x[e]) < CUDART_INF_F ? fmaxf(top, fabsf(x[e])) : top;
+                    }
 #pragma unroll
-                    for (int o = D / 16; o; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+                    for (int o = CH / 2; o; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
                     const int e2 = top > 0.0f ? max(-120, min(120, 14 - ilogbf(top))) : 0;
                     const float up = exp2f(static_cast<float>(e2));
-#pragma unroll
-                    for (int e = 0; e < 8; ++e) x[e] *= up;
                     down = exp2f(static_cast<float>(-e2));
+                    raw = make_uint4(pack_mma<M>(x[0] * up, x[1] * up), pack_mma<M>(x[2] * up, x[3] * up),
+                                     pack_mma<M>(x[4] * up, x[5] * up), pack_mma<M>(x[6] * up, x[7] * up));
                 }
-                put_q8<M, C, D>(smem, r, d, x);
-                if (d == 0) {
-                    q_unit[r] = unit * down;
-                    zs[r] = z;
-                    sees[r] = see;
+                if (lt < STEP * CH && r < padded) {
+                    *reinterpret_cast<uint4 *>(qs + mass_panel<S::ROWS>(r, ch)) = raw;
+                    if (ch == 0) {
+                        unsigned long long see = 0;
+                        float z = CUDART_INF_F;
+                        if (there) {
+                            see = visible_mask(p.parent ? p.parent + static_cast<int64_t>(c.b) * p.w.T : nullptr, t);
+                            z = __ldg(p.lse + at) * LOG2E;
+                            if (z == -CUDART_INF_F) see = 0;
+                            if (see == 0) *reinterpret_cast<volatile int *>(&ctl->careful[place]) = unit_no + 1;
+                        }
+                        ctl->row[place][r] = make_float2(unit * down, z);
+                        ctl->sees[place][r] = see;
+                    }
                 }
             }
-            __syncthreads();
-            auto carried = [&](int j) {  // what key j has so far
+            fence_async_shared();
+            mbar_arrive(&ctl->q_full[place]);
+        }
+    }
+}
+
+// One thread.
+template <typename T, typename C, int D, typename Ctl>
+__device__ void mass_multiply(const MassParams &p, Cursor c, char *smem, Ctl *ctl)
+{
+    using S = MassShape<C, D>;
+    using M = typename MmaOf<T, C>::type;
+    constexpr int KST = S::K_STAGES;
+    const uint32_t base = smem_u32(smem), tmem = ctl->tmem;
+    Counted count;
+    int n = 0, unit_no = 0;
+    for (; c.at < c.end; next_item(c, p.w, p.c)) {
+        count.at(p, c);
+        const int tiles = mass_last(c) - mass_first(c);
+        if (count.rows == 0 || tiles == 0) continue;
+        for (int r0 = 0; r0 < count.rows; r0 += S::ROWS, ++unit_no) {
+            const int place = unit_no & 1, padded = (min(S::ROWS, count.rows - r0) + 15) & ~15;
+            const uint32_t shape = mma_shape(std::is_same<M, __nv_bfloat16>::value, false, padded);
+            if (!mass_wait1(ctl, &ctl->q_full[place], (unit_no >> 1) & 1)) return;
+            for (int i = 0; i < tiles; ++i, ++n) {
+                if (n >= MASS_BUFFERS && !mass_wait1(ctl, &ctl->s_empty[n % MASS_BUFFERS], (n / MASS_BUFFERS - 1) & 1)) return;
+                if (!mass_wait1(ctl, &ctl->k_full[n % KST], (n / KST) & 1)) return;
+                tc_fence_after();
+                fence_async_shared();  // K was written by asynchronous copies of threads, q by threads
+                const uint32_t k = base + S::K_AT + (n % KST) * S::TILE, q = base + S::Q_AT + place * S::Q;
+#pragma unroll
+                for (int ks = 0; ks < D / 16; ++ks)
+                    tc_mma(tmem + (n % MASS_BUFFERS) * 128, desc_k_major(k + (ks >> 2) * (MASS_KEYS * 128) + (ks & 3) * 32),
+                           desc_k_major(q + (ks >> 2) * (S::ROWS * 128) + (ks & 3) * 32), shape, ks > 0);
+                tc_commit(&ctl->s_full[n % MASS_BUFFERS]);
+                tc_commit(&ctl->k_empty[n % KST]);
+            }
+            tc_commit(&ctl->q_empty[place]);
+        }
+    }
+}
+
+// Four warps, a key of the tile a thread.
+template <typename Shape, typename Ctl> __device__ void mass_sum(const MassParams &p, Cursor c, Ctl *ctl, int tid)
+{
+    constexpr int ROWS = Shape::ROWS;
+    const int lane = tid & 31, warp = tid >> 5;
+    const uint32_t quarter = ctl->tmem + (static_cast<uint32_t>(warp * 32) << 16);
+    Counted count;
+    int n = 0, unit_no = 0;
+    for (; c.at < c.end; next_item(c, p.w, p.c)) {
+        count.at(p, c);
+        const int32_t *table = p.c.table + static_cast<int64_t>(c.b) * p.c.max_pages;
+        const int t0 = mass_first(c), t1 = mass_last(c);
+        if (p.row_status && t0 == 0 && c.h == 0 && warp == 0) {  // one warp: no barrier between warps that may leave early
+            int any = count.bad;
+            for (int g = lane; c.s.total > 0 && g <= (c.s.total - 1) >> p.c.page_shift; g += 32)
+                any |= page_of(p.c, table, g << p.c.page_shift) < 0;
+            any = __any_sync(0xffffffffu, any);
+            if (lane == 0) p.row_status[c.b] = any ? KV_STATUS_BAD : 0;
+        }
+        if (count.bad) continue;
+        const int64_t out_row = (static_cast<int64_t>(c.b) * p.c.kv_heads + c.h) * p.stride;
+        auto page_for = [&](int tile) {  // -1: nothing is written
+            const int j = tile * MASS_KEYS + tid;
+            return tile < t1 && j < c.s.total ? __ldg(table + (j >> p.c.page_shift)) : -1;
+        };
+        for (int r0 = 0; r0 == 0 || r0 < count.rows; r0 += ROWS) {
+            auto mass_for = [&](int tile) {  // what this thread's key has so far
+                const int j = tile * MASS_KEYS + tid;
+                if (tile >= t1 || j >= c.s.total) return 0.0f;
                 if (r0 > 0) return p.mass_out[out_row + j];
                 return p.mass_in && j < c.s.ctx ? p.decay * p.mass_in[out_row + j] : 0.0f;
             };
-            // lanes 0..15: the page (-1: nothing is written) and the old mass of this lane's key of a tile, asked for
-            // a tile ahead
-            auto page_for = [&](int tile) {
-                const int j = tile * MASS_KEYS + warp * 16 + lane;
-                return lane < 16 && tile < t_end && j < c.s.total ? __ldg(table + (j >> p.c.page_shift)) : -1;
-            };
-            auto mass_for = [&](int tile) {
-                const int j = tile * MASS_KEYS + warp * 16 + lane;
-                return lane < 16 && tile < t_end && j < c.s.total ? carried(j) : 0.0f;
-            };
-            int next_page = page_for(t0);
-            float next_mass = mass_for(t0);
-            for (int tile = t0; tile < t_end; ++tile) {
-                __syncwarp();
-                issue(tile + NST - 1);
-                const int j0 = tile * MASS_KEYS + warp * 16;
-                if (j0 >= c.s.total) break;
-                const int j = j0 + lane, page = next_page;
-                const float old = next_mass;
-                next_page = page_for(tile + 1);
-                next_mass = mass_for(tile + 1);
-                cp_async_wait<NST - 1>();
-                __syncwarp();
-                const uint32_t slice = ring + ((tile - t0) % NST) * S::SLICE;
-                uint32_t kf[D / 16][4];
-                get_k<C, D>(kf, slice, lane);
-                const bool tail = j0 + 16 > c.s.ctx;
-                float sum[2][2] = {{0.0f, 0.0f}, {0.0f, 0.0f}};  // [key tile][column]
-                for (int g = 0; g < groups; ++g) {
-                    float s[2][4] = {{0.0f, 0.0f, 0.0f, 0.0f}, {0.0f, 0.0f, 0.0f, 0.0f}};
-#pragma unroll
-                    for (int ks = 0; ks < D / 16; ++ks) {
-                        uint32_t a[4];
-                        get_q<D>(a, qs32, g, ks, lane);
-                        mma16816<M>(s[0], a, kf[ks][0], kf[ks][1]);
-                        mma16816<M>(s[1], a, kf[ks][2], kf[ks][3]);
-                    }
-#pragma unroll
-                    for (int i = 0; i < 2; ++i) {
-                        const int r = g * 16 + i * 8 + (lane >> 2);
-                        const float f = q_unit[r], z = zs[r];
-#pragma unroll
-                        for (int k = 0; k < 2; ++k)
-#pragma unroll
-                            for (int e = 0; e < 2; ++e) {
-                                float w = fast_exp2(s[k][2 * i + e] * f - z);
-                                if (tail) {
-                                    const int key = j0 + 8 * k + 2 * (lane & 3) + e;
-                                    if (!(key < c.s.ctx || (key < c.s.total && (sees[r] >> (key - c.s.ctx) & 1)))) w = 0.0f;
-                                }
-                                if (z == CUDART_INF_F) w = 0.0f;
-                                sum[k][e] += w;
-                            }
-                    }
-                }
-#pragma unroll
-                for (int k = 0; k < 2; ++k)
-#pragma unroll
-                    for (int e = 0; e < 2; ++e) {
-#pragma unroll
-                        for (int o = 4; o < 32; o <<= 1) sum[k][e] += __shfl_xor_sync(0xffffffffu, sum[k][e], o);
-                    }
-                // lane l < 16 writes key l: column l & 1 of the thread (l % 8) / 2 in key tile l / 8
-                const int from = (lane & 7) >> 1;
-                const float a = __shfl_sync(0xffffffffu, sum[0][0], from), b = __shfl_sync(0xffffffffu, sum[0][1], from);
-                const float d = __shfl_sync(0xffffffffu, sum[1][0], from), e = __shfl_sync(0xffffffffu, sum[1][1], from);
-                const float mine = (lane & 8) ? ((lane & 1) ? e : d) : ((lane & 1) ? b : a);
-                if (static_cast<unsigned>(page) < static_cast<unsigned>(p.c.num_pages)) p.mass_out[out_row + j] = old + mine;
+            int pg = page_for(t0);  // both asked for a tile ahead
+            float had = mass_for(t0);
+            const int live = min(ROWS, count.rows - r0), place = unit_no & 1;
+            bool careful = false;
+            if (live > 0 && t0 < t1) {
+                if (!mass_wait(ctl, &ctl->q_full[place], (unit_no >> 1) & 1)) return;
+                careful = *reinterpret_cast<volatile int *>(&ctl->careful[place]) == unit_no + 1;
             }
-            cp_async_wait<0>();
-            if (rows == 0)
-                for (int j = t0 * MASS_KEYS + tid; j < min(t1 * MASS_KEYS, c.s.total); j += MASS_THREADS)
-                    if (page_of(p.c, table, j) >= 0) p.mass_out[out_row + j] = carried(j);
+            for (int tile = t0; tile < t1; ++tile) {
+                const int j = tile * MASS_KEYS + tid, page = pg;
+                float sum = had;
+                pg = page_for(tile + 1);
+                had = mass_for(tile + 1);
+                if (live > 0) {
+                    if (!mass_wait(ctl, &ctl->s_full[n % MASS_BUFFERS], (n / MASS_BUFFERS) & 1)) {
+                        if (tid == 0 && p.row_status) p.row_status[c.b] = STATUS_TIMEOUT;
+                        return;
+                    }
+                    tc_fence_after();
+                    __syncwarp();
+                    float s0 = 0.0f, s1 = 0.0f;
+                    const bool masks = careful || (tile + 1) * MASS_KEYS > c.s.ctx;
+                    for (int g = 0; g < live; g += 16) {
+                        uint32_t y[16];
+                        tc_ld16(y, quarter + (n % MASS_BUFFERS) * 128 + g);
+                        const float4 *k = reinterpret_cast<const float4 *>(&ctl->row[place][g]);
+                        if (!masks && g + 16 <= live) {
+#pragma unroll
+                            for (int i = 0; i < 8; ++i) {
+                                const float4 u = k[i];
+                                s0 += fast_exp2(__uint_as_float(y[2 * i]) * u.x - u.y);
+                                s1 += fast_exp2(__uint_as_float(y[2 * i + 1]) * u.z - u.w);
+                            }
+                        } else {
+#pragma unroll
+                            for (int i = 0; i < 16; ++i) {
+                                const int r = min(g + i, live - 1);
+                                const unsigned long long see = ctl->sees[place][r];
+                                const float2 u = ctl->row[place][r];
+                                const bool seen = g + i < live && see != 0 &&
+                                                  (j < c.s.ctx || (j < c.s.total && (see >> ((j - c.s.ctx) & 63) & 1)));
+                                const float w = fast_exp2(__uint_as_float(y[i]) * u.x - u.y);
+                                if (seen) s0 += w;
+                            }
+                        }
+                        __syncwarp();
+                    }
+                    tc_fence_before();
+                    mbar_arrive(&ctl->s_empty[n % MASS_BUFFERS]);
+                    ++n;
+                    sum += s0 + s1;
+                }
+                if (static_cast<unsigned>(page) < static_cast<unsigned>(p.c.num_pages)) p.mass_out[out_row + j] = sum;
+            }
+            if (live > 0 && t0 < t1) {
+                mbar_arrive(&ctl->q_empty[place]);
+                ++unit_no;
+            }
         }
     }
+}
+
+template <typename T, typename C, int D> __global__ void __launch_bounds__(MASS_THREADS, 1) mass_kernel(const MassParams p)
+{
+    using S = MassShape<C, D>;
+    using Ctl = MassCtl<S::ROWS>;
+    extern __shared__ char raw_smem[];
+    char *smem = raw_smem + ((1024u - (smem_u32(raw_smem) & 1023u)) & 1023u);
+    Ctl *ctl = reinterpret_cast<Ctl *>(smem + S::CTL_AT);
+    const int tid = threadIdx.x, warp = tid >> 5;
+    const Cursor c = find_range(p.w, p.c, blockIdx.x, gridDim.x, tid & 31);
+    if (c.at == c.end) return;  // the whole block
+    if (tid == 0) {
+        for (int i = 0; i < 8; ++i) {
+            mbar_init(&ctl->k_full[i], 128);
+            mbar_init(&ctl->k_empty[i], 1);
+        }
+        for (int i = 0; i < MASS_BUFFERS; ++i) {
+            mbar_init(&ctl->s_full[i], 1);
+            mbar_init(&ctl->s_empty[i], 128);
+        }
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(&ctl->q_full[i], 96);
+            mbar_init(&ctl->q_empty[i], 129);  // the products' end and the 128 readers of the constants
+        }
+        mbar_init(&ctl->spare, 1);
+        ctl->dead = ctl->careful[0] = ctl->careful[1] = 0;
+        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    }
+    if (warp == 4) tmem_alloc(&ctl->tmem, 512);
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    if (warp < 4) {
+        mass_sum<S>(p, c, ctl, tid);
+    } else if (warp == 4) {
+        if (tid == 128) {
+            mass_multiply<T, C, D>(p, c, smem, ctl);
+            if (*reinterpret_cast<volatile int *>(&ctl->dead)) {  // let what was issued end
+                tc_commit(&ctl->spare);
+                mbar_wait(&ctl->spare, 0);
+            }
+        }
+        __syncwarp();
+    } else if (warp < 8) {
+        mass_prepare<T, C, D>(p, c, smem, ctl, tid - 160);
+    } else {
+        mass_load<C, D>(p, c, smem, ctl, tid & 127, warp >= 12);
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    if (warp == 4) tmem_free(ctl->tmem, 512);
 }
 
 template <typename T, typename C, int D> static cudaError_t launch_dim(const MassParams &p, cudaStream_t st)
 {
     using S = MassShape<C, D>;
     auto kernel = mass_kernel<T, C, D>;
-    const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, S::SMEM);
+    constexpr int SMEM = S::CTL_AT + static_cast<int>(sizeof(MassCtl<S::ROWS>)) + 1024;
+    static_assert(SMEM <= 232448, "shared memory of a block");
+    const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, SMEM);
     if (e != cudaSuccess) return e;
-    kernel<<<MASS_SMS * S::BLOCKS_PER_SM, MASS_THREADS, S::SMEM, st>>>(p);
+    kernel<<<MASS_SMS, MASS_THREADS, SMEM, st>>>(p);
     return cudaGetLastError();
 }
 template <typename T, typename C> static cudaError_t launch_types(const MassParams &p, int D, cudaStream_t st)

@@ -191,29 +191,6 @@ __device__ __forceinline__ void slice_scores(float (&s)[MT][2][4], uint32_t k_sl
     }
 }
 
-// The K fragments of a slice, for several groups of rows: b[ks] holds both key
-// tiles' operands of elements 16 ks...
-template <typename C, int D> __device__ __forceinline__ void get_k(uint32_t (&b)[D / 16][4], uint32_t k_slice, int lane)
-{
-    constexpr int RB = D * static_cast<int>(sizeof(C));
-    const int mat = lane >> 3, r8 = lane & 7;
-    if (sizeof(C) == 2) {
-#pragma unroll
-        for (int ks = 0; ks < D / 16; ++ks) ldmatrix4(b[ks], k_slice + chunk_at<RB>((mat >> 1) * 8 + r8, 2 * ks + (mat & 1)));
-    } else {
-#pragma unroll
-        for (int kp = 0; kp < D / 32; ++kp) {
-            uint32_t x[4];
-            ldmatrix4(x, k_slice + chunk_at<RB>((mat & 1) * 8 + r8, 2 * kp + (mat >> 1)));
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                b[2 * kp + (i >> 1)][2 * (i & 1)] = e4m3x2_to_f16x2(x[i] & 0xffffu);
-                b[2 * kp + (i >> 1)][2 * (i & 1) + 1] = e4m3x2_to_f16x2(x[i] >> 16);
-            }
-        }
-    }
-}
-
 // o += p v over a slice: p[mt] the probabilities as a fragment.
 template <typename M, typename C, int D, int MT>
 __device__ __forceinline__ void slice_values(float (&o)[MT][D / 8][4], const uint32_t (&p)[MT][4], uint32_t v_slice, int lane)
