@@ -352,11 +352,13 @@ template <typename Shape, typename Ctl> __device__ void mass_sum(const MassParam
             return tile < t1 && j < c.s.total ? __ldg(table + (j >> p.c.page_shift)) : -1;
         };
         for (int r0 = 0; r0 == 0 || r0 < count.rows; r0 += ROWS) {
-            auto mass_for = [&](int tile) {  // what this thread's key has so far
+            // what this thread's key has so far, to be multiplied by `keep` (where it is used: here it would wait)
+            const float *so_far = r0 > 0 ? p.mass_out + out_row : p.mass_in ? p.mass_in + out_row : nullptr;
+            const int held = so_far == nullptr ? 0 : r0 > 0 ? c.s.total : c.s.ctx;
+            const float keep = r0 > 0 ? 1.0f : p.decay;
+            auto mass_for = [&](int tile) {
                 const int j = tile * MASS_KEYS + tid;
-                if (tile >= t1 || j >= c.s.total) return 0.0f;
-                if (r0 > 0) return p.mass_out[out_row + j];
-                return p.mass_in && j < c.s.ctx ? p.decay * p.mass_in[out_row + j] : 0.0f;
+                return tile < t1 && j < held ? so_far[j] : 0.0f;
             };
             int pg = page_for(t0);  // both asked for a tile ahead
             float had = mass_for(t0);
@@ -368,9 +370,10 @@ template <typename Shape, typename Ctl> __device__ void mass_sum(const MassParam
             }
             for (int tile = t0; tile < t1; ++tile) {
                 const int j = tile * MASS_KEYS + tid, page = pg;
-                float sum = had;
+                const float old = had;
                 pg = page_for(tile + 1);
                 had = mass_for(tile + 1);
+                float sum = 0.0f;
                 if (live > 0) {
                     if (!mass_wait(ctl, &ctl->s_full[n % MASS_BUFFERS], (n / MASS_BUFFERS) & 1)) {
                         if (tid == 0 && p.row_status) p.row_status[c.b] = STATUS_TIMEOUT;
@@ -384,12 +387,14 @@ template <typename Shape, typename Ctl> __device__ void mass_sum(const MassParam
                         uint32_t y[16];
                         tc_ld16(y, quarter + (n % MASS_BUFFERS) * 128 + g);
                         const float4 *k = reinterpret_cast<const float4 *>(&ctl->row[place][g]);
-                        if (!masks && g + 16 <= live) {
+                        if (!masks) {
 #pragma unroll
                             for (int i = 0; i < 8; ++i) {
                                 const float4 u = k[i];
-                                s0 += fast_exp2(__uint_as_float(y[2 * i]) * u.x - u.y);
-                                s1 += fast_exp2(__uint_as_float(y[2 * i + 1]) * u.z - u.w);
+                                const float a = fast_exp2(__uint_as_float(y[2 * i]) * u.x - u.y);
+                                const float b = fast_exp2(__uint_as_float(y[2 * i + 1]) * u.z - u.w);
+                                if (g + 2 * i < live) s0 += a;
+                                if (g + 2 * i + 1 < live) s1 += b;
                             }
                         } else {
 #pragma unroll
@@ -408,9 +413,9 @@ template <typename Shape, typename Ctl> __device__ void mass_sum(const MassParam
                     tc_fence_before();
                     mbar_arrive(&ctl->s_empty[n % MASS_BUFFERS]);
                     ++n;
-                    sum += s0 + s1;
+                    sum = s0 + s1;
                 }
-                if (static_cast<unsigned>(page) < static_cast<unsigned>(p.c.num_pages)) p.mass_out[out_row + j] = sum;
+                if (static_cast<unsigned>(page) < static_cast<unsigned>(p.c.num_pages)) p.mass_out[out_row + j] = old * keep + sum;
             }
             if (live > 0 && t0 < t1) {
                 mbar_arrive(&ctl->q_empty[place]);
