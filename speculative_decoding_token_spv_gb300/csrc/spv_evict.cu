@@ -1,18 +1,23 @@
 // spv_evict.cu -- cuts each sequence's cache back to its budget by the
 // accumulated attention weight, each key head by itself and in place.
 //
-// evict_select_kernel, one block per (sequence, head): every slot gets an
-// order-preserving 32-bit key (protected slots the largest); a radix select
-// over its digits finds the key of the last slot to stay and how many of its
-// equals do; bit masks of the kept slots and prefix counts over their words
-// then match the i-th hole below the budget with the i-th kept slot above.
-// evict_move_kernel copies the rows of the matched slots.
+// Selection, one block per (sequence, head): every slot gets an
+// order-preserving 32-bit key (protected slots the largest) and the key of the
+// last slot to stay is found digit by digit; bit masks of the kept slots and
+// prefix counts over their words then match the i-th hole below the budget
+// with the i-th kept slot above it.  Up to 16,384 slots the keys stay in
+// registers (evict_select_few), two bits a round by counting, and the rounds
+// end as soon as a count is exact, usually after about 12; beyond, a radix
+// select reads the weights again for each of four digits (evict_select_many).
+// evict_move_kernel, a dependent launch, copies the rows of the matched slots.
 #include "spv_kv.cuh"
 
 namespace spv {
 
 constexpr int EV_THREADS = 1024;
-constexpr int EV_MOVE_SLOTS = 64;  // slots that a block of the move looks at
+constexpr int EV_MOVE_SLOTS = 256;     // slots that a block of the move looks at, one a thread
+constexpr int EV_MOVE_AHEAD = 8;       // 16-byte pieces of a thread on their way
+constexpr int EV_FEW_SLOTS = 16384;
 
 struct EvictParams {
     PagedView c;
@@ -22,6 +27,7 @@ struct EvictParams {
     int32_t *pos_out, *new_lens, *slot_src, *row_status;
     int64_t stride, out_stride;
     int budget, sinks, recent, row_bytes, words;
+    int piece_shift;  // log2 of the 16-byte pieces of a slot's K and V rows together; -1: no power of two
 };
 
 // Ascending order of the keys is ascending order of the weights: NaN lowest,
@@ -65,25 +71,36 @@ __device__ __forceinline__ int block_prefix(int x, int *sh, int *all)
     return upto - x + (warp ? sh[warp - 1] : 0);
 }
 
-__global__ void __launch_bounds__(EV_THREADS) evict_select_kernel(const EvictParams p)
+__device__ __forceinline__ void dependents_go() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+
+// What both selections begin with, for block (h, b): the length, whether it is
+// bad, and the outputs that need no selection.  False: the item is done.
+struct EvictItem {
+    int b, h, n, m;  // slots in use, slots to keep
+    const float *mass;
+    const int32_t *pos;
+    int32_t *src;
+    float *mass_out;
+    int32_t *pos_out;
+};
+__device__ __forceinline__ bool evict_begin(const EvictParams &p, EvictItem *it)
 {
-    extern __shared__ unsigned words[];  // kept bits, then prefix counts
-    __shared__ unsigned hist[256];
-    __shared__ int sh[32];
-    __shared__ int tops[32];
-    __shared__ unsigned found[2];
-    const int b = blockIdx.y, h = blockIdx.x, tid = threadIdx.x, lane = tid & 31;
+    const int b = blockIdx.y, h = blockIdx.x, tid = threadIdx.x;
     const int64_t item = static_cast<int64_t>(b) * p.c.kv_heads + h;
-    const float *mass = p.mass + item * p.stride;
-    const int32_t *pos = p.pos ? p.pos + item * p.stride : nullptr;
-    int32_t *src = p.slot_src + item * p.budget;
+    it->b = b;
+    it->h = h;
+    it->mass = p.mass + item * p.stride;
+    it->pos = p.pos ? p.pos + item * p.stride : nullptr;
+    it->src = p.slot_src + item * p.budget;
+    it->mass_out = p.mass_out + item * p.out_stride;
+    it->pos_out = p.pos_out ? p.pos_out + item * p.out_stride : nullptr;
     const int n = p.lens[b];
     const int64_t cap = static_cast<int64_t>(p.c.max_pages) << p.c.page_shift;
     const bool bad = n < 0 || n > cap || n > p.stride;
     if (h == 0) {
-        int any = bad;
-        const int32_t *table = p.c.table + static_cast<int64_t>(b) * p.c.max_pages;
         if (p.row_status) {
+            int any = bad;
+            const int32_t *table = p.c.table + static_cast<int64_t>(b) * p.c.max_pages;
             for (int g = tid; !bad && n > p.budget && g <= (n - 1) >> p.c.page_shift; g += EV_THREADS)
                 any |= page_of(p.c, table, g << p.c.page_shift) < 0;
             any = __syncthreads_or(any);
@@ -91,17 +108,165 @@ __global__ void __launch_bounds__(EV_THREADS) evict_select_kernel(const EvictPar
         }
         if (tid == 0) p.new_lens[b] = bad || n < p.budget ? n : p.budget;
     }
-    const int m = bad ? 0 : n < p.budget ? n : p.budget;
-    if (bad || n <= p.budget) {  // nothing moves
-        for (int i = tid; i < p.budget; i += EV_THREADS) {
-            src[i] = i < m ? i : -1;
-            if (i < m) {
-                p.mass_out[item * p.out_stride + i] = mass[i];
-                if (p.pos_out) p.pos_out[item * p.out_stride + i] = pos ? pos[i] : i;
-            }
+    it->n = n;
+    it->m = bad ? 0 : n < p.budget ? n : p.budget;
+    if (!bad && n > p.budget) return true;
+    for (int i = tid; i < p.budget; i += EV_THREADS) {  // nothing moves
+        it->src[i] = i < it->m ? i : -1;
+        if (i < it->m) {
+            it->mass_out[i] = it->mass[i];
+            if (it->pos_out) it->pos_out[i] = it->pos ? it->pos[i] : i;
         }
-        return;
     }
+    return false;
+}
+__device__ __forceinline__ void evict_write(const EvictParams &p, const EvictItem &it, int i, int s)
+{
+    it.src[i] = s;
+    if (s != i || p.mass_out != p.mass) it.mass_out[i] = it.mass[s];
+    if (it.pos_out && (s != i || p.pos_out != p.pos)) it.pos_out[i] = it.pos ? it.pos[s] : s;
+}
+
+// Slots in registers: slot t + 1024 i is thread t's i-th.
+template <int PER> __global__ void __launch_bounds__(EV_THREADS) evict_select_few(const EvictParams p)
+{
+    constexpr int WORDS = PER * 32;
+    __shared__ unsigned kept[WORDS], before[WORDS];          // kept bits; holes and movers (high half) before a word
+    __shared__ unsigned short movers[WORDS * 16];            // kept slots at or above the budget, in order
+    __shared__ int sh[32], counts[3][4];
+    dependents_go();
+    EvictItem it;
+    if (!evict_begin(p, &it)) return;
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, n = it.n, m = it.m;
+    unsigned key[PER];
+    {
+        float w[PER];
+        int at[PER];
+#pragma unroll
+        for (int i = 0; i < PER; ++i) {
+            const int j = tid + i * EV_THREADS;
+            w[i] = j < n ? it.mass[j] : 0.0f;
+            at[i] = j < n ? (it.pos ? it.pos[j] : j) : -1;
+        }
+        int top = -1;
+#pragma unroll
+        for (int i = 0; i < PER; ++i) top = max(top, at[i]);
+        top = __reduce_max_sync(0xffffffffu, top);
+        if (lane == 0) sh[warp] = top;
+        if (tid < 12) (&counts[0][0])[tid] = 0;
+        __syncthreads();
+        top = __reduce_max_sync(0xffffffffu, sh[lane]);
+#pragma unroll
+        for (int i = 0; i < PER; ++i) {
+            const int j = tid + i * EV_THREADS;
+            const bool always = at[i] < p.sinks || static_cast<long long>(at[i]) > static_cast<long long>(top) - p.recent;
+            key[i] = j >= n ? 0u : always ? 0xffffffffu : mass_key(w[i]);
+        }
+    }
+    // the largest `least` with at least m keys >= it: two bits a round
+    unsigned least = 0;
+    bool exact = false;
+    int turn = 0;
+    auto count3 = [&](unsigned a, unsigned b, unsigned c) {  // keys >= a, b, c into counts[turn]
+        int x = 0, y = 0, z = 0;
+#pragma unroll
+        for (int i = 0; i < PER; ++i) {
+            x += key[i] >= a;
+            y += key[i] >= b;
+            z += key[i] >= c;
+        }
+        x = __reduce_add_sync(0xffffffffu, x);
+        y = __reduce_add_sync(0xffffffffu, y);
+        z = __reduce_add_sync(0xffffffffu, z);
+        if (lane == 0) {
+            atomicAdd(&counts[turn][0], x);
+            atomicAdd(&counts[turn][1], y);
+            atomicAdd(&counts[turn][2], z);
+        }
+        if (tid < 3) counts[turn == 2 ? 0 : turn + 1][tid] = 0;  // the next round's: read last a round ago
+        __syncthreads();
+    };
+    for (int bit = 30; bit >= 0 && !exact; bit -= 2) {
+        const unsigned a = least | 1u << bit, b = least | 2u << bit, c = least | 3u << bit;
+        count3(a, b, c);
+        const int x = counts[turn][0], y = counts[turn][1], z = counts[turn][2];
+        turn = turn == 2 ? 0 : turn + 1;
+        const int got = z >= m ? z : y >= m ? y : x >= m ? x : -1;
+        least = z >= m ? c : y >= m ? b : x >= m ? a : least;
+        exact = got == m;
+    }
+    int want = 0;  // of the keys equal to `least`, from the lowest slot on
+    if (!exact) {
+        if (least != 0xffffffffu) {
+            count3(least + 1u, 0xffffffffu, 0xffffffffu);
+            want = m - counts[turn][0];
+        } else {
+            want = m;
+        }
+    }
+#pragma unroll
+    for (int i = 0; i < PER; ++i) {
+        const int j = tid + i * EV_THREADS;
+        const unsigned gt = __ballot_sync(0xffffffffu, j < n && (exact ? key[i] >= least : key[i] > least));
+        const unsigned eq = __ballot_sync(0xffffffffu, j < n && !exact && key[i] == least);
+        if (lane == 0) {
+            kept[i * 32 + warp] = gt;
+            before[i * 32 + warp] = eq;
+        }
+    }
+    __syncthreads();
+    int all;
+    if (!exact) {
+        unsigned eq = tid < WORDS ? before[tid] : 0;
+        const int ahead = block_prefix(__popc(eq), sh, &all);
+        if (tid < WORDS) {
+            unsigned k = kept[tid];
+            for (int left = want - ahead; eq && left > 0; --left) {
+                k |= eq & -eq;
+                eq &= eq - 1;
+            }
+            kept[tid] = k;
+        }
+        __syncthreads();
+    }
+    const int wm = m >> 5;
+    const unsigned low = (1u << (m & 31)) - 1u;
+    {
+        const unsigned k = tid < WORDS ? kept[tid] : 0;
+        const unsigned below = tid < wm ? 0xffffffffu : tid == wm ? low : 0u;  // slots below the budget
+        const unsigned hole = tid < WORDS ? ~k & below : 0u, mover = k & ~below;
+        const int packed = __popc(hole) | __popc(mover) << 16;
+        const int ahead = block_prefix(packed, sh, &all);
+        if (tid < WORDS) before[tid] = ahead;
+        int at = ahead >> 16;
+        for (unsigned left = mover; left; left &= left - 1) movers[at++] = static_cast<unsigned short>(32 * tid + __ffs(left) - 1);
+    }
+    __syncthreads();
+    for (int i = tid; i < p.budget; i += EV_THREADS) {
+        int s = i;
+        if (i < m) {
+            const unsigned k = kept[i >> 5], bit = 1u << (i & 31);
+            if (!(k & bit)) s = movers[(before[i >> 5] & 0xffffu) + __popc(~k & (bit - 1u))];
+            evict_write(p, it, i, s);
+        } else {
+            it.src[i] = -1;
+        }
+    }
+}
+
+__global__ void __launch_bounds__(EV_THREADS) evict_select_many(const EvictParams p)
+{
+    extern __shared__ unsigned words[];  // kept bits, then prefix counts
+    __shared__ unsigned hist[256];
+    __shared__ int sh[32];
+    __shared__ int tops[32];
+    __shared__ unsigned found[2];
+    dependents_go();
+    EvictItem it;
+    if (!evict_begin(p, &it)) return;
+    const int tid = threadIdx.x, lane = tid & 31, n = it.n, m = it.m;
+    const float *mass = it.mass;
+    const int32_t *pos = it.pos;
     int top = pos ? -1 : n - 1;
     if (pos) {
         for (int j = tid; j < n; j += EV_THREADS) top = max(top, pos[j]);
@@ -206,30 +371,65 @@ __global__ void __launch_bounds__(EV_THREADS) evict_select_kernel(const EvictPar
             for (; rank > 0; --rank) from &= from - 1;
             s = 32 * w + __ffs(from) - 1;
         }
-        src[i] = s;
-        if (s != i || p.mass_out != p.mass) p.mass_out[item * p.out_stride + i] = mass[s];
-        if (p.pos_out && (s != i || p.pos_out != p.pos)) p.pos_out[item * p.out_stride + i] = pos ? pos[s] : s;
+        evict_write(p, it, i, s);
     }
-    for (int i = m + tid; i < p.budget; i += EV_THREADS) src[i] = -1;
+    for (int i = m + tid; i < p.budget; i += EV_THREADS) it.src[i] = -1;
 }
 
-__global__ void __launch_bounds__(256) evict_move_kernel(const EvictParams p)
+__global__ void __launch_bounds__(EV_MOVE_SLOTS) evict_move_kernel(const EvictParams p)
 {
-    const int h = blockIdx.y % p.c.kv_heads, b = blockIdx.y / p.c.kv_heads;
+    __shared__ int64_t from_k[EV_MOVE_SLOTS], to_k[EV_MOVE_SLOTS], from_v[EV_MOVE_SLOTS], to_v[EV_MOVE_SLOTS];
+    __shared__ int per_warp[EV_MOVE_SLOTS / 32];
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const int h = blockIdx.y % p.c.kv_heads, b = blockIdx.y / p.c.kv_heads, i = blockIdx.x * EV_MOVE_SLOTS + tid;
     const int32_t *table = p.c.table + static_cast<int64_t>(b) * p.c.max_pages;
-    const int32_t *src = p.slot_src + static_cast<int64_t>(blockIdx.y) * p.budget;
-    const int per = p.row_bytes >> 4, lanes = 2 * per;  // 16-byte pieces of a row, of K and V
-    for (int x = threadIdx.x; x < EV_MOVE_SLOTS * lanes; x += blockDim.x) {
-        const int i = blockIdx.x * EV_MOVE_SLOTS + x / lanes, e = x % lanes;
-        if (i >= p.budget) break;
-        const int s = src[i];
-        if (s < 0 || s == i) continue;
-        const int from = page_of(p.c, table, s), to = page_of(p.c, table, i);
-        if (from < 0 || to < 0) continue;
-        const PoolView &pool = e < per ? p.c.k : p.c.v;
-        const int o = (e < per ? e : e - per) << 4;
-        *reinterpret_cast<uint4 *>(const_cast<char *>(row_ptr(p.c, pool, to, i, h)) + o) =
-            *reinterpret_cast<const uint4 *>(row_ptr(p.c, pool, from, s, h) + o);
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    // the block's moves, in a row
+    const int s = i < p.budget ? p.slot_src[static_cast<int64_t>(blockIdx.y) * p.budget + i] : -1;
+    bool moves = s >= 0 && s != i;
+    int from = -1, to = -1;
+    if (moves) {
+        from = page_of(p.c, table, s);
+        to = page_of(p.c, table, i);
+        moves = from >= 0 && to >= 0;
+    }
+    const unsigned who = __ballot_sync(0xffffffffu, moves);
+    if (lane == 0) per_warp[warp] = __popc(who);
+    __syncthreads();
+    int at = __popc(who & ((1u << lane) - 1u)), count = 0;
+#pragma unroll
+    for (int w = 0; w < EV_MOVE_SLOTS / 32; ++w) {
+        if (w < warp) at += per_warp[w];
+        count += per_warp[w];
+    }
+    if (moves) {
+        from_k[at] = row_ptr(p.c, p.c.k, from, s, h) - p.c.k.base;
+        to_k[at] = row_ptr(p.c, p.c.k, to, i, h) - p.c.k.base;
+        from_v[at] = row_ptr(p.c, p.c.v, from, s, h) - p.c.v.base;
+        to_v[at] = row_ptr(p.c, p.c.v, to, i, h) - p.c.v.base;
+    }
+    __syncthreads();
+    const int per = p.row_bytes >> 4, pieces = 2 * per, all = count * pieces;  // 16-byte pieces of a row; K's, then V's
+    for (int x0 = tid; x0 < all; x0 += EV_MOVE_AHEAD * EV_MOVE_SLOTS) {
+        uint4 data[EV_MOVE_AHEAD];
+        char *dst[EV_MOVE_AHEAD];
+#pragma unroll
+        for (int e = 0; e < EV_MOVE_AHEAD; ++e) {
+            const int x = x0 + e * EV_MOVE_SLOTS;
+            dst[e] = nullptr;
+            if (x < all) {
+                const int r = p.piece_shift >= 0 ? x >> p.piece_shift : x / pieces;
+                int o = x - r * pieces;
+                const bool v = o >= per;
+                o = (v ? o - per : o) << 4;
+                char *base = v ? p.c.v.base : p.c.k.base;
+                data[e] = __ldcs(reinterpret_cast<const uint4 *>(base + (v ? from_v[r] : from_k[r]) + o));
+                dst[e] = base + (v ? to_v[r] : to_k[r]) + o;
+            }
+        }
+#pragma unroll
+        for (int e = 0; e < EV_MOVE_AHEAD; ++e)
+            if (dst[e]) *reinterpret_cast<uint4 *>(dst[e]) = data[e];
     }
 }
 
@@ -254,16 +454,37 @@ cudaError_t launch_evict(const EvictLaunch &L, cudaStream_t st)
     p.row_bytes = k.cache.head_dim * (k.cache.dtype == SPV_E4M3 ? 1 : 2);
     const int64_t cap = static_cast<int64_t>(k.max_pages) * k.cache.page_size;
     p.words = static_cast<int>(((cap < L.mass_stride ? cap : L.mass_stride) + 31) / 32);
-    const int smem = p.words * 2 * static_cast<int>(sizeof(unsigned));
-    if (smem > 40 * 1024) {
-        const cudaError_t e = cudaFuncSetAttribute(evict_select_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
-        if (e != cudaSuccess) return e;
+    const int pieces = p.row_bytes / 8;
+    p.piece_shift = (pieces & (pieces - 1)) == 0 ? log2_of(pieces) : -1;
+    const dim3 items(k.cache.kv_heads, k.B);
+    const int slots = p.words * 32;  // that a sequence can have
+    cudaError_t e;
+    if (slots <= 4096) {
+        evict_select_few<4><<<items, EV_THREADS, 0, st>>>(p);
+    } else if (slots <= 8192) {
+        evict_select_few<8><<<items, EV_THREADS, 0, st>>>(p);
+    } else if (slots <= EV_FEW_SLOTS) {
+        evict_select_few<16><<<items, EV_THREADS, 0, st>>>(p);
+    } else {
+        const int smem = p.words * 2 * static_cast<int>(sizeof(unsigned));
+        if (smem > 40 * 1024) {
+            e = cudaFuncSetAttribute(evict_select_many, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+            if (e != cudaSuccess) return e;
+        }
+        evict_select_many<<<items, EV_THREADS, smem, st>>>(p);
     }
-    evict_select_kernel<<<dim3(k.cache.kv_heads, k.B), EV_THREADS, smem, st>>>(p);
-    cudaError_t e = cudaGetLastError();
+    e = cudaGetLastError();
     if (e != cudaSuccess) return e;
-    evict_move_kernel<<<dim3((L.budget + EV_MOVE_SLOTS - 1) / EV_MOVE_SLOTS, k.B * k.cache.kv_heads), 256, 0, st>>>(p);
-    return cudaGetLastError();
+    cudaLaunchAttribute attr{};
+    attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr.val.programmaticStreamSerializationAllowed = 1;
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = dim3((L.budget + EV_MOVE_SLOTS - 1) / EV_MOVE_SLOTS, k.B * k.cache.kv_heads);
+    cfg.blockDim = dim3(EV_MOVE_SLOTS);
+    cfg.stream = st;
+    cfg.attrs = &attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, evict_move_kernel, p);
 }
 
 }  // namespace spv

@@ -12,22 +12,32 @@ from __future__ import annotations
 
 import ctypes
 import math
+import struct
 from dataclasses import dataclass
 
 import torch
 
-from . import SPV_BF16, SPV_E4M3, SPV_F16, _check, _cuda, _ptr, _stream, load_library, new_workspace
+from . import SPV_BF16, SPV_E4M3, SPV_F16, SpvError, _check, _stream, load_library, new_workspace
 
 ROPE_SCALINGS = {"plain": 0, "linear": 1, "base": 2, "by_parts": 3}
 _ACTIVATIONS = {torch.bfloat16: SPV_BF16, torch.float16: SPV_F16}
 _CACHES = {**_ACTIVATIONS, torch.float8_e4m3fn: SPV_E4M3}
+_F32, _I32, _I64, _U8 = torch.float32, torch.int32, torch.int64, torch.uint8
 
 
 class _CacheStruct(ctypes.Structure):
+    """spv_kv_cache of spv.h."""
     _fields_ = ([("k", ctypes.c_void_p), ("v", ctypes.c_void_p), ("dtype", ctypes.c_int)]
                 + [(n, ctypes.c_int32) for n in ("num_pages", "page_size", "kv_heads", "head_dim")]
                 + [(f"{p}_{n}_stride", ctypes.c_int64) for p in "kv" for n in ("page", "slot", "head")]
                 + [("k_scale", ctypes.c_void_p), ("v_scale", ctypes.c_void_p)])
+
+
+# These calls take a few microseconds on the GPU, so the checks below are written to cost little: the struct is packed
+# as bytes (the layout of _CacheStruct), and a tensor's properties are compared at once and looked at one by one only
+# to say what is wrong.
+_PACK = struct.Struct("@PPiiiii4xqqqqqqPP").pack
+_PACK_STRIDES = struct.Struct("@6q").pack
 
 
 @dataclass
@@ -40,81 +50,115 @@ class KVCache:
     k_scale: torch.Tensor | None = None
     v_scale: torch.Tensor | None = None
 
-    def struct(self) -> _CacheStruct:
+    def packed(self):
+        """(spv_kv_cache as bytes, device, its shape [pages, page_size, kv_heads, head_dim])."""
+        k, v = self.k, self.v
+        try:
+            shape, dtype, dev = k.shape, k.dtype, k.device
+            ks, vs = k.stride(), v.stride()
+            if not k.is_cuda or len(shape) != 4 or dtype not in _CACHES or v.shape != shape or v.dtype != dtype \
+                    or v.device != dev or (shape[3] > 1 and (ks[3] != 1 or vs[3] != 1)):
+                self._complain()
+        except AttributeError:
+            raise ValueError("cache.k and cache.v must be CUDA tensors") from None
+        heads = (shape[2],)
+        sk = 0 if self.k_scale is None else _arg(self.k_scale, "k_scale", _F32, heads, dev)
+        sv = 0 if self.v_scale is None else _arg(self.v_scale, "v_scale", _F32, heads, dev)
+        if 1 in shape:  # a dimension of one entry may carry any stride: it is never stepped over
+            ks = [x if n > 1 else 0 for x, n in zip(ks, shape)]
+            vs = [x if n > 1 else 0 for x, n in zip(vs, shape)]
+        try:
+            return (_PACK(k.data_ptr(), v.data_ptr(), _CACHES[dtype], *shape, ks[0], ks[1], ks[2], vs[0], vs[1], vs[2],
+                          sk, sv), dev, shape)
+        except struct.error:
+            raise ValueError("the cache's sizes do not fit 32 bits") from None
+
+    def _complain(self):
         k, v = self.k, self.v
         for name, t in (("cache.k", k), ("cache.v", v)):
-            if not isinstance(t, torch.Tensor) or not t.is_cuda:
+            if not t.is_cuda:
                 raise ValueError(f"{name} must be a CUDA tensor")
             if t.dim() != 4 or (t.shape[3] > 1 and t.stride(3) != 1):
                 raise ValueError(f"{name} must be [pages, page_size, kv_heads, head_dim] with contiguous rows")
             if t.dtype not in _CACHES:
                 raise TypeError(f"{name} must be bfloat16, float16 or float8_e4m3fn, got {t.dtype}")
-        if k.shape != v.shape or k.dtype != v.dtype or k.device != v.device:
-            raise ValueError("cache.k and cache.v must have the same shape, dtype and device")
-        for name, s in (("k_scale", self.k_scale), ("v_scale", self.v_scale)):
-            if s is not None:
-                _on(_cuda(s, name, torch.float32), name, k.device)
-                if tuple(s.shape) != (k.shape[2],):
-                    raise ValueError(f"{name} must be [kv_heads]")
-        # a dimension of one entry may carry any stride: it is never stepped over
-        strides = [t.stride(i) if t.shape[i] > 1 else 0 for t in (k, v) for i in (0, 1, 2)]
-        return _CacheStruct(_ptr(k), _ptr(v), _CACHES[k.dtype], *k.shape, *strides, _ptr(self.k_scale),
-                            _ptr(self.v_scale))
+        raise ValueError("cache.k and cache.v must have the same shape, dtype and device")
 
 
-def _on(t, name, device):
-    if t is not None and t.device != device:
-        raise ValueError(f"{name} must be on {device}, got {t.device}")
-    return t
-
-
-def _ints(t, name, shape, device):
-    """An optional int32 tensor of the given shape."""
-    if t is None:
-        return None
-    _on(_cuda(t, name, torch.int32), name, device)
+def _arg(t, name, dtype, shape, dev):
+    """Address of a contiguous tensor of this dtype, shape and device."""
+    try:
+        if t.dtype is dtype and t.shape == shape and t.device == dev and t.is_contiguous():
+            return t.data_ptr()
+    except AttributeError:
+        pass
+    if not isinstance(t, torch.Tensor) or not t.is_cuda:
+        raise ValueError(f"{name} must be a CUDA tensor")
+    if t.dtype != dtype:
+        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
     if tuple(t.shape) != tuple(shape):
         raise ValueError(f"{name} must be {list(shape)}, got {list(t.shape)}")
-    return t
+    if t.device != dev:
+        raise ValueError(f"{name} must be on {dev}, got {t.device}")
+    raise ValueError(f"{name} must be contiguous")
 
 
-def _floats(t, name, shape, device):
-    if t is None:
-        return None
-    _on(_cuda(t, name, torch.float32), name, device)
-    if tuple(t.shape) != tuple(shape):
-        raise ValueError(f"{name} must be {list(shape)}, got {list(t.shape)}")
-    return t
+def _opt(t, name, dtype, shape, dev):
+    return None if t is None else _arg(t, name, dtype, shape, dev)
 
 
-def _output(out, key, shape, dtype, device):
-    """The caller's output tensor `key`, checked, or a new one."""
+def _output(out, key, shape, dtype, dev):
+    """Address of the caller's output tensor `key`, checked, or of a new one."""
     t = out.get(key)
     if t is None:
-        t = out[key] = torch.empty(shape, dtype=dtype, device=device)
-        return t
-    _on(_cuda(t, f"out[{key!r}]", dtype), f"out[{key!r}]", device)
-    if tuple(t.shape) != tuple(shape):
-        raise ValueError(f"out[{key!r}] must be {list(shape)}, got {list(t.shape)}")
-    return t
+        t = out[key] = torch.empty(shape, dtype=dtype, device=dev)
+        return t.data_ptr()
+    return _arg(t, key, dtype, shape, dev)
 
 
-def _table(page_table, B, device):
-    _on(_cuda(page_table, "page_table", torch.int32), "page_table", device)
-    if page_table.dim() != 2 or page_table.shape[0] != B:
+def _table(page_table, B, dev):
+    try:
+        shape = page_table.shape
+    except AttributeError:
+        raise ValueError("page_table must be a CUDA tensor") from None
+    if len(shape) != 2 or shape[0] != B:
         raise ValueError("page_table must be [B, max_pages]")
-    return page_table
+    return _arg(page_table, "page_table", _I32, shape, dev), shape[1]
 
 
-def _queries(q, cache):
-    """Checks q [B, T, q_heads, head_dim] against the cache: its sizes, dtype code and the cache struct."""
-    c = cache.struct()
-    q = _on(_cuda(q, "q"), "q", cache.k.device)
-    if q.dim() != 4 or q.shape[3] != c.head_dim:
+def _queries(q, head_dim, dev):
+    """q [B, T, q_heads, head_dim]: its sizes, dtype code and address."""
+    try:
+        shape, code = q.shape, _ACTIVATIONS.get(q.dtype)
+    except AttributeError:
+        raise ValueError("q must be a CUDA tensor") from None
+    if len(shape) != 4 or shape[3] != head_dim:
         raise ValueError("q must be [B, T, q_heads, head_dim]")
-    if q.dtype not in _ACTIVATIONS:
+    if code is None:
         raise TypeError(f"q must be bfloat16 or float16, got {q.dtype}")
-    return c, *q.shape[:3], _ACTIVATIONS[q.dtype]
+    return shape, code, _arg(q, "q", q.dtype, shape, dev)
+
+
+def _complain_qkv(tensors, shape, kv_shape, dtype, dev):
+    for name, t, want in zip("qkv", tensors, (shape, kv_shape, kv_shape)):
+        if t.dtype != dtype:
+            raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+        if t.shape != want:
+            raise ValueError(f"{name} must be {list(want)}, got {list(t.shape)}")
+        if t.device != dev:
+            raise ValueError(f"{name} must be on {dev}, got {t.device}")
+        if t.stride(3) != 1 or (want[2] > 1 and t.stride(2) != want[3]):
+            raise ValueError(f"{name}: the heads of a token must be contiguous")
+
+
+_current_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+
+
+def _on_stream(stream, dev):
+    """The stream's handle: torch's current one unless the caller names another."""
+    if stream is None and _current_raw_stream is not None and dev.index is not None:
+        return _current_raw_stream(dev.index)
+    return _stream(stream, dev)
 
 
 def spv_rope_frequencies(rotary_dim: int, base: float = 10000.0, *, scaling: str = "plain", factor: float = 1.0,
@@ -142,51 +186,46 @@ def spv_rope_append(q, k, v, cache: KVCache, page_table, ctx_lens, freqs, *, int
     batch and token strides.  freqs: :func:`spv_rope_frequencies` of the
     rotary_dim.  Returns dict(q, and row_status when requested); out["q"] may
     be q itself."""
-    c = cache.struct()
-    dev = cache.k.device
-    if not isinstance(q, torch.Tensor) or q.dim() != 4 or q.shape[3] != c.head_dim:
-        raise ValueError("q must be [B, T, q_heads, head_dim]")
-    B, T, Hq, D = q.shape
-    if q.dtype not in _ACTIVATIONS:
-        raise TypeError(f"q must be bfloat16 or float16, got {q.dtype}")
-    strides = []
-    for name, t, heads in (("q", q, Hq), ("k", k, c.kv_heads), ("v", v, c.kv_heads)):
-        if not isinstance(t, torch.Tensor) or not t.is_cuda:
-            raise ValueError(f"{name} must be a CUDA tensor")
-        _on(t, name, dev)
-        if t.dtype != q.dtype:
-            raise TypeError(f"{name} must be {q.dtype}, got {t.dtype}")
-        if tuple(t.shape) != (B, T, heads, D):
-            raise ValueError(f"{name} must be [B, T, {heads}, {D}]")
-        if t.stride(3) != 1 or (heads > 1 and t.stride(2) != D):
-            raise ValueError(f"{name}: the heads of a token must be contiguous")
-        strides += [t.stride(0) if B > 1 else 0, t.stride(1) if T > 1 else 0]
-    if strides[0] == 0:  # one sequence: the packed stride, so that q can be its own output
-        strides[0] = T * Hq * D
-    if strides[1] == 0:
-        strides[1] = Hq * D
-    freqs = _on(_cuda(freqs, "freqs", torch.int64), "freqs", dev)
-    if freqs.dim() != 1 or 2 * freqs.numel() > D:
+    pack, dev, (_, _, Hkv, D) = cache.packed()
+    try:
+        shape, dtype = q.shape, q.dtype
+        code = _ACTIVATIONS.get(dtype)
+        if len(shape) != 4 or shape[3] != D:
+            raise ValueError("q must be [B, T, q_heads, head_dim]")
+        if code is None:
+            raise TypeError(f"q must be bfloat16 or float16, got {dtype}")
+        B, T, Hq, _ = shape
+        kv_shape = (B, T, Hkv, D)
+        sq, sk, sv = q.stride(), k.stride(), v.stride()
+        if k.shape != kv_shape or v.shape != kv_shape or k.dtype is not dtype or v.dtype is not dtype or q.device != dev \
+                or k.device != dev or v.device != dev or sq[3] != 1 or sk[3] != 1 or sv[3] != 1 \
+                or (Hq > 1 and sq[2] != D) or (Hkv > 1 and (sk[2] != D or sv[2] != D)):
+            _complain_qkv((q, k, v), shape, kv_shape, dtype, dev)
+        pairs = freqs.shape[0] if freqs.dim() == 1 else D
+    except AttributeError:
+        raise ValueError("q, k, v and freqs must be CUDA tensors") from None
+    if B == 1 or T == 1:
+        # a dimension of one entry may carry any stride: its packed one, so that q can be its own output
+        sq, sk, sv = (((T * (s[1] if T > 1 else h * D) if B == 1 else s[0]), s[1] if T > 1 else h * D)
+                      for s, h in ((sq, Hq), (sk, Hkv), (sv, Hkv)))
+    if 2 * pairs > D:
         raise ValueError("freqs must be [rotary_dim / 2], rotary_dim <= head_dim")
-    page_table = _table(page_table, B, dev)
-    ctx_lens = _ints(ctx_lens, "ctx_lens", (B,), dev)
-    new_lens = _ints(new_lens, "new_lens", (B,), dev)
-    positions = _ints(positions, "positions", (B, T), dev)
+    table, pages = _table(page_table, B, dev)
+    slots = 0
     if slot_pos is not None:
-        _on(_cuda(slot_pos, "slot_pos", torch.int32), "slot_pos", dev)
-        if slot_pos.dim() != 3 or tuple(slot_pos.shape[:2]) != (B, c.kv_heads):
+        if slot_pos.dim() != 3:
             raise ValueError("slot_pos must be [B, kv_heads, slots]")
+        slots = slot_pos.shape[2]
     out = dict(out) if out else {}
-    _output(out, "q", (B, T, Hq, D), q.dtype, dev)
-    if want_status:
-        _output(out, "row_status", (B,), torch.int32, dev)
     st = load_library().spv_rope_append(
-        _ptr(q), _ptr(k), _ptr(v), _ACTIVATIONS[q.dtype], (ctypes.c_int64 * 6)(*strides), B, T, Hq, _ptr(freqs),
-        2 * freqs.numel(), int(bool(interleaved)), float(mscale), _ptr(positions), _ptr(ctx_lens), _ptr(new_lens),
-        _ptr(page_table), page_table.shape[1], ctypes.byref(c), _ptr(slot_pos),
-        slot_pos.shape[2] if slot_pos is not None else 0, _ptr(out["q"]), _ptr(out.get("row_status")),
-        _stream(stream, dev))
-    _check(st, "spv_rope_append")
+        q.data_ptr(), k.data_ptr(), v.data_ptr(), code, _PACK_STRIDES(sq[0], sq[1], sk[0], sk[1], sv[0], sv[1]), B, T, Hq,
+        _arg(freqs, "freqs", _I64, (pairs,), dev), 2 * pairs, int(bool(interleaved)), mscale,
+        _opt(positions, "positions", _I32, (B, T), dev),
+        _arg(ctx_lens, "ctx_lens", _I32, (B,), dev), _opt(new_lens, "new_lens", _I32, (B,), dev), table, pages, pack,
+        _opt(slot_pos, "slot_pos", _I32, (B, Hkv, slots), dev), slots, _output(out, "q", (B, T, Hq, D), dtype, dev),
+        _output(out, "row_status", (B,), _I32, dev) if want_status else None, _on_stream(stream, dev))
+    if st:
+        raise SpvError(st, "spv_rope_append")
     return out
 
 
@@ -202,28 +241,23 @@ def spv_paged_attention(q, cache: KVCache, page_table, ctx_lens, *, new_lens=Non
     ``parent`` [B, T] a draft tree (see spv_paged_attention in spv.h).  scale
     defaults to 1 / sqrt(D).  Returns dict(out [B, T, q_heads, D], and lse [B,
     T, q_heads] / row_status when requested)."""
-    c, B, T, Hq, dt = _queries(q, cache)
-    dev = q.device
-    page_table = _table(page_table, B, dev)
-    ctx_lens = _ints(ctx_lens, "ctx_lens", (B,), dev)
-    new_lens = _ints(new_lens, "new_lens", (B,), dev)
-    parent = _ints(parent, "parent", (B, T), dev)
+    pack, dev, (_, _, Hkv, D) = cache.packed()
+    shape, code, address = _queries(q, D, dev)
+    B, T, Hq, _ = shape
+    table, pages = _table(page_table, B, dev)
     lib = load_library()
     if workspace is None:
-        workspace = new_workspace(lib.spv_attention_workspace_bytes(B, T, Hq, c.kv_heads, c.head_dim), dev)
-    _on(_cuda(workspace, "workspace"), "workspace", dev)
+        workspace = new_workspace(lib.spv_attention_workspace_bytes(B, T, Hq, Hkv, D), dev)
     out = dict(out) if out else {}
-    _output(out, "out", tuple(q.shape), q.dtype, dev)
-    if want_lse:
-        _output(out, "lse", (B, T, Hq), torch.float32, dev)
-    if want_status:
-        _output(out, "row_status", (B,), torch.int32, dev)
     st = lib.spv_paged_attention(
-        _ptr(q), dt, B, T, Hq, ctypes.byref(c), _ptr(page_table), page_table.shape[1], _ptr(ctx_lens), _ptr(new_lens),
-        _ptr(parent), 1.0 / math.sqrt(c.head_dim) if scale is None else float(scale), _ptr(out["out"]),
-        _ptr(out.get("lse")), _ptr(out.get("row_status")), _ptr(workspace),
-        workspace.numel() * workspace.element_size(), _stream(stream, dev))
-    _check(st, "spv_paged_attention")
+        address, code, B, T, Hq, pack, table, pages, _arg(ctx_lens, "ctx_lens", _I32, (B,), dev),
+        _opt(new_lens, "new_lens", _I32, (B,), dev), _opt(parent, "parent", _I32, (B, T), dev),
+        1.0 / math.sqrt(D) if scale is None else scale, _output(out, "out", shape, q.dtype, dev),
+        _output(out, "lse", (B, T, Hq), _F32, dev) if want_lse else None,
+        _output(out, "row_status", (B,), _I32, dev) if want_status else None,
+        _arg(workspace, "workspace", _U8, (workspace.numel(),), dev), workspace.numel(), _on_stream(stream, dev))
+    if st:
+        raise SpvError(st, "spv_paged_attention")
     return out
 
 
@@ -237,33 +271,27 @@ def spv_attention_mass(q, lse, cache: KVCache, page_table, ctx_lens, accept_coun
     (and, for a tree, nodes: out_nodes) from the verify call.  Without
     ``mass_in`` and ``out`` a zero-filled mass as wide as the page table is
     made."""
-    c, B, T, Hq, dt = _queries(q, cache)
-    dev = q.device
-    lse = _floats(lse, "lse", (B, T, Hq), dev)
-    page_table = _table(page_table, B, dev)
-    ctx_lens = _ints(ctx_lens, "ctx_lens", (B,), dev)
-    accept_count = _ints(accept_count, "accept_count", (B,), dev)
-    nodes = _ints(nodes, "nodes", (B, T), dev)
-    new_lens = _ints(new_lens, "new_lens", (B,), dev)
-    parent = _ints(parent, "parent", (B, T), dev)
+    pack, dev, (_, page_size, Hkv, D) = cache.packed()
+    shape, code, address = _queries(q, D, dev)
+    B, T, Hq, _ = shape
+    table, pages = _table(page_table, B, dev)
     out = dict(out) if out else {}
     mass = out.get("mass")
     if mass is None:
-        slots = mass_in.shape[2] if mass_in is not None else page_table.shape[1] * c.page_size
-        mass = out["mass"] = torch.zeros(B, c.kv_heads, slots, dtype=torch.float32, device=dev)
+        slots = mass_in.shape[2] if mass_in is not None and mass_in.dim() == 3 else pages * page_size
+        mass = out["mass"] = torch.zeros(B, Hkv, slots, dtype=_F32, device=dev)
     if mass.dim() != 3:
         raise ValueError("out['mass'] must be [B, kv_heads, slots]")
-    slots = mass.shape[2]
-    _floats(mass, "out['mass']", (B, c.kv_heads, slots), dev)
-    mass_in = _floats(mass_in, "mass_in", (B, c.kv_heads, slots), dev)
-    if want_status:
-        _output(out, "row_status", (B,), torch.int32, dev)
+    full = (B, Hkv, mass.shape[2])
     st = load_library().spv_attention_mass(
-        _ptr(q), dt, B, T, Hq, _ptr(lse), ctypes.byref(c), _ptr(page_table), page_table.shape[1], _ptr(ctx_lens),
-        _ptr(new_lens), _ptr(parent), 1.0 / math.sqrt(c.head_dim) if scale is None else float(scale),
-        _ptr(accept_count), _ptr(nodes), float(decay), _ptr(mass_in), _ptr(mass), slots, _ptr(out.get("row_status")),
-        _stream(stream, dev))
-    _check(st, "spv_attention_mass")
+        address, code, B, T, Hq, _arg(lse, "lse", _F32, (B, T, Hq), dev), pack, table, pages,
+        _arg(ctx_lens, "ctx_lens", _I32, (B,), dev), _opt(new_lens, "new_lens", _I32, (B,), dev),
+        _opt(parent, "parent", _I32, (B, T), dev), 1.0 / math.sqrt(D) if scale is None else scale,
+        _arg(accept_count, "accept_count", _I32, (B,), dev), _opt(nodes, "nodes", _I32, (B, T), dev), decay,
+        _opt(mass_in, "mass_in", _F32, full, dev), _arg(mass, "out['mass']", _F32, full, dev), full[2],
+        _output(out, "row_status", (B,), _I32, dev) if want_status else None, _on_stream(stream, dev))
+    if st:
+        raise SpvError(st, "spv_attention_mass")
     return out
 
 
@@ -275,27 +303,25 @@ def spv_kv_evict(cache: KVCache, page_table, lens, mass, budget: int, *, pos=Non
     budget], lens [B], slot_src [B, kv_heads, budget], and row_status when
     requested); pass ``mass`` and ``pos`` themselves in ``out`` to update them
     in place."""
-    c = cache.struct()
-    dev = cache.k.device
-    mass = _on(_cuda(mass, "mass", torch.float32), "mass", dev)
-    if mass.dim() != 3 or mass.shape[1] != c.kv_heads:
+    pack, dev, (_, _, Hkv, _) = cache.packed()
+    try:
+        full = mass.shape
+    except AttributeError:
+        raise ValueError("mass must be a CUDA tensor") from None
+    if len(full) != 3 or full[1] != Hkv:
         raise ValueError("mass must be [B, kv_heads, slots]")
-    B, Hkv, slots = mass.shape
-    page_table = _table(page_table, B, dev)
-    lens = _ints(lens, "lens", (B,), dev)
-    pos = _ints(pos, "pos", tuple(mass.shape), dev)
+    B, _, slots = full
+    table, pages = _table(page_table, B, dev)
     budget = int(budget)
     out = dict(out) if out else {}
-    width = max(out["mass"].shape[-1] if out.get("mass") is not None else min(budget, slots), 0)
-    _output(out, "mass", (B, Hkv, width), torch.float32, dev)
-    _output(out, "pos", (B, Hkv, width), torch.int32, dev)
-    _output(out, "lens", (B,), torch.int32, dev)
-    _output(out, "slot_src", (B, Hkv, max(budget, 0)), torch.int32, dev)
-    if want_status:
-        _output(out, "row_status", (B,), torch.int32, dev)
+    kept = out.get("mass")
+    width = kept.shape[-1] if kept is not None else max(min(budget, slots), 0)
     st = load_library().spv_kv_evict(
-        ctypes.byref(c), _ptr(page_table), page_table.shape[1], B, _ptr(lens), budget, int(sinks), int(recent),
-        _ptr(mass), _ptr(pos), slots, _ptr(out["mass"]), _ptr(out["pos"]), width, _ptr(out["lens"]),
-        _ptr(out["slot_src"]), _ptr(out.get("row_status")), _stream(stream, dev))
-    _check(st, "spv_kv_evict")
+        pack, table, pages, B, _arg(lens, "lens", _I32, (B,), dev), budget, int(sinks), int(recent),
+        _arg(mass, "mass", _F32, full, dev), _opt(pos, "pos", _I32, full, dev), slots,
+        _output(out, "mass", (B, Hkv, width), _F32, dev), _output(out, "pos", (B, Hkv, width), _I32, dev), width,
+        _output(out, "lens", (B,), _I32, dev), _output(out, "slot_src", (B, Hkv, max(budget, 0)), _I32, dev),
+        _output(out, "row_status", (B,), _I32, dev) if want_status else None, _on_stream(stream, dev))
+    if st:
+        raise SpvError(st, "spv_kv_evict")
     return out
