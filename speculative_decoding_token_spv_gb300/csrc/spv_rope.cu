@@ -1,11 +1,13 @@
 // spv_rope.cu -- rotary positions of new tokens' q and k, joined with the
 // write of k and v into the paged cache.
 //
-// A block takes one token: its threads first compute the token's rotary_dim / 2 cosines and sines into shared memory, once for all
-// heads, then move the heads 8 elements (16 bytes) at a time.  The angle is
-// the integer product of the position with a 64-bit fraction of a turn: the
-// wrap of the product is the reduction to one turn, exact at any position,
-// with no 64-bit floating point.
+// A block takes one token, or four of a sequence in turn where there are
+// enough to fill the GPU: its threads first compute the tokens' cosines and
+// sines into shared memory, once for all heads.  A thread then keeps its place
+// within a head -- 8 elements, 16 bytes, and their cosines and sines in
+// registers -- and walks over the heads.  The angle is the integer product of
+// the position with a 64-bit fraction of a turn: the wrap of the product is the
+// reduction to one turn, exact at any position, with no 64-bit floating point.
 #include "spv_kv.cuh"
 
 namespace spv {
@@ -52,132 +54,200 @@ enum RopeMode {
 template <int MODE> __device__ __forceinline__ int head_tasks(const RopeParams &p)
 {
     if (MODE == ROPE_PAIRS) return p.D >> 3;
-    if (MODE == ROPE_HALVES) return (p.half >> 3) + ((p.D - 2 * p.half) >> 3);
-    return ((p.half + 7) >> 3) + ((p.D - 2 * p.half + 7) >> 3);
+    return (p.half >> 3) + ((p.D - 2 * p.half) >> 3);
 }
 
-template <int MODE, typename T, typename C>
-__device__ __forceinline__ void rope_task(const T *src, C *dst, int i, const float2 *cs, const RopeParams &p, float div)
+constexpr int ROPE_THREADS = 256;
+constexpr int ROPE_TOKENS = 4;  // of a block, where there are many
+
+// A thread's place within each head that it visits, and what turns it there.
+template <int MODE> struct RopePlace {
+    int d, other;            // its 8 elements begin here, their partners there (-1: none)
+    float c[8], s[8];        // interleaved: of the 4 pairs, each twice
+    bool turns;
+};
+
+template <int MODE, typename T> struct RopeData {
+    uint4 x, y;
+};
+template <int MODE, typename T>
+__device__ __forceinline__ void rope_read(RopeData<MODE, T> &v, const T *row, const RopePlace<MODE> &at)
 {
-    if (MODE == ROPE_PAIRS) {
-        float y[8];
-        load8(src + 8 * i, y);
+    v.x = *reinterpret_cast<const uint4 *>(row + at.d);
+    if (MODE == ROPE_HALVES && at.other >= 0) v.y = *reinterpret_cast<const uint4 *>(row + at.other);
+}
+template <int MODE, typename T, typename C>
+__device__ __forceinline__ void rope_write(const RopeData<MODE, T> &v, C *row, const RopePlace<MODE> &at, float div)
+{
+    const T *xs = reinterpret_cast<const T *>(&v.x);
+    float u[8];
 #pragma unroll
-        for (int j = 0; j < 8; j += 2)
-            if (8 * i + j < 2 * p.half) {
-                const float2 w = cs[4 * i + (j >> 1)];
-                const float u = y[j], v = y[j + 1];
-                y[j] = u * w.x - v * w.y;
-                y[j + 1] = v * w.x + u * w.y;
-            }
-        store8(dst + 8 * i, y, div);
-    } else if (MODE == ROPE_HALVES) {
-        const int n = p.half >> 3;
-        float y[8];
-        if (i >= n) {
-            const int d = 2 * p.half + 8 * (i - n);
-            load8(src + d, y);
-            store8(dst + d, y, div);
-            return;
-        }
-        float z[8];
-        load8(src + 8 * i, y);
-        load8(src + 8 * i + p.half, z);
+    for (int j = 0; j < 8; ++j) u[j] = Num<T>::up(xs[j]);
+    if (MODE == ROPE_HALVES && at.other >= 0) {
+        const T *ys = reinterpret_cast<const T *>(&v.y);
+        float w[8];
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
-            const float2 w = cs[8 * i + j];
-            const float u = y[j], v = z[j];
-            y[j] = u * w.x - v * w.y;
-            z[j] = v * w.x + u * w.y;
+            const float u0 = u[j], w0 = Num<T>::up(ys[j]);
+            u[j] = u0 * at.c[j] - w0 * at.s[j];
+            w[j] = w0 * at.c[j] + u0 * at.s[j];
         }
-        store8(dst + 8 * i, y, div);
-        store8(dst + 8 * i + p.half, z, div);
-    } else {
-        const int n = (p.half + 7) >> 3;
-        for (int j = 0; j < 8; ++j) {
-            if (i >= n) {
-                const int d = 2 * p.half + 8 * (i - n) + j;
-                if (d < p.D) dst[d] = Num<C>::down(sizeof(C) == 1 ? Num<T>::up(src[d]) / div : Num<T>::up(src[d]));
-                continue;
-            }
-            const int d = 8 * i + j;
-            if (d >= p.half) return;
-            const float2 w = cs[d];
-            const float u = Num<T>::up(src[d]), v = Num<T>::up(src[d + p.half]);
-            const float a = u * w.x - v * w.y, b = v * w.x + u * w.y;
-            dst[d] = Num<C>::down(sizeof(C) == 1 ? a / div : a);
-            dst[d + p.half] = Num<C>::down(sizeof(C) == 1 ? b / div : b);
+        store8(row + at.other, w, div);
+    }
+    if (MODE == ROPE_PAIRS && at.turns) {
+#pragma unroll
+        for (int j = 0; j < 8; j += 2) {
+            const float u0 = u[j], w0 = u[j + 1];
+            u[j] = u0 * at.c[j] - w0 * at.s[j];
+            u[j + 1] = w0 * at.c[j] + u0 * at.s[j];
         }
     }
+    store8(row + at.d, u, div);
 }
 
-template <int MODE, typename T, typename C> __global__ void __launch_bounds__(256) rope_kernel(const RopeParams p)
+template <int MODE, int TOKENS, typename T, typename C>
+__global__ void __launch_bounds__(ROPE_THREADS) rope_kernel(const RopeParams p)
 {
-    __shared__ float2 cs[256];
-    const int n = blockIdx.x, b = n / p.T, t = n - b * p.T;
+    extern __shared__ float2 cs[];  // [token][pair]
+    const int tid = threadIdx.x, blocks = (p.T + TOKENS - 1) / TOKENS, b = blockIdx.x / blocks;
+    const int t0 = (blockIdx.x - b * blocks) * TOKENS, tokens = min(TOKENS, p.T - t0);
+    const int n0 = b * p.T + t0;
     const SeqLens s = seq_lens(p.ctx_lens, p.new_lens, b, p.T, p.c);
-    const int32_t *row = p.c.table + static_cast<int64_t>(b) * p.c.max_pages;
-    if (t == 0 && p.row_status) {  // all pages that the sequence's new tokens touch
+    const int32_t *table = p.c.table + static_cast<int64_t>(b) * p.c.max_pages;
+    if (t0 == 0 && p.row_status) {  // all pages that the sequence's new tokens touch
         int bad = s.bad;
         if (s.total > 0)
-            for (int g = (s.ctx >> p.c.page_shift) + threadIdx.x; g <= (s.total - 1) >> p.c.page_shift; g += blockDim.x)
-                bad |= page_of(p.c, row, g << p.c.page_shift) < 0;
+            for (int g = (s.ctx >> p.c.page_shift) + tid; g <= (s.total - 1) >> p.c.page_shift; g += ROPE_THREADS)
+                bad |= page_of(p.c, table, g << p.c.page_shift) < 0;
         bad = __syncthreads_or(bad);
-        if (threadIdx.x == 0) p.row_status[b] = bad ? KV_STATUS_BAD : 0;
+        if (tid == 0) p.row_status[b] = bad ? KV_STATUS_BAD : 0;
     }
-    T *q_out = static_cast<T *>(p.q_out) + static_cast<int64_t>(n) * p.q_heads * p.D;
-    if (s.bad || t >= s.fresh) {
-        for (int i = threadIdx.x; i < p.q_heads * (p.D >> 3); i += blockDim.x)
-            reinterpret_cast<uint4 *>(q_out)[i] = uint4{};
-        return;
-    }
-    const int slot = s.ctx + t;
-    const int pos = p.positions ? __ldg(p.positions + n) : slot;
-    for (int i = threadIdx.x; i < p.half; i += blockDim.x) {
-        const unsigned long long turn = static_cast<unsigned long long>(static_cast<long long>(pos)) * __ldg(p.freqs + i);
+    const int live = s.bad ? 0 : max(0, min(tokens, s.fresh - t0));
+    for (int i = tid; i < live * p.half; i += ROPE_THREADS) {
+        const int tk = TOKENS == 1 ? 0 : i / p.half, e = i - tk * p.half;
+        const int pos = p.positions ? __ldg(p.positions + n0 + tk) : s.ctx + t0 + tk;
+        const unsigned long long turn = static_cast<unsigned long long>(static_cast<long long>(pos)) * __ldg(p.freqs + e);
         // the top 32 bits, signed: half a turn either way, at most 2^-33 turns off
         float sn, cn;
         sincospif(static_cast<float>(static_cast<int>((turn + (1ull << 31)) >> 32)) * 0x1p-31f, &sn, &cn);
         cs[i] = make_float2(cn * p.mscale, sn * p.mscale);
     }
-    const int page = page_of(p.c, row, slot);
-    if (p.slot_pos && slot < p.pos_stride)
-        for (int h = threadIdx.x; h < p.c.kv_heads; h += blockDim.x)
-            p.slot_pos[(static_cast<int64_t>(b) * p.c.kv_heads + h) * p.pos_stride + slot] = pos;
+    if (p.slot_pos)
+        for (int i = tid; i < live * p.c.kv_heads; i += ROPE_THREADS) {
+            const int tk = i / p.c.kv_heads, h = i - tk * p.c.kv_heads, slot = s.ctx + t0 + tk;
+            if (slot < p.pos_stride)
+                p.slot_pos[(static_cast<int64_t>(b) * p.c.kv_heads + h) * p.pos_stride + slot] =
+                    p.positions ? __ldg(p.positions + n0 + tk) : slot;
+        }
     __syncthreads();
-    const int per = head_tasks<MODE>(p), D8 = p.D >> 3;
-    const T *q = static_cast<const T *>(p.q) + b * p.stride[0] + t * p.stride[1];
-    for (int i = threadIdx.x; i < p.q_heads * per; i += blockDim.x) {
-        const int h = i / per;
-        rope_task<MODE>(q + h * p.D, q_out + h * p.D, i - h * per, cs, p, 1.0f);
-    }
-    if (page < 0) return;
-    const T *k = static_cast<const T *>(p.k) + b * p.stride[2] + t * p.stride[3];
-    for (int i = threadIdx.x; i < p.c.kv_heads * per; i += blockDim.x) {
-        const int h = i / per;
-        C *dst = reinterpret_cast<C *>(const_cast<char *>(row_ptr(p.c, p.c.k, page, slot, h)));
-        rope_task<MODE>(k + h * p.D, dst, i - h * per, cs, p, sizeof(C) == 1 && p.c.k_scale ? __ldg(p.c.k_scale + h) : 1.0f);
-    }
-    const T *v = static_cast<const T *>(p.v) + b * p.stride[4] + t * p.stride[5];
-    for (int i = threadIdx.x; i < p.c.kv_heads * D8; i += blockDim.x) {
-        const int h = i / D8, d = (i - h * D8) << 3;
-        C *dst = reinterpret_cast<C *>(const_cast<char *>(row_ptr(p.c, p.c.v, page, slot, h)));
-        float y[8];
-        load8(v + h * p.D + d, y);
-        store8(dst + d, y, sizeof(C) == 1 && p.c.v_scale ? __ldg(p.c.v_scale + h) : 1.0f);
+    const int D8 = p.D >> 3, heads = p.q_heads + p.c.kv_heads;
+    for (int tk = 0; tk < tokens; ++tk) {
+        T *q_out = static_cast<T *>(p.q_out) + static_cast<int64_t>(n0 + tk) * p.q_heads * p.D;
+        if (tk >= live) {
+            for (int i = tid; i < p.q_heads * D8; i += ROPE_THREADS) reinterpret_cast<uint4 *>(q_out)[i] = uint4{};
+            continue;
+        }
+        const int slot = s.ctx + t0 + tk, page = page_of(p.c, table, slot);
+        const T *q = static_cast<const T *>(p.q) + b * p.stride[0] + (t0 + tk) * p.stride[1];
+        const T *k = static_cast<const T *>(p.k) + b * p.stride[2] + (t0 + tk) * p.stride[3];
+        const T *v = static_cast<const T *>(p.v) + b * p.stride[4] + (t0 + tk) * p.stride[5];
+        char *k_row = const_cast<char *>(row_ptr(p.c, p.c.k, page < 0 ? 0 : page, slot, 0));
+        char *v_row = const_cast<char *>(row_ptr(p.c, p.c.v, page < 0 ? 0 : page, slot, 0));
+        const float2 *mine = cs + tk * p.half;
+        auto k_at = [&](int h) { return reinterpret_cast<C *>(k_row + (h - p.q_heads) * p.c.k.head_stride); };
+        auto k_div = [&](int h) { return sizeof(C) == 1 && p.c.k_scale ? __ldg(p.c.k_scale + h - p.q_heads) : 1.0f; };
+        if constexpr (MODE == ROPE_SCALAR) {
+            // halves whose length is no multiple of 8: element by element, partners by one thread
+            const int each = p.half + p.D - 2 * p.half;
+            for (int i = tid; i < heads * each; i += ROPE_THREADS) {
+                const int h = i / each, e = i - h * each;
+                const T *from = h < p.q_heads ? q + h * p.D : k + (h - p.q_heads) * p.D;
+                const int d = e < p.half ? e : e + p.half, o = e < p.half ? e + p.half : -1;
+                float u = Num<T>::up(from[d]), w = 0.0f;
+                if (o >= 0) {
+                    const float2 a = mine[e];
+                    const float u0 = u, w0 = Num<T>::up(from[o]);
+                    u = u0 * a.x - w0 * a.y;
+                    w = w0 * a.x + u0 * a.y;
+                }
+                if (h < p.q_heads) {
+                    q_out[h * p.D + d] = Num<T>::down(u);
+                    if (o >= 0) q_out[h * p.D + o] = Num<T>::down(w);
+                } else if (page >= 0) {
+                    const float div = k_div(h);
+                    k_at(h)[d] = Num<C>::down(sizeof(C) == 1 ? u / div : u);
+                    if (o >= 0) k_at(h)[o] = Num<C>::down(sizeof(C) == 1 ? w / div : w);
+                }
+            }
+        } else {
+            const int per = head_tasks<MODE>(p), step = ROPE_THREADS / per, h0 = tid / per, e = tid - h0 * per;
+            if (h0 < step) {
+                RopePlace<MODE> at;
+                at.d = 8 * e;
+                at.other = -1;
+                at.turns = false;
+                if (MODE == ROPE_HALVES) {
+                    const int n = p.half >> 3;
+                    if (e < n) {
+                        at.other = at.d + p.half;
+#pragma unroll
+                        for (int j = 0; j < 8; ++j) at.c[j] = mine[at.d + j].x, at.s[j] = mine[at.d + j].y;
+                    } else {
+                        at.d = 2 * p.half + 8 * (e - n);
+                    }
+                } else if (at.d < 2 * p.half) {
+                    at.turns = true;
+#pragma unroll
+                    for (int j = 0; j < 8; j += 2) {
+                        const bool in = at.d + j < 2 * p.half;  // the rotation may end within the 8
+                        const float2 a = in ? mine[(at.d + j) >> 1] : make_float2(1.0f, 0.0f);
+                        at.c[j] = a.x, at.s[j] = a.y;
+                    }
+                }
+                auto from = [&](int h) { return h < p.q_heads ? q + h * p.D : k + (h - p.q_heads) * p.D; };
+                auto write = [&](int h, const RopeData<MODE, T> &x) {
+                    if (h < p.q_heads)
+                        rope_write<MODE, T, T>(x, q_out + h * p.D, at, 1.0f);
+                    else if (page >= 0)
+                        rope_write<MODE, T, C>(x, k_at(h), at, k_div(h));
+                };
+                // two heads' loads on their way together
+                for (int h = h0; h < heads; h += 2 * step) {
+                    RopeData<MODE, T> x, y;
+                    rope_read(x, from(h), at);
+                    if (h + step < heads) rope_read(y, from(h + step), at);
+                    write(h, x);
+                    if (h + step < heads) write(h + step, y);
+                }
+            }
+        }
+        if (page < 0) continue;
+        for (int i = tid; i < p.c.kv_heads * D8; i += ROPE_THREADS) {
+            const int h = i / D8, d = (i - h * D8) << 3;
+            float u[8];
+            load8(v + h * p.D + d, u);
+            store8(reinterpret_cast<C *>(v_row + h * p.c.v.head_stride) + d, u,
+                   sizeof(C) == 1 && p.c.v_scale ? __ldg(p.c.v_scale + h) : 1.0f);
+        }
     }
 }
 
+template <int MODE, typename T, typename C> static cudaError_t launch_mode(const RopeParams &p, cudaStream_t st)
+{
+    // four tokens a block once that still gives every SM eight blocks (at 8 prompts of up to 2,011 tokens, 40 heads of
+    // 128, f16: measured as below); fewer tokens are spread over as many SMs as there are
+    const int smem = p.half * static_cast<int>(sizeof(float2));
+    if (static_cast<int64_t>(p.B) * p.T >= 8 * 152 * ROPE_TOKENS)
+        rope_kernel<MODE, ROPE_TOKENS, T, C><<<p.B * ((p.T + ROPE_TOKENS - 1) / ROPE_TOKENS), ROPE_THREADS, ROPE_TOKENS * smem, st>>>(p);
+    else
+        rope_kernel<MODE, 1, T, C><<<p.B * p.T, ROPE_THREADS, smem, st>>>(p);
+    return cudaGetLastError();
+}
 template <typename T, typename C> static cudaError_t launch(const RopeParams &p, cudaStream_t st)
 {
-    const int grid = p.B * p.T;
-    if (p.interleaved || p.half == 0)
-        rope_kernel<ROPE_PAIRS, T, C><<<grid, 256, 0, st>>>(p);
-    else if (p.half % 8 == 0)
-        rope_kernel<ROPE_HALVES, T, C><<<grid, 256, 0, st>>>(p);
-    else
-        rope_kernel<ROPE_SCALAR, T, C><<<grid, 256, 0, st>>>(p);
-    return cudaGetLastError();
+    if (p.interleaved || p.half == 0) return launch_mode<ROPE_PAIRS, T, C>(p, st);
+    if (p.half % 8 == 0) return launch_mode<ROPE_HALVES, T, C>(p, st);
+    return launch_mode<ROPE_SCALAR, T, C>(p, st);
 }
 
 PagedView paged_view(const KvLaunch &L)
