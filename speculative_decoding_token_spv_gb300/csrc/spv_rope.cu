@@ -79,6 +79,12 @@ __device__ __forceinline__ void rope_read(RopeData<MODE, T> &v, const T *row, co
 template <int MODE, typename T, typename C>
 __device__ __forceinline__ void rope_write(const RopeData<MODE, T> &v, C *row, const RopePlace<MODE> &at, float div)
 {
+    if constexpr (std::is_same<T, C>::value) {
+        if (!at.turns) {
+            *reinterpret_cast<uint4 *>(row + at.d) = v.x;
+            return;
+        }
+    }
     const T *xs = reinterpret_cast<const T *>(&v.x);
     float u[8];
 #pragma unroll
@@ -105,13 +111,53 @@ __device__ __forceinline__ void rope_write(const RopeData<MODE, T> &v, C *row, c
     store8(row + at.d, u, div);
 }
 
+constexpr int ROPE_AHEAD = 3;   // heads of a thread whose elements are asked for a token ahead
+
 template <int MODE, int TOKENS, typename T, typename C>
 __global__ void __launch_bounds__(ROPE_THREADS) rope_kernel(const RopeParams p)
 {
     extern __shared__ float2 cs[];  // [token][pair]
     const int tid = threadIdx.x, blocks = (p.T + TOKENS - 1) / TOKENS, b = blockIdx.x / blocks;
     const int t0 = (blockIdx.x - b * blocks) * TOKENS, tokens = min(TOKENS, p.T - t0);
-    const int n0 = b * p.T + t0;
+    const int n0 = b * p.T + t0, D8 = p.D >> 3, heads = p.q_heads + p.c.kv_heads;
+    const T *q0 = static_cast<const T *>(p.q) + b * p.stride[0] + t0 * p.stride[1];
+    const T *k0 = static_cast<const T *>(p.k) + b * p.stride[2] + t0 * p.stride[3];
+    const T *v0 = static_cast<const T *>(p.v) + b * p.stride[4] + t0 * p.stride[5];
+    // this thread's place in the heads that turn, and in v's, which pass
+    RopePlace<MODE> at;
+    RopePlace<ROPE_PAIRS> v_place;
+    const int per = MODE == ROPE_SCALAR ? 1 : head_tasks<MODE>(p), step = ROPE_THREADS / per, h0 = tid / per < step ? tid / per : heads, e = tid % per;
+    const int v_step = ROPE_THREADS / D8, v_h0 = tid / D8 < v_step ? tid / D8 : p.c.kv_heads;
+    at.d = 8 * e;
+    at.other = -1;
+    at.turns = false;
+    if (MODE == ROPE_HALVES) {
+        at.turns = e < p.half >> 3;
+        if (at.turns)
+            at.other = at.d + p.half;
+        else
+            at.d += p.half;  // past both halves
+    } else if (MODE == ROPE_PAIRS) {
+        at.turns = at.d < 2 * p.half;
+    }
+    v_place.d = 8 * (tid % D8);
+    v_place.other = -1;
+    v_place.turns = false;
+    auto from = [&](int tk, int h) {
+        return h < p.q_heads ? q0 + tk * p.stride[1] + h * p.D : k0 + tk * p.stride[3] + (h - p.q_heads) * p.D;
+    };
+    // The first heads of a token are asked for while the one before is worked on, and those of the first token before
+    // lengths, pages and angles, a chain of loads of their own.
+    RopeData<MODE, T> x[ROPE_AHEAD], x_next[ROPE_AHEAD];
+    RopeData<ROPE_PAIRS, T> v, v_next;
+    auto fetch = [&](int tk, RopeData<MODE, T> (&to)[ROPE_AHEAD], RopeData<ROPE_PAIRS, T> &to_v) {
+        if (MODE == ROPE_SCALAR) return;
+#pragma unroll
+        for (int i = 0; i < ROPE_AHEAD; ++i)
+            if (h0 + i * step < heads) rope_read(to[i], from(tk, h0 + i * step), at);
+        if (v_h0 < p.c.kv_heads) rope_read(to_v, v0 + tk * p.stride[5] + v_h0 * p.D, v_place);
+    };
+    fetch(0, x, v);
     const SeqLens s = seq_lens(p.ctx_lens, p.new_lens, b, p.T, p.c);
     const int32_t *table = p.c.table + static_cast<int64_t>(b) * p.c.max_pages;
     if (t0 == 0 && p.row_status) {  // all pages that the sequence's new tokens touch
@@ -140,17 +186,14 @@ __global__ void __launch_bounds__(ROPE_THREADS) rope_kernel(const RopeParams p)
                     p.positions ? __ldg(p.positions + n0 + tk) : slot;
         }
     __syncthreads();
-    const int D8 = p.D >> 3, heads = p.q_heads + p.c.kv_heads;
     for (int tk = 0; tk < tokens; ++tk) {
+        if (TOKENS > 1 && tk + 1 < live) fetch(tk + 1, x_next, v_next);
         T *q_out = static_cast<T *>(p.q_out) + static_cast<int64_t>(n0 + tk) * p.q_heads * p.D;
         if (tk >= live) {
             for (int i = tid; i < p.q_heads * D8; i += ROPE_THREADS) reinterpret_cast<uint4 *>(q_out)[i] = uint4{};
             continue;
         }
         const int slot = s.ctx + t0 + tk, page = page_of(p.c, table, slot);
-        const T *q = static_cast<const T *>(p.q) + b * p.stride[0] + (t0 + tk) * p.stride[1];
-        const T *k = static_cast<const T *>(p.k) + b * p.stride[2] + (t0 + tk) * p.stride[3];
-        const T *v = static_cast<const T *>(p.v) + b * p.stride[4] + (t0 + tk) * p.stride[5];
         char *k_row = const_cast<char *>(row_ptr(p.c, p.c.k, page < 0 ? 0 : page, slot, 0));
         char *v_row = const_cast<char *>(row_ptr(p.c, p.c.v, page < 0 ? 0 : page, slot, 0));
         const float2 *mine = cs + tk * p.half;
@@ -161,12 +204,12 @@ __global__ void __launch_bounds__(ROPE_THREADS) rope_kernel(const RopeParams p)
             const int each = p.half + p.D - 2 * p.half;
             for (int i = tid; i < heads * each; i += ROPE_THREADS) {
                 const int h = i / each, e = i - h * each;
-                const T *from = h < p.q_heads ? q + h * p.D : k + (h - p.q_heads) * p.D;
+                const T *row = from(tk, h);
                 const int d = e < p.half ? e : e + p.half, o = e < p.half ? e + p.half : -1;
-                float u = Num<T>::up(from[d]), w = 0.0f;
+                float u = Num<T>::up(row[d]), w = 0.0f;
                 if (o >= 0) {
                     const float2 a = mine[e];
-                    const float u0 = u, w0 = Num<T>::up(from[o]);
+                    const float u0 = u, w0 = Num<T>::up(row[o]);
                     u = u0 * a.x - w0 * a.y;
                     w = w0 * a.x + u0 * a.y;
                 }
@@ -180,54 +223,43 @@ __global__ void __launch_bounds__(ROPE_THREADS) rope_kernel(const RopeParams p)
                 }
             }
         } else {
-            const int per = head_tasks<MODE>(p), step = ROPE_THREADS / per, h0 = tid / per, e = tid - h0 * per;
-            if (h0 < step) {
-                RopePlace<MODE> at;
-                at.d = 8 * e;
-                at.other = -1;
-                at.turns = false;
-                if (MODE == ROPE_HALVES) {
-                    const int n = p.half >> 3;
-                    if (e < n) {
-                        at.other = at.d + p.half;
+            if (MODE == ROPE_HALVES && at.turns) {
 #pragma unroll
-                        for (int j = 0; j < 8; ++j) at.c[j] = mine[at.d + j].x, at.s[j] = mine[at.d + j].y;
-                    } else {
-                        at.d = 2 * p.half + 8 * (e - n);
-                    }
-                } else if (at.d < 2 * p.half) {
-                    at.turns = true;
+                for (int j = 0; j < 8; ++j) at.c[j] = mine[at.d + j].x, at.s[j] = mine[at.d + j].y;
+            }
+            if (MODE == ROPE_PAIRS && at.turns) {
 #pragma unroll
-                    for (int j = 0; j < 8; j += 2) {
-                        const bool in = at.d + j < 2 * p.half;  // the rotation may end within the 8
-                        const float2 a = in ? mine[(at.d + j) >> 1] : make_float2(1.0f, 0.0f);
-                        at.c[j] = a.x, at.s[j] = a.y;
-                    }
-                }
-                auto from = [&](int h) { return h < p.q_heads ? q + h * p.D : k + (h - p.q_heads) * p.D; };
-                auto write = [&](int h, const RopeData<MODE, T> &x) {
-                    if (h < p.q_heads)
-                        rope_write<MODE, T, T>(x, q_out + h * p.D, at, 1.0f);
-                    else if (page >= 0)
-                        rope_write<MODE, T, C>(x, k_at(h), at, k_div(h));
-                };
-                // two heads' loads on their way together
-                for (int h = h0; h < heads; h += 2 * step) {
-                    RopeData<MODE, T> x, y;
-                    rope_read(x, from(h), at);
-                    if (h + step < heads) rope_read(y, from(h + step), at);
-                    write(h, x);
-                    if (h + step < heads) write(h + step, y);
+                for (int j = 0; j < 8; j += 2) {
+                    const bool in = at.d + j < 2 * p.half;  // the rotation may end within the 8
+                    const float2 a = in ? mine[(at.d + j) >> 1] : make_float2(1.0f, 0.0f);
+                    at.c[j] = a.x, at.s[j] = a.y;
                 }
             }
+            auto write = [&](int h, const RopeData<MODE, T> &data) {
+                if (h < p.q_heads)
+                    rope_write<MODE, T, T>(data, q_out + h * p.D, at, 1.0f);
+                else if (page >= 0)
+                    rope_write<MODE, T, C>(data, k_at(h), at, k_div(h));
+            };
+#pragma unroll
+            for (int i = 0; i < ROPE_AHEAD; ++i)
+                if (h0 + i * step < heads) write(h0 + i * step, x[i]);
+            for (int h = h0 + ROPE_AHEAD * step; h < heads; h += step) {
+                rope_read(x[0], from(tk, h), at);
+                write(h, x[0]);
+            }
         }
-        if (page < 0) continue;
-        for (int i = tid; i < p.c.kv_heads * D8; i += ROPE_THREADS) {
-            const int h = i / D8, d = (i - h * D8) << 3;
-            float u[8];
-            load8(v + h * p.D + d, u);
-            store8(reinterpret_cast<C *>(v_row + h * p.c.v.head_stride) + d, u,
-                   sizeof(C) == 1 && p.c.v_scale ? __ldg(p.c.v_scale + h) : 1.0f);
+        if (page >= 0) {
+            for (int h = v_h0; h < p.c.kv_heads; h += v_step) {
+                if (MODE == ROPE_SCALAR || h != v_h0) rope_read(v, v0 + tk * p.stride[5] + h * p.D, v_place);
+                rope_write<ROPE_PAIRS, T, C>(v, reinterpret_cast<C *>(v_row + h * p.c.v.head_stride), v_place,
+                                             sizeof(C) == 1 && p.c.v_scale ? __ldg(p.c.v_scale + h) : 1.0f);
+            }
+        }
+        if (TOKENS > 1) {
+#pragma unroll
+            for (int i = 0; i < ROPE_AHEAD; ++i) x[i] = x_next[i];
+            v = v_next;
         }
     }
 }
