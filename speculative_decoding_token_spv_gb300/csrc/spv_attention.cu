@@ -398,7 +398,7 @@ cudaError_t launch_attention(const AttentionLaunch &L, cudaStream_t st)
     // Over 16 rows the 5th-generation tensor cores: at 32 rows, two 131,001-key sequences of 8 key heads, D = 128,
     // they take 180 us of a bf16 cache where the warps here take 188; of an e4m3 cache 184 against 161, as its rows
     // pass through shared memory twice there and once here: then over 32 rows (at 40, 240 against 330).
-    if (p.rows > (eight ? 32 : 16) && D <= 128) return launch_attention_rows(p, k.dtype, k.cache.dtype, D, st);
+    if (p.rows > (eight ? 32 : 16) && D <= 128) return launch_attention_rows(p, k, st);
     if (k.dtype == SPV_BF16)
         return eight ? launch_types<__nv_bfloat16, __nv_fp8_e4m3>(p, D, st)
                      : launch_types<__nv_bfloat16, __nv_bfloat16>(p, D, st);

@@ -108,7 +108,7 @@ constexpr size_t split_bytes(int blocks) { return (static_cast<size_t>(blocks) *
 __device__ __forceinline__ void dependents_launch() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
 __device__ __forceinline__ void dependents_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 
-cudaError_t launch_attention_rows(const AttParams &p, spv_dtype q, spv_dtype cache, int D, cudaStream_t st);
+cudaError_t launch_attention_rows(const AttParams &p, const KvLaunch &L, cudaStream_t st);
 size_t attention_rows_part_floats(int head_dim);  // of all blocks' pieces
 
 }  // namespace spv

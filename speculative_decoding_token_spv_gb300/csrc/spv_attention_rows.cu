@@ -23,6 +23,7 @@
 // workspace, ends the block in order and leaves NaN in what it had to write.
 #include "spv_attention.cuh"
 #include "spv_tcgen.cuh"
+#include "spv_tma.cuh"
 
 namespace spv {
 
@@ -116,7 +117,7 @@ __device__ __forceinline__ int item_flags(int item) { return item % AR_ITEMS; }
 // ------------------------------------------------------------------ loaders
 // One of two groups of four warps: K (kv = 0) or V.
 template <typename C, int D, int kv>
-__device__ void rows_load(const AttParams &p, Cursor c, char *smem, RowsCtl *ctl, unsigned *err, int lt)
+__device__ void rows_load(const AttParams &p, Cursor c, char *smem, RowsCtl *ctl, unsigned *err, int lt, const CUtensorMap *map)
 {
     using S = RowsShape<C, D>;
     constexpr int CH = D * static_cast<int>(sizeof(C)) / 16, RPI = 32 / CH;
@@ -178,17 +179,53 @@ __device__ void rows_load(const AttParams &p, Cursor c, char *smem, RowsCtl *ctl
             const int j = tile * AR_KEYS + 32 * w + lane;
             return tile < t1 && j < c.s.total ? __ldg(table + (j >> p.c.page_shift)) : -1;
         };
-        int pg = lookup(t0), next = lookup(t0 + 1);
+        // With a map, the first warp's lanes ask the copy engine for a box each: a page (or 128 slots of a large one)
+        // by 64 elements.  V's tiles with new tokens still go through the threads, who look at them.
+        const int box_slots = min(mask + 1, AR_KEYS), boxes = map ? AR_KEYS / box_slots * (D / 64) : 0;
+        auto box_lookup = [&](int tile) {
+            const int j = tile * AR_KEYS + lane / (D / 64) * box_slots;
+            return w == 0 && lane < boxes && tile < t1 && j < c.s.total ? __ldg(table + (j >> p.c.page_shift)) : -1;
+        };
+        int pg = -1, next = -1;
+        if (map) {
+            pg = box_lookup(t0);
+            next = box_lookup(t0 + 1);
+        } else {
+            pg = lookup(t0);
+            next = lookup(t0 + 1);
+        }
         for (int tile = t0; tile < t1; ++tile, ++n) {
             const int st = n % NST, j0 = tile * AR_KEYS;
+            if constexpr (!S::WIDEN) {
+                if (map && (!kv || j0 + AR_KEYS <= c.s.ctx)) {
+                    const int page = pg, slot = j0 + lane / (D / 64) * box_slots;
+                    pg = next;
+                    next = box_lookup(tile + 2);
+                    if (w == 0 && lane < boxes && slot < c.s.total && static_cast<unsigned>(page) >= static_cast<unsigned>(p.c.num_pages))
+                        *reinterpret_cast<volatile int *>(&ctl->bad[flags]) = 1;
+                    if (n >= NST && !(ok = rows_wait(ctl, &empty[st], (n / NST - 1) & 1, err))) break;
+                    if (lt == 0)
+                        mbar_arrive_expect_tx(&full[st], S::TILE);
+                    else
+                        mbar_arrive(&full[st]);
+                    if (w == 0) {
+                        __syncwarp();
+                        if (lane < boxes)
+                            tma_box(base + AT + st * S::TILE + (lane % (D / 64)) * (AR_KEYS * 128) + lane / (D / 64) * box_slots * 128,
+                                    map, (lane % (D / 64)) * 64, slot & mask, c.h, page, &full[st]);
+                    }
+                    continue;
+                }
+                if (map) pg = lookup(tile);  // a tile of V with new tokens: by rows
+            }
             const int row0 = min(max(0, c.s.ctx - j0), AR_KEYS), token0 = max(0, j0 - c.s.ctx);  // the first new token
             if (static_cast<unsigned>(pg) >= static_cast<unsigned>(p.c.num_pages)) {
                 if (j0 + 32 * w + lane < c.s.total) *reinterpret_cast<volatile int *>(&ctl->bad[flags]) = 1;
                 pg = -1;
             }
             const int64_t mine = pg < 0 ? -1 : pg * pool.page_stride + ((j0 + 32 * w + lane) & mask) * pool.slot_stride;
-            pg = next;
-            next = lookup(tile + 2);  // two tiles ahead: its latency is behind that of the rows
+            pg = map ? box_lookup(tile + 1) : next;
+            next = map ? box_lookup(tile + 2) : lookup(tile + 2);  // two tiles ahead: its latency is behind that of the rows
             uint32_t to;
             if (S::WIDEN) {  // the raw stages are each thread's own
                 if (n >= NST) {
@@ -239,6 +276,8 @@ __device__ void rows_load(const AttParams &p, Cursor c, char *smem, RowsCtl *ctl
         }
     }
     asm volatile("cp.async.wait_all;" ::: "memory");
+    if (map && !ok)  // the copy engine's, before the block may end
+        for (int t = max(0, n - NST); t < n; ++t) mbar_wait(&full[t % NST], (t / NST) & 1);
     if (S::WIDEN)  // the tiles still on their way
         for (int t = n >= NST ? n - NST : 0; ok && t < n; ++t) ok = widen(t);
 }
@@ -630,7 +669,8 @@ __device__ void rows_softmax(const AttParams &p, Cursor c, char *smem, RowsCtl *
 }
 
 template <typename T, typename C, int D, int COLS>
-__global__ void __launch_bounds__(AR_THREADS, 1) attention_rows_kernel(const AttParams p)
+__global__ void __launch_bounds__(AR_THREADS, 1)
+    attention_rows_kernel(const AttParams p, const __grid_constant__ CUtensorMap map_k, const __grid_constant__ CUtensorMap map_v, const int maps)
 {
     using S = RowsShape<C, D>;
     extern __shared__ char raw_smem[];
@@ -685,9 +725,9 @@ __global__ void __launch_bounds__(AR_THREADS, 1) attention_rows_kernel(const Att
     } else {
         asm volatile("setmaxnreg.dec.sync.aligned.u32 112;");
         if (warp < 12)
-            rows_load<C, D, 0>(p, c, smem, ctl, err, tid & 127);
+            rows_load<C, D, 0>(p, c, smem, ctl, err, tid & 127, maps ? &map_k : nullptr);
         else
-            rows_load<C, D, 1>(p, c, smem, ctl, err, tid & 127);
+            rows_load<C, D, 1>(p, c, smem, ctl, err, tid & 127, maps ? &map_v : nullptr);
     }
     tc_fence_before();
     __syncthreads();
@@ -695,7 +735,8 @@ __global__ void __launch_bounds__(AR_THREADS, 1) attention_rows_kernel(const Att
     if (warp == 4) tmem_free(ctl->tmem, 512);
 }
 
-template <typename T, typename C, int D, int COLS> static cudaError_t launch_cols(AttParams p, cudaStream_t st)
+template <typename T, typename C, int D, int COLS>
+static cudaError_t launch_cols(AttParams p, const KvLaunch &L, cudaStream_t st)
 {
     using S = RowsShape<C, D>;
     constexpr int SMEM = S::CTL_AT + static_cast<int>(sizeof(RowsCtl)) + 1024;
@@ -705,21 +746,23 @@ template <typename T, typename C, int D, int COLS> static cudaError_t launch_col
     if (e != cudaSuccess) return e;
     p.w.tile = AR_KEYS;
     p.w.row_tiles = (p.rows + COLS - 1) / COLS;
-    kernel<<<ATT_SMS, AR_THREADS, SMEM, st>>>(p);
+    CUtensorMap map_k{}, map_v{};
+    const bool maps = pool_map(&map_k, L, false) && pool_map(&map_v, L, true);
+    kernel<<<ATT_SMS, AR_THREADS, SMEM, st>>>(p, map_k, map_v, maps);
     e = cudaGetLastError();
     return e != cudaSuccess ? e : launch_join(p, std::is_same<T, __half>::value ? SPV_F16 : SPV_BF16, D, AR_ROWS, ATT_SMS, st);
 }
-template <typename T, typename C, int D> static cudaError_t launch_dim(const AttParams &p, cudaStream_t st)
+template <typename T, typename C, int D> static cudaError_t launch_dim(const AttParams &p, const KvLaunch &L, cudaStream_t st)
 {
     if constexpr (sizeof(C) == 2) {  // an e4m3 cache comes here with more than 32 rows
-        if (p.rows <= 32) return launch_cols<T, C, D, 32>(p, st);
+        if (p.rows <= 32) return launch_cols<T, C, D, 32>(p, L, st);
     }
-    if (p.rows <= 64) return launch_cols<T, C, D, 64>(p, st);
-    return launch_cols<T, C, D, 128>(p, st);
+    if (p.rows <= 64) return launch_cols<T, C, D, 64>(p, L, st);
+    return launch_cols<T, C, D, 128>(p, L, st);
 }
-template <typename T, typename C> static cudaError_t launch_types(const AttParams &p, int D, cudaStream_t st)
+template <typename T, typename C> static cudaError_t launch_types(const AttParams &p, const KvLaunch &L, cudaStream_t st)
 {
-    return D == 64 ? launch_dim<T, C, 64>(p, st) : launch_dim<T, C, 128>(p, st);
+    return L.cache.head_dim == 64 ? launch_dim<T, C, 64>(p, L, st) : launch_dim<T, C, 128>(p, L, st);
 }
 
 size_t attention_rows_part_floats(int head_dim)
@@ -727,12 +770,12 @@ size_t attention_rows_part_floats(int head_dim)
     return static_cast<size_t>(ATT_SMS) * 2 * AR_ROWS * (head_dim + 2);
 }
 
-cudaError_t launch_attention_rows(const AttParams &p, spv_dtype q, spv_dtype cache, int D, cudaStream_t st)
+cudaError_t launch_attention_rows(const AttParams &p, const KvLaunch &L, cudaStream_t st)
 {
-    const bool eight = cache == SPV_E4M3;
-    if (q == SPV_BF16)
-        return eight ? launch_types<__nv_bfloat16, __nv_fp8_e4m3>(p, D, st) : launch_types<__nv_bfloat16, __nv_bfloat16>(p, D, st);
-    return eight ? launch_types<__half, __nv_fp8_e4m3>(p, D, st) : launch_types<__half, __half>(p, D, st);
+    const bool eight = L.cache.dtype == SPV_E4M3;
+    if (L.dtype == SPV_BF16)
+        return eight ? launch_types<__nv_bfloat16, __nv_fp8_e4m3>(p, L, st) : launch_types<__nv_bfloat16, __nv_bfloat16>(p, L, st);
+    return eight ? launch_types<__half, __nv_fp8_e4m3>(p, L, st) : launch_types<__half, __half>(p, L, st);
 }
 
 }  // namespace spv
