@@ -418,6 +418,19 @@ __device__ void rows_prepare(const AttParams &p, Cursor c, char *smem, RowsCtl *
 }
 
 // ------------------------------------------------------------------ rows
+// 32 bytes to a 16-byte aligned address: at once where it allows.
+__device__ __forceinline__ void store32(void *at, const uint32_t (&y)[8])
+{
+    if ((reinterpret_cast<uintptr_t>(at) & 31) == 0) {
+        asm volatile("st.global.v8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"l"(at), "r"(y[0]), "r"(y[1]), "r"(y[2]), "r"(y[3]),
+                     "r"(y[4]), "r"(y[5]), "r"(y[6]), "r"(y[7])
+                     : "memory");
+    } else {
+        reinterpret_cast<uint4 *>(at)[0] = make_uint4(y[0], y[1], y[2], y[3]);
+        reinterpret_cast<uint4 *>(at)[1] = make_uint4(y[4], y[5], y[6], y[7]);
+    }
+}
+
 __device__ __forceinline__ void rows_sync() { asm volatile("bar.sync 1, 128;" ::: "memory"); }
 
 // COLS: keys of a tile that a thread takes, and rows of a copy.
@@ -640,18 +653,25 @@ __device__ void rows_softmax(const AttParams &p, Cursor c, char *smem, RowsCtl *
                     }
                 }
             }
+            // 32 bytes a store: a thread's row is its own, and half a sector at a time cost twice the transactions
             if (!whole) {
 #pragma unroll
-                for (int k = 0; k < 32; k += 4)
-                    *reinterpret_cast<float4 *>(part + 2 * AR_ROWS + r * D + d0 + k) = make_float4(x[k], x[k + 1], x[k + 2], x[k + 3]);
+                for (int k = 0; k < 32; k += 8) {
+                    uint32_t y[8];
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) y[e] = __float_as_uint(x[k + e]);
+                    store32(part + 2 * AR_ROWS + r * D + d0 + k, y);
+                }
             } else {
 #pragma unroll
                 for (int k = 0; k < 32; ++k) x[k] = fixed ? instead : x[k] * out_scale;
 #pragma unroll
-                for (int k = 0; k < 32; k += 8)
-                    *reinterpret_cast<uint4 *>(static_cast<T *>(p.out) + row_at * D + d0 + k) =
-                        make_uint4(pack_mma<T>(x[k], x[k + 1]), pack_mma<T>(x[k + 2], x[k + 3]), pack_mma<T>(x[k + 4], x[k + 5]),
-                                   pack_mma<T>(x[k + 6], x[k + 7]));
+                for (int k = 0; k < 32; k += 16) {
+                    uint32_t y[8];
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) y[e] = pack_mma<T>(x[k + 2 * e], x[k + 2 * e + 1]);
+                    store32(static_cast<T *>(p.out) + row_at * D + d0 + k, y);
+                }
             }
         }
         tc_fence_before();

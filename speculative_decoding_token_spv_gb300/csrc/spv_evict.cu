@@ -17,7 +17,7 @@ namespace spv {
 constexpr int EV_THREADS = 1024;
 constexpr int EV_MOVE_SLOTS = 256;     // slots that a block of the move looks at, one a thread
 constexpr int EV_MOVE_AHEAD = 8;       // 16-byte pieces of a thread on their way
-constexpr int EV_FEW_SLOTS = 16384;
+constexpr int EV_FEW_SLOTS = 16384, EV_FEW_THREADS = 512;  // two blocks an SM for up to 8,192 slots
 
 struct EvictParams {
     PagedView c;
@@ -44,8 +44,8 @@ __device__ __forceinline__ unsigned slot_key(const EvictParams &p, const float *
     return at < p.sinks || at > top - p.recent ? 0xffffffffu : mass_key(mass[j]);
 }
 
-// Exclusive prefix of `x` over the block; *all gets the sum.
-__device__ __forceinline__ int block_prefix(int x, int *sh, int *all)
+// Exclusive prefix of `x` over a block of WARPS warps; *all gets the sum.
+template <int WARPS> __device__ __forceinline__ int block_prefix(int x, int *sh, int *all)
 {
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     int upto = x;
@@ -57,18 +57,11 @@ __device__ __forceinline__ int block_prefix(int x, int *sh, int *all)
     __syncthreads();
     if (lane == 31) sh[warp] = upto;
     __syncthreads();
-    if (warp == 0) {
-        int s = sh[lane];
-#pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-            const int y = __shfl_up_sync(0xffffffffu, s, o);
-            if (lane >= o) s += y;
-        }
-        sh[lane] = s;
-    }
-    __syncthreads();
-    *all = sh[31];
-    return upto - x + (warp ? sh[warp - 1] : 0);
+    // every warp by itself: the sums of all, and of those before it
+    int s = lane < WARPS ? sh[lane] : 0;
+    *all = __reduce_add_sync(0xffffffffu, s);
+    s = __reduce_add_sync(0xffffffffu, lane < warp ? s : 0);
+    return upto - x + s;
 }
 
 __device__ __forceinline__ void dependents_go() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
@@ -101,7 +94,7 @@ __device__ __forceinline__ bool evict_begin(const EvictParams &p, EvictItem *it)
         if (p.row_status) {
             int any = bad;
             const int32_t *table = p.c.table + static_cast<int64_t>(b) * p.c.max_pages;
-            for (int g = tid; !bad && n > p.budget && g <= (n - 1) >> p.c.page_shift; g += EV_THREADS)
+            for (int g = tid; !bad && n > p.budget && g <= (n - 1) >> p.c.page_shift; g += static_cast<int>(blockDim.x))
                 any |= page_of(p.c, table, g << p.c.page_shift) < 0;
             any = __syncthreads_or(any);
             if (tid == 0) p.row_status[b] = any ? KV_STATUS_BAD : 0;
@@ -111,7 +104,7 @@ __device__ __forceinline__ bool evict_begin(const EvictParams &p, EvictItem *it)
     it->n = n;
     it->m = bad ? 0 : n < p.budget ? n : p.budget;
     if (!bad && n > p.budget) return true;
-    for (int i = tid; i < p.budget; i += EV_THREADS) {  // nothing moves
+    for (int i = tid; i < p.budget; i += static_cast<int>(blockDim.x)) {  // nothing moves
         it->src[i] = i < it->m ? i : -1;
         if (i < it->m) {
             it->mass_out[i] = it->mass[i];
@@ -127,13 +120,15 @@ __device__ __forceinline__ void evict_write(const EvictParams &p, const EvictIte
     if (it.pos_out && (s != i || p.pos_out != p.pos)) it.pos_out[i] = it.pos ? it.pos[s] : s;
 }
 
-// Slots in registers: slot t + 1024 i is thread t's i-th.
-template <int PER> __global__ void __launch_bounds__(EV_THREADS) evict_select_few(const EvictParams p)
+// Slots in registers: slot t + 512 i is thread t's i-th.
+template <int PER> __global__ void __launch_bounds__(EV_FEW_THREADS) evict_select_few(const EvictParams p)
 {
-    constexpr int WORDS = PER * 32;
-    __shared__ unsigned kept[WORDS], before[WORDS];          // kept bits; holes and movers (high half) before a word
+    constexpr int NT = EV_FEW_THREADS, WARPS = NT / 32, WORDS = PER * WARPS, WPT = (WORDS + NT - 1) / NT;
+    static_assert(WORDS % NT == 0 || WPT == 1, "words of a thread");
+    __shared__ unsigned kept[WORDS], before[WORDS];  // kept bits; equals, later holes before a word
     __shared__ unsigned short movers[WORDS * 16];            // kept slots at or above the budget, in order
-    __shared__ int sh[32], counts[3][4];
+    __shared__ int sh[32];
+    __shared__ uint2 counts[2][WARPS];  // each warp's, in turn: at least b, c (16 bits each); at least a
     dependents_go();
     EvictItem it;
     if (!evict_begin(p, &it)) return;
@@ -144,7 +139,7 @@ template <int PER> __global__ void __launch_bounds__(EV_THREADS) evict_select_fe
         int at[PER];
 #pragma unroll
         for (int i = 0; i < PER; ++i) {
-            const int j = tid + i * EV_THREADS;
+            const int j = tid + i * NT;
             w[i] = j < n ? it.mass[j] : 0.0f;
             at[i] = j < n ? (it.pos ? it.pos[j] : j) : -1;
         }
@@ -153,12 +148,11 @@ template <int PER> __global__ void __launch_bounds__(EV_THREADS) evict_select_fe
         for (int i = 0; i < PER; ++i) top = max(top, at[i]);
         top = __reduce_max_sync(0xffffffffu, top);
         if (lane == 0) sh[warp] = top;
-        if (tid < 12) (&counts[0][0])[tid] = 0;
         __syncthreads();
-        top = __reduce_max_sync(0xffffffffu, sh[lane]);
+        top = __reduce_max_sync(0xffffffffu, sh[lane % WARPS]);
 #pragma unroll
         for (int i = 0; i < PER; ++i) {
-            const int j = tid + i * EV_THREADS;
+            const int j = tid + i * NT;
             const bool always = at[i] < p.sinks || static_cast<long long>(at[i]) > static_cast<long long>(top) - p.recent;
             key[i] = j >= n ? 0u : always ? 0xffffffffu : mass_key(w[i]);
         }
@@ -167,86 +161,98 @@ template <int PER> __global__ void __launch_bounds__(EV_THREADS) evict_select_fe
     unsigned least = 0;
     bool exact = false;
     int turn = 0;
-    auto count3 = [&](unsigned a, unsigned b, unsigned c) {  // keys >= a, b, c into counts[turn]
-        int x = 0, y = 0, z = 0;
+    auto count3 = [&](unsigned a, unsigned b, unsigned c, int *na, int *nb, int *nc) {  // keys >= a, b, c
+        unsigned x = 0, yz = 0;
 #pragma unroll
         for (int i = 0; i < PER; ++i) {
             x += key[i] >= a;
-            y += key[i] >= b;
-            z += key[i] >= c;
+            yz += (key[i] >= b ? 1u : 0u) + (key[i] >= c ? 0x10000u : 0u);
         }
         x = __reduce_add_sync(0xffffffffu, x);
-        y = __reduce_add_sync(0xffffffffu, y);
-        z = __reduce_add_sync(0xffffffffu, z);
-        if (lane == 0) {
-            atomicAdd(&counts[turn][0], x);
-            atomicAdd(&counts[turn][1], y);
-            atomicAdd(&counts[turn][2], z);
-        }
-        if (tid < 3) counts[turn == 2 ? 0 : turn + 1][tid] = 0;  // the next round's: read last a round ago
+        yz = __reduce_add_sync(0xffffffffu, yz);
+        if (lane == 0) counts[turn][warp] = make_uint2(yz, x);
         __syncthreads();
+        const uint2 w = lane < WARPS ? counts[turn][lane] : make_uint2(0, 0);
+        x = __reduce_add_sync(0xffffffffu, w.y);
+        yz = __reduce_add_sync(0xffffffffu, w.x);
+        *na = static_cast<int>(x);
+        *nb = static_cast<int>(yz & 0xffffu);
+        *nc = static_cast<int>(yz >> 16);
+        turn ^= 1;  // who writes this turn's places again has passed the other's barrier
     };
     for (int bit = 30; bit >= 0 && !exact; bit -= 2) {
         const unsigned a = least | 1u << bit, b = least | 2u << bit, c = least | 3u << bit;
-        count3(a, b, c);
-        const int x = counts[turn][0], y = counts[turn][1], z = counts[turn][2];
-        turn = turn == 2 ? 0 : turn + 1;
+        int x, y, z;
+        count3(a, b, c, &x, &y, &z);
         const int got = z >= m ? z : y >= m ? y : x >= m ? x : -1;
         least = z >= m ? c : y >= m ? b : x >= m ? a : least;
         exact = got == m;
     }
     int want = 0;  // of the keys equal to `least`, from the lowest slot on
     if (!exact) {
-        if (least != 0xffffffffu) {
-            count3(least + 1u, 0xffffffffu, 0xffffffffu);
-            want = m - counts[turn][0];
-        } else {
-            want = m;
-        }
+        int x = 0, y, z;
+        if (least != 0xffffffffu) count3(least + 1u, 0xffffffffu, 0xffffffffu, &x, &y, &z);
+        want = m - x;
     }
 #pragma unroll
     for (int i = 0; i < PER; ++i) {
-        const int j = tid + i * EV_THREADS;
+        const int j = tid + i * NT;
         const unsigned gt = __ballot_sync(0xffffffffu, j < n && (exact ? key[i] >= least : key[i] > least));
         const unsigned eq = __ballot_sync(0xffffffffu, j < n && !exact && key[i] == least);
         if (lane == 0) {
-            kept[i * 32 + warp] = gt;
-            before[i * 32 + warp] = eq;
+            kept[i * WARPS + warp] = gt;
+            before[i * WARPS + warp] = eq;
         }
     }
     __syncthreads();
     int all;
     if (!exact) {
-        unsigned eq = tid < WORDS ? before[tid] : 0;
-        const int ahead = block_prefix(__popc(eq), sh, &all);
-        if (tid < WORDS) {
-            unsigned k = kept[tid];
-            for (int left = want - ahead; eq && left > 0; --left) {
-                k |= eq & -eq;
-                eq &= eq - 1;
-            }
-            kept[tid] = k;
+        const int w0 = tid * WPT;  // this thread's words
+        int mine = 0;
+#pragma unroll
+        for (int i = 0; i < WPT; ++i) mine += w0 + i < WORDS ? __popc(before[w0 + i]) : 0;
+        int left = want - block_prefix<WARPS>(mine, sh, &all);
+#pragma unroll
+        for (int i = 0; i < WPT; ++i) {
+            if (w0 + i >= WORDS) break;
+            unsigned eq = before[w0 + i], k = kept[w0 + i];
+            for (; eq; eq &= eq - 1)
+                if (left-- > 0) k |= eq & -eq;
+            kept[w0 + i] = k;
         }
         __syncthreads();
     }
     const int wm = m >> 5;
     const unsigned low = (1u << (m & 31)) - 1u;
     {
-        const unsigned k = tid < WORDS ? kept[tid] : 0;
-        const unsigned below = tid < wm ? 0xffffffffu : tid == wm ? low : 0u;  // slots below the budget
-        const unsigned hole = tid < WORDS ? ~k & below : 0u, mover = k & ~below;
-        const int packed = __popc(hole) | __popc(mover) << 16;
-        const int ahead = block_prefix(packed, sh, &all);
-        if (tid < WORDS) before[tid] = ahead;
-        int at = ahead >> 16;
-        for (unsigned left = mover; left; left &= left - 1) movers[at++] = static_cast<unsigned short>(32 * tid + __ffs(left) - 1);
+        const int w0 = tid * WPT;
+        unsigned hole[WPT], mover[WPT];
+        int packed = 0;
+#pragma unroll
+        for (int i = 0; i < WPT; ++i) {
+            const int w = w0 + i;
+            const unsigned k = w < WORDS ? kept[w] : 0;
+            const unsigned below = w < wm ? 0xffffffffu : w == wm ? low : 0u;  // slots below the budget
+            hole[i] = w < WORDS ? ~k & below : 0u;
+            mover[i] = k & ~below;
+            packed += __popc(hole[i]) | __popc(mover[i]) << 16;
+        }
+        int ahead = block_prefix<WARPS>(packed, sh, &all);
+#pragma unroll
+        for (int i = 0; i < WPT; ++i) {
+            const int w = w0 + i;
+            if (w < WORDS) before[w] = ahead & 0xffff;
+            int at = ahead >> 16;
+            for (unsigned left = mover[i]; left; left &= left - 1) movers[at++] = static_cast<unsigned short>(32 * w + __ffs(left) - 1);
+            ahead += __popc(hole[i]) | __popc(mover[i]) << 16;
+        }
     }
     __syncthreads();
-    for (int i = tid; i < p.budget; i += EV_THREADS) {
+    for (int i = tid; i < p.budget; i += NT) {
         int s = i;
         if (i < m) {
             const unsigned k = kept[i >> 5], bit = 1u << (i & 31);
-            if (!(k & bit)) s = movers[(before[i >> 5] & 0xffffu) + __popc(~k & (bit - 1u))];
+            if (!(k & bit)) s = movers[before[i >> 5] + __popc(~k & (bit - 1u))];
             evict_write(p, it, i, s);
         } else {
             it.src[i] = -1;
@@ -288,7 +294,7 @@ __global__ void __launch_bounds__(EV_THREADS) evict_select_many(const EvictParam
         __syncthreads();
         const int x = tid < 256 ? static_cast<int>(hist[255 - tid]) : 0;
         int all;
-        const int before = block_prefix(x, sh, &all);  // of larger digits
+        const int before = block_prefix<EV_THREADS / 32>(x, sh, &all);  // of larger digits
         if (tid < 256 && before < want && want <= before + x) {
             found[0] = 255 - tid;
             found[1] = want - before;
@@ -317,7 +323,7 @@ __global__ void __launch_bounds__(EV_THREADS) evict_select_many(const EvictParam
         const int w = w0 + tid;
         unsigned eq = w < nw ? count[w] : 0;
         int all;
-        const int before = run + block_prefix(__popc(eq), sh, &all);
+        const int before = run + block_prefix<EV_THREADS / 32>(__popc(eq), sh, &all);
         if (w < nw) {
             for (int left = want - before; eq && left > 0; --left) {
                 kept[w] |= eq & -eq;
@@ -337,9 +343,9 @@ __global__ void __launch_bounds__(EV_THREADS) evict_select_many(const EvictParam
         const int hole = w >= nw || w > wm ? 0 : w < wm ? __popc(~k) : __popc(~k & low);
         const int mover = w >= nw || w < wm ? 0 : w > wm ? __popc(k) : __popc(k & ~low);
         int all;
-        const int hb = holes + block_prefix(hole, sh, &all);
+        const int hb = holes + block_prefix<EV_THREADS / 32>(hole, sh, &all);
         holes += all;
-        const int mb = movers + block_prefix(mover, sh, &all);
+        const int mb = movers + block_prefix<EV_THREADS / 32>(mover, sh, &all);
         movers += all;
         if (w < nw) count[w] = w <= wm ? hb : mb;
     }
@@ -460,11 +466,11 @@ cudaError_t launch_evict(const EvictLaunch &L, cudaStream_t st)
     const int slots = p.words * 32;  // that a sequence can have
     cudaError_t e;
     if (slots <= 4096) {
-        evict_select_few<4><<<items, EV_THREADS, 0, st>>>(p);
+        evict_select_few<8><<<items, EV_FEW_THREADS, 0, st>>>(p);
     } else if (slots <= 8192) {
-        evict_select_few<8><<<items, EV_THREADS, 0, st>>>(p);
+        evict_select_few<16><<<items, EV_FEW_THREADS, 0, st>>>(p);
     } else if (slots <= EV_FEW_SLOTS) {
-        evict_select_few<16><<<items, EV_THREADS, 0, st>>>(p);
+        evict_select_few<32><<<items, EV_FEW_THREADS, 0, st>>>(p);
     } else {
         const int smem = p.words * 2 * static_cast<int>(sizeof(unsigned));
         if (smem > 40 * 1024) {
