@@ -23,6 +23,7 @@ constexpr int ATT_WARPS = 4;
 constexpr int ATT_THREADS = 32 * ATT_WARPS;
 constexpr int ATT_KEYS = 16 * ATT_WARPS;  // keys of a tile: a slice for each warp
 constexpr int ATT_MAX_ROWS = 32;
+constexpr float ATT_GROWTH = 8.0f;  // growth of a maximum (powers of two) that the sums wait for
 
 // Workspace: header, the blocks' split items, their pieces.
 constexpr size_t ATT_PARTS_AT = WS_HEADER + split_bytes(ATT_MAX_BLOCKS);
@@ -97,6 +98,12 @@ __global__ void __launch_bounds__(ATT_THREADS, AttShape<C, D, MT>::BLOCKS_PER_SM
 #pragma unroll
         for (int i = 0; i < NST - 1; ++i) issue(t0 + i);
 
+        // Scores are q.k times a factor, which is kept positive (its sign goes into q; a scale of 0 makes q 0), so that
+        // the largest product is the largest score.  (The product is rounded as m was, not fused with the difference:
+        // of scores beyond 2^27 the largest would else miss m by more than p can hold.)
+        const float signed_unit = p.scale_log2 * (p.c.k_scale ? __ldg(p.c.k_scale + c.h) : 1.0f);
+        const float turn = signed_unit < 0.0f ? -1.0f : signed_unit == 0.0f ? 0.0f : 1.0f;
+        const float unit = signed_unit == 0.0f ? 1.0f : fabsf(signed_unit);
         // q of the tile's rows; for an e4m3 cache each row by a power of two into f16's range
         for (int i = tid; i < R * (D / 8); i += ATT_THREADS) {
             const int r = i / (D / 8), d = (i - r * (D / 8)) * 8, t = (row0 + r) / p.group, g = (row0 + r) - t * p.group;
@@ -109,7 +116,7 @@ __global__ void __launch_bounds__(ATT_THREADS, AttShape<C, D, MT>::BLOCKS_PER_SM
                 const uint4 raw = *reinterpret_cast<const uint4 *>(q);
                 const T *y = reinterpret_cast<const T *>(&raw);
 #pragma unroll
-                for (int e = 0; e < 8; ++e) x[e] = Num<T>::up(y[e]);
+                for (int e = 0; e < 8; ++e) x[e] = Num<T>::up(y[e]) * turn;
             }
             if (sizeof(C) == 1) {
                 float top = 0.0f;
@@ -149,7 +156,6 @@ __global__ void __launch_bounds__(ATT_THREADS, AttShape<C, D, MT>::BLOCKS_PER_SM
                 get_q<D>(a, qs32, mt, ks, lane);
             }
         };
-        const float unit = p.scale_log2 * (p.c.k_scale ? __ldg(p.c.k_scale + c.h) : 1.0f);
         float factor[MT][2], m[MT][2], l[MT][2], o[MT][D / 8][4];
 #pragma unroll
         for (int mt = 0; mt < MT; ++mt) {
@@ -178,10 +184,6 @@ __global__ void __launch_bounds__(ATT_THREADS, AttShape<C, D, MT>::BLOCKS_PER_SM
             uint32_t pf[MT][4];
 #pragma unroll
             for (int mt = 0; mt < MT; ++mt) {
-#pragma unroll
-                for (int i = 0; i < 2; ++i)
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) s[mt][i][e] *= factor[mt][e >> 1];
                 if (tail) {
 #pragma unroll
                     for (int e = 0; e < 4; ++e) {
@@ -193,6 +195,8 @@ __global__ void __launch_bounds__(ATT_THREADS, AttShape<C, D, MT>::BLOCKS_PER_SM
                         }
                     }
                 }
+                // m follows the maximum only where it has grown by more than 2^8 (or begins): p stays below 2^8, the 32-bit
+                // sums lose nothing, and o is seldom rescaled -- with every growth it was in nearly every slice
                 float top[2];
                 bool moved = false;
 #pragma unroll
@@ -200,14 +204,15 @@ __global__ void __launch_bounds__(ATT_THREADS, AttShape<C, D, MT>::BLOCKS_PER_SM
                     float x = fmaxf(fmaxf(s[mt][0][2 * i], s[mt][0][2 * i + 1]), fmaxf(s[mt][1][2 * i], s[mt][1][2 * i + 1]));
                     x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 1));
                     x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 2));
-                    top[i] = fmaxf(m[mt][i], x);
-                    moved |= top[i] > m[mt][i];
+                    top[i] = x * factor[mt][i];
+                    moved |= top[i] > m[mt][i] + ATT_GROWTH;  // m minus infinity: any score
                 }
                 if (__any_sync(0xffffffffu, moved)) {
 #pragma unroll
                     for (int i = 0; i < 2; ++i) {
-                        const float a = top[i] == -CUDART_INF_F ? 0.0f : fast_exp2(m[mt][i] - top[i]);
-                        m[mt][i] = top[i];
+                        const float grown = fmaxf(m[mt][i], top[i]);
+                        const float a = grown == -CUDART_INF_F ? 0.0f : fast_exp2(m[mt][i] - grown);
+                        m[mt][i] = grown;
                         l[mt][i] *= a;
 #pragma unroll
                         for (int k = 0; k < D / 8; ++k) {
@@ -218,11 +223,11 @@ __global__ void __launch_bounds__(ATT_THREADS, AttShape<C, D, MT>::BLOCKS_PER_SM
                 }
 #pragma unroll
                 for (int i = 0; i < 2; ++i) {
-                    const float base = m[mt][i] == -CUDART_INF_F ? 0.0f : m[mt][i];
+                    const float base = m[mt][i] == -CUDART_INF_F ? 0.0f : m[mt][i], f = factor[mt][i];
 #pragma unroll
                     for (int k = 0; k < 2; ++k)
 #pragma unroll
-                        for (int e = 2 * i; e < 2 * i + 2; ++e) s[mt][k][e] = fast_exp2(s[mt][k][e] - base);
+                        for (int e = 2 * i; e < 2 * i + 2; ++e) s[mt][k][e] = fast_exp2(__fmul_rn(s[mt][k][e], f) - base);
                     l[mt][i] += (s[mt][0][2 * i] + s[mt][0][2 * i + 1]) + (s[mt][1][2 * i] + s[mt][1][2 * i + 1]);
                 }
                 // rounded to the cache's 16-bit type for the product (half a step of it each); l keeps 32 bits

@@ -486,7 +486,7 @@ __device__ void rows_softmax(const AttParams &p, Cursor c, char *smem, RowsCtl *
                         uint32_t y[32];
                         tc_ld32(y, tm_s + (n & 1) * AR_KEYS + i);
 #pragma unroll
-                        for (int k = 0; k < 32; ++k) x[i + k] = __uint_as_float(y[k]) * factor;
+                        for (int k = 0; k < 32; ++k) x[i + k] = __fmul_rn(__uint_as_float(y[k]), factor);  // as m is: not fused with the difference
                     }
                     const int j0 = tile * AR_KEYS + copy * COLS;
                     if (j0 + COLS > c.s.ctx) {

@@ -174,9 +174,10 @@ def test_seen_nan_stays(spv):
     assert torch.isfinite(got["out"][0, :, G:]).all() and torch.isfinite(got["out"][1]).all()
 
 
-def test_scores_of_minus_infinity(spv):
+@pytest.mark.parametrize("T", [1, 12])
+def test_scores_of_minus_infinity(spv, T):
     """Every score minus infinity: a row without a sum; the lowest finite value of the type: an ordinary score."""
-    a = Layer(spv, 6, [40, 40], None, 1, 2, 1, 64, 16)
+    a = Layer(spv, 6, [40, 40], None, T, 2, 1, 64, 16)
     a.q = torch.ones_like(a.q)
     a.k[a.table[0].long()] = -math.inf
     a.k[a.table[1].long()] = torch.finfo(torch.bfloat16).min
@@ -188,9 +189,10 @@ def test_scores_of_minus_infinity(spv):
     a.q = torch.zeros_like(a.q)
     a.q[..., 0] = 2.0 ** -60
     got = a.attend()
-    v = torch.stack([ref.rows(a.v, a.table[b], 41).mean(0) for b in range(2)])[:, None]
     assert torch.isnan(got["out"][0]).all()  # 0 * -inf
-    assert (got["out"][1].cpu().double() - v[1]).abs().max() <= 2.0 ** -8 * (v[1].abs().max() + 1)
+    for t in range(T):  # equal scores, however large: the mean
+        v = ref.rows(a.v, a.table[1], 41 + t).mean(0)
+        assert (got["out"][1, t].cpu().double() - v).abs().max() <= 2.0 ** -8 * (v.abs().max() + 1)
 
 
 def test_bad_parents_empty_rows(spv):
@@ -630,3 +632,12 @@ def test_rope_bad_sequences(spv):
         assert torch.equal(cache.k[table[b].long().cuda()].cpu(), k[table[b].long()])
     assert torch.equal(cache.k[table[3, 1].long()].cpu(), k[table[3, 1].long()])
     assert not torch.equal(cache.k[table[3, 0].long()].cpu(), k[table[3, 0].long()])
+
+
+@pytest.mark.parametrize("scale", [0.0, -0.25, 1.5])
+@pytest.mark.parametrize("T, kv", [(2, "bf16"), (2, "e4m3"), (12, "bf16"), (12, "e4m3")])
+def test_attention_scale(spv, scale, T, kv):
+    """A scale of zero (every visible key alike), a negative one and a large one."""
+    a = Layer(spv, 16, [300, 45], None, T, 8, 2, 64, 16, dtype="bf16", kv=kv)
+    a.scale = scale
+    a.check(a.attend(scale=scale))
