@@ -66,6 +66,7 @@ __global__ void __launch_bounds__(ATT_THREADS, AttShape<C, D, MT>::BLOCKS_PER_SM
     char *qs = smem;
     float *merge = reinterpret_cast<float *>(smem + S::Q);
     const uint32_t qs32 = smem_u32(qs), ring = smem_u32(smem + S::Q) + warp * (NST * 2 * S::SLICE);
+    chain_begin();
     if (tid < 32) {
         const Cursor c = find_range(p.w, p.c, blockIdx.x, gridDim.x, tid);
         if (tid == 0) cur0 = c;
@@ -73,7 +74,6 @@ __global__ void __launch_bounds__(ATT_THREADS, AttShape<C, D, MT>::BLOCKS_PER_SM
     __syncthreads();
     Cursor c = cur0;
     const long long begin = c.at;
-    dependents_launch();
     if (tid < 2) p.split[blockIdx.x * 2 + tid].n = 0;
     for (; c.at < c.end; next_item(c, p.w, p.c)) {
         const int row0 = c.row_tile * R, live = min(R, p.rows - row0);
@@ -357,8 +357,7 @@ template <typename T, typename C, int D, int MT> static cudaError_t launch_rows(
     cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, S::SMEM);
     if (e != cudaSuccess) return e;
     constexpr int BLOCKS = ATT_SMS * S::BLOCKS_PER_SM;
-    kernel<<<BLOCKS, ATT_THREADS, S::SMEM, st>>>(p);
-    e = cudaGetLastError();
+    e = launch_chained(kernel, dim3(BLOCKS), ATT_THREADS, S::SMEM, st, p);
     return e != cudaSuccess ? e : launch_join(p, std::is_same<T, __half>::value ? SPV_F16 : SPV_BF16, D, S::R, BLOCKS, st);
 }
 template <typename T, typename C, int D> static cudaError_t launch_dim(AttParams &p, cudaStream_t st)

@@ -103,11 +103,6 @@ cudaError_t launch_join(const AttParams &p, spv_dtype q, int D, int R, int block
 // Room for the entries of `blocks` blocks.
 constexpr size_t split_bytes(int blocks) { return (static_cast<size_t>(blocks) * 2 * sizeof(SplitItem) + 255) / 256 * 256; }
 
-// Lets a dependent launch start; a kernel's last use of what its predecessor
-// wrote lies behind dependents_wait.
-__device__ __forceinline__ void dependents_launch() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
-__device__ __forceinline__ void dependents_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
-
 cudaError_t launch_attention_rows(const AttParams &p, const KvLaunch &L, cudaStream_t st);
 size_t attention_rows_part_floats(int head_dim);  // of all blocks' pieces
 

@@ -25,7 +25,7 @@ template <typename T, int D> __global__ void __launch_bounds__(32 * JOIN_WARPS) 
     __shared__ float ms[JOIN_WARPS], ls[JOIN_WARPS];
     __shared__ float xs[JOIN_WARPS][D];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    dependents_wait();
+    chain_begin();
     const SplitItem s = p.split[blockIdx.x * 2 + blockIdx.y];
     if (s.n == 0) return;
     const int first = blockIdx.x - s.b0, mine = (s.rows.live - first + s.n - 1) / s.n;  // rows first, first + n, ...
@@ -153,16 +153,7 @@ template <typename T, int D> __global__ void __launch_bounds__(32 * JOIN_WARPS) 
 
 template <typename T, int D> static cudaError_t launch(const AttParams &p, const JoinShape &js, int blocks, cudaStream_t st)
 {
-    cudaLaunchAttribute attr{};
-    attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr.val.programmaticStreamSerializationAllowed = 1;
-    cudaLaunchConfig_t cfg{};
-    cfg.gridDim = dim3(blocks, 2);
-    cfg.blockDim = dim3(32 * JOIN_WARPS);
-    cfg.stream = st;
-    cfg.attrs = &attr;
-    cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, join_kernel<T, D>, p, js);
+    return launch_chained(join_kernel<T, D>, dim3(blocks, 2), 32 * JOIN_WARPS, 0, st, p, js);
 }
 
 cudaError_t launch_join(const AttParams &p, spv_dtype q, int D, int R, int blocks, cudaStream_t st)

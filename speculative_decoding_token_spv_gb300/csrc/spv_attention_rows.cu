@@ -698,10 +698,6 @@ __global__ void __launch_bounds__(AR_THREADS, 1)
     RowsCtl *ctl = reinterpret_cast<RowsCtl *>(smem + S::CTL_AT);
     const int tid = threadIdx.x, warp = tid >> 5;
     unsigned *err = p.error;
-    const Cursor c = find_range(p.w, p.c, blockIdx.x, gridDim.x, tid & 31);
-    dependents_launch();
-    if (tid < 2) p.split[blockIdx.x * 2 + tid].n = 0;
-    if (c.at == c.end) return;  // the whole block
     if (tid == 0) {
         for (int i = 0; i < 5; ++i) {
             mbar_init(&ctl->k_full[i], 128);
@@ -724,9 +720,16 @@ __global__ void __launch_bounds__(AR_THREADS, 1)
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
     if (warp == 4) tmem_alloc(&ctl->tmem, 512);
+    chain_begin();
+    const Cursor c = find_range(p.w, p.c, blockIdx.x, gridDim.x, tid & 31);
+    if (tid < 2) p.split[blockIdx.x * 2 + tid].n = 0;
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
+    if (c.at == c.end) {  // the whole block
+        if (warp == 4) tmem_free(ctl->tmem, 512);
+        return;
+    }
     // registers: launched with 128 a thread, 4 x 128 = 208 + 80 + 2 x 112
     if (warp < 4) {
         asm volatile("setmaxnreg.inc.sync.aligned.u32 208;");
@@ -768,8 +771,7 @@ static cudaError_t launch_cols(AttParams p, const KvLaunch &L, cudaStream_t st)
     p.w.row_tiles = (p.rows + COLS - 1) / COLS;
     CUtensorMap map_k{}, map_v{};
     const bool maps = pool_map(&map_k, L, false) && pool_map(&map_v, L, true);
-    kernel<<<ATT_SMS, AR_THREADS, SMEM, st>>>(p, map_k, map_v, maps);
-    e = cudaGetLastError();
+    e = launch_chained(kernel, dim3(ATT_SMS), AR_THREADS, SMEM, st, p, map_k, map_v, static_cast<int>(maps));
     return e != cudaSuccess ? e : launch_join(p, std::is_same<T, __half>::value ? SPV_F16 : SPV_BF16, D, AR_ROWS, ATT_SMS, st);
 }
 template <typename T, typename C, int D> static cudaError_t launch_dim(const AttParams &p, const KvLaunch &L, cudaStream_t st)

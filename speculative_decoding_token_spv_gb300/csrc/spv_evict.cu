@@ -64,8 +64,6 @@ template <int WARPS> __device__ __forceinline__ int block_prefix(int x, int *sh,
     return upto - x + s;
 }
 
-__device__ __forceinline__ void dependents_go() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
-
 // What both selections begin with, for block (h, b): the length, whether it is
 // bad, and the outputs that need no selection.  False: the item is done.
 struct EvictItem {
@@ -129,7 +127,7 @@ template <int PER> __global__ void __launch_bounds__(EV_FEW_THREADS) evict_selec
     __shared__ unsigned short movers[WORDS * 16];            // kept slots at or above the budget, in order
     __shared__ int sh[32];
     __shared__ uint2 counts[2][WARPS];  // each warp's, in turn: at least b, c (16 bits each); at least a
-    dependents_go();
+    chain_begin();
     EvictItem it;
     if (!evict_begin(p, &it)) return;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, n = it.n, m = it.m;
@@ -267,7 +265,7 @@ __global__ void __launch_bounds__(EV_THREADS) evict_select_many(const EvictParam
     __shared__ int sh[32];
     __shared__ int tops[32];
     __shared__ unsigned found[2];
-    dependents_go();
+    chain_begin();
     EvictItem it;
     if (!evict_begin(p, &it)) return;
     const int tid = threadIdx.x, lane = tid & 31, n = it.n, m = it.m;
@@ -389,7 +387,7 @@ __global__ void __launch_bounds__(EV_MOVE_SLOTS) evict_move_kernel(const EvictPa
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int h = blockIdx.y % p.c.kv_heads, b = blockIdx.y / p.c.kv_heads, i = blockIdx.x * EV_MOVE_SLOTS + tid;
     const int32_t *table = p.c.table + static_cast<int64_t>(b) * p.c.max_pages;
-    asm volatile("griddepcontrol.wait;" ::: "memory");
+    chain_begin();
     // the block's moves, in a row
     const int s = i < p.budget ? p.slot_src[static_cast<int64_t>(blockIdx.y) * p.budget + i] : -1;
     bool moves = s >= 0 && s != i;
@@ -466,31 +464,22 @@ cudaError_t launch_evict(const EvictLaunch &L, cudaStream_t st)
     const int slots = p.words * 32;  // that a sequence can have
     cudaError_t e;
     if (slots <= 4096) {
-        evict_select_few<8><<<items, EV_FEW_THREADS, 0, st>>>(p);
+        e = launch_chained(evict_select_few<8>, items, EV_FEW_THREADS, 0, st, p);
     } else if (slots <= 8192) {
-        evict_select_few<16><<<items, EV_FEW_THREADS, 0, st>>>(p);
+        e = launch_chained(evict_select_few<16>, items, EV_FEW_THREADS, 0, st, p);
     } else if (slots <= EV_FEW_SLOTS) {
-        evict_select_few<32><<<items, EV_FEW_THREADS, 0, st>>>(p);
+        e = launch_chained(evict_select_few<32>, items, EV_FEW_THREADS, 0, st, p);
     } else {
         const int smem = p.words * 2 * static_cast<int>(sizeof(unsigned));
         if (smem > 40 * 1024) {
             e = cudaFuncSetAttribute(evict_select_many, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
             if (e != cudaSuccess) return e;
         }
-        evict_select_many<<<items, EV_THREADS, smem, st>>>(p);
+        e = launch_chained(evict_select_many, items, EV_THREADS, smem, st, p);
     }
-    e = cudaGetLastError();
     if (e != cudaSuccess) return e;
-    cudaLaunchAttribute attr{};
-    attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr.val.programmaticStreamSerializationAllowed = 1;
-    cudaLaunchConfig_t cfg{};
-    cfg.gridDim = dim3((L.budget + EV_MOVE_SLOTS - 1) / EV_MOVE_SLOTS, k.B * k.cache.kv_heads);
-    cfg.blockDim = dim3(EV_MOVE_SLOTS);
-    cfg.stream = st;
-    cfg.attrs = &attr;
-    cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, evict_move_kernel, p);
+    const dim3 moves((L.budget + EV_MOVE_SLOTS - 1) / EV_MOVE_SLOTS, k.B * k.cache.kv_heads);
+    return launch_chained(evict_move_kernel, moves, EV_MOVE_SLOTS, 0, st, p);
 }
 
 }  // namespace spv

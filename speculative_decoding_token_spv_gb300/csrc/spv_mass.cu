@@ -433,8 +433,6 @@ template <typename T, typename C, int D> __global__ void __launch_bounds__(MASS_
     char *smem = raw_smem + ((1024u - (smem_u32(raw_smem) & 1023u)) & 1023u);
     Ctl *ctl = reinterpret_cast<Ctl *>(smem + S::CTL_AT);
     const int tid = threadIdx.x, warp = tid >> 5;
-    const Cursor c = find_range(p.w, p.c, blockIdx.x, gridDim.x, tid & 31);
-    if (c.at == c.end) return;  // the whole block
     if (tid == 0) {
         for (int i = 0; i < 8; ++i) {
             mbar_init(&ctl->k_full[i], 128);
@@ -453,9 +451,15 @@ template <typename T, typename C, int D> __global__ void __launch_bounds__(MASS_
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
     if (warp == 4) tmem_alloc(&ctl->tmem, 512);
+    chain_begin();
+    const Cursor c = find_range(p.w, p.c, blockIdx.x, gridDim.x, tid & 31);
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
+    if (c.at == c.end) {  // the whole block
+        if (warp == 4) tmem_free(ctl->tmem, 512);
+        return;
+    }
     if (warp < 4) {
         mass_sum<S>(p, c, ctl, tid);
     } else if (warp == 4) {
@@ -486,8 +490,7 @@ template <typename T, typename C, int D> static cudaError_t launch_dim(const Mas
     static_assert(SMEM <= 232448, "shared memory of a block");
     const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, SMEM);
     if (e != cudaSuccess) return e;
-    kernel<<<MASS_SMS, MASS_THREADS, SMEM, st>>>(p);
-    return cudaGetLastError();
+    return launch_chained(kernel, dim3(MASS_SMS), MASS_THREADS, SMEM, st, p);
 }
 template <typename T, typename C> static cudaError_t launch_types(const MassParams &p, int D, cudaStream_t st)
 {

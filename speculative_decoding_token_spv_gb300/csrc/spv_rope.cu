@@ -157,6 +157,7 @@ __global__ void __launch_bounds__(ROPE_THREADS) rope_kernel(const RopeParams p)
             if (h0 + i * step < heads) rope_read(to[i], from(tk, h0 + i * step), at);
         if (v_h0 < p.c.kv_heads) rope_read(to_v, v0 + tk * p.stride[5] + v_h0 * p.D, v_place);
     };
+    chain_begin();
     fetch(0, x, v);
     const SeqLens s = seq_lens(p.ctx_lens, p.new_lens, b, p.T, p.c);
     const int32_t *table = p.c.table + static_cast<int64_t>(b) * p.c.max_pages;
@@ -270,10 +271,9 @@ template <int MODE, typename T, typename C> static cudaError_t launch_mode(const
     // 128, f16: measured as below); fewer tokens are spread over as many SMs as there are
     const int smem = p.half * static_cast<int>(sizeof(float2));
     if (static_cast<int64_t>(p.B) * p.T >= 8 * 152 * ROPE_TOKENS)
-        rope_kernel<MODE, ROPE_TOKENS, T, C><<<p.B * ((p.T + ROPE_TOKENS - 1) / ROPE_TOKENS), ROPE_THREADS, ROPE_TOKENS * smem, st>>>(p);
-    else
-        rope_kernel<MODE, 1, T, C><<<p.B * p.T, ROPE_THREADS, smem, st>>>(p);
-    return cudaGetLastError();
+        return launch_chained(rope_kernel<MODE, ROPE_TOKENS, T, C>, dim3(p.B * ((p.T + ROPE_TOKENS - 1) / ROPE_TOKENS)),
+                              ROPE_THREADS, ROPE_TOKENS * smem, st, p);
+    return launch_chained(rope_kernel<MODE, 1, T, C>, dim3(p.B * p.T), ROPE_THREADS, smem, st, p);
 }
 template <typename T, typename C> static cudaError_t launch(const RopeParams &p, cudaStream_t st)
 {
