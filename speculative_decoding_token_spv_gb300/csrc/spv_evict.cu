@@ -6,9 +6,10 @@
 // last slot to stay is found digit by digit; bit masks of the kept slots and
 // prefix counts over their words then match the i-th hole below the budget
 // with the i-th kept slot above it.  Up to 16,384 slots the keys stay in
-// registers (evict_select_few), two bits a round by counting, and the rounds
-// end as soon as a count is exact, usually after about 12; beyond, a radix
-// select reads the weights again for each of four digits (evict_select_many).
+// registers (evict_select_few), up to 49,152 in shared memory, and are counted,
+// two bits a round, until a count is exact, usually after about 12 rounds;
+// beyond, a radix select reads the weights again for each of four digits
+// (evict_select_many).
 // evict_move_kernel, a dependent launch, copies the rows of the matched slots.
 #include "spv_kv.cuh"
 
@@ -17,6 +18,7 @@ namespace spv {
 constexpr int EV_THREADS = 1024;
 constexpr int EV_MOVE_SLOTS = 256;     // slots that a block of the move looks at, one a thread
 constexpr int EV_MOVE_AHEAD = 8;       // 16-byte pieces of a thread on their way
+constexpr int EV_HELD_SLOTS = 49152;   // whose keys fit shared memory
 constexpr int EV_FEW_SLOTS = 16384, EV_FEW_THREADS = 512;  // two blocks an SM for up to 8,192 slots
 
 struct EvictParams {
@@ -118,6 +120,52 @@ __device__ __forceinline__ void evict_write(const EvictParams &p, const EvictIte
     if (it.pos_out && (s != i || p.pos_out != p.pos)) it.pos_out[i] = it.pos ? it.pos[s] : s;
 }
 
+// The m largest keys: those from `least` on where that is exactly m (exact),
+// else those above it and `want` of its equals.
+struct EvictCut {
+    unsigned least;
+    int want;
+    bool exact;
+};
+// `count(a, b, c, &x, &yz)` adds a thread's number of keys >= a to x, >= b and
+// >= c to the low and high half of yz (each below 65,536 in the block).  Two bits
+// a round; a round is two warp reductions on either side of one barrier.
+template <int WARPS, typename Count> __device__ __forceinline__ EvictCut find_cut(int m, uint2 (*counts)[WARPS], Count &&count)
+{
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    EvictCut cut{0, 0, false};
+    int turn = 0;
+    auto count3 = [&](unsigned a, unsigned b, unsigned c, int *na, int *nb, int *nc) {
+        unsigned x = 0, yz = 0;
+        count(a, b, c, &x, &yz);
+        x = __reduce_add_sync(0xffffffffu, x);
+        yz = __reduce_add_sync(0xffffffffu, yz);
+        if (lane == 0) counts[turn][warp] = make_uint2(yz, x);
+        __syncthreads();
+        const uint2 w = lane < WARPS ? counts[turn][lane] : make_uint2(0, 0);
+        x = __reduce_add_sync(0xffffffffu, w.y);
+        yz = __reduce_add_sync(0xffffffffu, w.x);
+        *na = static_cast<int>(x);
+        *nb = static_cast<int>(yz & 0xffffu);
+        *nc = static_cast<int>(yz >> 16);
+        turn ^= 1;  // who writes this turn's places again has passed the other's barrier
+    };
+    for (int bit = 30; bit >= 0 && !cut.exact; bit -= 2) {
+        const unsigned a = cut.least | 1u << bit, b = cut.least | 2u << bit, c = cut.least | 3u << bit;
+        int x, y, z;
+        count3(a, b, c, &x, &y, &z);
+        const int got = z >= m ? z : y >= m ? y : x >= m ? x : -1;
+        cut.least = z >= m ? c : y >= m ? b : x >= m ? a : cut.least;
+        cut.exact = got == m;
+    }
+    if (!cut.exact) {
+        int x = 0, y, z;
+        if (cut.least != 0xffffffffu) count3(cut.least + 1u, 0xffffffffu, 0xffffffffu, &x, &y, &z);
+        cut.want = m - x;
+    }
+    return cut;
+}
+
 // Slots in registers: slot t + 512 i is thread t's i-th.
 template <int PER> __global__ void __launch_bounds__(EV_FEW_THREADS) evict_select_few(const EvictParams p)
 {
@@ -155,43 +203,16 @@ template <int PER> __global__ void __launch_bounds__(EV_FEW_THREADS) evict_selec
             key[i] = j >= n ? 0u : always ? 0xffffffffu : mass_key(w[i]);
         }
     }
-    // the largest `least` with at least m keys >= it: two bits a round
-    unsigned least = 0;
-    bool exact = false;
-    int turn = 0;
-    auto count3 = [&](unsigned a, unsigned b, unsigned c, int *na, int *nb, int *nc) {  // keys >= a, b, c
-        unsigned x = 0, yz = 0;
+    const EvictCut cut = find_cut<WARPS>(m, counts, [&](unsigned a, unsigned b, unsigned c, unsigned *x, unsigned *yz) {
 #pragma unroll
         for (int i = 0; i < PER; ++i) {
-            x += key[i] >= a;
-            yz += (key[i] >= b ? 1u : 0u) + (key[i] >= c ? 0x10000u : 0u);
+            *x += key[i] >= a;
+            *yz += (key[i] >= b ? 1u : 0u) + (key[i] >= c ? 0x10000u : 0u);
         }
-        x = __reduce_add_sync(0xffffffffu, x);
-        yz = __reduce_add_sync(0xffffffffu, yz);
-        if (lane == 0) counts[turn][warp] = make_uint2(yz, x);
-        __syncthreads();
-        const uint2 w = lane < WARPS ? counts[turn][lane] : make_uint2(0, 0);
-        x = __reduce_add_sync(0xffffffffu, w.y);
-        yz = __reduce_add_sync(0xffffffffu, w.x);
-        *na = static_cast<int>(x);
-        *nb = static_cast<int>(yz & 0xffffu);
-        *nc = static_cast<int>(yz >> 16);
-        turn ^= 1;  // who writes this turn's places again has passed the other's barrier
-    };
-    for (int bit = 30; bit >= 0 && !exact; bit -= 2) {
-        const unsigned a = least | 1u << bit, b = least | 2u << bit, c = least | 3u << bit;
-        int x, y, z;
-        count3(a, b, c, &x, &y, &z);
-        const int got = z >= m ? z : y >= m ? y : x >= m ? x : -1;
-        least = z >= m ? c : y >= m ? b : x >= m ? a : least;
-        exact = got == m;
-    }
-    int want = 0;  // of the keys equal to `least`, from the lowest slot on
-    if (!exact) {
-        int x = 0, y, z;
-        if (least != 0xffffffffu) count3(least + 1u, 0xffffffffu, 0xffffffffu, &x, &y, &z);
-        want = m - x;
-    }
+    });
+    const unsigned least = cut.least;
+    const bool exact = cut.exact;
+    const int want = cut.want;
 #pragma unroll
     for (int i = 0; i < PER; ++i) {
         const int j = tid + i * NT;
@@ -258,9 +279,12 @@ template <int PER> __global__ void __launch_bounds__(EV_FEW_THREADS) evict_selec
     }
 }
 
-__global__ void __launch_bounds__(EV_THREADS) evict_select_many(const EvictParams p)
+// HELD: the keys fit shared memory and are counted there; else the weights are
+// read again for each digit of a radix select.
+template <bool HELD> __global__ void __launch_bounds__(EV_THREADS) evict_select_many(const EvictParams p)
 {
-    extern __shared__ unsigned words[];  // kept bits, then prefix counts
+    extern __shared__ unsigned words[];  // kept bits, prefix counts; HELD: the keys
+    __shared__ uint2 counts[2][EV_THREADS / 32];
     __shared__ unsigned hist[256];
     __shared__ int sh[32];
     __shared__ int tops[32];
@@ -279,35 +303,53 @@ __global__ void __launch_bounds__(EV_THREADS) evict_select_many(const EvictParam
         __syncthreads();
         top = __reduce_max_sync(0xffffffffu, tops[lane]);
     }
-    // the key of the m-th largest, digit by digit; `want` of its equals stay
+    unsigned *keys = words + 2 * p.words;  // each thread's own: slots tid + 1024 i
+    auto key_of = [&](int j) { return HELD ? keys[j] : slot_key(p, mass, pos, j, top); };
+    // the key of the m-th largest; `want` of its equals stay
     unsigned prefix = 0;
     int want = m;
-    for (int shift = 24; shift >= 0; shift -= 8) {
-        if (tid < 256) hist[tid] = 0;
-        __syncthreads();
-        for (int j = tid; j < n; j += EV_THREADS) {
-            const unsigned key = slot_key(p, mass, pos, j, top);
-            if (shift == 24 || (key >> (shift + 8)) == (prefix >> (shift + 8))) atomicAdd(&hist[key >> shift & 255u], 1u);
+    if constexpr (HELD) {
+#pragma unroll 8
+        for (int j = tid; j < n; j += EV_THREADS) keys[j] = slot_key(p, mass, pos, j, top);
+        const EvictCut cut = find_cut<EV_THREADS / 32>(m, counts, [&](unsigned a, unsigned b, unsigned c, unsigned *x, unsigned *yz) {
+#pragma unroll 8
+            for (int j = tid; j < n; j += EV_THREADS) {
+                const unsigned k = keys[j];
+                *x += k >= a;
+                *yz += (k >= b ? 1u : 0u) + (k >= c ? 0x10000u : 0u);
+            }
+        });
+        // exactly: all above the key before the least one
+        prefix = cut.exact ? cut.least - 1u : cut.least;
+        want = cut.exact ? 0 : cut.want;
+    } else {
+        for (int shift = 24; shift >= 0; shift -= 8) {
+            if (tid < 256) hist[tid] = 0;
+            __syncthreads();
+            for (int j = tid; j < n; j += EV_THREADS) {
+                const unsigned key = slot_key(p, mass, pos, j, top);
+                if (shift == 24 || (key >> (shift + 8)) == (prefix >> (shift + 8))) atomicAdd(&hist[key >> shift & 255u], 1u);
+            }
+            __syncthreads();
+            const int x = tid < 256 ? static_cast<int>(hist[255 - tid]) : 0;
+            int all;
+            const int before = block_prefix<EV_THREADS / 32>(x, sh, &all);  // of larger digits
+            if (tid < 256 && before < want && want <= before + x) {
+                found[0] = 255 - tid;
+                found[1] = want - before;
+            }
+            __syncthreads();
+            prefix |= found[0] << shift;
+            want = static_cast<int>(found[1]);
+            __syncthreads();
         }
-        __syncthreads();
-        const int x = tid < 256 ? static_cast<int>(hist[255 - tid]) : 0;
-        int all;
-        const int before = block_prefix<EV_THREADS / 32>(x, sh, &all);  // of larger digits
-        if (tid < 256 && before < want && want <= before + x) {
-            found[0] = 255 - tid;
-            found[1] = want - before;
-        }
-        __syncthreads();
-        prefix |= found[0] << shift;
-        want = static_cast<int>(found[1]);
-        __syncthreads();
     }
     // kept bits: larger keys, and the first `want` equals
     const int nw = (n + 31) >> 5;
     unsigned *kept = words, *count = words + p.words;
     for (int w = tid >> 5; w < nw; w += EV_THREADS / 32) {
         const int j = 32 * w + lane;
-        const unsigned key = j < n ? slot_key(p, mass, pos, j, top) : 0;
+        const unsigned key = j < n ? key_of(j) : 0;
         const unsigned gt = __ballot_sync(0xffffffffu, j < n && key > prefix);
         const unsigned eq = __ballot_sync(0xffffffffu, j < n && key == prefix);
         if (lane == 0) {
@@ -470,12 +512,12 @@ cudaError_t launch_evict(const EvictLaunch &L, cudaStream_t st)
     } else if (slots <= EV_FEW_SLOTS) {
         e = launch_chained(evict_select_few<32>, items, EV_FEW_THREADS, 0, st, p);
     } else {
-        const int smem = p.words * 2 * static_cast<int>(sizeof(unsigned));
-        if (smem > 40 * 1024) {
-            e = cudaFuncSetAttribute(evict_select_many, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
-            if (e != cudaSuccess) return e;
-        }
-        e = launch_chained(evict_select_many, items, EV_THREADS, smem, st, p);
+        const bool held = slots <= EV_HELD_SLOTS;
+        const int smem = (p.words * 2 + (held ? slots : 0)) * static_cast<int>(sizeof(unsigned));
+        auto kernel = held ? evict_select_many<true> : evict_select_many<false>;
+        e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+        if (e != cudaSuccess) return e;
+        e = launch_chained(kernel, items, EV_THREADS, smem, st, p);
     }
     if (e != cudaSuccess) return e;
     const dim3 moves((L.budget + EV_MOVE_SLOTS - 1) / EV_MOVE_SLOTS, k.B * k.cache.kv_heads);

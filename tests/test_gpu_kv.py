@@ -452,6 +452,7 @@ def _evict_case(spv, seed, lens, budget, sinks, recent, Hkv, D, page, order, kv,
     ([5000, 1], 1, 0, 0, 1, 256, 16, "nhd", "bf16"),
     ([4097], 2048, 2048, 0, 2, 64, 16, "nhd", "bf16"),
     ([4097, 4096], 2049, 1, 2048, 2, 64, 1, "nhd", "bf16"),
+    ([16384, 9000], 8191, 4, 100, 1, 64, 16, "nhd", "bf16"),
     ([20000], 12345, 4, 1000, 1, 64, 16, "nhd", "bf16"),
     ([70001], 65536, 4, 1000, 1, 64, 128, "nhd", "e4m3"),
 ], ids=lambda c: "-".join(str(x).replace(" ", "") for x in c))
