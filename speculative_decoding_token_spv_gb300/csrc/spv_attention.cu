@@ -399,9 +399,9 @@ cudaError_t launch_attention(const AttentionLaunch &L, cudaStream_t st)
     p.parts = reinterpret_cast<float *>(ws + ATT_PARTS_AT);
     const bool eight = k.cache.dtype == SPV_E4M3;
     const int D = k.cache.head_dim;
-    // Over 16 rows the 5th-generation tensor cores: at 32 rows, two 131,001-key sequences of 8 key heads, D = 128,
-    // they take 180 us of a bf16 cache where the warps here take 188; of an e4m3 cache 184 against 161, as its rows
-    // pass through shared memory twice there and once here: then over 32 rows (at 40, 240 against 330).
+    // Over 16 rows the 5th-generation tensor cores, for an e4m3 cache over 32: its rows pass through shared memory
+    // twice there.  Two sequences of 131,001 keys, 8 key heads, D = 128, from cold caches: bf16 at 20 rows 198 us
+    // there and 206 here, at 40 rows 202 and 366; e4m3 at 32 rows 236 and 177, at 40 rows 237 and 310.
     if (p.rows > (eight ? 32 : 16) && D <= 128) return launch_attention_rows(p, k, st);
     if (k.dtype == SPV_BF16)
         return eight ? launch_types<__nv_bfloat16, __nv_fp8_e4m3>(p, D, st)

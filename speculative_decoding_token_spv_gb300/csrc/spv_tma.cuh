@@ -46,7 +46,7 @@ inline bool pool_map(CUtensorMap *map, const KvLaunch &L, bool v)
     const cuuint32_t steps[4] = {1, 1, 1, 1};
     return encode(map, c.dtype == SPV_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 4,
                   v ? c.v : c.k, sizes, bytes, box, steps, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
-                  CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+                  CU_TENSOR_MAP_L2_PROMOTION_L2_128B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
 // Copies the box at (d, slot, head, page) -- d a multiple of 64 -- to shared
