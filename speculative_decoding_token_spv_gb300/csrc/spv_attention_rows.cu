@@ -382,34 +382,46 @@ __device__ void rows_prepare(const AttParams &p, Cursor c, char *smem, RowsCtl *
         if (item >= 2 && !rows_wait(ctl, &ctl->q_empty[place], ((item >> 1) - 1) & 1, err)) return;
         for (int t = lt; t < p.w.T; t += 96)
             ctl->sees[place][t] = t < c.s.fresh ? visible_mask(p.parent ? p.parent + static_cast<int64_t>(c.b) * p.w.T : nullptr, t) : 0ull;
-        constexpr int CH = D / 8, STEP = 96 / CH;  // rows at a time: 6 or 12
-        for (int r0 = 0; r0 < COLS; r0 += STEP) {
-            const int r = r0 + lt / CH, ch = lt % CH, t = (row0 + r) / p.group, g = (row0 + r) - t * p.group;
-            uint4 raw = make_uint4(0, 0, 0, 0);
-            if (r < live && t < c.s.fresh)
-                raw = *reinterpret_cast<const uint4 *>(static_cast<const T *>(p.q) +
-                                                       ((static_cast<int64_t>(c.b) * p.w.T + t) * p.q_heads + c.h * p.group + g) * D + ch * 8);
-            if (S::WIDEN) {
-                const T *y = reinterpret_cast<const T *>(&raw);
-                float x[8], top = 0.0f;
+        // rows at a time, 6 or 12; six loads of a thread on their way together (one by one they took 6 us)
+        constexpr int CH = D / 8, STEP = 96 / CH, AHEAD = 6;
+        const int ch = lt % CH;
+#pragma unroll 1
+        for (int b0 = 0; b0 < COLS; b0 += AHEAD * STEP) {
+            uint4 in[AHEAD];
 #pragma unroll
-                for (int e = 0; e < 8; ++e) {
-                    x[e] = Num<T>::up(y[e]);
-                    top = fabsf(x[e]) < CUDART_INF_F ? fmaxf(top, fabsf(x[e])) : top;
-                }
-#pragma unroll
-                for (int o = CH / 2; o; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
-                const int e2 = top > 0.0f ? max(-120, min(120, 14 - ilogbf(top))) : 0;
-                const float up = exp2f(static_cast<float>(e2));
-                if (ch == 0 && r < COLS)
-#pragma unroll
-                    for (int k = 0; k < AR_ROWS; k += COLS) ctl->q_power[place][k + r] = static_cast<signed char>(e2);
-                raw = make_uint4(pack_mma<M>(x[0] * up, x[1] * up), pack_mma<M>(x[2] * up, x[3] * up),
-                                 pack_mma<M>(x[4] * up, x[5] * up), pack_mma<M>(x[6] * up, x[7] * up));
+            for (int i = 0; i < AHEAD; ++i) {
+                const int r = b0 + i * STEP + lt / CH, t = (row0 + r) / p.group, g = (row0 + r) - t * p.group;
+                in[i] = make_uint4(0, 0, 0, 0);
+                if (r < live && t < c.s.fresh)
+                    in[i] = *reinterpret_cast<const uint4 *>(
+                        static_cast<const T *>(p.q) + ((static_cast<int64_t>(c.b) * p.w.T + t) * p.q_heads + c.h * p.group + g) * D + ch * 8);
             }
-            if (r < COLS)
 #pragma unroll
-                for (int k = 0; k < AR_ROWS; k += COLS) *reinterpret_cast<uint4 *>(qs + panel_at(k + r, ch)) = raw;
+            for (int i = 0; i < AHEAD; ++i) {
+                const int r = b0 + i * STEP + lt / CH;
+                uint4 raw = in[i];
+                if (S::WIDEN) {
+                    const T *y = reinterpret_cast<const T *>(&raw);
+                    float x[8], top = 0.0f;
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) {
+                        x[e] = Num<T>::up(y[e]);
+                        top = fabsf(x[e]) < CUDART_INF_F ? fmaxf(top, fabsf(x[e])) : top;
+                    }
+#pragma unroll
+                    for (int o = CH / 2; o; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+                    const int e2 = top > 0.0f ? max(-120, min(120, 14 - ilogbf(top))) : 0;
+                    const float up = exp2f(static_cast<float>(e2));
+                    if (ch == 0 && r < COLS)
+#pragma unroll
+                        for (int k = 0; k < AR_ROWS; k += COLS) ctl->q_power[place][k + r] = static_cast<signed char>(e2);
+                    raw = make_uint4(pack_mma<M>(x[0] * up, x[1] * up), pack_mma<M>(x[2] * up, x[3] * up),
+                                     pack_mma<M>(x[4] * up, x[5] * up), pack_mma<M>(x[6] * up, x[7] * up));
+                }
+                if (r < COLS)
+#pragma unroll
+                    for (int k = 0; k < AR_ROWS; k += COLS) *reinterpret_cast<uint4 *>(qs + panel_at(k + r, ch)) = raw;
+            }
         }
         fence_async_shared();
         mbar_arrive(&ctl->q_full[place]);

@@ -129,7 +129,7 @@ __device__ __forceinline__ Cursor find_range(const Work &w, const PagedView &v, 
     const int per = w.row_tiles * v.kv_heads;
     // Tiles of sequences lane, lane + 32, ...: the first KEEP of them stay in registers, their loads all under way
     // at once (a load is about a microsecond when the lengths come from memory).
-    constexpr int KEEP = 8;
+    constexpr int KEEP = 2;
     int tiles[KEEP];
     long long sum = 0;
 #pragma unroll
@@ -153,21 +153,20 @@ __device__ __forceinline__ Cursor find_range(const Work &w, const PagedView &v, 
     long long before = 0;
     bool found = false;
     auto look = [&](int b0, int mine) {  // among sequences b0 .. b0 + 31, whose tiles the lanes have
-        const long long n = static_cast<long long>(mine) * per;
-        long long upto = n;
+        int upto = mine;  // 32 sequences' tiles fit 32 bits
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
-            const long long y = __shfl_up_sync(0xffffffffu, upto, o);
+            const int y = __shfl_up_sync(0xffffffffu, upto, o);
             if (lane >= o) upto += y;
         }
-        const unsigned here = __ballot_sync(0xffffffffu, before + upto > c.at);
+        const unsigned here = __ballot_sync(0xffffffffu, before + static_cast<long long>(upto) * per > c.at);
         if (here) {
             const int l = __ffs(here) - 1;
             c.b = b0 + l;
-            before += __shfl_sync(0xffffffffu, upto - n, l);
+            before += static_cast<long long>(__shfl_sync(0xffffffffu, upto - mine, l)) * per;
             found = true;
         } else {
-            before += __shfl_sync(0xffffffffu, upto, 31);
+            before += static_cast<long long>(__shfl_sync(0xffffffffu, upto, 31)) * per;
         }
     };
 #pragma unroll

@@ -226,7 +226,7 @@ __device__ void mass_prepare(const MassParams &p, Cursor c, char *smem, Ctl *ctl
 {
     using S = MassShape<C, D>;
     using M = typename MmaOf<T, C>::type;
-    constexpr int CH = D / 8, STEP = 96 / CH;  // rows at a time
+    constexpr int CH = D / 8, STEP = 96 / CH, AHEAD = 6;  // rows at a time, loads of a thread on their way together
     Counted count;
     int unit_no = 0;
     for (; c.at < c.end; next_item(c, p.w, p.c)) {
@@ -237,50 +237,61 @@ __device__ void mass_prepare(const MassParams &p, Cursor c, char *smem, Ctl *ctl
             const int place = unit_no & 1, live = min(S::ROWS, count.rows - r0), padded = (live + 15) & ~15;
             char *qs = smem + S::Q_AT + place * S::Q;
             if (unit_no >= 2 && !mass_wait(ctl, &ctl->q_empty[place], ((unit_no >> 1) - 1) & 1)) return;
-            for (int b0 = 0; b0 < padded; b0 += STEP) {
-                const int r = b0 + lt / CH, ch = lt % CH;
-                const bool there = lt < STEP * CH && r < live;
-                uint4 raw = make_uint4(0, 0, 0, 0);
-                int64_t at = 0;
-                int t = 0;
-                if (there) {
-                    const int nth = (r0 + r) / p.group, g = r0 + r - nth * p.group;
-                    unsigned long long m = count.tokens;
-                    for (int e = 0; e < nth; ++e) m &= m - 1;
-                    t = __ffsll(m) - 1;
-                    at = (static_cast<int64_t>(c.b) * p.w.T + t) * p.q_heads + c.h * p.group + g;
-                    raw = *reinterpret_cast<const uint4 *>(static_cast<const T *>(p.q) + at * D + ch * 8);
-                }
-                float down = 1.0f;
-                if (S::WIDEN) {
-                    const T *y = reinterpret_cast<const T *>(&raw);
-                    float x[8], top = 0.0f;
+            const int ch = lt % CH;
+#pragma unroll 1
+            for (int b0 = 0; b0 < padded; b0 += AHEAD * STEP) {
+                uint4 in[AHEAD];
+                float z[AHEAD];
+                int token[AHEAD];
 #pragma unroll
-                    for (int e = 0; e < 8; ++e) {
-                        x[e] = Num<T>::up(y[e]);
-                        top = fabsf(x[e]) < CUDART_INF_F ? fmaxf(top, fabsf(x[e])) : top;
+                for (int i = 0; i < AHEAD; ++i) {
+                    const int r = b0 + i * STEP + lt / CH;
+                    in[i] = make_uint4(0, 0, 0, 0);
+                    z[i] = CUDART_INF_F;
+                    token[i] = -1;
+                    if (r < live) {
+                        const int nth = (r0 + r) / p.group, g = r0 + r - nth * p.group;
+                        unsigned long long m = count.tokens;
+                        for (int e = 0; e < nth; ++e) m &= m - 1;
+                        token[i] = __ffsll(m) - 1;
+                        const int64_t at = (static_cast<int64_t>(c.b) * p.w.T + token[i]) * p.q_heads + c.h * p.group + g;
+                        in[i] = *reinterpret_cast<const uint4 *>(static_cast<const T *>(p.q) + at * D + ch * 8);
+                        if (ch == 0) z[i] = __ldg(p.lse + at);
                     }
-#pragma unroll
-                    for (int o = CH / 2; o; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
-                    const int e2 = top > 0.0f ? max(-120, min(120, 14 - ilogbf(top))) : 0;
-                    const float up = exp2f(static_cast<float>(e2));
-                    down = exp2f(static_cast<float>(-e2));
-                    raw = make_uint4(pack_mma<M>(x[0] * up, x[1] * up), pack_mma<M>(x[2] * up, x[3] * up),
-                                     pack_mma<M>(x[4] * up, x[5] * up), pack_mma<M>(x[6] * up, x[7] * up));
                 }
-                if (lt < STEP * CH && r < padded) {
-                    *reinterpret_cast<uint4 *>(qs + mass_panel<S::ROWS>(r, ch)) = raw;
-                    if (ch == 0) {
-                        unsigned long long see = 0;
-                        float z = CUDART_INF_F;
-                        if (there) {
-                            see = visible_mask(p.parent ? p.parent + static_cast<int64_t>(c.b) * p.w.T : nullptr, t);
-                            z = __ldg(p.lse + at) * LOG2E;
-                            if (z == -CUDART_INF_F) see = 0;
-                            if (see == 0) *reinterpret_cast<volatile int *>(&ctl->careful[place]) = unit_no + 1;
+#pragma unroll
+                for (int i = 0; i < AHEAD; ++i) {
+                    const int r = b0 + i * STEP + lt / CH;
+                    uint4 raw = in[i];
+                    float down = 1.0f;
+                    if (S::WIDEN) {
+                        const T *y = reinterpret_cast<const T *>(&raw);
+                        float x[8], top = 0.0f;
+#pragma unroll
+                        for (int e = 0; e < 8; ++e) {
+                            x[e] = Num<T>::up(y[e]);
+                            top = fabsf(x[e]) < CUDART_INF_F ? fmaxf(top, fabsf(x[e])) : top;
                         }
-                        ctl->row[place][r] = make_float2(unit * down, z);
-                        ctl->sees[place][r] = see;
+#pragma unroll
+                        for (int o = CH / 2; o; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+                        const int e2 = top > 0.0f ? max(-120, min(120, 14 - ilogbf(top))) : 0;
+                        const float up = exp2f(static_cast<float>(e2));
+                        down = exp2f(static_cast<float>(-e2));
+                        raw = make_uint4(pack_mma<M>(x[0] * up, x[1] * up), pack_mma<M>(x[2] * up, x[3] * up),
+                                         pack_mma<M>(x[4] * up, x[5] * up), pack_mma<M>(x[6] * up, x[7] * up));
+                    }
+                    if (r < padded) {
+                        *reinterpret_cast<uint4 *>(qs + mass_panel<S::ROWS>(r, ch)) = raw;
+                        if (ch == 0) {
+                            unsigned long long see = 0;
+                            if (token[i] >= 0) {
+                                see = visible_mask(p.parent ? p.parent + static_cast<int64_t>(c.b) * p.w.T : nullptr, token[i]);
+                                if (z[i] == -CUDART_INF_F) see = 0;
+                                if (see == 0) *reinterpret_cast<volatile int *>(&ctl->careful[place]) = unit_no + 1;
+                            }
+                            ctl->row[place][r] = make_float2(unit * down, z[i] * LOG2E);
+                            ctl->sees[place][r] = see;
+                        }
                     }
                 }
             }
