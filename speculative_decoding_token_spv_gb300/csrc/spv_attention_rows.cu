@@ -28,7 +28,6 @@
 namespace spv {
 
 constexpr int AR_KEYS = 128;
-constexpr int AR_THREADS = 512;  // warps 0-3 rows, 4 products, 8-11 K, 12-15 V
 constexpr int AR_ROWS = 128;
 constexpr int AR_ITEMS = 16;          // items whose flags can be in use at once
 constexpr float AR_GROWTH = 8.0f;     // growth of a maximum (powers of two) that O waits for
@@ -59,10 +58,20 @@ struct RowsCtl {
     int dead, stop;
 };
 
+// Warps of a block: 4 for the rows, or 8 that share each row's keys where a row stands once; then 4 of products and q, 4
+// of K, 4 of V.
+template <int COLS> struct RowsWarps {
+    static constexpr int HALVES = COLS == AR_ROWS ? 2 : 1, SOFTMAX = 128 * HALVES, THREADS = SOFTMAX + 384;
+    // Columns of tensor memory: scores of two tiles at 0 and 128.  Rows in several copies keep their probabilities apart
+    // (the zeros of the other copies' keys stay there); with one copy each half's take the place of its scores and there
+    // is room for an O of each half.
+    static constexpr int P_AT = HALVES == 2 ? 0 : 256, P_STAGE = HALVES == 2 ? AR_KEYS : AR_KEYS / 2, O_AT = HALVES == 2 ? 256 : 384;
+};
+
 // What the warps of the rows exchange at the end of a piece, in the place of its q.
 template <int D> struct RowsMerge {
     static constexpr int ROUNDS = D == 128 ? 2 : 1;  // buffers in turn, as many as fit
-    float ms[AR_ROWS], ls[AR_ROWS];
+    float ms[2 * AR_ROWS], ls[2 * AR_ROWS];
     float x[ROUNDS][96 * 33];
 };
 
@@ -296,7 +305,7 @@ __device__ __forceinline__ bool mbar_test(uint64_t *bar, uint32_t parity)
 // One thread.  Issues whatever is ready: the scores of the next tile, up to
 // two ahead of the last tile whose probabilities were multiplied, and the
 // probabilities' product; neither waits for the other's operands.
-template <typename T, typename C, int D>
+template <typename T, typename C, int D, int COLS>
 __device__ void rows_multiply(const AttParams &p, const Cursor &c0, char *smem, RowsCtl *ctl, unsigned *err)
 {
     using S = RowsShape<C, D>;
@@ -305,7 +314,8 @@ __device__ void rows_multiply(const AttParams &p, const Cursor &c0, char *smem, 
     constexpr uint32_t SHAPE_S = mma_shape(BF, false, AR_KEYS), SHAPE_O = mma_shape(BF, true, D);
     constexpr int KST = S::K_STAGES, VST = S::V_STAGES;
     const uint32_t base = smem_u32(smem), tmem = ctl->tmem;
-    const uint32_t tm_s = tmem, tm_p = tmem + 256, tm_o = tmem + 384;
+    using W = RowsWarps<COLS>;
+    const uint32_t tm_s = tmem, tm_p = tmem + W::P_AT, tm_o = tmem + W::O_AT;
     // the item of the next scores and that of the next outputs: where its tiles begin and end, its number
     struct Side {
         Cursor c;
@@ -323,6 +333,8 @@ __device__ void rows_multiply(const AttParams &p, const Cursor &c0, char *smem, 
     uint32_t idle = 0;
     while (no < ou.end) {
         if (ns < sc.end && ns <= no + 1 && mbar_test(&ctl->k_full[ns % KST], (ns / KST) & 1) &&
+            // where probabilities stand in the scores' place, they have to be multiplied before it is written again
+            (W::HALVES == 1 || ns < 2 || mbar_test(&ctl->o_done[ns & 1], ((ns - 2) >> 1) & 1)) &&
             (ns > sc.begin || mbar_test(&ctl->q_full[sc.item & 1], (sc.item >> 1) & 1))) {
             tc_fence_after();
             fence_async_shared();  // K was written by asynchronous copies of threads, q by threads
@@ -345,9 +357,12 @@ __device__ void rows_multiply(const AttParams &p, const Cursor &c0, char *smem, 
             fence_async_shared();
             const uint32_t v = base + S::V_AT + (no % VST) * S::TILE;
 #pragma unroll
-            for (int ks = 0; ks < AR_KEYS / 16; ++ks)
-                tc_mma_ta(tm_o, tm_p + (no & 1) * (AR_KEYS / 2) + ks * 8, desc_n_major(v + ks * 2048, AR_KEYS * 128), SHAPE_O,
-                          no > ou.begin || ks > 0);
+            for (int ks = 0; ks < AR_KEYS / 16; ++ks) {
+                constexpr int PER = AR_KEYS / 16 / W::HALVES;  // steps of a half
+                const int half = ks / PER, step = ks % PER;
+                tc_mma_ta(tm_o + half * 128, tm_p + (no & 1) * W::P_STAGE + half * 64 + step * 8,
+                          desc_n_major(v + ks * 2048, AR_KEYS * 128), SHAPE_O, no > ou.begin || step > 0);
+            }
             tc_commit(&ctl->o_done[no & 1]);
             tc_commit(&ctl->v_empty[no % VST]);
             if (++no == ou.end) {
@@ -443,19 +458,21 @@ __device__ __forceinline__ void store32(void *at, const uint32_t (&y)[8])
     }
 }
 
-__device__ __forceinline__ void rows_sync() { asm volatile("bar.sync 1, 128;" ::: "memory"); }
+template <int N> __device__ __forceinline__ void rows_sync() { asm volatile("bar.sync 1, %0;" ::"n"(N) : "memory"); }
 
-// COLS: keys of a tile that a thread takes, and rows of a copy.
+// COLS: rows of a copy, and its keys of a tile; a thread takes these, or half of them.
 template <typename T, typename C, int D, int COLS>
 __device__ void rows_softmax(const AttParams &p, Cursor c, char *smem, RowsCtl *ctl, unsigned *err, int tid)
 {
     using S = RowsShape<C, D>;
     using M = typename MmaOf<T, C>::type;
     constexpr int COPIES = AR_ROWS / COLS, PART = AR_ROWS * (D + 2);
-    const int lane = tid & 31, warp = tid >> 5, copy = tid / COLS, r = tid % COLS;
-    const uint32_t quarter = static_cast<uint32_t>(warp * 32) << 16;
-    const uint32_t tm_s = ctl->tmem + quarter + copy * COLS, tm_p = ctl->tmem + quarter + 256 + copy * (COLS / 2),
-                   tm_o = ctl->tmem + quarter + 384;
+    using W = RowsWarps<COLS>;
+    constexpr int HALVES = W::HALVES, KEYS = COLS / HALVES;
+    const int half = tid / AR_ROWS, lane_row = tid % AR_ROWS, copy = lane_row / COLS, r = lane_row % COLS;
+    const uint32_t quarter = static_cast<uint32_t>(lane_row & ~31) << 16;
+    const uint32_t tm_s = ctl->tmem + quarter + copy * COLS + half * KEYS,
+                   tm_p = ctl->tmem + quarter + W::P_AT + copy * (COLS / 2) + half * 64, tm_o = ctl->tmem + quarter + W::O_AT;
     const long long begin = c.at;
     // the keys of other copies never get a probability
     if (COPIES > 1) {
@@ -485,25 +502,25 @@ __device__ void rows_softmax(const AttParams &p, Cursor c, char *smem, RowsCtl *
         if (t0 < t1) {
             ok = rows_wait(ctl, &ctl->q_full[place], (item >> 1) & 1, err);
             if (mine && token < c.s.fresh) see = ctl->sees[place][token];
-            if (S::WIDEN) factor *= exp2f(-static_cast<float>(ctl->q_power[place][tid]));
+            if (S::WIDEN) factor *= exp2f(-static_cast<float>(ctl->q_power[place][lane_row]));
             const bool works = __any_sync(0xffffffffu, mine);
             for (int tile = t0; ok && tile < t1; ++tile, ++n) {
                 if (!(ok = rows_wait(ctl, &ctl->s_full[n & 1], (n >> 1) & 1, err))) break;
                 tc_fence_after();
                 __syncwarp();
                 if (works) {
-                    float x[COLS];
+                    float x[KEYS];
 #pragma unroll
-                    for (int i = 0; i < COLS; i += 32) {
+                    for (int i = 0; i < KEYS; i += 32) {
                         uint32_t y[32];
                         tc_ld32(y, tm_s + (n & 1) * AR_KEYS + i);
 #pragma unroll
                         for (int k = 0; k < 32; ++k) x[i + k] = __fmul_rn(__uint_as_float(y[k]), factor);  // as m is: not fused with the difference
                     }
-                    const int j0 = tile * AR_KEYS + copy * COLS;
-                    if (j0 + COLS > c.s.ctx) {
+                    const int j0 = tile * AR_KEYS + copy * COLS + half * KEYS;
+                    if (j0 + KEYS > c.s.ctx) {
 #pragma unroll
-                        for (int i = 0; i < COLS; i += 32) {
+                        for (int i = 0; i < KEYS; i += 32) {
                             const int o = c.s.ctx - (j0 + i);  // the first new token's column, from here
                             unsigned bits = o >= 32 ? 0xffffffffu : o > 0 && see ? (1u << o) - 1u : 0u;
                             if (o < 32 && o > -64) bits |= static_cast<unsigned>(o >= 0 ? see << o : see >> -o);
@@ -513,8 +530,8 @@ __device__ void rows_softmax(const AttParams &p, Cursor c, char *smem, RowsCtl *
                     }
                     float top = x[0];
 #pragma unroll
-                    for (int i = 1; i + 1 < COLS; i += 2) top = fmax3(top, x[i], x[i + 1]);
-                    top = fmaxf(top, x[COLS - 1]);
+                    for (int i = 1; i + 1 < KEYS; i += 2) top = fmax3(top, x[i], x[i + 1]);
+                    top = fmaxf(top, x[KEYS - 1]);
                     if (tile == t0) {
                         m = fmaxf(m, top);
                     } else if (__any_sync(0xffffffffu, top > m + AR_GROWTH || (m == -CUDART_INF_F && top > m))) {
@@ -524,19 +541,19 @@ __device__ void rows_softmax(const AttParams &p, Cursor c, char *smem, RowsCtl *
                         if (!(ok = rows_wait(ctl, &ctl->o_done[(n - 1) & 1], ((n - 1) >> 1) & 1, err))) break;
                         tc_fence_after();
 #pragma unroll 1
-                        for (int i = 0; i < D; i += 32) {
-                            uint32_t y[32];
-                            tc_ld32(y, tm_o + i);
+                        for (int i = 0; i < D; i += 16) {
+                            uint32_t y[16];
+                            tc_ld16(y, tm_o + half * 128 + i);
 #pragma unroll
-                            for (int k = 0; k < 32; ++k) y[k] = __float_as_uint(__uint_as_float(y[k]) * a);
-                            tc_st32(tm_o + i, y);
+                            for (int k = 0; k < 16; ++k) y[k] = __float_as_uint(__uint_as_float(y[k]) * a);
+                            tc_st16(tm_o + half * 128 + i, y);
                         }
                     }
                     const float base = m == -CUDART_INF_F ? 0.0f : m;
                     float s0 = 0.0f, s1 = 0.0f;
-                    uint32_t pk[COLS / 2];
+                    uint32_t pk[KEYS / 2];
 #pragma unroll
-                    for (int i = 0; i < COLS; i += 2) {
+                    for (int i = 0; i < KEYS; i += 2) {
                         const float a = fast_exp2(x[i] - base), b = fast_exp2(x[i + 1] - base);
                         s0 += a;
                         s1 += b;
@@ -544,15 +561,15 @@ __device__ void rows_softmax(const AttParams &p, Cursor c, char *smem, RowsCtl *
                         pk[i / 2] = pack_mma<M>(a, b);
                     }
                     l += s0 + s1;
-                    // its place was read by the product two tiles ago
-                    if (n >= 2 && !(ok = rows_wait(ctl, &ctl->o_done[n & 1], ((n - 2) >> 1) & 1, err))) break;
+                    // its place was read by the product two tiles ago (where it is the scores', they have waited for that)
+                    if (HALVES == 1 && n >= 2 && !(ok = rows_wait(ctl, &ctl->o_done[n & 1], ((n - 2) >> 1) & 1, err))) break;
                     tc_fence_after();
-                    if (COLS == 32) {
-                        tc_st16(tm_p + (n & 1) * (AR_KEYS / 2), *reinterpret_cast<uint32_t(*)[16]>(pk));
+                    if (KEYS == 32) {
+                        tc_st16(tm_p + (n & 1) * W::P_STAGE, *reinterpret_cast<uint32_t(*)[16]>(pk));
                     } else {
 #pragma unroll
-                        for (int i = 0; i < COLS / 2; i += 32)
-                            tc_st32(tm_p + (n & 1) * (AR_KEYS / 2) + i, *reinterpret_cast<uint32_t(*)[32]>(pk + i));
+                        for (int i = 0; i < KEYS / 2; i += 32)
+                            tc_st32(tm_p + (n & 1) * W::P_STAGE + i, *reinterpret_cast<uint32_t(*)[32]>(pk + i));
                     }
                     tc_wait_st();
                 }
@@ -563,7 +580,7 @@ __device__ void rows_softmax(const AttParams &p, Cursor c, char *smem, RowsCtl *
             tc_fence_after();
             odd = *reinterpret_cast<volatile unsigned long long *>(&ctl->odd[item_flags(item)]);
             any_bad |= *reinterpret_cast<volatile int *>(&ctl->bad[item_flags(item)]) != 0;
-            rows_sync();  // all have read them, and all scores
+            rows_sync<W::SOFTMAX>();  // all have read them, and all scores
         }
         if (see == 0) {
             m = -CUDART_INF_F;
@@ -581,18 +598,20 @@ __device__ void rows_softmax(const AttParams &p, Cursor c, char *smem, RowsCtl *
                 ctl->bad[item_flags(item)] = 0;
             }
         }
-        rows_sync();
+        rows_sync<W::SOFTMAX>();
         const bool stop = *reinterpret_cast<volatile int *>(&ctl->stop) != 0;
         any_bad |= stop;
         float all_m = -CUDART_INF_F, all_l = 0.0f;
         if (tiles) {
 #pragma unroll
-            for (int k = 0; k < COPIES; ++k) all_m = fmaxf(all_m, merge->ms[k * COLS + r]);
+            for (int k = 0; k < COPIES * HALVES; ++k) all_m = fmaxf(all_m, merge->ms[k * COLS + r]);
         }
         const float base = all_m == -CUDART_INF_F ? 0.0f : all_m, mine_a = l == 0.0f ? 0.0f : fast_exp2(m - base);
+        float other_a = 0.0f;  // of the other half's O
+        if (HALVES == 2 && tiles && merge->ls[tid ^ AR_ROWS] != 0.0f) other_a = fast_exp2(merge->ms[tid ^ AR_ROWS] - base);
         if (tiles) {
 #pragma unroll
-            for (int k = 0; k < COPIES; ++k) {
+            for (int k = 0; k < COPIES * HALVES; ++k) {
                 const float lk = merge->ls[k * COLS + r];
                 if (lk != 0.0f) all_l += lk * fast_exp2(merge->ms[k * COLS + r] - base);
             }
@@ -604,7 +623,7 @@ __device__ void rows_softmax(const AttParams &p, Cursor c, char *smem, RowsCtl *
         const int64_t row_at = (static_cast<int64_t>(c.b) * p.w.T + token) * p.q_heads + c.h * p.group + (row0 + r) - token * p.group;
         const bool none = all_m == -CUDART_INF_F && all_l == 0.0f, fixed = none || any_bad;
         const float instead = any_bad ? CUDART_NAN_F : 0.0f, out_scale = v_scale / all_l;
-        if (copy == 0 && mine) {
+        if (copy == 0 && half == 0 && mine) {
             if (!whole) {
                 part[r] = out_m;
                 part[AR_ROWS + r] = all_l;
@@ -613,29 +632,34 @@ __device__ void rows_softmax(const AttParams &p, Cursor c, char *smem, RowsCtl *
             }
         }
 #pragma unroll 1
-        for (int d0 = 0; d0 < D; d0 += 32) {
-            // each 32 columns are put together by another copy
+        for (int d0 = half * (D / 2); d0 < (HALVES == 2 ? (half + 1) * (D / 2) : D); d0 += 32) {
+            // each 32 columns are put together by another copy; of the halves each takes half the columns, of both O
             const int keeper = (d0 >> 5) % COPIES;
             float x[32];
             __syncwarp();
             if (tiles && !stop) {
                 uint32_t y[32];
-                tc_ld32(y, tm_o + d0);
+                tc_ld32(y, tm_o + half * 128 + d0);
 #pragma unroll
                 for (int k = 0; k < 32; ++k) x[k] = mine_a == 0.0f ? 0.0f : __uint_as_float(y[k]) * mine_a;
+                if constexpr (HALVES == 2) {
+                    tc_ld32(y, tm_o + (half ^ 1) * 128 + d0);
+#pragma unroll
+                    for (int k = 0; k < 32; ++k) x[k] += other_a == 0.0f ? 0.0f : __uint_as_float(y[k]) * other_a;
+                }
             } else {
 #pragma unroll
                 for (int k = 0; k < 32; ++k) x[k] = 0.0f;
             }
             if (COPIES > 1 && tiles) {
                 float *buf = merge->x[(d0 >> 5) % Merge::ROUNDS];
-                if (Merge::ROUNDS == 1 && d0 > 0) rows_sync();
+                if (Merge::ROUNDS == 1 && d0 > 0) rows_sync<W::SOFTMAX>();
                 if (copy != keeper) {
                     float *to = buf + (((copy - keeper + COPIES) % COPIES - 1) * COLS + r) * 33;
 #pragma unroll
                     for (int k = 0; k < 32; ++k) to[k] = x[k];
                 }
-                rows_sync();
+                rows_sync<W::SOFTMAX>();
                 if (copy == keeper) {
 #pragma unroll
                     for (int q = 0; q < COPIES - 1; ++q)
@@ -695,16 +719,17 @@ __device__ void rows_softmax(const AttParams &p, Cursor c, char *smem, RowsCtl *
             mbar_arrive(&ctl->q_empty[place]);
             ++item;
         }
-        rows_sync();
+        rows_sync<W::SOFTMAX>();
         if (stop) break;
     }
 }
 
 template <typename T, typename C, int D, int COLS>
-__global__ void __launch_bounds__(AR_THREADS, 1)
+__global__ void __launch_bounds__(RowsWarps<COLS>::THREADS, 1)
     attention_rows_kernel(const AttParams p, const __grid_constant__ CUtensorMap map_k, const __grid_constant__ CUtensorMap map_v, const int maps)
 {
     using S = RowsShape<C, D>;
+    using W = RowsWarps<COLS>;
     extern __shared__ char raw_smem[];
     char *smem = raw_smem + ((1024u - (smem_u32(raw_smem) & 1023u)) & 1023u);
     RowsCtl *ctl = reinterpret_cast<RowsCtl *>(smem + S::CTL_AT);
@@ -719,19 +744,19 @@ __global__ void __launch_bounds__(AR_THREADS, 1)
         }
         for (int i = 0; i < 2; ++i) {
             mbar_init(&ctl->s_full[i], 1);
-            mbar_init(&ctl->p_full[i], 128);
+            mbar_init(&ctl->p_full[i], W::SOFTMAX);
             mbar_init(&ctl->o_done[i], 1);
         }
         for (int i = 0; i < 2; ++i) {
             mbar_init(&ctl->q_full[i], 96);
-            mbar_init(&ctl->q_empty[i], 128);
+            mbar_init(&ctl->q_empty[i], W::SOFTMAX);
         }
         mbar_init(&ctl->spare, 1);
         for (int i = 0; i < AR_ITEMS; ++i) ctl->odd[i] = 0, ctl->bad[i] = 0;
         ctl->dead = ctl->stop = 0;
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
-    if (warp == 4) tmem_alloc(&ctl->tmem, 512);
+    if (warp == W::SOFTMAX / 32) tmem_alloc(&ctl->tmem, 512);
     chain_begin();
     const Cursor c = find_range(p.w, p.c, blockIdx.x, gridDim.x, tid & 31);
     if (tid < 2) p.split[blockIdx.x * 2 + tid].n = 0;
@@ -739,27 +764,39 @@ __global__ void __launch_bounds__(AR_THREADS, 1)
     __syncthreads();
     tc_fence_after();
     if (c.at == c.end) {  // the whole block
-        if (warp == 4) tmem_free(ctl->tmem, 512);
+        if (warp == W::SOFTMAX / 32) tmem_free(ctl->tmem, 512);
         return;
     }
-    // registers: launched with 128 a thread, 4 x 128 = 208 + 80 + 2 x 112
-    if (warp < 4) {
-        asm volatile("setmaxnreg.inc.sync.aligned.u32 208;");
+    // registers: launched with 128 a thread, 4 x 128 = 208 + 80 + 2 x 112, or with 96, 5 x 96 = 2 x 128 + 80 + 2 x 72 and
+    // 2 x 120 + 3 x 80 (more for the widening)
+    const int role = warp - W::SOFTMAX / 32;
+    if (role < 0) {
+        if (W::HALVES == 1)
+            asm volatile("setmaxnreg.inc.sync.aligned.u32 208;");
+        else if (S::WIDEN)
+            asm volatile("setmaxnreg.inc.sync.aligned.u32 120;");
+        else
+            asm volatile("setmaxnreg.inc.sync.aligned.u32 128;");
         rows_softmax<T, C, D, COLS>(p, c, smem, ctl, err, tid);
-    } else if (warp < 8) {
+    } else if (role < 4) {
         asm volatile("setmaxnreg.dec.sync.aligned.u32 80;");
-        if (tid == 128) {
-            rows_multiply<T, C, D>(p, c, smem, ctl, err);
+        if (tid == W::SOFTMAX) {
+            rows_multiply<T, C, D, COLS>(p, c, smem, ctl, err);
             if (*reinterpret_cast<volatile int *>(&ctl->dead)) {  // let what was issued end
                 tc_commit(&ctl->spare);
                 mbar_wait(&ctl->spare, 0);
             }
         }
         __syncwarp();
-        if (warp > 4) rows_prepare<T, C, D, COLS>(p, c, smem, ctl, err, tid - 160);
+        if (role > 0) rows_prepare<T, C, D, COLS>(p, c, smem, ctl, err, tid - W::SOFTMAX - 32);
     } else {
-        asm volatile("setmaxnreg.dec.sync.aligned.u32 112;");
-        if (warp < 12)
+        if (W::HALVES == 1)
+            asm volatile("setmaxnreg.dec.sync.aligned.u32 112;");
+        else if (S::WIDEN)
+            asm volatile("setmaxnreg.dec.sync.aligned.u32 80;");
+        else
+            asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
+        if (role < 8)
             rows_load<C, D, 0>(p, c, smem, ctl, err, tid & 127, maps ? &map_k : nullptr);
         else
             rows_load<C, D, 1>(p, c, smem, ctl, err, tid & 127, maps ? &map_v : nullptr);
@@ -767,7 +804,7 @@ __global__ void __launch_bounds__(AR_THREADS, 1)
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
-    if (warp == 4) tmem_free(ctl->tmem, 512);
+    if (warp == W::SOFTMAX / 32) tmem_free(ctl->tmem, 512);
 }
 
 template <typename T, typename C, int D, int COLS>
@@ -783,7 +820,7 @@ static cudaError_t launch_cols(AttParams p, const KvLaunch &L, cudaStream_t st)
     p.w.row_tiles = (p.rows + COLS - 1) / COLS;
     CUtensorMap map_k{}, map_v{};
     const bool maps = pool_map(&map_k, L, false) && pool_map(&map_v, L, true);
-    e = launch_chained(kernel, dim3(ATT_SMS), AR_THREADS, SMEM, st, p, map_k, map_v, static_cast<int>(maps));
+    e = launch_chained(kernel, dim3(ATT_SMS), RowsWarps<COLS>::THREADS, SMEM, st, p, map_k, map_v, static_cast<int>(maps));
     return e != cudaSuccess ? e : launch_join(p, std::is_same<T, __half>::value ? SPV_F16 : SPV_BF16, D, AR_ROWS, ATT_SMS, st);
 }
 template <typename T, typename C, int D> static cudaError_t launch_dim(const AttParams &p, const KvLaunch &L, cudaStream_t st)
