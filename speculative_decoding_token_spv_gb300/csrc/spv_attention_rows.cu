@@ -2,22 +2,30 @@
 // a key head (drafted chains with wide groups, draft trees): 5th-generation
 // tensor cores, up to 128 rows at a time against tiles of 128 keys.
 //
-// One block an SM, with its equal range of all tiles (Work, Cursor), in three
-// roles that follow one another over shared and tensor memory:
-//   * four loader warps gather K and V rows through the page table with
-//     asynchronous copies, in the permuted layout the tensor cores read; an
-//     e4m3 cache lands as it is and is widened to f16 by the threads that
-//     loaded it (f16 holds every e4m3 value);
-//   * one thread issues S = Q K^T of the next tile, then O += P V of this one,
-//     P from tensor memory, both sums in 32 bits in tensor memory; three more
-//     warps bring q of the next item;
+// One block an SM, with its equal range of all tiles (Work, Cursor), in roles
+// that follow one another over shared and tensor memory:
+//   * four warps bring K and four V, through the page table.  Whole tiles of a
+//     16-bit cache with pages of eight slots or more come by the copy engine, a
+//     box a page; other pages, and V's tiles with new tokens (whose infinities
+//     are looked for), by asynchronous copies of the threads, in the permuted
+//     layout the tensor cores read.  An e4m3 cache lands as it is and is widened
+//     to f16 by the threads that loaded it (f16 holds every e4m3 value);
+//   * one thread issues S = Q K^T, another O += P V, P from tensor memory, all
+//     sums in 32 bits in tensor memory; two warps bring q of the next item;
 //   * four warps hold a row a thread: running maximum, exponentials, sum, P
 //     back to tensor memory.  O is only rescaled when a maximum has grown by
 //     more than 2^8, so p stays below 2^8 and the 32-bit sums lose nothing.
 // With 64 rows or fewer the rows stand in tensor memory two or four times,
 // each copy taking half or a quarter of every tile's keys (its P is zero
 // elsewhere): all four warps work whatever the number of rows, and the
-// copies join at the end like pieces.
+// copies join at the end like pieces.  With more rows than that eight warps
+// work, two on each row's keys: with four, the exponentials of 128 rows took
+// 2,850 cycles a tile where its K and V take 2,300 (draft trees: 110 us).
+//
+// What bounds it, and what it takes: 40 rows of 64 sequences of up to 8,191
+// slots, K and V 1.37 GB, 232 us (5.9 TB/s, 87% of a copy's rate; 206 with no
+// start, ends and joins); 84 rows of 32 sequences of up to 4,099 slots, 353 MB,
+// 94 us: exponentials, 1,800 cycles a tile, and the ends of items.
 //
 // Every wait is bounded; one that gives up records SPV_ERR_TIMEOUT in the
 // workspace, ends the block in order and leaves NaN in what it had to write.
@@ -29,6 +37,7 @@ namespace spv {
 
 constexpr int AR_KEYS = 128;
 constexpr int AR_ROWS = 128;
+constexpr int AR_PREPARE = 64;        // threads that bring q
 constexpr int AR_ITEMS = 16;          // items whose flags can be in use at once
 constexpr float AR_GROWTH = 8.0f;     // growth of a maximum (powers of two) that O waits for
 
@@ -46,10 +55,11 @@ template <typename C, int D> struct RowsShape {
 
 struct RowsCtl {
     uint64_t k_full[5], k_empty[5], v_full[5], v_empty[5];  // of a stage (e4m3: the one widened tile)
-    uint64_t s_full[2], p_full[2], o_done[2], q_full[2], q_empty[2], spare;
+    uint64_t s_full[2], p_full[2], o_done[2], q_full[2], q_empty[2], spare[2];
     unsigned long long odd[AR_ITEMS];  // new tokens whose v has infinities or NaN
     unsigned long long sees[2][64];    // per place of q: what each new token sees
     int bad[AR_ITEMS];                 // a page id outside the pool
+    float top[2 * AR_ROWS];            // a tile's maxima of the two halves
     // e4m3: what widening a tile needs to know of it, per loader warp and stage: the row of its first new token (128:
     // none), that token's number, the item's flags.
     short tail[8][5][3];
@@ -62,10 +72,6 @@ struct RowsCtl {
 // of K, 4 of V.
 template <int COLS> struct RowsWarps {
     static constexpr int HALVES = COLS == AR_ROWS ? 2 : 1, SOFTMAX = 128 * HALVES, THREADS = SOFTMAX + 384;
-    // Columns of tensor memory: scores of two tiles at 0 and 128.  Rows in several copies keep their probabilities apart
-    // (the zeros of the other copies' keys stay there); with one copy each half's take the place of its scores and there
-    // is room for an O of each half.
-    static constexpr int P_AT = HALVES == 2 ? 0 : 256, P_STAGE = HALVES == 2 ? AR_KEYS : AR_KEYS / 2, O_AT = HALVES == 2 ? 256 : 384;
 };
 
 // What the warps of the rows exchange at the end of a piece, in the place of its q.
@@ -292,96 +298,66 @@ __device__ void rows_load(const AttParams &p, Cursor c, char *smem, RowsCtl *ctl
 }
 
 // ------------------------------------------------------------------ products
-__device__ __forceinline__ bool mbar_test(uint64_t *bar, uint32_t parity)
-{
-    uint32_t ok;
-    asm volatile("{\n\t.reg .pred p;\n\tmbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\tselp.u32 %0, 1, 0, p;\n\t}"
-                 : "=r"(ok)
-                 : "r"(smem_u32(bar)), "r"(parity)
-                 : "memory");
-    return ok != 0;
-}
-
-// One thread.  Issues whatever is ready: the scores of the next tile, up to
-// two ahead of the last tile whose probabilities were multiplied, and the
-// probabilities' product; neither waits for the other's operands.
-template <typename T, typename C, int D, int COLS>
-__device__ void rows_multiply(const AttParams &p, const Cursor &c0, char *smem, RowsCtl *ctl, unsigned *err)
+// Two threads, one for the scores and one for the outputs: issuing a tile's 8
+// products takes either of them 600 to 1,100 cycles, and the rows wait for the
+// scores (one thread for both: 241 us for the verify batch, now 232).
+template <typename T, typename C, int D>
+__device__ void rows_scores(const AttParams &p, Cursor c, char *smem, RowsCtl *ctl, unsigned *err)
 {
     using S = RowsShape<C, D>;
-    using M = typename MmaOf<T, C>::type;
-    constexpr bool BF = std::is_same<M, __nv_bfloat16>::value;
-    constexpr uint32_t SHAPE_S = mma_shape(BF, false, AR_KEYS), SHAPE_O = mma_shape(BF, true, D);
-    constexpr int KST = S::K_STAGES, VST = S::V_STAGES;
-    const uint32_t base = smem_u32(smem), tmem = ctl->tmem;
-    using W = RowsWarps<COLS>;
-    const uint32_t tm_s = tmem, tm_p = tmem + W::P_AT, tm_o = tmem + W::O_AT;
-    // the item of the next scores and that of the next outputs: where its tiles begin and end, its number
-    struct Side {
-        Cursor c;
-        int begin, end, item;
-    };
-    auto to_item_with_tiles = [&](Side &x) {
-        while (x.c.at < x.c.end && last_tile(x.c) == first_tile(x.c)) next_item(x.c, p.w, p.c);
-        x.begin = x.end;
-        if (x.c.at < x.c.end) x.end += last_tile(x.c) - first_tile(x.c);
-    };
-    Side sc{c0, 0, 0, 0}, ou{c0, 0, 0, 0};
-    to_item_with_tiles(sc);
-    to_item_with_tiles(ou);
-    int ns = 0, no = 0;  // tiles whose scores, whose outputs were issued
-    uint32_t idle = 0;
-    while (no < ou.end) {
-        if (ns < sc.end && ns <= no + 1 && mbar_test(&ctl->k_full[ns % KST], (ns / KST) & 1) &&
-            // where probabilities stand in the scores' place, they have to be multiplied before it is written again
-            (W::HALVES == 1 || ns < 2 || mbar_test(&ctl->o_done[ns & 1], ((ns - 2) >> 1) & 1)) &&
-            (ns > sc.begin || mbar_test(&ctl->q_full[sc.item & 1], (sc.item >> 1) & 1))) {
+    constexpr uint32_t SHAPE = mma_shape(std::is_same<typename MmaOf<T, C>::type, __nv_bfloat16>::value, false, AR_KEYS);
+    constexpr int KST = S::K_STAGES;
+    const uint32_t base = smem_u32(smem), tm_s = ctl->tmem;
+    int n = 0, item = 0;
+    for (; c.at < c.end; next_item(c, p.w, p.c)) {
+        const int tiles = last_tile(c) - first_tile(c);
+        if (tiles == 0) continue;
+        const uint64_t q = desc_k_major(base + S::Q_AT + (item & 1) * S::TILE);
+        if (!rows_wait1(ctl, &ctl->q_full[item & 1], (item >> 1) & 1, err)) return;
+        for (int i = 0; i < tiles; ++i, ++n) {
+            if (!rows_wait1(ctl, &ctl->k_full[n % KST], (n / KST) & 1, err)) return;
+            if (n >= 2 && !rows_wait1(ctl, &ctl->p_full[n & 1], ((n - 2) >> 1) & 1, err)) return;  // its place has been read
             tc_fence_after();
             fence_async_shared();  // K was written by asynchronous copies of threads, q by threads
-            const uint32_t k = base + S::K_AT + (ns % KST) * S::TILE, q = base + S::Q_AT + (sc.item & 1) * S::TILE;
+            const uint64_t k = desc_k_major(base + S::K_AT + (n % KST) * S::TILE);
 #pragma unroll
             for (int ks = 0; ks < D / 16; ++ks) {
-                const uint32_t off = (ks >> 2) * (AR_KEYS * 128) + (ks & 3) * 32;
-                tc_mma(tm_s + (ns & 1) * AR_KEYS, desc_k_major(q + off), desc_k_major(k + off), SHAPE_S, ks > 0);
+                const int off = ((ks >> 2) * (AR_KEYS * 128) + (ks & 3) * 32) >> 4;
+                tc_mma(tm_s + (n & 1) * AR_KEYS, q + off, k + off, SHAPE, ks > 0);
             }
-            tc_commit(&ctl->s_full[ns & 1]);
-            tc_commit(&ctl->k_empty[ns % KST]);
-            if (++ns == sc.end) {
-                next_item(sc.c, p.w, p.c);
-                ++sc.item;
-                to_item_with_tiles(sc);
-            }
-            idle = 0;
-        } else if (no < ns && mbar_test(&ctl->p_full[no & 1], (no >> 1) & 1) && mbar_test(&ctl->v_full[no % VST], (no / VST) & 1)) {
+            tc_commit(&ctl->s_full[n & 1]);
+            tc_commit(&ctl->k_empty[n % KST]);
+        }
+        ++item;
+    }
+}
+template <typename T, typename C, int D>
+__device__ void rows_outputs(const AttParams &p, Cursor c, char *smem, RowsCtl *ctl, unsigned *err)
+{
+    using S = RowsShape<C, D>;
+    constexpr uint32_t SHAPE = mma_shape(std::is_same<typename MmaOf<T, C>::type, __nv_bfloat16>::value, true, D);
+    constexpr int VST = S::V_STAGES;
+    const uint32_t base = smem_u32(smem), tm_p = ctl->tmem + 256, tm_o = ctl->tmem + 384;
+    int n = 0;
+    for (; c.at < c.end; next_item(c, p.w, p.c)) {
+        const int tiles = last_tile(c) - first_tile(c);
+        for (int i = 0; i < tiles; ++i, ++n) {
+            if (!rows_wait1(ctl, &ctl->v_full[n % VST], (n / VST) & 1, err)) return;
+            if (!rows_wait1(ctl, &ctl->p_full[n & 1], (n >> 1) & 1, err)) return;
             tc_fence_after();
             fence_async_shared();
-            const uint32_t v = base + S::V_AT + (no % VST) * S::TILE;
+            const uint64_t v = desc_n_major(base + S::V_AT + (n % VST) * S::TILE, AR_KEYS * 128);
 #pragma unroll
-            for (int ks = 0; ks < AR_KEYS / 16; ++ks) {
-                constexpr int PER = AR_KEYS / 16 / W::HALVES;  // steps of a half
-                const int half = ks / PER, step = ks % PER;
-                tc_mma_ta(tm_o + half * 128, tm_p + (no & 1) * W::P_STAGE + half * 64 + step * 8,
-                          desc_n_major(v + ks * 2048, AR_KEYS * 128), SHAPE_O, no > ou.begin || step > 0);
-            }
-            tc_commit(&ctl->o_done[no & 1]);
-            tc_commit(&ctl->v_empty[no % VST]);
-            if (++no == ou.end) {
-                next_item(ou.c, p.w, p.c);
-                to_item_with_tiles(ou);
-            }
-            idle = 0;
-        } else if (++idle == 4 * WAIT_LIMIT) {
-            *reinterpret_cast<volatile int *>(&ctl->dead) = 1;
-            atomicExch(err, static_cast<unsigned>(STATUS_TIMEOUT));
-            return;
-        } else if ((idle & 63) == 63 && *reinterpret_cast<volatile int *>(&ctl->dead)) {
-            return;
+            for (int ks = 0; ks < AR_KEYS / 16; ++ks)
+                tc_mma_ta(tm_o, tm_p + (n & 1) * (AR_KEYS / 2) + ks * 8, v + ks * (2048 >> 4), SHAPE, i > 0 || ks > 0);
+            tc_commit(&ctl->o_done[n & 1]);
+            tc_commit(&ctl->v_empty[n % VST]);
         }
     }
 }
 
 // ------------------------------------------------------------------ q
-// Three warps, an item ahead of the others: q of every copy's rows, and what
+// Two warps, an item ahead of the others: q of every copy's rows, and what
 // the new tokens see.  For an e4m3 cache each row by a power of two into f16's
 // range.
 template <typename T, typename C, int D, int COLS>
@@ -395,10 +371,10 @@ __device__ void rows_prepare(const AttParams &p, Cursor c, char *smem, RowsCtl *
         const int place = item & 1, row0 = c.row_tile * COLS, live = min(COLS, p.rows - row0);
         char *qs = smem + S::Q_AT + place * S::TILE;
         if (item >= 2 && !rows_wait(ctl, &ctl->q_empty[place], ((item >> 1) - 1) & 1, err)) return;
-        for (int t = lt; t < p.w.T; t += 96)
+        for (int t = lt; t < p.w.T; t += AR_PREPARE)
             ctl->sees[place][t] = t < c.s.fresh ? visible_mask(p.parent ? p.parent + static_cast<int64_t>(c.b) * p.w.T : nullptr, t) : 0ull;
-        // rows at a time, 6 or 12; six loads of a thread on their way together (one by one they took 6 us)
-        constexpr int CH = D / 8, STEP = 96 / CH, AHEAD = 6;
+        // rows at a time, 4 or 8; four loads of a thread on their way together (one by one they took 6 us)
+        constexpr int CH = D / 8, STEP = AR_PREPARE / CH, AHEAD = 4;
         const int ch = lt % CH;
 #pragma unroll 1
         for (int b0 = 0; b0 < COLS; b0 += AHEAD * STEP) {
@@ -460,6 +436,9 @@ __device__ __forceinline__ void store32(void *at, const uint32_t (&y)[8])
 
 template <int N> __device__ __forceinline__ void rows_sync() { asm volatile("bar.sync 1, %0;" ::"n"(N) : "memory"); }
 
+// The two warps that have the same rows.
+__device__ __forceinline__ void pair_sync(int w) { asm volatile("bar.sync %0, 64;" ::"r"(2 + w) : "memory"); }
+
 // COLS: rows of a copy, and its keys of a tile; a thread takes these, or half of them.
 template <typename T, typename C, int D, int COLS>
 __device__ void rows_softmax(const AttParams &p, Cursor c, char *smem, RowsCtl *ctl, unsigned *err, int tid)
@@ -472,7 +451,7 @@ __device__ void rows_softmax(const AttParams &p, Cursor c, char *smem, RowsCtl *
     const int half = tid / AR_ROWS, lane_row = tid % AR_ROWS, copy = lane_row / COLS, r = lane_row % COLS;
     const uint32_t quarter = static_cast<uint32_t>(lane_row & ~31) << 16;
     const uint32_t tm_s = ctl->tmem + quarter + copy * COLS + half * KEYS,
-                   tm_p = ctl->tmem + quarter + W::P_AT + copy * (COLS / 2) + half * 64, tm_o = ctl->tmem + quarter + W::O_AT;
+                   tm_p = ctl->tmem + quarter + 256 + copy * (COLS / 2) + half * (KEYS / 2), tm_o = ctl->tmem + quarter + 384;
     const long long begin = c.at;
     // the keys of other copies never get a probability
     if (COPIES > 1) {
@@ -504,8 +483,8 @@ __device__ void rows_softmax(const AttParams &p, Cursor c, char *smem, RowsCtl *
             if (mine && token < c.s.fresh) see = ctl->sees[place][token];
             if (S::WIDEN) factor *= exp2f(-static_cast<float>(ctl->q_power[place][lane_row]));
             const bool works = __any_sync(0xffffffffu, mine);
-            for (int tile = t0; ok && tile < t1; ++tile, ++n) {
-                if (!(ok = rows_wait(ctl, &ctl->s_full[n & 1], (n >> 1) & 1, err))) break;
+            for (int tile = t0; tile < t1; ++tile, ++n) {  // to its end even after a wait gave up: the halves meet at each tile
+                ok = ok && rows_wait(ctl, &ctl->s_full[n & 1], (n >> 1) & 1, err);
                 tc_fence_after();
                 __syncwarp();
                 if (works) {
@@ -532,21 +511,27 @@ __device__ void rows_softmax(const AttParams &p, Cursor c, char *smem, RowsCtl *
 #pragma unroll
                     for (int i = 1; i + 1 < KEYS; i += 2) top = fmax3(top, x[i], x[i + 1]);
                     top = fmaxf(top, x[KEYS - 1]);
+                    if (HALVES == 2) {  // the maximum of both halves, by the two warps that have these rows
+                        pair_sync(lane_row / 32);  // the last tile's has been read
+                        ctl->top[tid] = top;
+                        pair_sync(lane_row / 32);
+                        top = fmaxf(top, ctl->top[tid ^ AR_ROWS]);
+                    }
                     if (tile == t0) {
                         m = fmaxf(m, top);
                     } else if (__any_sync(0xffffffffu, top > m + AR_GROWTH || (m == -CUDART_INF_F && top > m))) {
                         const float grown = fmaxf(m, top), a = grown == -CUDART_INF_F ? 0.0f : fast_exp2(m - grown);
                         m = grown;
                         l *= a;
-                        if (!(ok = rows_wait(ctl, &ctl->o_done[(n - 1) & 1], ((n - 1) >> 1) & 1, err))) break;
+                        ok = ok && rows_wait(ctl, &ctl->o_done[(n - 1) & 1], ((n - 1) >> 1) & 1, err);
                         tc_fence_after();
 #pragma unroll 1
-                        for (int i = 0; i < D; i += 16) {
+                        for (int i = half * (D / HALVES); i < (half + 1) * (D / HALVES); i += 16) {
                             uint32_t y[16];
-                            tc_ld16(y, tm_o + half * 128 + i);
+                            tc_ld16(y, tm_o + i);
 #pragma unroll
                             for (int k = 0; k < 16; ++k) y[k] = __float_as_uint(__uint_as_float(y[k]) * a);
-                            tc_st16(tm_o + half * 128 + i, y);
+                            tc_st16(tm_o + i, y);
                         }
                     }
                     const float base = m == -CUDART_INF_F ? 0.0f : m;
@@ -561,15 +546,15 @@ __device__ void rows_softmax(const AttParams &p, Cursor c, char *smem, RowsCtl *
                         pk[i / 2] = pack_mma<M>(a, b);
                     }
                     l += s0 + s1;
-                    // its place was read by the product two tiles ago (where it is the scores', they have waited for that)
-                    if (HALVES == 1 && n >= 2 && !(ok = rows_wait(ctl, &ctl->o_done[n & 1], ((n - 2) >> 1) & 1, err))) break;
+                    // its place was read by the product two tiles ago
+                    if (n >= 2) ok = ok && rows_wait(ctl, &ctl->o_done[n & 1], ((n - 2) >> 1) & 1, err);
                     tc_fence_after();
                     if (KEYS == 32) {
-                        tc_st16(tm_p + (n & 1) * W::P_STAGE, *reinterpret_cast<uint32_t(*)[16]>(pk));
+                        tc_st16(tm_p + (n & 1) * (AR_KEYS / 2), *reinterpret_cast<uint32_t(*)[16]>(pk));
                     } else {
 #pragma unroll
                         for (int i = 0; i < KEYS / 2; i += 32)
-                            tc_st32(tm_p + (n & 1) * W::P_STAGE + i, *reinterpret_cast<uint32_t(*)[32]>(pk + i));
+                            tc_st32(tm_p + (n & 1) * (AR_KEYS / 2) + i, *reinterpret_cast<uint32_t(*)[32]>(pk + i));
                     }
                     tc_wait_st();
                 }
@@ -606,9 +591,8 @@ __device__ void rows_softmax(const AttParams &p, Cursor c, char *smem, RowsCtl *
 #pragma unroll
             for (int k = 0; k < COPIES * HALVES; ++k) all_m = fmaxf(all_m, merge->ms[k * COLS + r]);
         }
-        const float base = all_m == -CUDART_INF_F ? 0.0f : all_m, mine_a = l == 0.0f ? 0.0f : fast_exp2(m - base);
-        float other_a = 0.0f;  // of the other half's O
-        if (HALVES == 2 && tiles && merge->ls[tid ^ AR_ROWS] != 0.0f) other_a = fast_exp2(merge->ms[tid ^ AR_ROWS] - base);
+        const float base = all_m == -CUDART_INF_F ? 0.0f : all_m, of_pair = l + (HALVES == 2 && tiles ? merge->ls[tid ^ AR_ROWS] : 0.0f),
+                    mine_a = of_pair == 0.0f ? 0.0f : fast_exp2(m - base);
         if (tiles) {
 #pragma unroll
             for (int k = 0; k < COPIES * HALVES; ++k) {
@@ -632,21 +616,16 @@ __device__ void rows_softmax(const AttParams &p, Cursor c, char *smem, RowsCtl *
             }
         }
 #pragma unroll 1
-        for (int d0 = half * (D / 2); d0 < (HALVES == 2 ? (half + 1) * (D / 2) : D); d0 += 32) {
-            // each 32 columns are put together by another copy; of the halves each takes half the columns, of both O
+        for (int d0 = half * (D / HALVES); d0 < (half + 1) * (D / HALVES); d0 += 32) {
+            // each 32 columns are put together by another copy; of the halves each takes half the columns
             const int keeper = (d0 >> 5) % COPIES;
             float x[32];
             __syncwarp();
             if (tiles && !stop) {
                 uint32_t y[32];
-                tc_ld32(y, tm_o + half * 128 + d0);
+                tc_ld32(y, tm_o + d0);
 #pragma unroll
                 for (int k = 0; k < 32; ++k) x[k] = mine_a == 0.0f ? 0.0f : __uint_as_float(y[k]) * mine_a;
-                if constexpr (HALVES == 2) {
-                    tc_ld32(y, tm_o + (half ^ 1) * 128 + d0);
-#pragma unroll
-                    for (int k = 0; k < 32; ++k) x[k] += other_a == 0.0f ? 0.0f : __uint_as_float(y[k]) * other_a;
-                }
             } else {
 #pragma unroll
                 for (int k = 0; k < 32; ++k) x[k] = 0.0f;
@@ -730,8 +709,7 @@ __global__ void __launch_bounds__(RowsWarps<COLS>::THREADS, 1)
 {
     using S = RowsShape<C, D>;
     using W = RowsWarps<COLS>;
-    extern __shared__ char raw_smem[];
-    char *smem = raw_smem + ((1024u - (smem_u32(raw_smem) & 1023u)) & 1023u);
+    extern __shared__ __align__(1024) char smem[];  // the swizzle's rows of 128 bytes come in groups of eight
     RowsCtl *ctl = reinterpret_cast<RowsCtl *>(smem + S::CTL_AT);
     const int tid = threadIdx.x, warp = tid >> 5;
     unsigned *err = p.error;
@@ -748,10 +726,10 @@ __global__ void __launch_bounds__(RowsWarps<COLS>::THREADS, 1)
             mbar_init(&ctl->o_done[i], 1);
         }
         for (int i = 0; i < 2; ++i) {
-            mbar_init(&ctl->q_full[i], 96);
+            mbar_init(&ctl->q_full[i], AR_PREPARE);
+            mbar_init(&ctl->spare[i], 1);
             mbar_init(&ctl->q_empty[i], W::SOFTMAX);
         }
-        mbar_init(&ctl->spare, 1);
         for (int i = 0; i < AR_ITEMS; ++i) ctl->odd[i] = 0, ctl->bad[i] = 0;
         ctl->dead = ctl->stop = 0;
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
@@ -768,7 +746,7 @@ __global__ void __launch_bounds__(RowsWarps<COLS>::THREADS, 1)
         return;
     }
     // registers: launched with 128 a thread, 4 x 128 = 208 + 80 + 2 x 112, or with 96, 5 x 96 = 2 x 128 + 80 + 2 x 72 and
-    // 2 x 120 + 3 x 80 (more for the widening)
+    // 2 x 120 + 3 x 80 (more for the widening); what spills comes back from the L2, shared memory has most of the L1
     const int role = warp - W::SOFTMAX / 32;
     if (role < 0) {
         if (W::HALVES == 1)
@@ -780,15 +758,18 @@ __global__ void __launch_bounds__(RowsWarps<COLS>::THREADS, 1)
         rows_softmax<T, C, D, COLS>(p, c, smem, ctl, err, tid);
     } else if (role < 4) {
         asm volatile("setmaxnreg.dec.sync.aligned.u32 80;");
-        if (tid == W::SOFTMAX) {
-            rows_multiply<T, C, D, COLS>(p, c, smem, ctl, err);
+        if (role < 2 && (tid & 31) == 0) {
+            if (role == 0)
+                rows_scores<T, C, D>(p, c, smem, ctl, err);
+            else
+                rows_outputs<T, C, D>(p, c, smem, ctl, err);
             if (*reinterpret_cast<volatile int *>(&ctl->dead)) {  // let what was issued end
-                tc_commit(&ctl->spare);
-                mbar_wait(&ctl->spare, 0);
+                tc_commit(&ctl->spare[role]);
+                mbar_wait(&ctl->spare[role], 0);
             }
         }
         __syncwarp();
-        if (role > 0) rows_prepare<T, C, D, COLS>(p, c, smem, ctl, err, tid - W::SOFTMAX - 32);
+        if (role >= 2) rows_prepare<T, C, D, COLS>(p, c, smem, ctl, err, tid - W::SOFTMAX - 64);
     } else {
         if (W::HALVES == 1)
             asm volatile("setmaxnreg.dec.sync.aligned.u32 112;");
@@ -811,7 +792,7 @@ template <typename T, typename C, int D, int COLS>
 static cudaError_t launch_cols(AttParams p, const KvLaunch &L, cudaStream_t st)
 {
     using S = RowsShape<C, D>;
-    constexpr int SMEM = S::CTL_AT + static_cast<int>(sizeof(RowsCtl)) + 1024;
+    constexpr int SMEM = S::CTL_AT + static_cast<int>(sizeof(RowsCtl));
     static_assert(SMEM <= 232448, "shared memory of a block");
     auto kernel = attention_rows_kernel<T, C, D, COLS>;
     cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, SMEM);
