@@ -481,8 +481,15 @@ spv_status spv_rope_append(const void *q, const void *k, const void *v, spv_dtyp
  *   1 <= T <= SPV_MAX_NEW_TOKENS; q_heads / kv_heads <= SPV_MAX_GROUP
  *   lse          [B, T, q_heads] fp32, optional; row_status [B], optional
  *   workspace    >= spv_attention_workspace_bytes(...) bytes, 256-byte
- *                aligned, zero-filled once, as for spv_verify_chain; it does
- *                not depend on the cached lengths
+ *                aligned; it does not depend on the cached lengths.  Only its
+ *                error word is kept from call to call: zero-fill it once, and
+ *                again after a failed call; calls of any shapes may follow one
+ *                another on it, calls that can overlap may not share it
+ * Two kernels: the attention, and the join of what several blocks have of one
+ * key head; like the other calls here they are launched so that their blocks
+ * may start while the kernel before them in the stream ends, and wait for its
+ * results before they read anything.  A bounded wait that gives up records SPV_ERR_TIMEOUT in the workspace's
+ * error word and leaves NaN in the rows that it cost.
  * Tokens t >= new_lens[b], and tree nodes whose path to the root has a parent
  * outside [0, node): rows that see nothing.  Bad sequences: out and lse NaN.
  * The result does not depend on the order in which the GPU runs the blocks.
@@ -512,6 +519,7 @@ size_t spv_attention_workspace_bytes(int B, int T, int q_heads, int kv_heads, in
  *   row_status   [B] optional
  * Bad sequences (also: accept_count outside [-1, T - 1], a counted node
  * outside [0, T), ctx + new > mass_stride): nothing is written; slots of a bad page: neither.
+ * A bounded wait that gives up: SPV_ERR_TIMEOUT in row_status of the sequences that it cost.
  */
 spv_status spv_attention_mass(const void *q, spv_dtype dtype, int B, int T, int q_heads, const float *lse,
                               const spv_kv_cache *cache, const int32_t *page_table, int max_pages,

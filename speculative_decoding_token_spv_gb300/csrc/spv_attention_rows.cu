@@ -23,9 +23,10 @@
 // 2,850 cycles a tile where its K and V take 2,300 (draft trees: 110 us).
 //
 // What bounds it, and what it takes: 40 rows of 64 sequences of up to 8,191
-// slots, K and V 1.37 GB, 232 us (5.9 TB/s, 87% of a copy's rate; 206 with no
-// start, ends and joins); 84 rows of 32 sequences of up to 4,099 slots, 353 MB,
-// 94 us: exponentials, 1,800 cycles a tile, and the ends of items.
+// slots, K and V 1.37 GB, 232 us (5.9 TB/s, 87% of a copy's rate: reading K and
+// V, then starts, ends of items and joins); 84 rows of 32 sequences of up to
+// 4,099 slots, 353 MB, 94 us: exponentials, 1,800 of a tile's 2,450 cycles, and
+// the ends of items.
 //
 // Every wait is bounded; one that gives up records SPV_ERR_TIMEOUT in the
 // workspace, ends the block in order and leaves NaN in what it had to write.
