@@ -7,7 +7,9 @@
 // a block gets fewer rows than it has warps, its warps share out the pieces of
 // a row.  M = max m_i, l = sum l_i 2^(m_i - M), o likewise, always in the
 // order of the pieces.  All loads come from the L2, about a microsecond away
-// for the far half of it: each warp has eight rows under way.
+// for the far half of it: each warp has eight rows under way.  (Joined by the
+// last block to finish an item, the attention of 40 rows over 64 sequences of up
+// to 8,191 slots took 257 us where it took 245 like this.)
 #include "spv_attention.cuh"
 
 namespace spv {

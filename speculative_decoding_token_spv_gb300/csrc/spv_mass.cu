@@ -10,6 +10,10 @@
 // cores, whose lanes share a key's column, masks, exchanges and fragments came
 // to 750 instructions per 16 keys: 329 us for the case below.)
 //
+// What bounds it is reading K, the old weights and writing the new ones once: 64
+// sequences of up to 8,191 slots, 8 key heads of 8 query heads, D = 128, bf16,
+// 704 MB: 128 us, 5.5 TB/s, 81% of a copy's rate.
+//
 // One block an SM has an equal range of all tiles (Work, Cursor).  Two groups
 // of four loader warps take turns at the tiles, gathering K through the page
 // table with asynchronous copies (e4m3 is widened to f16 by the thread that

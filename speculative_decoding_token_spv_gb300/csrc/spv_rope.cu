@@ -8,6 +8,12 @@
 // registers -- and walks over the heads.  The angle is the integer product of
 // the position with a 64-bit fraction of a turn: the wrap of the product is the
 // reduction to one turn, exact at any position, with no 64-bit floating point.
+//
+// What bounds it is reading q, k, v and writing q, K, V once.  8 prompts of up
+// to 2,011 tokens, 32 + 8 heads of 128, f16, 395 MB: 64.6 us, 6.1 TB/s, 90% of a
+// copy's rate (the next token's elements are asked for while one is worked on;
+// without that 88 us).  One token of one sequence: 2.8 us, of which the angle's
+// sine, the page lookup and two trips to memory are a chain.
 #include "spv_kv.cuh"
 
 namespace spv {
@@ -267,8 +273,9 @@ __global__ void __launch_bounds__(ROPE_THREADS) rope_kernel(const RopeParams p)
 
 template <int MODE, typename T, typename C> static cudaError_t launch_mode(const RopeParams &p, cudaStream_t st)
 {
-    // four tokens a block once that still gives every SM eight blocks (at 8 prompts of up to 2,011 tokens, 40 heads of
-    // 128, f16: measured as below); fewer tokens are spread over as many SMs as there are
+    // four tokens a block once that still gives every SM eight blocks: 8 prompts of up to 2,011 tokens take 64.6 us, with
+    // one token a block 70.2; fewer tokens are spread over as many SMs as there are: the verify tokens of 64 sequences
+    // take 5.5 us, with four a block 9.8
     const int smem = p.half * static_cast<int>(sizeof(float2));
     if (static_cast<int64_t>(p.B) * p.T >= 8 * 152 * ROPE_TOKENS)
         return launch_chained(rope_kernel<MODE, ROPE_TOKENS, T, C>, dim3(p.B * ((p.T + ROPE_TOKENS - 1) / ROPE_TOKENS)),
