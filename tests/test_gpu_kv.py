@@ -642,3 +642,19 @@ def test_attention_scale(spv, scale, T, kv):
     a = Layer(spv, 16, [300, 45], None, T, 8, 2, 64, 16, dtype="bf16", kv=kv)
     a.scale = scale
     a.check(a.attend(scale=scale))
+
+
+@pytest.mark.parametrize("T, Hq, Hkv", [(24, 8, 2), (64, 6, 2), (17, 16, 2), (5, 8, 2)])
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("kv", ["bf16", "e4m3"])
+def test_attention_growing_maximum(spv, T, Hq, Hkv, D, kv):
+    """Scores that grow along the cache, more so in one half of every 128 slots: sums are rescaled on the way."""
+    ctx, page = [900, 131, 0], 16
+    a = Layer(spv, 21, ctx, None, T, Hq, Hkv, D, page, dtype="bf16", kv=kv)
+    gain = torch.ones(a.k.shape[:2])
+    for b, n in enumerate(ctx):
+        for j in range(n + T):
+            gain[a.table[b, j // page].long(), j % page] = (0.1 + 5.0 * j / 1000) * (1.4 if j % 128 >= 64 else 1.0)
+    a.k = (a.k.float() * gain[:, :, None, None]).to(DTYPES[kv])
+    a.cache.k.copy_(a.k)
+    a.check(a.attend())
