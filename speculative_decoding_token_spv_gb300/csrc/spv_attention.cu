@@ -203,7 +203,9 @@ __global__ void __launch_bounds__(ATT_THREADS, AttShape<C, D, MT>::BLOCKS_PER_SM
                     }
                 }
                 // m follows the maximum only where it has grown by more than 2^8 (or begins): p stays below 2^8, the 32-bit
-                // sums lose nothing, and o is seldom rescaled -- with every growth it was in nearly every slice
+                // sums lose nothing, and o is seldom rescaled -- with every growth it was in nearly every slice.  (The growth as a
+                // difference: m + 8 may round up to the next score where these are 16 apart, which would then be 2^16, more than
+                // an f16 holds.)
                 float top[2];
                 bool moved = false;
 #pragma unroll
@@ -212,7 +214,7 @@ __global__ void __launch_bounds__(ATT_THREADS, AttShape<C, D, MT>::BLOCKS_PER_SM
                     x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 1));
                     x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 2));
                     top[i] = x * factor[mt][i];
-                    moved |= top[i] > m[mt][i] + ATT_GROWTH;  // m minus infinity: any score
+                    moved |= top[i] - m[mt][i] > ATT_GROWTH;  // m minus infinity: any score
                 }
                 if (__any_sync(0xffffffffu, moved)) {
 #pragma unroll

@@ -524,7 +524,7 @@ __device__ void rows_softmax(const AttParams &p, Cursor c, char *smem, RowsCtl *
                     }
                     if (tile == t0) {
                         m = fmaxf(m, top);
-                    } else if (__any_sync(0xffffffffu, top > m + AR_GROWTH || (m == -CUDART_INF_F && top > m))) {
+                    } else if (__any_sync(0xffffffffu, top - m > AR_GROWTH)) {  // as a difference: m + 8 may round up to a score 16 above
                         const float grown = fmaxf(m, top), a = grown == -CUDART_INF_F ? 0.0f : fast_exp2(m - grown);
                         m = grown;
                         l *= a;

@@ -1,0 +1,67 @@
+"""GPU tests of the calls around the verify step where a plain computation in
+fewer bits goes wrong: scores and weights at the ends of their types."""
+import math
+
+import pytest
+import torch
+
+from kv_reference import DTYPES, half_step
+from test_gpu_kv import i32, spv  # noqa: F401  (spv: the fixture)
+
+pytestmark = pytest.mark.gpu
+
+POWERS_OF_TWO = 0.6931472  # as a float32, times log2(e) it is 1: scores are powers of two, exactly
+
+
+def _attend(spv, q, k, v, ctx, page, k_scale=None, v_scale=None, B=456):
+    """The same sequence B times, on the same pages, so that each block has whole sequences and takes their keys one after
+    another: q [T, Hq, D], k and v [slots, Hkv, D] on the GPU."""
+    pages = -(-k.shape[0] // page)
+    pools = []
+    for x in (k, v):
+        pool = torch.zeros(pages * page, *x.shape[1:], dtype=x.dtype, device="cuda")
+        pool.view(torch.int8)[: x.shape[0]] = x.view(torch.int8)
+        pools.append(pool.view(pages, page, *x.shape[1:]))
+    table = torch.arange(pages, dtype=torch.int32, device="cuda").expand(B, pages).contiguous()
+    got = spv.spv_paged_attention(q.expand(B, *q.shape).contiguous(), spv.KVCache(*pools, k_scale, v_scale), table,
+                                  i32([ctx] * B), scale=POWERS_OF_TWO, want_lse=True)
+    torch.cuda.synchronize()
+    assert (got["row_status"] == 0).all()
+    return got["out"].cpu().double(), got["lse"].cpu().double()
+
+
+# rows of a key head: the warp kernel, and each layout of the rows kernel
+ROWS = [(1, 4), (5, 4), (12, 4), (24, 4), (40, 4)]
+
+
+@pytest.mark.parametrize("T, G", ROWS)
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("dtype, kv", [("f16", "f16"), ("bf16", "e4m3"), ("bf16", "bf16")])
+def test_attention_scores_beyond_2_to_27(spv, T, G, D, dtype, kv):
+    """Scores whose 32-bit neighbours are 16 powers of two apart: 2^27 + 16, then 2^27 + 32 for the later half.  The
+    second ones have weight 1, the first 2^-16; every sum is exact but for the weights' rounding and the result's."""
+    ctx = 600
+    n = ctx + T
+    late = (torch.arange(n, device="cuda") >= 300).float()
+    q = torch.zeros(T, G, D, device="cuda")
+    k = torch.zeros(n, 1, D, device="cuda")
+    q[..., 0], q[..., 1] = 2.0 ** 15, 1.0
+    ks = None
+    if kv == "e4m3":  # 16 (2^15 2^8 + 1 or 2)
+        k[:, 0, 0], k[:, 0, 1] = 2.0 ** 8, 1.0 + late
+        ks = torch.full((1,), 16.0, device="cuda")
+    else:             # 2^15 2^12 + 16 or 32
+        k[:, 0, 0], k[:, 0, 1] = 2.0 ** 12, 16.0 + 16.0 * late
+    v = torch.randn(n, 1, D, generator=torch.Generator(device="cuda").manual_seed(1), device="cuda").to(DTYPES[kv])
+    vs = torch.ones(1, device="cuda") if ks is not None else None
+    out, lse = _attend(spv, q.to(DTYPES[dtype]), k.to(DTYPES[kv]), v, ctx, 16, ks, vs)
+    x = v[:, 0].float().cpu().double()
+    w = torch.where(late.cpu() > 0, 1.0, 2.0 ** -16).double()
+    for t in range(T):
+        seen = w[: ctx + t + 1, None] / w[: ctx + t + 1].sum()
+        want, size = (seen * x[: ctx + t + 1]).sum(0), (seen * x[: ctx + t + 1].abs()).sum(0)
+        # weights equal to a power of two or its rounding; result rounded once
+        tol = 2 * half_step(DTYPES[dtype]) * size + 2.0 ** -24
+        assert ((out[:, t] - want).abs() <= tol).all()
+        z = math.log(2.0) * (2.0 ** 27 + 32 + math.log2(w[: ctx + t + 1].sum().item()))
+        assert ((lse[:, t] - z).abs() <= z * 2.0 ** -22).all()
