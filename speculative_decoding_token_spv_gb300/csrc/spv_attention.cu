@@ -30,7 +30,6 @@ constexpr int ATT_WARPS = 4;
 constexpr int ATT_THREADS = 32 * ATT_WARPS;
 constexpr int ATT_KEYS = 16 * ATT_WARPS;  // keys of a tile: a slice for each warp
 constexpr int ATT_MAX_ROWS = 32;
-constexpr float ATT_GROWTH = 8.0f;  // growth of a maximum (powers of two) that the sums wait for
 
 // Workspace: header, the blocks' split items, their pieces.
 constexpr size_t ATT_PARTS_AT = WS_HEADER + split_bytes(ATT_MAX_BLOCKS);
@@ -202,10 +201,10 @@ __global__ void __launch_bounds__(ATT_THREADS, AttShape<C, D, MT>::BLOCKS_PER_SM
                         }
                     }
                 }
-                // m follows the maximum only where it has grown by more than 2^8 (or begins): p stays below 2^8, the 32-bit
-                // sums lose nothing, and o is seldom rescaled -- with every growth it was in nearly every slice.  (The growth as a
-                // difference: m + 8 may round up to the next score where these are 16 apart, which would then be 2^16, more than
-                // an f16 holds.)
+                // m follows the maximum only where it has grown by more than 2^LAG (or begins): p stays below 2^(LAG + UP), the
+                // 32-bit sums lose nothing, and o is seldom rescaled -- with every growth it was in nearly every slice.  (The
+                // growth as a difference: m + LAG may round up to the next score where these are 16 apart, which would then be
+                // 2^16, more than an f16 holds.)
                 float top[2];
                 bool moved = false;
 #pragma unroll
@@ -214,7 +213,7 @@ __global__ void __launch_bounds__(ATT_THREADS, AttShape<C, D, MT>::BLOCKS_PER_SM
                     x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 1));
                     x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 2));
                     top[i] = x * factor[mt][i];
-                    moved |= top[i] - m[mt][i] > ATT_GROWTH;  // m minus infinity: any score
+                    moved |= top[i] - m[mt][i] > Weights<M>::LAG;  // m minus infinity: any score
                 }
                 if (__any_sync(0xffffffffu, moved)) {
 #pragma unroll
@@ -232,7 +231,7 @@ __global__ void __launch_bounds__(ATT_THREADS, AttShape<C, D, MT>::BLOCKS_PER_SM
                 }
 #pragma unroll
                 for (int i = 0; i < 2; ++i) {
-                    const float base = m[mt][i] == -CUDART_INF_F ? 0.0f : m[mt][i], f = factor[mt][i];
+                    const float base = m[mt][i] == -CUDART_INF_F ? 0.0f : m[mt][i] - Weights<M>::UP, f = factor[mt][i];
 #pragma unroll
                     for (int k = 0; k < 2; ++k)
 #pragma unroll
@@ -299,7 +298,7 @@ __global__ void __launch_bounds__(ATT_THREADS, AttShape<C, D, MT>::BLOCKS_PER_SM
                 x += __shfl_xor_sync(0xffffffffu, x, 2);
                 const int r = mt * 16 + i * 8 + (lane >> 2);
                 if ((lane & 3) == 0) {
-                    ms[warp][r] = sees[r] ? m[mt][i] : -CUDART_INF_F;
+                    ms[warp][r] = sees[r] ? m[mt][i] - Weights<M>::UP : -CUDART_INF_F;  // what l and o are sums against
                     ls[warp][r] = sees[r] ? x : 0.0f;
                 }
             }

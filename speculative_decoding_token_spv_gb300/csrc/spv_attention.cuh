@@ -24,6 +24,15 @@ struct AttParams {
     float scale_log2;
 };
 
+// The weights of a product in M are 2^(s - (m - UP)), m the running maximum, which may lag the largest score by LAG: at
+// most 2^15 in f16, whose smallest value is then 2^-32 of the largest weight and not 2^-25 -- a long cache of keys below
+// that would add to the sum l, held in 32 bits, and not to the output (262,143 keys of 2^-25 beside one of 1: 2^-7 of the
+// result).  bf16 has the exponents of 32 bits.
+template <typename M> struct Weights {
+    static constexpr bool F16 = std::is_same<M, __half>::value;
+    static constexpr float UP = F16 ? 7.0f : 0.0f, LAG = F16 ? 7.0f : 8.0f;
+};
+
 template <typename T> __device__ __forceinline__ bool not_finite16(uint32_t two)
 {
     const uint32_t e = sizeof(T) == 1 ? 0 : std::is_same<T, __half>::value ? 0x7c00u : 0x7f80u;

@@ -14,7 +14,8 @@
 //     sums in 32 bits in tensor memory; two warps bring q of the next item;
 //   * four warps hold a row a thread: running maximum, exponentials, sum, P
 //     back to tensor memory.  O is only rescaled when a maximum has grown by
-//     more than 2^8, so p stays below 2^8 and the 32-bit sums lose nothing.
+//     more than 2^8 (2^7 for f16 products), so p stays below 2^8 (2^14) and the
+//     32-bit sums lose nothing.
 // With 64 rows or fewer the rows stand in tensor memory two or four times,
 // each copy taking half or a quarter of every tile's keys (its P is zero
 // elsewhere): all four warps work whatever the number of rows, and the
@@ -40,7 +41,6 @@ constexpr int AR_KEYS = 128;
 constexpr int AR_ROWS = 128;
 constexpr int AR_PREPARE = 64;        // threads that bring q
 constexpr int AR_ITEMS = 16;          // items whose flags can be in use at once
-constexpr float AR_GROWTH = 8.0f;     // growth of a maximum (powers of two) that O waits for
 
 template <typename C, int D> struct RowsShape {
     static constexpr bool WIDEN = sizeof(C) == 1;
@@ -524,7 +524,7 @@ __device__ void rows_softmax(const AttParams &p, Cursor c, char *smem, RowsCtl *
                     }
                     if (tile == t0) {
                         m = fmaxf(m, top);
-                    } else if (__any_sync(0xffffffffu, top - m > AR_GROWTH)) {  // as a difference: m + 8 may round up to a score 16 above
+                    } else if (__any_sync(0xffffffffu, top - m > Weights<M>::LAG)) {  // as a difference: m + 8 may round up to a score 16 above
                         const float grown = fmaxf(m, top), a = grown == -CUDART_INF_F ? 0.0f : fast_exp2(m - grown);
                         m = grown;
                         l *= a;
@@ -539,7 +539,7 @@ __device__ void rows_softmax(const AttParams &p, Cursor c, char *smem, RowsCtl *
                             tc_st16(tm_o + i, y);
                         }
                     }
-                    const float base = m == -CUDART_INF_F ? 0.0f : m;
+                    const float base = m == -CUDART_INF_F ? 0.0f : m - Weights<M>::UP;
                     float s0 = 0.0f, s1 = 0.0f;
                     uint32_t pk[KEYS / 2];
 #pragma unroll
@@ -572,6 +572,7 @@ __device__ void rows_softmax(const AttParams &p, Cursor c, char *smem, RowsCtl *
             any_bad |= *reinterpret_cast<volatile int *>(&ctl->bad[item_flags(item)]) != 0;
             rows_sync<W::SOFTMAX>();  // all have read them, and all scores
         }
+        m -= Weights<M>::UP;  // what l and O are sums against
         if (see == 0) {
             m = -CUDART_INF_F;
             l = 0.0f;

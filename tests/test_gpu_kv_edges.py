@@ -65,3 +65,28 @@ def test_attention_scores_beyond_2_to_27(spv, T, G, D, dtype, kv):
         assert ((out[:, t] - want).abs() <= tol).all()
         z = math.log(2.0) * (2.0 ** 27 + 32 + math.log2(w[: ctx + t + 1].sum().item()))
         assert ((lse[:, t] - z).abs() <= z * 2.0 ** -22).all()
+
+
+@pytest.mark.parametrize("T, G", ROWS)
+@pytest.mark.parametrize("dtype, kv", [("f16", "f16"), ("bf16", "e4m3"), ("f16", "e4m3"), ("bf16", "bf16")])
+@pytest.mark.parametrize("peak", [0, 170_001, 262_143])
+def test_attention_peak_over_a_long_flat_background(spv, T, G, dtype, kv, peak):
+    """262,143 keys each 2^-25 of the largest: together 2^-7 of the result, though each is below what f16 holds."""
+    ctx, D = 262_144, 64
+    n = ctx + T
+    q = torch.zeros(T, G, D, device="cuda")
+    q[..., 0] = 1.0
+    k = torch.full((n, 1, D), 0.0, device="cuda")
+    k[:, 0, 0] = -12.0
+    k[peak, 0, 0] = 13.0
+    v = torch.full((n, 1, D), -1.0, device="cuda")
+    v[peak] = 1.0
+    one = torch.ones(1, device="cuda") if kv == "e4m3" else None
+    out, lse = _attend(spv, q.to(DTYPES[dtype]), k.to(DTYPES[kv]), v.to(DTYPES[kv]), ctx, 64, one, one)
+    for t in range(T):
+        rest = (ctx + t) * 2.0 ** -25
+        want = (1.0 - rest) / (1.0 + rest)
+        # every product and sum of these powers of two is exact up to the 32-bit sums' roundings
+        assert ((out[:, t] - want).abs() <= half_step(DTYPES[dtype]) + 2.0 ** -15).all()
+        z = math.log(2.0) * (13.0 + math.log2(1.0 + rest))
+        assert ((lse[:, t] - z).abs() <= z * 2.0 ** -20).all()
