@@ -11,6 +11,7 @@ not on a CUDA device.
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
 
 import torch
@@ -136,6 +137,18 @@ def _stream(stream, device):
     if stream is None:
         stream = torch.cuda.current_stream(device)
     return stream.cuda_stream
+
+
+def _on_its_stream(call):
+    """With ``stream`` given, the call runs with it as torch's current stream: what it allocates and clears belongs to
+    that stream, in order with the kernels that use it, and goes back to it."""
+    @functools.wraps(call)
+    def on_its_stream(*args, stream=None, **kw):
+        if stream is None:
+            return call(*args, **kw)
+        with torch.cuda.stream(stream):
+            return call(*args, stream=stream, **kw)
+    return on_its_stream
 
 
 def _check(status: int, what: str):

@@ -3,7 +3,9 @@ spv_rope_append, spv_paged_attention, spv_attention_mass and spv_kv_evict.
 
 Like the verify calls: torch CUDA tensors in, work on torch's current stream
 (or ``stream``), outputs allocated when the caller passes none in ``out``, no
-CPU fallback.  A cache is two 4-D pools [pages, page_size, kv_heads, head_dim];
+CPU fallback.  What a call with ``stream`` allocates belongs to that stream, as
+under ``torch.cuda.stream(stream)``; tensors that come from another one are in
+order only if the caller has made them so.  A cache is two 4-D pools [pages, page_size, kv_heads, head_dim];
 any strides will do as long as a row's elements are contiguous, so
 ``pool.transpose(1, 2)`` of a [pages, kv_heads, page_size, head_dim] tensor or
 a slice of a joint K/V tensor can be passed.
@@ -17,7 +19,7 @@ from dataclasses import dataclass
 
 import torch
 
-from . import SPV_BF16, SPV_E4M3, SPV_F16, SpvError, _check, _stream, load_library, new_workspace
+from . import SPV_BF16, SPV_E4M3, SPV_F16, SpvError, _check, _on_its_stream, _stream, load_library, new_workspace
 
 ROPE_SCALINGS = {"plain": 0, "linear": 1, "base": 2, "by_parts": 3}
 _ACTIVATIONS = {torch.bfloat16: SPV_BF16, torch.float16: SPV_F16}
@@ -176,6 +178,7 @@ def spv_rope_frequencies(rotary_dim: int, base: float = 10000.0, *, scaling: str
     return host.to(device)
 
 
+@_on_its_stream
 def spv_rope_append(q, k, v, cache: KVCache, page_table, ctx_lens, freqs, *, interleaved: bool = False,
                     mscale: float = 1.0, positions=None, new_lens=None, slot_pos=None, out=None,
                     want_status: bool = True, stream=None) -> dict:
@@ -233,6 +236,7 @@ def spv_attention_workspace_bytes(B: int, T: int, q_heads: int, kv_heads: int, h
     return load_library().spv_attention_workspace_bytes(B, T, q_heads, kv_heads, head_dim)
 
 
+@_on_its_stream
 def spv_paged_attention(q, cache: KVCache, page_table, ctx_lens, *, new_lens=None, parent=None, scale=None,
                         workspace=None, out=None, want_lse: bool = False, want_status: bool = True,
                         stream=None) -> dict:
@@ -261,6 +265,7 @@ def spv_paged_attention(q, cache: KVCache, page_table, ctx_lens, *, new_lens=Non
     return out
 
 
+@_on_its_stream
 def spv_attention_mass(q, lse, cache: KVCache, page_table, ctx_lens, accept_count, *, nodes=None, new_lens=None,
                        parent=None, scale=None, decay: float = 1.0, mass_in=None, out=None,
                        want_status: bool = True, stream=None) -> dict:
@@ -295,6 +300,7 @@ def spv_attention_mass(q, lse, cache: KVCache, page_table, ctx_lens, accept_coun
     return out
 
 
+@_on_its_stream
 def spv_kv_evict(cache: KVCache, page_table, lens, mass, budget: int, *, pos=None, sinks: int = 0, recent: int = 0,
                  out=None, want_status: bool = True, stream=None) -> dict:
     """Cuts every sequence of more than ``budget`` slots back to it, in place

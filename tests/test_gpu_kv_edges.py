@@ -1,12 +1,13 @@
 """GPU tests of the calls around the verify step where a plain computation in
-fewer bits goes wrong: scores and weights at the ends of their types."""
+fewer bits goes wrong -- scores and weights at the ends of their types -- and
+on streams of their own."""
 import math
 
 import pytest
 import torch
 
 from kv_reference import DTYPES, half_step
-from test_gpu_kv import i32, spv  # noqa: F401  (spv: the fixture)
+from test_gpu_kv import Layer, i32, spv  # noqa: F401  (spv: the fixture)
 
 pytestmark = pytest.mark.gpu
 
@@ -90,3 +91,33 @@ def test_attention_peak_over_a_long_flat_background(spv, T, G, dtype, kv, peak):
         assert ((out[:, t] - want).abs() <= half_step(DTYPES[dtype]) + 2.0 ** -15).all()
         z = math.log(2.0) * (13.0 + math.log2(1.0 + rest))
         assert ((lse[:, t] - z).abs() <= z * 2.0 ** -20).all()
+
+
+@pytest.mark.parametrize("T", [1, 12])
+def test_calls_on_a_side_stream_have_buffers_of_their_own(spv, T):
+    """Without workspace and outputs, while torch's current stream is far behind: nothing of the call waits there."""
+    a = Layer(spv, 53, [5000, 700], None, T, 8, 2, 64, 16)
+    b = Layer(spv, 54, [4000], None, T, 8, 2, 64, 16)
+    inputs = [(x, x.q.cuda(), x.table.cuda(), i32(x.ctx), i32([T - 1] * x.B)) for x in (a, b)]
+
+    def run(stream):
+        res = []
+        for x, q, table, ctx, acc in inputs:  # one after another: the second call may get the first one's memory
+            got = spv.spv_paged_attention(q, x.cache, table, ctx, want_lse=True, stream=stream)
+            mass = spv.spv_attention_mass(q, got["lse"], x.cache, table, ctx, acc, stream=stream)["mass"]
+            keep = spv.spv_kv_evict(x.cache, table, ctx, mass, 8192, stream=stream)["mass"]
+            res += [got["out"], got["lse"], mass, keep[:, :, : min(x.ctx)]]
+            del got
+        return res
+
+    want = run(None)
+    torch.cuda.synchronize()
+    side = torch.cuda.Stream()
+    for _ in range(3):
+        torch.cuda._sleep(200_000_000)  # about 0.1 s of the current stream
+        got = run(side)
+        side.synchronize()
+        got = [x.cpu() for x in got]
+        for x, y in zip(want, got):
+            assert torch.equal(x.cpu(), y)
+        torch.cuda.synchronize()
