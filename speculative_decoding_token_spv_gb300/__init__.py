@@ -4,9 +4,9 @@ Thin ctypes marshalling over the C ABI in ``include/spv.h`` -- the functions
 keep the C names.  Tensors are torch CUDA tensors (contiguous, row-major);
 outputs and the zero-filled workspace are allocated with torch when the caller
 does not pass them.  Every step of the verify step runs in libspv's kernels on
-the tensors' device, on torch's current CUDA stream (or ``stream``).  There is
-no CPU fallback: calls fail loudly if libspv.so is missing or the tensors are
-not on a CUDA device.
+the tensors' device, on torch's current CUDA stream (or ``stream``, where what
+the call allocates then belongs too).  There is no CPU fallback: calls fail
+loudly if libspv.so is missing or the tensors are not on a CUDA device.
 """
 from __future__ import annotations
 
@@ -192,6 +192,7 @@ def spv_selftest_timeout(workspace: torch.Tensor, polls: int = 20000, stream=Non
     _check(st, "spv_selftest_timeout")
 
 
+@_on_its_stream
 def spv_verify_chain(target_logits, draft_logits, draft_tokens, r, sample_keys, temperature: float, *,
                      workspace=None, out=None, want_pq: bool = True, want_resid_norm: bool = False,
                      want_status: bool = True, stream=None) -> dict:
@@ -205,6 +206,7 @@ def spv_verify_chain(target_logits, draft_logits, draft_tokens, r, sample_keys, 
                          workspace, out, want_pq, want_resid_norm, want_status, stream)
 
 
+@_on_its_stream
 def spv_verify_chain_cached(target_logits, draft_logits, draft_tokens, r, sample_keys, temperature: float,
                             cache_ids, fanout, *, workspace=None, out=None, want_pq: bool = True,
                             want_resid_norm: bool = False, want_status: bool = True, stream=None) -> dict:
@@ -216,6 +218,7 @@ def spv_verify_chain_cached(target_logits, draft_logits, draft_tokens, r, sample
                          fanout, workspace, out, want_pq, want_resid_norm, want_status, stream)
 
 
+@_on_its_stream
 def spv_verify_chain_saguaro(target_logits, draft_logits, draft_tokens, r, sample_keys, temperature: float,
                              cache_ids, fanout, C: float, *, workspace=None, out=None, want_pq: bool = True,
                              want_resid_norm: bool = False, want_status: bool = True, stream=None) -> dict:
@@ -295,6 +298,7 @@ def spv_filtered_workspace_bytes(B: int, gamma: int, V: int) -> int:
     return load_library().spv_filtered_workspace_bytes(B, gamma, V)
 
 
+@_on_its_stream
 def spv_verify_chain_filtered(target_logits, draft_logits, draft_tokens, r, sample_keys, temperature: float,
                               top_k: int, top_p: float = 1.0, *, workspace=None, out=None, want_pq: bool = True,
                               want_resid_norm: bool = False, want_status: bool = True, stream=None) -> dict:
@@ -346,6 +350,7 @@ def spv_tree_workspace_bytes(B: int, N: int, V: int) -> int:
     return load_library().spv_tree_workspace_bytes(B, N, V)
 
 
+@_on_its_stream
 def spv_verify_tree(target_logits, draft_logits, parent, tokens, r, sample_keys, temperature: float, *,
                     workspace=None, out=None, want_nodes: bool = True, want_status: bool = True, stream=None) -> dict:
     """Verify of a draft token tree per sequence (see spv_verify_tree in
@@ -390,6 +395,7 @@ def spv_verify_tree(target_logits, draft_logits, parent, tokens, r, sample_keys,
     return out
 
 
+@_on_its_stream
 def spv_verify_greedy(target_logits, draft_tokens, *, workspace=None, out=None, want_status: bool = True,
                       stream=None) -> dict:
     """Greedy (T = 0) verify: argmax agreement.  target_logits [B, g+1, V]."""
@@ -417,6 +423,7 @@ def spv_verify_greedy(target_logits, draft_tokens, *, workspace=None, out=None, 
     return out
 
 
+@_on_its_stream
 def spv_fanout_topk(draft_logits, exclude, fanout, *, workspace=None, out=None, want_status: bool = True,
                     stream=None) -> dict:
     """Top-F_k ids per (b, k) of draft_logits [B, K+1, V], skipping exclude[b, k]."""

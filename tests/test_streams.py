@@ -82,3 +82,24 @@ def test_rope_and_evict(world):
     world.made.clear()
     spv.spv_kv_evict(Cache(), table, one, torch.ones(1, 2, 32), 8, stream=STREAM)
     check(world, "spv_kv_evict", 5)
+
+
+LOGITS, DRAFT = torch.ones(1, 3, 8), torch.ones(1, 2, 8)
+TOKENS, R, KEYS = torch.ones(1, 2, dtype=I32), torch.ones(1, 2), torch.ones(1, dtype=torch.int64)
+CHAIN = (LOGITS, DRAFT, TOKENS, R, KEYS, 1.0)
+TREE = (LOGITS, LOGITS, torch.ones(1, 3, dtype=I32), torch.ones(1, 3, dtype=I32), torch.ones(1, 3), KEYS, 1.0)
+IDS = torch.ones(1, 6, dtype=I32)
+
+
+@pytest.mark.parametrize("name, args, made", [  # the workspace, then the outputs
+    ("spv_verify_chain", CHAIN, 5),
+    ("spv_verify_chain_cached", (*CHAIN, IDS, [2, 2, 2]), 6),
+    ("spv_verify_chain_saguaro", (*CHAIN, IDS, [2, 2, 2], 2.0), 6),
+    ("spv_verify_chain_filtered", (*CHAIN, 4, 0.9), 5),
+    ("spv_verify_tree", TREE, 5),
+    ("spv_verify_greedy", (LOGITS, TOKENS), 4),
+    ("spv_fanout_topk", (LOGITS, torch.ones(1, 3, dtype=I32), [2, 2, 2]), 3),
+])
+def test_verify_calls(world, name, args, made):
+    getattr(spv, name)(*args, stream=STREAM)
+    check(world, name, made)
