@@ -544,7 +544,7 @@ spv_status spv_attention_mass(const void *q, spv_dtype dtype, int B, int T, int 
  *   mass_out     [B, kv_heads, out_stride] fp32, out_stride >= min(budget, mass_stride): the
  *                kept entries' mass in their new slots; may be `mass` itself (same stride)
  *   pos_out      likewise int32, optional
- *   new_lens     [B] out: min(lens[b], budget)
+ *   new_lens     [B] out: min(lens[b], budget); may be `lens` itself
  *   slot_src     [B, kv_heads, budget] out: the slot that the entry came from, -1 from new_lens[b] on
  *   row_status   [B] optional
  * Entries of mass_out and pos_out from new_lens[b] on are not written.

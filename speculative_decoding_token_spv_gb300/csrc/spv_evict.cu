@@ -10,7 +10,9 @@
 // two bits a round, until a count is exact, usually after about 12 rounds;
 // beyond, a radix select reads the weights again for each of four digits
 // (evict_select_many).
-// evict_move_kernel, a dependent launch, copies the rows of the matched slots.
+// evict_move_kernel, a dependent launch, copies the rows of the matched slots
+// and writes the new lengths: all blocks of the selection have read the old ones
+// by then, so the new may take their place.
 //
 // What bounds it: for many sequences the moves, read once and written once (32
 // sequences of 8,191 slots, 8 heads of 128, bf16, cut to 4,096: 633 MB, 117 us,
@@ -72,6 +74,13 @@ template <int WARPS> __device__ __forceinline__ int block_prefix(int x, int *sh,
     return upto - x + s;
 }
 
+// Whether a length is out of range.
+__device__ __forceinline__ bool evict_bad(const EvictParams &p, int n)
+{
+    const int64_t cap = static_cast<int64_t>(p.c.max_pages) << p.c.page_shift;
+    return n < 0 || n > cap || n > p.stride;
+}
+
 // What both selections begin with, for block (h, b): the length, whether it is
 // bad, and the outputs that need no selection.  False: the item is done.
 struct EvictItem {
@@ -94,18 +103,14 @@ __device__ __forceinline__ bool evict_begin(const EvictParams &p, EvictItem *it)
     it->mass_out = p.mass_out + item * p.out_stride;
     it->pos_out = p.pos_out ? p.pos_out + item * p.out_stride : nullptr;
     const int n = p.lens[b];
-    const int64_t cap = static_cast<int64_t>(p.c.max_pages) << p.c.page_shift;
-    const bool bad = n < 0 || n > cap || n > p.stride;
-    if (h == 0) {
-        if (p.row_status) {
-            int any = bad;
-            const int32_t *table = p.c.table + static_cast<int64_t>(b) * p.c.max_pages;
-            for (int g = tid; !bad && n > p.budget && g <= (n - 1) >> p.c.page_shift; g += static_cast<int>(blockDim.x))
-                any |= page_of(p.c, table, g << p.c.page_shift) < 0;
-            any = __syncthreads_or(any);
-            if (tid == 0) p.row_status[b] = any ? KV_STATUS_BAD : 0;
-        }
-        if (tid == 0) p.new_lens[b] = bad || n < p.budget ? n : p.budget;
+    const bool bad = evict_bad(p, n);
+    if (h == 0 && p.row_status) {
+        int any = bad;
+        const int32_t *table = p.c.table + static_cast<int64_t>(b) * p.c.max_pages;
+        for (int g = tid; !bad && n > p.budget && g <= (n - 1) >> p.c.page_shift; g += static_cast<int>(blockDim.x))
+            any |= page_of(p.c, table, g << p.c.page_shift) < 0;
+        any = __syncthreads_or(any);
+        if (tid == 0) p.row_status[b] = any ? KV_STATUS_BAD : 0;
     }
     it->n = n;
     it->m = bad ? 0 : n < p.budget ? n : p.budget;
@@ -436,6 +441,10 @@ __global__ void __launch_bounds__(EV_MOVE_SLOTS) evict_move_kernel(const EvictPa
     const int h = blockIdx.y % p.c.kv_heads, b = blockIdx.y / p.c.kv_heads, i = blockIdx.x * EV_MOVE_SLOTS + tid;
     const int32_t *table = p.c.table + static_cast<int64_t>(b) * p.c.max_pages;
     chain_begin();
+    if (tid == 0 && blockIdx.x == 0 && h == 0) {
+        const int n = p.lens[b];  // may be new_lens
+        p.new_lens[b] = evict_bad(p, n) || n < p.budget ? n : p.budget;
+    }
     // the block's moves, in a row
     const int s = i < p.budget ? p.slot_src[static_cast<int64_t>(blockIdx.y) * p.budget + i] : -1;
     bool moves = s >= 0 && s != i;

@@ -307,8 +307,8 @@ def spv_kv_evict(cache: KVCache, page_table, lens, mass, budget: int, *, pos=Non
     and per key head, by the accumulated weight ``mass`` [B, kv_heads, slots]
     (see spv_kv_evict in spv.h).  Returns dict(mass, pos [B, kv_heads, >=
     budget], lens [B], slot_src [B, kv_heads, budget], and row_status when
-    requested); pass ``mass`` and ``pos`` themselves in ``out`` to update them
-    in place."""
+    requested); pass ``mass``, ``pos`` and ``lens`` themselves in ``out`` to
+    update them in place."""
     pack, dev, (_, _, Hkv, _) = cache.packed()
     try:
         full = mass.shape

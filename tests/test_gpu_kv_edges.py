@@ -121,3 +121,45 @@ def test_calls_on_a_side_stream_have_buffers_of_their_own(spv, T):
         for x, y in zip(want, got):
             assert torch.equal(x.cpu(), y)
         torch.cuda.synchronize()
+
+
+@pytest.mark.parametrize("W, budget", [(400, 64), (20_000, 9_000), (70_000, 30_000)])
+def test_evict_lengths_in_place(spv, W, budget):
+    """lens as its own output: every head of every sequence is cut as with lengths apart, also in a replayed graph."""
+    B, Hkv, D, page = 5, 8, 64, 16
+    lens = [W, budget + 1, budget, 3, W - 1]
+    gen = torch.Generator(device="cuda").manual_seed(55)
+    pages = -(-W // page)
+    pool = lambda: torch.randn(pages * B, page, Hkv, D, generator=gen, device="cuda").bfloat16()  # noqa: E731
+    k, v = pool(), pool()
+    table = torch.arange(B * pages, dtype=torch.int32, device="cuda").reshape(B, pages)
+    mass = torch.rand(B, Hkv, W, generator=gen, device="cuda")
+    apart = spv.KVCache(k.clone(), v.clone())
+    want = spv.spv_kv_evict(apart, table, i32(lens), mass, budget, sinks=2, recent=5)
+    cache, at = spv.KVCache(k.clone(), v.clone()), i32(lens)
+    out = {x: torch.empty_like(want[x]) for x in ("mass", "pos", "slot_src", "row_status")}
+
+    def run():
+        return spv.spv_kv_evict(cache, table, at, mass, budget, sinks=2, recent=5, out={**out, "lens": at})
+
+    def check():
+        torch.cuda.synchronize()
+        assert at.tolist() == [min(n, budget) for n in lens] and out["row_status"].tolist() == [0] * B
+        assert torch.equal(out["slot_src"], want["slot_src"])
+        assert torch.equal(cache.k, apart.k) and torch.equal(cache.v, apart.v)
+        for b, n in enumerate(at.tolist()):
+            assert torch.equal(out["mass"][b, :, :n], want["mass"][b, :, :n])
+
+    run()
+    check()
+    again = run()  # nothing is above the budget now
+    torch.cuda.synchronize()
+    assert again["lens"] is at and at.tolist() == [min(n, budget) for n in lens]
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        run()
+    for _ in range(2):
+        at.copy_(i32(lens))
+        cache.k.copy_(k), cache.v.copy_(v)
+        g.replay()
+        check()
