@@ -54,12 +54,14 @@ template <typename C> __device__ __forceinline__ void store8(C *dst, const float
 // needs before it writes (q may be rotated in place).
 enum RopeMode {
     ROPE_PAIRS,   // interleaved, or nothing rotates: a task is 8 elements
+    ROPE_PARTIAL, // the same where the rotation ends within a task's 8: what is behind its end keeps its bits
     ROPE_HALVES,  // a task is 8 elements and their partners half a rotation away; then 8 passing elements each
     ROPE_SCALAR   // halves whose length is no multiple of 8: the same, element by element
 };
+constexpr bool rope_pairs(int mode) { return mode == ROPE_PAIRS || mode == ROPE_PARTIAL; }
 template <int MODE> __device__ __forceinline__ int head_tasks(const RopeParams &p)
 {
-    if (MODE == ROPE_PAIRS) return p.D >> 3;
+    if (rope_pairs(MODE)) return p.D >> 3;
     return (p.half >> 3) + ((p.D - 2 * p.half) >> 3);
 }
 
@@ -71,6 +73,7 @@ template <int MODE> struct RopePlace {
     int d, other;            // its 8 elements begin here, their partners there (-1: none)
     float c[8], s[8];        // interleaved: of the 4 pairs, each twice
     bool turns;
+    int n;                   // ROPE_PARTIAL: elements that turn, the first ones
 };
 
 template <int MODE, typename T> struct RopeData {
@@ -106,13 +109,21 @@ __device__ __forceinline__ void rope_write(const RopeData<MODE, T> &v, C *row, c
         }
         store8(row + at.other, w, div);
     }
-    if (MODE == ROPE_PAIRS && at.turns) {
+    if (rope_pairs(MODE) && at.turns) {
 #pragma unroll
         for (int j = 0; j < 8; j += 2) {
+            if (MODE == ROPE_PARTIAL && j >= at.n) continue;
             const float u0 = u[j], w0 = u[j + 1];
             u[j] = u0 * at.c[j] - w0 * at.s[j];
             u[j + 1] = w0 * at.c[j] + u0 * at.s[j];
         }
+    }
+    if constexpr (MODE == ROPE_PARTIAL && std::is_same<T, C>::value) {
+        Vec8<C> o;
+#pragma unroll
+        for (int j = 0; j < 8; ++j) o.x[j] = j < at.n ? Num<C>::down(u[j]) : xs[j];
+        *reinterpret_cast<Vec8<C> *>(row + at.d) = o;
+        return;
     }
     store8(row + at.d, u, div);
 }
@@ -143,8 +154,9 @@ __global__ void __launch_bounds__(ROPE_THREADS) rope_kernel(const RopeParams p)
             at.other = at.d + p.half;
         else
             at.d += p.half;  // past both halves
-    } else if (MODE == ROPE_PAIRS) {
+    } else if (rope_pairs(MODE)) {
         at.turns = at.d < 2 * p.half;
+        at.n = min(8, 2 * p.half - at.d);
     }
     v_place.d = 8 * (tid % D8);
     v_place.other = -1;
@@ -221,11 +233,14 @@ __global__ void __launch_bounds__(ROPE_THREADS) rope_kernel(const RopeParams p)
                     w = w0 * a.x + u0 * a.y;
                 }
                 if (h < p.q_heads) {
-                    q_out[h * p.D + d] = Num<T>::down(u);
+                    q_out[h * p.D + d] = o >= 0 ? Num<T>::down(u) : row[d];  // what passes keeps its bits
                     if (o >= 0) q_out[h * p.D + o] = Num<T>::down(w);
                 } else if (page >= 0) {
                     const float div = k_div(h);
-                    k_at(h)[d] = Num<C>::down(sizeof(C) == 1 ? u / div : u);
+                    if constexpr (std::is_same<T, C>::value)
+                        k_at(h)[d] = o >= 0 ? Num<C>::down(u) : row[d];
+                    else
+                        k_at(h)[d] = Num<C>::down(u / div);
                     if (o >= 0) k_at(h)[o] = Num<C>::down(sizeof(C) == 1 ? w / div : w);
                 }
             }
@@ -234,11 +249,11 @@ __global__ void __launch_bounds__(ROPE_THREADS) rope_kernel(const RopeParams p)
 #pragma unroll
                 for (int j = 0; j < 8; ++j) at.c[j] = mine[at.d + j].x, at.s[j] = mine[at.d + j].y;
             }
-            if (MODE == ROPE_PAIRS && at.turns) {
+            if (rope_pairs(MODE) && at.turns) {
 #pragma unroll
                 for (int j = 0; j < 8; j += 2) {
-                    const bool in = at.d + j < 2 * p.half;  // the rotation may end within the 8
-                    const float2 a = in ? mine[(at.d + j) >> 1] : make_float2(1.0f, 0.0f);
+                    if (MODE == ROPE_PARTIAL && j >= at.n) continue;
+                    const float2 a = mine[(at.d + j) >> 1];
                     at.c[j] = a.x, at.s[j] = a.y;
                 }
             }
@@ -284,6 +299,7 @@ template <int MODE, typename T, typename C> static cudaError_t launch_mode(const
 }
 template <typename T, typename C> static cudaError_t launch(const RopeParams &p, cudaStream_t st)
 {
+    if (p.interleaved && p.half % 4 != 0) return launch_mode<ROPE_PARTIAL, T, C>(p, st);
     if (p.interleaved || p.half == 0) return launch_mode<ROPE_PAIRS, T, C>(p, st);
     if (p.half % 8 == 0) return launch_mode<ROPE_HALVES, T, C>(p, st);
     return launch_mode<ROPE_SCALAR, T, C>(p, st);

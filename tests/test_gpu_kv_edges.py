@@ -6,6 +6,7 @@ import math
 import pytest
 import torch
 
+import kv_reference as ref
 from kv_reference import DTYPES, half_step
 from test_gpu_kv import Layer, i32, spv  # noqa: F401  (spv: the fixture)
 
@@ -163,3 +164,28 @@ def test_evict_lengths_in_place(spv, W, budget):
         cache.k.copy_(k), cache.v.copy_(v)
         g.replay()
         check()
+
+
+@pytest.mark.parametrize("inter, r", [(True, 26), (True, 6), (True, 60), (False, 26), (False, 48)])
+@pytest.mark.parametrize("dtype", ["bf16", "f16"])
+def test_rope_passes_elements_unchanged(spv, inter, r, dtype):
+    """The elements from rotary_dim on keep their bits, whatever their neighbours are: infinities, NaN, signed zeros."""
+    B, T, Hq, Hkv, D, page = 2, 3, 4, 2, 64, 16
+    gen = torch.Generator().manual_seed(52)
+    k, v, _, _, table = ref.make_cache(gen, [20] * B, page, Hkv, D, dtype, garbage=False)
+    x = torch.randn(B, T, Hq + 2 * Hkv, D, generator=gen).to(DTYPES[dtype])
+    odd = torch.tensor([math.inf, -0.0, -0.0, -1.0, math.nan, 2.0, -math.inf, 0.0, -0.0, math.inf])
+    passing = odd.repeat(B * T * (Hq + Hkv) * D)[: B * T * (Hq + Hkv) * (D - r)].reshape(B, T, Hq + Hkv, D - r).to(DTYPES[dtype])
+    x[:, :, : Hq + Hkv, r:] = passing
+    cache = spv.KVCache(k.cuda(), v.cuda())
+    q, kk, vv = x.cuda().split([Hq, Hkv, Hkv], dim=2)
+    got = spv.spv_rope_append(q, kk, vv, cache, table.cuda(), i32([17] * B), spv.spv_rope_frequencies(r), interleaved=inter)
+    torch.cuda.synchronize()
+    bits = lambda y: y.contiguous().view(torch.int16).cpu()  # noqa: E731
+    assert torch.equal(bits(got["q"][..., r:]), bits(x[:, :, :Hq, r:]))
+    assert torch.isfinite(got["q"][..., :r]).all()
+    for b in range(B):
+        for t in range(T):
+            at = (table[b, (17 + t) // page].long(), (17 + t) % page)
+            assert torch.equal(bits(cache.k[at][:, r:]), bits(x[b, t, Hq: Hq + Hkv, r:]))
+            assert torch.equal(bits(cache.v[at]), bits(x[b, t, Hq + Hkv:]))
