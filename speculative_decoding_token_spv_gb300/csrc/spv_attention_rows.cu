@@ -67,6 +67,7 @@ struct RowsCtl {
     signed char q_power[2][AR_ROWS];   // e4m3: the rows of q are stored times 2^q_power
     uint32_t tmem;
     int dead, stop;
+    int lost;                          // some row's output may have NaN
 };
 
 // Warps of a block: 4 for the rows, or 8 that share each row's keys where a row stands once; then 4 of products and q, 4
@@ -444,6 +445,89 @@ template <int N> __device__ __forceinline__ void rows_sync() { asm volatile("bar
 // The two warps that have the same rows.
 __device__ __forceinline__ void pair_sync(int w) { asm volatile("bar.sync %0, 64;" ::"r"(2 + w) : "memory"); }
 
+// The NaN columns of an item's rows, or of the block's piece of them, anew: a
+// warp a row, key by key in 32 bits, without weights of keys that a row does
+// not have.  Rows whose scores are NaN, or that have a bad page, stay as they
+// are.
+template <typename T, int D, int COLS> __device__ void rows_again(const AttParams &p, const Cursor &c, long long begin, int tid)
+{
+    constexpr int PER = D / 32;  // columns of a lane, next to one another
+    const int lane = tid & 31, row0 = c.row_tile * COLS, live = min(COLS, p.rows - row0), t0 = first_tile(c), t1 = last_tile(c);
+    if (t0 == t1) return;
+    const bool whole = t0 == 0 && t1 == c.tiles;
+    float *part = p.parts + (static_cast<int64_t>(blockIdx.x) * 2 + (c.first < begin ? 0 : 1)) * (AR_ROWS * (D + 2));
+    const int32_t *table = p.c.table + static_cast<int64_t>(c.b) * p.c.max_pages;
+#pragma unroll 1
+    for (int r = tid >> 5; r < live; r += AR_ROWS / 32) {
+        const int token = (row0 + r) / p.group, g = row0 + r - token * p.group;
+        const int64_t at = ((static_cast<int64_t>(c.b) * p.w.T + token) * p.q_heads + c.h * p.group + g) * D + PER * lane;
+        T *out = static_cast<T *>(p.out) + at;
+        float *piece = part + 2 * AR_ROWS + r * D + PER * lane;
+        unsigned nan = 0;
+#pragma unroll
+        for (int e = 0; e < PER; ++e) {
+            const float y = whole ? Num<T>::up(out[e]) : piece[e];
+            if (y != y) nan |= 1u << e;
+        }
+        if (!__any_sync(0xffffffffu, nan != 0)) continue;
+        const unsigned long long see =
+            token < c.s.fresh ? visible_mask(p.parent ? p.parent + static_cast<int64_t>(c.b) * p.w.T : nullptr, token) : 0ull;
+        float m = -CUDART_INF_F, l = 0.0f, q[PER], x[PER];
+#pragma unroll
+        for (int e = 0; e < PER; ++e) {
+            q[e] = Num<T>::up(static_cast<const T *>(p.q)[at + e]);
+            x[e] = 0.0f;
+        }
+        bool fine = see != 0;
+        const int end = min(t1 * AR_KEYS, c.s.total);
+#pragma unroll 1
+        for (int j = t0 * AR_KEYS; fine && j < end; ++j) {
+            const int page = page_of(p.c, table, j);
+            fine = page >= 0;
+            if (!fine || (j >= c.s.ctx && !(see >> (j - c.s.ctx) & 1))) continue;
+            const T *k = reinterpret_cast<const T *>(row_ptr(p.c, p.c.k, page, j, c.h)) + PER * lane;
+            const T *v = reinterpret_cast<const T *>(row_ptr(p.c, p.c.v, page, j, c.h)) + PER * lane;
+            float s = 0.0f;
+#pragma unroll
+            for (int e = 0; e < PER; ++e) s += q[e] * Num<T>::up(k[e]);
+#pragma unroll
+            for (int o = 16; o; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
+            s *= p.scale_log2;
+            fine = s == s;
+            if (!fine || s == -CUDART_INF_F) continue;
+            if (s > m) {
+                const float a = fast_exp2(m - s);
+                m = s;
+                l *= a;
+#pragma unroll
+                for (int e = 0; e < PER; ++e) x[e] *= a;
+            }
+            const float w = fast_exp2(s - m);
+            l += w;
+#pragma unroll
+            for (int e = 0; e < PER; ++e) x[e] += w * Num<T>::up(v[e]);
+        }
+        if (!fine || l == 0.0f) continue;
+        const float unit = whole ? 1.0f / l : fast_exp2(m - part[r]);
+#pragma unroll
+        for (int e = 0; e < PER; ++e) {
+            if (!(nan >> e & 1)) continue;
+            if (whole)
+                out[e] = Num<T>::down(x[e] * unit);
+            else
+                piece[e] = x[e] * unit;
+        }
+    }
+}
+
+// The block's whole range; out of line, away from the loops that have to fit the
+// instruction caches.
+template <typename T, int D, int COLS> __device__ __noinline__ void rows_walk_again(const AttParams &p, long long begin, int tid)
+{
+    for (Cursor c = find_range(p.w, p.c, blockIdx.x, gridDim.x, tid & 31); c.at < c.end; next_item(c, p.w, p.c))
+        rows_again<T, D, COLS>(p, c, begin, tid);
+}
+
 // COLS: rows of a copy, and its keys of a tile; a thread takes these, or half of them.
 template <typename T, typename C, int D, int COLS>
 __device__ void rows_softmax(const AttParams &p, Cursor c, char *smem, RowsCtl *ctl, unsigned *err, int tid)
@@ -458,6 +542,9 @@ __device__ void rows_softmax(const AttParams &p, Cursor c, char *smem, RowsCtl *
     const uint32_t tm_s = ctl->tmem + quarter + copy * COLS + half * KEYS,
                    tm_p = ctl->tmem + quarter + 256 + copy * (COLS / 2) + half * (KEYS / 2), tm_o = ctl->tmem + quarter + 384;
     const long long begin = c.at;
+    // An infinity in a cached slot of V, which all rows see, meets a weight of 0 in the copies that do not have its key:
+    // rows with NaN are looked at again when the range is done.  (Looking for NaN costs the verify batch 4 us of 236.)
+    constexpr bool LOOK_AGAIN = COPIES > 1 && !S::WIDEN;
     // the keys of other copies never get a probability
     if (COPIES > 1) {
         uint32_t zero[32];
@@ -653,6 +740,15 @@ __device__ void rows_softmax(const AttParams &p, Cursor c, char *smem, RowsCtl *
                 }
             }
             if (copy != keeper || !mine) continue;
+            if (LOOK_AGAIN) {
+                float sum[4];  // NaN if one of them is
+#pragma unroll
+                for (int k = 0; k < 4; ++k) sum[k] = x[k];
+#pragma unroll
+                for (int k = 4; k < 32; ++k) sum[k & 3] += x[k];
+                const float any = (sum[0] + sum[1]) + (sum[2] + sum[3]);
+                if (any != any) *reinterpret_cast<volatile int *>(&ctl->lost) = 1;
+            }
             if (odd) {
                 // New tokens whose v has infinities or NaN (cleared for the product): for the rows that see them.
                 for (unsigned long long left = odd & see; left; left &= left - 1) {
@@ -707,6 +803,10 @@ __device__ void rows_softmax(const AttParams &p, Cursor c, char *smem, RowsCtl *
         rows_sync<W::SOFTMAX>();
         if (stop) break;
     }
+    if constexpr (LOOK_AGAIN) {
+        if (*reinterpret_cast<volatile int *>(&ctl->lost) && !*reinterpret_cast<volatile int *>(&ctl->dead))
+            rows_walk_again<T, D, COLS>(p, begin, tid);
+    }
 }
 
 template <typename T, typename C, int D, int COLS>
@@ -737,7 +837,7 @@ __global__ void __launch_bounds__(RowsWarps<COLS>::THREADS, 1)
             mbar_init(&ctl->q_empty[i], W::SOFTMAX);
         }
         for (int i = 0; i < AR_ITEMS; ++i) ctl->odd[i] = 0, ctl->bad[i] = 0;
-        ctl->dead = ctl->stop = 0;
+        ctl->dead = ctl->stop = ctl->lost = 0;
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
     if (warp == W::SOFTMAX / 32) tmem_alloc(&ctl->tmem, 512);

@@ -189,3 +189,32 @@ def test_rope_passes_elements_unchanged(spv, inter, r, dtype):
             at = (table[b, (17 + t) // page].long(), (17 + t) % page)
             assert torch.equal(bits(cache.k[at][:, r:]), bits(x[b, t, Hq: Hq + Hkv, r:]))
             assert torch.equal(bits(cache.v[at]), bits(x[b, t, Hq + Hkv:]))
+
+
+@pytest.mark.parametrize("T, G", ROWS)
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("dtype", ["bf16", "f16"])
+def test_infinities_in_cached_v_are_seen(spv, T, G, D, dtype):
+    """An infinity in a cached slot is every row's result in its column; infinities of both signs, or NaN, make NaN;
+    the other columns keep every bit."""
+    a = Layer(spv, 51, [700, 131], None, T, 2 * G, 2, D, 16, dtype=dtype)
+    clean = a.attend()
+    for b, slots in enumerate(((3, 130, 301, 699), (0, 64, 129, 130))):
+        for i, j in enumerate(slots):
+            at = (a.table[b, j // 16].long(), j % 16, 1)
+            a.cache.v[at + (8 + i,)] = math.inf                        # one slot each
+            a.cache.v[at + (40 + i,)] = -math.inf
+            a.cache.v[at + (16,)] = math.inf                           # all four slots
+            a.cache.v[at + (17,)] = math.inf if i % 2 else -math.inf   # both signs
+            a.cache.v[at + (63,)] = math.nan if i == 2 else math.inf
+    got = a.attend()
+    want = clean["out"].clone()
+    h = slice(G, 2 * G)
+    want[:, :, h, 8:12] = math.inf
+    want[:, :, h, 40:44] = -math.inf
+    want[:, :, h, 16] = math.inf
+    want[:, :, h, 17] = math.nan
+    want[:, :, h, 63] = math.nan
+    assert torch.equal(torch.isnan(got["out"]), torch.isnan(want))
+    assert torch.equal(got["out"].nan_to_num(nan=0.5), want.nan_to_num(nan=0.5))
+    assert torch.equal(got["lse"], clean["lse"])
