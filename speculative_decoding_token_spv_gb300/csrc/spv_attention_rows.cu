@@ -24,10 +24,10 @@
 // 2,850 cycles a tile where its K and V take 2,300 (draft trees: 110 us).
 //
 // What bounds it, and what it takes: 40 rows of 64 sequences of up to 8,191
-// slots, K and V 1.37 GB, 232 us (5.9 TB/s, 87% of a copy's rate: reading K and
+// slots, K and V 1.37 GB, 236 us (5.8 TB/s, 86% of a copy's rate: reading K and
 // V, then starts, ends of items and joins); 84 rows of 32 sequences of up to
-// 4,099 slots, 353 MB, 94 us: exponentials, 1,800 of a tile's 2,450 cycles, and
-// the ends of items.
+// 4,099 slots, 353 MB, 88 us: exponentials, 1,800 of a tile's 2,450 cycles when it
+// took 94 us, and the ends of items.
 //
 // Every wait is bounded; one that gives up records SPV_ERR_TIMEOUT in the
 // workspace, ends the block in order and leaves NaN in what it had to write.
@@ -57,17 +57,17 @@ template <typename C, int D> struct RowsShape {
 struct RowsCtl {
     uint64_t k_full[5], k_empty[5], v_full[5], v_empty[5];  // of a stage (e4m3: the one widened tile)
     uint64_t s_full[2], p_full[2], o_done[2], q_full[2], q_empty[2], spare[2];
-    unsigned long long odd[AR_ITEMS];  // new tokens whose v has infinities or NaN
+    int odd[AR_ITEMS];                 // some new token's v has infinities or NaN
     unsigned long long sees[2][64];    // per place of q: what each new token sees
     int bad[AR_ITEMS];                 // a page id outside the pool
     float top[2 * AR_ROWS];            // a tile's maxima of the two halves
     // e4m3: what widening a tile needs to know of it, per loader warp and stage: the row of its first new token (128:
-    // none), that token's number, the item's flags.
-    short tail[8][5][3];
+    // none), the item's flags.
+    short tail[8][5][2];
     signed char q_power[2][AR_ROWS];   // e4m3: the rows of q are stored times 2^q_power
     uint32_t tmem;
     int dead, stop;
-    int lost;                          // some row's output may have NaN
+    int lost;                          // infinities or NaN of V are missing in some row's output, or may be there in vain
 };
 
 // Warps of a block: 4 for the rows, or 8 that share each row's keys where a row stands once; then 4 of products and q, 4
@@ -149,7 +149,7 @@ __device__ void rows_load(const AttParams &p, Cursor c, char *smem, RowsCtl *ctl
     // e4m3: widens tile t, whose copies have landed; each thread what it has loaded.
     auto widen = [&](int t) -> bool {
         const int st = t % NST;
-        const int row0 = ctl->tail[4 * kv + w][st][0], token0 = ctl->tail[4 * kv + w][st][1], flags = ctl->tail[4 * kv + w][st][2];
+        const int row0 = ctl->tail[4 * kv + w][st][0], flags = ctl->tail[4 * kv + w][st][1];
         const char *raw = smem + S::RAW_AT + (st * 2 + kv) * S::RAW;
         char *to = smem + AT;
         if (t > 0 && !rows_wait(ctl, empty, (t - 1) & 1, err)) return false;
@@ -170,7 +170,7 @@ __device__ void rows_load(const AttParams &p, Cursor c, char *smem, RowsCtl *ctl
 #pragma unroll
                     for (int k = 0; k < 4; ++k)  // bytes 0x7f and 0xff, to 0
                         b[k] &= ~(((((b[k] & 0x7f7f7f7fu) + 0x01010101u) & 0x80808080u) >> 7) * 0xffu);
-                    atomicOr(&ctl->odd[flags], 1ull << ((token0 + row - row0) & 63));
+                    *reinterpret_cast<volatile int *>(&ctl->odd[flags]) = 1;
                 }
                 uint32_t y[8];
 #pragma unroll
@@ -239,7 +239,7 @@ __device__ void rows_load(const AttParams &p, Cursor c, char *smem, RowsCtl *ctl
                 }
                 if (map) pg = lookup(tile);  // a tile of V with new tokens: by rows
             }
-            const int row0 = min(max(0, c.s.ctx - j0), AR_KEYS), token0 = max(0, j0 - c.s.ctx);  // the first new token
+            const int row0 = min(max(0, c.s.ctx - j0), AR_KEYS);  // of the first new token
             if (static_cast<unsigned>(pg) >= static_cast<unsigned>(p.c.num_pages)) {
                 if (j0 + 32 * w + lane < c.s.total) *reinterpret_cast<volatile int *>(&ctl->bad[flags]) = 1;
                 pg = -1;
@@ -256,8 +256,7 @@ __device__ void rows_load(const AttParams &p, Cursor c, char *smem, RowsCtl *ctl
                 __syncwarp();
                 if (lane == 0) {
                     ctl->tail[4 * kv + w][st][0] = row0;
-                    ctl->tail[4 * kv + w][st][1] = token0;
-                    ctl->tail[4 * kv + w][st][2] = flags;
+                    ctl->tail[4 * kv + w][st][1] = flags;
                 }
                 __syncwarp();
                 to = base + S::RAW_AT + (st * 2 + kv) * S::RAW;
@@ -265,7 +264,7 @@ __device__ void rows_load(const AttParams &p, Cursor c, char *smem, RowsCtl *ctl
                 if (n >= NST && !(ok = rows_wait(ctl, &empty[st], (n / NST - 1) & 1, err))) break;
                 to = base + AT + st * S::TILE;
             }
-#pragma unroll 2
+#pragma unroll 1
             for (int i = 0; i < CH; ++i) {
                 const int row = 32 * w + i * RPI + sub;
                 const int64_t at = __shfl_sync(0xffffffffu, mine, i * RPI + sub);
@@ -276,7 +275,7 @@ __device__ void rows_load(const AttParams &p, Cursor c, char *smem, RowsCtl *ctl
                 cp_async_commit();
             } else if (kv && row0 < AR_KEYS) {
                 // Infinities and NaN in a new token's v: cleared here, as 0 x inf would reach rows that do not see it;
-                // the rows that do get them at the end.
+                // the rows that do get them at the end of the range.
                 asm volatile("cp.async.wait_all;" ::: "memory");
 #pragma unroll 1
                 for (int i = 0; i < CH; ++i) {
@@ -286,7 +285,7 @@ __device__ void rows_load(const AttParams &p, Cursor c, char *smem, RowsCtl *ctl
                     const uint4 x = *v;
                     if (chunk_not_finite<C>(x)) {
                         *v = finite_only<C>(x);
-                        atomicOr(&ctl->odd[flags], 1ull << ((token0 + row - row0) & 63));
+                        *reinterpret_cast<volatile int *>(&ctl->odd[flags]) = 1;
                     }
                 }
                 fence_async_shared();
@@ -306,7 +305,9 @@ __device__ void rows_load(const AttParams &p, Cursor c, char *smem, RowsCtl *ctl
 // ------------------------------------------------------------------ products
 // Two threads, one for the scores and one for the outputs: issuing a tile's 8
 // products takes either of them 600 to 1,100 cycles, and the rows wait for the
-// scores (one thread for both: 241 us for the verify batch, now 232).
+// scores (one thread for both: 241 us for the verify batch against 232).  Their
+// loops are unrolled by two only: all roles' loops together have to fit the
+// instruction caches (all eight: draft trees 91 us, 88 so).
 template <typename T, typename C, int D>
 __device__ void rows_scores(const AttParams &p, Cursor c, char *smem, RowsCtl *ctl, unsigned *err)
 {
@@ -326,7 +327,7 @@ __device__ void rows_scores(const AttParams &p, Cursor c, char *smem, RowsCtl *c
             tc_fence_after();
             fence_async_shared();  // K was written by asynchronous copies of threads, q by threads
             const uint64_t k = desc_k_major(base + S::K_AT + (n % KST) * S::TILE);
-#pragma unroll
+#pragma unroll 2
             for (int ks = 0; ks < D / 16; ++ks) {
                 const int off = ((ks >> 2) * (AR_KEYS * 128) + (ks & 3) * 32) >> 4;
                 tc_mma(tm_s + (n & 1) * AR_KEYS, q + off, k + off, SHAPE, ks > 0);
@@ -353,7 +354,7 @@ __device__ void rows_outputs(const AttParams &p, Cursor c, char *smem, RowsCtl *
             tc_fence_after();
             fence_async_shared();
             const uint64_t v = desc_n_major(base + S::V_AT + (n % VST) * S::TILE, AR_KEYS * 128);
-#pragma unroll
+#pragma unroll 2
             for (int ks = 0; ks < AR_KEYS / 16; ++ks)
                 tc_mma_ta(tm_o, tm_p + (n & 1) * (AR_KEYS / 2) + ks * 8, v + ks * (2048 >> 4), SHAPE, i > 0 || ks > 0);
             tc_commit(&ctl->o_done[n & 1]);
@@ -445,11 +446,13 @@ template <int N> __device__ __forceinline__ void rows_sync() { asm volatile("bar
 // The two warps that have the same rows.
 __device__ __forceinline__ void pair_sync(int w) { asm volatile("bar.sync %0, 64;" ::"r"(2 + w) : "memory"); }
 
-// The NaN columns of an item's rows, or of the block's piece of them, anew: a
-// warp a row, key by key in 32 bits, without weights of keys that a row does
-// not have.  Rows whose scores are NaN, or that have a bad page, stay as they
-// are.
-template <typename T, int D, int COLS> __device__ void rows_again(const AttParams &p, const Cursor &c, long long begin, int tid)
+// Columns of an item's rows, or of the block's piece of them, that the products
+// could not have: those where a new token that the row sees has an infinity or
+// NaN in v (cleared there), and those that are NaN.  A warp a row, anew, key by
+// key in 32 bits and without weights of keys that the row does not have.  Rows
+// whose scores are NaN, or that have a bad page, stay as they are.
+template <typename T, typename C, int D, int COLS>
+__device__ __forceinline__ void rows_again(const AttParams &p, const Cursor &c, long long begin, int tid)
 {
     constexpr int PER = D / 32;  // columns of a lane, next to one another
     const int lane = tid & 31, row0 = c.row_tile * COLS, live = min(COLS, p.rows - row0), t0 = first_tile(c), t1 = last_tile(c);
@@ -457,42 +460,55 @@ template <typename T, int D, int COLS> __device__ void rows_again(const AttParam
     const bool whole = t0 == 0 && t1 == c.tiles;
     float *part = p.parts + (static_cast<int64_t>(blockIdx.x) * 2 + (c.first < begin ? 0 : 1)) * (AR_ROWS * (D + 2));
     const int32_t *table = p.c.table + static_cast<int64_t>(c.b) * p.c.max_pages;
+    const int end = min(t1 * AR_KEYS, c.s.total);
+    const float factor = p.scale_log2 * (p.c.k_scale ? __ldg(p.c.k_scale + c.h) : 1.0f);
+    auto row_of = [&](const PoolView &pool, int page, int j) {
+        return reinterpret_cast<const C *>(row_ptr(p.c, pool, page, j, c.h)) + PER * lane;
+    };
 #pragma unroll 1
-    for (int r = tid >> 5; r < live; r += AR_ROWS / 32) {
+    for (int r = tid >> 5; r < live; r += RowsWarps<COLS>::SOFTMAX / 32) {
         const int token = (row0 + r) / p.group, g = row0 + r - token * p.group;
         const int64_t at = ((static_cast<int64_t>(c.b) * p.w.T + token) * p.q_heads + c.h * p.group + g) * D + PER * lane;
+        const unsigned long long see =
+            token < c.s.fresh ? visible_mask(p.parent ? p.parent + static_cast<int64_t>(c.b) * p.w.T : nullptr, token) : 0ull;
+        if (see == 0) continue;
         T *out = static_cast<T *>(p.out) + at;
         float *piece = part + 2 * AR_ROWS + r * D + PER * lane;
-        unsigned nan = 0;
+        unsigned redo = 0;
 #pragma unroll
         for (int e = 0; e < PER; ++e) {
             const float y = whole ? Num<T>::up(out[e]) : piece[e];
-            if (y != y) nan |= 1u << e;
+            if (y != y) redo |= 1u << e;
         }
-        if (!__any_sync(0xffffffffu, nan != 0)) continue;
-        const unsigned long long see =
-            token < c.s.fresh ? visible_mask(p.parent ? p.parent + static_cast<int64_t>(c.b) * p.w.T : nullptr, token) : 0ull;
+#pragma unroll 1
+        for (int j = max(c.s.ctx, t0 * AR_KEYS); j < end; ++j) {
+            const int page = page_of(p.c, table, j);
+            if (page < 0 || !(see >> (j - c.s.ctx) & 1)) continue;
+            const C *v = row_of(p.c.v, page, j);
+#pragma unroll
+            for (int e = 0; e < PER; ++e)
+                if (!(fabsf(Num<C>::up(v[e])) < CUDART_INF_F)) redo |= 1u << e;
+        }
+        if (!__any_sync(0xffffffffu, redo != 0)) continue;
         float m = -CUDART_INF_F, l = 0.0f, q[PER], x[PER];
 #pragma unroll
         for (int e = 0; e < PER; ++e) {
             q[e] = Num<T>::up(static_cast<const T *>(p.q)[at + e]);
             x[e] = 0.0f;
         }
-        bool fine = see != 0;
-        const int end = min(t1 * AR_KEYS, c.s.total);
+        bool fine = true;
 #pragma unroll 1
         for (int j = t0 * AR_KEYS; fine && j < end; ++j) {
             const int page = page_of(p.c, table, j);
             fine = page >= 0;
             if (!fine || (j >= c.s.ctx && !(see >> (j - c.s.ctx) & 1))) continue;
-            const T *k = reinterpret_cast<const T *>(row_ptr(p.c, p.c.k, page, j, c.h)) + PER * lane;
-            const T *v = reinterpret_cast<const T *>(row_ptr(p.c, p.c.v, page, j, c.h)) + PER * lane;
+            const C *k = row_of(p.c.k, page, j), *v = row_of(p.c.v, page, j);
             float s = 0.0f;
 #pragma unroll
-            for (int e = 0; e < PER; ++e) s += q[e] * Num<T>::up(k[e]);
+            for (int e = 0; e < PER; ++e) s += q[e] * Num<C>::up(k[e]);
 #pragma unroll
             for (int o = 16; o; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
-            s *= p.scale_log2;
+            s *= factor;
             fine = s == s;
             if (!fine || s == -CUDART_INF_F) continue;
             if (s > m) {
@@ -505,13 +521,13 @@ template <typename T, int D, int COLS> __device__ void rows_again(const AttParam
             const float w = fast_exp2(s - m);
             l += w;
 #pragma unroll
-            for (int e = 0; e < PER; ++e) x[e] += w * Num<T>::up(v[e]);
+            for (int e = 0; e < PER; ++e) x[e] += w * Num<C>::up(v[e]);
         }
         if (!fine || l == 0.0f) continue;
-        const float unit = whole ? 1.0f / l : fast_exp2(m - part[r]);
+        const float unit = whole ? (p.c.v_scale ? __ldg(p.c.v_scale + c.h) : 1.0f) / l : fast_exp2(m - part[r]);
 #pragma unroll
         for (int e = 0; e < PER; ++e) {
-            if (!(nan >> e & 1)) continue;
+            if (!(redo >> e & 1)) continue;
             if (whole)
                 out[e] = Num<T>::down(x[e] * unit);
             else
@@ -521,11 +537,12 @@ template <typename T, int D, int COLS> __device__ void rows_again(const AttParam
 }
 
 // The block's whole range; out of line, away from the loops that have to fit the
-// instruction caches.
-template <typename T, int D, int COLS> __device__ __noinline__ void rows_walk_again(const AttParams &p, long long begin, int tid)
+// instruction caches.  (What few lines of it stood in the rows' epilogue cost the
+// verify batch up to 25 us by the place alone that the loops then had.)
+template <typename T, typename C, int D, int COLS> __device__ __noinline__ void rows_walk_again(const AttParams &p, long long begin, int tid)
 {
     for (Cursor c = find_range(p.w, p.c, blockIdx.x, gridDim.x, tid & 31); c.at < c.end; next_item(c, p.w, p.c))
-        rows_again<T, D, COLS>(p, c, begin, tid);
+        rows_again<T, C, D, COLS>(p, c, begin, tid);
 }
 
 // COLS: rows of a copy, and its keys of a tile; a thread takes these, or half of them.
@@ -543,7 +560,7 @@ __device__ void rows_softmax(const AttParams &p, Cursor c, char *smem, RowsCtl *
                    tm_p = ctl->tmem + quarter + 256 + copy * (COLS / 2) + half * (KEYS / 2), tm_o = ctl->tmem + quarter + 384;
     const long long begin = c.at;
     // An infinity in a cached slot of V, which all rows see, meets a weight of 0 in the copies that do not have its key:
-    // rows with NaN are looked at again when the range is done.  (Looking for NaN costs the verify batch 4 us of 236.)
+    // rows with NaN are looked at again when the range is done.
     constexpr bool LOOK_AGAIN = COPIES > 1 && !S::WIDEN;
     // the keys of other copies never get a probability
     if (COPIES > 1) {
@@ -564,7 +581,6 @@ __device__ void rows_softmax(const AttParams &p, Cursor c, char *smem, RowsCtl *
         unsigned long long see = 0;
         float m = -CUDART_INF_F, l = 0.0f;
         float factor = p.scale_log2 * (p.c.k_scale ? __ldg(p.c.k_scale + c.h) : 1.0f);
-        unsigned long long odd = 0;
         bool any_bad = c.s.bad, ok = true;
         const int place = item & 1;
         using Merge = RowsMerge<D>;
@@ -655,7 +671,7 @@ __device__ void rows_softmax(const AttParams &p, Cursor c, char *smem, RowsCtl *
             }
             if (ok) ok = rows_wait(ctl, &ctl->o_done[(n - 1) & 1], ((n - 1) >> 1) & 1, err);
             tc_fence_after();
-            odd = *reinterpret_cast<volatile unsigned long long *>(&ctl->odd[item_flags(item)]);
+            if (tid == 0 && *reinterpret_cast<volatile int *>(&ctl->odd[item_flags(item)])) *reinterpret_cast<volatile int *>(&ctl->lost) = 1;
             any_bad |= *reinterpret_cast<volatile int *>(&ctl->bad[item_flags(item)]) != 0;
             rows_sync<W::SOFTMAX>();  // all have read them, and all scores
         }
@@ -749,27 +765,6 @@ __device__ void rows_softmax(const AttParams &p, Cursor c, char *smem, RowsCtl *
                 const float any = (sum[0] + sum[1]) + (sum[2] + sum[3]);
                 if (any != any) *reinterpret_cast<volatile int *>(&ctl->lost) = 1;
             }
-            if (odd) {
-                // New tokens whose v has infinities or NaN (cleared for the product): for the rows that see them.
-                for (unsigned long long left = odd & see; left; left &= left - 1) {
-                    const int j = c.s.ctx + __ffsll(left) - 1;
-                    const int page = page_of(p.c, p.c.table + static_cast<int64_t>(c.b) * p.c.max_pages, j);
-                    if (page < 0) continue;
-                    const C *k = reinterpret_cast<const C *>(row_ptr(p.c, p.c.k, page, j, c.h));
-                    const C *v = reinterpret_cast<const C *>(row_ptr(p.c, p.c.v, page, j, c.h));
-                    const T *q = static_cast<const T *>(p.q) +
-                                 ((static_cast<int64_t>(c.b) * p.w.T + token) * p.q_heads + c.h * p.group + (row0 + r) % p.group) * D;
-                    float s = 0.0f;
-                    for (int d = 0; d < D; ++d) s += Num<T>::up(q[d]) * Num<C>::up(k[d]);
-                    const float w = fast_exp2(s * p.scale_log2 * (p.c.k_scale ? __ldg(p.c.k_scale + c.h) : 1.0f) - base);
-                    if (w == 0.0f) continue;
-#pragma unroll
-                    for (int e = 0; e < 32; ++e) {
-                        const float y = Num<C>::up(v[d0 + e]);
-                        if (!(fabsf(y) < CUDART_INF_F)) x[e] += w * y;
-                    }
-                }
-            }
             // 32 bytes a store: a thread's row is its own, and half a sector at a time cost twice the transactions
             if (!whole) {
 #pragma unroll
@@ -803,10 +798,8 @@ __device__ void rows_softmax(const AttParams &p, Cursor c, char *smem, RowsCtl *
         rows_sync<W::SOFTMAX>();
         if (stop) break;
     }
-    if constexpr (LOOK_AGAIN) {
-        if (*reinterpret_cast<volatile int *>(&ctl->lost) && !*reinterpret_cast<volatile int *>(&ctl->dead))
-            rows_walk_again<T, D, COLS>(p, begin, tid);
-    }
+    if (*reinterpret_cast<volatile int *>(&ctl->lost) && !*reinterpret_cast<volatile int *>(&ctl->dead))
+        rows_walk_again<T, C, D, COLS>(p, begin, tid);
 }
 
 template <typename T, typename C, int D, int COLS>
