@@ -489,7 +489,8 @@ spv_status spv_rope_append(const void *q, const void *k, const void *v, spv_dtyp
  * key head; like the other calls here they are launched so that their blocks
  * may start while the kernel before them in the stream ends, and wait for its
  * results before they read anything.  A bounded wait that gives up records SPV_ERR_TIMEOUT in the workspace's
- * error word and leaves NaN in the rows that it cost.
+ * error word and leaves NaN in out and lse of the rows that it cost; row_status[b] is SPV_ERR_TIMEOUT where that is
+ * so of the first rows of sequence b's first head.
  * Tokens t >= new_lens[b], and tree nodes whose path to the root has a parent
  * outside [0, node): rows that see nothing.  Bad sequences: out and lse NaN.
  * The result does not depend on the order in which the GPU runs the blocks.
@@ -576,6 +577,15 @@ spv_status spv_workspace_status(const void *workspace, void *stream);
  * Returns SPV_OK once enqueued.
  */
 spv_status spv_selftest_timeout(void *workspace, size_t workspace_bytes, unsigned polls, void *stream);
+
+/*
+ * spv_selftest_give_up -- in the following spv_paged_attention calls of this
+ * process a wait gives up in block `block` of the kernel, at the
+ * item-th (sequence, key head, row tile) that it has keys of: what a call
+ * leaves then can be checked without a wait that runs out.  Calls of few rows
+ * a key head have no such wait.  block -1 ends it.  HOST function.
+ */
+spv_status spv_selftest_give_up(int block, int item);
 
 /* Human-readable name of a status code (static string). */
 const char *spv_status_string(spv_status s);

@@ -87,6 +87,8 @@ def load_library():
     lib.spv_workspace_status.argtypes = [P, P]
     lib.spv_selftest_timeout.argtypes = [P, S, ctypes.c_uint, P]
     lib.spv_selftest_timeout.restype = I
+    lib.spv_selftest_give_up.argtypes = [I, I]
+    lib.spv_selftest_give_up.restype = I
     lib.spv_workspace_status.restype = I
     lib.spv_status_string.argtypes = [I]
     lib.spv_status_string.restype = ctypes.c_char_p
@@ -190,6 +192,12 @@ def spv_selftest_timeout(workspace: torch.Tensor, polls: int = 20000, stream=Non
     st = load_library().spv_selftest_timeout(_ptr(workspace), workspace.numel() * workspace.element_size(),
                                              int(polls), _stream(stream, workspace.device))
     _check(st, "spv_selftest_timeout")
+
+
+def spv_selftest_give_up(block: int, item: int = 0) -> None:
+    """From now on a wait gives up in this block of the attention calls' kernels, at its item-th item; block -1 ends it
+    (see spv_selftest_give_up in spv.h)."""
+    _check(load_library().spv_selftest_give_up(int(block), int(item)), "spv_selftest_give_up")
 
 
 @_on_its_stream

@@ -401,6 +401,7 @@ cudaError_t launch_attention(const AttentionLaunch &L, cudaStream_t st)
     p.q_heads = k.q_heads;
     p.rows = k.T * p.group;
     p.scale_log2 = k.scale * LOG2E;
+    p.give_up = give_up();
     char *ws = static_cast<char *>(L.ws);
     p.error = reinterpret_cast<unsigned *>(ws);
     p.split = reinterpret_cast<SplitItem *>(ws + WS_HEADER);

@@ -22,6 +22,7 @@ struct AttParams {
     float *parts;             // [block][2] pieces: m and l of each row, then o
     int q_heads, group, rows;
     float scale_log2;
+    GiveUp give_up;
 };
 
 // The weights of a product in M are 2^(s - (m - UP)), m the running maximum, which may lag the largest score by LAG: at

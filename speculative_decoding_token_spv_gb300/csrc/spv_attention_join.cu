@@ -148,7 +148,7 @@ template <typename T, int D> __global__ void __launch_bounds__(32 * JOIN_WARPS) 
                     write_row<T, D>(p, s.rows, r, e * 32 + 4 * lane, make_float4(x[e], x[e + 1], x[e + 2], x[e + 3]), m, l, v_scale);
             }
             if (lane == 0 && r == 0 && p.row_status && s.rows.h == 0 && s.rows.row0 == 0)
-                p.row_status[s.rows.b] = m != m ? KV_STATUS_BAD : 0;
+                p.row_status[s.rows.b] = m == m ? 0 : __ldcg(p.error) ? STATUS_TIMEOUT : KV_STATUS_BAD;
         }
     }
 }

@@ -30,7 +30,8 @@
 // took 94 us, and the ends of items.
 //
 // Every wait is bounded; one that gives up records SPV_ERR_TIMEOUT in the
-// workspace, ends the block in order and leaves NaN in what it had to write.
+// workspace, ends the block in order and leaves NaN in all that it still had to
+// write, the pieces of shared items among them.
 #include "spv_attention.cuh"
 #include "spv_tcgen.cuh"
 #include "spv_tma.cuh"
@@ -296,8 +297,8 @@ __device__ void rows_load(const AttParams &p, Cursor c, char *smem, RowsCtl *ctl
         }
     }
     asm volatile("cp.async.wait_all;" ::: "memory");
-    if (map && !ok)  // the copy engine's, before the block may end
-        for (int t = max(0, n - NST); t < n; ++t) mbar_wait(&full[t % NST], (t / NST) & 1);
+    if (map && w == 0)  // the copy engine's, before the block may end: nobody else may have waited for them
+        for (int t = max(0, n - NST); t < n; ++t) mbar_drain(&full[t % NST], (t / NST) & 1);
     if (S::WIDEN)  // the tiles still on their way
         for (int t = n >= NST ? n - NST : 0; ok && t < n; ++t) ok = widen(t);
 }
@@ -375,6 +376,11 @@ __device__ void rows_prepare(const AttParams &p, Cursor c, char *smem, RowsCtl *
     int item = 0;
     for (; c.at < c.end; next_item(c, p.w, p.c)) {
         if (first_tile(c) == last_tile(c)) continue;
+        if (item == p.give_up.item && static_cast<int>(blockIdx.x) == p.give_up.block) {  // the self-test
+            *reinterpret_cast<volatile int *>(&ctl->dead) = 1;
+            atomicExch(err, static_cast<unsigned>(STATUS_TIMEOUT));
+            return;
+        }
         const int place = item & 1, row0 = c.row_tile * COLS, live = min(COLS, p.rows - row0);
         char *qs = smem + S::Q_AT + place * S::TILE;
         if (item >= 2 && !rows_wait(ctl, &ctl->q_empty[place], ((item >> 1) - 1) & 1, err)) return;
@@ -536,13 +542,45 @@ __device__ __forceinline__ void rows_again(const AttParams &p, const Cursor &c, 
     }
 }
 
-// The block's whole range; out of line, away from the loops that have to fit the
-// instruction caches.  (What few lines of it stood in the rows' epilogue cost the
-// verify batch up to 25 us by the place alone that the loops then had.)
-template <typename T, typename C, int D, int COLS> __device__ __noinline__ void rows_walk_again(const AttParams &p, long long begin, int tid)
+// What is left of a block's range, from an item's beginning on, after a wait
+// gave up: NaN for every row, the pieces of a shared item among them.  Items
+// without keys have what they always have.
+template <typename T, int D, int COLS> __device__ __forceinline__ void rows_lost(const AttParams &p, Cursor c, int tid)
 {
-    for (Cursor c = find_range(p.w, p.c, blockIdx.x, gridDim.x, tid & 31); c.at < c.end; next_item(c, p.w, p.c))
-        rows_again<T, C, D, COLS>(p, c, begin, tid);
+    constexpr int THREADS = RowsWarps<COLS>::SOFTMAX;
+    for (; c.at < c.end; next_item(c, p.w, p.c)) {
+        const AttRows rows{c.b, c.h, c.row_tile * COLS, min(COLS, p.rows - c.row_tile * COLS)};
+        const bool empty = c.s.total == 0 && !c.s.bad;
+        if (c.s.total == 0 || c.end >= c.first + c.tiles) {  // whole
+            const float m = empty ? -CUDART_INF_F : CUDART_NAN_F;
+            for (int i = tid; i < rows.live * (D / 4); i += THREADS)
+                write_row<T, D>(p, rows, i / (D / 4), i % (D / 4) * 4, make_float4(0.0f, 0.0f, 0.0f, 0.0f), m, 0.0f, 1.0f);
+            if (tid == 0 && p.row_status && c.h == 0 && c.row_tile == 0)
+                p.row_status[c.b] = c.s.bad ? KV_STATUS_BAD : empty ? 0 : STATUS_TIMEOUT;
+        } else {  // a piece in the second place; its maximum is enough
+            float *part = p.parts + (static_cast<int64_t>(blockIdx.x) * 2 + 1) * (AR_ROWS * (D + 2));
+            for (int r = tid; r < rows.live; r += THREADS) {
+                part[r] = CUDART_NAN_F;
+                part[AR_ROWS + r] = 0.0f;
+            }
+            note_split(p, c, rows, c.first, tid);
+        }
+    }
+}
+
+// The items that begin before tile `done`, again; then, where that is not the
+// range's end, NaN for those behind the one that a wait cost.  Out of line, away
+// from the loops that have to fit the instruction caches.  (What few lines of it
+// stood in the rows' epilogue cost the verify batch up to 25 us by the place
+// alone that the loops then had.)
+template <typename T, typename C, int D, int COLS>
+__device__ __noinline__ void rows_finish(const AttParams &p, long long begin, long long done, int tid)
+{
+    Cursor c = find_range(p.w, p.c, blockIdx.x, gridDim.x, tid & 31);
+    for (; c.at < done; next_item(c, p.w, p.c)) rows_again<T, C, D, COLS>(p, c, begin, tid);
+    if (c.at >= c.end) return;
+    next_item(c, p.w, p.c);
+    rows_lost<T, D, COLS>(p, c, tid);
 }
 
 // COLS: rows of a copy, and its keys of a tile; a thread takes these, or half of them.
@@ -790,7 +828,7 @@ __device__ void rows_softmax(const AttParams &p, Cursor c, char *smem, RowsCtl *
         if (!whole)
             note_split(p, c, rows, begin, tid);
         else if (tid == 0 && p.row_status && c.h == 0 && c.row_tile == 0)
-            p.row_status[c.b] = any_bad ? KV_STATUS_BAD : 0;
+            p.row_status[c.b] = c.s.bad ? KV_STATUS_BAD : stop ? STATUS_TIMEOUT : any_bad ? KV_STATUS_BAD : 0;
         if (tiles) {
             mbar_arrive(&ctl->q_empty[place]);
             ++item;
@@ -798,8 +836,8 @@ __device__ void rows_softmax(const AttParams &p, Cursor c, char *smem, RowsCtl *
         rows_sync<W::SOFTMAX>();
         if (stop) break;
     }
-    if (*reinterpret_cast<volatile int *>(&ctl->lost) && !*reinterpret_cast<volatile int *>(&ctl->dead))
-        rows_walk_again<T, C, D, COLS>(p, begin, tid);
+    // c.at before the end: a wait gave up
+    if (*reinterpret_cast<volatile int *>(&ctl->lost) || c.at < c.end) rows_finish<T, C, D, COLS>(p, begin, c.at, tid);
 }
 
 template <typename T, typename C, int D, int COLS>
@@ -862,10 +900,9 @@ __global__ void __launch_bounds__(RowsWarps<COLS>::THREADS, 1)
                 rows_scores<T, C, D>(p, c, smem, ctl, err);
             else
                 rows_outputs<T, C, D>(p, c, smem, ctl, err);
-            if (*reinterpret_cast<volatile int *>(&ctl->dead)) {  // let what was issued end
-                tc_commit(&ctl->spare[role]);
-                mbar_wait(&ctl->spare[role], 0);
-            }
+            // what was issued ends before the block may: others may have given up on it
+            tc_commit(&ctl->spare[role]);
+            mbar_drain(&ctl->spare[role], 0);
         }
         __syncwarp();
         if (role >= 2) rows_prepare<T, C, D, COLS>(p, c, smem, ctl, err, tid - W::SOFTMAX - 64);

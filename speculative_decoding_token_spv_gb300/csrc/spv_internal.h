@@ -146,6 +146,13 @@ struct EvictLaunch {
     int64_t out_stride;
     int32_t *new_lens, *slot_src;
 };
+// Self-test: in block `block` of an attention or mass kernel a wait gives up at
+// its item `item` (block -1: nowhere).
+struct GiveUp {
+    int block, item;
+};
+GiveUp give_up();
+
 inline int log2_of(int pow2)
 {
     int s = 0;

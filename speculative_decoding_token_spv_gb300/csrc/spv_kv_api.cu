@@ -4,6 +4,7 @@
 #include "spv.h"
 #include "spv_internal.h"
 
+#include <atomic>
 #include <cmath>
 #include <cstdint>
 
@@ -62,9 +63,26 @@ spv::KvLaunch kv_launch(const spv_kv_cache *cache, const int32_t *page_table, in
                          row_status};
 }
 
+std::atomic<int64_t> give_up_at{-1};  // block << 32 | item
+
 }  // namespace
 
+namespace spv {
+GiveUp give_up()
+{
+    const int64_t x = give_up_at.load(std::memory_order_relaxed);
+    return GiveUp{static_cast<int>(x >> 32), static_cast<int>(x & 0x7fffffff)};
+}
+}  // namespace spv
+
 extern "C" {
+
+spv_status spv_selftest_give_up(int block, int item)
+{
+    if (block < -1 || item < 0) return SPV_ERR_INVALID_ARG;
+    give_up_at.store(block < 0 ? -1 : static_cast<int64_t>(block) << 32 | item, std::memory_order_relaxed);
+    return SPV_OK;
+}
 
 spv_status spv_rope_frequencies(int rotary_dim, double base, int scaling, double factor, double low, double high,
                                 double original_len, uint64_t *out)

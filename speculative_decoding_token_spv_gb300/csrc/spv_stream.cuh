@@ -36,6 +36,7 @@ constexpr int NCW = 8;                        // consumer warps (one block each)
 constexpr int THREADS = (NCW + 1) * 32;       // + one producer warp
 constexpr int RING_BYTES_PER_SM = 192 * 1024; // shared-memory ring of all resident CTAs of an SM
 constexpr uint32_t WAIT_LIMIT = 1u << 22;     // try_wait polls before giving up
+constexpr uint32_t DRAIN_LIMIT = 10000;       // polls, 0.2 us apart, for copies and products to land
 constexpr int SKIP_TABLE_MAX = 1024;          // sequences whose row-skip table fits shared memory (8 KB)
 constexpr int MAX_TRIALS = 64;                // residual rejection trials
 constexpr int STATUS_BAD_ROW = 4;
@@ -158,6 +159,24 @@ __device__ __forceinline__ bool mbar_wait(uint64_t *bar, uint32_t parity)
     for (uint32_t i = 0; i < WAIT_LIMIT; ++i)
         if (mbar_try_wait(bar, parity)) return true;
     return false;
+}
+
+// A short wait for work that is on its way and needs nobody else -- copies,
+// products -- before a block may end: about 2 ms at most.
+__device__ __forceinline__ void mbar_drain(uint64_t *bar, uint32_t parity)
+{
+    for (uint32_t i = 0; i < DRAIN_LIMIT; ++i) {
+        uint32_t ok;
+        asm volatile(
+            "{\n\t.reg .pred p;\n\t"
+            "mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+            "selp.u32 %0, 1, 0, p;\n\t}"
+            : "=r"(ok)
+            : "r"(smem_u32(bar)), "r"(parity)
+            : "memory");
+        if (ok) return;
+        __nanosleep(200);
+    }
 }
 
 __device__ __forceinline__ unsigned ld_acquire_gpu(const unsigned *p)

@@ -218,3 +218,50 @@ def test_infinities_in_cached_v_are_seen(spv, T, G, D, dtype):
     assert torch.equal(torch.isnan(got["out"]), torch.isnan(want))
     assert torch.equal(got["out"].nan_to_num(nan=0.5), want.nan_to_num(nan=0.5))
     assert torch.equal(got["lse"], clean["lse"])
+
+
+@pytest.fixture
+def gives_up(spv):
+    yield spv.spv_selftest_give_up
+    spv.spv_selftest_give_up(-1)
+
+
+@pytest.mark.parametrize("T, G, kv", [(5, 4, "bf16"), (12, 4, "bf16"), (24, 4, "bf16"), (12, 4, "e4m3"), (24, 4, "e4m3")])
+@pytest.mark.parametrize("page", [16, 2])
+def test_attention_after_a_wait_gave_up(spv, gives_up, T, G, kv, page):
+    """What a block still had to write is NaN, the pieces of items that it shares among them, the rest is as ever, and the
+    workspace says so; nothing is left of what the outputs and the workspace held."""
+    gen = torch.Generator().manual_seed(56)
+    ctx = torch.randint(0, 500, (300,), generator=gen).tolist()
+    ctx[20], ctx[250] = 6000, 3000
+    a = Layer(spv, 57, ctx, None, T, 2 * G, 2, 64, page, dtype="bf16", kv=kv)
+    ws = spv.new_workspace(spv.spv_attention_workspace_bytes(a.B, T, 2 * G, 2, 64), "cuda")
+    q, table, at = a.q.cuda(), a.table.cuda(), i32(ctx)
+
+    def run():
+        out = {"out": torch.full_like(q, 7.0), "lse": torch.full((a.B, T, 2 * G), 7.0, device="cuda"),
+               "row_status": torch.full((a.B,), 7, dtype=torch.int32, device="cuda")}
+        spv.spv_paged_attention(q, a.cache, table, at, workspace=ws, out=out, want_lse=True)
+        torch.cuda.synchronize()
+        return out
+
+    good = run()
+    assert (good["row_status"] == 0).all() and torch.isfinite(good["out"]).all()
+    for block, item in ((0, 0), (1, 1), (77, 0), (77, 2), (151, 1)):
+        gives_up(block, item)
+        got = run()
+        gives_up(-1)
+        gone = torch.isnan(got["lse"])
+        assert gone.any() and not gone.all()
+        assert spv.spv_workspace_status(ws) == spv.SPV_ERR_TIMEOUT
+        assert torch.isnan(got["out"][gone]).all()
+        assert torch.equal(got["out"][~gone], good["out"][~gone]) and torch.equal(got["lse"][~gone], good["lse"][~gone])
+        assert torch.equal(got["row_status"] == spv.SPV_ERR_TIMEOUT, gone[:, 0, 0])
+        assert ((got["row_status"] == 0) | (got["row_status"] == spv.SPV_ERR_TIMEOUT)).all()
+        ws.zero_()
+        again = run()
+        assert spv.spv_workspace_status(ws) == spv.SPV_OK
+        assert torch.equal(again["out"], good["out"]) and torch.equal(again["lse"], good["lse"])
+        assert (again["row_status"] == 0).all()
+    with pytest.raises(spv.SpvError):
+        gives_up(-2)

@@ -222,3 +222,8 @@ def test_cache_struct_matches_header(spv):
     from speculative_decoding_token_spv_gb300 import kv
     assert names == [n for n, _ in kv._CacheStruct._fields_]
     assert ctypes.sizeof(kv._CacheStruct) == 8 * 2 + 4 * 5 + 4 + 8 * 6 + 8 * 2
+
+
+def test_give_up_arguments(spv):
+    f = spv.load_library().spv_selftest_give_up
+    assert f(-2, 0) == INV and f(0, -1) == INV and f(-1, 0) == 0
