@@ -520,7 +520,8 @@ size_t spv_attention_workspace_bytes(int B, int T, int q_heads, int kv_heads, in
  *   row_status   [B] optional
  * Bad sequences (also: accept_count outside [-1, T - 1], a counted node
  * outside [0, T), ctx + new > mass_stride): nothing is written; slots of a bad page: neither.
- * A bounded wait that gives up: SPV_ERR_TIMEOUT in row_status of the sequences that it cost.
+ * A bounded wait that gives up: NaN in the entries of mass_out that it cost, and SPV_ERR_TIMEOUT in row_status of
+ * their sequences.  (With row_status a small kernel of its own goes before the other.)
  */
 spv_status spv_attention_mass(const void *q, spv_dtype dtype, int B, int T, int q_heads, const float *lse,
                               const spv_kv_cache *cache, const int32_t *page_table, int max_pages,
@@ -579,11 +580,11 @@ spv_status spv_workspace_status(const void *workspace, void *stream);
 spv_status spv_selftest_timeout(void *workspace, size_t workspace_bytes, unsigned polls, void *stream);
 
 /*
- * spv_selftest_give_up -- in the following spv_paged_attention calls of this
- * process a wait gives up in block `block` of the kernel, at the
- * item-th (sequence, key head, row tile) that it has keys of: what a call
- * leaves then can be checked without a wait that runs out.  Calls of few rows
- * a key head have no such wait.  block -1 ends it.  HOST function.
+ * spv_selftest_give_up -- in the following spv_paged_attention and
+ * spv_attention_mass calls of this process a wait gives up in block `block` of
+ * the kernel, at the item-th (sequence, key head, row tile) that it has keys of: what a call
+ * leaves then can be checked without a wait that runs out.  Attention of few
+ * rows a key head has no such wait.  block -1 ends it.  HOST function.
  */
 spv_status spv_selftest_give_up(int block, int item);
 

@@ -195,7 +195,7 @@ def spv_selftest_timeout(workspace: torch.Tensor, polls: int = 20000, stream=Non
 
 
 def spv_selftest_give_up(block: int, item: int = 0) -> None:
-    """From now on a wait gives up in this block of the attention calls' kernels, at its item-th item; block -1 ends it
+    """From now on a wait gives up in this block of the attention and mass kernels, at its item-th item; block -1 ends it
     (see spv_selftest_give_up in spv.h)."""
     _check(load_library().spv_selftest_give_up(int(block), int(item)), "spv_selftest_give_up")
 

@@ -20,8 +20,10 @@
 // loaded it); three warps bring q and the rows' constants an item ahead; one
 // thread issues the products; four warps, a key a thread, sum and write.
 //
-// Every wait is bounded; one that gives up ends the block in order and leaves
-// SPV_ERR_TIMEOUT in the row_status of the sequence that it was at.
+// Every wait is bounded; one that gives up ends the block in order: the weights
+// that it still had to write become NaN, and the row_status of their sequences
+// SPV_ERR_TIMEOUT.  So that no other block can overwrite that, a small kernel
+// before this one writes all statuses.
 #include "spv_mma.cuh"
 #include "spv_tcgen.cuh"
 
@@ -43,6 +45,7 @@ struct MassParams {
     int32_t *row_status;
     int q_heads, group;
     float scale_log2, decay;
+    GiveUp give_up;
 };
 
 // Which new tokens of sequence b count; *bad if what says so is out of range.
@@ -84,6 +87,21 @@ struct Counted {
         rows = bad || c.s.total == 0 ? 0 : __popcll(tokens) * p.group;
     }
 };
+
+// row_status of every sequence, a block each.
+__global__ void __launch_bounds__(128) mass_status_kernel(const MassParams p)
+{
+    const int b = blockIdx.x;
+    chain_begin();
+    const SeqLens s = seq_lens(p.w.ctx_lens, p.w.new_lens, b, p.w.T, p.c, p.w.idle);
+    bool bad = s.bad || s.total > p.stride;
+    counted_tokens(p, b, &bad);
+    const int32_t *table = p.c.table + static_cast<int64_t>(b) * p.c.max_pages;
+    int any = bad;
+    for (int g = threadIdx.x; s.total > 0 && g <= (s.total - 1) >> p.c.page_shift; g += 128) any |= page_of(p.c, table, g << p.c.page_shift) < 0;
+    any = __syncthreads_or(any);
+    if (threadIdx.x == 0) p.row_status[b] = any ? KV_STATUS_BAD : 0;
+}
 
 // ROWS rows at once; more go in several passes over the item's tiles.
 template <typename C, int D> struct MassShape {
@@ -232,10 +250,14 @@ __device__ void mass_prepare(const MassParams &p, Cursor c, char *smem, Ctl *ctl
     using M = typename MmaOf<T, C>::type;
     constexpr int CH = D / 8, STEP = 96 / CH, AHEAD = 6;  // rows at a time, loads of a thread on their way together
     Counted count;
-    int unit_no = 0;
+    int unit_no = 0, item = 0;
     for (; c.at < c.end; next_item(c, p.w, p.c)) {
         count.at(p, c);
         if (count.rows == 0 || mass_first(c) == mass_last(c)) continue;
+        if (item++ == p.give_up.item && static_cast<int>(blockIdx.x) == p.give_up.block) {  // the self-test
+            *reinterpret_cast<volatile int *>(&ctl->dead) = 1;
+            return;
+        }
         const float unit = p.scale_log2 * (p.c.k_scale ? __ldg(p.c.k_scale + c.h) : 1.0f);
         for (int r0 = 0; r0 < count.rows; r0 += S::ROWS, ++unit_no) {
             const int place = unit_no & 1, live = min(S::ROWS, count.rows - r0), padded = (live + 15) & ~15;
@@ -341,8 +363,11 @@ __device__ void mass_multiply(const MassParams &p, Cursor c, char *smem, Ctl *ct
     }
 }
 
-// Four warps, a key of the tile a thread.
-template <typename Shape, typename Ctl> __device__ void mass_sum(const MassParams &p, Cursor c, Ctl *ctl, int tid)
+// Four warps, a key of the tile a thread.  Returns the tile up to which the
+// range is done: where its item began, if a wait gave up.  A warp that leaves so
+// arrives on no barrier any more: 32 arrivals where a barrier lacks fewer (q's
+// lacks 129) end in a fault.
+template <typename Shape, typename Ctl> __device__ long long mass_sum(const MassParams &p, Cursor c, Ctl *ctl, int tid)
 {
     constexpr int ROWS = Shape::ROWS;
     const int lane = tid & 31, warp = tid >> 5;
@@ -353,13 +378,6 @@ template <typename Shape, typename Ctl> __device__ void mass_sum(const MassParam
         count.at(p, c);
         const int32_t *table = p.c.table + static_cast<int64_t>(c.b) * p.c.max_pages;
         const int t0 = mass_first(c), t1 = mass_last(c);
-        if (p.row_status && t0 == 0 && c.h == 0 && warp == 0) {  // one warp: no barrier between warps that may leave early
-            int any = count.bad;
-            for (int g = lane; c.s.total > 0 && g <= (c.s.total - 1) >> p.c.page_shift; g += 32)
-                any |= page_of(p.c, table, g << p.c.page_shift) < 0;
-            any = __any_sync(0xffffffffu, any);
-            if (lane == 0) p.row_status[c.b] = any ? KV_STATUS_BAD : 0;
-        }
         if (count.bad) continue;
         const int64_t out_row = (static_cast<int64_t>(c.b) * p.c.kv_heads + c.h) * p.stride;
         auto page_for = [&](int tile) {  // -1: nothing is written
@@ -380,7 +398,7 @@ template <typename Shape, typename Ctl> __device__ void mass_sum(const MassParam
             const int live = min(ROWS, count.rows - r0), place = unit_no & 1;
             bool careful = false;
             if (live > 0 && t0 < t1) {
-                if (!mass_wait(ctl, &ctl->q_full[place], (unit_no >> 1) & 1)) return;
+                if (!mass_wait(ctl, &ctl->q_full[place], (unit_no >> 1) & 1)) return c.at;
                 careful = *reinterpret_cast<volatile int *>(&ctl->careful[place]) == unit_no + 1;
             }
             for (int tile = t0; tile < t1; ++tile) {
@@ -390,10 +408,7 @@ template <typename Shape, typename Ctl> __device__ void mass_sum(const MassParam
                 had = mass_for(tile + 1);
                 float sum = 0.0f;
                 if (live > 0) {
-                    if (!mass_wait(ctl, &ctl->s_full[n % MASS_BUFFERS], (n / MASS_BUFFERS) & 1)) {
-                        if (tid == 0 && p.row_status) p.row_status[c.b] = STATUS_TIMEOUT;
-                        return;
-                    }
+                    if (!mass_wait(ctl, &ctl->s_full[n % MASS_BUFFERS], (n / MASS_BUFFERS) & 1)) return c.at;
                     tc_fence_after();
                     __syncwarp();
                     float s0 = 0.0f, s1 = 0.0f;
@@ -438,6 +453,28 @@ template <typename Shape, typename Ctl> __device__ void mass_sum(const MassParam
             }
         }
     }
+    return c.at;
+}
+
+// The items from tile `done` on, after a wait gave up: NaN where rows count, what
+// does not depend on them as ever.  No barrier is touched any more.
+__device__ __noinline__ void mass_lost(const MassParams &p, long long done, int tid)
+{
+    Counted count;
+    for (Cursor c = find_range(p.w, p.c, blockIdx.x, gridDim.x, tid & 31); c.at < c.end; next_item(c, p.w, p.c)) {
+        if (c.at < done) continue;
+        count.at(p, c);
+        if (count.bad) continue;
+        const int32_t *table = p.c.table + static_cast<int64_t>(c.b) * p.c.max_pages;
+        const int64_t out_row = (static_cast<int64_t>(c.b) * p.c.kv_heads + c.h) * p.stride;
+        const int end = min(mass_last(c) * MASS_KEYS, c.s.total);
+        for (int j = mass_first(c) * MASS_KEYS + tid; j < end; j += MASS_KEYS) {
+            if (page_of(p.c, table, j) < 0) continue;
+            const float old = p.mass_in && j < c.s.ctx ? p.mass_in[out_row + j] : 0.0f;
+            p.mass_out[out_row + j] = count.rows > 0 ? CUDART_NAN_F : old * p.decay;
+        }
+        if (count.rows > 0 && mass_first(c) < mass_last(c) && tid == 0 && p.row_status) p.row_status[c.b] = STATUS_TIMEOUT;
+    }
 }
 
 template <typename T, typename C, int D> __global__ void __launch_bounds__(MASS_THREADS, 1) mass_kernel(const MassParams p)
@@ -476,14 +513,14 @@ template <typename T, typename C, int D> __global__ void __launch_bounds__(MASS_
         return;
     }
     if (warp < 4) {
-        mass_sum<S>(p, c, ctl, tid);
+        const long long done = mass_sum<S>(p, c, ctl, tid);
+        if (done < c.end) mass_lost(p, done, tid);
     } else if (warp == 4) {
         if (tid == 128) {
             mass_multiply<T, C, D>(p, c, smem, ctl);
-            if (*reinterpret_cast<volatile int *>(&ctl->dead)) {  // let what was issued end
-                tc_commit(&ctl->spare);
-                mbar_wait(&ctl->spare, 0);
-            }
+            // what was issued ends before the block may: others may have given up on it
+            tc_commit(&ctl->spare);
+            mbar_drain(&ctl->spare, 0);
         }
         __syncwarp();
     } else if (warp < 8) {
@@ -533,6 +570,11 @@ cudaError_t launch_mass(const MassLaunch &L, cudaStream_t st)
     p.q_heads = k.q_heads;
     p.scale_log2 = k.scale * LOG2E;
     p.decay = L.decay;
+    p.give_up = give_up();
+    if (p.row_status) {
+        const cudaError_t e = launch_chained(mass_status_kernel, dim3(k.B), 128, 0, st, p);
+        if (e != cudaSuccess) return e;
+    }
     const bool eight = k.cache.dtype == SPV_E4M3;
     const int D = k.cache.head_dim;
     if (k.dtype == SPV_BF16)

@@ -265,3 +265,40 @@ def test_attention_after_a_wait_gave_up(spv, gives_up, T, G, kv, page):
         assert (again["row_status"] == 0).all()
     with pytest.raises(spv.SpvError):
         gives_up(-2)
+
+
+@pytest.mark.parametrize("D, kv", [(64, "bf16"), (128, "bf16"), (256, "bf16"), (64, "e4m3"), (128, "e4m3"), (256, "e4m3")])
+def test_mass_after_a_wait_gave_up(spv, gives_up, D, kv):
+    """The weights that a block still had to write are NaN and their sequences' status says so; the rest is as ever."""
+    gen = torch.Generator().manual_seed(58)
+    ctx = torch.randint(0, 400, (200,), generator=gen).tolist()
+    ctx[20], ctx[150] = 4000, 2000
+    T, G = 6, 8
+    a = Layer(spv, 59, ctx, None, T, 2 * G, 2, D, 16, dtype="bf16", kv=kv)
+    q, table, at = a.q.cuda(), a.table.cuda(), i32(ctx)
+    lse = spv.spv_paged_attention(q, a.cache, table, at, want_lse=True)["lse"]
+    accept = torch.randint(-1, T, (a.B,), generator=gen).to(torch.int32).cuda()
+    W = 4010
+    old = torch.rand(a.B, 2, W, generator=gen).cuda()
+
+    def run(status=True):
+        out = {"mass": torch.full((a.B, 2, W), 7.0, device="cuda"), "row_status": torch.full((a.B,), 7, dtype=torch.int32, device="cuda")}
+        spv.spv_attention_mass(q, lse, a.cache, table, at, accept, mass_in=old, out=out, want_status=status)
+        torch.cuda.synchronize()
+        return out
+
+    good = run()
+    assert (good["row_status"] == 0).all() and torch.isfinite(good["mass"]).all()
+    for block, item in ((0, 0), (1, 1), (77, 0), (77, 2), (151, 0)):
+        gives_up(block, item)
+        got, silent = run(), run(status=False)
+        gives_up(-1)
+        for x in (got, silent):
+            gone = torch.isnan(x["mass"])
+            assert gone.any() and not gone.all()
+            assert torch.equal(x["mass"][~gone], good["mass"][~gone])
+        assert (silent["row_status"] == 7).all()
+        lost = torch.isnan(got["mass"]).any(-1).any(-1)
+        assert torch.equal(got["row_status"], torch.where(lost, spv.SPV_ERR_TIMEOUT, 0).to(torch.int32))
+        again = run()
+        assert torch.equal(again["mass"], good["mass"]) and (again["row_status"] == 0).all()
