@@ -450,7 +450,8 @@ spv_status spv_rope_frequencies(int rotary_dim, double base, int scaling, double
  *   the same or SPV_E4M3; D = head_dim, a multiple of 8 up to 512
  *   freqs        [rotary_dim / 2] uint64 (spv_rope_frequencies), 0 <= rotary_dim <= D even
  *   slot_pos     optional [B, kv_heads, pos_stride] int32: entry ctx_lens[b] + t
- *                of every head is set to p (spv_kv_evict's pos)
+ *                of every head is set to p (spv_kv_evict's pos); slots from
+ *                pos_stride on have none
  *   q_out        [B, T, q_heads, D] contiguous; may be q itself when that is
  *                contiguous
  *   row_status   [B] optional
@@ -475,10 +476,15 @@ spv_status spv_rope_append(const void *q, const void *k, const void *v, spv_dtyp
  *   out = v_scale[h] sum_j exp(s_j - m) v_j / sum_j exp(s_j - m),  lse = m + ln sum_j exp(s_j - m).
  * A row that sees nothing, or only scores of minus infinity: out 0, lse minus
  * infinity.  What lies in slots that a row does not see (NaN and infinities
- * included) has no effect on it.
- *   q, out       [B, T, q_heads, D] contiguous, SPV_BF16 or SPV_F16; D = head_dim 64, 128 or 256
+ * included) has no effect on it; infinities and NaN that it does see are in its
+ * result as the formula has them.  Scores, sums and lse are held in 32 bits;
+ * each weight is rounded to q's type (f16 for an e4m3 cache) for its product
+ * with v, half a step, so that out is off by about a third more than its own
+ * rounding alone would have it.
+ *   q, out       [B, T, q_heads, D] contiguous and apart, SPV_BF16 or SPV_F16; D = head_dim 64, 128 or 256
  *   parent       [B, T] int32, optional
- *   1 <= T <= SPV_MAX_NEW_TOKENS; q_heads / kv_heads <= SPV_MAX_GROUP
+ *   1 <= T <= SPV_MAX_NEW_TOKENS (a prompt: appended whole, attended in pieces of that many);
+ *   q_heads / kv_heads <= SPV_MAX_GROUP
  *   lse          [B, T, q_heads] fp32, optional; row_status [B], optional
  *   workspace    >= spv_attention_workspace_bytes(...) bytes, 256-byte
  *                aligned; it does not depend on the cached lengths.  Only its

@@ -19,7 +19,7 @@ from dataclasses import dataclass
 
 import torch
 
-from . import SPV_BF16, SPV_E4M3, SPV_F16, SpvError, _check, _on_its_stream, _stream, load_library, new_workspace
+from . import SPV_BF16, SPV_E4M3, SPV_F16, SpvError, _check, _stream, load_library, new_workspace
 
 ROPE_SCALINGS = {"plain": 0, "linear": 1, "base": 2, "by_parts": 3}
 _ACTIVATIONS = {torch.bfloat16: SPV_BF16, torch.float16: SPV_F16}
@@ -109,11 +109,19 @@ def _opt(t, name, dtype, shape, dev):
     return None if t is None else _arg(t, name, dtype, shape, dev)
 
 
-def _output(out, key, shape, dtype, dev):
+def _made(stream, make, *args, **kw):
+    """make(...) with the call's stream as torch's current one: what is made belongs to it, in order with its kernels."""
+    if stream is None:
+        return make(*args, **kw)
+    with torch.cuda.stream(stream):
+        return make(*args, **kw)
+
+
+def _output(out, key, shape, dtype, dev, stream):
     """Address of the caller's output tensor `key`, checked, or of a new one."""
     t = out.get(key)
     if t is None:
-        t = out[key] = torch.empty(shape, dtype=dtype, device=dev)
+        t = out[key] = _made(stream, torch.empty, shape, dtype=dtype, device=dev)
         return t.data_ptr()
     return _arg(t, key, dtype, shape, dev)
 
@@ -178,7 +186,6 @@ def spv_rope_frequencies(rotary_dim: int, base: float = 10000.0, *, scaling: str
     return host.to(device)
 
 
-@_on_its_stream
 def spv_rope_append(q, k, v, cache: KVCache, page_table, ctx_lens, freqs, *, interleaved: bool = False,
                     mscale: float = 1.0, positions=None, new_lens=None, slot_pos=None, out=None,
                     want_status: bool = True, stream=None) -> dict:
@@ -225,8 +232,8 @@ def spv_rope_append(q, k, v, cache: KVCache, page_table, ctx_lens, freqs, *, int
         _arg(freqs, "freqs", _I64, (pairs,), dev), 2 * pairs, int(bool(interleaved)), mscale,
         _opt(positions, "positions", _I32, (B, T), dev),
         _arg(ctx_lens, "ctx_lens", _I32, (B,), dev), _opt(new_lens, "new_lens", _I32, (B,), dev), table, pages, pack,
-        _opt(slot_pos, "slot_pos", _I32, (B, Hkv, slots), dev), slots, _output(out, "q", (B, T, Hq, D), dtype, dev),
-        _output(out, "row_status", (B,), _I32, dev) if want_status else None, _on_stream(stream, dev))
+        _opt(slot_pos, "slot_pos", _I32, (B, Hkv, slots), dev), slots, _output(out, "q", (B, T, Hq, D), dtype, dev, stream),
+        _output(out, "row_status", (B,), _I32, dev, stream) if want_status else None, _on_stream(stream, dev))
     if st:
         raise SpvError(st, "spv_rope_append")
     return out
@@ -236,7 +243,6 @@ def spv_attention_workspace_bytes(B: int, T: int, q_heads: int, kv_heads: int, h
     return load_library().spv_attention_workspace_bytes(B, T, q_heads, kv_heads, head_dim)
 
 
-@_on_its_stream
 def spv_paged_attention(q, cache: KVCache, page_table, ctx_lens, *, new_lens=None, parent=None, scale=None,
                         workspace=None, out=None, want_lse: bool = False, want_status: bool = True,
                         stream=None) -> dict:
@@ -251,21 +257,20 @@ def spv_paged_attention(q, cache: KVCache, page_table, ctx_lens, *, new_lens=Non
     table, pages = _table(page_table, B, dev)
     lib = load_library()
     if workspace is None:
-        workspace = new_workspace(lib.spv_attention_workspace_bytes(B, T, Hq, Hkv, D), dev)
+        workspace = _made(stream, new_workspace, lib.spv_attention_workspace_bytes(B, T, Hq, Hkv, D), dev)
     out = dict(out) if out else {}
     st = lib.spv_paged_attention(
         address, code, B, T, Hq, pack, table, pages, _arg(ctx_lens, "ctx_lens", _I32, (B,), dev),
         _opt(new_lens, "new_lens", _I32, (B,), dev), _opt(parent, "parent", _I32, (B, T), dev),
-        1.0 / math.sqrt(D) if scale is None else scale, _output(out, "out", shape, q.dtype, dev),
-        _output(out, "lse", (B, T, Hq), _F32, dev) if want_lse else None,
-        _output(out, "row_status", (B,), _I32, dev) if want_status else None,
+        1.0 / math.sqrt(D) if scale is None else scale, _output(out, "out", shape, q.dtype, dev, stream),
+        _output(out, "lse", (B, T, Hq), _F32, dev, stream) if want_lse else None,
+        _output(out, "row_status", (B,), _I32, dev, stream) if want_status else None,
         _arg(workspace, "workspace", _U8, (workspace.numel(),), dev), workspace.numel(), _on_stream(stream, dev))
     if st:
         raise SpvError(st, "spv_paged_attention")
     return out
 
 
-@_on_its_stream
 def spv_attention_mass(q, lse, cache: KVCache, page_table, ctx_lens, accept_count, *, nodes=None, new_lens=None,
                        parent=None, scale=None, decay: float = 1.0, mass_in=None, out=None,
                        want_status: bool = True, stream=None) -> dict:
@@ -284,7 +289,7 @@ def spv_attention_mass(q, lse, cache: KVCache, page_table, ctx_lens, accept_coun
     mass = out.get("mass")
     if mass is None:
         slots = mass_in.shape[2] if mass_in is not None and mass_in.dim() == 3 else pages * page_size
-        mass = out["mass"] = torch.zeros(B, Hkv, slots, dtype=_F32, device=dev)
+        mass = out["mass"] = _made(stream, torch.zeros, B, Hkv, slots, dtype=_F32, device=dev)
     if mass.dim() != 3:
         raise ValueError("out['mass'] must be [B, kv_heads, slots]")
     full = (B, Hkv, mass.shape[2])
@@ -294,13 +299,12 @@ def spv_attention_mass(q, lse, cache: KVCache, page_table, ctx_lens, accept_coun
         _opt(parent, "parent", _I32, (B, T), dev), 1.0 / math.sqrt(D) if scale is None else scale,
         _arg(accept_count, "accept_count", _I32, (B,), dev), _opt(nodes, "nodes", _I32, (B, T), dev), decay,
         _opt(mass_in, "mass_in", _F32, full, dev), _arg(mass, "out['mass']", _F32, full, dev), full[2],
-        _output(out, "row_status", (B,), _I32, dev) if want_status else None, _on_stream(stream, dev))
+        _output(out, "row_status", (B,), _I32, dev, stream) if want_status else None, _on_stream(stream, dev))
     if st:
         raise SpvError(st, "spv_attention_mass")
     return out
 
 
-@_on_its_stream
 def spv_kv_evict(cache: KVCache, page_table, lens, mass, budget: int, *, pos=None, sinks: int = 0, recent: int = 0,
                  out=None, want_status: bool = True, stream=None) -> dict:
     """Cuts every sequence of more than ``budget`` slots back to it, in place
@@ -325,9 +329,9 @@ def spv_kv_evict(cache: KVCache, page_table, lens, mass, budget: int, *, pos=Non
     st = load_library().spv_kv_evict(
         pack, table, pages, B, _arg(lens, "lens", _I32, (B,), dev), budget, int(sinks), int(recent),
         _arg(mass, "mass", _F32, full, dev), _opt(pos, "pos", _I32, full, dev), slots,
-        _output(out, "mass", (B, Hkv, width), _F32, dev), _output(out, "pos", (B, Hkv, width), _I32, dev), width,
-        _output(out, "lens", (B,), _I32, dev), _output(out, "slot_src", (B, Hkv, max(budget, 0)), _I32, dev),
-        _output(out, "row_status", (B,), _I32, dev) if want_status else None, _on_stream(stream, dev))
+        _output(out, "mass", (B, Hkv, width), _F32, dev, stream), _output(out, "pos", (B, Hkv, width), _I32, dev, stream), width,
+        _output(out, "lens", (B,), _I32, dev, stream), _output(out, "slot_src", (B, Hkv, max(budget, 0)), _I32, dev, stream),
+        _output(out, "row_status", (B,), _I32, dev, stream) if want_status else None, _on_stream(stream, dev))
     if st:
         raise SpvError(st, "spv_kv_evict")
     return out
