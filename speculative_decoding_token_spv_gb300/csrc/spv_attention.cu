@@ -62,6 +62,7 @@ __global__ void __launch_bounds__(ATT_THREADS, AttShape<C, D, MT>::BLOCKS_PER_SM
     using S = AttShape<C, D, MT>;
     using M = typename MmaOf<T, C>::type;
     constexpr int R = S::R, PART = R * (D + 2), NST = S::STAGES;
+    constexpr float UP = Weights<M>::UP;
     extern __shared__ __align__(1024) char smem[];
     __shared__ float ms[ATT_WARPS][R], ls[ATT_WARPS][R];
     __shared__ float q_unit[R];                // what a unit of the stored q row stands for
@@ -201,10 +202,10 @@ __global__ void __launch_bounds__(ATT_THREADS, AttShape<C, D, MT>::BLOCKS_PER_SM
                         }
                     }
                 }
-                // m follows the maximum only where it has grown by more than 2^LAG (or begins): p stays below 2^(LAG + UP), the
-                // 32-bit sums lose nothing, and o is seldom rescaled -- with every growth it was in nearly every slice.  (The
-                // growth as a difference: m + LAG may round up to the next score where these are 16 apart, which would then be
-                // 2^16, more than an f16 holds.)
+                // m, the maximum less UP, follows it only where it has grown by more than 2^LAG (or begins): p stays below
+                // 2^(UP + LAG), the 32-bit sums lose nothing, and o is seldom rescaled -- with every growth it was in nearly
+                // every slice.  (The growth as a difference: a sum may round up to the next score where these are 16 apart,
+                // which would then be 2^16, more than an f16 holds.)
                 float top[2];
                 bool moved = false;
 #pragma unroll
@@ -213,12 +214,12 @@ __global__ void __launch_bounds__(ATT_THREADS, AttShape<C, D, MT>::BLOCKS_PER_SM
                     x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 1));
                     x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 2));
                     top[i] = x * factor[mt][i];
-                    moved |= top[i] - m[mt][i] > Weights<M>::LAG;  // m minus infinity: any score
+                    moved |= top[i] - m[mt][i] > UP + Weights<M>::LAG;  // m minus infinity: any score
                 }
                 if (__any_sync(0xffffffffu, moved)) {
 #pragma unroll
                     for (int i = 0; i < 2; ++i) {
-                        const float grown = fmaxf(m[mt][i], top[i]);
+                        const float grown = fmaxf(m[mt][i], top[i] - UP);
                         const float a = grown == -CUDART_INF_F ? 0.0f : fast_exp2(m[mt][i] - grown);
                         m[mt][i] = grown;
                         l[mt][i] *= a;
@@ -231,7 +232,7 @@ __global__ void __launch_bounds__(ATT_THREADS, AttShape<C, D, MT>::BLOCKS_PER_SM
                 }
 #pragma unroll
                 for (int i = 0; i < 2; ++i) {
-                    const float base = m[mt][i] == -CUDART_INF_F ? 0.0f : m[mt][i] - Weights<M>::UP, f = factor[mt][i];
+                    const float base = m[mt][i] == -CUDART_INF_F ? 0.0f : m[mt][i], f = factor[mt][i];
 #pragma unroll
                     for (int k = 0; k < 2; ++k)
 #pragma unroll
@@ -298,7 +299,7 @@ __global__ void __launch_bounds__(ATT_THREADS, AttShape<C, D, MT>::BLOCKS_PER_SM
                 x += __shfl_xor_sync(0xffffffffu, x, 2);
                 const int r = mt * 16 + i * 8 + (lane >> 2);
                 if ((lane & 3) == 0) {
-                    ms[warp][r] = sees[r] ? m[mt][i] - Weights<M>::UP : -CUDART_INF_F;  // what l and o are sums against
+                    ms[warp][r] = sees[r] ? m[mt][i] : -CUDART_INF_F;
                     ls[warp][r] = sees[r] ? x : 0.0f;
                 }
             }

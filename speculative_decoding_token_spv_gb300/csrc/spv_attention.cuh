@@ -25,8 +25,8 @@ struct AttParams {
     GiveUp give_up;
 };
 
-// The weights of a product in M are 2^(s - (m - UP)), m the running maximum, which may lag the largest score by LAG: at
-// most 2^15 in f16, whose smallest value is then 2^-32 of the largest weight and not 2^-25 -- a long cache of keys below
+// The weights of a product in M are 2^(s - m), m the running maximum less UP, which the largest score may pass by LAG: at
+// most 2^14 in f16, whose smallest value is then 2^-32 of the largest weight and not 2^-25 -- a long cache of keys below
 // that would add to the sum l, held in 32 bits, and not to the output (262,143 keys of 2^-25 beside one of 1: 2^-7 of the
 // result).  bf16 has the exponents of 32 bits.
 template <typename M> struct Weights {

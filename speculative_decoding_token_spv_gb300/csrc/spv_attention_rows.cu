@@ -265,7 +265,7 @@ __device__ void rows_load(const AttParams &p, Cursor c, char *smem, RowsCtl *ctl
                 if (n >= NST && !(ok = rows_wait(ctl, &empty[st], (n / NST - 1) & 1, err))) break;
                 to = base + AT + st * S::TILE;
             }
-#pragma unroll 1
+#pragma unroll(S::WIDEN ? 2 : 1)
             for (int i = 0; i < CH; ++i) {
                 const int row = 32 * w + i * RPI + sub;
                 const int64_t at = __shfl_sync(0xffffffffu, mine, i * RPI + sub);
@@ -307,8 +307,10 @@ __device__ void rows_load(const AttParams &p, Cursor c, char *smem, RowsCtl *ctl
 // Two threads, one for the scores and one for the outputs: issuing a tile's 8
 // products takes either of them 600 to 1,100 cycles, and the rows wait for the
 // scores (one thread for both: 241 us for the verify batch against 232).  Their
-// loops are unrolled by two only: all roles' loops together have to fit the
-// instruction caches (all eight: draft trees 91 us, 88 so).
+// loops are unrolled by two only, and the loaders' not at all: all roles' loops
+// together have to fit the instruction caches (draft trees 91 us otherwise, 88
+// so).  With e4m3 they issue in time only when unrolled: two sequences of 131,001
+// slots 204 us at 40 rows and 249 at 84 like the others, 194 and 240 so.
 template <typename T, typename C, int D>
 __device__ void rows_scores(const AttParams &p, Cursor c, char *smem, RowsCtl *ctl, unsigned *err)
 {
@@ -328,7 +330,7 @@ __device__ void rows_scores(const AttParams &p, Cursor c, char *smem, RowsCtl *c
             tc_fence_after();
             fence_async_shared();  // K was written by asynchronous copies of threads, q by threads
             const uint64_t k = desc_k_major(base + S::K_AT + (n % KST) * S::TILE);
-#pragma unroll 2
+#pragma unroll(S::WIDEN ? D / 16 : 2)
             for (int ks = 0; ks < D / 16; ++ks) {
                 const int off = ((ks >> 2) * (AR_KEYS * 128) + (ks & 3) * 32) >> 4;
                 tc_mma(tm_s + (n & 1) * AR_KEYS, q + off, k + off, SHAPE, ks > 0);
@@ -355,7 +357,7 @@ __device__ void rows_outputs(const AttParams &p, Cursor c, char *smem, RowsCtl *
             tc_fence_after();
             fence_async_shared();
             const uint64_t v = desc_n_major(base + S::V_AT + (n % VST) * S::TILE, AR_KEYS * 128);
-#pragma unroll 2
+#pragma unroll(S::WIDEN ? AR_KEYS / 16 : 2)
             for (int ks = 0; ks < AR_KEYS / 16; ++ks)
                 tc_mma_ta(tm_o, tm_p + (n & 1) * (AR_KEYS / 2) + ks * 8, v + ks * (2048 >> 4), SHAPE, i > 0 || ks > 0);
             tc_commit(&ctl->o_done[n & 1]);
@@ -591,6 +593,7 @@ __device__ void rows_softmax(const AttParams &p, Cursor c, char *smem, RowsCtl *
     using M = typename MmaOf<T, C>::type;
     constexpr int COPIES = AR_ROWS / COLS, PART = AR_ROWS * (D + 2);
     using W = RowsWarps<COLS>;
+    constexpr float UP = Weights<M>::UP;
     constexpr int HALVES = W::HALVES, KEYS = COLS / HALVES;
     const int half = tid / AR_ROWS, lane_row = tid % AR_ROWS, copy = lane_row / COLS, r = lane_row % COLS;
     const uint32_t quarter = static_cast<uint32_t>(lane_row & ~31) << 16;
@@ -617,7 +620,7 @@ __device__ void rows_softmax(const AttParams &p, Cursor c, char *smem, RowsCtl *
         const bool mine = r < live;
         const int token = (row0 + r) / p.group;
         unsigned long long see = 0;
-        float m = -CUDART_INF_F, l = 0.0f;
+        float m = -CUDART_INF_F, l = 0.0f;  // a maximum so far less UP: what l and O are sums against
         float factor = p.scale_log2 * (p.c.k_scale ? __ldg(p.c.k_scale + c.h) : 1.0f);
         bool any_bad = c.s.bad, ok = true;
         const int place = item & 1;
@@ -664,9 +667,9 @@ __device__ void rows_softmax(const AttParams &p, Cursor c, char *smem, RowsCtl *
                         top = fmaxf(top, ctl->top[tid ^ AR_ROWS]);
                     }
                     if (tile == t0) {
-                        m = fmaxf(m, top);
-                    } else if (__any_sync(0xffffffffu, top - m > Weights<M>::LAG)) {  // as a difference: m + 8 may round up to a score 16 above
-                        const float grown = fmaxf(m, top), a = grown == -CUDART_INF_F ? 0.0f : fast_exp2(m - grown);
+                        m = top - UP;
+                    } else if (__any_sync(0xffffffffu, top - m > UP + Weights<M>::LAG)) {  // as a difference: a sum may round up to a score 16 above
+                        const float grown = fmaxf(m, top - UP), a = grown == -CUDART_INF_F ? 0.0f : fast_exp2(m - grown);
                         m = grown;
                         l *= a;
                         ok = ok && rows_wait(ctl, &ctl->o_done[(n - 1) & 1], ((n - 1) >> 1) & 1, err);
@@ -680,7 +683,7 @@ __device__ void rows_softmax(const AttParams &p, Cursor c, char *smem, RowsCtl *
                             tc_st16(tm_o + i, y);
                         }
                     }
-                    const float base = m == -CUDART_INF_F ? 0.0f : m - Weights<M>::UP;
+                    const float base = m == -CUDART_INF_F ? 0.0f : m;
                     float s0 = 0.0f, s1 = 0.0f;
                     uint32_t pk[KEYS / 2];
 #pragma unroll
@@ -713,7 +716,6 @@ __device__ void rows_softmax(const AttParams &p, Cursor c, char *smem, RowsCtl *
             any_bad |= *reinterpret_cast<volatile int *>(&ctl->bad[item_flags(item)]) != 0;
             rows_sync<W::SOFTMAX>();  // all have read them, and all scores
         }
-        m -= Weights<M>::UP;  // what l and O are sums against
         if (see == 0) {
             m = -CUDART_INF_F;
             l = 0.0f;
