@@ -411,8 +411,8 @@ cudaError_t launch_attention(const AttentionLaunch &L, cudaStream_t st)
     const int D = k.cache.head_dim;
     // Over 16 rows the 5th-generation tensor cores, for an e4m3 cache over 32: its rows pass through shared memory
     // twice there.  Two sequences of 131,001 keys, 8 key heads, D = 128, from cold caches: bf16 at 16 rows 194 us there
-    // and 198 here, at 20 rows 195 and 363 (16 sequences of up to 4,000: 62 and 56, 62 and 72); e4m3 at 32 rows 191 and
-    // 171 (66 and 55), at 40 rows 202 there and two passes here.
+    // and 200 here, at 20 rows 194 and 362 (16 sequences of up to 4,000: 61 and 56, 62 and 77); e4m3 at 32 rows 194 and
+    // 173 (71 and 56), at 40 rows 192 there and two passes here.
     if (p.rows > (eight ? 32 : 16) && D <= 128) return launch_attention_rows(p, k, st);
     if (k.dtype == SPV_BF16)
         return eight ? launch_types<__nv_bfloat16, __nv_fp8_e4m3>(p, D, st)

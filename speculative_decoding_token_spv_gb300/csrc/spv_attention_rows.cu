@@ -26,7 +26,7 @@
 // What bounds it, and what it takes: 40 rows of 64 sequences of up to 8,191
 // slots, K and V 1.37 GB, 236 us (5.8 TB/s, 86% of a copy's rate: reading K and
 // V, then starts, ends of items and joins); 84 rows of 32 sequences of up to
-// 4,099 slots, 353 MB, 88 us: exponentials, 1,800 of a tile's 2,450 cycles when it
+// 4,099 slots, 353 MB, 89 us: exponentials, 1,800 of a tile's 2,450 cycles when it
 // took 94 us, and the ends of items.
 //
 // Every wait is bounded; one that gives up records SPV_ERR_TIMEOUT in the
