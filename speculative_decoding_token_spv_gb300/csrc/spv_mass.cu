@@ -473,7 +473,7 @@ __device__ __noinline__ void mass_lost(const MassParams &p, long long done, int 
             const float old = p.mass_in && j < c.s.ctx ? p.mass_in[out_row + j] : 0.0f;
             p.mass_out[out_row + j] = count.rows > 0 ? CUDART_NAN_F : old * p.decay;
         }
-        if (count.rows > 0 && mass_first(c) < mass_last(c) && tid == 0 && p.row_status) p.row_status[c.b] = STATUS_TIMEOUT;
+        if (count.rows > 0 && mass_first(c) < mass_last(c) && (tid & 31) == 0 && p.row_status) p.row_status[c.b] = STATUS_TIMEOUT;
     }
 }
 
