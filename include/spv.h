@@ -465,6 +465,32 @@ spv_status spv_rope_append(const void *q, const void *k, const void *v, spv_dtyp
                            int64_t pos_stride, void *q_out, int32_t *row_status, void *stream);
 
 /*
+ * spv_norm_rope_append -- spv_rope_append for models that norm each head of q
+ * and k first, or whose positions have several axes:
+ *   y = w x / sqrt(mean(x^2) + eps) over a head's head_dim elements,
+ * then the rotation of spv_rope_append on y, in 32 bits to the end: nothing is
+ * rounded between the two.
+ *   q_weight, k_weight  [head_dim] fp32 (models that learn w - 1: add the 1);
+ *                NULL: that tensor is not normed
+ *   eps          >= 0, finite
+ *   axes         [rotary_dim / 2] int32, optional: the axis of each pair, 0 ..
+ *                num_axes - 1 (others count as the nearest of these); NULL: 0
+ *   positions    [B, T, num_axes] int32; NULL (num_axes 1 only): ctx_lens[b] + t
+ *   num_axes     1 .. 8
+ *   D = head_dim, a multiple of 8 up to 256
+ *   slot_pos     receives the position on axis 0
+ * All else as spv_rope_append.  With both weights NULL and one axis it is that
+ * call.
+ */
+spv_status spv_norm_rope_append(const void *q, const void *k, const void *v, spv_dtype dtype, const int64_t *strides,
+                                int B, int T, int q_heads, const float *q_weight, const float *k_weight, float eps,
+                                const uint64_t *freqs, const int32_t *axes, int num_axes, int rotary_dim,
+                                int interleaved, float mscale, const int32_t *positions, const int32_t *ctx_lens,
+                                const int32_t *new_lens, const int32_t *page_table, int max_pages,
+                                const spv_kv_cache *cache, int32_t *slot_pos, int64_t pos_stride, void *q_out,
+                                int32_t *row_status, void *stream);
+
+/*
  * spv_paged_attention -- attention of the new tokens over the paged cache,
  * which already holds their own keys and values (spv_rope_append).  Token t
  * of sequence b sees the slots j < ctx_lens[b] and, among the new tokens u at
@@ -534,6 +560,74 @@ spv_status spv_attention_mass(const void *q, spv_dtype dtype, int B, int T, int 
                               const int32_t *ctx_lens, const int32_t *new_lens, const int32_t *parent, float scale,
                               const int32_t *accept_count, const int32_t *nodes, float decay, const float *mass_in,
                               float *mass_out, int64_t mass_stride, int32_t *row_status, void *stream);
+
+/*
+ * Scores and masks of attention that is not plain.  With x = scale k_scale[h]
+ * q . k_j, a score is
+ *   s = y - slopes[g] |p_t - p_j|,   y = cap tanh(x / cap)  (cap 0: x),
+ * and token t sees slot j where all of these hold:
+ *   - it comes no later in the sequence (a tree: it is cached, t itself or an
+ *     ancestor), or lies before last[b, t];
+ *   - j >= first[b, t];
+ *   - p_t - p_j < window (window 0: always).
+ * Positions p: the slot itself, of a tree's node ctx_lens[b] + its depth; with
+ * slot_pos those of each slot and key head, the new tokens' among them
+ * (spv_rope_append and spv_norm_rope_append write them, spv_kv_evict moves
+ * them): after an eviction a slot is not a position.
+ */
+typedef struct {
+    float cap;               /* > 0, or 0: none */
+    const float *slopes;     /* [q_heads] fp32, optional */
+    int32_t window;          /* > 0, or 0: none */
+    const int32_t *first;    /* [B, T], optional: the slot where a token's document begins */
+    const int32_t *last;     /* [B, T], optional, chains only: the slot where the prefix ends that a token sees whole */
+    const int32_t *slot_pos; /* [B, kv_heads, pos_stride], optional; pos_stride >= ctx + new of every sequence */
+    int64_t pos_stride;
+} spv_scores;
+
+/*
+ * spv_paged_attention_scored -- spv_paged_attention with the scores and masks
+ * of `scores` (HOST struct of device pointers).  All else as there, the
+ * workspace (spv_attention_workspace_bytes) too, but for this:
+ * Pages that lie wholly before the first slot that a sequence's tokens can see
+ * (first, window without slot_pos) are not read and may be gone.  A page id
+ * outside the pool among the others makes row_status[b] SPV_ERR_BAD_ROW and
+ * the rows that see one of its slots NaN; other rows of that sequence may be
+ * NaN too.  Bad sequences also: ctx + new > pos_stride.  With row_status a
+ * small kernel of its own goes before the others.
+ */
+spv_status spv_paged_attention_scored(const void *q, spv_dtype dtype, int B, int T, int q_heads,
+                                      const spv_kv_cache *cache, const int32_t *page_table, int max_pages,
+                                      const int32_t *ctx_lens, const int32_t *new_lens, const int32_t *parent,
+                                      float scale, const spv_scores *scores, void *out, float *lse,
+                                      int32_t *row_status, void *workspace, size_t workspace_bytes, void *stream);
+
+/*
+ * spv_prompt_attention -- the same for prompts: any number of new tokens, T >=
+ * 1, in one call; `scores` may be NULL (plain causal attention).  No trees.
+ *   T (q_heads / kv_heads) <= 2^24; head_dim 64, 128 or 256
+ *   workspace    >= spv_prompt_workspace_bytes(...) bytes; it does not depend
+ *                on the lengths.  Otherwise as spv_paged_attention's
+ */
+spv_status spv_prompt_attention(const void *q, spv_dtype dtype, int B, int T, int q_heads, const spv_kv_cache *cache,
+                                const int32_t *page_table, int max_pages, const int32_t *ctx_lens,
+                                const int32_t *new_lens, float scale, const spv_scores *scores, void *out, float *lse,
+                                int32_t *row_status, void *workspace, size_t workspace_bytes, void *stream);
+
+size_t spv_prompt_workspace_bytes(int B, int T, int q_heads, int kv_heads, int head_dim);
+
+/*
+ * spv_attention_mass_scored -- spv_attention_mass after
+ * spv_paged_attention_scored: the weights are those of its scores and masks.
+ * All else as there; pages before the first slot that a sequence's tokens can
+ * see are needed only for the old weights of their slots to be kept.
+ */
+spv_status spv_attention_mass_scored(const void *q, spv_dtype dtype, int B, int T, int q_heads, const float *lse,
+                                     const spv_kv_cache *cache, const int32_t *page_table, int max_pages,
+                                     const int32_t *ctx_lens, const int32_t *new_lens, const int32_t *parent,
+                                     float scale, const spv_scores *scores, const int32_t *accept_count,
+                                     const int32_t *nodes, float decay, const float *mass_in, float *mass_out,
+                                     int64_t mass_stride, int32_t *row_status, void *stream);
 
 /*
  * spv_kv_evict -- cuts every sequence with lens[b] > budget back to `budget`

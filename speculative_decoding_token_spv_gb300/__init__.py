@@ -103,6 +103,16 @@ def load_library():
     lib.spv_paged_attention.restype = I
     lib.spv_attention_mass.argtypes = [P, I, I, I, I, P, P, P, I, P, P, P, F, P, P, F, P, P, L, P, P]
     lib.spv_attention_mass.restype = I
+    lib.spv_norm_rope_append.argtypes = [P, P, P, I, P, I, I, I, P, P, F, P, P, I, I, I, F, P, P, P, P, I, P, P, L, P, P, P]
+    lib.spv_norm_rope_append.restype = I
+    lib.spv_paged_attention_scored.argtypes = [P, I, I, I, I, P, P, I, P, P, P, F, P, P, P, P, P, S, P]
+    lib.spv_paged_attention_scored.restype = I
+    lib.spv_prompt_workspace_bytes.argtypes = [I, I, I, I, I]
+    lib.spv_prompt_workspace_bytes.restype = S
+    lib.spv_prompt_attention.argtypes = [P, I, I, I, I, P, P, I, P, P, F, P, P, P, P, P, S, P]
+    lib.spv_prompt_attention.restype = I
+    lib.spv_attention_mass_scored.argtypes = [P, I, I, I, I, P, P, P, I, P, P, P, F, P, P, P, F, P, P, L, P, P]
+    lib.spv_attention_mass_scored.restype = I
     lib.spv_kv_evict.argtypes = [P, P, I, I, P, I, I, I, P, P, L, P, P, L, P, P, P, P]
     lib.spv_kv_evict.restype = I
     _lib = lib
@@ -471,5 +481,6 @@ def spv_fanout_sizes(F0: int, a: float, r: float, K: int, V: int) -> list:
 fanout_sizes = spv_fanout_sizes
 
 from .kv import (  # noqa: E402  (the calls around the verify step; they use the helpers above)
-    KVCache, ROPE_SCALINGS, spv_attention_mass, spv_attention_workspace_bytes, spv_kv_evict, spv_paged_attention,
-    spv_rope_append, spv_rope_frequencies)
+    KVCache, ROPE_SCALINGS, Scores, spv_attention_mass, spv_attention_mass_scored, spv_attention_workspace_bytes,
+    spv_kv_evict, spv_norm_rope_append, spv_paged_attention, spv_paged_attention_scored, spv_prompt_attention,
+    spv_prompt_workspace_bytes, spv_rope_append, spv_rope_frequencies)

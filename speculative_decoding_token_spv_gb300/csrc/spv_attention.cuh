@@ -78,7 +78,8 @@ __device__ __forceinline__ float *piece_of(const AttParams &p, int i, int b0, in
 
 // Notes that this block has a piece of the cursor's item; `begin` is the start
 // of its range.
-__device__ __forceinline__ void note_split(const AttParams &p, const Cursor &c, const AttRows &rows, long long begin, int tid)
+template <typename Lens>
+__device__ __forceinline__ void note_split(const AttParams &p, const CursorOf<Lens> &c, const AttRows &rows, long long begin, int tid)
 {
     if (tid != 0) return;
     SplitItem s;
@@ -112,6 +113,9 @@ cudaError_t launch_join(const AttParams &p, spv_dtype q, int D, int R, int block
 
 // Room for the entries of `blocks` blocks.
 constexpr size_t split_bytes(int blocks) { return (static_cast<size_t>(blocks) * 2 * sizeof(SplitItem) + 255) / 256 * 256; }
+
+// Workspace: header, the blocks' split items, their pieces.
+constexpr size_t ATT_PARTS_AT = WS_HEADER + split_bytes(ATT_MAX_BLOCKS);
 
 cudaError_t launch_attention_rows(const AttParams &p, const KvLaunch &L, cudaStream_t st);
 size_t attention_rows_part_floats(int head_dim);  // of all blocks' pieces

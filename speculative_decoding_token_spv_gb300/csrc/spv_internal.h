@@ -117,12 +117,20 @@ struct RopeLaunch {
     int64_t pos_stride;
     void *q_out;
 };
+struct NormRopeLaunch {
+    RopeLaunch rope;
+    const float *q_weight, *k_weight;
+    float eps;
+    const int32_t *axes;
+    int num_axes;
+};
 struct AttentionLaunch {
     KvLaunch kv;
     const void *q;
     void *out;
     float *lse;
     void *ws;
+    spv_scores scores;  // of the calls that take them
 };
 struct MassLaunch {
     KvLaunch kv;
@@ -133,6 +141,7 @@ struct MassLaunch {
     const float *mass_in;
     float *mass_out;
     int64_t mass_stride;
+    spv_scores scores;  // of the call that takes them
 };
 struct EvictLaunch {
     KvLaunch kv;
@@ -176,8 +185,13 @@ cudaError_t launch_tree(const TreeLaunch &L, cudaStream_t st);
 size_t attention_ws_bytes(int B, int T, int q_heads, int kv_heads, int head_dim);
 struct PagedView paged_view(const KvLaunch &L);
 cudaError_t launch_rope(const RopeLaunch &L, cudaStream_t st);
+cudaError_t launch_norm_rope(const NormRopeLaunch &L, cudaStream_t st);
 cudaError_t launch_attention(const AttentionLaunch &L, cudaStream_t st);
+cudaError_t launch_attention_scored(const AttentionLaunch &L, cudaStream_t st);
+cudaError_t launch_prompt(const AttentionLaunch &L, cudaStream_t st);
+size_t prompt_ws_bytes(int B, int T, int q_heads, int kv_heads, int head_dim);
 cudaError_t launch_mass(const MassLaunch &L, cudaStream_t st);
+cudaError_t launch_mass_scored(const MassLaunch &L, cudaStream_t st);
 cudaError_t launch_evict(const EvictLaunch &L, cudaStream_t st);
 
 }  // namespace spv

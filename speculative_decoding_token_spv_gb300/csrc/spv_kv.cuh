@@ -91,19 +91,26 @@ struct Work {
     const int32_t *ctx_lens, *new_lens;
     bool idle;  // sequences without new tokens have work too
 };
+__device__ __forceinline__ SeqLens lens_of(const Work &w, int b, const PagedView &c)
+{
+    return seq_lens(w.ctx_lens, w.new_lens, b, w.T, c, w.idle);
+}
+// Tiles at a sequence's beginning that its new tokens do not see at all.
+__device__ __forceinline__ int skipped_tiles(const Work &, const SeqLens &) { return 0; }
 
 // A block's range [at, end) and the item that it is in: `first` is the number
 // of the item's first tile, `tiles` how many it has.
-struct Cursor {
+template <typename Lens> struct CursorOf {
     long long all, at, end, first;
     long long part;  // tiles of a block; the first `more` blocks have one tile more
     int blocks, more;  // blocks that have work
     int b, row_tile, h, tiles;
-    SeqLens s;
+    Lens s;
 };
-__device__ __forceinline__ int tiles_of(const Work &w, const SeqLens &s)
+using Cursor = CursorOf<SeqLens>;
+template <typename W, typename Lens> __device__ __forceinline__ int tiles_of(const W &w, const Lens &s)
 {
-    return s.total == 0 ? 1 : (s.total + w.tile - 1) / w.tile;
+    return s.total == 0 ? 1 : (s.total + w.tile - 1) / w.tile - skipped_tiles(w, s);
 }
 // a / b; in 32 bits, a tenth of the time, where a fits them (nearly always).
 __device__ __forceinline__ long long quotient(long long a, long long b)
@@ -111,12 +118,12 @@ __device__ __forceinline__ long long quotient(long long a, long long b)
     if (((a | b) >> 32) == 0) return static_cast<unsigned>(a) / static_cast<unsigned>(b);
     return a / b;
 }
-__device__ __forceinline__ long long range_begin(const Cursor &c, int block)
+template <typename Lens> __device__ __forceinline__ long long range_begin(const CursorOf<Lens> &c, int block)
 {
     return c.part * block + min(block, c.more);
 }
 // The block whose range holds tile x.
-__device__ __forceinline__ int range_owner(const Cursor &c, long long x)
+template <typename Lens> __device__ __forceinline__ int range_owner(const CursorOf<Lens> &c, long long x)
 {
     const long long large = (c.part + 1) * c.more;  // tiles of the blocks that have one more
     return static_cast<int>(x < large ? quotient(x, c.part + 1) : c.more + quotient(x - large, c.part));
@@ -124,8 +131,9 @@ __device__ __forceinline__ int range_owner(const Cursor &c, long long x)
 
 // Finds the range of block `block` of `grid`; one warp, all lanes get the
 // same.  at == end: nothing to do.
-__device__ __forceinline__ Cursor find_range(const Work &w, const PagedView &v, int block, int grid, int lane)
+template <typename W> __device__ __forceinline__ auto find_range(const W &w, const PagedView &v, int block, int grid, int lane)
 {
+    using Lens = decltype(lens_of(w, 0, v));
     const int per = w.row_tiles * v.kv_heads;
     // Tiles of sequences lane, lane + 32, ...: the first KEEP of them stay in registers, their loads all under way
     // at once (a load is about a microsecond when the lengths come from memory).
@@ -135,14 +143,14 @@ __device__ __forceinline__ Cursor find_range(const Work &w, const PagedView &v, 
 #pragma unroll
     for (int i = 0; i < KEEP; ++i) {
         const int b = 32 * i + lane;
-        tiles[i] = b < w.B ? tiles_of(w, seq_lens(w.ctx_lens, w.new_lens, b, w.T, v, w.idle)) : 0;
+        tiles[i] = b < w.B ? tiles_of(w, lens_of(w, b, v)) : 0;
         sum += tiles[i];
     }
-    for (int b = 32 * KEEP + lane; b < w.B; b += 32) sum += tiles_of(w, seq_lens(w.ctx_lens, w.new_lens, b, w.T, v, w.idle));
+    for (int b = 32 * KEEP + lane; b < w.B; b += 32) sum += tiles_of(w, lens_of(w, b, v));
 #pragma unroll
     for (int o = 16; o; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
     sum *= per;
-    Cursor c{};
+    CursorOf<Lens> c{};
     c.all = sum;
     c.blocks = sum < grid ? static_cast<int>(sum) : grid;
     if (block >= c.blocks) return c;
@@ -174,9 +182,9 @@ __device__ __forceinline__ Cursor find_range(const Work &w, const PagedView &v, 
         if (!found && 32 * i < w.B) look(32 * i, tiles[i]);
     for (int b0 = 32 * KEEP; !found && b0 < w.B; b0 += 32) {
         const int b = b0 + lane;
-        look(b0, b < w.B ? tiles_of(w, seq_lens(w.ctx_lens, w.new_lens, b, w.T, v, w.idle)) : 0);
+        look(b0, b < w.B ? tiles_of(w, lens_of(w, b, v)) : 0);
     }
-    c.s = seq_lens(w.ctx_lens, w.new_lens, c.b, w.T, v, w.idle);
+    c.s = lens_of(w, c.b, v);
     c.tiles = tiles_of(w, c.s);
     const long long in = c.at - before;
     const int item = static_cast<int>(quotient(in, c.tiles));
@@ -186,7 +194,7 @@ __device__ __forceinline__ Cursor find_range(const Work &w, const PagedView &v, 
     return c;
 }
 // To the next item (the range goes on behind the present one).
-__device__ __forceinline__ void next_item(Cursor &c, const Work &w, const PagedView &v)
+template <typename Lens, typename W> __device__ __forceinline__ void next_item(CursorOf<Lens> &c, const W &w, const PagedView &v)
 {
     c.first += c.tiles;
     c.at = c.first;
@@ -195,7 +203,7 @@ __device__ __forceinline__ void next_item(Cursor &c, const Work &w, const PagedV
     if (++c.row_tile < w.row_tiles) return;
     c.row_tile = 0;
     if (++c.b == w.B) return;  // the end of everything
-    c.s = seq_lens(w.ctx_lens, w.new_lens, c.b, w.T, v, w.idle);
+    c.s = lens_of(w, c.b, v);
     c.tiles = tiles_of(w, c.s);
 }
 

@@ -63,6 +63,113 @@ spv::KvLaunch kv_launch(const spv_kv_cache *cache, const int32_t *page_table, in
                          row_status};
 }
 
+// The checks and the launch that the two rotary calls share.
+spv_status rope_launch(spv::RopeLaunch *out, const void *q, const void *k, const void *v, spv_dtype dtype,
+                       const int64_t *strides, int B, int T, int q_heads, const uint64_t *freqs, int rotary_dim,
+                       int interleaved, float mscale, const int32_t *positions, const int32_t *ctx_lens,
+                       const int32_t *new_lens, const int32_t *page_table, int max_pages, const spv_kv_cache *cache,
+                       int32_t *slot_pos, int64_t pos_stride, void *q_out, int32_t *row_status)
+{
+    const spv_status st = check_tokens(q, dtype, B, T, q_heads, cache, page_table, max_pages, ctx_lens);
+    if (st != SPV_OK) return st;
+    const int D = cache->head_dim, kv_heads = cache->kv_heads;
+    if (!k || !v || !q_out || !aligned(k, 16) || !aligned(v, 16) || !aligned(q_out, 16)) return SPV_ERR_INVALID_ARG;
+    if (D > 512) return SPV_ERR_UNSUPPORTED;
+    if (rotary_dim < 0 || rotary_dim > D || rotary_dim % 2 != 0 || (rotary_dim > 0 && !freqs)) return SPV_ERR_INVALID_ARG;
+    if (!std::isfinite(mscale)) return SPV_ERR_INVALID_ARG;
+    if (slot_pos && pos_stride < 1) return SPV_ERR_INVALID_ARG;
+    if (static_cast<int64_t>(B) * T > 0x7fffffffll) return SPV_ERR_UNSUPPORTED;
+    spv::RopeLaunch &L = *out;
+    const int64_t qd = static_cast<int64_t>(q_heads) * D, kd = static_cast<int64_t>(kv_heads) * D;
+    const int64_t packed[6] = {T * qd, qd, T * kd, kd, T * kd, kd};
+    for (int i = 0; i < 6; ++i) {
+        L.strides[i] = strides ? strides[i] : packed[i];
+        if (L.strides[i] < 0 || L.strides[i] % 8 != 0) return SPV_ERR_INVALID_ARG;
+    }
+    if (q_out == q && (L.strides[0] != packed[0] || L.strides[1] != packed[1])) return SPV_ERR_INVALID_ARG;
+    L.kv = kv_launch(cache, page_table, max_pages, B, T, q_heads, dtype, ctx_lens, new_lens, nullptr, 0.0f, row_status);
+    L.q = q;
+    L.k = k;
+    L.v = v;
+    L.freqs = freqs;
+    L.rotary_dim = rotary_dim;
+    L.interleaved = interleaved != 0;
+    L.mscale = mscale;
+    L.positions = positions;
+    L.slot_pos = slot_pos;
+    L.pos_stride = pos_stride;
+    L.q_out = q_out;
+    return SPV_OK;
+}
+
+// The scores of a call; `tree`: its new tokens are one.
+spv_status check_scores(const spv_scores *s, bool tree)
+{
+    if (!s || !(s->cap >= 0.0f) || std::isinf(s->cap) || s->window < 0) return SPV_ERR_INVALID_ARG;
+    if (s->cap > 0.0f && s->cap < 1e-30f) return SPV_ERR_INVALID_ARG;  // 2 / cap has to be a number
+    if (s->last && tree) return SPV_ERR_INVALID_ARG;
+    if (s->slot_pos && s->pos_stride < 1) return SPV_ERR_INVALID_ARG;
+    return SPV_OK;
+}
+
+// The checks and the launch that the paged attention calls share.
+spv_status attention_launch(spv::AttentionLaunch *out_launch, const void *q, spv_dtype dtype, int B, int T, int q_heads,
+                            const spv_kv_cache *cache, const int32_t *page_table, int max_pages, const int32_t *ctx_lens,
+                            const int32_t *new_lens, const int32_t *parent, float scale, void *out, float *lse,
+                            int32_t *row_status, void *workspace, size_t workspace_bytes)
+{
+    spv_status st = check_tokens(q, dtype, B, T, q_heads, cache, page_table, max_pages, ctx_lens);
+    if (st != SPV_OK) return st;
+    st = check_attention_sizes(B, T, q_heads, cache->kv_heads, cache->head_dim);
+    if (st != SPV_OK) return st;
+    if (!out || !aligned(out, 16) || !workspace || !aligned(workspace, 256) || !std::isfinite(scale))
+        return SPV_ERR_INVALID_ARG;
+    if (workspace_bytes < spv::attention_ws_bytes(B, T, q_heads, cache->kv_heads, cache->head_dim))
+        return SPV_ERR_INVALID_ARG;
+    spv::AttentionLaunch &L = *out_launch;
+    L.kv = kv_launch(cache, page_table, max_pages, B, T, q_heads, dtype, ctx_lens, new_lens, parent, scale, row_status);
+    L.q = q;
+    L.out = out;
+    L.lse = lse;
+    L.ws = workspace;
+    return SPV_OK;
+}
+
+// The same of the weights of cached keys.
+spv_status mass_launch(spv::MassLaunch *out, const void *q, spv_dtype dtype, int B, int T, int q_heads, const float *lse,
+                       const spv_kv_cache *cache, const int32_t *page_table, int max_pages, const int32_t *ctx_lens,
+                       const int32_t *new_lens, const int32_t *parent, float scale, const int32_t *accept_count,
+                       const int32_t *nodes, float decay, const float *mass_in, float *mass_out, int64_t mass_stride,
+                       int32_t *row_status)
+{
+    spv_status st = check_tokens(q, dtype, B, T, q_heads, cache, page_table, max_pages, ctx_lens);
+    if (st != SPV_OK) return st;
+    st = check_attention_sizes(B, T, q_heads, cache->kv_heads, cache->head_dim);
+    if (st != SPV_OK) return st;
+    if (!lse || !accept_count || !mass_out || mass_stride < 1) return SPV_ERR_INVALID_ARG;
+    if (!std::isfinite(scale) || !std::isfinite(decay)) return SPV_ERR_INVALID_ARG;
+    spv::MassLaunch &L = *out;
+    L.kv = kv_launch(cache, page_table, max_pages, B, T, q_heads, dtype, ctx_lens, new_lens, parent, scale, row_status);
+    L.q = q;
+    L.lse = lse;
+    L.accept_count = accept_count;
+    L.nodes = nodes;
+    L.decay = decay;
+    L.mass_in = mass_in;
+    L.mass_out = mass_out;
+    L.mass_stride = mass_stride;
+    return SPV_OK;
+}
+
+// The shapes that the prompt kernels are built for.
+spv_status check_prompt_sizes(int B, int T, int q_heads, int kv_heads, int head_dim)
+{
+    if (q_heads / kv_heads > SPV_MAX_GROUP || B > 65535) return SPV_ERR_UNSUPPORTED;
+    if (static_cast<int64_t>(T) * (q_heads / kv_heads) > (1ll << 24)) return SPV_ERR_UNSUPPORTED;
+    if (head_dim != 64 && head_dim != 128 && head_dim != 256) return SPV_ERR_UNSUPPORTED;
+    return SPV_OK;
+}
+
 std::atomic<int64_t> give_up_at{-1};  // block << 32 | item
 
 }  // namespace
@@ -118,36 +225,36 @@ spv_status spv_rope_append(const void *q, const void *k, const void *v, spv_dtyp
                            const int32_t *page_table, int max_pages, const spv_kv_cache *cache, int32_t *slot_pos,
                            int64_t pos_stride, void *q_out, int32_t *row_status, void *stream)
 {
-    const spv_status st = check_tokens(q, dtype, B, T, q_heads, cache, page_table, max_pages, ctx_lens);
-    if (st != SPV_OK) return st;
-    const int D = cache->head_dim, kv_heads = cache->kv_heads;
-    if (!k || !v || !q_out || !aligned(k, 16) || !aligned(v, 16) || !aligned(q_out, 16)) return SPV_ERR_INVALID_ARG;
-    if (D > 512) return SPV_ERR_UNSUPPORTED;
-    if (rotary_dim < 0 || rotary_dim > D || rotary_dim % 2 != 0 || (rotary_dim > 0 && !freqs)) return SPV_ERR_INVALID_ARG;
-    if (!std::isfinite(mscale)) return SPV_ERR_INVALID_ARG;
-    if (slot_pos && pos_stride < 1) return SPV_ERR_INVALID_ARG;
-    if (static_cast<int64_t>(B) * T > 0x7fffffffll) return SPV_ERR_UNSUPPORTED;
     spv::RopeLaunch L{};
-    const int64_t qd = static_cast<int64_t>(q_heads) * D, kd = static_cast<int64_t>(kv_heads) * D;
-    const int64_t packed[6] = {T * qd, qd, T * kd, kd, T * kd, kd};
-    for (int i = 0; i < 6; ++i) {
-        L.strides[i] = strides ? strides[i] : packed[i];
-        if (L.strides[i] < 0 || L.strides[i] % 8 != 0) return SPV_ERR_INVALID_ARG;
-    }
-    if (q_out == q && (L.strides[0] != packed[0] || L.strides[1] != packed[1])) return SPV_ERR_INVALID_ARG;
-    L.kv = kv_launch(cache, page_table, max_pages, B, T, q_heads, dtype, ctx_lens, new_lens, nullptr, 0.0f, row_status);
-    L.q = q;
-    L.k = k;
-    L.v = v;
-    L.freqs = freqs;
-    L.rotary_dim = rotary_dim;
-    L.interleaved = interleaved != 0;
-    L.mscale = mscale;
-    L.positions = positions;
-    L.slot_pos = slot_pos;
-    L.pos_stride = pos_stride;
-    L.q_out = q_out;
+    const spv_status st = rope_launch(&L, q, k, v, dtype, strides, B, T, q_heads, freqs, rotary_dim, interleaved, mscale,
+                                      positions, ctx_lens, new_lens, page_table, max_pages, cache, slot_pos, pos_stride, q_out,
+                                      row_status);
+    if (st != SPV_OK) return st;
     return cuda_status(spv::launch_rope(L, static_cast<cudaStream_t>(stream)));
+}
+
+spv_status spv_norm_rope_append(const void *q, const void *k, const void *v, spv_dtype dtype, const int64_t *strides,
+                                int B, int T, int q_heads, const float *q_weight, const float *k_weight, float eps,
+                                const uint64_t *freqs, const int32_t *axes, int num_axes, int rotary_dim,
+                                int interleaved, float mscale, const int32_t *positions, const int32_t *ctx_lens,
+                                const int32_t *new_lens, const int32_t *page_table, int max_pages,
+                                const spv_kv_cache *cache, int32_t *slot_pos, int64_t pos_stride, void *q_out,
+                                int32_t *row_status, void *stream)
+{
+    spv::NormRopeLaunch L{};
+    const spv_status st = rope_launch(&L.rope, q, k, v, dtype, strides, B, T, q_heads, freqs, rotary_dim, interleaved, mscale,
+                                      positions, ctx_lens, new_lens, page_table, max_pages, cache, slot_pos, pos_stride, q_out,
+                                      row_status);
+    if (st != SPV_OK) return st;
+    if (cache->head_dim > 256) return SPV_ERR_UNSUPPORTED;
+    if (!(eps >= 0.0f) || std::isinf(eps) || num_axes < 1 || num_axes > 8) return SPV_ERR_INVALID_ARG;
+    if (num_axes > 1 && !positions) return SPV_ERR_INVALID_ARG;
+    L.q_weight = q_weight;
+    L.k_weight = k_weight;
+    L.eps = eps;
+    L.axes = axes;
+    L.num_axes = num_axes;
+    return cuda_status(spv::launch_norm_rope(L, static_cast<cudaStream_t>(stream)));
 }
 
 size_t spv_attention_workspace_bytes(int B, int T, int q_heads, int kv_heads, int head_dim)
@@ -162,21 +269,60 @@ spv_status spv_paged_attention(const void *q, spv_dtype dtype, int B, int T, int
                                const int32_t *new_lens, const int32_t *parent, float scale, void *out, float *lse,
                                int32_t *row_status, void *workspace, size_t workspace_bytes, void *stream)
 {
+    spv::AttentionLaunch L{};
+    const spv_status st = attention_launch(&L, q, dtype, B, T, q_heads, cache, page_table, max_pages, ctx_lens, new_lens, parent,
+                                           scale, out, lse, row_status, workspace, workspace_bytes);
+    if (st != SPV_OK) return st;
+    return cuda_status(spv::launch_attention(L, static_cast<cudaStream_t>(stream)));
+}
+
+spv_status spv_paged_attention_scored(const void *q, spv_dtype dtype, int B, int T, int q_heads,
+                                      const spv_kv_cache *cache, const int32_t *page_table, int max_pages,
+                                      const int32_t *ctx_lens, const int32_t *new_lens, const int32_t *parent,
+                                      float scale, const spv_scores *scores, void *out, float *lse,
+                                      int32_t *row_status, void *workspace, size_t workspace_bytes, void *stream)
+{
+    spv::AttentionLaunch L{};
+    spv_status st = attention_launch(&L, q, dtype, B, T, q_heads, cache, page_table, max_pages, ctx_lens, new_lens, parent,
+                                     scale, out, lse, row_status, workspace, workspace_bytes);
+    if (st != SPV_OK) return st;
+    st = check_scores(scores, parent != nullptr);
+    if (st != SPV_OK) return st;
+    L.scores = *scores;
+    return cuda_status(spv::launch_attention_scored(L, static_cast<cudaStream_t>(stream)));
+}
+
+size_t spv_prompt_workspace_bytes(int B, int T, int q_heads, int kv_heads, int head_dim)
+{
+    if (B < 1 || T < 1 || q_heads < 1 || kv_heads < 1 || q_heads % kv_heads != 0) return 0;
+    if (check_prompt_sizes(B, T, q_heads, kv_heads, head_dim) != SPV_OK) return 0;
+    return spv::prompt_ws_bytes(B, T, q_heads, kv_heads, head_dim);
+}
+
+spv_status spv_prompt_attention(const void *q, spv_dtype dtype, int B, int T, int q_heads, const spv_kv_cache *cache,
+                                const int32_t *page_table, int max_pages, const int32_t *ctx_lens,
+                                const int32_t *new_lens, float scale, const spv_scores *scores, void *out, float *lse,
+                                int32_t *row_status, void *workspace, size_t workspace_bytes, void *stream)
+{
     spv_status st = check_tokens(q, dtype, B, T, q_heads, cache, page_table, max_pages, ctx_lens);
     if (st != SPV_OK) return st;
-    st = check_attention_sizes(B, T, q_heads, cache->kv_heads, cache->head_dim);
+    st = check_prompt_sizes(B, T, q_heads, cache->kv_heads, cache->head_dim);
     if (st != SPV_OK) return st;
     if (!out || !aligned(out, 16) || !workspace || !aligned(workspace, 256) || !std::isfinite(scale))
         return SPV_ERR_INVALID_ARG;
-    if (workspace_bytes < spv::attention_ws_bytes(B, T, q_heads, cache->kv_heads, cache->head_dim))
-        return SPV_ERR_INVALID_ARG;
+    if (workspace_bytes < spv::prompt_ws_bytes(B, T, q_heads, cache->kv_heads, cache->head_dim)) return SPV_ERR_INVALID_ARG;
     spv::AttentionLaunch L{};
-    L.kv = kv_launch(cache, page_table, max_pages, B, T, q_heads, dtype, ctx_lens, new_lens, parent, scale, row_status);
+    if (scores) {
+        st = check_scores(scores, false);
+        if (st != SPV_OK) return st;
+        L.scores = *scores;
+    }
+    L.kv = kv_launch(cache, page_table, max_pages, B, T, q_heads, dtype, ctx_lens, new_lens, nullptr, scale, row_status);
     L.q = q;
     L.out = out;
     L.lse = lse;
     L.ws = workspace;
-    return cuda_status(spv::launch_attention(L, static_cast<cudaStream_t>(stream)));
+    return cuda_status(spv::launch_prompt(L, static_cast<cudaStream_t>(stream)));
 }
 
 spv_status spv_attention_mass(const void *q, spv_dtype dtype, int B, int T, int q_heads, const float *lse,
@@ -185,23 +331,28 @@ spv_status spv_attention_mass(const void *q, spv_dtype dtype, int B, int T, int 
                               const int32_t *accept_count, const int32_t *nodes, float decay, const float *mass_in,
                               float *mass_out, int64_t mass_stride, int32_t *row_status, void *stream)
 {
-    spv_status st = check_tokens(q, dtype, B, T, q_heads, cache, page_table, max_pages, ctx_lens);
-    if (st != SPV_OK) return st;
-    st = check_attention_sizes(B, T, q_heads, cache->kv_heads, cache->head_dim);
-    if (st != SPV_OK) return st;
-    if (!lse || !accept_count || !mass_out || mass_stride < 1) return SPV_ERR_INVALID_ARG;
-    if (!std::isfinite(scale) || !std::isfinite(decay)) return SPV_ERR_INVALID_ARG;
     spv::MassLaunch L{};
-    L.kv = kv_launch(cache, page_table, max_pages, B, T, q_heads, dtype, ctx_lens, new_lens, parent, scale, row_status);
-    L.q = q;
-    L.lse = lse;
-    L.accept_count = accept_count;
-    L.nodes = nodes;
-    L.decay = decay;
-    L.mass_in = mass_in;
-    L.mass_out = mass_out;
-    L.mass_stride = mass_stride;
+    const spv_status st = mass_launch(&L, q, dtype, B, T, q_heads, lse, cache, page_table, max_pages, ctx_lens, new_lens, parent,
+                                      scale, accept_count, nodes, decay, mass_in, mass_out, mass_stride, row_status);
+    if (st != SPV_OK) return st;
     return cuda_status(spv::launch_mass(L, static_cast<cudaStream_t>(stream)));
+}
+
+spv_status spv_attention_mass_scored(const void *q, spv_dtype dtype, int B, int T, int q_heads, const float *lse,
+                                     const spv_kv_cache *cache, const int32_t *page_table, int max_pages,
+                                     const int32_t *ctx_lens, const int32_t *new_lens, const int32_t *parent,
+                                     float scale, const spv_scores *scores, const int32_t *accept_count,
+                                     const int32_t *nodes, float decay, const float *mass_in, float *mass_out,
+                                     int64_t mass_stride, int32_t *row_status, void *stream)
+{
+    spv::MassLaunch L{};
+    spv_status st = mass_launch(&L, q, dtype, B, T, q_heads, lse, cache, page_table, max_pages, ctx_lens, new_lens, parent, scale,
+                                accept_count, nodes, decay, mass_in, mass_out, mass_stride, row_status);
+    if (st != SPV_OK) return st;
+    st = check_scores(scores, parent != nullptr);
+    if (st != SPV_OK) return st;
+    L.scores = *scores;
+    return cuda_status(spv::launch_mass_scored(L, static_cast<cudaStream_t>(stream)));
 }
 
 spv_status spv_kv_evict(const spv_kv_cache *cache, const int32_t *page_table, int max_pages, int B,

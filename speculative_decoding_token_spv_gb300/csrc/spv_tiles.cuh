@@ -1,0 +1,1127 @@
+// spv_tiles.cuh -- attention over the paged cache in tiles of query rows: whole
+// prompts, and drafted chains and trees of many rows a key head with scores and
+// masks (spv_scores).  5th-generation tensor cores.
+//
+// Mathematics: as in spv_attention_warps.cuh.  The rows of an item -- a
+// sequence, a tile of new tokens x query heads of a key head's group, a key head
+// -- see slots of an interval each, so the item has the tiles of keys between
+// the lowest and the highest slot that any of its rows sees, and masks are
+// looked at only in tiles that some row does not see whole.
+//
+// What bounds it are the products, 4 D operations for a row and a key, and the
+// exponentials beside them (a prompt reads its keys from the L2 after the first
+// time).  One block an SM with an equal range of all tiles of all items, found
+// from the lengths on the device; in it
+//   * PAIR: 256 rows as two tiles of 128.  Four warps hold the first's rows, a
+//     row a thread, four the second's, and while one of them makes its
+//     exponentials the tensor cores have the products of the other.  Scores and
+//     outputs of both fill tensor memory (2 x 128 + 2 x 128 columns); the
+//     weights go where their scores were;
+//   * else 128 rows, of which two warps share each row's keys (few rows; and D =
+//     256, whose outputs take half of tensor memory).  Scores stand in two
+//     places in turn;
+//   * a warp issues the products, three bring q, four K and V in turn into one
+//     ring, a box a page by the copy engine, or row by row (small pages; a
+//     sequence's last tile of V, whose slots past the end become zero; e4m3,
+//     which lands as it is and is widened to f16 by the threads that loaded it).
+// O is only rescaled when a maximum has grown by more than 2^8 (2^7 for f16).
+// The blocks' pieces of an item that they share are joined by a dependent
+// launch, in their order.
+//
+// A weight of 0 and an infinity in V make NaN, which a row must not get from a
+// slot that it does not see: rows whose result is not finite are computed again
+// at the end of a block's range, key by key over what they see.
+//
+// Every wait is bounded; one that gives up records SPV_ERR_TIMEOUT in the
+// workspace, ends the block in order and leaves NaN in all that it still had to
+// write.
+#pragma once
+
+#include "spv_scored.cuh"
+#include "spv_tcgen.cuh"
+#include "spv_tma.cuh"
+
+namespace spv {
+
+constexpr int TILES_THREADS = 512;
+constexpr int TILES_WARPS = TILES_THREADS / 32;
+constexpr int TILES_PREPARE = 96;  // threads that bring q
+constexpr int TILES_ITEMS = 16;    // items whose flags can be in use at once
+
+struct TilesParams : ScoredParams {
+    int32_t *timeouts;  // row_status, for waits that gave up
+    int q_bf16;
+};
+
+template <typename C, int D, bool PAIR> struct TilesShape {
+    static constexpr bool WIDEN = sizeof(C) == 1;
+    static constexpr int SUBS = PAIR ? 2 : 1, ROWS = 128 * SUBS;
+    static constexpr int KEYS = D == 256 ? 64 : 128;             // of a tile
+    static constexpr int MINE = PAIR ? KEYS : KEYS / 2;          // of them a thread's
+    static constexpr int TILE = KEYS * D * 2, RAW = KEYS * D;    // bytes of K or V as multiplied, and of e4m3
+    static constexpr int Q_SUB = 128 * D * 2, Q = SUBS * Q_SUB;
+    static constexpr int Q_PLACES = 2 * Q <= 64 * 1024 ? 2 : 1;
+    static constexpr int ROOM = 224 * 1024 - Q_PLACES * Q;
+    static constexpr int RAW_STAGES = WIDEN ? 64 * 1024 / RAW : 0;
+    static constexpr int FIT = (ROOM - RAW_STAGES * RAW) / TILE, STAGES = FIT < 10 ? FIT : 10;
+    static constexpr int K_AT = Q_PLACES * Q, RAW_AT = K_AT + STAGES * TILE, CTL_AT = RAW_AT + RAW_STAGES * RAW;
+    static constexpr int GROUP = PAIR ? 128 : 256;               // threads that belong to the same rows
+};
+
+// An item's tiles of keys: [from, to), and of each tile of rows.
+struct TileLens : SeqLens {
+    int from, to, lo[2], hi[2];
+};
+using TileCursor = CursorOf<TileLens>;
+
+template <typename S> struct TilesCtl {
+    uint64_t full[10], empty[10], s_full[2], p_full[2], o_done[2], q_full[2], q_empty[2], spare;
+    TileCursor start;
+    int bad[2][TILES_ITEMS];                                     // a page id outside the pool, for each group of row warps
+    int stop[2], lost[2];
+    alignas(16) int positions[2][S::MINE];                       // of moved slots: of a tile's keys, for each four row warps
+    uint32_t tmem;
+    int dead;
+    union {
+        struct {
+            long long sums[TILES_WARPS];                         // before the roles begin
+        } find;
+        struct {
+            signed char depth[2][S::SUBS == 1 ? 64 : 1];         // trees: per place of q the depth of each new token
+            float top[S::SUBS == 1 ? 256 : 1];                   // maxima and sums of the two halves
+            signed char q_power[S::WIDEN ? S::Q_PLACES * S::ROWS : 1];  // e4m3: the rows of q are stored times 2^q_power
+        } at;
+    };
+};
+
+template <typename Ctl> __device__ __forceinline__ bool tiles_wait(Ctl *ctl, uint64_t *bar, uint32_t parity, unsigned *err)
+{
+    bool ok = false;
+    for (uint32_t i = 0; i < WAIT_LIMIT; ++i) {
+        if (mbar_try_wait(bar, parity)) {
+            ok = true;
+            break;
+        }
+        if ((i & 63) == 63 && *reinterpret_cast<volatile int *>(&ctl->dead)) break;
+    }
+    if (!ok && !*reinterpret_cast<volatile int *>(&ctl->dead)) {
+        *reinterpret_cast<volatile int *>(&ctl->dead) = 1;
+        atomicExch(err, static_cast<unsigned>(STATUS_TIMEOUT));
+    }
+    return __all_sync(0xffffffffu, ok);
+}
+
+// ------------------------------------------------------------------ the cut of the work
+__device__ __forceinline__ SeqLens tiles_lens(const TilesParams &p, int b)
+{
+    SeqLens s = seq_lens(p.w.ctx_lens, p.w.new_lens, b, p.w.T, p.c);
+    if (p.sc.slot_pos && !s.bad && s.ctx + s.fresh > p.sc.pos_stride) {
+        s.bad = true;
+        s.total = 0;
+    }
+    return s;
+}
+
+// Slots [lo, hi) that new token t sees (not of a tree).
+struct Interval {
+    int lo, hi;
+};
+__device__ __forceinline__ Interval token_interval(const TilesParams &p, const SeqLens &s, int b, int t)
+{
+    Interval r{0, s.ctx + t + 1};
+    if (p.sc.window > 0 && !p.sc.slot_pos) r.lo = max(0, s.ctx + t - p.sc.window + 1);
+    const int64_t at = static_cast<int64_t>(b) * p.w.T + t;
+    if (p.sc.first) r.lo = max(r.lo, __ldg(p.sc.first + at));
+    if (p.sc.last) r.hi = max(r.hi, min(s.total, __ldg(p.sc.last + at)));
+    return r;
+}
+
+// Tiles of the item's rows.  Where tokens have documents or prefixes a warp
+// looks at them together, all lanes for the same item; else each lane may ask
+// for an item of its own.
+template <typename S> __device__ __forceinline__ TileLens item_tiles(const TilesParams &p, const SeqLens &s, int b, int row_tile, int lane)
+{
+    TileLens r;
+    static_cast<SeqLens &>(r) = s;
+    r.from = 0x7fffffff;
+    r.to = 0;
+    const bool sliding = p.sc.window > 0 && !p.sc.slot_pos;
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+        r.lo[k] = r.hi[k] = 0;
+        if (k >= S::SUBS) continue;
+        const int r0 = row_tile * S::ROWS + 128 * k, r1 = min(r0 + 128, p.rows);
+        if (r0 >= r1 || s.total == 0) continue;
+        const int ta = r0 / p.group, tb = min((r1 - 1) / p.group, s.fresh - 1);
+        if (ta > tb) continue;
+        int lo, hi;
+        if (!p.sc.first && !p.sc.last) {
+            lo = sliding ? max(0, s.ctx + (p.parent ? 0 : ta) - p.sc.window + 1) : 0;
+            hi = p.parent ? s.total : s.ctx + tb + 1;
+        } else {
+            lo = 0x7fffffff;
+            hi = 0;
+            for (int t = ta + lane; t <= tb; t += 32) {
+                Interval x = token_interval(p, s, b, t);
+                if (p.parent) {  // a node's depth is not known here: at least 0
+                    x.lo = max(__ldg(p.sc.first + static_cast<int64_t>(b) * p.w.T + t), sliding ? max(0, s.ctx - p.sc.window + 1) : 0);
+                    x.hi = s.total;
+                }
+                if (x.lo < x.hi) {
+                    lo = min(lo, x.lo);
+                    hi = max(hi, x.hi);
+                }
+            }
+            lo = __reduce_min_sync(0xffffffffu, lo);
+            hi = __reduce_max_sync(0xffffffffu, hi);
+            lo = max(lo, 0);
+        }
+        if (lo >= hi) continue;
+        r.lo[k] = lo / S::KEYS;
+        r.hi[k] = (hi + S::KEYS - 1) / S::KEYS;
+        r.from = min(r.from, r.lo[k]);
+        r.to = max(r.to, r.hi[k]);
+    }
+    if (r.to == 0) r.from = 0;
+    return r;
+}
+__device__ __forceinline__ int count_of(const TileLens &s) { return max(1, s.to - s.from); }
+
+// The block's range, by all its threads; `c` is the same for all.
+template <typename S> __device__ TileCursor tiles_find(const TilesParams &p, TilesCtl<S> *ctl, int tid)
+{
+    const int lane = tid & 31, warp = tid >> 5, entries = p.w.B * p.w.row_tiles;
+    const int each = (entries + TILES_WARPS - 1) / TILES_WARPS, e0 = warp * each, e1 = min(entries, e0 + each);
+    const bool together = p.sc.first || p.sc.last;
+    auto count32 = [&](int e) {  // tiles of a head of entry e + lane
+        int mine = 0;
+        if (!together) {
+            if (e + lane < e1) {
+                const int b = (e + lane) / p.w.row_tiles;
+                mine = count_of(item_tiles<S>(p, tiles_lens(p, b), b, e + lane - b * p.w.row_tiles, lane));
+            }
+        } else {
+            for (int i = 0; i < 32 && e + i < e1; ++i) {
+                const int b = (e + i) / p.w.row_tiles;
+                const int n = count_of(item_tiles<S>(p, tiles_lens(p, b), b, e + i - b * p.w.row_tiles, lane));
+                if (i == lane) mine = n;
+            }
+        }
+        return mine;
+    };
+    long long sum = 0;
+    for (int e = e0; e < e1; e += 32) sum += count32(e);
+#pragma unroll
+    for (int o = 16; o; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+    if (lane == 0) ctl->find.sums[warp] = sum * p.c.kv_heads;
+    __syncthreads();
+    TileCursor c{};
+    long long before = 0, mine = ctl->find.sums[warp];
+    for (int i = 0; i < TILES_WARPS; ++i) {
+        if (i < warp) before += ctl->find.sums[i];
+        c.all += ctl->find.sums[i];
+    }
+    c.blocks = c.all < gridDim.x ? static_cast<int>(c.all) : static_cast<int>(gridDim.x);
+    const int block = blockIdx.x;
+    if (block < c.blocks) {
+        c.part = quotient(c.all, c.blocks);
+        c.more = static_cast<int>(c.all - c.part * c.blocks);
+        c.at = range_begin(c, block);
+        c.end = range_begin(c, block + 1);
+        if (c.at >= before && c.at < before + mine) {
+            for (int e = e0; e < e1; e += 32) {
+                const int n = count32(e);
+                int upto = n;
+#pragma unroll
+                for (int o = 1; o < 32; o <<= 1) {
+                    const int y = __shfl_up_sync(0xffffffffu, upto, o);
+                    if (lane >= o) upto += y;
+                }
+                const unsigned here = __ballot_sync(0xffffffffu, before + static_cast<long long>(upto) * p.c.kv_heads > c.at);
+                if (here) {
+                    const int l = __ffs(here) - 1;
+                    const int tiles = __shfl_sync(0xffffffffu, n, l);
+                    before += static_cast<long long>(__shfl_sync(0xffffffffu, upto, l) - tiles) * p.c.kv_heads;
+                    c.tiles = tiles;
+                    c.b = (e + l) / p.w.row_tiles;
+                    c.row_tile = e + l - c.b * p.w.row_tiles;
+                    c.h = static_cast<int>(quotient(c.at - before, tiles));
+                    c.first = before + static_cast<long long>(c.h) * tiles;
+                    if (lane == 0) ctl->start = c;
+                    break;
+                }
+                before += static_cast<long long>(__shfl_sync(0xffffffffu, upto, 31)) * p.c.kv_heads;
+            }
+        }
+    }
+    __syncthreads();
+    if (block < c.blocks) {
+        c = ctl->start;
+        c.s = item_tiles<S>(p, tiles_lens(p, c.b), c.b, c.row_tile, lane);
+    }
+    __syncthreads();  // the sums' place is free
+    return c;
+}
+// To the next item; a whole warp.
+template <typename S> __device__ __forceinline__ void tiles_next(TileCursor &c, const TilesParams &p, int lane)
+{
+    c.first += c.tiles;
+    c.at = c.first;
+    if (++c.h < p.c.kv_heads) return;
+    c.h = 0;
+    if (++c.row_tile == p.w.row_tiles) {
+        c.row_tile = 0;
+        if (++c.b == p.w.B) return;  // the end of everything
+    }
+    c.s = item_tiles<S>(p, tiles_lens(p, c.b), c.b, c.row_tile, lane);
+    c.tiles = count_of(c.s);
+}
+// The block's tiles of the cursor's item: [first, last), none for an item without keys.
+__device__ __forceinline__ int tiles_first(const TileCursor &c) { return c.s.from + static_cast<int>(c.at - c.first); }
+__device__ __forceinline__ int tiles_last(const TileCursor &c)
+{
+    if (c.s.to == 0) return tiles_first(c);
+    const long long e = c.first + c.tiles;
+    return c.s.from + static_cast<int>((c.end < e ? c.end : e) - c.first);
+}
+__device__ __forceinline__ bool item_whole(const TileCursor &c) { return c.s.to == 0 || (c.at == c.first && c.end >= c.first + c.tiles); }
+
+// 16-byte chunk `chunk` of row `row` in an operand of ROWS rows.
+template <int ROWS> __device__ __forceinline__ uint32_t tile_at(int row, int chunk)
+{
+    return (chunk >> 3) * (ROWS * 128) + row * 128 + (((chunk & 7) ^ (row & 7)) << 4);
+}
+
+// ------------------------------------------------------------------ K and V
+// Four warps: tiles of K and V in turn.
+template <typename C, int D, bool PAIR, typename S = TilesShape<C, D, PAIR>>
+__device__ void tiles_load(const TilesParams &p, TileCursor c, char *smem, TilesCtl<S> *ctl, unsigned *err, int lt,
+                           const CUtensorMap *map_k, const CUtensorMap *map_v)
+{
+    constexpr int CH = D * static_cast<int>(sizeof(C)) / 16, RPI = 32 / CH, NST = S::STAGES, KEYS = S::KEYS, WARP_ROWS = KEYS / 4;
+    constexpr int RST = S::WIDEN ? S::RAW_STAGES : 1;
+    const int lane = lt & 31, w = lt >> 5, chunk = lane % CH, sub = lane / CH;
+    const uint32_t base = smem_u32(smem);
+    const int mask = (1 << p.c.page_shift) - 1;
+    int n = 0, item = 0;  // tiles of K and V so far, items with tiles
+
+    // e4m3: widens tile t, whose copies have landed; each thread what it has loaded.
+    auto widen = [&](int t) -> bool {
+        const int st = t % NST;
+        if (t >= NST && !tiles_wait(ctl, &ctl->empty[st], (t / NST - 1) & 1, err)) return false;
+        const char *raw = smem + S::RAW_AT + (t % RST) * S::RAW;
+        char *to = smem + S::K_AT + st * S::TILE;
+#pragma unroll 2
+        for (int i = 0; i < WARP_ROWS / RPI; ++i) {
+            const int row = WARP_ROWS * w + i * RPI + sub;
+            const uint4 x = *reinterpret_cast<const uint4 *>(raw + row * D + chunk * 16);
+            const uint32_t b[4] = {x.x, x.y, x.z, x.w};
+            uint32_t y[8];
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                y[2 * k] = e4m3x2_to_f16x2(b[k] & 0xffffu);
+                y[2 * k + 1] = e4m3x2_to_f16x2(b[k] >> 16);
+            }
+            const bool swap = (chunk >> 2) & 1;  // lanes of two panels store their halves in opposite order
+            const uint4 lo = make_uint4(y[0], y[1], y[2], y[3]), hi = make_uint4(y[4], y[5], y[6], y[7]);
+            *reinterpret_cast<uint4 *>(to + tile_at<KEYS>(row, 2 * chunk + swap)) = swap ? hi : lo;
+            *reinterpret_cast<uint4 *>(to + tile_at<KEYS>(row, 2 * chunk + !swap)) = swap ? lo : hi;
+        }
+        fence_async_shared();
+        mbar_arrive(&ctl->full[st]);
+        return true;
+    };
+    bool ok = true;
+    for (; ok && c.at < c.end; tiles_next<S>(c, p, lane)) {
+        const int t0 = tiles_first(c), t1 = tiles_last(c);
+        if (t0 == t1) continue;
+        const int32_t *table = p.c.table + static_cast<int64_t>(c.b) * p.c.max_pages;
+        const int flags = item++ % TILES_ITEMS;
+        auto lookup = [&](int tile) {  // the page id of this lane's row of a tile, unchecked; -1: no such row
+            const int j = tile * KEYS + WARP_ROWS * w + lane;
+            return lane < WARP_ROWS && tile < t1 && j < c.s.total ? __ldg(table + (j >> p.c.page_shift)) : -1;
+        };
+        // With maps the first warp's lanes ask the copy engine for a box each: a page (or what a tile holds of a larger one)
+        // by 64 elements.
+        const int box_slots = min(mask + 1, KEYS), boxes = map_k ? KEYS / box_slots * (D / 64) : 0;
+        auto box_lookup = [&](int tile) {
+            const int j = tile * KEYS + lane / (D / 64) * box_slots;
+            return w == 0 && lane < boxes && tile < t1 && j < c.s.total ? __ldg(table + (j >> p.c.page_shift)) : -1;
+        };
+        int next = map_k ? box_lookup(t0) : lookup(t0);
+        for (int tile = t0; ok && tile < t1; ++tile) {
+            const int j0 = tile * KEYS, page = next;
+            next = map_k ? box_lookup(tile + 1) : lookup(tile + 1);
+#pragma unroll 1
+            for (int kv = 0; kv < 2; ++kv, ++n) {
+                const PoolView &pool = kv ? p.c.v : p.c.k;
+                const int st = n % NST;
+                if (map_k && (!kv || j0 + KEYS <= c.s.total)) {
+                    const int slot = j0 + lane / (D / 64) * box_slots;
+                    if (w == 0 && lane < boxes && slot < c.s.total && static_cast<unsigned>(page) >= static_cast<unsigned>(p.c.num_pages))
+                        *reinterpret_cast<volatile int *>(&ctl->bad[0][flags]) = *reinterpret_cast<volatile int *>(&ctl->bad[1][flags]) = 1;
+                    if (n >= NST && !(ok = tiles_wait(ctl, &ctl->empty[st], (n / NST - 1) & 1, err))) break;
+                    if (lt == 0)
+                        mbar_arrive_expect_tx(&ctl->full[st], S::TILE);
+                    else
+                        mbar_arrive(&ctl->full[st]);
+                    if (w == 0) {
+                        __syncwarp();
+                        if (lane < boxes)
+                            tma_box(base + S::K_AT + st * S::TILE + (lane % (D / 64)) * (KEYS * 128) + lane / (D / 64) * box_slots * 128,
+                                    kv ? map_v : map_k, (lane % (D / 64)) * 64, slot & mask, c.h, page, &ctl->full[st]);
+                    }
+                    continue;
+                }
+                int pg = map_k ? lookup(tile) : page;
+                if (static_cast<unsigned>(pg) >= static_cast<unsigned>(p.c.num_pages)) {
+                    if (lane < WARP_ROWS && j0 + WARP_ROWS * w + lane < c.s.total)
+                        *reinterpret_cast<volatile int *>(&ctl->bad[0][flags]) = *reinterpret_cast<volatile int *>(&ctl->bad[1][flags]) = 1;
+                    pg = -1;
+                }
+                const int64_t mine = pg < 0 ? -1 : pg * pool.page_stride + ((j0 + WARP_ROWS * w + lane) & mask) * pool.slot_stride;
+                const char *from = pool.base + c.h * pool.head_stride + chunk * 16;
+                uint32_t to;
+                if (S::WIDEN) {  // the raw stages are each thread's own
+                    if (n >= RST) {
+                        cp_async_wait<RST - 1>();
+                        if (!(ok = widen(n - RST))) break;
+                    }
+                    to = base + S::RAW_AT + (n % RST) * S::RAW;
+                } else {
+                    if (n >= NST && !(ok = tiles_wait(ctl, &ctl->empty[st], (n / NST - 1) & 1, err))) break;
+                    to = base + S::K_AT + st * S::TILE;
+                }
+#pragma unroll 2
+                for (int i = 0; i < WARP_ROWS / RPI; ++i) {
+                    const int row = WARP_ROWS * w + i * RPI + sub;
+                    const int64_t at = __shfl_sync(0xffffffffu, mine, i * RPI + sub);
+                    cp_async16_zfill(to + (S::WIDEN ? row * D + chunk * 16 : tile_at<KEYS>(row, chunk)), at < 0 ? pool.base : from + at,
+                                     at < 0 ? 0 : 16);
+                }
+                if (S::WIDEN)
+                    cp_async_commit();
+                else
+                    cp_async_arrive(&ctl->full[st]);
+            }
+        }
+    }
+    asm volatile("cp.async.wait_all;" ::: "memory");
+    if (S::WIDEN) {  // the tiles still on their way
+        for (int t = n >= RST ? n - RST : 0; ok && t < n; ++t) ok = widen(t);
+    } else if (map_k && w == 0) {  // the copy engine's, before the block may end: nobody else may have waited for them
+        for (int t = max(0, n - NST); t < n; ++t) mbar_drain(&ctl->full[t % NST], (t / NST) & 1);
+    }
+}
+
+// ------------------------------------------------------------------ products
+// One warp; its first lane issues.
+template <typename C, int D, bool PAIR, typename S = TilesShape<C, D, PAIR>>
+__device__ void tiles_multiply(const TilesParams &p, TileCursor c, char *smem, TilesCtl<S> *ctl, unsigned *err, int lane)
+{
+    constexpr bool BF16 = std::is_same<C, __nv_bfloat16>::value;
+    constexpr uint32_t QK = mma_shape(BF16, false, S::KEYS), PV = mma_shape(BF16, true, D);
+    constexpr int NST = S::STAGES, KEYS = S::KEYS;
+    const uint32_t base = smem_u32(smem), tmem = ctl->tmem;
+    int n = 0, item = 0, weights[2] = {0, 0};  // tiles of K and V before the item's; weights of each place so far
+    bool ok = true;
+    for (; ok && c.at < c.end; tiles_next<S>(c, p, lane)) {
+        const int t0 = tiles_first(c), tiles = tiles_last(c) - t0;
+        if (tiles == 0) continue;
+        const int place = item % S::Q_PLACES;
+        if (!tiles_wait(ctl, &ctl->q_full[place], (item / S::Q_PLACES) & 1, err)) return;
+        bool begun[2] = {false, false}, pending[2] = {false, false};
+        auto waits = [&](int t) { return tiles_wait(ctl, &ctl->full[t % NST], (t / NST) & 1, err); };
+        auto release = [&](int t) {
+            if (lane == 0) tc_commit(&ctl->empty[t % NST]);
+        };
+        auto scores = [&](int s, int i) {  // of the rows' tile (PAIR) or place s with tile i of keys
+            if (lane == 0) {
+                tc_fence_after();
+                fence_async_shared();  // K may have been written by asynchronous copies of threads
+                const uint64_t q = desc_k_major(base + place * S::Q + (PAIR ? s * S::Q_SUB : 0));
+                const uint64_t k = desc_k_major(base + S::K_AT + ((n + 2 * i) % NST) * S::TILE);
+#pragma unroll
+                for (int ks = 0; ks < D / 16; ++ks)
+                    tc_mma(tmem + s * 128, q + (((ks >> 2) * (128 * 128) + (ks & 3) * 32) >> 4),
+                           k + (((ks >> 2) * (KEYS * 128) + (ks & 3) * 32) >> 4), QK, ks > 0);
+                tc_commit(&ctl->s_full[s]);
+            }
+            __syncwarp();
+        };
+        auto outputs = [&](int s, int i, bool done) {
+            if (!tiles_wait(ctl, &ctl->p_full[s], weights[s]++ & 1, err)) return false;
+            const int o = PAIR ? s : 0;
+            if (lane == 0) {
+                tc_fence_after();
+                fence_async_shared();
+                const uint64_t v = desc_n_major(base + S::K_AT + ((n + 2 * i + 1) % NST) * S::TILE, KEYS * 128);
+#pragma unroll
+                for (int ks = 0; ks < KEYS / 16; ++ks)
+                    tc_mma_ta(tmem + 256 + o * 128, tmem + s * 128 + 16 * ks / S::MINE * S::MINE + 16 * ks % S::MINE / 2,
+                              v + ks * (2048 >> 4), PV, begun[o] || ks > 0);
+                if (done) tc_commit(&ctl->o_done[s]);
+            }
+            begun[o] = true;
+            __syncwarp();
+            return true;
+        };
+        if constexpr (PAIR) {
+            for (int i = 0; ok && i < tiles; ++i) {
+#pragma unroll
+                for (int s = 0; s < 2; ++s) {
+                    const bool here = t0 + i >= c.s.lo[s] && t0 + i < c.s.hi[s];
+                    if (pending[s]) ok = ok && waits(n + 2 * i - 1) && outputs(s, i - 1, !here);
+                    if (s == 1 && i > 0 && ok) {
+                        ok = waits(n + 2 * i - 1);
+                        release(n + 2 * i - 1);
+                    }
+                    ok = ok && waits(n + 2 * i);
+                    if (here && ok) scores(s, i);
+                    pending[s] = here;
+                }
+                if (ok) release(n + 2 * i);
+            }
+            if (ok && lane == 0) tc_commit(&ctl->q_empty[place]);
+            __syncwarp();
+#pragma unroll
+            for (int s = 0; s < 2; ++s)
+                if (pending[s]) ok = ok && waits(n + 2 * tiles - 1) && outputs(s, tiles - 1, true);
+            ok = ok && waits(n + 2 * tiles - 1);
+            if (ok) release(n + 2 * tiles - 1);
+        } else {
+            // the places of scores go on in turn from item to item
+            for (int i = 0; ok && i < tiles + 2; ++i) {
+                const int s = (n / 2 + i) & 1;
+                if (i >= 2) {
+                    ok = waits(n + 2 * i - 3) && outputs(s, i - 2, true);
+                    if (ok) release(n + 2 * i - 3);
+                }
+                if (i < tiles) {
+                    ok = ok && waits(n + 2 * i);
+                    if (ok) {
+                        scores(s, i);
+                        release(n + 2 * i);
+                    }
+                }
+                if (i == tiles - 1 && ok && lane == 0) tc_commit(&ctl->q_empty[place]);
+                __syncwarp();
+            }
+        }
+        n += 2 * tiles;
+        ++item;
+    }
+}
+
+// ------------------------------------------------------------------ q
+// Three warps, an item ahead of the others where there is room: q, and of trees
+// what the new tokens see.
+template <typename C, int D, bool PAIR, typename S = TilesShape<C, D, PAIR>>
+__device__ void tiles_prepare(const TilesParams &p, TileCursor c, char *smem, TilesCtl<S> *ctl, unsigned *err, int lt)
+{
+    const int lane = lt & 31;
+    const uint32_t base = smem_u32(smem);
+    int item = 0;
+    for (; c.at < c.end; tiles_next<S>(c, p, lane)) {
+        if (tiles_first(c) == tiles_last(c)) continue;
+        if (item == p.give_up.item && static_cast<int>(blockIdx.x) == p.give_up.block) {  // the self-test
+            *reinterpret_cast<volatile int *>(&ctl->dead) = 1;
+            atomicExch(err, static_cast<unsigned>(STATUS_TIMEOUT));
+            return;
+        }
+        const int place = item % S::Q_PLACES, row0 = c.row_tile * S::ROWS, live = min(S::ROWS, p.rows - row0);
+        if (item >= S::Q_PLACES && !tiles_wait(ctl, &ctl->q_empty[place], (item / S::Q_PLACES - 1) & 1, err)) return;
+        if constexpr (!PAIR) {
+            if (p.parent && p.sc.slopes)
+                for (int t = lt; t < c.s.fresh; t += TILES_PREPARE)
+                    ctl->at.depth[place][t] =
+                        static_cast<signed char>(token_view(p.sc, p.parent + static_cast<int64_t>(c.b) * p.w.T, c.s, c.b, p.w.T, t).depth);
+        }
+        constexpr int CH = D / 8, STEP = TILES_PREPARE / CH;
+        const int ch = lt % CH, first = lt / CH;
+        auto source = [&](int r) {  // null: a row of zeros
+            const int t = (row0 + r) / p.group, g = (row0 + r) - t * p.group;
+            return r < live && t < c.s.fresh ? static_cast<const char *>(p.q) +
+                                                   (((static_cast<int64_t>(c.b) * p.w.T + t) * p.q_heads + c.h * p.group + g) * D + ch * 8) * 2
+                                             : nullptr;
+        };
+        if constexpr (!S::WIDEN) {
+            const uint32_t to = base + place * S::Q;
+#pragma unroll 4
+            for (int r = first; r < S::ROWS; r += STEP) {
+                const char *from = source(r);
+                cp_async16_zfill(to + (r >> 7) * S::Q_SUB + tile_at<128>(r & 127, ch), from ? from : static_cast<const char *>(p.q), from ? 16 : 0);
+            }
+            asm volatile("cp.async.wait_all;" ::: "memory");
+        } else {
+            char *to = smem + place * S::Q;
+#pragma unroll 1
+            for (int r0 = 0; r0 < S::ROWS; r0 += 4 * STEP) {
+                uint4 in[4];
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const char *from = source(r0 + i * STEP + first);
+                    in[i] = from ? *reinterpret_cast<const uint4 *>(from) : make_uint4(0, 0, 0, 0);
+                }
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const int r = r0 + i * STEP + first;
+                    float x[8], top = 0.0f;
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) {
+                        x[e] = p.q_bf16 ? Num<__nv_bfloat16>::up(reinterpret_cast<const __nv_bfloat16 *>(&in[i])[e])
+                                        : Num<__half>::up(reinterpret_cast<const __half *>(&in[i])[e]);
+                        top = fabsf(x[e]) < CUDART_INF_F ? fmaxf(top, fabsf(x[e])) : top;
+                    }
+#pragma unroll
+                    for (int o = CH / 2; o; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+                    const int e2 = top > 0.0f ? max(-120, min(120, 14 - ilogbf(top))) : 0;  // the largest below 2^15
+                    const float up = exp2f(static_cast<float>(e2));
+                    if (r < S::ROWS) {
+                        if (ch == 0) ctl->at.q_power[place * S::ROWS + r] = static_cast<signed char>(e2);
+                        *reinterpret_cast<uint4 *>(to + (r >> 7) * S::Q_SUB + tile_at<128>(r & 127, ch)) =
+                            make_uint4(pack_mma<__half>(x[0] * up, x[1] * up), pack_mma<__half>(x[2] * up, x[3] * up),
+                                       pack_mma<__half>(x[4] * up, x[5] * up), pack_mma<__half>(x[6] * up, x[7] * up));
+                    }
+                }
+            }
+        }
+        fence_async_shared();
+        mbar_arrive(&ctl->q_full[place]);
+        ++item;
+    }
+}
+
+// ------------------------------------------------------------------ rows
+// All threads that have rows of the same tile of rows.
+template <int N> __device__ __forceinline__ void group_sync(int group) { asm volatile("bar.sync %0, %1;" ::"r"(1 + group), "n"(N) : "memory"); }
+// The 128 threads that have the same keys of a tile.
+template <bool PAIR> __device__ __forceinline__ void quad_sync(int quad) { asm volatile("bar.sync %0, 128;" ::"r"((PAIR ? 1 : 7) + quad) : "memory"); }
+// The two warps that share rows.
+__device__ __forceinline__ void halves_sync(int w) { asm volatile("bar.sync %0, 64;" ::"r"(3 + w) : "memory"); }
+
+__device__ __forceinline__ void store_32bytes(void *at, const uint32_t (&y)[8])
+{
+    if ((reinterpret_cast<uintptr_t>(at) & 31) == 0) {
+        asm volatile("st.global.v8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"l"(at), "r"(y[0]), "r"(y[1]), "r"(y[2]), "r"(y[3]),
+                     "r"(y[4]), "r"(y[5]), "r"(y[6]), "r"(y[7])
+                     : "memory");
+    } else {
+        reinterpret_cast<uint4 *>(at)[0] = make_uint4(y[0], y[1], y[2], y[3]);
+        reinterpret_cast<uint4 *>(at)[1] = make_uint4(y[4], y[5], y[6], y[7]);
+    }
+}
+
+// Rows [r_from, r_from + r_count) of the cursor's item (or of the block's piece
+// of it) whose result is not finite, again: a warp a row, key by key over what
+// the row sees, in 32 bits.  Rows whose scores are NaN, or that have a bad page,
+// stay as they are.
+template <typename C, int D, bool PAIR>
+__device__ void tiles_again(const TilesParams &p, const TileCursor &c, long long begin, int r_from, int r_count, int warp, int warps, int lane)
+{
+    using S = TilesShape<C, D, PAIR>;
+    constexpr int PER = D / 32;  // columns of a lane, next to one another
+    const int row0 = c.row_tile * S::ROWS, live = min(S::ROWS, p.rows - row0), t0 = tiles_first(c), t1 = tiles_last(c);
+    if (t0 == t1) return;
+    const bool whole = item_whole(c);
+    float *part = p.parts + (static_cast<int64_t>(blockIdx.x) * 2 + (c.first < begin ? 0 : 1)) * (S::ROWS * (D + 2));
+    const int32_t *table = p.c.table + static_cast<int64_t>(c.b) * p.c.max_pages;
+    const float factor = p.scale_log2 * (p.c.k_scale ? __ldg(p.c.k_scale + c.h) : 1.0f);
+    const int32_t *pos = p.sc.slot_pos ? p.sc.slot_pos + (static_cast<int64_t>(c.b) * p.c.kv_heads + c.h) * p.sc.pos_stride : nullptr;
+    auto up = [&](const void *x, int64_t i) {
+        return p.q_bf16 ? Num<__nv_bfloat16>::up(static_cast<const __nv_bfloat16 *>(x)[i]) : Num<__half>::up(static_cast<const __half *>(x)[i]);
+    };
+#pragma unroll 1
+    for (int r = r_from + warp; r < min(r_from + r_count, live); r += warps) {
+        const int t = (row0 + r) / p.group, g = row0 + r - t * p.group;
+        if (t >= c.s.fresh) continue;
+        const int64_t at = ((static_cast<int64_t>(c.b) * p.w.T + t) * p.q_heads + c.h * p.group + g) * D + PER * lane;
+        float *piece = part + 2 * S::ROWS + r * D + PER * lane;
+        bool redo = false;
+#pragma unroll
+        for (int e = 0; e < PER; ++e) {
+            const float y = whole ? up(p.out, at + e) : piece[e];
+            redo |= !(fabsf(y) < CUDART_INF_F);
+        }
+        if (!__any_sync(0xffffffffu, redo)) continue;
+        Interval see = token_interval(p, c.s, c.b, t);
+        TokenView view{};
+        if (p.parent) {
+            view = token_view(p.sc, p.parent + static_cast<int64_t>(c.b) * p.w.T, c.s, c.b, p.w.T, t);
+            see.lo = view.bits ? view.lo : c.s.total;
+            see.hi = c.s.total;
+        }
+        const int own = pos ? __ldg(pos + c.s.ctx + t) : c.s.ctx + (p.parent ? view.depth : t);
+        const float slope = p.sc.slopes ? __ldg(p.sc.slopes + c.h * p.group + g) * LOG2E : 0.0f;
+        float m = -CUDART_INF_F, l = 0.0f, q[PER], x[PER];
+#pragma unroll
+        for (int e = 0; e < PER; ++e) {
+            q[e] = up(p.q, at + e);
+            x[e] = 0.0f;
+        }
+        bool fine = true;
+#pragma unroll 1
+        for (int j = max(see.lo, t0 * S::KEYS); fine && j < min(see.hi, t1 * S::KEYS); ++j) {
+            if (p.parent && j >= c.s.ctx && !(view.bits >> (j - c.s.ctx) & 1)) continue;
+            int there = pos ? __ldg(pos + j) : j;
+            if (!pos && p.parent && j >= c.s.ctx && p.sc.slopes)
+                there = c.s.ctx + token_view(p.sc, p.parent + static_cast<int64_t>(c.b) * p.w.T, c.s, c.b, p.w.T, j - c.s.ctx).depth;
+            if (pos && p.sc.window > 0 && own - there >= p.sc.window) continue;
+            const int page = page_of(p.c, table, j);
+            fine = page >= 0;
+            if (!fine) continue;
+            const C *k = reinterpret_cast<const C *>(row_ptr(p.c, p.c.k, page, j, c.h)) + PER * lane;
+            const C *v = reinterpret_cast<const C *>(row_ptr(p.c, p.c.v, page, j, c.h)) + PER * lane;
+            float s = 0.0f;
+#pragma unroll
+            for (int e = 0; e < PER; ++e) s += q[e] * Num<C>::up(k[e]);
+#pragma unroll
+            for (int o = 16; o; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
+            s *= factor;
+            fine = s == s;
+            if (p.sc.cap2 != 0.0f) {
+                float y[1] = {s};
+                cap_all(p.sc, y);
+                s = y[0];
+            }
+            if (p.sc.slopes) s = fmaf(-slope, fabsf(static_cast<float>(own - there)), s);
+            if (!fine || s == -CUDART_INF_F) continue;
+            if (s > m) {
+                const float a = fast_exp2(m - s);
+                m = s;
+                l *= a;
+#pragma unroll
+                for (int e = 0; e < PER; ++e) x[e] *= a;
+            }
+            const float w = fast_exp2(s - m);
+            l += w;
+#pragma unroll
+            for (int e = 0; e < PER; ++e) x[e] += w * Num<C>::up(v[e]);
+        }
+        if (!fine || l == 0.0f) continue;
+        const float unit = whole ? (p.c.v_scale ? __ldg(p.c.v_scale + c.h) : 1.0f) / l : fast_exp2(m - part[r]);
+#pragma unroll
+        for (int e = 0; e < PER; ++e) {
+            if (!whole)
+                piece[e] = x[e] * unit;
+            else if (p.q_bf16)
+                static_cast<__nv_bfloat16 *>(p.out)[at + e] = __float2bfloat16_rn(x[e] * unit);
+            else
+                static_cast<__half *>(p.out)[at + e] = __float2half_rn(x[e] * unit);
+        }
+    }
+}
+
+// NaN for these rows of the cursor's item, after a wait gave up.  Items without
+// keys have what they always have.
+template <int D, typename S> __device__ void tiles_lost(const TilesParams &p, const TileCursor &c, long long begin, int r_from, int r_count, int tid, int threads)
+{
+    const AttRows rows{c.b, c.h, c.row_tile * S::ROWS, min(S::ROWS, p.rows - c.row_tile * S::ROWS)};
+    const int to = min(r_from + r_count, rows.live);
+    const bool empty = c.s.to == 0 && !c.s.bad;
+    if (item_whole(c)) {
+        const float m = empty ? -CUDART_INF_F : CUDART_NAN_F;
+        for (int i = r_from * (D / 4) + tid; i < to * (D / 4); i += threads) {
+            const float4 zero = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+            if (p.q_bf16)
+                write_row<__nv_bfloat16, D>(p, rows, i / (D / 4), i % (D / 4) * 4, zero, m, 0.0f, 1.0f);
+            else
+                write_row<__half, D>(p, rows, i / (D / 4), i % (D / 4) * 4, zero, m, 0.0f, 1.0f);
+        }
+    } else {  // a piece: its maximum is enough
+        float *part = p.parts + (static_cast<int64_t>(blockIdx.x) * 2 + (c.first < begin ? 0 : 1)) * (S::ROWS * (D + 2));
+        for (int r = r_from + tid; r < to; r += threads) {
+            part[r] = CUDART_NAN_F;
+            part[S::ROWS + r] = 0.0f;
+        }
+        if (r_from == 0) note_split(p, c, rows, begin, tid);
+    }
+    if (!empty && !c.s.bad && tid == 0 && p.timeouts) p.timeouts[c.b] = STATUS_TIMEOUT;
+}
+
+// What is left to do for a group's rows at the end of its range, out of line:
+// rows that were not finite, of the items before tile `done`, and NaN from there
+// on where a wait gave up.
+template <typename C, int D, bool PAIR>
+__device__ __noinline__ void tiles_finish(const TilesParams &p, TilesCtl<TilesShape<C, D, PAIR>> *ctl, long long done, int group, int tid)
+{
+    using S = TilesShape<C, D, PAIR>;
+    const int lane = tid & 31;
+    TileCursor c = ctl->start;
+    const long long begin = c.at;
+    c.s = item_tiles<S>(p, tiles_lens(p, c.b), c.b, c.row_tile, lane);
+    const int r_from = 128 * group, r_count = PAIR ? 128 : S::ROWS;
+    for (; c.at < done; tiles_next<S>(c, p, lane))
+        if (ctl->lost[group]) tiles_again<C, D, PAIR>(p, c, begin, r_from, r_count, tid >> 5, S::GROUP / 32, lane);
+    for (; c.at < c.end; tiles_next<S>(c, p, lane)) tiles_lost<D, S>(p, c, begin, r_from, r_count, tid, S::GROUP);
+}
+
+// A row a thread (PAIR), or half of its keys.  tid: 0 .. 255.
+template <typename C, int D, bool PAIR, typename S = TilesShape<C, D, PAIR>>
+__device__ void tiles_rows(const TilesParams &p, TileCursor c, char *smem, TilesCtl<S> *ctl, unsigned *err, int tid)
+{
+    using M = typename MmaOf<C, C>::type;  // e4m3: f16
+    constexpr float UP = Weights<M>::UP;
+    constexpr int KEYS = S::KEYS, MINE = S::MINE, GROUP = S::GROUP, PART = S::ROWS * (D + 2), HALVES = PAIR ? 1 : 2;
+    const int lane = tid & 31, half = PAIR ? 0 : tid >> 7, group = PAIR ? tid >> 7 : 0, lane_row = tid & 127;
+    const int r = 128 * group + lane_row, group_tid = tid - 128 * group;  // row of the item; place in the group
+    const uint32_t quarter = static_cast<uint32_t>(lane_row & ~31) << 16;
+    const uint32_t tm_o = ctl->tmem + quarter + 256 + group * 128;
+    const long long begin = c.at;
+    const ScoresView &v = p.sc;
+    const bool moved = moved_slots(v);
+    int n = 0, item = 0, outs = 0;  // tiles of this group; items with tiles; items with outputs of this group (PAIR)
+    for (; c.at < c.end; tiles_next<S>(c, p, lane)) {
+        const int t0 = tiles_first(c), t1 = tiles_last(c), row0 = c.row_tile * S::ROWS, live = min(S::ROWS, p.rows - row0);
+        const int s0 = PAIR ? max(t0, c.s.lo[group]) : t0, s1 = max(s0, PAIR ? min(t1, c.s.hi[group]) : t1);
+        const AttRows rows{c.b, c.h, row0, live};
+        const float v_scale = p.c.v_scale ? __ldg(p.c.v_scale + c.h) : 1.0f;
+        const bool mine = r < live;
+        const int token = (row0 + r) / p.group;
+        const int64_t row_at = (static_cast<int64_t>(c.b) * p.w.T + token) * p.q_heads + c.h * p.group + (row0 + r) - token * p.group;
+        float m = -CUDART_INF_F, l = 0.0f;  // a maximum so far less UP: what l and O are sums against
+        bool any_bad = c.s.bad, ok = true;
+        const int place = item % S::Q_PLACES;
+        if (t0 < t1) {
+            const bool there = mine && token < c.s.fresh;
+            Interval see{0, 0};
+            unsigned long long bits = 0;
+            int own = 0;
+            const int32_t *pos = v.slot_pos ? v.slot_pos + (static_cast<int64_t>(c.b) * p.c.kv_heads + c.h) * v.pos_stride : nullptr;
+            if (there && !p.parent) {
+                see = token_interval(p, c.s, c.b, token);
+                own = moved ? __ldg(pos + c.s.ctx + token) : c.s.ctx + token;
+            }
+            if constexpr (!PAIR) {
+                if (there && p.parent) {
+                    const TokenView view = token_view(v, p.parent + static_cast<int64_t>(c.b) * p.w.T, c.s, c.b, p.w.T, token);
+                    bits = view.bits;
+                    own = moved ? __ldg(pos + c.s.ctx + token) : c.s.ctx + view.depth;
+                    see.hi = bits ? c.s.ctx : 0;
+                    see.lo = view.lo;
+                }
+            }
+            const float slope = there && v.slopes ? __ldg(v.slopes + c.h * p.group + (row0 + r) - token * p.group) * LOG2E : 0.0f;
+            float factor = p.scale_log2 * (p.c.k_scale ? __ldg(p.c.k_scale + c.h) : 1.0f);
+            ok = tiles_wait(ctl, &ctl->q_full[place], (item / S::Q_PLACES) & 1, err);
+            if (S::WIDEN) factor *= exp2f(-static_cast<float>(ctl->at.q_power[place * S::ROWS + r]));
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&ctl->q_empty[place]);
+            const bool shaped = v.cap2 != 0.0f || v.slopes || moved || !(factor > 0.0f);
+            const bool works = __any_sync(0xffffffffu, there);
+#pragma unroll 1
+            for (int tile = s0; tile < s1; ++tile, ++n) {  // to its end even after a wait gave up: the halves meet at each tile
+                const int buf = PAIR ? group : n & 1;
+                const uint32_t tm_s = ctl->tmem + quarter + buf * 128 + half * MINE;
+                const int jb = tile * KEYS + half * MINE;
+                if (moved) {  // positions of these keys, by the 128 threads that have them
+                    const int j = jb + lane_row, at = lane_row < MINE && j < c.s.total ? __ldg(pos + j) : 0;
+                    quad_sync<PAIR>(tid >> 7);  // the last tile's have been read
+                    if (lane_row < MINE) ctl->positions[tid >> 7][lane_row] = at;
+                    quad_sync<PAIR>(tid >> 7);
+                }
+                ok = ok && tiles_wait(ctl, &ctl->s_full[buf], (PAIR ? n : n >> 1) & 1, err);
+                tc_fence_after();
+                __syncwarp();
+                if (works) {
+                    float x[MINE];
+                    {
+#pragma unroll
+                        for (int i = 0; i < MINE; i += 32) {
+                            uint32_t y[32];
+                            tc_ld32(y, tm_s + i);
+#pragma unroll
+                            for (int k = 0; k < 32; ++k) x[i + k] = __uint_as_float(y[k]);
+                        }
+                    }
+                    float f = factor;
+                    if (shaped) {
+                        f = 1.0f;
+#pragma unroll
+                        for (int i = 0; i < MINE; ++i) x[i] *= factor;
+                        if (v.cap2 != 0.0f) cap_all(v, x);
+                        if (moved) {
+#pragma unroll
+                            for (int i = 0; i < MINE; ++i) {
+                                const int far = own - ctl->positions[tid >> 7][i];
+                                x[i] = fmaf(-slope, fabsf(static_cast<float>(far)), x[i]);
+                                if (v.window > 0 && far >= v.window) x[i] = -CUDART_INF_F;
+                            }
+                        } else if (v.slopes) {
+                            if (!PAIR && p.parent && jb + MINE > c.s.ctx) {  // a node's position is its depth's
+#pragma unroll
+                                for (int i = 0; i < MINE; ++i) {
+                                    const int j = jb + i, there = j >= c.s.ctx && j < c.s.total ? c.s.ctx + ctl->at.depth[place][j - c.s.ctx] : j;
+                                    x[i] = fmaf(-slope, fabsf(static_cast<float>(own - there)), x[i]);
+                                }
+                            } else {
+                                const float far = static_cast<float>(own - jb);
+#pragma unroll
+                                for (int i = 0; i < MINE; ++i) x[i] = fmaf(-slope, fabsf(far - static_cast<float>(i)), x[i]);
+                            }
+                        }
+                    }
+                    const bool seen = see.lo <= jb && see.hi >= jb + MINE;
+                    if (!__all_sync(0xffffffffu, seen)) {
+#pragma unroll
+                        for (int i = 0; i < MINE; i += 32) {
+                            const int lo = min(max(see.lo - jb - i, 0), 32), hi = min(max(see.hi - jb - i, 0), 32);
+                            unsigned mask = hi == 32 ? 0xffffffffu : (1u << hi) - 1u;
+                            if (!PAIR && p.parent) {
+                                const int o = c.s.ctx - (jb + i);  // the first new token's column, from here
+                                if (o < 32 && o > -64) mask |= static_cast<unsigned>(o >= 0 ? bits << o : bits >> -o);
+                            }
+                            mask = lo == 32 ? 0u : mask & ~((1u << lo) - 1u);
+#pragma unroll
+                            for (int k = 0; k < 32; ++k) x[i + k] = mask >> k & 1 ? x[i + k] : -CUDART_INF_F;
+                        }
+                    }
+                    float top = x[0];
+#pragma unroll
+                    for (int i = 1; i + 1 < MINE; i += 2) top = fmax3(top, x[i], x[i + 1]);
+                    top = fmaxf(top, x[MINE - 1]) * f;
+                    if (HALVES == 2) {  // the maximum of both halves, by the two warps that have these rows
+                        halves_sync(lane_row / 32);  // the last tile's has been read
+                        ctl->at.top[tid] = top;
+                        halves_sync(lane_row / 32);
+                        top = fmaxf(top, ctl->at.top[tid ^ 128]);
+                        if (n >= 2) ok = ok && tiles_wait(ctl, &ctl->o_done[buf], ((n - 2) >> 1) & 1, err);
+                    }
+                    if (tile == s0) {
+                        m = top - UP;
+                    } else if (__any_sync(0xffffffffu, top - m > UP + Weights<M>::LAG)) {  // as a difference: a sum may round up to a score 16 above
+                        const float grown = fmaxf(m, top - UP), a = grown == -CUDART_INF_F ? 0.0f : fast_exp2(m - grown);
+                        m = grown;
+                        l *= a;
+                        // PAIR: the scores were issued behind the outputs before them and are there
+                        if (HALVES == 2) ok = ok && tiles_wait(ctl, &ctl->o_done[(n - 1) & 1], ((n - 1) >> 1) & 1, err);
+                        tc_fence_after();
+#pragma unroll 1
+                        for (int i = half * (D / HALVES); i < (half + 1) * (D / HALVES); i += 16) {
+                            uint32_t y[16];
+                            tc_ld16(y, tm_o + i);
+#pragma unroll
+                            for (int k = 0; k < 16; ++k) y[k] = __float_as_uint(__uint_as_float(y[k]) * a);
+                            tc_st16(tm_o + i, y);
+                        }
+                    }
+                    const float base = m == -CUDART_INF_F ? 0.0f : m;
+                    if (f != 1.0f && __any_sync(0xffffffffu, fabsf(base) > 0x1p20f)) {
+                        // the product is rounded as m was, not fused with the difference: of scores this large the largest
+                        // would else miss m by more than a weight can hold
+#pragma unroll
+                        for (int i = 0; i < MINE; ++i) x[i] = __fmul_rn(x[i], f);
+                        f = 1.0f;
+                    }
+                    float sum0 = 0.0f, sum1 = 0.0f;
+                    constexpr int AT_ONCE = MINE < 64 ? MINE : 64;
+#pragma unroll
+                    for (int i0 = 0; i0 < MINE; i0 += AT_ONCE) {
+                        uint32_t pk[AT_ONCE / 2];
+#pragma unroll
+                        for (int i = 0; i < AT_ONCE; i += 2) {
+                            const float a = fast_exp2(fmaf(x[i0 + i], f, -base)), b = fast_exp2(fmaf(x[i0 + i + 1], f, -base));
+                            sum0 += a;
+                            sum1 += b;
+                            // rounded to 16 bits for the product (half a step of the type each); l keeps 32 bits
+                            pk[i / 2] = pack_mma<M>(a, b);
+                        }
+                        if constexpr (AT_ONCE == 64)
+                            tc_st32(tm_s + i0 / 2, pk);
+                        else
+                            tc_st16(tm_s + i0 / 2, pk);
+                    }
+                    l += sum0 + sum1;
+                    tc_wait_st();
+                }
+                tc_fence_before();
+                mbar_arrive(&ctl->p_full[buf]);
+            }
+            if (PAIR) {
+                if (s0 < s1) {
+                    ok = ok && tiles_wait(ctl, &ctl->o_done[group], outs & 1, err);
+                    ++outs;
+                }
+            } else {
+                ok = ok && tiles_wait(ctl, &ctl->o_done[(n - 1) & 1], ((n - 1) >> 1) & 1, err);
+            }
+            tc_fence_after();
+            any_bad |= *reinterpret_cast<volatile int *>(&ctl->bad[group][item % TILES_ITEMS]) != 0;
+            ++item;
+        }
+        const bool tiles = s0 < s1;
+        group_sync<GROUP>(group);  // all have read the item's flag, and the last tile's maxima
+        if (group_tid == 0) {
+            ctl->stop[group] = *reinterpret_cast<volatile int *>(&ctl->dead);
+            if (t0 < t1) ctl->bad[group][(item - 1) % TILES_ITEMS] = 0;
+        }
+        if (HALVES == 2) ctl->at.top[tid] = l;
+        group_sync<GROUP>(group);
+        if (*reinterpret_cast<volatile int *>(&ctl->stop[group])) break;  // a wait gave up: this item is among what is lost
+        if (HALVES == 2) l += ctl->at.top[tid ^ 128];
+        const bool whole = item_whole(c);
+        float *part = p.parts + (static_cast<int64_t>(blockIdx.x) * 2 + (c.first < begin ? 0 : 1)) * PART;
+        const bool none = m == -CUDART_INF_F && l == 0.0f, fixed = none || any_bad;
+        const float instead = any_bad ? CUDART_NAN_F : 0.0f, out_scale = v_scale / l;
+        if (half == 0 && mine) {
+            if (!whole) {
+                part[r] = any_bad ? CUDART_NAN_F : m;
+                part[S::ROWS + r] = l;
+            } else if (p.lse) {
+                p.lse[row_at] = any_bad ? CUDART_NAN_F : none ? -CUDART_INF_F : LN2 * (m + log2f(l));
+            }
+        }
+        bool odd = false;
+#pragma unroll 1
+        for (int d0 = half * (D / HALVES); d0 < (half + 1) * (D / HALVES); d0 += 32) {
+            float x[32];
+            __syncwarp();
+            if (tiles) {
+                uint32_t y[32];
+                tc_ld32(y, tm_o + d0);
+#pragma unroll
+                for (int k = 0; k < 32; ++k) x[k] = __uint_as_float(y[k]);
+            } else {
+#pragma unroll
+                for (int k = 0; k < 32; ++k) x[k] = 0.0f;
+            }
+            if (!mine) continue;
+            // 32 bytes a store: a thread's row is its own, and half a sector at a time costs twice the transactions
+            if (!whole) {
+#pragma unroll
+                for (int k = 0; k < 32; ++k) {
+                    x[k] = fixed ? 0.0f : x[k];
+                    odd |= !(fabsf(x[k]) < CUDART_INF_F);
+                }
+#pragma unroll
+                for (int k = 0; k < 32; k += 8) {
+                    uint32_t y[8];
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) y[e] = __float_as_uint(x[k + e]);
+                    store_32bytes(part + 2 * S::ROWS + r * D + d0 + k, y);
+                }
+            } else {
+#pragma unroll
+                for (int k = 0; k < 32; ++k) {
+                    x[k] = fixed ? instead : x[k] * out_scale;
+                    odd |= !(fabsf(x[k]) < CUDART_INF_F);
+                }
+#pragma unroll
+                for (int k = 0; k < 32; k += 16) {
+                    uint32_t y[8];
+#pragma unroll
+                    for (int e = 0; e < 8; ++e)
+                        y[e] = S::WIDEN && p.q_bf16 ? pack_mma<__nv_bfloat16>(x[k + 2 * e], x[k + 2 * e + 1])
+                                                    : pack_mma<M>(x[k + 2 * e], x[k + 2 * e + 1]);
+                    store_32bytes(static_cast<char *>(p.out) + (row_at * D + d0 + k) * 2, y);
+                }
+            }
+        }
+        tc_fence_before();
+        if (odd && !any_bad) *reinterpret_cast<volatile int *>(&ctl->lost[group]) = 1;
+        if (!whole && group == 0) note_split(p, c, rows, begin, tid);
+        group_sync<GROUP>(group);  // sums and flags have been read
+    }
+    // c.at before the end: a wait gave up
+    if (*reinterpret_cast<volatile int *>(&ctl->lost[group]) || c.at < c.end) tiles_finish<C, D, PAIR>(p, ctl, c.at, group, group_tid);
+}
+
+template <typename C, int D, bool PAIR>
+__global__ void __launch_bounds__(TILES_THREADS, 1)
+    tiles_kernel(const TilesParams p, const __grid_constant__ CUtensorMap map_k, const __grid_constant__ CUtensorMap map_v, const int maps)
+{
+    using S = TilesShape<C, D, PAIR>;
+    using Ctl = TilesCtl<S>;
+    extern __shared__ __align__(1024) char smem[];  // the swizzle's rows of 128 bytes come in groups of eight
+    Ctl *ctl = reinterpret_cast<Ctl *>(smem + S::CTL_AT);
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    unsigned *err = p.error;
+    if (tid == 0) {
+        for (int i = 0; i < 10; ++i) {
+            mbar_init(&ctl->full[i], 128);
+            mbar_init(&ctl->empty[i], 1);
+        }
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(&ctl->s_full[i], 1);
+            mbar_init(&ctl->p_full[i], S::GROUP);
+            mbar_init(&ctl->o_done[i], 1);
+            mbar_init(&ctl->q_full[i], TILES_PREPARE);
+            mbar_init(&ctl->q_empty[i], 1 + 8);  // the products' end, and the row warps, who have read what lies beside q
+            ctl->stop[i] = ctl->lost[i] = 0;
+            for (int k = 0; k < TILES_ITEMS; ++k) ctl->bad[i][k] = 0;
+        }
+        mbar_init(&ctl->spare, 1);
+        ctl->dead = 0;
+        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    }
+    if (warp == 8) tmem_alloc(&ctl->tmem, 512);
+    chain_begin();
+    const TileCursor c = tiles_find<S>(p, ctl, tid);
+    if (tid < 2) p.split[blockIdx.x * 2 + tid].n = 0;
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    if (c.at == c.end) {  // the whole block
+        if (warp == 8) tmem_free(ctl->tmem, 512);
+        return;
+    }
+    // registers: launched with 128 a thread, 4 x 128 = 2 x 184 + 2 x 72 (a row's 128 scores) or 2 x 160 + 2 x 96
+    if (warp < 8) {
+        if (PAIR)
+            asm volatile("setmaxnreg.inc.sync.aligned.u32 184;");
+        else
+            asm volatile("setmaxnreg.inc.sync.aligned.u32 160;");
+        tiles_rows<C, D, PAIR>(p, c, smem, ctl, err, tid);
+    } else if (warp < 12) {
+        if (PAIR)
+            asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
+        else
+            asm volatile("setmaxnreg.dec.sync.aligned.u32 96;");
+        if (warp == 8) {
+            tiles_multiply<C, D, PAIR>(p, c, smem, ctl, err, lane);
+            if (lane == 0) {  // what was issued ends before the block may: others may have given up on it
+                tc_commit(&ctl->spare);
+                mbar_drain(&ctl->spare, 0);
+            }
+            __syncwarp();
+        } else {
+            tiles_prepare<C, D, PAIR>(p, c, smem, ctl, err, tid - 288);
+        }
+    } else {
+        if (PAIR)
+            asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
+        else
+            asm volatile("setmaxnreg.dec.sync.aligned.u32 96;");
+        tiles_load<C, D, PAIR>(p, c, smem, ctl, err, tid - 384, maps ? &map_k : nullptr, maps ? &map_v : nullptr);
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    if (warp == 8) tmem_free(ctl->tmem, 512);
+}
+
+template <typename C, int D, bool PAIR> cudaError_t launch_tiles_of(TilesParams p, const KvLaunch &L, cudaStream_t st)
+{
+    using S = TilesShape<C, D, PAIR>;
+    constexpr int SMEM = S::CTL_AT + static_cast<int>(sizeof(TilesCtl<S>));
+    static_assert(SMEM <= 232448, "shared memory of a block");
+    auto kernel = tiles_kernel<C, D, PAIR>;
+    cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, SMEM);
+    if (e != cudaSuccess) return e;
+    p.w.tile = S::KEYS;
+    p.w.row_tiles = (p.rows + S::ROWS - 1) / S::ROWS;
+    CUtensorMap map_k{}, map_v{};
+    const bool maps = pool_map(&map_k, L, false, S::KEYS) && pool_map(&map_v, L, true, S::KEYS);
+    e = launch_chained(kernel, dim3(ATT_SMS), TILES_THREADS, SMEM, st, p, map_k, map_v, static_cast<int>(maps));
+    return e != cudaSuccess ? e : launch_join(p, L.dtype, D, S::ROWS, ATT_SMS, st);
+}
+template <typename C> cudaError_t launch_tiles_types(const TilesParams &p, const KvLaunch &L, bool pairs, cudaStream_t st)
+{
+    switch (L.cache.head_dim) {
+    case 64: return pairs ? launch_tiles_of<C, 64, true>(p, L, st) : launch_tiles_of<C, 64, false>(p, L, st);
+    case 128: return pairs ? launch_tiles_of<C, 128, true>(p, L, st) : launch_tiles_of<C, 128, false>(p, L, st);
+    default: return launch_tiles_of<C, 256, false>(p, L, st);
+    }
+}
+
+}  // namespace spv

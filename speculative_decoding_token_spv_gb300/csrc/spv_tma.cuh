@@ -12,10 +12,10 @@
 namespace spv {
 
 // The map of a 16-bit pool: element, slot, head, page; a box is 64 elements
-// (the width of an operand's panel) of min(page_size, 128) slots.  False where
+// (the width of an operand's panel) of min(page_size, `slots`) slots.  False where
 // the pool cannot be described so (pages under 8 slots, a driver without the
 // call): the kernels then copy row by row.
-inline bool pool_map(CUtensorMap *map, const KvLaunch &L, bool v)
+inline bool pool_map(CUtensorMap *map, const KvLaunch &L, bool v, int slots = 128)
 {
     const spv_kv_cache &c = L.cache;
     if (c.dtype == SPV_E4M3 || c.page_size < 8 || c.head_dim % 64 != 0) return false;
@@ -42,7 +42,7 @@ inline bool pool_map(CUtensorMap *map, const KvLaunch &L, bool v)
         bytes[i] = static_cast<cuuint64_t>(strides[i] > 0 ? strides[i] : c.head_dim) * 2;
         if (bytes[i] >= (1ull << 40)) return false;
     }
-    const cuuint32_t box[4] = {64, static_cast<cuuint32_t>(c.page_size < 128 ? c.page_size : 128), 1, 1};
+    const cuuint32_t box[4] = {64, static_cast<cuuint32_t>(c.page_size < slots ? c.page_size : slots), 1, 1};
     const cuuint32_t steps[4] = {1, 1, 1, 1};
     return encode(map, c.dtype == SPV_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 4,
                   v ? c.v : c.k, sizes, bytes, box, steps, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,

@@ -1,5 +1,8 @@
 """The target model's attention layer around a verify step: binding of
-spv_rope_append, spv_paged_attention, spv_attention_mass and spv_kv_evict.
+spv_rope_append, spv_paged_attention, spv_attention_mass and spv_kv_evict, of
+their forms for models whose attention is not plain (spv_norm_rope_append,
+spv_paged_attention_scored, spv_attention_mass_scored), and of
+spv_prompt_attention.
 
 Like the verify calls: torch CUDA tensors in, work on torch's current stream
 (or ``stream``), outputs allocated when the caller passes none in ``out``, no
@@ -186,16 +189,9 @@ def spv_rope_frequencies(rotary_dim: int, base: float = 10000.0, *, scaling: str
     return host.to(device)
 
 
-def spv_rope_append(q, k, v, cache: KVCache, page_table, ctx_lens, freqs, *, interleaved: bool = False,
-                    mscale: float = 1.0, positions=None, new_lens=None, slot_pos=None, out=None,
-                    want_status: bool = True, stream=None) -> dict:
-    """Rotary positions for q [B, T, q_heads, D] and k [B, T, kv_heads, D], and
-    k, v into the cache's slots ctx_lens[b] + t (see spv_rope_append in spv.h).
-
-    q, k and v may be views of one projection's output: heads contiguous, any
-    batch and token strides.  freqs: :func:`spv_rope_frequencies` of the
-    rotary_dim.  Returns dict(q, and row_status when requested); out["q"] may
-    be q itself."""
+def _rope_args(q, k, v, cache, page_table, freqs, slot_pos):
+    """The checks that the two rotary calls share: (cache bytes, device, q's shape, dtype and its code, kv heads, packed
+    strides, pairs, table, pages, slots of slot_pos)."""
     pack, dev, (_, _, Hkv, D) = cache.packed()
     try:
         shape, dtype = q.shape, q.dtype
@@ -226,9 +222,25 @@ def spv_rope_append(q, k, v, cache: KVCache, page_table, ctx_lens, freqs, *, int
         if slot_pos.dim() != 3:
             raise ValueError("slot_pos must be [B, kv_heads, slots]")
         slots = slot_pos.shape[2]
+    return pack, dev, shape, dtype, code, Hkv, _PACK_STRIDES(sq[0], sq[1], sk[0], sk[1], sv[0], sv[1]), pairs, table, pages, slots
+
+
+def spv_rope_append(q, k, v, cache: KVCache, page_table, ctx_lens, freqs, *, interleaved: bool = False,
+                    mscale: float = 1.0, positions=None, new_lens=None, slot_pos=None, out=None,
+                    want_status: bool = True, stream=None) -> dict:
+    """Rotary positions for q [B, T, q_heads, D] and k [B, T, kv_heads, D], and
+    k, v into the cache's slots ctx_lens[b] + t (see spv_rope_append in spv.h).
+
+    q, k and v may be views of one projection's output: heads contiguous, any
+    batch and token strides.  freqs: :func:`spv_rope_frequencies` of the
+    rotary_dim.  Returns dict(q, and row_status when requested); out["q"] may
+    be q itself."""
+    pack, dev, shape, dtype, code, Hkv, strides, pairs, table, pages, slots = _rope_args(q, k, v, cache, page_table, freqs,
+                                                                                         slot_pos)
+    B, T, Hq, D = shape
     out = dict(out) if out else {}
     st = load_library().spv_rope_append(
-        q.data_ptr(), k.data_ptr(), v.data_ptr(), code, _PACK_STRIDES(sq[0], sq[1], sk[0], sk[1], sv[0], sv[1]), B, T, Hq,
+        q.data_ptr(), k.data_ptr(), v.data_ptr(), code, strides, B, T, Hq,
         _arg(freqs, "freqs", _I64, (pairs,), dev), 2 * pairs, int(bool(interleaved)), mscale,
         _opt(positions, "positions", _I32, (B, T), dev),
         _arg(ctx_lens, "ctx_lens", _I32, (B,), dev), _opt(new_lens, "new_lens", _I32, (B,), dev), table, pages, pack,
@@ -237,6 +249,71 @@ def spv_rope_append(q, k, v, cache: KVCache, page_table, ctx_lens, freqs, *, int
     if st:
         raise SpvError(st, "spv_rope_append")
     return out
+
+
+def spv_norm_rope_append(q, k, v, cache: KVCache, page_table, ctx_lens, freqs, *, q_weight=None, k_weight=None,
+                         eps: float = 1e-6, axes=None, interleaved: bool = False, mscale: float = 1.0, positions=None,
+                         new_lens=None, slot_pos=None, out=None, want_status: bool = True, stream=None) -> dict:
+    """:func:`spv_rope_append` of q and k whose heads are normed first, with
+    weights ``q_weight`` and ``k_weight`` [D] float32 (None: not normed), and of
+    positions with several axes (see spv_norm_rope_append in spv.h): ``axes``
+    [rotary_dim / 2] int32 names the axis of each pair and ``positions`` is [B,
+    T, axes]; without ``axes`` [B, T], or None for the slots."""
+    pack, dev, shape, dtype, code, Hkv, strides, pairs, table, pages, slots = _rope_args(q, k, v, cache, page_table, freqs,
+                                                                                         slot_pos)
+    B, T, Hq, D = shape
+    num_axes, where = 1, (B, T)
+    if axes is not None:
+        if not isinstance(positions, torch.Tensor) or positions.dim() != 3:
+            raise ValueError("axes need positions [B, T, axes]")
+        num_axes = positions.shape[2]
+        where = (B, T, num_axes)
+    out = dict(out) if out else {}
+    st = load_library().spv_norm_rope_append(
+        q.data_ptr(), k.data_ptr(), v.data_ptr(), code, strides, B, T, Hq, _opt(q_weight, "q_weight", _F32, (D,), dev),
+        _opt(k_weight, "k_weight", _F32, (D,), dev), eps, _arg(freqs, "freqs", _I64, (pairs,), dev),
+        _opt(axes, "axes", _I32, (pairs,), dev), num_axes, 2 * pairs, int(bool(interleaved)), mscale,
+        _opt(positions, "positions", _I32, where, dev), _arg(ctx_lens, "ctx_lens", _I32, (B,), dev),
+        _opt(new_lens, "new_lens", _I32, (B,), dev), table, pages, pack,
+        _opt(slot_pos, "slot_pos", _I32, (B, Hkv, slots), dev), slots, _output(out, "q", (B, T, Hq, D), dtype, dev, stream),
+        _output(out, "row_status", (B,), _I32, dev, stream) if want_status else None, _on_stream(stream, dev))
+    if st:
+        raise SpvError(st, "spv_norm_rope_append")
+    return out
+
+
+_PACK_SCORES = struct.Struct("@fPiPPPq").pack
+
+
+@dataclass
+class Scores:
+    """Scores and masks of attention that is not plain (spv_scores in spv.h):
+    ``cap`` tanh(s / cap); ``slopes`` [q_heads] float32 times the distance off
+    them; a ``window`` of positions; ``first`` [B, T] int32, the slot where a
+    token's document begins; ``last`` [B, T] int32, the slot where the prefix
+    ends that a token sees whole; ``slot_pos`` [B, kv_heads, slots] int32, the
+    positions of the slots where an eviction has moved them."""
+    cap: float = 0.0
+    slopes: torch.Tensor | None = None
+    window: int = 0
+    first: torch.Tensor | None = None
+    last: torch.Tensor | None = None
+    slot_pos: torch.Tensor | None = None
+
+    def packed(self, B, T, q_heads, kv_heads, dev):
+        """spv_scores as bytes, for calls of these sizes."""
+        slots, moved = 0, 0
+        if self.slot_pos is not None:
+            if not isinstance(self.slot_pos, torch.Tensor) or self.slot_pos.dim() != 3:
+                raise ValueError("slot_pos must be [B, kv_heads, slots]")
+            slots = self.slot_pos.shape[2]
+            moved = _arg(self.slot_pos, "slot_pos", _I32, (B, kv_heads, slots), dev)
+        try:
+            return _PACK_SCORES(self.cap, _opt(self.slopes, "slopes", _F32, (q_heads,), dev) or 0, self.window,
+                                _opt(self.first, "first", _I32, (B, T), dev) or 0,
+                                _opt(self.last, "last", _I32, (B, T), dev) or 0, moved, slots)
+        except struct.error:
+            raise ValueError("cap must be a number and window an integer of 32 bits") from None
 
 
 def spv_attention_workspace_bytes(B: int, T: int, q_heads: int, kv_heads: int, head_dim: int) -> int:
@@ -271,16 +348,63 @@ def spv_paged_attention(q, cache: KVCache, page_table, ctx_lens, *, new_lens=Non
     return out
 
 
-def spv_attention_mass(q, lse, cache: KVCache, page_table, ctx_lens, accept_count, *, nodes=None, new_lens=None,
-                       parent=None, scale=None, decay: float = 1.0, mass_in=None, out=None,
-                       want_status: bool = True, stream=None) -> dict:
-    """What each cached key received from the tokens that stand after the
-    verify step (see spv_attention_mass in spv.h): out["mass"] [B, kv_heads,
-    slots] float32 = decay * mass_in + the sum of the weights.  q, lse and the
-    other arguments as in the :func:`spv_paged_attention` call; accept_count
-    (and, for a tree, nodes: out_nodes) from the verify call.  Without
-    ``mass_in`` and ``out`` a zero-filled mass as wide as the page table is
-    made."""
+def spv_paged_attention_scored(q, cache: KVCache, page_table, ctx_lens, scores: Scores, *, new_lens=None, parent=None,
+                               scale=None, workspace=None, out=None, want_lse: bool = False, want_status: bool = True,
+                               stream=None) -> dict:
+    """:func:`spv_paged_attention` with the scores and masks of ``scores`` (see
+    spv_paged_attention_scored in spv.h)."""
+    pack, dev, (_, _, Hkv, D) = cache.packed()
+    shape, code, address = _queries(q, D, dev)
+    B, T, Hq, _ = shape
+    table, pages = _table(page_table, B, dev)
+    lib = load_library()
+    if workspace is None:
+        workspace = _made(stream, new_workspace, lib.spv_attention_workspace_bytes(B, T, Hq, Hkv, D), dev)
+    out = dict(out) if out else {}
+    st = lib.spv_paged_attention_scored(
+        address, code, B, T, Hq, pack, table, pages, _arg(ctx_lens, "ctx_lens", _I32, (B,), dev),
+        _opt(new_lens, "new_lens", _I32, (B,), dev), _opt(parent, "parent", _I32, (B, T), dev),
+        1.0 / math.sqrt(D) if scale is None else scale, scores.packed(B, T, Hq, Hkv, dev),
+        _output(out, "out", shape, q.dtype, dev, stream),
+        _output(out, "lse", (B, T, Hq), _F32, dev, stream) if want_lse else None,
+        _output(out, "row_status", (B,), _I32, dev, stream) if want_status else None,
+        _arg(workspace, "workspace", _U8, (workspace.numel(),), dev), workspace.numel(), _on_stream(stream, dev))
+    if st:
+        raise SpvError(st, "spv_paged_attention_scored")
+    return out
+
+
+def spv_prompt_workspace_bytes(B: int, T: int, q_heads: int, kv_heads: int, head_dim: int) -> int:
+    return load_library().spv_prompt_workspace_bytes(B, T, q_heads, kv_heads, head_dim)
+
+
+def spv_prompt_attention(q, cache: KVCache, page_table, ctx_lens, scores: Scores | None = None, *, new_lens=None, scale=None,
+                         workspace=None, out=None, want_lse: bool = False, want_status: bool = True, stream=None) -> dict:
+    """Attention of prompts: any number of new tokens q [B, T, q_heads, D] over
+    the paged cache that holds their keys and values, causal, with the scores
+    and masks of ``scores`` (see spv_prompt_attention in spv.h)."""
+    pack, dev, (_, _, Hkv, D) = cache.packed()
+    shape, code, address = _queries(q, D, dev)
+    B, T, Hq, _ = shape
+    table, pages = _table(page_table, B, dev)
+    lib = load_library()
+    if workspace is None:
+        workspace = _made(stream, new_workspace, lib.spv_prompt_workspace_bytes(B, T, Hq, Hkv, D), dev)
+    out = dict(out) if out else {}
+    st = lib.spv_prompt_attention(
+        address, code, B, T, Hq, pack, table, pages, _arg(ctx_lens, "ctx_lens", _I32, (B,), dev),
+        _opt(new_lens, "new_lens", _I32, (B,), dev), 1.0 / math.sqrt(D) if scale is None else scale,
+        None if scores is None else scores.packed(B, T, Hq, Hkv, dev), _output(out, "out", shape, q.dtype, dev, stream),
+        _output(out, "lse", (B, T, Hq), _F32, dev, stream) if want_lse else None,
+        _output(out, "row_status", (B,), _I32, dev, stream) if want_status else None,
+        _arg(workspace, "workspace", _U8, (workspace.numel(),), dev), workspace.numel(), _on_stream(stream, dev))
+    if st:
+        raise SpvError(st, "spv_prompt_attention")
+    return out
+
+
+def _mass(name, q, lse, cache, page_table, ctx_lens, accept_count, scores, nodes, new_lens, parent, scale, decay, mass_in, out,
+          want_status, stream):
     pack, dev, (_, page_size, Hkv, D) = cache.packed()
     shape, code, address = _queries(q, D, dev)
     B, T, Hq, _ = shape
@@ -293,16 +417,40 @@ def spv_attention_mass(q, lse, cache: KVCache, page_table, ctx_lens, accept_coun
     if mass.dim() != 3:
         raise ValueError("out['mass'] must be [B, kv_heads, slots]")
     full = (B, Hkv, mass.shape[2])
-    st = load_library().spv_attention_mass(
+    shaped = () if scores is None else (scores.packed(B, T, Hq, Hkv, dev),)
+    st = getattr(load_library(), name)(
         address, code, B, T, Hq, _arg(lse, "lse", _F32, (B, T, Hq), dev), pack, table, pages,
         _arg(ctx_lens, "ctx_lens", _I32, (B,), dev), _opt(new_lens, "new_lens", _I32, (B,), dev),
-        _opt(parent, "parent", _I32, (B, T), dev), 1.0 / math.sqrt(D) if scale is None else scale,
+        _opt(parent, "parent", _I32, (B, T), dev), 1.0 / math.sqrt(D) if scale is None else scale, *shaped,
         _arg(accept_count, "accept_count", _I32, (B,), dev), _opt(nodes, "nodes", _I32, (B, T), dev), decay,
         _opt(mass_in, "mass_in", _F32, full, dev), _arg(mass, "out['mass']", _F32, full, dev), full[2],
         _output(out, "row_status", (B,), _I32, dev, stream) if want_status else None, _on_stream(stream, dev))
     if st:
-        raise SpvError(st, "spv_attention_mass")
+        raise SpvError(st, name)
     return out
+
+
+def spv_attention_mass(q, lse, cache: KVCache, page_table, ctx_lens, accept_count, *, nodes=None, new_lens=None,
+                       parent=None, scale=None, decay: float = 1.0, mass_in=None, out=None,
+                       want_status: bool = True, stream=None) -> dict:
+    """What each cached key received from the tokens that stand after the
+    verify step (see spv_attention_mass in spv.h): out["mass"] [B, kv_heads,
+    slots] float32 = decay * mass_in + the sum of the weights.  q, lse and the
+    other arguments as in the :func:`spv_paged_attention` call; accept_count
+    (and, for a tree, nodes: out_nodes) from the verify call.  Without
+    ``mass_in`` and ``out`` a zero-filled mass as wide as the page table is
+    made."""
+    return _mass("spv_attention_mass", q, lse, cache, page_table, ctx_lens, accept_count, None, nodes, new_lens, parent,
+                 scale, decay, mass_in, out, want_status, stream)
+
+
+def spv_attention_mass_scored(q, lse, cache: KVCache, page_table, ctx_lens, accept_count, scores: Scores, *, nodes=None,
+                              new_lens=None, parent=None, scale=None, decay: float = 1.0, mass_in=None, out=None,
+                              want_status: bool = True, stream=None) -> dict:
+    """:func:`spv_attention_mass` after :func:`spv_paged_attention_scored`, with
+    the same ``scores`` (see spv_attention_mass_scored in spv.h)."""
+    return _mass("spv_attention_mass_scored", q, lse, cache, page_table, ctx_lens, accept_count, scores, nodes, new_lens, parent,
+                 scale, decay, mass_in, out, want_status, stream)
 
 
 def spv_kv_evict(cache: KVCache, page_table, lens, mass, budget: int, *, pos=None, sinks: int = 0, recent: int = 0,
