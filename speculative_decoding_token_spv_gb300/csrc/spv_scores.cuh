@@ -37,10 +37,11 @@ __host__ __device__ __forceinline__ bool moved_slots(const ScoresView &v) { retu
 // so that a cap far above the scores changes nothing in them.  Beyond: cap - 2
 // cap / (1 + e^(2 x / cap)), 2^-22 cap off, which is 2^-21 of a result there.
 constexpr float CAP_SMALL = 0.625f;
+constexpr float CAP_0 = 0.999999896f, CAP_1 = -0.333319736f, CAP_2 = 0.133047715f, CAP_3 = -0.0518318566f, CAP_4 = 0.0150636728f;
 __device__ __forceinline__ float capped_small(const ScoresView &v, float x)
 {
     const float u = x * v.cap_inv, w = u * u;
-    return x * fmaf(w, fmaf(w, fmaf(w, fmaf(w, 0.0150636728f, -0.0518318566f), 0.133047715f), -0.333319736f), 0.999999896f);
+    return x * fmaf(w, fmaf(w, fmaf(w, fmaf(w, CAP_4, CAP_3), CAP_2), CAP_1), CAP_0);
 }
 __device__ __forceinline__ float capped_large(const ScoresView &v, float x)
 {

@@ -60,6 +60,38 @@ __device__ __forceinline__ void tc_mma_ta(uint32_t d, uint32_t a, uint64_t b, ui
                  "r"(static_cast<uint32_t>(add))
                  : "memory");
 }
+// The same for a whole converged warp, of which one lane issues: operands that
+// the compiler knows to be the same in all lanes (constants, loop counters,
+// same_in_warp) come from the uniform registers that the instruction reads, and
+// need not be moved there one by one.  a, b: the low words of descriptors, whose
+// high words are constants.
+__device__ __forceinline__ uint32_t same_in_warp(uint32_t x) { return __shfl_sync(0xffffffffu, x, 0); }
+__device__ __forceinline__ int same_in_warp(int x) { return __shfl_sync(0xffffffffu, x, 0); }
+constexpr uint32_t DESC_HIGH = (1024u >> 4) | (1u << 14) | (2u << 29);  // groups of 8 rows 1024 bytes apart, 128-byte permutation
+__device__ __forceinline__ uint32_t desc_low(uint32_t addr, uint32_t panel) { return ((addr & 0x3ffffu) >> 4) | ((panel >> 4) << 16); }
+template <uint32_t SHAPE> __device__ __forceinline__ void warp_mma(uint32_t d, uint32_t a, uint32_t b, bool add)
+{
+    asm volatile("{\n\t.reg .pred p, e;\n\t.reg .b64 x, y;\n\t"
+                 "elect.sync _|e, 0xffffffff;\n\tsetp.ne.u32 p, %3, 0;\n\tmov.b64 x, {%1, %5};\n\tmov.b64 y, {%2, %5};\n\t"
+                 "@e tcgen05.mma.cta_group::1.kind::f16 [%0], x, y, %4, p;\n\t}" ::"r"(d), "r"(a), "r"(b),
+                 "r"(static_cast<uint32_t>(add)), "n"(SHAPE), "n"(DESC_HIGH)
+                 : "memory");
+}
+template <uint32_t SHAPE> __device__ __forceinline__ void warp_mma_ta(uint32_t d, uint32_t a, uint32_t b, bool add)
+{
+    asm volatile("{\n\t.reg .pred p, e;\n\t.reg .b64 y;\n\t"
+                 "elect.sync _|e, 0xffffffff;\n\tsetp.ne.u32 p, %3, 0;\n\tmov.b64 y, {%2, %5};\n\t"
+                 "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], y, %4, p;\n\t}" ::"r"(d), "r"(a), "r"(b),
+                 "r"(static_cast<uint32_t>(add)), "n"(SHAPE), "n"(DESC_HIGH)
+                 : "memory");
+}
+__device__ __forceinline__ void warp_commit(uint64_t *bar)
+{
+    asm volatile("{\n\t.reg .pred e;\n\telect.sync _|e, 0xffffffff;\n\t"
+                 "@e tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}" ::"r"(smem_u32(bar))
+                 : "memory");
+}
+
 // Arrives on `bar` when the products issued so far by this thread are done.
 __device__ __forceinline__ void tc_commit(uint64_t *bar)
 {

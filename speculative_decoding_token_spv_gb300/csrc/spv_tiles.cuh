@@ -46,7 +46,6 @@ namespace spv {
 constexpr int TILES_THREADS = 512;
 constexpr int TILES_WARPS = TILES_THREADS / 32;
 constexpr int TILES_PREPARE = 96;  // threads that bring q
-constexpr int TILES_ITEMS = 16;    // items whose flags can be in use at once
 
 struct TilesParams : ScoredParams {
     int32_t *timeouts;  // row_status, for waits that gave up
@@ -60,11 +59,12 @@ template <typename C, int D, bool PAIR> struct TilesShape {
     static constexpr int MINE = PAIR ? KEYS : KEYS / 2;          // of them a thread's
     static constexpr int TILE = KEYS * D * 2, RAW = KEYS * D;    // bytes of K or V as multiplied, and of e4m3
     static constexpr int Q_SUB = 128 * D * 2, Q = SUBS * Q_SUB;
-    static constexpr int Q_PLACES = 2 * Q <= 64 * 1024 ? 2 : 1;
+    static constexpr int Q_PLACES = !WIDEN && 2 * Q <= 64 * 1024 ? 2 : 1;
     static constexpr int ROOM = 224 * 1024 - Q_PLACES * Q;
-    static constexpr int RAW_STAGES = WIDEN ? 64 * 1024 / RAW : 0;
+    static constexpr int RAW_STAGES = WIDEN ? 32 * 1024 / RAW : 0;
     static constexpr int FIT = (ROOM - RAW_STAGES * RAW) / TILE, STAGES = FIT < 10 ? FIT : 10;
     static constexpr int K_AT = Q_PLACES * Q, RAW_AT = K_AT + STAGES * TILE, CTL_AT = RAW_AT + RAW_STAGES * RAW;
+    static constexpr int ITEMS = (STAGES + RAW_STAGES) / 2 + 3;  // whose flags can be in use at once: an item has two tiles at least
     static constexpr int GROUP = PAIR ? 128 : 256;               // threads that belong to the same rows
 };
 
@@ -75,9 +75,9 @@ struct TileLens : SeqLens {
 using TileCursor = CursorOf<TileLens>;
 
 template <typename S> struct TilesCtl {
-    uint64_t full[10], empty[10], s_full[2], p_full[2], o_done[2], q_full[2], q_empty[2], spare;
+    uint64_t full[S::STAGES], empty[S::STAGES], s_full[2], p_full[2], o_done[2], q_full[2], q_empty[2], spare;
     TileCursor start;
-    int bad[2][TILES_ITEMS];                                     // a page id outside the pool, for each group of row warps
+    char bad[2][S::ITEMS];                                    // a page id outside the pool, for each group of row warps
     int stop[2], lost[2];
     alignas(16) int positions[2][S::MINE];                       // of moved slots: of a tile's keys, for each four row warps
     uint32_t tmem;
@@ -87,8 +87,8 @@ template <typename S> struct TilesCtl {
             long long sums[TILES_WARPS];                         // before the roles begin
         } find;
         struct {
-            signed char depth[2][S::SUBS == 1 ? 64 : 1];         // trees: per place of q the depth of each new token
-            float top[S::SUBS == 1 ? 256 : 1];                   // maxima and sums of the two halves
+            signed char depth[S::Q_PLACES][S::SUBS == 1 ? 64 : 1];         // trees: per place of q the depth of each new token
+            float top[2][S::SUBS == 1 ? 256 : 1];                // maxima of the two halves, of a tile and the next; sums
             signed char q_power[S::WIDEN ? S::Q_PLACES * S::ROWS : 1];  // e4m3: the rows of q are stored times 2^q_power
         } at;
     };
@@ -186,6 +186,9 @@ template <typename S> __device__ __forceinline__ TileLens item_tiles(const Tiles
     return r;
 }
 __device__ __forceinline__ int count_of(const TileLens &s) { return max(1, s.to - s.from); }
+// An item's beginning and end -- its q, the first scores, writing the rows -- take about as long as OVERHEAD tiles, and the
+// ranges are cut as if it had so many more, before the first.
+constexpr int TILES_OVERHEAD = 2;
 
 // The block's range, by all its threads; `c` is the same for all.
 template <typename S> __device__ TileCursor tiles_find(const TilesParams &p, TilesCtl<S> *ctl, int tid)
@@ -210,7 +213,7 @@ template <typename S> __device__ TileCursor tiles_find(const TilesParams &p, Til
         return mine;
     };
     long long sum = 0;
-    for (int e = e0; e < e1; e += 32) sum += count32(e);
+    for (int e = e0; e < e1; e += 32) sum += count32(e) + (e + lane < e1 ? TILES_OVERHEAD : 0);
 #pragma unroll
     for (int o = 16; o; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
     if (lane == 0) ctl->find.sums[warp] = sum * p.c.kv_heads;
@@ -230,8 +233,8 @@ template <typename S> __device__ TileCursor tiles_find(const TilesParams &p, Til
         c.end = range_begin(c, block + 1);
         if (c.at >= before && c.at < before + mine) {
             for (int e = e0; e < e1; e += 32) {
-                const int n = count32(e);
-                int upto = n;
+                const int n = count32(e), units = n + (e + lane < e1 ? TILES_OVERHEAD : 0);
+                int upto = units;
 #pragma unroll
                 for (int o = 1; o < 32; o <<= 1) {
                     const int y = __shfl_up_sync(0xffffffffu, upto, o);
@@ -241,12 +244,13 @@ template <typename S> __device__ TileCursor tiles_find(const TilesParams &p, Til
                 if (here) {
                     const int l = __ffs(here) - 1;
                     const int tiles = __shfl_sync(0xffffffffu, n, l);
-                    before += static_cast<long long>(__shfl_sync(0xffffffffu, upto, l) - tiles) * p.c.kv_heads;
+                    before += static_cast<long long>(__shfl_sync(0xffffffffu, upto - units, l)) * p.c.kv_heads;
                     c.tiles = tiles;
                     c.b = (e + l) / p.w.row_tiles;
                     c.row_tile = e + l - c.b * p.w.row_tiles;
-                    c.h = static_cast<int>(quotient(c.at - before, tiles));
-                    c.first = before + static_cast<long long>(c.h) * tiles;
+                    c.h = static_cast<int>(quotient(c.at - before, tiles + TILES_OVERHEAD));
+                    c.first = before + static_cast<long long>(c.h) * (tiles + TILES_OVERHEAD) + TILES_OVERHEAD;
+                    if (c.at < c.first) c.at = c.first < c.end ? c.first : c.end;
                     if (lane == 0) ctl->start = c;
                     break;
                 }
@@ -265,7 +269,7 @@ template <typename S> __device__ TileCursor tiles_find(const TilesParams &p, Til
 // To the next item; a whole warp.
 template <typename S> __device__ __forceinline__ void tiles_next(TileCursor &c, const TilesParams &p, int lane)
 {
-    c.first += c.tiles;
+    c.first += c.tiles + TILES_OVERHEAD;
     c.at = c.first;
     if (++c.h < p.c.kv_heads) return;
     c.h = 0;
@@ -311,7 +315,7 @@ __device__ void tiles_load(const TilesParams &p, TileCursor c, char *smem, Tiles
         if (t >= NST && !tiles_wait(ctl, &ctl->empty[st], (t / NST - 1) & 1, err)) return false;
         const char *raw = smem + S::RAW_AT + (t % RST) * S::RAW;
         char *to = smem + S::K_AT + st * S::TILE;
-#pragma unroll 2
+#pragma unroll 4
         for (int i = 0; i < WARP_ROWS / RPI; ++i) {
             const int row = WARP_ROWS * w + i * RPI + sub;
             const uint4 x = *reinterpret_cast<const uint4 *>(raw + row * D + chunk * 16);
@@ -328,7 +332,8 @@ __device__ void tiles_load(const TilesParams &p, TileCursor c, char *smem, Tiles
             *reinterpret_cast<uint4 *>(to + tile_at<KEYS>(row, 2 * chunk + !swap)) = swap ? lo : hi;
         }
         fence_async_shared();
-        mbar_arrive(&ctl->full[st]);
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&ctl->full[st]);
         return true;
     };
     bool ok = true;
@@ -336,17 +341,20 @@ __device__ void tiles_load(const TilesParams &p, TileCursor c, char *smem, Tiles
         const int t0 = tiles_first(c), t1 = tiles_last(c);
         if (t0 == t1) continue;
         const int32_t *table = p.c.table + static_cast<int64_t>(c.b) * p.c.max_pages;
-        const int flags = item++ % TILES_ITEMS;
+        const int flags = item++ % S::ITEMS;
         auto lookup = [&](int tile) {  // the page id of this lane's row of a tile, unchecked; -1: no such row
             const int j = tile * KEYS + WARP_ROWS * w + lane;
             return lane < WARP_ROWS && tile < t1 && j < c.s.total ? __ldg(table + (j >> p.c.page_shift)) : -1;
         };
-        // With maps the first warp's lanes ask the copy engine for a box each: a page (or what a tile holds of a larger one)
-        // by 64 elements.
-        const int box_slots = min(mask + 1, KEYS), boxes = map_k ? KEYS / box_slots * (D / 64) : 0;
+        // With maps each warp asks the copy engine for a quarter of the boxes: a page (or what a tile holds of a larger one)
+        // by 64 elements, from a lane each.  (A lane's takes 80 to 100 cycles: from one warp, 16 of a tile of K and 16 of V
+        // took longer than the tile's products.)
+        const int box_slots = min(mask + 1, KEYS), boxes = map_k ? KEYS / box_slots * (D / 64) : 0, quarter = max(1, boxes >> 2);
+        const int box = w * quarter + lane, boxes_here = max(0, min(quarter, boxes - w * quarter));
+        const bool asks = lane < boxes_here;
         auto box_lookup = [&](int tile) {
-            const int j = tile * KEYS + lane / (D / 64) * box_slots;
-            return w == 0 && lane < boxes && tile < t1 && j < c.s.total ? __ldg(table + (j >> p.c.page_shift)) : -1;
+            const int j = tile * KEYS + box / (D / 64) * box_slots;
+            return asks && tile < t1 && j < c.s.total ? __ldg(table + (j >> p.c.page_shift)) : -1;
         };
         int next = map_k ? box_lookup(t0) : lookup(t0);
         for (int tile = t0; ok && tile < t1; ++tile) {
@@ -357,26 +365,22 @@ __device__ void tiles_load(const TilesParams &p, TileCursor c, char *smem, Tiles
                 const PoolView &pool = kv ? p.c.v : p.c.k;
                 const int st = n % NST;
                 if (map_k && (!kv || j0 + KEYS <= c.s.total)) {
-                    const int slot = j0 + lane / (D / 64) * box_slots;
-                    if (w == 0 && lane < boxes && slot < c.s.total && static_cast<unsigned>(page) >= static_cast<unsigned>(p.c.num_pages))
-                        *reinterpret_cast<volatile int *>(&ctl->bad[0][flags]) = *reinterpret_cast<volatile int *>(&ctl->bad[1][flags]) = 1;
+                    const int slot = j0 + box / (D / 64) * box_slots;
+                    if (asks && slot < c.s.total && static_cast<unsigned>(page) >= static_cast<unsigned>(p.c.num_pages))
+                        *reinterpret_cast<volatile char *>(&ctl->bad[0][flags]) = *reinterpret_cast<volatile char *>(&ctl->bad[1][flags]) = 1;
                     if (n >= NST && !(ok = tiles_wait(ctl, &ctl->empty[st], (n / NST - 1) & 1, err))) break;
-                    if (lt == 0)
-                        mbar_arrive_expect_tx(&ctl->full[st], S::TILE);
-                    else
-                        mbar_arrive(&ctl->full[st]);
-                    if (w == 0) {
-                        __syncwarp();
-                        if (lane < boxes)
-                            tma_box(base + S::K_AT + st * S::TILE + (lane % (D / 64)) * (KEYS * 128) + lane / (D / 64) * box_slots * 128,
-                                    kv ? map_v : map_k, (lane % (D / 64)) * 64, slot & mask, c.h, page, &ctl->full[st]);
-                    }
+                    if (lane == 0) mbar_arrive_expect_tx(&ctl->full[st], boxes_here * box_slots * 128);
+                    __syncwarp();
+                    if (asks)
+                        tma_box(base + S::K_AT + st * S::TILE + (box % (D / 64)) * (KEYS * 128) + box / (D / 64) * box_slots * 128,
+                                kv ? map_v : map_k, (box % (D / 64)) * 64, slot & mask, c.h, page, &ctl->full[st]);
+                    __syncwarp();
                     continue;
                 }
                 int pg = map_k ? lookup(tile) : page;
                 if (static_cast<unsigned>(pg) >= static_cast<unsigned>(p.c.num_pages)) {
                     if (lane < WARP_ROWS && j0 + WARP_ROWS * w + lane < c.s.total)
-                        *reinterpret_cast<volatile int *>(&ctl->bad[0][flags]) = *reinterpret_cast<volatile int *>(&ctl->bad[1][flags]) = 1;
+                        *reinterpret_cast<volatile char *>(&ctl->bad[0][flags]) = *reinterpret_cast<volatile char *>(&ctl->bad[1][flags]) = 1;
                     pg = -1;
                 }
                 const int64_t mine = pg < 0 ? -1 : pg * pool.page_stride + ((j0 + WARP_ROWS * w + lane) & mask) * pool.slot_stride;
@@ -399,117 +403,129 @@ __device__ void tiles_load(const TilesParams &p, TileCursor c, char *smem, Tiles
                     cp_async16_zfill(to + (S::WIDEN ? row * D + chunk * 16 : tile_at<KEYS>(row, chunk)), at < 0 ? pool.base : from + at,
                                      at < 0 ? 0 : 16);
                 }
-                if (S::WIDEN)
+                if (S::WIDEN) {
                     cp_async_commit();
-                else
-                    cp_async_arrive(&ctl->full[st]);
+                } else {  // the fence for the tensor cores is the writers': in the products' warp it took a thousand cycles a tile
+                    asm volatile("cp.async.wait_all;" ::: "memory");
+                    fence_async_shared();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(&ctl->full[st]);
+                }
             }
         }
     }
     asm volatile("cp.async.wait_all;" ::: "memory");
     if (S::WIDEN) {  // the tiles still on their way
         for (int t = n >= RST ? n - RST : 0; ok && t < n; ++t) ok = widen(t);
-    } else if (map_k && w == 0) {  // the copy engine's, before the block may end: nobody else may have waited for them
+    } else if (map_k) {  // the copy engine's, before the block may end: nobody else may have waited for them
         for (int t = max(0, n - NST); t < n; ++t) mbar_drain(&ctl->full[t % NST], (t / NST) & 1);
     }
 }
 
 // ------------------------------------------------------------------ products
-// One warp; its first lane issues.
+// One warp.
 template <typename C, int D, bool PAIR, typename S = TilesShape<C, D, PAIR>>
 __device__ void tiles_multiply(const TilesParams &p, TileCursor c, char *smem, TilesCtl<S> *ctl, unsigned *err, int lane)
 {
     constexpr bool BF16 = std::is_same<C, __nv_bfloat16>::value;
     constexpr uint32_t QK = mma_shape(BF16, false, S::KEYS), PV = mma_shape(BF16, true, D);
     constexpr int NST = S::STAGES, KEYS = S::KEYS;
-    const uint32_t base = smem_u32(smem), tmem = ctl->tmem;
-    int n = 0, item = 0, weights[2] = {0, 0};  // tiles of K and V before the item's; weights of each place so far
+    // all values here are the same in all lanes, and the compiler is told so
+    const uint32_t base = smem_u32(smem), tmem = same_in_warp(ctl->tmem);
+    int st = 0, phase = 0;             // the ring's place and pass of the next tile of K; V's is the one behind it
+    int item = 0, buf = 0;
+    uint32_t passes = 0;               // bit s: parity of the weights' barrier of place s
     bool ok = true;
+    auto after = [&](int x) { return x + 1 == NST ? 0 : x + 1; };
     for (; ok && c.at < c.end; tiles_next<S>(c, p, lane)) {
-        const int t0 = tiles_first(c), tiles = tiles_last(c) - t0;
+        const int t0 = same_in_warp(tiles_first(c)), tiles = same_in_warp(tiles_last(c)) - t0;
         if (tiles == 0) continue;
-        const int place = item % S::Q_PLACES;
+        const int place = S::Q_PLACES == 1 ? 0 : item & 1;
         if (!tiles_wait(ctl, &ctl->q_full[place], (item / S::Q_PLACES) & 1, err)) return;
-        bool begun[2] = {false, false}, pending[2] = {false, false};
-        auto waits = [&](int t) { return tiles_wait(ctl, &ctl->full[t % NST], (t / NST) & 1, err); };
-        auto release = [&](int t) {
-            if (lane == 0) tc_commit(&ctl->empty[t % NST]);
-        };
-        auto scores = [&](int s, int i) {  // of the rows' tile (PAIR) or place s with tile i of keys
-            if (lane == 0) {
-                tc_fence_after();
-                fence_async_shared();  // K may have been written by asynchronous copies of threads
-                const uint64_t q = desc_k_major(base + place * S::Q + (PAIR ? s * S::Q_SUB : 0));
-                const uint64_t k = desc_k_major(base + S::K_AT + ((n + 2 * i) % NST) * S::TILE);
+        ++item;
+        const uint32_t q0 = desc_low(base + place * S::Q, 16);
+        auto scores = [&](int s, int k_st) {  // of the rows' tile (PAIR) or place s with a tile of keys
+            tc_fence_after();
+            const uint32_t q = q0 + (PAIR ? s * (S::Q_SUB >> 4) : 0), k = desc_low(base + S::K_AT + k_st * S::TILE, 16);
 #pragma unroll
-                for (int ks = 0; ks < D / 16; ++ks)
-                    tc_mma(tmem + s * 128, q + (((ks >> 2) * (128 * 128) + (ks & 3) * 32) >> 4),
-                           k + (((ks >> 2) * (KEYS * 128) + (ks & 3) * 32) >> 4), QK, ks > 0);
-                tc_commit(&ctl->s_full[s]);
-            }
-            __syncwarp();
+            for (int ks = 0; ks < D / 16; ++ks)
+                warp_mma<QK>(tmem + s * 128, q + (((ks >> 2) * (128 * 128) + (ks & 3) * 32) >> 4),
+                             k + (((ks >> 2) * (KEYS * 128) + (ks & 3) * 32) >> 4), ks > 0);
+            warp_commit(&ctl->s_full[s]);
         };
-        auto outputs = [&](int s, int i, bool done) {
-            if (!tiles_wait(ctl, &ctl->p_full[s], weights[s]++ & 1, err)) return false;
-            const int o = PAIR ? s : 0;
-            if (lane == 0) {
-                tc_fence_after();
-                fence_async_shared();
-                const uint64_t v = desc_n_major(base + S::K_AT + ((n + 2 * i + 1) % NST) * S::TILE, KEYS * 128);
+        auto outputs = [&](int s, int v_st, bool add, bool done) {
+            tc_fence_after();
+            const uint32_t o = tmem + 256 + (PAIR ? s * 128 : 0), v = desc_low(base + S::K_AT + v_st * S::TILE, KEYS * 128);
 #pragma unroll
-                for (int ks = 0; ks < KEYS / 16; ++ks)
-                    tc_mma_ta(tmem + 256 + o * 128, tmem + s * 128 + 16 * ks / S::MINE * S::MINE + 16 * ks % S::MINE / 2,
-                              v + ks * (2048 >> 4), PV, begun[o] || ks > 0);
-                if (done) tc_commit(&ctl->o_done[s]);
-            }
-            begun[o] = true;
-            __syncwarp();
-            return true;
+            for (int ks = 0; ks < KEYS / 16; ++ks)
+                warp_mma_ta<PV>(o, tmem + s * 128 + 16 * ks / S::MINE * S::MINE + 16 * ks % S::MINE / 2, v + ks * (2048 >> 4),
+                                add || ks > 0);
+            if (done) warp_commit(&ctl->o_done[s]);
         };
+        auto full = [&](int place, int pass) { return tiles_wait(ctl, &ctl->full[place], pass, err); };
         if constexpr (PAIR) {
-            for (int i = 0; ok && i < tiles; ++i) {
-#pragma unroll
-                for (int s = 0; s < 2; ++s) {
-                    const bool here = t0 + i >= c.s.lo[s] && t0 + i < c.s.hi[s];
-                    if (pending[s]) ok = ok && waits(n + 2 * i - 1) && outputs(s, i - 1, !here);
-                    if (s == 1 && i > 0 && ok) {
-                        ok = waits(n + 2 * i - 1);
-                        release(n + 2 * i - 1);
-                    }
-                    ok = ok && waits(n + 2 * i);
-                    if (here && ok) scores(s, i);
-                    pending[s] = here;
+            const int lo0 = same_in_warp(c.s.lo[0]), hi0 = same_in_warp(c.s.hi[0]), lo1 = same_in_warp(c.s.lo[1]), hi1 = same_in_warp(c.s.hi[1]);
+            bool begun0 = false, begun1 = false, pending0 = false, pending1 = false;
+            int v_st = 0, v_pass = 0;
+            for (int i = 0; i <= tiles; ++i) {  // the outputs of the tile before, and the scores of this one
+                const bool keys = i < tiles;
+                const bool here0 = keys && t0 + i >= lo0 && t0 + i < hi0, here1 = keys && t0 + i >= lo1 && t0 + i < hi1;
+                if (i > 0 && !(ok = full(v_st, v_pass))) return;
+                if (pending0) {
+                    if (!(ok = tiles_wait(ctl, &ctl->p_full[0], passes & 1, err))) return;
+                    passes ^= 1;
+                    outputs(0, v_st, begun0, !here0);
+                    begun0 = true;
                 }
-                if (ok) release(n + 2 * i);
+                if (keys && !(ok = full(st, phase))) return;
+                if (here0) scores(0, st);
+                if (pending1) {
+                    if (!(ok = tiles_wait(ctl, &ctl->p_full[1], passes >> 1 & 1, err))) return;
+                    passes ^= 2;
+                    outputs(1, v_st, begun1, !here1);
+                    begun1 = true;
+                }
+                if (i > 0) warp_commit(&ctl->empty[v_st]);
+                if (here1) scores(1, st);
+                pending0 = here0;
+                pending1 = here1;
+                if (!keys) break;
+                warp_commit(&ctl->empty[st]);
+                if (i == tiles - 1) warp_commit(&ctl->q_empty[place]);
+                st = after(st);
+                if (st == 0) phase ^= 1;
+                v_st = st, v_pass = phase;
+                st = after(st);
+                if (st == 0) phase ^= 1;
             }
-            if (ok && lane == 0) tc_commit(&ctl->q_empty[place]);
-            __syncwarp();
-#pragma unroll
-            for (int s = 0; s < 2; ++s)
-                if (pending[s]) ok = ok && waits(n + 2 * tiles - 1) && outputs(s, tiles - 1, true);
-            ok = ok && waits(n + 2 * tiles - 1);
-            if (ok) release(n + 2 * tiles - 1);
         } else {
             // the places of scores go on in turn from item to item
-            for (int i = 0; ok && i < tiles + 2; ++i) {
-                const int s = (n / 2 + i) & 1;
+            int v_st[2] = {0, 0}, v_pass[2] = {0, 0};
+            for (int i = 0; i < tiles + 2; ++i) {  // the outputs of the tile two before, and the scores of this one
+                const int s = buf;
                 if (i >= 2) {
-                    ok = waits(n + 2 * i - 3) && outputs(s, i - 2, true);
-                    if (ok) release(n + 2 * i - 3);
+                    if (!(ok = full(v_st[0], v_pass[0]))) return;
+                    if (!(ok = tiles_wait(ctl, &ctl->p_full[s], passes >> s & 1, err))) return;
+                    passes ^= 1u << s;
+                    outputs(s, v_st[0], i > 2, true);
+                    warp_commit(&ctl->empty[v_st[0]]);
                 }
+                v_st[0] = v_st[1], v_pass[0] = v_pass[1];
                 if (i < tiles) {
-                    ok = ok && waits(n + 2 * i);
-                    if (ok) {
-                        scores(s, i);
-                        release(n + 2 * i);
-                    }
+                    if (!(ok = full(st, phase))) return;
+                    scores(s, st);
+                    warp_commit(&ctl->empty[st]);
+                    st = after(st);
+                    if (st == 0) phase ^= 1;
+                    v_st[1] = st, v_pass[1] = phase;
+                    st = after(st);
+                    if (st == 0) phase ^= 1;
                 }
-                if (i == tiles - 1 && ok && lane == 0) tc_commit(&ctl->q_empty[place]);
-                __syncwarp();
+                if (i == tiles - 1) warp_commit(&ctl->q_empty[place]);
+                buf ^= 1;
             }
+            // two turns more than tiles: the next item begins at the place behind this one's last
         }
-        n += 2 * tiles;
-        ++item;
     }
 }
 
@@ -756,6 +772,108 @@ __device__ __noinline__ void tiles_finish(const TilesParams &p, TilesCtl<TilesSh
     for (; c.at < c.end; tiles_next<S>(c, p, lane)) tiles_lost<D, S>(p, c, begin, r_from, r_count, tid, S::GROUP);
 }
 
+__device__ __forceinline__ float2 unpair(unsigned long long x)
+{
+    float2 y;
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(y.x), "=f"(y.y) : "l"(x));
+    return y;
+}
+
+// Cap, bias and a window over moved slots of a row's MINE scores of a tile whose
+// first key is jb: the true scores are then x f - off.
+template <int MINE, bool PAIR, typename Ctl>
+__device__ __forceinline__ void tile_shape(const TilesParams &p, unsigned long long (&x)[MINE / 2], float *f, float *off, const TileCursor &c,
+                                           Ctl *ctl, int place, int jb, int own, float slope, int origin, int quad)
+{
+    const ScoresView &v = p.sc;
+    if (v.cap2 != 0.0f) {
+        float large = 0.0f;
+#pragma unroll
+        for (int i = 0; i < MINE / 2; ++i) {
+            const float2 y = unpair(x[i]);
+            large = fmax3(large, fabsf(y.x), fabsf(y.y));
+        }
+        const float edge = CAP_SMALL * v.cap2;
+        if (__any_sync(0xffffffffu, large * fabsf(*f) >= edge)) {
+#pragma unroll
+            for (int i = 0; i < MINE / 2; ++i) {
+                const float2 y = unpair(x[i]);
+                const float a = y.x * *f, b = y.y * *f;
+                x[i] = pack2(fabsf(a) >= edge ? capped_large(v, a) : capped_small(v, a), fabsf(b) >= edge ? capped_large(v, b) : capped_small(v, b));
+            }
+        } else {  // x f P((x f / cap)^2), as capped_small
+            const float u = *f * v.cap_inv;
+            const unsigned long long u2 = pack2(u, u), c0 = pack2(CAP_0 * *f, CAP_0 * *f), c1 = pack2(CAP_1 * *f, CAP_1 * *f),
+                                     c2 = pack2(CAP_2 * *f, CAP_2 * *f), c3 = pack2(CAP_3 * *f, CAP_3 * *f), c4 = pack2(CAP_4 * *f, CAP_4 * *f);
+#pragma unroll
+            for (int i = 0; i < MINE / 2; ++i) {
+                const unsigned long long y = mul2(x[i], u2), w = mul2(y, y);
+                x[i] = mul2(x[i], ffma2(w, ffma2(w, ffma2(w, ffma2(w, c4, c3), c2), c1), c0));
+            }
+        }
+        *f = 1.0f;
+    } else if (!(*f > 0.0f)) {  // the largest product has to be the largest score
+        const unsigned long long f2 = pack2(*f, *f);
+#pragma unroll
+        for (int i = 0; i < MINE / 2; ++i) x[i] = mul2(x[i], f2);
+        *f = 1.0f;
+    }
+    if (moved_slots(v)) {
+        const float s = -slope / *f;
+        if (v.window > 0) {
+            const int2 *at = reinterpret_cast<const int2 *>(ctl->positions[quad]);
+#pragma unroll
+            for (int i = 0; i < MINE / 2; ++i) {
+                const int2 there = at[i];
+                const int a = own - there.x, b = own - there.y;
+                const float2 y = unpair(x[i]);
+                x[i] = pack2(a >= v.window ? -CUDART_INF_F : fmaf(s, fabsf(static_cast<float>(a)), y.x),
+                             b >= v.window ? -CUDART_INF_F : fmaf(s, fabsf(static_cast<float>(b)), y.y));
+            }
+        } else {
+            const ulonglong2 *at = reinterpret_cast<const ulonglong2 *>(ctl->positions[quad]);
+            const float mine = static_cast<float>(own - origin);
+            const unsigned long long mine2 = pack2(mine, mine);
+#pragma unroll
+            for (int i = 0; i < MINE / 2; i += 2) {
+                const ulonglong2 there = at[i / 2];
+                const float2 a = unpair(fadd2(mine2, there.x)), b = unpair(fadd2(mine2, there.y)), y = unpair(x[i]), z = unpair(x[i + 1]);
+                x[i] = pack2(fmaf(s, fabsf(a.x), y.x), fmaf(s, fabsf(a.y), y.y));
+                x[i + 1] = pack2(fmaf(s, fabsf(b.x), z.x), fmaf(s, fabsf(b.y), z.y));
+            }
+        }
+    } else if (v.slopes) {
+        const float s = slope / *f;
+        if (!PAIR && p.parent && jb + MINE > c.s.ctx) {  // a node's position is its depth's
+#pragma unroll
+            for (int i = 0; i < MINE / 2; ++i) {
+                const float2 y = unpair(x[i]);
+                float z[2] = {y.x, y.y};
+#pragma unroll
+                for (int k = 0; k < 2; ++k) {
+                    const int j = jb + 2 * i + k, there = j >= c.s.ctx && j < c.s.total ? c.s.ctx + ctl->at.depth[place][j - c.s.ctx] : j;
+                    z[k] = fmaf(-s, fabsf(static_cast<float>(own - there)), z[k]);
+                }
+                x[i] = pack2(z[0], z[1]);
+            }
+        } else if (__all_sync(0xffffffffu, own >= jb + MINE - 1)) {  // no key is ahead: the distance is own - jb less the key's place
+            *off = slope * static_cast<float>(own - jb);
+#pragma unroll
+            for (int i = 0; i < MINE / 2; ++i) {
+                const float2 y = unpair(x[i]);
+                x[i] = pack2(fmaf(s, static_cast<float>(2 * i), y.x), fmaf(s, static_cast<float>(2 * i + 1), y.y));
+            }
+        } else {
+            const float far = static_cast<float>(own - jb);
+#pragma unroll
+            for (int i = 0; i < MINE / 2; ++i) {
+                const float2 y = unpair(x[i]);
+                x[i] = pack2(fmaf(-s, fabsf(far - static_cast<float>(2 * i)), y.x), fmaf(-s, fabsf(far - static_cast<float>(2 * i + 1)), y.y));
+            }
+        }
+    }
+}
+
 // A row a thread (PAIR), or half of its keys.  tid: 0 .. 255.
 template <typename C, int D, bool PAIR, typename S = TilesShape<C, D, PAIR>>
 __device__ void tiles_rows(const TilesParams &p, TileCursor c, char *smem, TilesCtl<S> *ctl, unsigned *err, int tid)
@@ -801,13 +919,14 @@ __device__ void tiles_rows(const TilesParams &p, TileCursor c, char *smem, Tiles
                     see.lo = view.lo;
                 }
             }
+            const int origin = moved ? __ldg(pos + c.s.ctx) : 0;  // the first new token's position
             const float slope = there && v.slopes ? __ldg(v.slopes + c.h * p.group + (row0 + r) - token * p.group) * LOG2E : 0.0f;
             float factor = p.scale_log2 * (p.c.k_scale ? __ldg(p.c.k_scale + c.h) : 1.0f);
             ok = tiles_wait(ctl, &ctl->q_full[place], (item / S::Q_PLACES) & 1, err);
             if (S::WIDEN) factor *= exp2f(-static_cast<float>(ctl->at.q_power[place * S::ROWS + r]));
             __syncwarp();
             if (lane == 0) mbar_arrive(&ctl->q_empty[place]);
-            const bool shaped = v.cap2 != 0.0f || v.slopes || moved || !(factor > 0.0f);
+            const bool shaped = v.cap2 != 0.0f || v.slopes || moved || __any_sync(0xffffffffu, !(factor > 0.0f));
             const bool works = __any_sync(0xffffffffu, there);
 #pragma unroll 1
             for (int tile = s0; tile < s1; ++tile, ++n) {  // to its end even after a wait gave up: the halves meet at each tile
@@ -817,50 +936,26 @@ __device__ void tiles_rows(const TilesParams &p, TileCursor c, char *smem, Tiles
                 if (moved) {  // positions of these keys, by the 128 threads that have them
                     const int j = jb + lane_row, at = lane_row < MINE && j < c.s.total ? __ldg(pos + j) : 0;
                     quad_sync<PAIR>(tid >> 7);  // the last tile's have been read
-                    if (lane_row < MINE) ctl->positions[tid >> 7][lane_row] = at;
+                    // as distances to the item's first token where no window has to be exact: 32 bits hold those below 2^24
+                    if (lane_row < MINE) ctl->positions[tid >> 7][lane_row] = v.window > 0 ? at : __float_as_int(static_cast<float>(origin - at));
                     quad_sync<PAIR>(tid >> 7);
                 }
                 ok = ok && tiles_wait(ctl, &ctl->s_full[buf], (PAIR ? n : n >> 1) & 1, err);
                 tc_fence_after();
                 __syncwarp();
                 if (works) {
-                    float x[MINE];
-                    {
+                    // Pairs of scores, so that one instruction works on two.
+                    unsigned long long x[MINE / 2];
 #pragma unroll
-                        for (int i = 0; i < MINE; i += 32) {
-                            uint32_t y[32];
-                            tc_ld32(y, tm_s + i);
+                    for (int i = 0; i < MINE; i += 32) {
+                        uint32_t y[32];
+                        tc_ld32(y, tm_s + i);
 #pragma unroll
-                            for (int k = 0; k < 32; ++k) x[i + k] = __uint_as_float(y[k]);
-                        }
+                        for (int k = 0; k < 32; k += 2) x[(i + k) / 2] = pack2(__uint_as_float(y[k]), __uint_as_float(y[k + 1]));
                     }
-                    float f = factor;
-                    if (shaped) {
-                        f = 1.0f;
-#pragma unroll
-                        for (int i = 0; i < MINE; ++i) x[i] *= factor;
-                        if (v.cap2 != 0.0f) cap_all(v, x);
-                        if (moved) {
-#pragma unroll
-                            for (int i = 0; i < MINE; ++i) {
-                                const int far = own - ctl->positions[tid >> 7][i];
-                                x[i] = fmaf(-slope, fabsf(static_cast<float>(far)), x[i]);
-                                if (v.window > 0 && far >= v.window) x[i] = -CUDART_INF_F;
-                            }
-                        } else if (v.slopes) {
-                            if (!PAIR && p.parent && jb + MINE > c.s.ctx) {  // a node's position is its depth's
-#pragma unroll
-                                for (int i = 0; i < MINE; ++i) {
-                                    const int j = jb + i, there = j >= c.s.ctx && j < c.s.total ? c.s.ctx + ctl->at.depth[place][j - c.s.ctx] : j;
-                                    x[i] = fmaf(-slope, fabsf(static_cast<float>(own - there)), x[i]);
-                                }
-                            } else {
-                                const float far = static_cast<float>(own - jb);
-#pragma unroll
-                                for (int i = 0; i < MINE; ++i) x[i] = fmaf(-slope, fabsf(far - static_cast<float>(i)), x[i]);
-                            }
-                        }
-                    }
+                    // The true scores are x f - off.
+                    float f = factor, off = 0.0f;
+                    if (shaped) tile_shape<MINE, PAIR>(p, x, &f, &off, c, ctl, place, jb, own, slope, origin, tid >> 7);
                     const bool seen = see.lo <= jb && see.hi >= jb + MINE;
                     if (!__all_sync(0xffffffffu, seen)) {
 #pragma unroll
@@ -873,18 +968,28 @@ __device__ void tiles_rows(const TilesParams &p, TileCursor c, char *smem, Tiles
                             }
                             mask = lo == 32 ? 0u : mask & ~((1u << lo) - 1u);
 #pragma unroll
-                            for (int k = 0; k < 32; ++k) x[i + k] = mask >> k & 1 ? x[i + k] : -CUDART_INF_F;
+                            for (int k = 0; k < 32; k += 2) {
+                                const float2 y = unpair(x[(i + k) / 2]);
+                                x[(i + k) / 2] = pack2(mask >> k & 1 ? y.x : -CUDART_INF_F, mask >> (k + 1) & 1 ? y.y : -CUDART_INF_F);
+                            }
                         }
                     }
-                    float top = x[0];
+                    float tops[4];
 #pragma unroll
-                    for (int i = 1; i + 1 < MINE; i += 2) top = fmax3(top, x[i], x[i + 1]);
-                    top = fmaxf(top, x[MINE - 1]) * f;
+                    for (int i = 0; i < 4; ++i) {
+                        const float2 y = unpair(x[i]);
+                        tops[i] = fmaxf(y.x, y.y);
+                    }
+#pragma unroll
+                    for (int i = 4; i < MINE / 2; ++i) {
+                        const float2 y = unpair(x[i]);
+                        tops[i & 3] = fmax3(tops[i & 3], y.x, y.y);
+                    }
+                    float top = fmaxf(fmaxf(tops[0], tops[1]), fmaxf(tops[2], tops[3])) * f - off;
                     if (HALVES == 2) {  // the maximum of both halves, by the two warps that have these rows
-                        halves_sync(lane_row / 32);  // the last tile's has been read
-                        ctl->at.top[tid] = top;
-                        halves_sync(lane_row / 32);
-                        top = fmaxf(top, ctl->at.top[tid ^ 128]);
+                        ctl->at.top[n & 1][tid] = top;
+                        halves_sync(lane_row / 32);  // (the places of two tiles: the one before has been read when both are here)
+                        top = fmaxf(top, ctl->at.top[n & 1][tid ^ 128]);
                         if (n >= 2) ok = ok && tiles_wait(ctl, &ctl->o_done[buf], ((n - 2) >> 1) & 1, err);
                     }
                     if (tile == s0) {
@@ -905,24 +1010,27 @@ __device__ void tiles_rows(const TilesParams &p, TileCursor c, char *smem, Tiles
                             tc_st16(tm_o + i, y);
                         }
                     }
-                    const float base = m == -CUDART_INF_F ? 0.0f : m;
-                    if (f != 1.0f && __any_sync(0xffffffffu, fabsf(base) > 0x1p20f)) {
-                        // the product is rounded as m was, not fused with the difference: of scores this large the largest
-                        // would else miss m by more than a weight can hold
+                    float base = m == -CUDART_INF_F ? 0.0f : m + off;
+                    if (__any_sync(0xffffffffu, fabsf(base) > 0x1p20f)) {
+                        // the score is rounded as m was, not fused with the difference: of scores this large the largest would
+                        // else miss m by more than a weight can hold
+                        const unsigned long long f2 = pack2(f, f), none = pack2(-off, -off);
 #pragma unroll
-                        for (int i = 0; i < MINE; ++i) x[i] = __fmul_rn(x[i], f);
+                        for (int i = 0; i < MINE / 2; ++i) x[i] = fadd2(mul2(x[i], f2), none);
                         f = 1.0f;
+                        base = m == -CUDART_INF_F ? 0.0f : m;
                     }
-                    float sum0 = 0.0f, sum1 = 0.0f;
+                    const unsigned long long f2 = pack2(f, f), base2 = pack2(-base, -base);
+                    unsigned long long sum[2] = {0, 0};
                     constexpr int AT_ONCE = MINE < 64 ? MINE : 64;
 #pragma unroll
                     for (int i0 = 0; i0 < MINE; i0 += AT_ONCE) {
                         uint32_t pk[AT_ONCE / 2];
 #pragma unroll
                         for (int i = 0; i < AT_ONCE; i += 2) {
-                            const float a = fast_exp2(fmaf(x[i0 + i], f, -base)), b = fast_exp2(fmaf(x[i0 + i + 1], f, -base));
-                            sum0 += a;
-                            sum1 += b;
+                            const float2 y = unpair(ffma2(x[(i0 + i) / 2], f2, base2));
+                            const float a = fast_exp2(y.x), b = fast_exp2(y.y);
+                            sum[i / 2 & 1] = fadd2(sum[i / 2 & 1], pack2(a, b));
                             // rounded to 16 bits for the product (half a step of the type each); l keeps 32 bits
                             pk[i / 2] = pack_mma<M>(a, b);
                         }
@@ -931,7 +1039,8 @@ __device__ void tiles_rows(const TilesParams &p, TileCursor c, char *smem, Tiles
                         else
                             tc_st16(tm_s + i0 / 2, pk);
                     }
-                    l += sum0 + sum1;
+                    const float2 all = unpair(fadd2(sum[0], sum[1]));
+                    l += all.x + all.y;
                     tc_wait_st();
                 }
                 tc_fence_before();
@@ -946,19 +1055,19 @@ __device__ void tiles_rows(const TilesParams &p, TileCursor c, char *smem, Tiles
                 ok = ok && tiles_wait(ctl, &ctl->o_done[(n - 1) & 1], ((n - 1) >> 1) & 1, err);
             }
             tc_fence_after();
-            any_bad |= *reinterpret_cast<volatile int *>(&ctl->bad[group][item % TILES_ITEMS]) != 0;
+            any_bad |= *reinterpret_cast<volatile char *>(&ctl->bad[group][item % S::ITEMS]) != 0;
             ++item;
         }
         const bool tiles = s0 < s1;
         group_sync<GROUP>(group);  // all have read the item's flag, and the last tile's maxima
         if (group_tid == 0) {
             ctl->stop[group] = *reinterpret_cast<volatile int *>(&ctl->dead);
-            if (t0 < t1) ctl->bad[group][(item - 1) % TILES_ITEMS] = 0;
+            if (t0 < t1) ctl->bad[group][(item - 1) % S::ITEMS] = 0;
         }
-        if (HALVES == 2) ctl->at.top[tid] = l;
+        if (HALVES == 2) ctl->at.top[0][tid] = l;
         group_sync<GROUP>(group);
         if (*reinterpret_cast<volatile int *>(&ctl->stop[group])) break;  // a wait gave up: this item is among what is lost
-        if (HALVES == 2) l += ctl->at.top[tid ^ 128];
+        if (HALVES == 2) l += ctl->at.top[0][tid ^ 128];
         const bool whole = item_whole(c);
         float *part = p.parts + (static_cast<int64_t>(blockIdx.x) * 2 + (c.first < begin ? 0 : 1)) * PART;
         const bool none = m == -CUDART_INF_F && l == 0.0f, fixed = none || any_bad;
@@ -1037,8 +1146,8 @@ __global__ void __launch_bounds__(TILES_THREADS, 1)
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     unsigned *err = p.error;
     if (tid == 0) {
-        for (int i = 0; i < 10; ++i) {
-            mbar_init(&ctl->full[i], 128);
+        for (int i = 0; i < S::STAGES; ++i) {
+            mbar_init(&ctl->full[i], 4);  // the loaders' warps
             mbar_init(&ctl->empty[i], 1);
         }
         for (int i = 0; i < 2; ++i) {
@@ -1048,7 +1157,7 @@ __global__ void __launch_bounds__(TILES_THREADS, 1)
             mbar_init(&ctl->q_full[i], TILES_PREPARE);
             mbar_init(&ctl->q_empty[i], 1 + 8);  // the products' end, and the row warps, who have read what lies beside q
             ctl->stop[i] = ctl->lost[i] = 0;
-            for (int k = 0; k < TILES_ITEMS; ++k) ctl->bad[i][k] = 0;
+            for (int k = 0; k < S::ITEMS; ++k) ctl->bad[i][k] = 0;
         }
         mbar_init(&ctl->spare, 1);
         ctl->dead = 0;
@@ -1061,7 +1170,7 @@ __global__ void __launch_bounds__(TILES_THREADS, 1)
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
-    if (c.at == c.end) {  // the whole block
+    if (c.at >= c.end) {  // the whole block
         if (warp == 8) tmem_free(ctl->tmem, 512);
         return;
     }
@@ -1079,11 +1188,8 @@ __global__ void __launch_bounds__(TILES_THREADS, 1)
             asm volatile("setmaxnreg.dec.sync.aligned.u32 96;");
         if (warp == 8) {
             tiles_multiply<C, D, PAIR>(p, c, smem, ctl, err, lane);
-            if (lane == 0) {  // what was issued ends before the block may: others may have given up on it
-                tc_commit(&ctl->spare);
-                mbar_drain(&ctl->spare, 0);
-            }
-            __syncwarp();
+            warp_commit(&ctl->spare);  // what was issued ends before the block may: others may have given up on it
+            mbar_drain(&ctl->spare, 0);
         } else {
             tiles_prepare<C, D, PAIR>(p, c, smem, ctl, err, tid - 288);
         }
