@@ -147,7 +147,8 @@ template <typename C, int D> struct MassShape {
 template <int ROWS, bool SCORED> struct MassCtl {
     uint64_t k_full[8], k_empty[8], s_full[MASS_BUFFERS], s_empty[MASS_BUFFERS], q_full[2], q_empty[2], spare;
     unsigned long long sees[2][ROWS];
-    alignas(16) int4 shape[2][SCORED ? ROWS : 1];  // position, first slot seen, slope
+    // position, first slot seen, slope, position less the first new token's
+    alignas(16) int4 shape[2][SCORED ? ROWS : 1];
     alignas(16) float2 row[2][ROWS];  // (read in pairs) what a unit of the stored q.k stands for, and the log-sum-exp, in powers of two
     int careful[2];       // number (from 1) of the last pass in which some row gives nothing: masks are then looked at everywhere
     uint32_t tmem;
@@ -350,11 +351,11 @@ __device__ void mass_prepare(const P &p, Cursor c, char *smem, Ctl *ctl, int lt)
                                     const int g = (r0 + r) % p.group;
                                     see = view.bits;
                                     int4 shape;
-                                    shape.x = p.sc.slot_pos ? __ldg(p.sc.slot_pos + (static_cast<int64_t>(c.b) * p.c.kv_heads + c.h) * p.sc.pos_stride + c.s.ctx + token[i])
-                                                            : c.s.ctx + view.depth;
+                                    const int32_t *pos = p.sc.slot_pos ? p.sc.slot_pos + (static_cast<int64_t>(c.b) * p.c.kv_heads + c.h) * p.sc.pos_stride + c.s.ctx : nullptr;
+                                    shape.x = pos ? __ldg(pos + token[i]) : c.s.ctx + view.depth;
                                     shape.y = view.lo;
                                     shape.z = __float_as_int(p.sc.slopes ? __ldg(p.sc.slopes + c.h * p.group + g) * LOG2E : 0.0f);
-                                    shape.w = 0;
+                                    shape.w = __float_as_int(static_cast<float>(shape.x - (pos ? __ldg(pos) : c.s.ctx)));
                                     ctl->shape[place][r] = shape;
                                 } else {
                                     see = visible_mask(parent, token[i]);
@@ -455,7 +456,11 @@ template <typename Shape, typename Ctl, typename P> __device__ long long mass_su
                 }
                 return j;
             };
-            int next_at = SCORED ? position_for(t0) : 0;
+            int next_at = SCORED ? position_for(t0) : 0, origin = c.s.ctx;  // the first new token's position
+            if constexpr (SCORED) {
+                if (moved_slots(p.sc) && c.s.fresh > 0)
+                    origin = __ldg(p.sc.slot_pos + (static_cast<int64_t>(c.b) * p.c.kv_heads + c.h) * p.sc.pos_stride + c.s.ctx);
+            }
             const int live = min(ROWS, count.rows - r0), place = unit_no & 1;
             bool careful = false;
             if (live > 0 && seen0 < t1) {
@@ -468,6 +473,7 @@ template <typename Shape, typename Ctl, typename P> __device__ long long mass_su
                 pg = page_for(tile + 1);
                 had = mass_for(tile + 1);
                 const int key_at = next_at;
+                const float key_rel = SCORED ? static_cast<float>(key_at - origin) : 0.0f;
                 if (SCORED) next_at = position_for(tile + 1);
                 float sum = 0.0f;
                 if (live > 0 && tile >= seen0) {
@@ -481,28 +487,47 @@ template <typename Shape, typename Ctl, typename P> __device__ long long mass_su
                         tc_ld16(y, quarter + (n % MASS_BUFFERS) * 128 + g);
                         const float4 *k = reinterpret_cast<const float4 *>(&ctl->row[place][g]);
                         if constexpr (SCORED) {
+                            // pairs of rows, so that one instruction works on two
                             const ScoresView &v = p.sc;
-                            float z[16];
+                            unsigned long long z[8], lse[8];
 #pragma unroll
-                            for (int i = 0; i < 16; ++i) z[i] = __uint_as_float(y[i]) * ctl->row[place][min(g + i, live - 1)].x;
-                            if (v.cap2 != 0.0f) cap_all(v, z);
+                            for (int i = 0; i < 8; ++i) {
+                                const float4 u = k[i];
+                                z[i] = mul2(pack2(__uint_as_float(y[2 * i]), __uint_as_float(y[2 * i + 1])), pack2(u.x, u.z));
+                                lse[i] = pack2(-u.y, -u.w);
+                            }
+                            if (v.cap2 != 0.0f) cap_pairs(v, z);
+                            if (v.slopes) {
 #pragma unroll
-                            for (int i = 0; i < 16; ++i) {
-                                const int r = min(g + i, live - 1);
-                                bool seen = g + i < live;
-                                if (v.slopes || masks) {
-                                    const int4 shape = ctl->shape[place][r];
-                                    const int far = shape.x - key_at;
-                                    if (v.slopes) z[i] = fmaf(-__int_as_float(shape.z), fabsf(static_cast<float>(far)), z[i]);
-                                    if (masks) {
-                                        const unsigned long long see = ctl->sees[place][r];
-                                        seen &= see != 0 && j >= shape.y &&
-                                                (j < c.s.ctx || (j < c.s.total && (see >> ((j - c.s.ctx) & 63) & 1)));
-                                        if (v.window > 0 && v.slot_pos && far >= v.window) seen = false;
+                                for (int i = 0; i < 8; ++i) {
+                                    const int4 a = ctl->shape[place][g + 2 * i], b = ctl->shape[place][g + 2 * i + 1];
+                                    const float2 x = unpair(z[i]);
+                                    z[i] = pack2(fmaf(-__int_as_float(a.z), fabsf(__int_as_float(a.w) - key_rel), x.x),
+                                                 fmaf(-__int_as_float(b.z), fabsf(__int_as_float(b.w) - key_rel), x.y));
+                                }
+                            }
+                            const bool some = g + 16 > live;  // some of these rows are not there
+#pragma unroll
+                            for (int i = 0; i < 8; ++i) {
+                                const float2 x = unpair(fadd2(z[i], lse[i]));
+                                float w[2] = {fast_exp2(x.x), fast_exp2(x.y)};
+                                if (masks || some) {
+#pragma unroll
+                                    for (int e = 0; e < 2; ++e) {
+                                        const int r = g + 2 * i + e;
+                                        bool seen = r < live;
+                                        if (masks && seen) {
+                                            const int4 shape = ctl->shape[place][r];
+                                            const unsigned long long see = ctl->sees[place][r];
+                                            seen = see != 0 && j >= shape.y &&
+                                                   (j < c.s.ctx || (j < c.s.total && (see >> ((j - c.s.ctx) & 63) & 1)));
+                                            if (v.window > 0 && v.slot_pos && shape.x - key_at >= v.window) seen = false;
+                                        }
+                                        if (!seen) w[e] = 0.0f;
                                     }
                                 }
-                                const float w = fast_exp2(z[i] - ctl->row[place][r].y);
-                                if (seen) s0 += w;
+                                s0 += w[0];
+                                s1 += w[1];
                             }
                         } else if (!masks) {
 #pragma unroll

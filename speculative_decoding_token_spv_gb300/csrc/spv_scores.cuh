@@ -65,6 +65,59 @@ template <int N> __device__ __forceinline__ void cap_all(const ScoresView &v, fl
     }
 }
 
+__device__ __forceinline__ float2 unpair(unsigned long long x)
+{
+    float2 y;
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(y.x), "=f"(y.y) : "l"(x));
+    return y;
+}
+// x f P((x f / cap)^2) of pairs, P of N coefficients.
+template <int M, int N> __device__ __forceinline__ void cap_polynomial(const ScoresView &v, unsigned long long (&x)[M], float f, const float (&c)[N])
+{
+    const float u = f * v.cap_inv;
+    const unsigned long long u2 = pack2(u, u);
+    unsigned long long k[N];
+#pragma unroll
+    for (int i = 0; i < N; ++i) k[i] = pack2(c[i] * f, c[i] * f);
+#pragma unroll
+    for (int i = 0; i < M; ++i) {
+        const unsigned long long y = mul2(x[i], u2), w = mul2(y, y);
+        unsigned long long t = k[N - 1];
+#pragma unroll
+        for (int j = N - 2; j >= 0; --j) t = ffma2(w, t, k[j]);
+        x[i] = mul2(x[i], t);
+    }
+}
+// The same of N pairs of products, whose scores are f times them.  Up to 1.25 of
+// the cap a polynomial of more terms serves all of them (2e-7 off): packed, its
+// ten operations for two scores cost less than two exponentials and reciprocals.
+template <int N> __device__ __forceinline__ void cap_pairs(const ScoresView &v, unsigned long long (&x)[N], float f = 1.0f)
+{
+    float large[2] = {0.0f, 0.0f};
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+        const float2 y = unpair(x[i]);
+        large[i & 1] = fmax3(large[i & 1], fabsf(y.x), fabsf(y.y));
+    }
+    const float edge = CAP_SMALL * v.cap2;
+    large[0] = fmaxf(large[0], large[1]) * fabsf(f);
+    if (__any_sync(0xffffffffu, large[0] >= 2.0f * edge)) {
+#pragma unroll
+        for (int i = 0; i < N; ++i) {
+            const float2 y = unpair(x[i]);
+            const float a = y.x * f, b = y.y * f;
+            x[i] = pack2(fabsf(a) >= edge ? capped_large(v, a) : capped_small(v, a), fabsf(b) >= edge ? capped_large(v, b) : capped_small(v, b));
+        }
+    } else if (__any_sync(0xffffffffu, large[0] >= edge)) {
+        constexpr float MEDIUM[8] = {0.999999929f, -0.333327294f, 0.133248116f, -0.0535018186f, 0.0205778305f, -0.006815299f, 0.00159693103f,
+                                     -0.000184196065f};
+        cap_polynomial(v, x, f, MEDIUM);
+    } else {
+        constexpr float SMALL[5] = {CAP_0, CAP_1, CAP_2, CAP_3, CAP_4};
+        cap_polynomial(v, x, f, SMALL);
+    }
+}
+
 // Lengths of a sequence, with the first slot that any of its new tokens can
 // see, and the one from which on all of them see all cached slots.
 struct SpanLens : SeqLens {

@@ -20,10 +20,11 @@
 //   * else 128 rows, of which two warps share each row's keys (few rows; and D =
 //     256, whose outputs take half of tensor memory).  Scores stand in two
 //     places in turn;
-//   * a warp issues the products, three bring q, four K and V in turn into one
-//     ring, a box a page by the copy engine, or row by row (small pages; a
-//     sequence's last tile of V, whose slots past the end become zero; e4m3,
-//     which lands as it is and is widened to f16 by the threads that loaded it).
+//   * one warp works out the items, one issues the products, two bring q, four K
+//     and V in turn into one ring, a box a page by the copy engine, or row by row
+//     (small pages; a sequence's last tile of V, whose slots past the end become
+//     zero).  e4m3 lands as it is and is widened to f16 by the warp that asked for
+//     it.
 // O is only rescaled when a maximum has grown by more than 2^8 (2^7 for f16).
 // The blocks' pieces of an item that they share are joined by a dependent
 // launch, in their order.
@@ -45,7 +46,7 @@ namespace spv {
 
 constexpr int TILES_THREADS = 512;
 constexpr int TILES_WARPS = TILES_THREADS / 32;
-constexpr int TILES_PREPARE = 96;  // threads that bring q
+constexpr int TILES_PREPARE = 64;  // threads that bring q
 
 struct TilesParams : ScoredParams {
     int32_t *timeouts;  // row_status, for waits that gave up
@@ -61,8 +62,8 @@ template <typename C, int D, bool PAIR> struct TilesShape {
     static constexpr int Q_SUB = 128 * D * 2, Q = SUBS * Q_SUB;
     static constexpr int Q_PLACES = !WIDEN && 2 * Q <= 64 * 1024 ? 2 : 1;
     static constexpr int ROOM = 224 * 1024 - Q_PLACES * Q;
-    static constexpr int RAW_STAGES = WIDEN ? 32 * 1024 / RAW : 0;
-    static constexpr int FIT = (ROOM - RAW_STAGES * RAW) / TILE, STAGES = FIT < 10 ? FIT : 10;
+    static constexpr int RAW_STAGES = !WIDEN ? 0 : (PAIR || D == 256 ? 32 : 48) * 1024 / RAW;
+    static constexpr int FIT = (ROOM - RAW_STAGES * RAW) / TILE, MOST = WIDEN ? 8 : 10, STAGES = FIT < MOST ? FIT : MOST;
     static constexpr int K_AT = Q_PLACES * Q, RAW_AT = K_AT + STAGES * TILE, CTL_AT = RAW_AT + RAW_STAGES * RAW;
     static constexpr int ITEMS = (STAGES + RAW_STAGES) / 2 + 3;  // whose flags can be in use at once: an item has two tiles at least
     static constexpr int GROUP = PAIR ? 128 : 256;               // threads that belong to the same rows
@@ -74,20 +75,34 @@ struct TileLens : SeqLens {
 };
 using TileCursor = CursorOf<TileLens>;
 
+// What the block has of an item, as one warp works it out and passes it to the others.
+struct alignas(16) TileItem {
+    int b, row_tile, h, flags;
+    int ctx, fresh, total, t0;
+    int t1, lo0, hi0, lo1;
+    int hi1, pad[3];
+};
+enum TileFlags { ITEM_BAD = 1, ITEM_WHOLE = 2, ITEM_SECOND = 4, ITEM_END = 8 };  // ITEM_SECOND: a piece goes to the block's second place
+
 template <typename S> struct TilesCtl {
-    uint64_t full[S::STAGES], empty[S::STAGES], s_full[2], p_full[2], o_done[2], q_full[2], q_empty[2], spare;
-    TileCursor start;
-    char bad[2][S::ITEMS];                                    // a page id outside the pool, for each group of row warps
+    TileItem items[2];
+    uint64_t item_full[2], item_empty[2];
+    uint64_t full[S::STAGES], empty[S::STAGES], s_full[2], p_half[2], p_full[2], o_done[2], q_full[2], q_empty[2], spare;
+    uint64_t raw_full[S::WIDEN ? 4 : 1][S::WIDEN ? S::RAW_STAGES : 1];  // of each loader warp's rows
+    char bad[2][S::ITEMS];                                       // a page id outside the pool, for each group of row warps
     int stop[2], lost[2];
-    alignas(16) int positions[2][S::MINE];                       // of moved slots: of a tile's keys, for each four row warps
     uint32_t tmem;
     int dead;
     union {
         struct {
-            long long sums[TILES_WARPS];                         // before the roles begin
-        } find;
+            TileCursor start;
+            long long sums[TILES_WARPS];
+        } find;                                                  // before the roles begin
         struct {
-            signed char depth[S::Q_PLACES][S::SUBS == 1 ? 64 : 1];         // trees: per place of q the depth of each new token
+            union {
+                alignas(16) int positions[2][S::MINE];           // of moved slots: of a tile's keys, for each four row warps
+                signed char depth[S::Q_PLACES][S::SUBS == 1 ? 64 : 1];  // else, of trees: per place of q the depth of each new token
+            };
             float top[2][S::SUBS == 1 ? 256 : 1];                // maxima of the two halves, of a tile and the next; sums
             signed char q_power[S::WIDEN ? S::Q_PLACES * S::ROWS : 1];  // e4m3: the rows of q are stored times 2^q_power
         } at;
@@ -251,7 +266,7 @@ template <typename S> __device__ TileCursor tiles_find(const TilesParams &p, Til
                     c.h = static_cast<int>(quotient(c.at - before, tiles + TILES_OVERHEAD));
                     c.first = before + static_cast<long long>(c.h) * (tiles + TILES_OVERHEAD) + TILES_OVERHEAD;
                     if (c.at < c.first) c.at = c.first < c.end ? c.first : c.end;
-                    if (lane == 0) ctl->start = c;
+                    if (lane == 0) ctl->find.start = c;
                     break;
                 }
                 before += static_cast<long long>(__shfl_sync(0xffffffffu, upto, 31)) * p.c.kv_heads;
@@ -260,10 +275,41 @@ template <typename S> __device__ TileCursor tiles_find(const TilesParams &p, Til
     }
     __syncthreads();
     if (block < c.blocks) {
-        c = ctl->start;
+        c = ctl->find.start;
         c.s = item_tiles<S>(p, tiles_lens(p, c.b), c.b, c.row_tile, lane);
     }
-    __syncthreads();  // the sums' place is free
+    __syncthreads();  // this place is free
+    return c;
+}
+// The same by one warp, slowly, for what is seldom done at a range's end.
+template <typename S> __device__ __noinline__ TileCursor tiles_find_again(const TilesParams &p, int lane)
+{
+    TileCursor c{};
+    long long before = 0;
+    const int entries = p.w.B * p.w.row_tiles;
+    for (int pass = 0; pass < 2; ++pass) {
+        before = 0;
+        for (int e = 0; e < entries; ++e) {
+            c.b = e / p.w.row_tiles;
+            c.row_tile = e - c.b * p.w.row_tiles;
+            c.s = item_tiles<S>(p, tiles_lens(p, c.b), c.b, c.row_tile, lane);
+            c.tiles = count_of(c.s);
+            const long long units = static_cast<long long>(c.tiles + TILES_OVERHEAD) * p.c.kv_heads;
+            if (pass == 1 && before + units > c.at) break;
+            before += units;
+        }
+        if (pass == 0) {
+            c.all = before;
+            c.blocks = c.all < gridDim.x ? static_cast<int>(c.all) : static_cast<int>(gridDim.x);
+            c.part = quotient(c.all, c.blocks);
+            c.more = static_cast<int>(c.all - c.part * c.blocks);
+            c.at = range_begin(c, blockIdx.x);
+            c.end = range_begin(c, blockIdx.x + 1);
+        }
+    }
+    c.h = static_cast<int>(quotient(c.at - before, c.tiles + TILES_OVERHEAD));
+    c.first = before + static_cast<long long>(c.h) * (c.tiles + TILES_OVERHEAD) + TILES_OVERHEAD;
+    if (c.at < c.first) c.at = c.first < c.end ? c.first : c.end;
     return c;
 }
 // To the next item; a whole warp.
@@ -296,10 +342,52 @@ template <int ROWS> __device__ __forceinline__ uint32_t tile_at(int row, int chu
     return (chunk >> 3) * (ROWS * 128) + row * 128 + (((chunk & 7) ^ (row & 7)) << 4);
 }
 
+// ------------------------------------------------------------------ items
+// One warp works out the block's items, two ahead of the others, and notes the
+// shared ones.  (Each role by itself, the next item's lengths, spans and
+// divisions took all of them thousands of cycles, much of it fetching the code.)
+template <typename S> __device__ void tiles_items(const TilesParams &p, TileCursor c, TilesCtl<S> *ctl, unsigned *err, int lane)
+{
+    const long long begin = c.at;
+    int k = 0;
+    for (;; tiles_next<S>(c, p, lane), ++k) {
+        const bool end = c.at >= c.end;
+        if (k >= 2 && !tiles_wait(ctl, &ctl->item_empty[k & 1], (k / 2 - 1) & 1, err)) return;
+        if (lane == 0) {
+            TileItem &it = ctl->items[k & 1];
+            it.b = c.b, it.row_tile = c.row_tile, it.h = c.h;
+            it.flags = end ? ITEM_END : (c.s.bad ? ITEM_BAD : 0) | (item_whole(c) ? ITEM_WHOLE : 0) | (c.first < begin ? 0 : ITEM_SECOND);
+            it.ctx = c.s.ctx, it.fresh = c.s.fresh, it.total = c.s.total;
+            it.t0 = tiles_first(c), it.t1 = tiles_last(c);
+            it.lo0 = c.s.lo[0], it.hi0 = c.s.hi[0], it.lo1 = c.s.lo[1], it.hi1 = c.s.hi[1];
+            mbar_arrive(&ctl->item_full[k & 1]);
+            if (!end && !item_whole(c))
+                note_split(p, c, AttRows{c.b, c.h, c.row_tile * S::ROWS, min(S::ROWS, p.rows - c.row_tile * S::ROWS)}, begin, 0);
+        }
+        __syncwarp();
+        if (end) return;
+    }
+}
+// The block's item k, for a whole warp; false at the end, or after a wait gave up.
+constexpr int TILES_TAKERS = 8 + 1 + 2 + 4;  // warps that take every item
+template <typename Ctl> __device__ __forceinline__ bool take_item(Ctl *ctl, int k, TileItem *it, unsigned *err, int lane)
+{
+    if (!tiles_wait(ctl, &ctl->item_full[k & 1], (k >> 1) & 1, err)) return false;
+    const int4 *from = reinterpret_cast<const int4 *>(&ctl->items[k & 1]);
+    const int4 x = from[0], y = from[1], z = from[2];
+    it->b = x.x, it->row_tile = x.y, it->h = x.z, it->flags = x.w;
+    it->ctx = y.x, it->fresh = y.y, it->total = y.z, it->t0 = y.w;
+    it->t1 = z.x, it->lo0 = z.y, it->hi0 = z.z, it->lo1 = z.w;
+    it->hi1 = from[3].x;
+    __syncwarp();
+    if (lane == 0) mbar_arrive(&ctl->item_empty[k & 1]);
+    return !(it->flags & ITEM_END);
+}
+
 // ------------------------------------------------------------------ K and V
-// Four warps: tiles of K and V in turn.
+// Four warps: tiles of K and V in turn, each warp a quarter of their slots.
 template <typename C, int D, bool PAIR, typename S = TilesShape<C, D, PAIR>>
-__device__ void tiles_load(const TilesParams &p, TileCursor c, char *smem, TilesCtl<S> *ctl, unsigned *err, int lt,
+__device__ void tiles_load(const TilesParams &p, char *smem, TilesCtl<S> *ctl, unsigned *err, int lt,
                            const CUtensorMap *map_k, const CUtensorMap *map_v)
 {
     constexpr int CH = D * static_cast<int>(sizeof(C)) / 16, RPI = 32 / CH, NST = S::STAGES, KEYS = S::KEYS, WARP_ROWS = KEYS / 4;
@@ -307,18 +395,37 @@ __device__ void tiles_load(const TilesParams &p, TileCursor c, char *smem, Tiles
     const int lane = lt & 31, w = lt >> 5, chunk = lane % CH, sub = lane / CH;
     const uint32_t base = smem_u32(smem);
     const int mask = (1 << p.c.page_shift) - 1;
-    int n = 0, item = 0;  // tiles of K and V so far, items with tiles
+    int st = 0, pass = 1, filled = 0;  // the ring's place of the next tile, and the parity of its being free (at first it is); places filled
+    int raw = 0, waiting = 0;          // e4m3: the place of the next raw tile; raw tiles not widened yet
+    int rows[RST];          // e4m3: slots of this warp that exist, of the raw tiles in turn
+    bool ok = true;
+    auto flag = [&](int flags) {
+        *reinterpret_cast<volatile char *>(&ctl->bad[0][flags]) = *reinterpret_cast<volatile char *>(&ctl->bad[1][flags]) = 1;
+    };
+    auto free_place = [&]() { return tiles_wait(ctl, &ctl->empty[st], pass, err); };
+    auto step = [&]() {
+        if (++st == NST) st = 0, pass ^= 1;
+        if (filled < NST) ++filled;
+    };
 
-    // e4m3: widens tile t, whose copies have landed; each thread what it has loaded.
-    auto widen = [&](int t) -> bool {
-        const int st = t % NST;
-        if (t >= NST && !tiles_wait(ctl, &ctl->empty[st], (t / NST - 1) & 1, err)) return false;
-        const char *raw = smem + S::RAW_AT + (t % RST) * S::RAW;
+    // e4m3: widens the oldest raw tile, each warp the rows that it brought; `place` of raw ones, passing parity.
+    int oldest = 0, oldest_pass = 0;
+    auto widen = [&]() -> bool {
+        if (map_k) {
+            if (!tiles_wait(ctl, &ctl->raw_full[S::WIDEN ? w : 0][oldest], oldest_pass, err)) return false;
+        } else {
+            asm volatile("cp.async.wait_all;" ::: "memory");
+            __syncwarp();
+        }
+        if (!free_place()) return false;
+        const char *from = smem + S::RAW_AT + oldest * S::RAW;
         char *to = smem + S::K_AT + st * S::TILE;
+        const int there = rows[0];
 #pragma unroll 4
         for (int i = 0; i < WARP_ROWS / RPI; ++i) {
-            const int row = WARP_ROWS * w + i * RPI + sub;
-            const uint4 x = *reinterpret_cast<const uint4 *>(raw + row * D + chunk * 16);
+            const int r = i * RPI + sub, row = WARP_ROWS * w + r;
+            uint4 x = *reinterpret_cast<const uint4 *>(from + row * D + chunk * 16);
+            if (r >= there) x = make_uint4(0, 0, 0, 0);  // behind the sequence's end: anything
             const uint32_t b[4] = {x.x, x.y, x.z, x.w};
             uint32_t y[8];
 #pragma unroll
@@ -334,98 +441,124 @@ __device__ void tiles_load(const TilesParams &p, TileCursor c, char *smem, Tiles
         fence_async_shared();
         __syncwarp();
         if (lane == 0) mbar_arrive(&ctl->full[st]);
+        step();
+        if (++oldest == RST) oldest = 0, oldest_pass ^= 1;
+        --waiting;
+#pragma unroll
+        for (int i = 0; i + 1 < RST; ++i) rows[i] = rows[i + 1];
         return true;
     };
-    bool ok = true;
-    for (; ok && c.at < c.end; tiles_next<S>(c, p, lane)) {
-        const int t0 = tiles_first(c), t1 = tiles_last(c);
+
+    TileItem it;
+    int item = 0;
+    for (int k = 0; ok && take_item(ctl, k, &it, err, lane); ++k) {
+        const int t0 = it.t0, t1 = it.t1;
         if (t0 == t1) continue;
-        const int32_t *table = p.c.table + static_cast<int64_t>(c.b) * p.c.max_pages;
-        const int flags = item++ % S::ITEMS;
-        auto lookup = [&](int tile) {  // the page id of this lane's row of a tile, unchecked; -1: no such row
-            const int j = tile * KEYS + WARP_ROWS * w + lane;
-            return lane < WARP_ROWS && tile < t1 && j < c.s.total ? __ldg(table + (j >> p.c.page_shift)) : -1;
+        const int32_t *table = p.c.table + static_cast<int64_t>(it.b) * p.c.max_pages;
+        const int flags = item;
+        if (++item == S::ITEMS) item = 0;
+        // With maps each warp asks the copy engine for its slots: a box a page (or what the warp has of a larger one), of 64
+        // elements, or e4m3's whole rows; a lane each.  (A lane's takes 80 to 100 cycles: from one warp, 16 of a tile of K
+        // and 16 of V took longer than the tile's products.)
+        constexpr int PANELS = S::WIDEN ? 1 : D / 64;
+        const int box_slots = min(mask + 1, S::WIDEN ? WARP_ROWS : KEYS);
+        const int boxes = S::WIDEN ? WARP_ROWS / box_slots : KEYS / box_slots * PANELS;
+        const int quarter = S::WIDEN ? boxes : max(1, boxes >> 2), box = S::WIDEN ? lane : w * quarter + lane;
+        const int boxes_here = max(0, min(quarter, S::WIDEN ? boxes : boxes - w * quarter));
+        const bool asks = map_k && lane < boxes_here;
+        const int box_slot = (S::WIDEN ? WARP_ROWS * w : 0) + box / PANELS * box_slots;
+        auto lookup = [&](int tile) {  // the page id of this lane's box or row of a tile, unchecked; -1: no such row
+            const int j = tile * KEYS + (map_k ? box_slot : WARP_ROWS * w + lane);
+            return (map_k ? asks : lane < WARP_ROWS) && tile < t1 && j < it.total ? __ldg(table + (j >> p.c.page_shift)) : -1;
         };
-        // With maps each warp asks the copy engine for a quarter of the boxes: a page (or what a tile holds of a larger one)
-        // by 64 elements, from a lane each.  (A lane's takes 80 to 100 cycles: from one warp, 16 of a tile of K and 16 of V
-        // took longer than the tile's products.)
-        const int box_slots = min(mask + 1, KEYS), boxes = map_k ? KEYS / box_slots * (D / 64) : 0, quarter = max(1, boxes >> 2);
-        const int box = w * quarter + lane, boxes_here = max(0, min(quarter, boxes - w * quarter));
-        const bool asks = lane < boxes_here;
-        auto box_lookup = [&](int tile) {
-            const int j = tile * KEYS + box / (D / 64) * box_slots;
-            return asks && tile < t1 && j < c.s.total ? __ldg(table + (j >> p.c.page_shift)) : -1;
-        };
-        int next = map_k ? box_lookup(t0) : lookup(t0);
+        int next = lookup(t0);
         for (int tile = t0; ok && tile < t1; ++tile) {
             const int j0 = tile * KEYS, page = next;
-            next = map_k ? box_lookup(tile + 1) : lookup(tile + 1);
+            next = lookup(tile + 1);
 #pragma unroll 1
-            for (int kv = 0; kv < 2; ++kv, ++n) {
+            for (int kv = 0; kv < 2; ++kv) {
                 const PoolView &pool = kv ? p.c.v : p.c.k;
-                const int st = n % NST;
-                if (map_k && (!kv || j0 + KEYS <= c.s.total)) {
-                    const int slot = j0 + box / (D / 64) * box_slots;
-                    if (asks && slot < c.s.total && static_cast<unsigned>(page) >= static_cast<unsigned>(p.c.num_pages))
-                        *reinterpret_cast<volatile char *>(&ctl->bad[0][flags]) = *reinterpret_cast<volatile char *>(&ctl->bad[1][flags]) = 1;
-                    if (n >= NST && !(ok = tiles_wait(ctl, &ctl->empty[st], (n / NST - 1) & 1, err))) break;
-                    if (lane == 0) mbar_arrive_expect_tx(&ctl->full[st], boxes_here * box_slots * 128);
-                    __syncwarp();
-                    if (asks)
-                        tma_box(base + S::K_AT + st * S::TILE + (box % (D / 64)) * (KEYS * 128) + box / (D / 64) * box_slots * 128,
-                                kv ? map_v : map_k, (box % (D / 64)) * 64, slot & mask, c.h, page, &ctl->full[st]);
-                    __syncwarp();
-                    continue;
-                }
-                int pg = map_k ? lookup(tile) : page;
-                if (static_cast<unsigned>(pg) >= static_cast<unsigned>(p.c.num_pages)) {
-                    if (lane < WARP_ROWS && j0 + WARP_ROWS * w + lane < c.s.total)
-                        *reinterpret_cast<volatile char *>(&ctl->bad[0][flags]) = *reinterpret_cast<volatile char *>(&ctl->bad[1][flags]) = 1;
-                    pg = -1;
-                }
-                const int64_t mine = pg < 0 ? -1 : pg * pool.page_stride + ((j0 + WARP_ROWS * w + lane) & mask) * pool.slot_stride;
-                const char *from = pool.base + c.h * pool.head_stride + chunk * 16;
-                uint32_t to;
-                if (S::WIDEN) {  // the raw stages are each thread's own
-                    if (n >= RST) {
-                        cp_async_wait<RST - 1>();
-                        if (!(ok = widen(n - RST))) break;
+                if (S::WIDEN && waiting == RST && !(ok = widen())) break;
+                if (map_k && (S::WIDEN || !kv || j0 + KEYS <= it.total)) {
+                    const int slot = j0 + box_slot;
+                    if (asks && slot < it.total && static_cast<unsigned>(page) >= static_cast<unsigned>(p.c.num_pages)) flag(flags);
+                    uint64_t *bar;
+                    uint32_t to;
+                    if constexpr (S::WIDEN) {
+                        bar = &ctl->raw_full[w][raw];
+                        to = base + S::RAW_AT + raw * S::RAW + box_slot * D;
+                        fence_async_shared();  // its last bytes have been read
+                        __syncwarp();
+                    } else {
+                        if (!(ok = free_place())) break;
+                        bar = &ctl->full[st];
+                        to = base + S::K_AT + st * S::TILE + (box % PANELS) * (KEYS * 128) + box / PANELS * box_slots * 128;
                     }
-                    to = base + S::RAW_AT + (n % RST) * S::RAW;
-                } else {
-                    if (n >= NST && !(ok = tiles_wait(ctl, &ctl->empty[st], (n / NST - 1) & 1, err))) break;
-                    to = base + S::K_AT + st * S::TILE;
-                }
-#pragma unroll 2
-                for (int i = 0; i < WARP_ROWS / RPI; ++i) {
-                    const int row = WARP_ROWS * w + i * RPI + sub;
-                    const int64_t at = __shfl_sync(0xffffffffu, mine, i * RPI + sub);
-                    cp_async16_zfill(to + (S::WIDEN ? row * D + chunk * 16 : tile_at<KEYS>(row, chunk)), at < 0 ? pool.base : from + at,
-                                     at < 0 ? 0 : 16);
-                }
-                if (S::WIDEN) {
-                    cp_async_commit();
-                } else {  // the fence for the tensor cores is the writers': in the products' warp it took a thousand cycles a tile
-                    asm volatile("cp.async.wait_all;" ::: "memory");
-                    fence_async_shared();
+                    if (lane == 0) mbar_arrive_expect_tx(bar, boxes_here * box_slots * (S::WIDEN ? D : 128));
                     __syncwarp();
-                    if (lane == 0) mbar_arrive(&ctl->full[st]);
+                    if (asks) tma_box(to, kv ? map_v : map_k, S::WIDEN ? 0 : (box % PANELS) * 64, slot & mask, it.h, page, bar);
+                    __syncwarp();
+                } else {
+                    int pg = page;
+                    if (map_k) {  // the last tile of V by rows: slots behind the end become zero
+                        const int j = j0 + WARP_ROWS * w + lane;
+                        pg = lane < WARP_ROWS && j < it.total ? __ldg(table + (j >> p.c.page_shift)) : -1;
+                    }
+                    if (static_cast<unsigned>(pg) >= static_cast<unsigned>(p.c.num_pages)) {
+                        if (lane < WARP_ROWS && j0 + WARP_ROWS * w + lane < it.total) flag(flags);
+                        pg = -1;
+                    }
+                    const int64_t mine = pg < 0 ? -1 : pg * pool.page_stride + ((j0 + WARP_ROWS * w + lane) & mask) * pool.slot_stride;
+                    const char *from = pool.base + it.h * pool.head_stride + chunk * 16;
+                    if (!S::WIDEN && !(ok = free_place())) break;
+                    const uint32_t to = base + (S::WIDEN ? S::RAW_AT + raw * S::RAW : S::K_AT + st * S::TILE);
+#pragma unroll 2
+                    for (int i = 0; i < WARP_ROWS / RPI; ++i) {
+                        const int row = WARP_ROWS * w + i * RPI + sub;
+                        const int64_t at = __shfl_sync(0xffffffffu, mine, i * RPI + sub);
+                        cp_async16_zfill(to + (S::WIDEN ? row * D + chunk * 16 : tile_at<KEYS>(row, chunk)), at < 0 ? pool.base : from + at,
+                                         at < 0 ? 0 : 16);
+                    }
+                    if (!S::WIDEN) {  // the fence for the tensor cores is the writers'
+                        asm volatile("cp.async.wait_all;" ::: "memory");
+                        fence_async_shared();
+                        __syncwarp();
+                        if (lane == 0) mbar_arrive(&ctl->full[st]);
+                    }
+                }
+                if constexpr (S::WIDEN) {
+                    rows[0] = waiting == 0 ? it.total - j0 - WARP_ROWS * w : rows[0];
+#pragma unroll
+                    for (int i = 1; i < RST; ++i) rows[i] = waiting == i ? it.total - j0 - WARP_ROWS * w : rows[i];
+                    ++waiting;
+                    if (++raw == RST) raw = 0;
+                } else {
+                    step();
                 }
             }
         }
     }
+    if (S::WIDEN)  // the tiles still on their way
+        while (ok && waiting > 0) ok = widen();
     asm volatile("cp.async.wait_all;" ::: "memory");
-    if (S::WIDEN) {  // the tiles still on their way
-        for (int t = n >= RST ? n - RST : 0; ok && t < n; ++t) ok = widen(t);
-    } else if (map_k) {  // the copy engine's, before the block may end: nobody else may have waited for them
-        for (int t = max(0, n - NST); t < n; ++t) mbar_drain(&ctl->full[t % NST], (t / NST) & 1);
+    // the copy engine's, before the block may end: nobody else may have waited for them
+    if (map_k && S::WIDEN) {
+        for (; waiting > 0; --waiting) {
+            mbar_drain(&ctl->raw_full[S::WIDEN ? w : 0][oldest], oldest_pass);
+            if (++oldest == RST) oldest = 0, oldest_pass ^= 1;
+        }
+    } else if (map_k) {
+        for (; filled > 0; --filled) {
+            if (--st < 0) st = NST - 1, pass ^= 1;
+            mbar_drain(&ctl->full[st], pass ^ 1);
+        }
     }
 }
 
 // ------------------------------------------------------------------ products
 // One warp.
 template <typename C, int D, bool PAIR, typename S = TilesShape<C, D, PAIR>>
-__device__ void tiles_multiply(const TilesParams &p, TileCursor c, char *smem, TilesCtl<S> *ctl, unsigned *err, int lane)
+__device__ void tiles_multiply(char *smem, TilesCtl<S> *ctl, unsigned *err, int lane)
 {
     constexpr bool BF16 = std::is_same<C, __nv_bfloat16>::value;
     constexpr uint32_t QK = mma_shape(BF16, false, S::KEYS), PV = mma_shape(BF16, true, D);
@@ -435,10 +568,10 @@ __device__ void tiles_multiply(const TilesParams &p, TileCursor c, char *smem, T
     int st = 0, phase = 0;             // the ring's place and pass of the next tile of K; V's is the one behind it
     int item = 0, buf = 0;
     uint32_t passes = 0;               // bit s: parity of the weights' barrier of place s
-    bool ok = true;
     auto after = [&](int x) { return x + 1 == NST ? 0 : x + 1; };
-    for (; ok && c.at < c.end; tiles_next<S>(c, p, lane)) {
-        const int t0 = same_in_warp(tiles_first(c)), tiles = same_in_warp(tiles_last(c)) - t0;
+    TileItem it;
+    for (int k = 0; take_item(ctl, k, &it, err, lane); ++k) {
+        const int t0 = same_in_warp(it.t0), tiles = same_in_warp(it.t1) - t0;
         if (tiles == 0) continue;
         const int place = S::Q_PLACES == 1 ? 0 : item & 1;
         if (!tiles_wait(ctl, &ctl->q_full[place], (item / S::Q_PLACES) & 1, err)) return;
@@ -454,35 +587,40 @@ __device__ void tiles_multiply(const TilesParams &p, TileCursor c, char *smem, T
             warp_commit(&ctl->s_full[s]);
         };
         auto outputs = [&](int s, int v_st, bool add, bool done) {
-            tc_fence_after();
             const uint32_t o = tmem + 256 + (PAIR ? s * 128 : 0), v = desc_low(base + S::K_AT + v_st * S::TILE, KEYS * 128);
+            // PAIR: the first half of the weights is there before the second
+            if (!tiles_wait(ctl, PAIR ? &ctl->p_half[s] : &ctl->p_full[s], passes >> s & 1, err)) return false;
+            tc_fence_after();
 #pragma unroll
-            for (int ks = 0; ks < KEYS / 16; ++ks)
+            for (int ks = 0; ks < KEYS / 16; ++ks) {
+                if (PAIR && ks == KEYS / 32) {
+                    if (!tiles_wait(ctl, &ctl->p_full[s], passes >> s & 1, err)) return false;
+                    tc_fence_after();
+                }
                 warp_mma_ta<PV>(o, tmem + s * 128 + 16 * ks / S::MINE * S::MINE + 16 * ks % S::MINE / 2, v + ks * (2048 >> 4),
                                 add || ks > 0);
+            }
+            passes ^= 1u << s;
             if (done) warp_commit(&ctl->o_done[s]);
+            return true;
         };
         auto full = [&](int place, int pass) { return tiles_wait(ctl, &ctl->full[place], pass, err); };
         if constexpr (PAIR) {
-            const int lo0 = same_in_warp(c.s.lo[0]), hi0 = same_in_warp(c.s.hi[0]), lo1 = same_in_warp(c.s.lo[1]), hi1 = same_in_warp(c.s.hi[1]);
+            const int lo0 = same_in_warp(it.lo0), hi0 = same_in_warp(it.hi0), lo1 = same_in_warp(it.lo1), hi1 = same_in_warp(it.hi1);
             bool begun0 = false, begun1 = false, pending0 = false, pending1 = false;
             int v_st = 0, v_pass = 0;
             for (int i = 0; i <= tiles; ++i) {  // the outputs of the tile before, and the scores of this one
                 const bool keys = i < tiles;
                 const bool here0 = keys && t0 + i >= lo0 && t0 + i < hi0, here1 = keys && t0 + i >= lo1 && t0 + i < hi1;
-                if (i > 0 && !(ok = full(v_st, v_pass))) return;
+                if (i > 0 && !full(v_st, v_pass)) return;
                 if (pending0) {
-                    if (!(ok = tiles_wait(ctl, &ctl->p_full[0], passes & 1, err))) return;
-                    passes ^= 1;
-                    outputs(0, v_st, begun0, !here0);
+                    if (!outputs(0, v_st, begun0, !here0)) return;
                     begun0 = true;
                 }
-                if (keys && !(ok = full(st, phase))) return;
+                if (keys && !full(st, phase)) return;
                 if (here0) scores(0, st);
                 if (pending1) {
-                    if (!(ok = tiles_wait(ctl, &ctl->p_full[1], passes >> 1 & 1, err))) return;
-                    passes ^= 2;
-                    outputs(1, v_st, begun1, !here1);
+                    if (!outputs(1, v_st, begun1, !here1)) return;
                     begun1 = true;
                 }
                 if (i > 0) warp_commit(&ctl->empty[v_st]);
@@ -504,15 +642,13 @@ __device__ void tiles_multiply(const TilesParams &p, TileCursor c, char *smem, T
             for (int i = 0; i < tiles + 2; ++i) {  // the outputs of the tile two before, and the scores of this one
                 const int s = buf;
                 if (i >= 2) {
-                    if (!(ok = full(v_st[0], v_pass[0]))) return;
-                    if (!(ok = tiles_wait(ctl, &ctl->p_full[s], passes >> s & 1, err))) return;
-                    passes ^= 1u << s;
-                    outputs(s, v_st[0], i > 2, true);
+                    if (!full(v_st[0], v_pass[0])) return;
+                    if (!outputs(s, v_st[0], i > 2, true)) return;
                     warp_commit(&ctl->empty[v_st[0]]);
                 }
                 v_st[0] = v_st[1], v_pass[0] = v_pass[1];
                 if (i < tiles) {
-                    if (!(ok = full(st, phase))) return;
+                    if (!full(st, phase)) return;
                     scores(s, st);
                     warp_commit(&ctl->empty[st]);
                     st = after(st);
@@ -530,36 +666,44 @@ __device__ void tiles_multiply(const TilesParams &p, TileCursor c, char *smem, T
 }
 
 // ------------------------------------------------------------------ q
-// Three warps, an item ahead of the others where there is room: q, and of trees
-// what the new tokens see.
+// Two warps, an item ahead of the others where there is room: q, and of trees
+// the depths of the new tokens.
 template <typename C, int D, bool PAIR, typename S = TilesShape<C, D, PAIR>>
-__device__ void tiles_prepare(const TilesParams &p, TileCursor c, char *smem, TilesCtl<S> *ctl, unsigned *err, int lt)
+__device__ void tiles_prepare(const TilesParams &p, char *smem, TilesCtl<S> *ctl, unsigned *err, int lt)
 {
     const int lane = lt & 31;
     const uint32_t base = smem_u32(smem);
+    constexpr int CH = D / 8, STEP = TILES_PREPARE / CH;  // rows at a time
+    const int ch = lt % CH, first = lt / CH;
+    const int step_t = STEP / p.group, step_g = STEP - step_t * p.group;
+    const int64_t token = static_cast<int64_t>(p.q_heads) * D * 2;
+    TileItem it;
     int item = 0;
-    for (; c.at < c.end; tiles_next<S>(c, p, lane)) {
-        if (tiles_first(c) == tiles_last(c)) continue;
+    for (int k = 0; take_item(ctl, k, &it, err, lane); ++k) {
+        if (it.t0 == it.t1) continue;
         if (item == p.give_up.item && static_cast<int>(blockIdx.x) == p.give_up.block) {  // the self-test
             *reinterpret_cast<volatile int *>(&ctl->dead) = 1;
             atomicExch(err, static_cast<unsigned>(STATUS_TIMEOUT));
             return;
         }
-        const int place = item % S::Q_PLACES, row0 = c.row_tile * S::ROWS, live = min(S::ROWS, p.rows - row0);
+        const int place = item % S::Q_PLACES, row0 = it.row_tile * S::ROWS, live = min(S::ROWS, p.rows - row0);
         if (item >= S::Q_PLACES && !tiles_wait(ctl, &ctl->q_empty[place], (item / S::Q_PLACES - 1) & 1, err)) return;
         if constexpr (!PAIR) {
-            if (p.parent && p.sc.slopes)
-                for (int t = lt; t < c.s.fresh; t += TILES_PREPARE)
+            if (p.parent && p.sc.slopes && !p.sc.slot_pos)
+                for (int t = lt; t < it.fresh; t += TILES_PREPARE) {
+                    SeqLens s{it.ctx, it.fresh, it.total, false};
                     ctl->at.depth[place][t] =
-                        static_cast<signed char>(token_view(p.sc, p.parent + static_cast<int64_t>(c.b) * p.w.T, c.s, c.b, p.w.T, t).depth);
+                        static_cast<signed char>(token_view(p.sc, p.parent + static_cast<int64_t>(it.b) * p.w.T, s, it.b, p.w.T, t).depth);
+                }
         }
-        constexpr int CH = D / 8, STEP = TILES_PREPARE / CH;
-        const int ch = lt % CH, first = lt / CH;
-        auto source = [&](int r) {  // null: a row of zeros
-            const int t = (row0 + r) / p.group, g = (row0 + r) - t * p.group;
-            return r < live && t < c.s.fresh ? static_cast<const char *>(p.q) +
-                                                   (((static_cast<int64_t>(c.b) * p.w.T + t) * p.q_heads + c.h * p.group + g) * D + ch * 8) * 2
-                                             : nullptr;
+        // rows first, first + STEP, ...: their tokens and heads, without a division each
+        int t = (row0 + first) / p.group, g = row0 + first - t * p.group;
+        const char *row = static_cast<const char *>(p.q) + (static_cast<int64_t>(it.b) * p.w.T * p.q_heads + it.h * p.group) * (D * 2) + ch * 16;
+        auto source = [&](int r) {  // null: a row of zeros; steps on
+            const char *from = r < live && t < it.fresh ? row + t * token + g * (D * 2) : nullptr;
+            t += step_t, g += step_g;
+            if (g >= p.group) g -= p.group, ++t;
+            return from;
         };
         if constexpr (!S::WIDEN) {
             const uint32_t to = base + place * S::Q;
@@ -591,8 +735,9 @@ __device__ void tiles_prepare(const TilesParams &p, TileCursor c, char *smem, Ti
                     }
 #pragma unroll
                     for (int o = CH / 2; o; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
-                    const int e2 = top > 0.0f ? max(-120, min(120, 14 - ilogbf(top))) : 0;  // the largest below 2^15
-                    const float up = exp2f(static_cast<float>(e2));
+                    // the largest below 2^15 (the exponent of a number that is not normal counts as the smallest's)
+                    const int e2 = top > 0.0f ? max(-120, min(120, 14 - (static_cast<int>(__float_as_uint(top) >> 23) - 127))) : 0;
+                    const float up = __uint_as_float(static_cast<uint32_t>(e2 + 127) << 23);
                     if (r < S::ROWS) {
                         if (ch == 0) ctl->at.q_power[place * S::ROWS + r] = static_cast<signed char>(e2);
                         *reinterpret_cast<uint4 *>(to + (r >> 7) * S::Q_SUB + tile_at<128>(r & 127, ch)) =
@@ -756,61 +901,33 @@ template <int D, typename S> __device__ void tiles_lost(const TilesParams &p, co
 }
 
 // What is left to do for a group's rows at the end of its range, out of line:
-// rows that were not finite, of the items before tile `done`, and NaN from there
-// on where a wait gave up.
+// rows that were not finite, of the first `done` items, and NaN from there on
+// where a wait gave up.
 template <typename C, int D, bool PAIR>
-__device__ __noinline__ void tiles_finish(const TilesParams &p, TilesCtl<TilesShape<C, D, PAIR>> *ctl, long long done, int group, int tid)
+__device__ __noinline__ void tiles_finish(const TilesParams &p, bool again, int done, int group, int tid)
 {
     using S = TilesShape<C, D, PAIR>;
     const int lane = tid & 31;
-    TileCursor c = ctl->start;
+    TileCursor c = tiles_find_again<S>(p, lane);
     const long long begin = c.at;
-    c.s = item_tiles<S>(p, tiles_lens(p, c.b), c.b, c.row_tile, lane);
     const int r_from = 128 * group, r_count = PAIR ? 128 : S::ROWS;
-    for (; c.at < done; tiles_next<S>(c, p, lane))
-        if (ctl->lost[group]) tiles_again<C, D, PAIR>(p, c, begin, r_from, r_count, tid >> 5, S::GROUP / 32, lane);
-    for (; c.at < c.end; tiles_next<S>(c, p, lane)) tiles_lost<D, S>(p, c, begin, r_from, r_count, tid, S::GROUP);
-}
-
-__device__ __forceinline__ float2 unpair(unsigned long long x)
-{
-    float2 y;
-    asm("mov.b64 {%0, %1}, %2;" : "=f"(y.x), "=f"(y.y) : "l"(x));
-    return y;
+    for (int k = 0; c.at < c.end; tiles_next<S>(c, p, lane), ++k) {
+        if (k >= done)
+            tiles_lost<D, S>(p, c, begin, r_from, r_count, tid, S::GROUP);
+        else if (again)
+            tiles_again<C, D, PAIR>(p, c, begin, r_from, r_count, tid >> 5, S::GROUP / 32, lane);
+    }
 }
 
 // Cap, bias and a window over moved slots of a row's MINE scores of a tile whose
 // first key is jb: the true scores are then x f - off.
 template <int MINE, bool PAIR, typename Ctl>
-__device__ __forceinline__ void tile_shape(const TilesParams &p, unsigned long long (&x)[MINE / 2], float *f, float *off, const TileCursor &c,
+__device__ __forceinline__ void tile_shape(const TilesParams &p, unsigned long long (&x)[MINE / 2], float *f, float *off, int ctx, int total,
                                            Ctl *ctl, int place, int jb, int own, float slope, int origin, int quad)
 {
     const ScoresView &v = p.sc;
     if (v.cap2 != 0.0f) {
-        float large = 0.0f;
-#pragma unroll
-        for (int i = 0; i < MINE / 2; ++i) {
-            const float2 y = unpair(x[i]);
-            large = fmax3(large, fabsf(y.x), fabsf(y.y));
-        }
-        const float edge = CAP_SMALL * v.cap2;
-        if (__any_sync(0xffffffffu, large * fabsf(*f) >= edge)) {
-#pragma unroll
-            for (int i = 0; i < MINE / 2; ++i) {
-                const float2 y = unpair(x[i]);
-                const float a = y.x * *f, b = y.y * *f;
-                x[i] = pack2(fabsf(a) >= edge ? capped_large(v, a) : capped_small(v, a), fabsf(b) >= edge ? capped_large(v, b) : capped_small(v, b));
-            }
-        } else {  // x f P((x f / cap)^2), as capped_small
-            const float u = *f * v.cap_inv;
-            const unsigned long long u2 = pack2(u, u), c0 = pack2(CAP_0 * *f, CAP_0 * *f), c1 = pack2(CAP_1 * *f, CAP_1 * *f),
-                                     c2 = pack2(CAP_2 * *f, CAP_2 * *f), c3 = pack2(CAP_3 * *f, CAP_3 * *f), c4 = pack2(CAP_4 * *f, CAP_4 * *f);
-#pragma unroll
-            for (int i = 0; i < MINE / 2; ++i) {
-                const unsigned long long y = mul2(x[i], u2), w = mul2(y, y);
-                x[i] = mul2(x[i], ffma2(w, ffma2(w, ffma2(w, ffma2(w, c4, c3), c2), c1), c0));
-            }
-        }
+        cap_pairs(v, x, *f);
         *f = 1.0f;
     } else if (!(*f > 0.0f)) {  // the largest product has to be the largest score
         const unsigned long long f2 = pack2(*f, *f);
@@ -821,7 +938,7 @@ __device__ __forceinline__ void tile_shape(const TilesParams &p, unsigned long l
     if (moved_slots(v)) {
         const float s = -slope / *f;
         if (v.window > 0) {
-            const int2 *at = reinterpret_cast<const int2 *>(ctl->positions[quad]);
+            const int2 *at = reinterpret_cast<const int2 *>(ctl->at.positions[quad]);
 #pragma unroll
             for (int i = 0; i < MINE / 2; ++i) {
                 const int2 there = at[i];
@@ -831,7 +948,7 @@ __device__ __forceinline__ void tile_shape(const TilesParams &p, unsigned long l
                              b >= v.window ? -CUDART_INF_F : fmaf(s, fabsf(static_cast<float>(b)), y.y));
             }
         } else {
-            const ulonglong2 *at = reinterpret_cast<const ulonglong2 *>(ctl->positions[quad]);
+            const ulonglong2 *at = reinterpret_cast<const ulonglong2 *>(ctl->at.positions[quad]);
             const float mine = static_cast<float>(own - origin);
             const unsigned long long mine2 = pack2(mine, mine);
 #pragma unroll
@@ -844,14 +961,14 @@ __device__ __forceinline__ void tile_shape(const TilesParams &p, unsigned long l
         }
     } else if (v.slopes) {
         const float s = slope / *f;
-        if (!PAIR && p.parent && jb + MINE > c.s.ctx) {  // a node's position is its depth's
+        if (!PAIR && p.parent && jb + MINE > ctx) {  // a node's position is its depth's
 #pragma unroll
             for (int i = 0; i < MINE / 2; ++i) {
                 const float2 y = unpair(x[i]);
                 float z[2] = {y.x, y.y};
 #pragma unroll
                 for (int k = 0; k < 2; ++k) {
-                    const int j = jb + 2 * i + k, there = j >= c.s.ctx && j < c.s.total ? c.s.ctx + ctl->at.depth[place][j - c.s.ctx] : j;
+                    const int j = jb + 2 * i + k, there = j >= ctx && j < total ? ctx + ctl->at.depth[place][j - ctx] : j;
                     z[k] = fmaf(-s, fabsf(static_cast<float>(own - there)), z[k]);
                 }
                 x[i] = pack2(z[0], z[1]);
@@ -876,7 +993,7 @@ __device__ __forceinline__ void tile_shape(const TilesParams &p, unsigned long l
 
 // A row a thread (PAIR), or half of its keys.  tid: 0 .. 255.
 template <typename C, int D, bool PAIR, typename S = TilesShape<C, D, PAIR>>
-__device__ void tiles_rows(const TilesParams &p, TileCursor c, char *smem, TilesCtl<S> *ctl, unsigned *err, int tid)
+__device__ void tiles_rows(const TilesParams &p, TilesCtl<S> *ctl, unsigned *err, int tid)
 {
     using M = typename MmaOf<C, C>::type;  // e4m3: f16
     constexpr float UP = Weights<M>::UP;
@@ -885,60 +1002,76 @@ __device__ void tiles_rows(const TilesParams &p, TileCursor c, char *smem, Tiles
     const int r = 128 * group + lane_row, group_tid = tid - 128 * group;  // row of the item; place in the group
     const uint32_t quarter = static_cast<uint32_t>(lane_row & ~31) << 16;
     const uint32_t tm_o = ctl->tmem + quarter + 256 + group * 128;
-    const long long begin = c.at;
     const ScoresView &v = p.sc;
     const bool moved = moved_slots(v);
     int n = 0, item = 0, outs = 0;  // tiles of this group; items with tiles; items with outputs of this group (PAIR)
-    for (; c.at < c.end; tiles_next<S>(c, p, lane)) {
-        const int t0 = tiles_first(c), t1 = tiles_last(c), row0 = c.row_tile * S::ROWS, live = min(S::ROWS, p.rows - row0);
-        const int s0 = PAIR ? max(t0, c.s.lo[group]) : t0, s1 = max(s0, PAIR ? min(t1, c.s.hi[group]) : t1);
-        const AttRows rows{c.b, c.h, row0, live};
-        const float v_scale = p.c.v_scale ? __ldg(p.c.v_scale + c.h) : 1.0f;
+    TileItem it;
+    int k = 0;
+    bool ok = true;
+    // The next item, for the whole group: a warp that a wait has given up stops all.
+    auto take = [&]() {
+        const bool some = take_item(ctl, k, &it, err, lane);
+        if (!some && !(it.flags & ITEM_END) && lane == 0) *reinterpret_cast<volatile int *>(&ctl->stop[group]) = 1;
+        group_sync<GROUP>(group);  // and all have read the last item's sums and flags
+        return some && !*reinterpret_cast<volatile int *>(&ctl->stop[group]);
+    };
+    it.flags = 0;
+    for (; take(); ++k) {
+        const int t0 = it.t0, t1 = it.t1, row0 = it.row_tile * S::ROWS, live = min(S::ROWS, p.rows - row0);
+        const int s0 = PAIR ? max(t0, group ? it.lo1 : it.lo0) : t0, s1 = max(s0, PAIR ? min(t1, group ? it.hi1 : it.hi0) : t1);
+        const float v_scale = p.c.v_scale ? __ldg(p.c.v_scale + it.h) : 1.0f;
         const bool mine = r < live;
         const int token = (row0 + r) / p.group;
-        const int64_t row_at = (static_cast<int64_t>(c.b) * p.w.T + token) * p.q_heads + c.h * p.group + (row0 + r) - token * p.group;
+        const int64_t row_at = (static_cast<int64_t>(it.b) * p.w.T + token) * p.q_heads + it.h * p.group + (row0 + r) - token * p.group;
         float m = -CUDART_INF_F, l = 0.0f;  // a maximum so far less UP: what l and O are sums against
-        bool any_bad = c.s.bad, ok = true;
+        bool any_bad = it.flags & ITEM_BAD;
         const int place = item % S::Q_PLACES;
         if (t0 < t1) {
-            const bool there = mine && token < c.s.fresh;
+            const bool there = mine && token < it.fresh;
+            const SeqLens lens{it.ctx, it.fresh, it.total, false};
             Interval see{0, 0};
             unsigned long long bits = 0;
             int own = 0;
-            const int32_t *pos = v.slot_pos ? v.slot_pos + (static_cast<int64_t>(c.b) * p.c.kv_heads + c.h) * v.pos_stride : nullptr;
+            const int32_t *pos = v.slot_pos ? v.slot_pos + (static_cast<int64_t>(it.b) * p.c.kv_heads + it.h) * v.pos_stride : nullptr;
             if (there && !p.parent) {
-                see = token_interval(p, c.s, c.b, token);
-                own = moved ? __ldg(pos + c.s.ctx + token) : c.s.ctx + token;
+                see = token_interval(p, lens, it.b, token);
+                own = moved ? __ldg(pos + it.ctx + token) : it.ctx + token;
             }
             if constexpr (!PAIR) {
                 if (there && p.parent) {
-                    const TokenView view = token_view(v, p.parent + static_cast<int64_t>(c.b) * p.w.T, c.s, c.b, p.w.T, token);
+                    const TokenView view = token_view(v, p.parent + static_cast<int64_t>(it.b) * p.w.T, lens, it.b, p.w.T, token);
                     bits = view.bits;
-                    own = moved ? __ldg(pos + c.s.ctx + token) : c.s.ctx + view.depth;
-                    see.hi = bits ? c.s.ctx : 0;
+                    own = moved ? __ldg(pos + it.ctx + token) : it.ctx + view.depth;
+                    see.hi = bits ? it.ctx : 0;
                     see.lo = view.lo;
                 }
             }
-            const int origin = moved ? __ldg(pos + c.s.ctx) : 0;  // the first new token's position
-            const float slope = there && v.slopes ? __ldg(v.slopes + c.h * p.group + (row0 + r) - token * p.group) * LOG2E : 0.0f;
-            float factor = p.scale_log2 * (p.c.k_scale ? __ldg(p.c.k_scale + c.h) : 1.0f);
+            const int origin = moved ? __ldg(pos + it.ctx) : 0;  // the first new token's position
+            const float slope = there && v.slopes ? __ldg(v.slopes + it.h * p.group + (row0 + r) - token * p.group) * LOG2E : 0.0f;
+            float factor = p.scale_log2 * (p.c.k_scale ? __ldg(p.c.k_scale + it.h) : 1.0f);
             ok = tiles_wait(ctl, &ctl->q_full[place], (item / S::Q_PLACES) & 1, err);
             if (S::WIDEN) factor *= exp2f(-static_cast<float>(ctl->at.q_power[place * S::ROWS + r]));
             __syncwarp();
             if (lane == 0) mbar_arrive(&ctl->q_empty[place]);
             const bool shaped = v.cap2 != 0.0f || v.slopes || moved || __any_sync(0xffffffffu, !(factor > 0.0f));
             const bool works = __any_sync(0xffffffffu, there);
+            auto position = [&](int tile) {
+                const int j = tile * KEYS + half * MINE + lane_row;
+                return moved && lane_row < MINE && tile < s1 && j < it.total ? __ldg(pos + j) : 0;
+            };
+            int next_at = position(s0);
 #pragma unroll 1
             for (int tile = s0; tile < s1; ++tile, ++n) {  // to its end even after a wait gave up: the halves meet at each tile
                 const int buf = PAIR ? group : n & 1;
                 const uint32_t tm_s = ctl->tmem + quarter + buf * 128 + half * MINE;
                 const int jb = tile * KEYS + half * MINE;
-                if (moved) {  // positions of these keys, by the 128 threads that have them
-                    const int j = jb + lane_row, at = lane_row < MINE && j < c.s.total ? __ldg(pos + j) : 0;
+                if (moved) {  // positions of these keys, by the 128 threads that have them, asked for a tile ahead
                     quad_sync<PAIR>(tid >> 7);  // the last tile's have been read
                     // as distances to the item's first token where no window has to be exact: 32 bits hold those below 2^24
-                    if (lane_row < MINE) ctl->positions[tid >> 7][lane_row] = v.window > 0 ? at : __float_as_int(static_cast<float>(origin - at));
+                    if (lane_row < MINE)
+                        ctl->at.positions[tid >> 7][lane_row] = v.window > 0 ? next_at : __float_as_int(static_cast<float>(origin - next_at));
                     quad_sync<PAIR>(tid >> 7);
+                    next_at = position(tile + 1);
                 }
                 ok = ok && tiles_wait(ctl, &ctl->s_full[buf], (PAIR ? n : n >> 1) & 1, err);
                 tc_fence_after();
@@ -946,16 +1079,20 @@ __device__ void tiles_rows(const TilesParams &p, TileCursor c, char *smem, Tiles
                 if (works) {
                     // Pairs of scores, so that one instruction works on two.
                     unsigned long long x[MINE / 2];
+                    constexpr int LOAD = MINE < 64 ? MINE : 64;
 #pragma unroll
-                    for (int i = 0; i < MINE; i += 32) {
-                        uint32_t y[32];
-                        tc_ld32(y, tm_s + i);
+                    for (int i = 0; i < MINE; i += LOAD) {
+                        uint32_t y[LOAD];
+                        if constexpr (LOAD == 64)
+                            tc_ld64(y, tm_s + i);
+                        else
+                            tc_ld32(y, tm_s + i);
 #pragma unroll
-                        for (int k = 0; k < 32; k += 2) x[(i + k) / 2] = pack2(__uint_as_float(y[k]), __uint_as_float(y[k + 1]));
+                        for (int e = 0; e < LOAD; e += 2) x[(i + e) / 2] = pack2(__uint_as_float(y[e]), __uint_as_float(y[e + 1]));
                     }
                     // The true scores are x f - off.
                     float f = factor, off = 0.0f;
-                    if (shaped) tile_shape<MINE, PAIR>(p, x, &f, &off, c, ctl, place, jb, own, slope, origin, tid >> 7);
+                    if (shaped) tile_shape<MINE, PAIR>(p, x, &f, &off, it.ctx, it.total, ctl, place, jb, own, slope, origin, tid >> 7);
                     const bool seen = see.lo <= jb && see.hi >= jb + MINE;
                     if (!__all_sync(0xffffffffu, seen)) {
 #pragma unroll
@@ -963,7 +1100,7 @@ __device__ void tiles_rows(const TilesParams &p, TileCursor c, char *smem, Tiles
                             const int lo = min(max(see.lo - jb - i, 0), 32), hi = min(max(see.hi - jb - i, 0), 32);
                             unsigned mask = hi == 32 ? 0xffffffffu : (1u << hi) - 1u;
                             if (!PAIR && p.parent) {
-                                const int o = c.s.ctx - (jb + i);  // the first new token's column, from here
+                                const int o = it.ctx - (jb + i);  // the first new token's column, from here
                                 if (o < 32 && o > -64) mask |= static_cast<unsigned>(o >= 0 ? bits << o : bits >> -o);
                             }
                             mask = lo == 32 ? 0u : mask & ~((1u << lo) - 1u);
@@ -1038,10 +1175,17 @@ __device__ void tiles_rows(const TilesParams &p, TileCursor c, char *smem, Tiles
                             tc_st32(tm_s + i0 / 2, pk);
                         else
                             tc_st16(tm_s + i0 / 2, pk);
+                        if (PAIR && i0 == 0) {  // the products with these may begin
+                            tc_wait_st();
+                            tc_fence_before();
+                            mbar_arrive(&ctl->p_half[buf]);
+                        }
                     }
                     const float2 all = unpair(fadd2(sum[0], sum[1]));
                     l += all.x + all.y;
                     tc_wait_st();
+                } else if (PAIR) {
+                    mbar_arrive(&ctl->p_half[buf]);
                 }
                 tc_fence_before();
                 mbar_arrive(&ctl->p_full[buf]);
@@ -1061,15 +1205,15 @@ __device__ void tiles_rows(const TilesParams &p, TileCursor c, char *smem, Tiles
         const bool tiles = s0 < s1;
         group_sync<GROUP>(group);  // all have read the item's flag, and the last tile's maxima
         if (group_tid == 0) {
-            ctl->stop[group] = *reinterpret_cast<volatile int *>(&ctl->dead);
+            if (*reinterpret_cast<volatile int *>(&ctl->dead)) ctl->stop[group] = 1;
             if (t0 < t1) ctl->bad[group][(item - 1) % S::ITEMS] = 0;
         }
         if (HALVES == 2) ctl->at.top[0][tid] = l;
         group_sync<GROUP>(group);
         if (*reinterpret_cast<volatile int *>(&ctl->stop[group])) break;  // a wait gave up: this item is among what is lost
         if (HALVES == 2) l += ctl->at.top[0][tid ^ 128];
-        const bool whole = item_whole(c);
-        float *part = p.parts + (static_cast<int64_t>(blockIdx.x) * 2 + (c.first < begin ? 0 : 1)) * PART;
+        const bool whole = it.flags & ITEM_WHOLE;
+        float *part = p.parts + (static_cast<int64_t>(blockIdx.x) * 2 + (it.flags & ITEM_SECOND ? 1 : 0)) * PART;
         const bool none = m == -CUDART_INF_F && l == 0.0f, fixed = none || any_bad;
         const float instead = any_bad ? CUDART_NAN_F : 0.0f, out_scale = v_scale / l;
         if (half == 0 && mine) {
@@ -1080,7 +1224,7 @@ __device__ void tiles_rows(const TilesParams &p, TileCursor c, char *smem, Tiles
                 p.lse[row_at] = any_bad ? CUDART_NAN_F : none ? -CUDART_INF_F : LN2 * (m + log2f(l));
             }
         }
-        bool odd = false;
+        float odd = 0.0f;  // NaN if something is not finite
 #pragma unroll 1
         for (int d0 = half * (D / HALVES); d0 < (half + 1) * (D / HALVES); d0 += 32) {
             float x[32];
@@ -1100,7 +1244,7 @@ __device__ void tiles_rows(const TilesParams &p, TileCursor c, char *smem, Tiles
 #pragma unroll
                 for (int k = 0; k < 32; ++k) {
                     x[k] = fixed ? 0.0f : x[k];
-                    odd |= !(fabsf(x[k]) < CUDART_INF_F);
+                    odd = fmaf(x[k], 0.0f, odd);
                 }
 #pragma unroll
                 for (int k = 0; k < 32; k += 8) {
@@ -1113,7 +1257,7 @@ __device__ void tiles_rows(const TilesParams &p, TileCursor c, char *smem, Tiles
 #pragma unroll
                 for (int k = 0; k < 32; ++k) {
                     x[k] = fixed ? instead : x[k] * out_scale;
-                    odd |= !(fabsf(x[k]) < CUDART_INF_F);
+                    odd = fmaf(x[k], 0.0f, odd);
                 }
 #pragma unroll
                 for (int k = 0; k < 32; k += 16) {
@@ -1127,12 +1271,11 @@ __device__ void tiles_rows(const TilesParams &p, TileCursor c, char *smem, Tiles
             }
         }
         tc_fence_before();
-        if (odd && !any_bad) *reinterpret_cast<volatile int *>(&ctl->lost[group]) = 1;
-        if (!whole && group == 0) note_split(p, c, rows, begin, tid);
-        group_sync<GROUP>(group);  // sums and flags have been read
+        if (odd != odd && !any_bad) *reinterpret_cast<volatile int *>(&ctl->lost[group]) = 1;
     }
-    // c.at before the end: a wait gave up
-    if (*reinterpret_cast<volatile int *>(&ctl->lost[group]) || c.at < c.end) tiles_finish<C, D, PAIR>(p, ctl, c.at, group, group_tid);
+    group_sync<GROUP>(group);
+    const bool again = *reinterpret_cast<volatile int *>(&ctl->lost[group]), stopped = *reinterpret_cast<volatile int *>(&ctl->stop[group]);
+    if (again || stopped) tiles_finish<C, D, PAIR>(p, again, stopped ? k : 0x7fffffff, group, group_tid);
 }
 
 template <typename C, int D, bool PAIR>
@@ -1152,6 +1295,9 @@ __global__ void __launch_bounds__(TILES_THREADS, 1)
         }
         for (int i = 0; i < 2; ++i) {
             mbar_init(&ctl->s_full[i], 1);
+            mbar_init(&ctl->item_full[i], 1);
+            mbar_init(&ctl->item_empty[i], TILES_TAKERS);
+            mbar_init(&ctl->p_half[i], S::GROUP);
             mbar_init(&ctl->p_full[i], S::GROUP);
             mbar_init(&ctl->o_done[i], 1);
             mbar_init(&ctl->q_full[i], TILES_PREPARE);
@@ -1160,6 +1306,9 @@ __global__ void __launch_bounds__(TILES_THREADS, 1)
             for (int k = 0; k < S::ITEMS; ++k) ctl->bad[i][k] = 0;
         }
         mbar_init(&ctl->spare, 1);
+        if (S::WIDEN)
+            for (int i = 0; i < 4; ++i)
+                for (int k = 0; k < S::RAW_STAGES; ++k) mbar_init(&ctl->raw_full[S::WIDEN ? i : 0][k], 1);
         ctl->dead = 0;
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
@@ -1180,25 +1329,27 @@ __global__ void __launch_bounds__(TILES_THREADS, 1)
             asm volatile("setmaxnreg.inc.sync.aligned.u32 184;");
         else
             asm volatile("setmaxnreg.inc.sync.aligned.u32 160;");
-        tiles_rows<C, D, PAIR>(p, c, smem, ctl, err, tid);
+        tiles_rows<C, D, PAIR>(p, ctl, err, tid);
     } else if (warp < 12) {
         if (PAIR)
             asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
         else
             asm volatile("setmaxnreg.dec.sync.aligned.u32 96;");
         if (warp == 8) {
-            tiles_multiply<C, D, PAIR>(p, c, smem, ctl, err, lane);
+            tiles_multiply<C, D, PAIR>(smem, ctl, err, lane);
             warp_commit(&ctl->spare);  // what was issued ends before the block may: others may have given up on it
             mbar_drain(&ctl->spare, 0);
+        } else if (warp == 9) {
+            tiles_items<S>(p, c, ctl, err, lane);
         } else {
-            tiles_prepare<C, D, PAIR>(p, c, smem, ctl, err, tid - 288);
+            tiles_prepare<C, D, PAIR>(p, smem, ctl, err, tid - 320);
         }
     } else {
         if (PAIR)
             asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
         else
             asm volatile("setmaxnreg.dec.sync.aligned.u32 96;");
-        tiles_load<C, D, PAIR>(p, c, smem, ctl, err, tid - 384, maps ? &map_k : nullptr, maps ? &map_v : nullptr);
+        tiles_load<C, D, PAIR>(p, smem, ctl, err, tid - 384, maps ? &map_k : nullptr, maps ? &map_v : nullptr);
     }
     tc_fence_before();
     __syncthreads();
@@ -1217,7 +1368,8 @@ template <typename C, int D, bool PAIR> cudaError_t launch_tiles_of(TilesParams 
     p.w.tile = S::KEYS;
     p.w.row_tiles = (p.rows + S::ROWS - 1) / S::ROWS;
     CUtensorMap map_k{}, map_v{};
-    const bool maps = pool_map(&map_k, L, false, S::KEYS) && pool_map(&map_v, L, true, S::KEYS);
+    const int slots = S::WIDEN ? S::KEYS / 4 : S::KEYS;
+    const bool maps = pool_map(&map_k, L, false, slots, S::WIDEN) && pool_map(&map_v, L, true, slots, S::WIDEN);
     e = launch_chained(kernel, dim3(ATT_SMS), TILES_THREADS, SMEM, st, p, map_k, map_v, static_cast<int>(maps));
     return e != cudaSuccess ? e : launch_join(p, L.dtype, D, S::ROWS, ATT_SMS, st);
 }

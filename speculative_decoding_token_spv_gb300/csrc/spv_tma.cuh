@@ -12,13 +12,15 @@
 namespace spv {
 
 // The map of a 16-bit pool: element, slot, head, page; a box is 64 elements
-// (the width of an operand's panel) of min(page_size, `slots`) slots.  False where
+// (the width of an operand's panel) of min(page_size, `slots`) slots, or, with
+// `rows` (e4m3 pools too), the whole rows of so many, as they lie.  False where
 // the pool cannot be described so (pages under 8 slots, a driver without the
 // call): the kernels then copy row by row.
-inline bool pool_map(CUtensorMap *map, const KvLaunch &L, bool v, int slots = 128)
+inline bool pool_map(CUtensorMap *map, const KvLaunch &L, bool v, int slots = 128, bool rows = false)
 {
     const spv_kv_cache &c = L.cache;
-    if (c.dtype == SPV_E4M3 || c.page_size < 8 || c.head_dim % 64 != 0) return false;
+    const bool eight = c.dtype == SPV_E4M3;
+    if ((eight && !rows) || c.page_size < 8 || c.head_dim % 64 != 0) return false;
     using Encode = CUresult (*)(CUtensorMap *, CUtensorMapDataType, cuuint32_t, void *, const cuuint64_t *, const cuuint64_t *,
                                 const cuuint32_t *, const cuuint32_t *, CUtensorMapInterleave, CUtensorMapSwizzle,
                                 CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
@@ -39,13 +41,13 @@ inline bool pool_map(CUtensorMap *map, const KvLaunch &L, bool v, int slots = 12
     for (int i = 0; i < 3; ++i) {
         // a dimension of one entry is never stepped over, but its stride has to be one
         if (strides[i] <= 0 && sizes[i + 1] > 1) return false;
-        bytes[i] = static_cast<cuuint64_t>(strides[i] > 0 ? strides[i] : c.head_dim) * 2;
+        bytes[i] = static_cast<cuuint64_t>(strides[i] > 0 ? strides[i] : c.head_dim) * (eight ? 1 : 2);
         if (bytes[i] >= (1ull << 40)) return false;
     }
-    const cuuint32_t box[4] = {64, static_cast<cuuint32_t>(c.page_size < slots ? c.page_size : slots), 1, 1};
+    const cuuint32_t box[4] = {static_cast<cuuint32_t>(rows ? c.head_dim : 64), static_cast<cuuint32_t>(c.page_size < slots ? c.page_size : slots), 1, 1};
     const cuuint32_t steps[4] = {1, 1, 1, 1};
-    return encode(map, c.dtype == SPV_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 4,
-                  v ? c.v : c.k, sizes, bytes, box, steps, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+    return encode(map, eight ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : c.dtype == SPV_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 4,
+                  v ? c.v : c.k, sizes, bytes, box, steps, CU_TENSOR_MAP_INTERLEAVE_NONE, rows ? CU_TENSOR_MAP_SWIZZLE_NONE : CU_TENSOR_MAP_SWIZZLE_128B,
                   CU_TENSOR_MAP_L2_PROMOTION_L2_128B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
