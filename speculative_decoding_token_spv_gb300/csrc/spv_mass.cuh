@@ -65,6 +65,12 @@ __device__ __forceinline__ ScoredWork scored_work(const ScoredMassParams &p)
     return w;
 }
 
+// Groups of four warps that sum, taking turns at the tiles.  Scores that have to
+// be capped or biased take long chains of dependent operations, which one warp a
+// scheduler does not hide: the capped verify batch took FIRST us with four warps.
+template <typename P> constexpr int mass_turns() { return std::is_same<P, ScoredMassParams>::value ? 2 : 1; }
+template <typename P> constexpr int mass_threads() { return MASS_THREADS + 128 * (mass_turns<P>() - 1); }
+
 // Which new tokens of sequence b count; *bad if what says so is out of range.
 __device__ __forceinline__ unsigned long long counted_tokens(const MassParams &p, int b, bool *bad)
 {
@@ -411,18 +417,19 @@ __device__ void mass_multiply(const P &p, Cursor c, char *smem, Ctl *ctl)
     }
 }
 
-// Four warps, a key of the tile a thread.  Returns the tile up to which the
+// Four warps, a key of the tile a thread, for every tile of theirs (`turn` of mass_turns).  Returns the tile up to which the
 // range is done: where its item began, if a wait gave up.  A warp that leaves so
 // arrives on no barrier any more: 32 arrivals where a barrier lacks fewer (q's
 // lacks 129) end in a fault.
-template <typename Shape, typename Ctl, typename P> __device__ long long mass_sum(const P &p, Cursor c, Ctl *ctl, int tid)
+template <typename Shape, typename Ctl, typename P> __device__ long long mass_sum(const P &p, Cursor c, Ctl *ctl, int tid, int turn)
 {
+    constexpr int TURNS = mass_turns<P>();
     constexpr bool SCORED = std::is_same<P, ScoredMassParams>::value;
     constexpr int ROWS = Shape::ROWS;
     const int lane = tid & 31, warp = tid >> 5;
     const uint32_t quarter = ctl->tmem + (static_cast<uint32_t>(warp * 32) << 16);
     Counted count;
-    int n = 0, unit_no = 0;
+    int before = 0, unit_no = 0;  // tiles with products before the present pass
     for (; c.at < c.end; next_item(c, p.w, p.c)) {
         count.at(p, c);
         const int32_t *table = p.c.table + static_cast<int64_t>(c.b) * p.c.max_pages;
@@ -442,8 +449,8 @@ template <typename Shape, typename Ctl, typename P> __device__ long long mass_su
                 const int j = tile * MASS_KEYS + tid;
                 return tile < t1 && j < held ? so_far[j] : 0.0f;
             };
-            int pg = page_for(t0);  // both asked for a tile ahead
-            float had = mass_for(t0);
+            int pg = page_for(t0 + turn);  // both asked for a tile ahead
+            float had = mass_for(t0 + turn);
             auto position_for = [&](int tile) {  // of this thread's key
                 const int j = tile * MASS_KEYS + tid;
                 if constexpr (SCORED) {
@@ -456,7 +463,7 @@ template <typename Shape, typename Ctl, typename P> __device__ long long mass_su
                 }
                 return j;
             };
-            int next_at = SCORED ? position_for(t0) : 0, origin = c.s.ctx;  // the first new token's position
+            int next_at = SCORED ? position_for(t0 + turn) : 0, origin = c.s.ctx;  // the first new token's position
             if constexpr (SCORED) {
                 if (moved_slots(p.sc) && c.s.fresh > 0)
                     origin = __ldg(p.sc.slot_pos + (static_cast<int64_t>(c.b) * p.c.kv_heads + c.h) * p.sc.pos_stride + c.s.ctx);
@@ -467,14 +474,14 @@ template <typename Shape, typename Ctl, typename P> __device__ long long mass_su
                 if (!mass_wait(ctl, &ctl->q_full[place], (unit_no >> 1) & 1)) return c.at;
                 careful = *reinterpret_cast<volatile int *>(&ctl->careful[place]) == unit_no + 1;
             }
-            for (int tile = t0; tile < t1; ++tile) {
-                const int j = tile * MASS_KEYS + tid, page = pg;
+            for (int tile = t0 + turn; tile < t1; tile += TURNS) {
+                const int j = tile * MASS_KEYS + tid, page = pg, n = before + tile - seen0;
                 const float old = had;
-                pg = page_for(tile + 1);
-                had = mass_for(tile + 1);
+                pg = page_for(tile + TURNS);
+                had = mass_for(tile + TURNS);
                 const int key_at = next_at;
                 const float key_rel = SCORED ? static_cast<float>(key_at - origin) : 0.0f;
-                if (SCORED) next_at = position_for(tile + 1);
+                if (SCORED) next_at = position_for(tile + TURNS);
                 float sum = 0.0f;
                 if (live > 0 && tile >= seen0) {
                     if (!mass_wait(ctl, &ctl->s_full[n % MASS_BUFFERS], (n / MASS_BUFFERS) & 1)) return c.at;
@@ -554,7 +561,6 @@ template <typename Shape, typename Ctl, typename P> __device__ long long mass_su
                     }
                     tc_fence_before();
                     mbar_arrive(&ctl->s_empty[n % MASS_BUFFERS]);
-                    ++n;
                     sum = s0 + s1;
                 }
                 if (static_cast<unsigned>(page) < static_cast<unsigned>(p.c.num_pages)) p.mass_out[out_row + j] = old * keep + sum;
@@ -562,6 +568,7 @@ template <typename Shape, typename Ctl, typename P> __device__ long long mass_su
             if (live > 0 && seen0 < t1) {
                 mbar_arrive(&ctl->q_empty[place]);
                 ++unit_no;
+                before += t1 - seen0;
             }
         }
     }
@@ -589,7 +596,7 @@ template <typename P> __device__ __noinline__ void mass_lost(const P &p, long lo
     }
 }
 
-template <typename T, typename C, int D, typename P> __global__ void __launch_bounds__(MASS_THREADS, 1) mass_kernel(const P p)
+template <typename T, typename C, int D, typename P> __global__ void __launch_bounds__(mass_threads<P>(), 1) mass_kernel(const P p)
 {
     using S = MassShape<C, D>;
     using Ctl = MassCtl<S::ROWS, std::is_same<P, ScoredMassParams>::value>;
@@ -608,7 +615,7 @@ template <typename T, typename C, int D, typename P> __global__ void __launch_bo
         }
         for (int i = 0; i < 2; ++i) {
             mbar_init(&ctl->q_full[i], 96);
-            mbar_init(&ctl->q_empty[i], 129);  // the products' end and the 128 readers of the constants
+            mbar_init(&ctl->q_empty[i], 1 + 128 * mass_turns<P>());  // the products' end and the readers of the constants
         }
         mbar_init(&ctl->spare, 1);
         ctl->dead = ctl->careful[0] = ctl->careful[1] = 0;
@@ -624,9 +631,16 @@ template <typename T, typename C, int D, typename P> __global__ void __launch_bo
         if (warp == 4) tmem_free(ctl->tmem, 512);
         return;
     }
-    if (warp < 4) {
-        const long long done = mass_sum<S>(p, c, ctl, tid);
-        if (done < c.end) mass_lost(p, done, tid);
+    // registers: launched with 96 a thread, 5 x 96 = 2 x 120 + 3 x 80
+    if (mass_turns<P>() > 1) {
+        if (warp < 4 || warp >= 16)
+            asm volatile("setmaxnreg.inc.sync.aligned.u32 120;");
+        else
+            asm volatile("setmaxnreg.dec.sync.aligned.u32 80;");
+    }
+    if (warp < 4 || warp >= 16) {  // the second group's warps are the last four
+        const long long done = mass_sum<S>(p, c, ctl, tid & 127, warp >= 16);
+        if (done < c.end) mass_lost(p, done, tid & 127);
     } else if (warp == 4) {
         if (tid == 128) {
             mass_multiply<T, C, D>(p, c, smem, ctl);
@@ -655,7 +669,7 @@ template <typename T, typename C, int D, typename P> static cudaError_t launch_d
     static_assert(SMEM <= 232448, "shared memory of a block");
     const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, SMEM);
     if (e != cudaSuccess) return e;
-    return launch_chained(kernel, dim3(MASS_SMS), MASS_THREADS, SMEM, st, p);
+    return launch_chained(kernel, dim3(MASS_SMS), mass_threads<P>(), SMEM, st, p);
 }
 template <typename T, typename C, typename P> static cudaError_t launch_types(const P &p, int D, cudaStream_t st)
 {
