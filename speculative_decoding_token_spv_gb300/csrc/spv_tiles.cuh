@@ -19,7 +19,10 @@
 //     weights go where their scores were;
 //   * else 128 rows, of which two warps share each row's keys (few rows; and D =
 //     256, whose outputs take half of tensor memory).  Scores stand in two
-//     places in turn;
+//     places in turn.  64 rows or fewer stand in tensor memory twice, 32 or fewer
+//     four times, each copy with half or a quarter of a tile's keys (its weights
+//     are zero elsewhere): all warps work whatever the number of rows, and the
+//     copies are put together at the item's end;
 //   * one warp works out the items, one issues the products, two bring q, four K
 //     and V in turn into one ring, a box a page by the copy engine, or row by row
 //     (small pages; a sequence's last tile of V, whose slots past the end become
@@ -53,11 +56,14 @@ struct TilesParams : ScoredParams {
     int q_bf16;
 };
 
-template <typename C, int D, bool PAIR> struct TilesShape {
+// COPIES 0: PAIR.
+template <typename C, int D, int COPIES> struct TilesShape {
+    static constexpr bool PAIR = COPIES == 0;
     static constexpr bool WIDEN = sizeof(C) == 1;
-    static constexpr int SUBS = PAIR ? 2 : 1, ROWS = 128 * SUBS;
+    static constexpr int SUBS = PAIR ? 2 : 1, ROWS = PAIR ? 256 : 128 / (PAIR ? 1 : COPIES);
     static constexpr int KEYS = D == 256 ? 64 : 128;             // of a tile
-    static constexpr int MINE = PAIR ? KEYS : KEYS / 2;          // of them a thread's
+    static constexpr int OF_COPY = KEYS / (PAIR ? 1 : COPIES);   // of them a copy's
+    static constexpr int MINE = PAIR ? KEYS : OF_COPY / 2;       // and a thread's
     static constexpr int TILE = KEYS * D * 2, RAW = KEYS * D;    // bytes of K or V as multiplied, and of e4m3
     static constexpr int Q_SUB = 128 * D * 2, Q = SUBS * Q_SUB;
     static constexpr int Q_PLACES = !WIDEN && 2 * Q <= 64 * 1024 ? 2 : 1;
@@ -100,7 +106,7 @@ template <typename S> struct TilesCtl {
         } find;                                                  // before the roles begin
         struct {
             union {
-                alignas(16) int positions[2][S::MINE];           // of moved slots: of a tile's keys, for each four row warps
+                alignas(16) int positions[S::SUBS][S::KEYS];     // of moved slots: of a tile's keys, for each group of row warps
                 signed char depth[S::Q_PLACES][S::SUBS == 1 ? 64 : 1];  // else, of trees: per place of q the depth of each new token
             };
             float top[2][S::SUBS == 1 ? 256 : 1];                // maxima of the two halves, of a tile and the next; sums
@@ -386,7 +392,7 @@ template <typename Ctl> __device__ __forceinline__ bool take_item(Ctl *ctl, int 
 
 // ------------------------------------------------------------------ K and V
 // Four warps: tiles of K and V in turn, each warp a quarter of their slots.
-template <typename C, int D, bool PAIR, typename S = TilesShape<C, D, PAIR>>
+template <typename C, int D, int COPIES, typename S = TilesShape<C, D, COPIES>>
 __device__ void tiles_load(const TilesParams &p, char *smem, TilesCtl<S> *ctl, unsigned *err, int lt,
                            const CUtensorMap *map_k, const CUtensorMap *map_v)
 {
@@ -557,10 +563,10 @@ __device__ void tiles_load(const TilesParams &p, char *smem, TilesCtl<S> *ctl, u
 
 // ------------------------------------------------------------------ products
 // One warp.
-template <typename C, int D, bool PAIR, typename S = TilesShape<C, D, PAIR>>
+template <typename C, int D, int COPIES, typename S = TilesShape<C, D, COPIES>>
 __device__ void tiles_multiply(char *smem, TilesCtl<S> *ctl, unsigned *err, int lane)
 {
-    constexpr bool BF16 = std::is_same<C, __nv_bfloat16>::value;
+    constexpr bool BF16 = std::is_same<C, __nv_bfloat16>::value, PAIR = S::PAIR;
     constexpr uint32_t QK = mma_shape(BF16, false, S::KEYS), PV = mma_shape(BF16, true, D);
     constexpr int NST = S::STAGES, KEYS = S::KEYS;
     // all values here are the same in all lanes, and the compiler is told so
@@ -668,7 +674,7 @@ __device__ void tiles_multiply(char *smem, TilesCtl<S> *ctl, unsigned *err, int 
 // ------------------------------------------------------------------ q
 // Two warps, an item ahead of the others where there is room: q, and of trees
 // the depths of the new tokens.
-template <typename C, int D, bool PAIR, typename S = TilesShape<C, D, PAIR>>
+template <typename C, int D, int COPIES, typename S = TilesShape<C, D, COPIES>>
 __device__ void tiles_prepare(const TilesParams &p, char *smem, TilesCtl<S> *ctl, unsigned *err, int lt)
 {
     const int lane = lt & 31;
@@ -688,7 +694,7 @@ __device__ void tiles_prepare(const TilesParams &p, char *smem, TilesCtl<S> *ctl
         }
         const int place = item % S::Q_PLACES, row0 = it.row_tile * S::ROWS, live = min(S::ROWS, p.rows - row0);
         if (item >= S::Q_PLACES && !tiles_wait(ctl, &ctl->q_empty[place], (item / S::Q_PLACES - 1) & 1, err)) return;
-        if constexpr (!PAIR) {
+        if constexpr (!S::PAIR) {
             if (p.parent && p.sc.slopes && !p.sc.slot_pos)
                 for (int t = lt; t < it.fresh; t += TILES_PREPARE) {
                     SeqLens s{it.ctx, it.fresh, it.total, false};
@@ -710,7 +716,10 @@ __device__ void tiles_prepare(const TilesParams &p, char *smem, TilesCtl<S> *ctl
 #pragma unroll 4
             for (int r = first; r < S::ROWS; r += STEP) {
                 const char *from = source(r);
-                cp_async16_zfill(to + (r >> 7) * S::Q_SUB + tile_at<128>(r & 127, ch), from ? from : static_cast<const char *>(p.q), from ? 16 : 0);
+#pragma unroll
+                for (int i = 0; i < (S::PAIR ? 1 : COPIES); ++i)
+                    cp_async16_zfill(to + (r >> 7) * S::Q_SUB + tile_at<128>((r & 127) + i * S::ROWS, ch), from ? from : static_cast<const char *>(p.q),
+                                     from ? 16 : 0);
             }
             asm volatile("cp.async.wait_all;" ::: "memory");
         } else {
@@ -740,9 +749,11 @@ __device__ void tiles_prepare(const TilesParams &p, char *smem, TilesCtl<S> *ctl
                     const float up = __uint_as_float(static_cast<uint32_t>(e2 + 127) << 23);
                     if (r < S::ROWS) {
                         if (ch == 0) ctl->at.q_power[place * S::ROWS + r] = static_cast<signed char>(e2);
-                        *reinterpret_cast<uint4 *>(to + (r >> 7) * S::Q_SUB + tile_at<128>(r & 127, ch)) =
-                            make_uint4(pack_mma<__half>(x[0] * up, x[1] * up), pack_mma<__half>(x[2] * up, x[3] * up),
-                                       pack_mma<__half>(x[4] * up, x[5] * up), pack_mma<__half>(x[6] * up, x[7] * up));
+                        const uint4 y = make_uint4(pack_mma<__half>(x[0] * up, x[1] * up), pack_mma<__half>(x[2] * up, x[3] * up),
+                                                   pack_mma<__half>(x[4] * up, x[5] * up), pack_mma<__half>(x[6] * up, x[7] * up));
+#pragma unroll
+                        for (int k = 0; k < (S::PAIR ? 1 : COPIES); ++k)
+                            *reinterpret_cast<uint4 *>(to + (r >> 7) * S::Q_SUB + tile_at<128>((r & 127) + k * S::ROWS, ch)) = y;
                     }
                 }
             }
@@ -756,8 +767,6 @@ __device__ void tiles_prepare(const TilesParams &p, char *smem, TilesCtl<S> *ctl
 // ------------------------------------------------------------------ rows
 // All threads that have rows of the same tile of rows.
 template <int N> __device__ __forceinline__ void group_sync(int group) { asm volatile("bar.sync %0, %1;" ::"r"(1 + group), "n"(N) : "memory"); }
-// The 128 threads that have the same keys of a tile.
-template <bool PAIR> __device__ __forceinline__ void quad_sync(int quad) { asm volatile("bar.sync %0, 128;" ::"r"((PAIR ? 1 : 7) + quad) : "memory"); }
 // The two warps that share rows.
 __device__ __forceinline__ void halves_sync(int w) { asm volatile("bar.sync %0, 64;" ::"r"(3 + w) : "memory"); }
 
@@ -777,10 +786,10 @@ __device__ __forceinline__ void store_32bytes(void *at, const uint32_t (&y)[8])
 // of it) whose result is not finite, again: a warp a row, key by key over what
 // the row sees, in 32 bits.  Rows whose scores are NaN, or that have a bad page,
 // stay as they are.
-template <typename C, int D, bool PAIR>
+template <typename C, int D, int COPIES>
 __device__ void tiles_again(const TilesParams &p, const TileCursor &c, long long begin, int r_from, int r_count, int warp, int warps, int lane)
 {
-    using S = TilesShape<C, D, PAIR>;
+    using S = TilesShape<C, D, COPIES>;
     constexpr int PER = D / 32;  // columns of a lane, next to one another
     const int row0 = c.row_tile * S::ROWS, live = min(S::ROWS, p.rows - row0), t0 = tiles_first(c), t1 = tiles_last(c);
     if (t0 == t1) return;
@@ -903,19 +912,19 @@ template <int D, typename S> __device__ void tiles_lost(const TilesParams &p, co
 // What is left to do for a group's rows at the end of its range, out of line:
 // rows that were not finite, of the first `done` items, and NaN from there on
 // where a wait gave up.
-template <typename C, int D, bool PAIR>
+template <typename C, int D, int COPIES>
 __device__ __noinline__ void tiles_finish(const TilesParams &p, bool again, int done, int group, int tid)
 {
-    using S = TilesShape<C, D, PAIR>;
+    using S = TilesShape<C, D, COPIES>;
     const int lane = tid & 31;
     TileCursor c = tiles_find_again<S>(p, lane);
     const long long begin = c.at;
-    const int r_from = 128 * group, r_count = PAIR ? 128 : S::ROWS;
+    const int r_from = 128 * group, r_count = S::PAIR ? 128 : S::ROWS;
     for (int k = 0; c.at < c.end; tiles_next<S>(c, p, lane), ++k) {
         if (k >= done)
             tiles_lost<D, S>(p, c, begin, r_from, r_count, tid, S::GROUP);
         else if (again)
-            tiles_again<C, D, PAIR>(p, c, begin, r_from, r_count, tid >> 5, S::GROUP / 32, lane);
+            tiles_again<C, D, COPIES>(p, c, begin, r_from, r_count, tid >> 5, S::GROUP / 32, lane);
     }
 }
 
@@ -923,7 +932,7 @@ __device__ __noinline__ void tiles_finish(const TilesParams &p, bool again, int 
 // first key is jb: the true scores are then x f - off.
 template <int MINE, bool PAIR, typename Ctl>
 __device__ __forceinline__ void tile_shape(const TilesParams &p, unsigned long long (&x)[MINE / 2], float *f, float *off, int ctx, int total,
-                                           Ctl *ctl, int place, int jb, int own, float slope, int origin, int quad)
+                                           Ctl *ctl, int place, int jb, int own, float slope, int origin, const int *positions)
 {
     const ScoresView &v = p.sc;
     if (v.cap2 != 0.0f) {
@@ -938,7 +947,7 @@ __device__ __forceinline__ void tile_shape(const TilesParams &p, unsigned long l
     if (moved_slots(v)) {
         const float s = -slope / *f;
         if (v.window > 0) {
-            const int2 *at = reinterpret_cast<const int2 *>(ctl->at.positions[quad]);
+            const int2 *at = reinterpret_cast<const int2 *>(positions);
 #pragma unroll
             for (int i = 0; i < MINE / 2; ++i) {
                 const int2 there = at[i];
@@ -948,7 +957,7 @@ __device__ __forceinline__ void tile_shape(const TilesParams &p, unsigned long l
                              b >= v.window ? -CUDART_INF_F : fmaf(s, fabsf(static_cast<float>(b)), y.y));
             }
         } else {
-            const ulonglong2 *at = reinterpret_cast<const ulonglong2 *>(ctl->at.positions[quad]);
+            const ulonglong2 *at = reinterpret_cast<const ulonglong2 *>(positions);
             const float mine = static_cast<float>(own - origin);
             const unsigned long long mine2 = pack2(mine, mine);
 #pragma unroll
@@ -992,14 +1001,17 @@ __device__ __forceinline__ void tile_shape(const TilesParams &p, unsigned long l
 }
 
 // A row a thread (PAIR), or half of its keys.  tid: 0 .. 255.
-template <typename C, int D, bool PAIR, typename S = TilesShape<C, D, PAIR>>
-__device__ void tiles_rows(const TilesParams &p, TilesCtl<S> *ctl, unsigned *err, int tid)
+template <typename C, int D, int COPIES, typename S = TilesShape<C, D, COPIES>>
+__device__ void tiles_rows(const TilesParams &p, char *smem, TilesCtl<S> *ctl, unsigned *err, int tid)
 {
     using M = typename MmaOf<C, C>::type;  // e4m3: f16
     constexpr float UP = Weights<M>::UP;
-    constexpr int KEYS = S::KEYS, MINE = S::MINE, GROUP = S::GROUP, PART = S::ROWS * (D + 2), HALVES = PAIR ? 1 : 2;
+    constexpr int KEYS = S::KEYS, MINE = S::MINE, GROUP = S::GROUP, PART = S::ROWS * (D + 2);
+    constexpr bool PAIR = S::PAIR;
+    constexpr int HALVES = PAIR ? 1 : 2, OF_ROW = PAIR ? 1 : COPIES;
     const int lane = tid & 31, half = PAIR ? 0 : tid >> 7, group = PAIR ? tid >> 7 : 0, lane_row = tid & 127;
-    const int r = 128 * group + lane_row, group_tid = tid - 128 * group;  // row of the item; place in the group
+    const int copy = PAIR ? 0 : lane_row / S::ROWS;
+    const int r = PAIR ? 128 * group + lane_row : lane_row % S::ROWS, group_tid = tid - 128 * group;  // row of the item; place in the group
     const uint32_t quarter = static_cast<uint32_t>(lane_row & ~31) << 16;
     const uint32_t tm_o = ctl->tmem + quarter + 256 + group * 128;
     const ScoresView &v = p.sc;
@@ -1051,26 +1063,29 @@ __device__ void tiles_rows(const TilesParams &p, TilesCtl<S> *ctl, unsigned *err
             float factor = p.scale_log2 * (p.c.k_scale ? __ldg(p.c.k_scale + it.h) : 1.0f);
             ok = tiles_wait(ctl, &ctl->q_full[place], (item / S::Q_PLACES) & 1, err);
             if (S::WIDEN) factor *= exp2f(-static_cast<float>(ctl->at.q_power[place * S::ROWS + r]));
-            __syncwarp();
-            if (lane == 0) mbar_arrive(&ctl->q_empty[place]);
+            if (OF_ROW == 1) {
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&ctl->q_empty[place]);
+            }
             const bool shaped = v.cap2 != 0.0f || v.slopes || moved || __any_sync(0xffffffffu, !(factor > 0.0f));
             const bool works = __any_sync(0xffffffffu, there);
             auto position = [&](int tile) {
-                const int j = tile * KEYS + half * MINE + lane_row;
-                return moved && lane_row < MINE && tile < s1 && j < it.total ? __ldg(pos + j) : 0;
+                const int j = tile * KEYS + group_tid;
+                return moved && group_tid < KEYS && tile < s1 && j < it.total ? __ldg(pos + j) : 0;
             };
             int next_at = position(s0);
 #pragma unroll 1
             for (int tile = s0; tile < s1; ++tile, ++n) {  // to its end even after a wait gave up: the halves meet at each tile
                 const int buf = PAIR ? group : n & 1;
-                const uint32_t tm_s = ctl->tmem + quarter + buf * 128 + half * MINE;
-                const int jb = tile * KEYS + half * MINE;
-                if (moved) {  // positions of these keys, by the 128 threads that have them, asked for a tile ahead
-                    quad_sync<PAIR>(tid >> 7);  // the last tile's have been read
+                const int of_tile = copy * S::OF_COPY + half * MINE;  // this thread's keys
+                const uint32_t tm_s = ctl->tmem + quarter + buf * 128 + of_tile;
+                const int jb = tile * KEYS + of_tile;
+                if (moved) {  // positions of the tile's keys, asked for a tile ahead
+                    group_sync<GROUP>(group);  // the last tile's have been read
                     // as distances to the item's first token where no window has to be exact: 32 bits hold those below 2^24
-                    if (lane_row < MINE)
-                        ctl->at.positions[tid >> 7][lane_row] = v.window > 0 ? next_at : __float_as_int(static_cast<float>(origin - next_at));
-                    quad_sync<PAIR>(tid >> 7);
+                    if (group_tid < KEYS)
+                        ctl->at.positions[group][group_tid] = v.window > 0 ? next_at : __float_as_int(static_cast<float>(origin - next_at));
+                    group_sync<GROUP>(group);
                     next_at = position(tile + 1);
                 }
                 ok = ok && tiles_wait(ctl, &ctl->s_full[buf], (PAIR ? n : n >> 1) & 1, err);
@@ -1085,18 +1100,21 @@ __device__ void tiles_rows(const TilesParams &p, TilesCtl<S> *ctl, unsigned *err
                         uint32_t y[LOAD];
                         if constexpr (LOAD == 64)
                             tc_ld64(y, tm_s + i);
-                        else
+                        else if constexpr (LOAD == 32)
                             tc_ld32(y, tm_s + i);
+                        else
+                            tc_ld16(y, tm_s + i);
 #pragma unroll
                         for (int e = 0; e < LOAD; e += 2) x[(i + e) / 2] = pack2(__uint_as_float(y[e]), __uint_as_float(y[e + 1]));
                     }
                     // The true scores are x f - off.
                     float f = factor, off = 0.0f;
-                    if (shaped) tile_shape<MINE, PAIR>(p, x, &f, &off, it.ctx, it.total, ctl, place, jb, own, slope, origin, tid >> 7);
+                    if (shaped) tile_shape<MINE, PAIR>(p, x, &f, &off, it.ctx, it.total, ctl, place, jb, own, slope, origin, ctl->at.positions[group] + of_tile);
                     const bool seen = see.lo <= jb && see.hi >= jb + MINE;
                     if (!__all_sync(0xffffffffu, seen)) {
 #pragma unroll
                         for (int i = 0; i < MINE; i += 32) {
+                            constexpr int AT_A_TIME = MINE < 32 ? MINE : 32;
                             const int lo = min(max(see.lo - jb - i, 0), 32), hi = min(max(see.hi - jb - i, 0), 32);
                             unsigned mask = hi == 32 ? 0xffffffffu : (1u << hi) - 1u;
                             if (!PAIR && p.parent) {
@@ -1105,7 +1123,7 @@ __device__ void tiles_rows(const TilesParams &p, TilesCtl<S> *ctl, unsigned *err
                             }
                             mask = lo == 32 ? 0u : mask & ~((1u << lo) - 1u);
 #pragma unroll
-                            for (int k = 0; k < 32; k += 2) {
+                            for (int k = 0; k < AT_A_TIME; k += 2) {
                                 const float2 y = unpair(x[(i + k) / 2]);
                                 x[(i + k) / 2] = pack2(mask >> k & 1 ? y.x : -CUDART_INF_F, mask >> (k + 1) & 1 ? y.y : -CUDART_INF_F);
                             }
@@ -1173,12 +1191,27 @@ __device__ void tiles_rows(const TilesParams &p, TilesCtl<S> *ctl, unsigned *err
                         }
                         if constexpr (AT_ONCE == 64)
                             tc_st32(tm_s + i0 / 2, pk);
-                        else
+                        else if constexpr (AT_ONCE == 32)
                             tc_st16(tm_s + i0 / 2, pk);
+                        else
+                            tc_st8(tm_s + i0 / 2, pk);
                         if (PAIR && i0 == 0) {  // the products with these may begin
                             tc_wait_st();
                             tc_fence_before();
                             mbar_arrive(&ctl->p_half[buf]);
+                        }
+                    }
+                    if (OF_ROW > 1) {  // no weights for the keys of the row's other copies
+                        uint32_t none[MINE / 2];
+#pragma unroll
+                        for (int i = 0; i < MINE / 2; ++i) none[i] = 0;
+#pragma unroll
+                        for (int i = 1; i < OF_ROW; ++i) {
+                            const uint32_t to = ctl->tmem + quarter + buf * 128 + (copy + i) % OF_ROW * S::OF_COPY + half * MINE;
+                            if constexpr (MINE == 32)
+                                tc_st16(to, none);
+                            else if constexpr (MINE == 16)
+                                tc_st8(to, none);
                         }
                     }
                     const float2 all = unpair(fadd2(sum[0], sum[1]));
@@ -1208,15 +1241,28 @@ __device__ void tiles_rows(const TilesParams &p, TilesCtl<S> *ctl, unsigned *err
             if (*reinterpret_cast<volatile int *>(&ctl->dead)) ctl->stop[group] = 1;
             if (t0 < t1) ctl->bad[group][(item - 1) % S::ITEMS] = 0;
         }
-        if (HALVES == 2) ctl->at.top[0][tid] = l;
+        if (HALVES == 2) ctl->at.top[0][tid] = l, ctl->at.top[1][tid] = m;
         group_sync<GROUP>(group);
         if (*reinterpret_cast<volatile int *>(&ctl->stop[group])) break;  // a wait gave up: this item is among what is lost
         if (HALVES == 2) l += ctl->at.top[0][tid ^ 128];
+        float part_of = 1.0f;  // what this copy's sums are multiplied by
+        if (OF_ROW > 1) {
+            float of_all = -CUDART_INF_F, sum = 0.0f;
+#pragma unroll
+            for (int i = 0; i < OF_ROW; ++i) of_all = fmaxf(of_all, ctl->at.top[1][i * S::ROWS + r]);
+            const float base = of_all == -CUDART_INF_F ? 0.0f : of_all;
+#pragma unroll
+            for (int i = 0; i < OF_ROW; ++i)
+                sum += (ctl->at.top[0][i * S::ROWS + r] + ctl->at.top[0][128 + i * S::ROWS + r]) * fast_exp2(ctl->at.top[1][i * S::ROWS + r] - base);
+            part_of = fast_exp2(m - base);
+            m = of_all;
+            l = sum;
+        }
         const bool whole = it.flags & ITEM_WHOLE;
         float *part = p.parts + (static_cast<int64_t>(blockIdx.x) * 2 + (it.flags & ITEM_SECOND ? 1 : 0)) * PART;
         const bool none = m == -CUDART_INF_F && l == 0.0f, fixed = none || any_bad;
         const float instead = any_bad ? CUDART_NAN_F : 0.0f, out_scale = v_scale / l;
-        if (half == 0 && mine) {
+        if (half == 0 && copy == 0 && mine) {
             if (!whole) {
                 part[r] = any_bad ? CUDART_NAN_F : m;
                 part[S::ROWS + r] = l;
@@ -1225,29 +1271,55 @@ __device__ void tiles_rows(const TilesParams &p, TilesCtl<S> *ctl, unsigned *err
             }
         }
         float odd = 0.0f;  // NaN if something is not finite
+        // With copies all but the first leave theirs in q's place, which is free by now, some columns at a time.
+        constexpr int AT_A_TIME = OF_ROW > 1 && D == 64 ? 16 : 32;
 #pragma unroll 1
-        for (int d0 = half * (D / HALVES); d0 < (half + 1) * (D / HALVES); d0 += 32) {
-            float x[32];
+        for (int d0 = half * (D / HALVES); d0 < (half + 1) * (D / HALVES); d0 += AT_A_TIME) {
+            float x[AT_A_TIME];
             __syncwarp();
             if (tiles) {
-                uint32_t y[32];
-                tc_ld32(y, tm_o + d0);
+                uint32_t y[AT_A_TIME];
+                if constexpr (AT_A_TIME == 32)
+                    tc_ld32(y, tm_o + d0);
+                else
+                    tc_ld16(y, tm_o + d0);
 #pragma unroll
-                for (int k = 0; k < 32; ++k) x[k] = __uint_as_float(y[k]);
+                for (int k = 0; k < AT_A_TIME; ++k) x[k] = __uint_as_float(y[k]);
             } else {
 #pragma unroll
-                for (int k = 0; k < 32; ++k) x[k] = 0.0f;
+                for (int k = 0; k < AT_A_TIME; ++k) x[k] = 0.0f;
             }
+            if (OF_ROW > 1 && t0 < t1) {
+                float *buf = reinterpret_cast<float *>(smem + (item - 1) % S::Q_PLACES * S::Q);
+#pragma unroll
+                for (int k = 0; k < AT_A_TIME; ++k) x[k] = part_of == 0.0f ? 0.0f : x[k] * part_of;  // a copy without keys: anything
+                group_sync<GROUP>(group);
+                if (copy > 0) {
+                    float *to = buf + ((2 * copy - 2 + half) * S::ROWS + r) * AT_A_TIME;
+#pragma unroll
+                    for (int k = 0; k < AT_A_TIME; ++k) to[(k + r) % AT_A_TIME] = x[k];  // a column's rows on different banks
+                }
+                group_sync<GROUP>(group);
+                if (copy == 0) {
+#pragma unroll
+                    for (int i = 0; i < OF_ROW - 1; ++i) {
+                        const float *from = buf + ((2 * i + half) * S::ROWS + r) * AT_A_TIME;
+#pragma unroll
+                        for (int k = 0; k < AT_A_TIME; ++k) x[k] += from[(k + r) % AT_A_TIME];
+                    }
+                }
+            }
+            if (copy > 0) continue;
             if (!mine) continue;
             // 32 bytes a store: a thread's row is its own, and half a sector at a time costs twice the transactions
             if (!whole) {
 #pragma unroll
-                for (int k = 0; k < 32; ++k) {
+                for (int k = 0; k < AT_A_TIME; ++k) {
                     x[k] = fixed ? 0.0f : x[k];
                     odd = fmaf(x[k], 0.0f, odd);
                 }
 #pragma unroll
-                for (int k = 0; k < 32; k += 8) {
+                for (int k = 0; k < AT_A_TIME; k += 8) {
                     uint32_t y[8];
 #pragma unroll
                     for (int e = 0; e < 8; ++e) y[e] = __float_as_uint(x[k + e]);
@@ -1255,12 +1327,12 @@ __device__ void tiles_rows(const TilesParams &p, TilesCtl<S> *ctl, unsigned *err
                 }
             } else {
 #pragma unroll
-                for (int k = 0; k < 32; ++k) {
+                for (int k = 0; k < AT_A_TIME; ++k) {
                     x[k] = fixed ? instead : x[k] * out_scale;
                     odd = fmaf(x[k], 0.0f, odd);
                 }
 #pragma unroll
-                for (int k = 0; k < 32; k += 16) {
+                for (int k = 0; k < AT_A_TIME; k += 16) {
                     uint32_t y[8];
 #pragma unroll
                     for (int e = 0; e < 8; ++e)
@@ -1271,18 +1343,23 @@ __device__ void tiles_rows(const TilesParams &p, TilesCtl<S> *ctl, unsigned *err
             }
         }
         tc_fence_before();
+        if (OF_ROW > 1 && t0 < t1) {
+            fence_async_shared();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&ctl->q_empty[(item - 1) % S::Q_PLACES]);
+        }
         if (odd != odd && !any_bad) *reinterpret_cast<volatile int *>(&ctl->lost[group]) = 1;
     }
     group_sync<GROUP>(group);
     const bool again = *reinterpret_cast<volatile int *>(&ctl->lost[group]), stopped = *reinterpret_cast<volatile int *>(&ctl->stop[group]);
-    if (again || stopped) tiles_finish<C, D, PAIR>(p, again, stopped ? k : 0x7fffffff, group, group_tid);
+    if (again || stopped) tiles_finish<C, D, COPIES>(p, again, stopped ? k : 0x7fffffff, group, group_tid);
 }
 
-template <typename C, int D, bool PAIR>
+template <typename C, int D, int COPIES>
 __global__ void __launch_bounds__(TILES_THREADS, 1)
     tiles_kernel(const TilesParams p, const __grid_constant__ CUtensorMap map_k, const __grid_constant__ CUtensorMap map_v, const int maps)
 {
-    using S = TilesShape<C, D, PAIR>;
+    using S = TilesShape<C, D, COPIES>;
     using Ctl = TilesCtl<S>;
     extern __shared__ __align__(1024) char smem[];  // the swizzle's rows of 128 bytes come in groups of eight
     Ctl *ctl = reinterpret_cast<Ctl *>(smem + S::CTL_AT);
@@ -1325,31 +1402,31 @@ __global__ void __launch_bounds__(TILES_THREADS, 1)
     }
     // registers: launched with 128 a thread, 4 x 128 = 2 x 184 + 2 x 72 (a row's 128 scores) or 2 x 160 + 2 x 96
     if (warp < 8) {
-        if (PAIR)
+        if (S::PAIR)
             asm volatile("setmaxnreg.inc.sync.aligned.u32 184;");
         else
             asm volatile("setmaxnreg.inc.sync.aligned.u32 160;");
-        tiles_rows<C, D, PAIR>(p, ctl, err, tid);
+        tiles_rows<C, D, COPIES>(p, smem, ctl, err, tid);
     } else if (warp < 12) {
-        if (PAIR)
+        if (S::PAIR)
             asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
         else
             asm volatile("setmaxnreg.dec.sync.aligned.u32 96;");
         if (warp == 8) {
-            tiles_multiply<C, D, PAIR>(smem, ctl, err, lane);
+            tiles_multiply<C, D, COPIES>(smem, ctl, err, lane);
             warp_commit(&ctl->spare);  // what was issued ends before the block may: others may have given up on it
             mbar_drain(&ctl->spare, 0);
         } else if (warp == 9) {
             tiles_items<S>(p, c, ctl, err, lane);
         } else {
-            tiles_prepare<C, D, PAIR>(p, smem, ctl, err, tid - 320);
+            tiles_prepare<C, D, COPIES>(p, smem, ctl, err, tid - 320);
         }
     } else {
-        if (PAIR)
+        if (S::PAIR)
             asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
         else
             asm volatile("setmaxnreg.dec.sync.aligned.u32 96;");
-        tiles_load<C, D, PAIR>(p, smem, ctl, err, tid - 384, maps ? &map_k : nullptr, maps ? &map_v : nullptr);
+        tiles_load<C, D, COPIES>(p, smem, ctl, err, tid - 384, maps ? &map_k : nullptr, maps ? &map_v : nullptr);
     }
     tc_fence_before();
     __syncthreads();
@@ -1357,12 +1434,12 @@ __global__ void __launch_bounds__(TILES_THREADS, 1)
     if (warp == 8) tmem_free(ctl->tmem, 512);
 }
 
-template <typename C, int D, bool PAIR> cudaError_t launch_tiles_of(TilesParams p, const KvLaunch &L, cudaStream_t st)
+template <typename C, int D, int COPIES> cudaError_t launch_tiles_of(TilesParams p, const KvLaunch &L, cudaStream_t st)
 {
-    using S = TilesShape<C, D, PAIR>;
+    using S = TilesShape<C, D, COPIES>;
     constexpr int SMEM = S::CTL_AT + static_cast<int>(sizeof(TilesCtl<S>));
     static_assert(SMEM <= 232448, "shared memory of a block");
-    auto kernel = tiles_kernel<C, D, PAIR>;
+    auto kernel = tiles_kernel<C, D, COPIES>;
     cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, SMEM);
     if (e != cudaSuccess) return e;
     p.w.tile = S::KEYS;
@@ -1373,12 +1450,21 @@ template <typename C, int D, bool PAIR> cudaError_t launch_tiles_of(TilesParams 
     e = launch_chained(kernel, dim3(ATT_SMS), TILES_THREADS, SMEM, st, p, map_k, map_v, static_cast<int>(maps));
     return e != cudaSuccess ? e : launch_join(p, L.dtype, D, S::ROWS, ATT_SMS, st);
 }
+template <typename C, int D> cudaError_t launch_tiles_dim(const TilesParams &p, const KvLaunch &L, bool pairs, cudaStream_t st)
+{
+    if (pairs) return launch_tiles_of<C, D, 0>(p, L, st);
+    if constexpr (sizeof(C) == 2) {  // (of e4m3 so few rows are a rare prompt)
+        if (p.rows <= 32) return launch_tiles_of<C, D, 4>(p, L, st);
+    }
+    if (p.rows <= 64) return launch_tiles_of<C, D, 2>(p, L, st);
+    return launch_tiles_of<C, D, 1>(p, L, st);
+}
 template <typename C> cudaError_t launch_tiles_types(const TilesParams &p, const KvLaunch &L, bool pairs, cudaStream_t st)
 {
     switch (L.cache.head_dim) {
-    case 64: return pairs ? launch_tiles_of<C, 64, true>(p, L, st) : launch_tiles_of<C, 64, false>(p, L, st);
-    case 128: return pairs ? launch_tiles_of<C, 128, true>(p, L, st) : launch_tiles_of<C, 128, false>(p, L, st);
-    default: return launch_tiles_of<C, 256, false>(p, L, st);
+    case 64: return launch_tiles_dim<C, 64>(p, L, pairs, st);
+    case 128: return launch_tiles_dim<C, 128>(p, L, pairs, st);
+    default: return launch_tiles_of<C, 256, 1>(p, L, st);
     }
 }
 
