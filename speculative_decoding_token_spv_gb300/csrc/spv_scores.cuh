@@ -74,6 +74,7 @@ __device__ __forceinline__ float2 unpair(unsigned long long x)
 // x f P((x f / cap)^2) of pairs, P of N coefficients.
 template <int M, int N> __device__ __forceinline__ void cap_polynomial(const ScoresView &v, unsigned long long (&x)[M], float f, const float (&c)[N])
 {
+    asm volatile("" : "+f"(f));  // the coefficients are made here, and not kept in registers from tile to tile
     const float u = f * v.cap_inv;
     const unsigned long long u2 = pack2(u, u);
     unsigned long long k[N];

@@ -13,10 +13,12 @@
 // time).  One block an SM with an equal range of all tiles of all items, found
 // from the lengths on the device; in it
 //   * PAIR: 256 rows as two tiles of 128.  Four warps hold the first's rows, a
-//     row a thread, four the second's, and while one of them makes its
-//     exponentials the tensor cores have the products of the other.  Scores and
-//     outputs of both fill tensor memory (2 x 128 + 2 x 128 columns); the
-//     weights go where their scores were;
+//     row a thread, four the second's.  Tiles of keys are 64 long, so that beside
+//     the outputs of both (2 x 128 columns of tensor memory) two tiles of scores
+//     of each fit: the next one's products are there when a thread has made its
+//     weights, which go where their scores were, and their way through the tensor
+//     cores is behind the exponentials.  (With tiles of 128 the warps waited for
+//     them: 609 us for the prompt below.)
 //   * else 128 rows, of which two warps share each row's keys (few rows; and D =
 //     256, whose outputs take half of tensor memory).  Scores stand in two
 //     places in turn.  64 rows or fewer stand in tensor memory twice, 32 or fewer
@@ -60,8 +62,10 @@ struct TilesParams : ScoredParams {
 template <typename C, int D, int COPIES> struct TilesShape {
     static constexpr bool PAIR = COPIES == 0;
     static constexpr bool WIDEN = sizeof(C) == 1;
+    static constexpr int PLACE = PAIR ? 64 : 128;                // columns from one place of scores to the next
     static constexpr int SUBS = PAIR ? 2 : 1, ROWS = PAIR ? 256 : 128 / (PAIR ? 1 : COPIES);
-    static constexpr int KEYS = D == 256 ? 64 : 128;             // of a tile
+    static constexpr int KEYS = PAIR || D == 256 ? 64 : 128;     // of a tile
+    static constexpr int OVERHEAD = PAIR ? 6 : 2;                // tiles that an item's beginning and end take as long as
     static constexpr int OF_COPY = KEYS / (PAIR ? 1 : COPIES);   // of them a copy's
     static constexpr int MINE = PAIR ? KEYS : OF_COPY / 2;       // and a thread's
     static constexpr int TILE = KEYS * D * 2, RAW = KEYS * D;    // bytes of K or V as multiplied, and of e4m3
@@ -93,7 +97,7 @@ enum TileFlags { ITEM_BAD = 1, ITEM_WHOLE = 2, ITEM_SECOND = 4, ITEM_END = 8 }; 
 template <typename S> struct TilesCtl {
     TileItem items[2];
     uint64_t item_full[2], item_empty[2];
-    uint64_t full[S::STAGES], empty[S::STAGES], s_full[2], p_half[2], p_full[2], o_done[2], q_full[2], q_empty[2], spare;
+    uint64_t full[S::STAGES], empty[S::STAGES], s_full[4], p_full[4], o_done[4], q_full[2], q_empty[2], spare;
     uint64_t raw_full[S::WIDEN ? 4 : 1][S::WIDEN ? S::RAW_STAGES : 1];  // of each loader warp's rows
     char bad[2][S::ITEMS];                                       // a page id outside the pool, for each group of row warps
     int stop[2], lost[2];
@@ -209,7 +213,6 @@ template <typename S> __device__ __forceinline__ TileLens item_tiles(const Tiles
 __device__ __forceinline__ int count_of(const TileLens &s) { return max(1, s.to - s.from); }
 // An item's beginning and end -- its q, the first scores, writing the rows -- take about as long as OVERHEAD tiles, and the
 // ranges are cut as if it had so many more, before the first.
-constexpr int TILES_OVERHEAD = 2;
 
 // The block's range, by all its threads; `c` is the same for all.
 template <typename S> __device__ TileCursor tiles_find(const TilesParams &p, TilesCtl<S> *ctl, int tid)
@@ -234,7 +237,7 @@ template <typename S> __device__ TileCursor tiles_find(const TilesParams &p, Til
         return mine;
     };
     long long sum = 0;
-    for (int e = e0; e < e1; e += 32) sum += count32(e) + (e + lane < e1 ? TILES_OVERHEAD : 0);
+    for (int e = e0; e < e1; e += 32) sum += count32(e) + (e + lane < e1 ? S::OVERHEAD : 0);
 #pragma unroll
     for (int o = 16; o; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
     if (lane == 0) ctl->find.sums[warp] = sum * p.c.kv_heads;
@@ -254,7 +257,7 @@ template <typename S> __device__ TileCursor tiles_find(const TilesParams &p, Til
         c.end = range_begin(c, block + 1);
         if (c.at >= before && c.at < before + mine) {
             for (int e = e0; e < e1; e += 32) {
-                const int n = count32(e), units = n + (e + lane < e1 ? TILES_OVERHEAD : 0);
+                const int n = count32(e), units = n + (e + lane < e1 ? S::OVERHEAD : 0);
                 int upto = units;
 #pragma unroll
                 for (int o = 1; o < 32; o <<= 1) {
@@ -269,8 +272,8 @@ template <typename S> __device__ TileCursor tiles_find(const TilesParams &p, Til
                     c.tiles = tiles;
                     c.b = (e + l) / p.w.row_tiles;
                     c.row_tile = e + l - c.b * p.w.row_tiles;
-                    c.h = static_cast<int>(quotient(c.at - before, tiles + TILES_OVERHEAD));
-                    c.first = before + static_cast<long long>(c.h) * (tiles + TILES_OVERHEAD) + TILES_OVERHEAD;
+                    c.h = static_cast<int>(quotient(c.at - before, tiles + S::OVERHEAD));
+                    c.first = before + static_cast<long long>(c.h) * (tiles + S::OVERHEAD) + S::OVERHEAD;
                     if (c.at < c.first) c.at = c.first < c.end ? c.first : c.end;
                     if (lane == 0) ctl->find.start = c;
                     break;
@@ -300,7 +303,7 @@ template <typename S> __device__ __noinline__ TileCursor tiles_find_again(const 
             c.row_tile = e - c.b * p.w.row_tiles;
             c.s = item_tiles<S>(p, tiles_lens(p, c.b), c.b, c.row_tile, lane);
             c.tiles = count_of(c.s);
-            const long long units = static_cast<long long>(c.tiles + TILES_OVERHEAD) * p.c.kv_heads;
+            const long long units = static_cast<long long>(c.tiles + S::OVERHEAD) * p.c.kv_heads;
             if (pass == 1 && before + units > c.at) break;
             before += units;
         }
@@ -313,15 +316,15 @@ template <typename S> __device__ __noinline__ TileCursor tiles_find_again(const 
             c.end = range_begin(c, blockIdx.x + 1);
         }
     }
-    c.h = static_cast<int>(quotient(c.at - before, c.tiles + TILES_OVERHEAD));
-    c.first = before + static_cast<long long>(c.h) * (c.tiles + TILES_OVERHEAD) + TILES_OVERHEAD;
+    c.h = static_cast<int>(quotient(c.at - before, c.tiles + S::OVERHEAD));
+    c.first = before + static_cast<long long>(c.h) * (c.tiles + S::OVERHEAD) + S::OVERHEAD;
     if (c.at < c.first) c.at = c.first < c.end ? c.first : c.end;
     return c;
 }
 // To the next item; a whole warp.
 template <typename S> __device__ __forceinline__ void tiles_next(TileCursor &c, const TilesParams &p, int lane)
 {
-    c.first += c.tiles + TILES_OVERHEAD;
+    c.first += c.tiles + S::OVERHEAD;
     c.at = c.first;
     if (++c.h < p.c.kv_heads) return;
     c.h = 0;
@@ -381,10 +384,11 @@ template <typename Ctl> __device__ __forceinline__ bool take_item(Ctl *ctl, int 
     if (!tiles_wait(ctl, &ctl->item_full[k & 1], (k >> 1) & 1, err)) return false;
     const int4 *from = reinterpret_cast<const int4 *>(&ctl->items[k & 1]);
     const int4 x = from[0], y = from[1], z = from[2];
-    it->b = x.x, it->row_tile = x.y, it->h = x.z, it->flags = x.w;
-    it->ctx = y.x, it->fresh = y.y, it->total = y.z, it->t0 = y.w;
-    it->t1 = z.x, it->lo0 = z.y, it->hi0 = z.z, it->lo1 = z.w;
-    it->hi1 = from[3].x;
+    // the same in all lanes, and the compiler is told so: what depends on them is then decided once for the warp
+    it->b = same_in_warp(x.x), it->row_tile = same_in_warp(x.y), it->h = same_in_warp(x.z), it->flags = same_in_warp(x.w);
+    it->ctx = same_in_warp(y.x), it->fresh = same_in_warp(y.y), it->total = same_in_warp(y.z), it->t0 = same_in_warp(y.w);
+    it->t1 = same_in_warp(z.x), it->lo0 = same_in_warp(z.y), it->hi0 = same_in_warp(z.z), it->lo1 = same_in_warp(z.w);
+    it->hi1 = same_in_warp(from[3].x);
     __syncwarp();
     if (lane == 0) mbar_arrive(&ctl->item_empty[k & 1]);
     return !(it->flags & ITEM_END);
@@ -572,8 +576,8 @@ __device__ void tiles_multiply(char *smem, TilesCtl<S> *ctl, unsigned *err, int 
     // all values here are the same in all lanes, and the compiler is told so
     const uint32_t base = smem_u32(smem), tmem = same_in_warp(ctl->tmem);
     int st = 0, phase = 0;             // the ring's place and pass of the next tile of K; V's is the one behind it
-    int item = 0, buf = 0;
-    uint32_t passes = 0;               // bit s: parity of the weights' barrier of place s
+    int item = 0, turn0 = 0, turn1 = 0, out0 = 0, out1 = 0;  // which place is next, for scores and for outputs
+    uint32_t passes = 0;               // bit i: parity of the weights' barrier of place i
     auto after = [&](int x) { return x + 1 == NST ? 0 : x + 1; };
     TileItem it;
     for (int k = 0; take_item(ctl, k, &it, err, lane); ++k) {
@@ -583,91 +587,69 @@ __device__ void tiles_multiply(char *smem, TilesCtl<S> *ctl, unsigned *err, int 
         if (!tiles_wait(ctl, &ctl->q_full[place], (item / S::Q_PLACES) & 1, err)) return;
         ++item;
         const uint32_t q0 = desc_low(base + place * S::Q, 16);
-        auto scores = [&](int s, int k_st) {  // of the rows' tile (PAIR) or place s with a tile of keys
+        // s: the tile of rows (PAIR; else 0).  Its tiles of keys have two places of scores in turn.
+        auto scores = [&](int s, int k_st) {
             tc_fence_after();
-            const uint32_t q = q0 + (PAIR ? s * (S::Q_SUB >> 4) : 0), k = desc_low(base + S::K_AT + k_st * S::TILE, 16);
+            const int place = s * 2 + (PAIR && s ? turn1 : turn0);
+            const uint32_t q = q0 + s * (S::Q_SUB >> 4), k = desc_low(base + S::K_AT + k_st * S::TILE, 16), to = tmem + place * S::PLACE;
 #pragma unroll
             for (int ks = 0; ks < D / 16; ++ks)
-                warp_mma<QK>(tmem + s * 128, q + (((ks >> 2) * (128 * 128) + (ks & 3) * 32) >> 4),
-                             k + (((ks >> 2) * (KEYS * 128) + (ks & 3) * 32) >> 4), ks > 0);
-            warp_commit(&ctl->s_full[s]);
+                warp_mma<QK>(to, q + (((ks >> 2) * (128 * 128) + (ks & 3) * 32) >> 4), k + (((ks >> 2) * (KEYS * 128) + (ks & 3) * 32) >> 4), ks > 0);
+            warp_commit(&ctl->s_full[place]);
+            (PAIR && s ? turn1 : turn0) ^= 1;
         };
-        auto outputs = [&](int s, int v_st, bool add, bool done) {
-            const uint32_t o = tmem + 256 + (PAIR ? s * 128 : 0), v = desc_low(base + S::K_AT + v_st * S::TILE, KEYS * 128);
-            // PAIR: the first half of the weights is there before the second
-            if (!tiles_wait(ctl, PAIR ? &ctl->p_half[s] : &ctl->p_full[s], passes >> s & 1, err)) return false;
+        auto outputs = [&](int s, int v_st, bool add) {
+            const int place = s * 2 + (PAIR && s ? out1 : out0);
+            const uint32_t o = tmem + 256 + s * 128, w = tmem + place * S::PLACE, v = desc_low(base + S::K_AT + v_st * S::TILE, KEYS * 128);
+            if (!tiles_wait(ctl, &ctl->p_full[place], passes >> place & 1, err)) return false;
             tc_fence_after();
 #pragma unroll
-            for (int ks = 0; ks < KEYS / 16; ++ks) {
-                if (PAIR && ks == KEYS / 32) {
-                    if (!tiles_wait(ctl, &ctl->p_full[s], passes >> s & 1, err)) return false;
-                    tc_fence_after();
-                }
-                warp_mma_ta<PV>(o, tmem + s * 128 + 16 * ks / S::MINE * S::MINE + 16 * ks % S::MINE / 2, v + ks * (2048 >> 4),
-                                add || ks > 0);
-            }
-            passes ^= 1u << s;
-            if (done) warp_commit(&ctl->o_done[s]);
+            for (int ks = 0; ks < KEYS / 16; ++ks)
+                warp_mma_ta<PV>(o, w + 16 * ks / S::MINE * S::MINE + 16 * ks % S::MINE / 2, v + ks * (2048 >> 4), add || ks > 0);
+            passes ^= 1u << place;
+            warp_commit(&ctl->o_done[place]);
+            (PAIR && s ? out1 : out0) ^= 1;
             return true;
         };
         auto full = [&](int place, int pass) { return tiles_wait(ctl, &ctl->full[place], pass, err); };
-        if constexpr (PAIR) {
-            const int lo0 = same_in_warp(it.lo0), hi0 = same_in_warp(it.hi0), lo1 = same_in_warp(it.lo1), hi1 = same_in_warp(it.hi1);
-            bool begun0 = false, begun1 = false, pending0 = false, pending1 = false;
-            int v_st = 0, v_pass = 0;
-            for (int i = 0; i <= tiles; ++i) {  // the outputs of the tile before, and the scores of this one
-                const bool keys = i < tiles;
-                const bool here0 = keys && t0 + i >= lo0 && t0 + i < hi0, here1 = keys && t0 + i >= lo1 && t0 + i < hi1;
-                if (i > 0 && !full(v_st, v_pass)) return;
-                if (pending0) {
-                    if (!outputs(0, v_st, begun0, !here0)) return;
-                    begun0 = true;
-                }
-                if (keys && !full(st, phase)) return;
+        const int lo0 = PAIR ? it.lo0 : t0, hi0 = PAIR ? it.hi0 : t0 + tiles, lo1 = it.lo1, hi1 = it.hi1;
+        bool begun0 = false, begun1 = false, pending0 = false, pending1 = false;
+        int v_st = 0, v_pass = 0;
+        for (int i = 0; i <= tiles; ++i) {  // the scores of a tile, and the outputs of the one before
+            const bool keys = i < tiles;
+            const bool here0 = keys && t0 + i >= lo0 && t0 + i < hi0, here1 = PAIR && keys && t0 + i >= lo1 && t0 + i < hi1;
+            if (keys) {
+                if (!full(st, phase)) return;
                 if (here0) scores(0, st);
-                if (pending1) {
-                    if (!outputs(1, v_st, begun1, !here1)) return;
-                    begun1 = true;
-                }
-                if (i > 0) warp_commit(&ctl->empty[v_st]);
                 if (here1) scores(1, st);
-                pending0 = here0;
-                pending1 = here1;
-                if (!keys) break;
                 warp_commit(&ctl->empty[st]);
                 if (i == tiles - 1) warp_commit(&ctl->q_empty[place]);
-                st = after(st);
-                if (st == 0) phase ^= 1;
-                v_st = st, v_pass = phase;
-                st = after(st);
-                if (st == 0) phase ^= 1;
             }
-        } else {
-            // the places of scores go on in turn from item to item
-            int v_st[2] = {0, 0}, v_pass[2] = {0, 0};
-            for (int i = 0; i < tiles + 2; ++i) {  // the outputs of the tile two before, and the scores of this one
-                const int s = buf;
-                if (i >= 2) {
-                    if (!full(v_st[0], v_pass[0])) return;
-                    if (!outputs(s, v_st[0], i > 2, true)) return;
-                    warp_commit(&ctl->empty[v_st[0]]);
+            if (i > 0) {
+                if (!full(v_st, v_pass)) return;
+                if (pending0) {
+                    if (!outputs(0, v_st, begun0)) return;
+                    begun0 = true;
                 }
-                v_st[0] = v_st[1], v_pass[0] = v_pass[1];
-                if (i < tiles) {
-                    if (!full(st, phase)) return;
-                    scores(s, st);
-                    warp_commit(&ctl->empty[st]);
-                    st = after(st);
-                    if (st == 0) phase ^= 1;
-                    v_st[1] = st, v_pass[1] = phase;
-                    st = after(st);
-                    if (st == 0) phase ^= 1;
+                if (pending1) {
+                    if (!outputs(1, v_st, begun1)) return;
+                    begun1 = true;
                 }
-                if (i == tiles - 1) warp_commit(&ctl->q_empty[place]);
-                buf ^= 1;
+                warp_commit(&ctl->empty[v_st]);
             }
-            // two turns more than tiles: the next item begins at the place behind this one's last
+            pending0 = here0;
+            pending1 = here1;
+            st = after(st);
+            if (st == 0) phase ^= 1;
+            v_st = st, v_pass = phase;
+            st = after(st);
+            if (st == 0) phase ^= 1;
         }
+        // one turn more than tiles
+        if (st == 0) phase ^= 1;
+        st = st == 0 ? NST - 1 : st - 1;
+        if (st == 0) phase ^= 1;
+        st = st == 0 ? NST - 1 : st - 1;
     }
 }
 
@@ -1009,14 +991,14 @@ __device__ void tiles_rows(const TilesParams &p, char *smem, TilesCtl<S> *ctl, u
     constexpr int KEYS = S::KEYS, MINE = S::MINE, GROUP = S::GROUP, PART = S::ROWS * (D + 2);
     constexpr bool PAIR = S::PAIR;
     constexpr int HALVES = PAIR ? 1 : 2, OF_ROW = PAIR ? 1 : COPIES;
-    const int lane = tid & 31, half = PAIR ? 0 : tid >> 7, group = PAIR ? tid >> 7 : 0, lane_row = tid & 127;
+    const int lane = tid & 31, quad = same_in_warp(tid >> 7), half = PAIR ? 0 : quad, group = PAIR ? quad : 0, lane_row = tid & 127;
     const int copy = PAIR ? 0 : lane_row / S::ROWS;
     const int r = PAIR ? 128 * group + lane_row : lane_row % S::ROWS, group_tid = tid - 128 * group;  // row of the item; place in the group
     const uint32_t quarter = static_cast<uint32_t>(lane_row & ~31) << 16;
     const uint32_t tm_o = ctl->tmem + quarter + 256 + group * 128;
     const ScoresView &v = p.sc;
     const bool moved = moved_slots(v);
-    int n = 0, item = 0, outs = 0;  // tiles of this group; items with tiles; items with outputs of this group (PAIR)
+    int n = 0, item = 0;  // tiles of this group; items with tiles
     TileItem it;
     int k = 0;
     bool ok = true;
@@ -1069,6 +1051,9 @@ __device__ void tiles_rows(const TilesParams &p, char *smem, TilesCtl<S> *ctl, u
             }
             const bool shaped = v.cap2 != 0.0f || v.slopes || moved || __any_sync(0xffffffffu, !(factor > 0.0f));
             const bool works = __any_sync(0xffffffffu, there);
+            // the slots that all rows of the warp see (votes of each tile took hundreds of cycles)
+            const int all_lo = __reduce_max_sync(0xffffffffu, see.lo), all_hi = __reduce_min_sync(0xffffffffu, see.hi);
+            bool huge = false;  // scores beyond what a fused difference allows
             auto position = [&](int tile) {
                 const int j = tile * KEYS + group_tid;
                 return moved && group_tid < KEYS && tile < s1 && j < it.total ? __ldg(pos + j) : 0;
@@ -1076,9 +1061,9 @@ __device__ void tiles_rows(const TilesParams &p, char *smem, TilesCtl<S> *ctl, u
             int next_at = position(s0);
 #pragma unroll 1
             for (int tile = s0; tile < s1; ++tile, ++n) {  // to its end even after a wait gave up: the halves meet at each tile
-                const int buf = PAIR ? group : n & 1;
+                const int buf = group * 2 + (n & 1);
                 const int of_tile = copy * S::OF_COPY + half * MINE;  // this thread's keys
-                const uint32_t tm_s = ctl->tmem + quarter + buf * 128 + of_tile;
+                const uint32_t tm_s = ctl->tmem + quarter + buf * S::PLACE + of_tile;
                 const int jb = tile * KEYS + of_tile;
                 if (moved) {  // positions of the tile's keys, asked for a tile ahead
                     group_sync<GROUP>(group);  // the last tile's have been read
@@ -1088,7 +1073,7 @@ __device__ void tiles_rows(const TilesParams &p, char *smem, TilesCtl<S> *ctl, u
                     group_sync<GROUP>(group);
                     next_at = position(tile + 1);
                 }
-                ok = ok && tiles_wait(ctl, &ctl->s_full[buf], (PAIR ? n : n >> 1) & 1, err);
+                ok = ok && tiles_wait(ctl, &ctl->s_full[buf], (n >> 1) & 1, err);
                 tc_fence_after();
                 __syncwarp();
                 if (works) {
@@ -1110,8 +1095,7 @@ __device__ void tiles_rows(const TilesParams &p, char *smem, TilesCtl<S> *ctl, u
                     // The true scores are x f - off.
                     float f = factor, off = 0.0f;
                     if (shaped) tile_shape<MINE, PAIR>(p, x, &f, &off, it.ctx, it.total, ctl, place, jb, own, slope, origin, ctl->at.positions[group] + of_tile);
-                    const bool seen = see.lo <= jb && see.hi >= jb + MINE;
-                    if (!__all_sync(0xffffffffu, seen)) {
+                    if (all_lo > jb || all_hi < jb + MINE) {
 #pragma unroll
                         for (int i = 0; i < MINE; i += 32) {
                             constexpr int AT_A_TIME = MINE < 32 ? MINE : 32;
@@ -1145,16 +1129,17 @@ __device__ void tiles_rows(const TilesParams &p, char *smem, TilesCtl<S> *ctl, u
                         ctl->at.top[n & 1][tid] = top;
                         halves_sync(lane_row / 32);  // (the places of two tiles: the one before has been read when both are here)
                         top = fmaxf(top, ctl->at.top[n & 1][tid ^ 128]);
-                        if (n >= 2) ok = ok && tiles_wait(ctl, &ctl->o_done[buf], ((n - 2) >> 1) & 1, err);
                     }
+                    if (n >= 2) ok = ok && tiles_wait(ctl, &ctl->o_done[buf], ((n - 2) >> 1) & 1, err);
                     if (tile == s0) {
                         m = top - UP;
+                        huge = __any_sync(0xffffffffu, fabsf(m) > 0x1p20f && m != -CUDART_INF_F);
                     } else if (__any_sync(0xffffffffu, top - m > UP + Weights<M>::LAG)) {  // as a difference: a sum may round up to a score 16 above
                         const float grown = fmaxf(m, top - UP), a = grown == -CUDART_INF_F ? 0.0f : fast_exp2(m - grown);
                         m = grown;
+                        huge |= __any_sync(0xffffffffu, fabsf(m) > 0x1p20f && m != -CUDART_INF_F);
                         l *= a;
-                        // PAIR: the scores were issued behind the outputs before them and are there
-                        if (HALVES == 2) ok = ok && tiles_wait(ctl, &ctl->o_done[(n - 1) & 1], ((n - 1) >> 1) & 1, err);
+                        ok = ok && tiles_wait(ctl, &ctl->o_done[buf ^ 1], ((n - 1) >> 1) & 1, err);
                         tc_fence_after();
 #pragma unroll 1
                         for (int i = half * (D / HALVES); i < (half + 1) * (D / HALVES); i += 16) {
@@ -1166,7 +1151,7 @@ __device__ void tiles_rows(const TilesParams &p, char *smem, TilesCtl<S> *ctl, u
                         }
                     }
                     float base = m == -CUDART_INF_F ? 0.0f : m + off;
-                    if (__any_sync(0xffffffffu, fabsf(base) > 0x1p20f)) {
+                    if (huge) {
                         // the score is rounded as m was, not fused with the difference: of scores this large the largest would
                         // else miss m by more than a weight can hold
                         const unsigned long long f2 = pack2(f, f), none = pack2(-off, -off);
@@ -1195,11 +1180,6 @@ __device__ void tiles_rows(const TilesParams &p, char *smem, TilesCtl<S> *ctl, u
                             tc_st16(tm_s + i0 / 2, pk);
                         else
                             tc_st8(tm_s + i0 / 2, pk);
-                        if (PAIR && i0 == 0) {  // the products with these may begin
-                            tc_wait_st();
-                            tc_fence_before();
-                            mbar_arrive(&ctl->p_half[buf]);
-                        }
                     }
                     if (OF_ROW > 1) {  // no weights for the keys of the row's other copies
                         uint32_t none[MINE / 2];
@@ -1207,7 +1187,7 @@ __device__ void tiles_rows(const TilesParams &p, char *smem, TilesCtl<S> *ctl, u
                         for (int i = 0; i < MINE / 2; ++i) none[i] = 0;
 #pragma unroll
                         for (int i = 1; i < OF_ROW; ++i) {
-                            const uint32_t to = ctl->tmem + quarter + buf * 128 + (copy + i) % OF_ROW * S::OF_COPY + half * MINE;
+                            const uint32_t to = ctl->tmem + quarter + buf * S::PLACE + (copy + i) % OF_ROW * S::OF_COPY + half * MINE;
                             if constexpr (MINE == 32)
                                 tc_st16(to, none);
                             else if constexpr (MINE == 16)
@@ -1217,20 +1197,11 @@ __device__ void tiles_rows(const TilesParams &p, char *smem, TilesCtl<S> *ctl, u
                     const float2 all = unpair(fadd2(sum[0], sum[1]));
                     l += all.x + all.y;
                     tc_wait_st();
-                } else if (PAIR) {
-                    mbar_arrive(&ctl->p_half[buf]);
                 }
                 tc_fence_before();
                 mbar_arrive(&ctl->p_full[buf]);
             }
-            if (PAIR) {
-                if (s0 < s1) {
-                    ok = ok && tiles_wait(ctl, &ctl->o_done[group], outs & 1, err);
-                    ++outs;
-                }
-            } else {
-                ok = ok && tiles_wait(ctl, &ctl->o_done[(n - 1) & 1], ((n - 1) >> 1) & 1, err);
-            }
+            if (s0 < s1) ok = ok && tiles_wait(ctl, &ctl->o_done[group * 2 + ((n - 1) & 1)], ((n - 1) >> 1) & 1, err);
             tc_fence_after();
             any_bad |= *reinterpret_cast<volatile char *>(&ctl->bad[group][item % S::ITEMS]) != 0;
             ++item;
@@ -1370,13 +1341,14 @@ __global__ void __launch_bounds__(TILES_THREADS, 1)
             mbar_init(&ctl->full[i], 4);  // the loaders' warps
             mbar_init(&ctl->empty[i], 1);
         }
-        for (int i = 0; i < 2; ++i) {
+        for (int i = 0; i < 4; ++i) {
             mbar_init(&ctl->s_full[i], 1);
-            mbar_init(&ctl->item_full[i], 1);
-            mbar_init(&ctl->item_empty[i], TILES_TAKERS);
-            mbar_init(&ctl->p_half[i], S::GROUP);
             mbar_init(&ctl->p_full[i], S::GROUP);
             mbar_init(&ctl->o_done[i], 1);
+        }
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(&ctl->item_full[i], 1);
+            mbar_init(&ctl->item_empty[i], TILES_TAKERS);
             mbar_init(&ctl->q_full[i], TILES_PREPARE);
             mbar_init(&ctl->q_empty[i], 1 + 8);  // the products' end, and the row warps, who have read what lies beside q
             ctl->stop[i] = ctl->lost[i] = 0;
@@ -1400,18 +1372,12 @@ __global__ void __launch_bounds__(TILES_THREADS, 1)
         if (warp == 8) tmem_free(ctl->tmem, 512);
         return;
     }
-    // registers: launched with 128 a thread, 4 x 128 = 2 x 184 + 2 x 72 (a row's 128 scores) or 2 x 160 + 2 x 96
+    // registers: launched with 128 a thread, 4 x 128 = 2 x 160 + 2 x 96
     if (warp < 8) {
-        if (S::PAIR)
-            asm volatile("setmaxnreg.inc.sync.aligned.u32 184;");
-        else
-            asm volatile("setmaxnreg.inc.sync.aligned.u32 160;");
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 160;");
         tiles_rows<C, D, COPIES>(p, smem, ctl, err, tid);
     } else if (warp < 12) {
-        if (S::PAIR)
-            asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
-        else
-            asm volatile("setmaxnreg.dec.sync.aligned.u32 96;");
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 96;");
         if (warp == 8) {
             tiles_multiply<C, D, COPIES>(smem, ctl, err, lane);
             warp_commit(&ctl->spare);  // what was issued ends before the block may: others may have given up on it
@@ -1422,10 +1388,7 @@ __global__ void __launch_bounds__(TILES_THREADS, 1)
             tiles_prepare<C, D, COPIES>(p, smem, ctl, err, tid - 320);
         }
     } else {
-        if (S::PAIR)
-            asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
-        else
-            asm volatile("setmaxnreg.dec.sync.aligned.u32 96;");
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 96;");
         tiles_load<C, D, COPIES>(p, smem, ctl, err, tid - 384, maps ? &map_k : nullptr, maps ? &map_v : nullptr);
     }
     tc_fence_before();
