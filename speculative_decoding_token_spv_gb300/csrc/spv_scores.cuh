@@ -75,18 +75,33 @@ __device__ __forceinline__ float2 unpair(unsigned long long x)
 template <int M, int N> __device__ __forceinline__ void cap_polynomial(const ScoresView &v, unsigned long long (&x)[M], float f, const float (&c)[N])
 {
     asm volatile("" : "+f"(f));  // the coefficients are made here, and not kept in registers from tile to tile
-    const float u = f * v.cap_inv;
-    const unsigned long long u2 = pack2(u, u);
-    unsigned long long k[N];
+    const float u = f * v.cap_inv, uu = u * u;
+    if (uu > 0x1p-16f && uu < 0x1p16f) {  // the polynomial in x^2: one product less for each pair
+        unsigned long long k[N];
+        float unit = f;
 #pragma unroll
-    for (int i = 0; i < N; ++i) k[i] = pack2(c[i] * f, c[i] * f);
+        for (int i = 0; i < N; ++i) {
+            k[i] = pack2(c[i] * unit, c[i] * unit);
+            unit *= uu;
+        }
 #pragma unroll
-    for (int i = 0; i < M; ++i) {
-        const unsigned long long y = mul2(x[i], u2), w = mul2(y, y);
-        unsigned long long t = k[N - 1];
+        for (int i = 0; i < M; ++i) {
+            const unsigned long long w = mul2(x[i], x[i]);
+            unsigned long long t = k[N - 1];
 #pragma unroll
-        for (int j = N - 2; j >= 0; --j) t = ffma2(w, t, k[j]);
-        x[i] = mul2(x[i], t);
+            for (int j = N - 2; j >= 0; --j) t = ffma2(w, t, k[j]);
+            x[i] = mul2(x[i], t);
+        }
+    } else {
+        const unsigned long long u2 = pack2(u, u);
+#pragma unroll
+        for (int i = 0; i < M; ++i) {
+            const unsigned long long y = mul2(x[i], u2), w = mul2(y, y);
+            unsigned long long t = pack2(c[N - 1], c[N - 1]);
+#pragma unroll
+            for (int j = N - 2; j >= 0; --j) t = ffma2(w, t, pack2(c[j], c[j]));
+            x[i] = mul2(mul2(x[i], pack2(f, f)), t);
+        }
     }
 }
 // The same of N pairs of products, whose scores are f times them.  Up to 1.25 of

@@ -98,6 +98,7 @@ template <typename S> struct TilesCtl {
     TileItem items[2];
     uint64_t item_full[2], item_empty[2];
     uint64_t full[S::STAGES], empty[S::STAGES], s_full[4], p_full[4], o_done[4], q_full[2], q_empty[2], spare;
+    uint64_t q_raw[S::Q_PLACES];
     uint64_t raw_full[S::WIDEN ? 4 : 1][S::WIDEN ? S::RAW_STAGES : 1];  // of each loader warp's rows
     char bad[2][S::ITEMS];                                       // a page id outside the pool, for each group of row warps
     int stop[2], lost[2];
@@ -479,12 +480,12 @@ __device__ void tiles_load(const TilesParams &p, char *smem, TilesCtl<S> *ctl, u
         const int box_slot = (S::WIDEN ? WARP_ROWS * w : 0) + box / PANELS * box_slots;
         auto lookup = [&](int tile) {  // the page id of this lane's box or row of a tile, unchecked; -1: no such row
             const int j = tile * KEYS + (map_k ? box_slot : WARP_ROWS * w + lane);
-            return (map_k ? asks : lane < WARP_ROWS) && tile < t1 && j < it.total ? __ldg(table + (j >> p.c.page_shift)) : -1;
+            return (map_k ? asks : lane < WARP_ROWS) && tile >= t0 && j < it.total ? __ldg(table + (j >> p.c.page_shift)) : -1;
         };
-        int next = lookup(t0);
-        for (int tile = t0; ok && tile < t1; ++tile) {
+        int next = lookup(t1 - 1);
+        for (int tile = t1 - 1; ok && tile >= t0; --tile) {
             const int j0 = tile * KEYS, page = next;
-            next = lookup(tile + 1);
+            next = lookup(tile - 1);
 #pragma unroll 1
             for (int kv = 0; kv < 2; ++kv) {
                 const PoolView &pool = kv ? p.c.v : p.c.k;
@@ -617,7 +618,8 @@ __device__ void tiles_multiply(char *smem, TilesCtl<S> *ctl, unsigned *err, int 
         int v_st = 0, v_pass = 0;
         for (int i = 0; i <= tiles; ++i) {  // the scores of a tile, and the outputs of the one before
             const bool keys = i < tiles;
-            const bool here0 = keys && t0 + i >= lo0 && t0 + i < hi0, here1 = PAIR && keys && t0 + i >= lo1 && t0 + i < hi1;
+            const int tile = t0 + tiles - 1 - i;  // from the last: a bias that falls with the distance has its largest scores there
+            const bool here0 = keys && tile >= lo0 && tile < hi0, here1 = PAIR && keys && tile >= lo1 && tile < hi1;
             if (keys) {
                 if (!full(st, phase)) return;
                 if (here0) scores(0, st);
@@ -655,13 +657,16 @@ __device__ void tiles_multiply(char *smem, TilesCtl<S> *ctl, unsigned *err, int 
 
 // ------------------------------------------------------------------ q
 // Two warps, an item ahead of the others where there is room: q, and of trees
-// the depths of the new tokens.
+// the depths of the new tokens.  The copy engine brings it where a tile's rows
+// are whole tokens (the threads, some 20 instructions for 16 bytes, took 18,000
+// cycles for 256 rows); e4m3 caches: it is then multiplied into f16's range where
+// it lies.
 template <typename C, int D, int COPIES, typename S = TilesShape<C, D, COPIES>>
-__device__ void tiles_prepare(const TilesParams &p, char *smem, TilesCtl<S> *ctl, unsigned *err, int lt)
+__device__ void tiles_prepare(const TilesParams &p, char *smem, TilesCtl<S> *ctl, unsigned *err, int lt, const CUtensorMap *map_q)
 {
     const int lane = lt & 31;
     const uint32_t base = smem_u32(smem);
-    constexpr int CH = D / 8, STEP = TILES_PREPARE / CH;  // rows at a time
+    constexpr int CH = D / 8, STEP = TILES_PREPARE / CH, TIMES = S::PAIR ? 1 : COPIES;  // rows at a time, places of each row
     const int ch = lt % CH, first = lt / CH;
     const int step_t = STEP / p.group, step_g = STEP - step_t * p.group;
     const int64_t token = static_cast<int64_t>(p.q_heads) * D * 2;
@@ -672,10 +677,10 @@ __device__ void tiles_prepare(const TilesParams &p, char *smem, TilesCtl<S> *ctl
         if (item == p.give_up.item && static_cast<int>(blockIdx.x) == p.give_up.block) {  // the self-test
             *reinterpret_cast<volatile int *>(&ctl->dead) = 1;
             atomicExch(err, static_cast<unsigned>(STATUS_TIMEOUT));
-            return;
+            break;
         }
         const int place = item % S::Q_PLACES, row0 = it.row_tile * S::ROWS, live = min(S::ROWS, p.rows - row0);
-        if (item >= S::Q_PLACES && !tiles_wait(ctl, &ctl->q_empty[place], (item / S::Q_PLACES - 1) & 1, err)) return;
+        if (item >= S::Q_PLACES && !tiles_wait(ctl, &ctl->q_empty[place], (item / S::Q_PLACES - 1) & 1, err)) break;
         if constexpr (!S::PAIR) {
             if (p.parent && p.sc.slopes && !p.sc.slot_pos)
                 for (int t = lt; t < it.fresh; t += TILES_PREPARE) {
@@ -684,66 +689,76 @@ __device__ void tiles_prepare(const TilesParams &p, char *smem, TilesCtl<S> *ctl
                         static_cast<signed char>(token_view(p.sc, p.parent + static_cast<int64_t>(it.b) * p.w.T, s, it.b, p.w.T, t).depth);
                 }
         }
-        // rows first, first + STEP, ...: their tokens and heads, without a division each
-        int t = (row0 + first) / p.group, g = row0 + first - t * p.group;
-        const char *row = static_cast<const char *>(p.q) + (static_cast<int64_t>(it.b) * p.w.T * p.q_heads + it.h * p.group) * (D * 2) + ch * 16;
-        auto source = [&](int r) {  // null: a row of zeros; steps on
-            const char *from = r < live && t < it.fresh ? row + t * token + g * (D * 2) : nullptr;
-            t += step_t, g += step_g;
-            if (g >= p.group) g -= p.group, ++t;
-            return from;
-        };
-        if constexpr (!S::WIDEN) {
-            const uint32_t to = base + place * S::Q;
+        char *to = smem + place * S::Q;
+        const uint32_t to32 = base + place * S::Q;
+        if (map_q) {
+            constexpr int PANELS = D / 64, PARTS = S::PAIR ? 2 : COPIES;  // a box each: 64 elements of 128 rows, or of a copy's
+            uint64_t *bar = S::WIDEN ? &ctl->q_raw[place] : &ctl->q_full[place];
+            if (lt == 0) mbar_arrive_expect_tx(bar, S::Q);
+            __syncwarp();
+            if (lt < PANELS * PARTS) {
+                const int panel = lt % PANELS, part = lt / PANELS;
+                tma_box(to32 + (S::PAIR ? part * S::Q_SUB : part * S::ROWS * 128) + panel * (128 * 128), map_q, panel * 64, it.h * p.group,
+                        (row0 + (S::PAIR ? part * 128 : 0)) / p.group, it.b, bar);
+            }
+            __syncwarp();
+            if (S::WIDEN) {
+                if (!tiles_wait(ctl, bar, (item / S::Q_PLACES) & 1, err)) break;
+            } else if (lt != 0) {
+                mbar_arrive(bar);
+            }
+        } else {
+            // rows first, first + STEP, ...: their tokens and heads, without a division each
+            int t = (row0 + first) / p.group, g = row0 + first - t * p.group;
+            const char *row = static_cast<const char *>(p.q) + (static_cast<int64_t>(it.b) * p.w.T * p.q_heads + it.h * p.group) * (D * 2) + ch * 16;
 #pragma unroll 4
             for (int r = first; r < S::ROWS; r += STEP) {
-                const char *from = source(r);
+                const bool there = r < live && t < it.fresh;
+                const char *from = there ? row + t * token + g * (D * 2) : static_cast<const char *>(p.q);
+                t += step_t, g += step_g;
+                if (g >= p.group) g -= p.group, ++t;
 #pragma unroll
-                for (int i = 0; i < (S::PAIR ? 1 : COPIES); ++i)
-                    cp_async16_zfill(to + (r >> 7) * S::Q_SUB + tile_at<128>((r & 127) + i * S::ROWS, ch), from ? from : static_cast<const char *>(p.q),
-                                     from ? 16 : 0);
+                for (int i = 0; i < TIMES; ++i)
+                    cp_async16_zfill(to32 + (r >> 7) * S::Q_SUB + tile_at<128>((r & 127) + i * S::ROWS, ch), from, there ? 16 : 0);
             }
             asm volatile("cp.async.wait_all;" ::: "memory");
-        } else {
-            char *to = smem + place * S::Q;
-#pragma unroll 1
-            for (int r0 = 0; r0 < S::ROWS; r0 += 4 * STEP) {
-                uint4 in[4];
+        }
+        if constexpr (S::WIDEN) {
+#pragma unroll 2
+            for (int r = first; r < S::ROWS; r += STEP) {  // every thread the same number of times
+                char *at = to + (r >> 7) * S::Q_SUB;
+                const uint4 in = *reinterpret_cast<const uint4 *>(at + tile_at<128>(r & 127, ch));
+                float x[8], top = 0.0f;
 #pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    const char *from = source(r0 + i * STEP + first);
-                    in[i] = from ? *reinterpret_cast<const uint4 *>(from) : make_uint4(0, 0, 0, 0);
+                for (int e = 0; e < 8; ++e) {
+                    x[e] = p.q_bf16 ? Num<__nv_bfloat16>::up(reinterpret_cast<const __nv_bfloat16 *>(&in)[e])
+                                    : Num<__half>::up(reinterpret_cast<const __half *>(&in)[e]);
+                    top = fabsf(x[e]) < CUDART_INF_F ? fmaxf(top, fabsf(x[e])) : top;
                 }
 #pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    const int r = r0 + i * STEP + first;
-                    float x[8], top = 0.0f;
+                for (int o = CH / 2; o; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+                // the largest below 2^15 (the exponent of a number that is not normal counts as the smallest's)
+                const int e2 = top > 0.0f ? max(-120, min(120, 14 - (static_cast<int>(__float_as_uint(top) >> 23) - 127))) : 0;
+                const float up = __uint_as_float(static_cast<uint32_t>(e2 + 127) << 23);
+                if (ch == 0) ctl->at.q_power[place * S::ROWS + r] = static_cast<signed char>(e2);
+                const uint4 y = make_uint4(pack_mma<__half>(x[0] * up, x[1] * up), pack_mma<__half>(x[2] * up, x[3] * up),
+                                           pack_mma<__half>(x[4] * up, x[5] * up), pack_mma<__half>(x[6] * up, x[7] * up));
 #pragma unroll
-                    for (int e = 0; e < 8; ++e) {
-                        x[e] = p.q_bf16 ? Num<__nv_bfloat16>::up(reinterpret_cast<const __nv_bfloat16 *>(&in[i])[e])
-                                        : Num<__half>::up(reinterpret_cast<const __half *>(&in[i])[e]);
-                        top = fabsf(x[e]) < CUDART_INF_F ? fmaxf(top, fabsf(x[e])) : top;
-                    }
-#pragma unroll
-                    for (int o = CH / 2; o; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
-                    // the largest below 2^15 (the exponent of a number that is not normal counts as the smallest's)
-                    const int e2 = top > 0.0f ? max(-120, min(120, 14 - (static_cast<int>(__float_as_uint(top) >> 23) - 127))) : 0;
-                    const float up = __uint_as_float(static_cast<uint32_t>(e2 + 127) << 23);
-                    if (r < S::ROWS) {
-                        if (ch == 0) ctl->at.q_power[place * S::ROWS + r] = static_cast<signed char>(e2);
-                        const uint4 y = make_uint4(pack_mma<__half>(x[0] * up, x[1] * up), pack_mma<__half>(x[2] * up, x[3] * up),
-                                                   pack_mma<__half>(x[4] * up, x[5] * up), pack_mma<__half>(x[6] * up, x[7] * up));
-#pragma unroll
-                        for (int k = 0; k < (S::PAIR ? 1 : COPIES); ++k)
-                            *reinterpret_cast<uint4 *>(to + (r >> 7) * S::Q_SUB + tile_at<128>((r & 127) + k * S::ROWS, ch)) = y;
-                    }
-                }
+                for (int i = 0; i < TIMES; ++i) *reinterpret_cast<uint4 *>(at + tile_at<128>((r & 127) + i * S::ROWS, ch)) = y;
             }
         }
-        fence_async_shared();
-        mbar_arrive(&ctl->q_full[place]);
+        if (S::WIDEN || !map_q) {
+            fence_async_shared();
+            mbar_arrive(&ctl->q_full[place]);
+        }
         ++item;
     }
+    // the copy engine's, before the block may end: nobody else may have waited for it
+    if (map_q && *reinterpret_cast<volatile int *>(&ctl->dead))
+        for (int i = max(0, item - S::Q_PLACES); i <= item; ++i) {
+            uint64_t *bar = S::WIDEN ? &ctl->q_raw[i % S::Q_PLACES] : &ctl->q_full[i % S::Q_PLACES];
+            mbar_drain(bar, (i / S::Q_PLACES) & 1);
+        }
 }
 
 // ------------------------------------------------------------------ rows
@@ -911,10 +926,11 @@ __device__ __noinline__ void tiles_finish(const TilesParams &p, bool again, int 
 }
 
 // Cap, bias and a window over moved slots of a row's MINE scores of a tile whose
-// first key is jb: the true scores are then x f - off.
+// first key is jb: the true scores are then x f - off.  slope_in: the slope in
+// units of x.
 template <int MINE, bool PAIR, typename Ctl>
 __device__ __forceinline__ void tile_shape(const TilesParams &p, unsigned long long (&x)[MINE / 2], float *f, float *off, int ctx, int total,
-                                           Ctl *ctl, int place, int jb, int own, float slope, int origin, const int *positions)
+                                           Ctl *ctl, int place, int jb, int own, int all_own, float slope, float slope_in, int origin, const int *positions)
 {
     const ScoresView &v = p.sc;
     if (v.cap2 != 0.0f) {
@@ -927,7 +943,7 @@ __device__ __forceinline__ void tile_shape(const TilesParams &p, unsigned long l
         *f = 1.0f;
     }
     if (moved_slots(v)) {
-        const float s = -slope / *f;
+        const float s = -slope_in;
         if (v.window > 0) {
             const int2 *at = reinterpret_cast<const int2 *>(positions);
 #pragma unroll
@@ -951,7 +967,7 @@ __device__ __forceinline__ void tile_shape(const TilesParams &p, unsigned long l
             }
         }
     } else if (v.slopes) {
-        const float s = slope / *f;
+        const float s = slope_in;
         if (!PAIR && p.parent && jb + MINE > ctx) {  // a node's position is its depth's
 #pragma unroll
             for (int i = 0; i < MINE / 2; ++i) {
@@ -964,7 +980,7 @@ __device__ __forceinline__ void tile_shape(const TilesParams &p, unsigned long l
                 }
                 x[i] = pack2(z[0], z[1]);
             }
-        } else if (__all_sync(0xffffffffu, own >= jb + MINE - 1)) {  // no key is ahead: the distance is own - jb less the key's place
+        } else if (all_own >= jb + MINE - 1) {  // no key is ahead: the distance is own - jb less the key's place
             *off = slope * static_cast<float>(own - jb);
 #pragma unroll
             for (int i = 0; i < MINE / 2; ++i) {
@@ -1049,18 +1065,20 @@ __device__ void tiles_rows(const TilesParams &p, char *smem, TilesCtl<S> *ctl, u
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&ctl->q_empty[place]);
             }
+            const float slope_in = v.cap2 != 0.0f || !(factor > 0.0f) ? slope : slope / factor;
             const bool shaped = v.cap2 != 0.0f || v.slopes || moved || __any_sync(0xffffffffu, !(factor > 0.0f));
             const bool works = __any_sync(0xffffffffu, there);
             // the slots that all rows of the warp see (votes of each tile took hundreds of cycles)
             const int all_lo = __reduce_max_sync(0xffffffffu, see.lo), all_hi = __reduce_min_sync(0xffffffffu, see.hi);
+            const int all_own = __reduce_min_sync(0xffffffffu, there ? own : 0x7fffffff);
             bool huge = false;  // scores beyond what a fused difference allows
             auto position = [&](int tile) {
                 const int j = tile * KEYS + group_tid;
-                return moved && group_tid < KEYS && tile < s1 && j < it.total ? __ldg(pos + j) : 0;
+                return moved && group_tid < KEYS && tile >= s0 && j < it.total ? __ldg(pos + j) : 0;
             };
-            int next_at = position(s0);
+            int next_at = position(s1 - 1);
 #pragma unroll 1
-            for (int tile = s0; tile < s1; ++tile, ++n) {  // to its end even after a wait gave up: the halves meet at each tile
+            for (int tile = s1 - 1; tile >= s0; --tile, ++n) {  // to its end even after a wait gave up: the halves meet at each tile
                 const int buf = group * 2 + (n & 1);
                 const int of_tile = copy * S::OF_COPY + half * MINE;  // this thread's keys
                 const uint32_t tm_s = ctl->tmem + quarter + buf * S::PLACE + of_tile;
@@ -1071,7 +1089,7 @@ __device__ void tiles_rows(const TilesParams &p, char *smem, TilesCtl<S> *ctl, u
                     if (group_tid < KEYS)
                         ctl->at.positions[group][group_tid] = v.window > 0 ? next_at : __float_as_int(static_cast<float>(origin - next_at));
                     group_sync<GROUP>(group);
-                    next_at = position(tile + 1);
+                    next_at = position(tile - 1);
                 }
                 ok = ok && tiles_wait(ctl, &ctl->s_full[buf], (n >> 1) & 1, err);
                 tc_fence_after();
@@ -1094,7 +1112,7 @@ __device__ void tiles_rows(const TilesParams &p, char *smem, TilesCtl<S> *ctl, u
                     }
                     // The true scores are x f - off.
                     float f = factor, off = 0.0f;
-                    if (shaped) tile_shape<MINE, PAIR>(p, x, &f, &off, it.ctx, it.total, ctl, place, jb, own, slope, origin, ctl->at.positions[group] + of_tile);
+                    if (shaped) tile_shape<MINE, PAIR>(p, x, &f, &off, it.ctx, it.total, ctl, place, jb, own, all_own, slope, slope_in, origin, ctl->at.positions[group] + of_tile);
                     if (all_lo > jb || all_hi < jb + MINE) {
 #pragma unroll
                         for (int i = 0; i < MINE; i += 32) {
@@ -1130,8 +1148,7 @@ __device__ void tiles_rows(const TilesParams &p, char *smem, TilesCtl<S> *ctl, u
                         halves_sync(lane_row / 32);  // (the places of two tiles: the one before has been read when both are here)
                         top = fmaxf(top, ctl->at.top[n & 1][tid ^ 128]);
                     }
-                    if (n >= 2) ok = ok && tiles_wait(ctl, &ctl->o_done[buf], ((n - 2) >> 1) & 1, err);
-                    if (tile == s0) {
+                    if (tile == s1 - 1) {
                         m = top - UP;
                         huge = __any_sync(0xffffffffu, fabsf(m) > 0x1p20f && m != -CUDART_INF_F);
                     } else if (__any_sync(0xffffffffu, top - m > UP + Weights<M>::LAG)) {  // as a difference: a sum may round up to a score 16 above
@@ -1139,6 +1156,7 @@ __device__ void tiles_rows(const TilesParams &p, char *smem, TilesCtl<S> *ctl, u
                         m = grown;
                         huge |= __any_sync(0xffffffffu, fabsf(m) > 0x1p20f && m != -CUDART_INF_F);
                         l *= a;
+                        // (those of the tile before that were done before this tile's scores)
                         ok = ok && tiles_wait(ctl, &ctl->o_done[buf ^ 1], ((n - 1) >> 1) & 1, err);
                         tc_fence_after();
 #pragma unroll 1
@@ -1328,7 +1346,8 @@ __device__ void tiles_rows(const TilesParams &p, char *smem, TilesCtl<S> *ctl, u
 
 template <typename C, int D, int COPIES>
 __global__ void __launch_bounds__(TILES_THREADS, 1)
-    tiles_kernel(const TilesParams p, const __grid_constant__ CUtensorMap map_k, const __grid_constant__ CUtensorMap map_v, const int maps)
+    tiles_kernel(const TilesParams p, const __grid_constant__ CUtensorMap map_k, const __grid_constant__ CUtensorMap map_v,
+                 const __grid_constant__ CUtensorMap map_q, const int maps, const int q_map)
 {
     using S = TilesShape<C, D, COPIES>;
     using Ctl = TilesCtl<S>;
@@ -1355,6 +1374,7 @@ __global__ void __launch_bounds__(TILES_THREADS, 1)
             for (int k = 0; k < S::ITEMS; ++k) ctl->bad[i][k] = 0;
         }
         mbar_init(&ctl->spare, 1);
+        for (int i = 0; i < S::Q_PLACES; ++i) mbar_init(&ctl->q_raw[i], 1);
         if (S::WIDEN)
             for (int i = 0; i < 4; ++i)
                 for (int k = 0; k < S::RAW_STAGES; ++k) mbar_init(&ctl->raw_full[S::WIDEN ? i : 0][k], 1);
@@ -1385,7 +1405,7 @@ __global__ void __launch_bounds__(TILES_THREADS, 1)
         } else if (warp == 9) {
             tiles_items<S>(p, c, ctl, err, lane);
         } else {
-            tiles_prepare<C, D, COPIES>(p, smem, ctl, err, tid - 320);
+            tiles_prepare<C, D, COPIES>(p, smem, ctl, err, tid - 320, q_map ? &map_q : nullptr);
         }
     } else {
         asm volatile("setmaxnreg.dec.sync.aligned.u32 96;");
@@ -1407,10 +1427,11 @@ template <typename C, int D, int COPIES> cudaError_t launch_tiles_of(TilesParams
     if (e != cudaSuccess) return e;
     p.w.tile = S::KEYS;
     p.w.row_tiles = (p.rows + S::ROWS - 1) / S::ROWS;
-    CUtensorMap map_k{}, map_v{};
+    CUtensorMap map_k{}, map_v{}, map_q{};
+    const bool q_map = query_map(&map_q, p.q, L, p.group, S::PAIR ? 128 : S::ROWS);
     const int slots = S::WIDEN ? S::KEYS / 4 : S::KEYS;
     const bool maps = pool_map(&map_k, L, false, slots, S::WIDEN) && pool_map(&map_v, L, true, slots, S::WIDEN);
-    e = launch_chained(kernel, dim3(ATT_SMS), TILES_THREADS, SMEM, st, p, map_k, map_v, static_cast<int>(maps));
+    e = launch_chained(kernel, dim3(ATT_SMS), TILES_THREADS, SMEM, st, p, map_k, map_v, map_q, static_cast<int>(maps), static_cast<int>(q_map));
     return e != cudaSuccess ? e : launch_join(p, L.dtype, D, S::ROWS, ATT_SMS, st);
 }
 template <typename C, int D> cudaError_t launch_tiles_dim(const TilesParams &p, const KvLaunch &L, bool pairs, cudaStream_t st)
