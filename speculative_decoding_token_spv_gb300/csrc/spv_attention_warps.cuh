@@ -204,6 +204,7 @@ __global__ void __launch_bounds__(ATT_THREADS, AttShape<C, D, MT>::BLOCKS_PER_SM
         }
         // positions of this lane's four keys of a slice, a tile ahead
         const bool moved = SCORED && moved_slots(p_scores(p));
+        const bool shaped = SCORED && (p_scores(p).cap2 != 0.0f || p_scores(p).slopes || moved);  // scores are more than products
         const int32_t *pos = moved ? p_scores(p).slot_pos + (static_cast<int64_t>(c.b) * p.c.kv_heads + c.h) * p_scores(p).pos_stride : nullptr;
         int key_pos[4], next_pos[4];
         auto positions = [&](int tile, int (&to)[4]) {
@@ -238,22 +239,34 @@ __global__ void __launch_bounds__(ATT_THREADS, AttShape<C, D, MT>::BLOCKS_PER_SM
                         if (key_pos[i] >= c.s.ctx && key_pos[i] < c.s.total) key_pos[i] = c.s.ctx + depths[key_pos[i] - c.s.ctx];
                 }
                 tail |= j0 < c.s.solid;
+                if (shaped) {
 #pragma unroll
-                for (int mt = 0; mt < MT; ++mt) {
-                    float x[8];  // key tile, then the fragment's four
+                    for (int mt = 0; mt < MT; ++mt) {
+                        float x[8];  // key tile, then the fragment's four
 #pragma unroll
-                    for (int k = 0; k < 8; ++k) x[k] = s[mt][k >> 2][k & 3] * factor[mt][(k & 3) >> 1];
-                    if (v.cap2 != 0.0f) cap_all(v, x);
-                    if (v.slopes || moved) {
+                        for (int k = 0; k < 8; ++k) x[k] = s[mt][k >> 2][k & 3] * factor[mt][(k & 3) >> 1];
+                        if (v.cap2 != 0.0f) {
+                            unsigned long long y[4];
 #pragma unroll
-                        for (int k = 0; k < 8; ++k) {
-                            const int r = mt * 16 + ((k & 3) >> 1) * 8 + (lane >> 2), far = row_pos[r] - key_pos[2 * (k >> 2) + (k & 1)];
-                            if (v.slopes) x[k] = fmaf(-row_slope[r], fabsf(static_cast<float>(far)), x[k]);
-                            if (moved && v.window > 0 && far >= v.window) x[k] = -CUDART_INF_F;
+                            for (int k = 0; k < 4; ++k) y[k] = pack2(x[2 * k], x[2 * k + 1]);
+                            cap_pairs(v, y);
+#pragma unroll
+                            for (int k = 0; k < 4; ++k) {
+                                const float2 z = unpair(y[k]);
+                                x[2 * k] = z.x, x[2 * k + 1] = z.y;
+                            }
                         }
-                    }
+                        if (v.slopes || moved) {
 #pragma unroll
-                    for (int k = 0; k < 8; ++k) s[mt][k >> 2][k & 3] = x[k];
+                            for (int k = 0; k < 8; ++k) {
+                                const int r = mt * 16 + ((k & 3) >> 1) * 8 + (lane >> 2), far = row_pos[r] - key_pos[2 * (k >> 2) + (k & 1)];
+                                if (v.slopes) x[k] = fmaf(-row_slope[r], fabsf(static_cast<float>(far)), x[k]);
+                                if (moved && v.window > 0 && far >= v.window) x[k] = -CUDART_INF_F;
+                            }
+                        }
+#pragma unroll
+                        for (int k = 0; k < 8; ++k) s[mt][k >> 2][k & 3] = x[k];
+                    }
                 }
             }
             uint32_t pf[MT][4];
@@ -282,7 +295,7 @@ __global__ void __launch_bounds__(ATT_THREADS, AttShape<C, D, MT>::BLOCKS_PER_SM
                     float x = fmaxf(fmaxf(s[mt][0][2 * i], s[mt][0][2 * i + 1]), fmaxf(s[mt][1][2 * i], s[mt][1][2 * i + 1]));
                     x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 1));
                     x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 2));
-                    top[i] = SCORED ? x : x * factor[mt][i];
+                    top[i] = shaped ? x : x * factor[mt][i];
                     moved |= top[i] - m[mt][i] > UP + Weights<M>::LAG;  // m minus infinity: any score
                 }
                 if (__any_sync(0xffffffffu, moved)) {
@@ -301,7 +314,7 @@ __global__ void __launch_bounds__(ATT_THREADS, AttShape<C, D, MT>::BLOCKS_PER_SM
                 }
 #pragma unroll
                 for (int i = 0; i < 2; ++i) {
-                    const float base = m[mt][i] == -CUDART_INF_F ? 0.0f : m[mt][i], f = SCORED ? 1.0f : factor[mt][i];
+                    const float base = m[mt][i] == -CUDART_INF_F ? 0.0f : m[mt][i], f = shaped ? 1.0f : factor[mt][i];
 #pragma unroll
                     for (int k = 0; k < 2; ++k)
 #pragma unroll

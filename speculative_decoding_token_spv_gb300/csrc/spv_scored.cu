@@ -72,7 +72,16 @@ cudaError_t launch_attention_scored(const AttentionLaunch &L, cudaStream_t st)
         const cudaError_t e = launch_scored_status(p.c, work_of(p), k.row_status, st);
         if (e != cudaSuccess) return e;
     }
-    if (p.rows > (eight ? 32 : 16) || (eight && D == 256 && p.rows > 16)) return launch_tiles(p, k, false, st);
+    // Many rows a key head: in tiles.  Few rows too where a 16-bit cache may be large: at D = 256 from 64 MB on (1 token, 2 rows,
+    // 8 key heads: 8 x 500 slots 24.9 us there and 24.1 here, 1 x 30,000 65.7 and 72.0, 64 x 2,000 193 and 223), at D = 128 from
+    // 1 GB on (64 x 2,000 124 and 121, 64 x 6,000 266 and 304), at D = 64 never (64 x 6,000 197 and 165); e4m3, whose rows pass
+    // through shared memory twice there, never (64 x 2,000 of 128: 169 and 90).  How long the caches are the host does not know:
+    // what the page table has room for counts, or the window.
+    int64_t slots = static_cast<int64_t>(k.max_pages) << log2_of(k.cache.page_size);
+    if (p.sc.window > 0 && !p.sc.slot_pos && p.sc.window + k.T < slots) slots = p.sc.window + k.T;
+    const double bytes = 4.0 * D * k.cache.kv_heads * k.B * static_cast<double>(slots);
+    const bool large = !eight && (D == 256 ? bytes >= 64e6 : D == 128 && bytes >= 1e9);
+    if (large || p.rows > (eight && D <= 128 ? 32 : 16)) return launch_tiles(p, k, false, st);
     if (k.dtype == SPV_BF16)
         return eight ? launch_types<__nv_bfloat16, __nv_fp8_e4m3>(p, D, st)
                      : launch_types<__nv_bfloat16, __nv_bfloat16>(p, D, st);

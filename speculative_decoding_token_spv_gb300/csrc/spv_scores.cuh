@@ -74,34 +74,27 @@ __device__ __forceinline__ float2 unpair(unsigned long long x)
 // x f P((x f / cap)^2) of pairs, P of N coefficients.
 template <int M, int N> __device__ __forceinline__ void cap_polynomial(const ScoresView &v, unsigned long long (&x)[M], float f, const float (&c)[N])
 {
-    asm volatile("" : "+f"(f));  // the coefficients are made here, and not kept in registers from tile to tile
-    const float u = f * v.cap_inv, uu = u * u;
-    if (uu > 0x1p-16f && uu < 0x1p16f) {  // the polynomial in x^2: one product less for each pair
-        unsigned long long k[N];
-        float unit = f;
+    const float u = f * v.cap_inv;
+    const unsigned long long u2 = pack2(u, u);
+    unsigned long long k[N];
 #pragma unroll
-        for (int i = 0; i < N; ++i) {
-            k[i] = pack2(c[i] * unit, c[i] * unit);
-            unit *= uu;
-        }
+    for (int i = 0; i < N; ++i) k[i] = pack2(c[i] * f, c[i] * f);
+    constexpr int TOGETHER = M < 8 ? M : 8;  // pairs whose chains of operations go side by side
 #pragma unroll
-        for (int i = 0; i < M; ++i) {
-            const unsigned long long w = mul2(x[i], x[i]);
-            unsigned long long t = k[N - 1];
+    for (int i0 = 0; i0 < M; i0 += TOGETHER) {
+        unsigned long long w[TOGETHER], t[TOGETHER];
 #pragma unroll
-            for (int j = N - 2; j >= 0; --j) t = ffma2(w, t, k[j]);
-            x[i] = mul2(x[i], t);
-        }
-    } else {
-        const unsigned long long u2 = pack2(u, u);
+        for (int i = 0; i < TOGETHER; ++i) w[i] = mul2(x[i0 + i], u2);
 #pragma unroll
-        for (int i = 0; i < M; ++i) {
-            const unsigned long long y = mul2(x[i], u2), w = mul2(y, y);
-            unsigned long long t = pack2(c[N - 1], c[N - 1]);
+        for (int i = 0; i < TOGETHER; ++i) w[i] = mul2(w[i], w[i]);
 #pragma unroll
-            for (int j = N - 2; j >= 0; --j) t = ffma2(w, t, pack2(c[j], c[j]));
-            x[i] = mul2(mul2(x[i], pack2(f, f)), t);
-        }
+        for (int i = 0; i < TOGETHER; ++i) t[i] = ffma2(w[i], k[N - 1], k[N - 2]);
+#pragma unroll
+        for (int j = N - 3; j >= 0; --j)
+#pragma unroll
+            for (int i = 0; i < TOGETHER; ++i) t[i] = ffma2(w[i], t[i], k[j]);
+#pragma unroll
+        for (int i = 0; i < TOGETHER; ++i) x[i0 + i] = mul2(x[i0 + i], t[i]);
     }
 }
 // The same of N pairs of products, whose scores are f times them.  Up to 1.25 of
