@@ -381,38 +381,40 @@ __device__ void mass_prepare(const P &p, Cursor c, char *smem, Ctl *ctl, int lt)
     }
 }
 
-// One thread.
+// One warp.
 template <typename T, typename C, int D, typename Ctl, typename P>
 __device__ void mass_multiply(const P &p, Cursor c, char *smem, Ctl *ctl)
 {
     using S = MassShape<C, D>;
     using M = typename MmaOf<T, C>::type;
     constexpr int KST = S::K_STAGES;
-    const uint32_t base = smem_u32(smem), tmem = ctl->tmem;
+    const uint32_t base = smem_u32(smem), tmem = same_in_warp(ctl->tmem);
     Counted count;
     int n = 0, unit_no = 0;
     for (; c.at < c.end; next_item(c, p.w, p.c)) {
         count.at(p, c);
-        const int tiles = mass_last(c) - mass_start(c, count);
-        if (count.rows == 0 || tiles <= 0) continue;
-        for (int r0 = 0; r0 < count.rows; r0 += S::ROWS, ++unit_no) {
-            const int place = unit_no & 1, padded = (min(S::ROWS, count.rows - r0) + 15) & ~15;
-            const uint32_t shape = mma_shape(std::is_same<M, __nv_bfloat16>::value, false, padded);
-            if (!mass_wait1(ctl, &ctl->q_full[place], (unit_no >> 1) & 1)) return;
-            for (int i = 0; i < tiles; ++i, ++n) {
-                if (n >= MASS_BUFFERS && !mass_wait1(ctl, &ctl->s_empty[n % MASS_BUFFERS], (n / MASS_BUFFERS - 1) & 1)) return;
-                if (!mass_wait1(ctl, &ctl->k_full[n % KST], (n / KST) & 1)) return;
+        const int tiles = same_in_warp(mass_last(c) - mass_start(c, count)), rows = same_in_warp(count.rows);
+        if (rows == 0 || tiles <= 0) continue;
+        for (int r0 = 0; r0 < rows; r0 += S::ROWS, ++unit_no) {
+            const int place = same_in_warp(unit_no & 1), n0 = same_in_warp(n), padded = (min(S::ROWS, rows - r0) + 15) & ~15;
+            const uint32_t shape = mma_shape(std::is_same<M, __nv_bfloat16>::value, false, padded), q = desc_low(base + S::Q_AT + place * S::Q, 16);
+            if (!mass_wait(ctl, &ctl->q_full[place], (unit_no >> 1) & 1)) return;
+            for (int i = 0; i < tiles; ++i) {
+                const int t = n0 + i;
+                if (t >= MASS_BUFFERS && !mass_wait(ctl, &ctl->s_empty[t % MASS_BUFFERS], (t / MASS_BUFFERS - 1) & 1)) return;
+                if (!mass_wait(ctl, &ctl->k_full[t % KST], (t / KST) & 1)) return;
                 tc_fence_after();
                 fence_async_shared();  // K was written by asynchronous copies of threads, q by threads
-                const uint32_t k = base + S::K_AT + (n % KST) * S::TILE, q = base + S::Q_AT + place * S::Q;
+                const uint32_t k = desc_low(base + S::K_AT + (t % KST) * S::TILE, 16);
 #pragma unroll
                 for (int ks = 0; ks < D / 16; ++ks)
-                    tc_mma(tmem + (n % MASS_BUFFERS) * 128, desc_k_major(k + (ks >> 2) * (MASS_KEYS * 128) + (ks & 3) * 32),
-                           desc_k_major(q + (ks >> 2) * (S::ROWS * 128) + (ks & 3) * 32), shape, ks > 0);
-                tc_commit(&ctl->s_full[n % MASS_BUFFERS]);
-                tc_commit(&ctl->k_empty[n % KST]);
+                    warp_mma(tmem + (t % MASS_BUFFERS) * 128, k + (((ks >> 2) * (MASS_KEYS * 128) + (ks & 3) * 32) >> 4),
+                             q + (((ks >> 2) * (S::ROWS * 128) + (ks & 3) * 32) >> 4), shape, ks > 0);
+                warp_commit(&ctl->s_full[t % MASS_BUFFERS]);
+                warp_commit(&ctl->k_empty[t % KST]);
             }
-            tc_commit(&ctl->q_empty[place]);
+            n = n0 + tiles;
+            warp_commit(&ctl->q_empty[place]);
         }
     }
 }
@@ -513,28 +515,33 @@ template <typename Shape, typename Ctl, typename P> __device__ long long mass_su
                                                  fmaf(-__int_as_float(b.z), fabsf(__int_as_float(b.w) - key_rel), x.y));
                                 }
                             }
-                            const bool some = g + 16 > live;  // some of these rows are not there
+                            float w[16];
 #pragma unroll
                             for (int i = 0; i < 8; ++i) {
                                 const float2 x = unpair(fadd2(z[i], lse[i]));
-                                float w[2] = {fast_exp2(x.x), fast_exp2(x.y)};
-                                if (masks || some) {
+                                w[2 * i] = fast_exp2(x.x);
+                                w[2 * i + 1] = fast_exp2(x.y);
+                            }
+                            if (masks) {
 #pragma unroll
-                                    for (int e = 0; e < 2; ++e) {
-                                        const int r = g + 2 * i + e;
-                                        bool seen = r < live;
-                                        if (masks && seen) {
-                                            const int4 shape = ctl->shape[place][r];
-                                            const unsigned long long see = ctl->sees[place][r];
-                                            seen = see != 0 && j >= shape.y &&
-                                                   (j < c.s.ctx || (j < c.s.total && (see >> ((j - c.s.ctx) & 63) & 1)));
-                                            if (v.window > 0 && v.slot_pos && shape.x - key_at >= v.window) seen = false;
-                                        }
-                                        if (!seen) w[e] = 0.0f;
-                                    }
+                                for (int i = 0; i < 16; ++i) {
+                                    const int r = min(g + i, live - 1);
+                                    const int4 shape = ctl->shape[place][r];
+                                    const unsigned long long see = ctl->sees[place][r];
+                                    bool seen = g + i < live && see != 0 && j >= shape.y &&
+                                                (j < c.s.ctx || (j < c.s.total && (see >> ((j - c.s.ctx) & 63) & 1)));
+                                    if (v.window > 0 && v.slot_pos && shape.x - key_at >= v.window) seen = false;
+                                    if (!seen) w[i] = 0.0f;
                                 }
-                                s0 += w[0];
-                                s1 += w[1];
+                            } else if (g + 16 > live) {
+#pragma unroll
+                                for (int i = 0; i < 16; ++i)
+                                    if (g + i >= live) w[i] = 0.0f;
+                            }
+#pragma unroll
+                            for (int i = 0; i < 16; i += 2) {
+                                s0 += w[i];
+                                s1 += w[i + 1];
                             }
                         } else if (!masks) {
 #pragma unroll
@@ -642,13 +649,11 @@ template <typename T, typename C, int D, typename P> __global__ void __launch_bo
         const long long done = mass_sum<S>(p, c, ctl, tid & 127, warp >= 16);
         if (done < c.end) mass_lost(p, done, tid & 127);
     } else if (warp == 4) {
-        if (tid == 128) {
-            mass_multiply<T, C, D>(p, c, smem, ctl);
-            // what was issued ends before the block may: others may have given up on it
-            tc_commit(&ctl->spare);
-            mbar_drain(&ctl->spare, 0);
-        }
+        mass_multiply<T, C, D>(p, c, smem, ctl);
+        // what was issued ends before the block may: others may have given up on it
         __syncwarp();
+        warp_commit(&ctl->spare);
+        mbar_drain(&ctl->spare, 0);
     } else if (warp < 8) {
         mass_prepare<T, C, D>(p, c, smem, ctl, tid - 160);
     } else {

@@ -77,6 +77,15 @@ template <uint32_t SHAPE> __device__ __forceinline__ void warp_mma(uint32_t d, u
                  "r"(static_cast<uint32_t>(add)), "n"(SHAPE), "n"(DESC_HIGH)
                  : "memory");
 }
+// The same with a shape that is known only when it runs.
+__device__ __forceinline__ void warp_mma(uint32_t d, uint32_t a, uint32_t b, uint32_t shape, bool add)
+{
+    asm volatile("{\n\t.reg .pred p, e;\n\t.reg .b64 x, y;\n\t"
+                 "elect.sync _|e, 0xffffffff;\n\tsetp.ne.u32 p, %3, 0;\n\tmov.b64 x, {%1, %5};\n\tmov.b64 y, {%2, %5};\n\t"
+                 "@e tcgen05.mma.cta_group::1.kind::f16 [%0], x, y, %4, p;\n\t}" ::"r"(d), "r"(a), "r"(b),
+                 "r"(static_cast<uint32_t>(add)), "r"(shape), "n"(DESC_HIGH)
+                 : "memory");
+}
 template <uint32_t SHAPE> __device__ __forceinline__ void warp_mma_ta(uint32_t d, uint32_t a, uint32_t b, bool add)
 {
     asm volatile("{\n\t.reg .pred p, e;\n\t.reg .b64 y;\n\t"
