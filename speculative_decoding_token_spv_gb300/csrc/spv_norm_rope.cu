@@ -55,6 +55,22 @@ template <typename T> __device__ __forceinline__ void widen8(float *y, const uin
 #pragma unroll
     for (int i = 0; i < 8; ++i) y[i] = Num<T>::up(x[i]);
 }
+// x times unit and the eight weights from w on.
+__device__ __forceinline__ void weigh8(float *x, const float *w, float unit)
+{
+#pragma unroll
+    for (int i = 0; i < 8; i += 4) {
+        const float4 a = *reinterpret_cast<const float4 *>(w + i);
+        x[i] *= unit * a.x, x[i + 1] *= unit * a.y, x[i + 2] *= unit * a.z, x[i + 3] *= unit * a.w;
+    }
+}
+// (u, z) turned by the angle whose cosine and sine are (c, s).
+__device__ __forceinline__ void turn(float &u, float &z, float c, float s)
+{
+    const float x = u;
+    u = x * c - z * s;
+    z = z * c + x * s;
+}
 template <typename C> struct alignas(8 * sizeof(C)) Eight {
     C x[8];
 };
@@ -70,6 +86,7 @@ template <int MODE, int TOKENS, typename T, typename C>
 __global__ void __launch_bounds__(NORM_THREADS) norm_rope_kernel(const NormRopeParams p, const int width)
 {
     extern __shared__ __align__(16) float shared[];
+    __shared__ int pages[TOKENS];  // of the tokens; -1: not written
     const int D = p.D, half = p.half;
     float2 *cs = reinterpret_cast<float2 *>(shared);             // [token][pair], padded to 16 bytes
     const int cs_row = (half + 1) & ~1;
@@ -89,19 +106,21 @@ __global__ void __launch_bounds__(NORM_THREADS) norm_rope_kernel(const NormRopeP
     struct Data {
         uint4 x, y;
     };
-    const int all = tokens * heads;
     struct Where {
         int token, head;
     };
-    auto where = [&](int i) {
-        const int tk = TOKENS == 1 ? 0 : i / heads;
-        return Where{tk, i - tk * heads};
+    // a group's heads are `groups` apart in the row of work
+    const int step = TOKENS == 1 ? 0 : groups / heads, step_heads = groups - step * heads;
+    auto after = [&](Where w) {
+        w.token += step;
+        w.head += step_heads;
+        if (TOKENS > 1 && w.head >= heads) ++w.token, w.head -= heads;
+        return w;
     };
     // v has no partners: its lanes take 8 elements at 8 lane, and where a group has fewer lanes than that, 8 more behind
     auto v_at = [&](int i) { return 8 * (lane + i * width); };
-    auto fetch = [&](int i, Data &to) {
-        if (i >= all) return;
-        const Where w = where(i);
+    auto fetch = [&](Where w, Data &to) {
+        if (w.token >= tokens || w.head >= heads) return;
         if (w.head >= p.q_heads + kv_heads) {
             const T *row = v0 + w.token * p.stride[5] + (w.head - p.q_heads - kv_heads) * D;
             if (v_at(0) < D) to.x = *reinterpret_cast<const uint4 *>(row + v_at(0));
@@ -115,7 +134,9 @@ __global__ void __launch_bounds__(NORM_THREADS) norm_rope_kernel(const NormRopeP
     };
     Data now{}, next{};
     chain_begin();
-    fetch(group, now);
+    Where w{TOKENS == 1 ? 0 : group / heads, 0};
+    w.head = group - w.token * heads;
+    fetch(w, now);
     const SeqLens s = seq_lens(p.ctx_lens, p.new_lens, b, p.T, p.c);
     const int32_t *table = p.c.table + static_cast<int64_t>(b) * p.c.max_pages;
     if (t0 == 0 && p.row_status) {  // all pages that the sequence's new tokens touch
@@ -143,6 +164,7 @@ __global__ void __launch_bounds__(NORM_THREADS) norm_rope_kernel(const NormRopeP
         const float *w = i < D ? p.q_weight : p.k_weight;
         weights[i] = w ? __ldg(w + (i < D ? i : i - D)) : 1.0f;
     }
+    if (tid < live) pages[tid] = page_of(p.c, table, s.ctx + t0 + tid);
     if (p.slot_pos)
         for (int i = tid; i < live * kv_heads; i += NORM_THREADS) {
             const int tk = i / kv_heads, h = i - tk * kv_heads, slot = s.ctx + t0 + tk;
@@ -155,10 +177,10 @@ __global__ void __launch_bounds__(NORM_THREADS) norm_rope_kernel(const NormRopeP
     const int todo = live * heads;
     const int rounds = (todo + groups - 1) / groups;  // of every group: shuffles need whole warps
     for (int round = 0; round < rounds; ++round) {
-        const int i = round * groups + group;
-        fetch(i + groups, next);
-        const bool here = i < todo;
-        const Where w = where(here ? i : 0);
+        const Where then = after(w);
+        fetch(then, next);
+        const bool here = round * groups + group < todo;
+        if (!here) w = Where{0, 0};
         const bool is_q = w.head < p.q_heads, is_v = w.head >= p.q_heads + kv_heads;
         const int h = is_q ? w.head : is_v ? w.head - p.q_heads - kv_heads : w.head - p.q_heads;  // in its tensor
         const bool pair = MODE == NORM_HALVES && turns;
@@ -180,31 +202,25 @@ __global__ void __launch_bounds__(NORM_THREADS) norm_rope_kernel(const NormRopeP
                 const float unit = 1.0f / sqrtf(sum / static_cast<float>(D) + p.eps);
                 const float *wt = weights + (is_q ? 0 : D);
                 if (works) {
-#pragma unroll
-                    for (int e = 0; e < 8; ++e) x[e] *= unit * wt[d + e];
-                    if (pair) {
-#pragma unroll
-                        for (int e = 0; e < 8; ++e) y[e] *= unit * wt[other + e];
-                    }
+                    weigh8(x, wt + d, unit);
+                    if (pair) weigh8(y, wt + other, unit);
                 }
             }
             const float2 *mine = cs + w.token * cs_row;
             if (pair) {
 #pragma unroll
-                for (int e = 0; e < 8; ++e) {
-                    const float2 a = mine[d + e];
-                    const float u = x[e], z = y[e];
-                    x[e] = u * a.x - z * a.y;
-                    y[e] = z * a.x + u * a.y;
+                for (int e = 0; e < 8; e += 2) {
+                    const float4 a = *reinterpret_cast<const float4 *>(mine + d + e);
+                    turn(x[e], y[e], a.x, a.y);
+                    turn(x[e + 1], y[e + 1], a.z, a.w);
                 }
             } else if (MODE == NORM_PAIRS && turns) {
 #pragma unroll
-                for (int e = 0; e < 8; e += 2) {
+                for (int e = 0; e < 8; e += 4) {
                     if (d + e >= 2 * half) continue;
-                    const float2 a = mine[(d + e) >> 1];
-                    const float u = x[e], z = x[e + 1];
-                    x[e] = u * a.x - z * a.y;
-                    x[e + 1] = z * a.x + u * a.y;
+                    const float4 a = *reinterpret_cast<const float4 *>(mine + ((d + e) >> 1));
+                    turn(x[e], x[e + 1], a.x, a.y);
+                    if (d + e + 2 < 2 * half) turn(x[e + 2], x[e + 3], a.z, a.w);
                 }
             }
         }
@@ -232,7 +248,7 @@ __global__ void __launch_bounds__(NORM_THREADS) norm_rope_kernel(const NormRopeP
                 if (works) narrow8(row + d, x, 1.0f);
                 if (works && pair) narrow8(row + other, y, 1.0f);
             } else {
-                const int slot = s.ctx + t0 + w.token, page = page_of(p.c, table, slot);
+                const int slot = s.ctx + t0 + w.token, page = pages[w.token];
                 if (page >= 0) {
                     const PoolView &pool = is_v ? p.c.v : p.c.k;
                     C *row = reinterpret_cast<C *>(const_cast<char *>(row_ptr(p.c, pool, page, slot, h)));
@@ -254,6 +270,7 @@ __global__ void __launch_bounds__(NORM_THREADS) norm_rope_kernel(const NormRopeP
             }
         }
         now = next;
+        w = then;
     }
 }
 
