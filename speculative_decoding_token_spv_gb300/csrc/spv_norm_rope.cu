@@ -9,13 +9,19 @@
 // and the store is held in 32 bits.
 //
 // What bounds it is reading q, k, v and writing q, K, V once.  A block takes one
-// token, or four of a sequence where there are enough to fill the GPU, and
-// computes their cosines and sines once for all heads.  The heads of q, k and v
-// of these tokens are one row of work: groups of lanes take a head each, a lane
-// 8 elements and, of halves, their partners, so that the sum of squares is a few
-// shuffles and the rotation needs no exchange; a head is asked for while the one
-// before it is worked on.
-#include "spv_kv.cuh"
+// token, or four or eight of a sequence where there are enough to fill the GPU,
+// and computes their cosines and sines once for all heads.  Groups of lanes take
+// every so many heads of one token each, a lane 8 elements and, of halves, their
+// partners, so that the sum of squares is a few shuffles, the rotation needs no
+// exchange, and a lane's cosines, sines and weights stay in its registers from
+// head to head; a head is asked for while the one before it is worked on.
+// Arithmetic is in pairs.  Measured (32 heads on 8 of 128, 16 bits): 16,088
+// tokens 88 us, 4.5 TB/s, 74 us where a quarter of them is padding; 4,800 tokens
+// 30 us, 2,400 (in L2) 15 us; one token 6.3 us.  Instructions and their waits are
+// half of it: with no arithmetic 62 us are left of 77.  Rows by way of shared
+// memory, all at once (77 us) or an item ahead in blocks that stay (102 us), one
+// token a block (158 us) and more blocks of fewer registers (78 us) were slower.
+#include "spv_mma.cuh"
 
 namespace spv {
 
@@ -35,7 +41,6 @@ struct NormRopeParams {
 };
 
 constexpr int NORM_THREADS = 256;
-constexpr int NORM_TOKENS = 4;  // of a block, where there are many
 
 enum NormMode {
     NORM_PAIRS,   // interleaved, or nothing turns: a lane has 8 elements
@@ -49,95 +54,143 @@ template <int MODE> __host__ __device__ inline int norm_tasks(int D, int half)
     return MODE == NORM_HALVES ? (half >> 3) + ((D - 2 * half) >> 3) : D >> 3;
 }
 
+// Floats of a token's cosines and sines, a multiple of four.
+__host__ __device__ inline int norm_angles(int half) { return 2 * ((half + 1) & ~1); }
+
 template <typename T> __device__ __forceinline__ void widen8(float *y, const uint4 &raw)
 {
     const T *x = reinterpret_cast<const T *>(&raw);
 #pragma unroll
     for (int i = 0; i < 8; ++i) y[i] = Num<T>::up(x[i]);
 }
-// x times unit and the eight weights from w on.
-__device__ __forceinline__ void weigh8(float *x, const float *w, float unit)
+// Four pairs of floats, on each of which one instruction works.
+__device__ __forceinline__ void pairs_of(unsigned long long (&y)[4], const float *x)
 {
 #pragma unroll
-    for (int i = 0; i < 8; i += 4) {
-        const float4 a = *reinterpret_cast<const float4 *>(w + i);
-        x[i] *= unit * a.x, x[i + 1] *= unit * a.y, x[i + 2] *= unit * a.z, x[i + 3] *= unit * a.w;
+    for (int i = 0; i < 4; ++i) y[i] = pack2(x[2 * i], x[2 * i + 1]);
+}
+__device__ __forceinline__ void floats_of(float *x, const unsigned long long (&y)[4])
+{
+#pragma unroll
+    for (int i = 0; i < 4; ++i) unpack2(y[i], x[2 * i], x[2 * i + 1]);
+}
+// Eight floats of shared memory, 16 bytes at a time.
+__device__ __forceinline__ void pairs_at(unsigned long long (&y)[4], const float *at)
+{
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+        const float4 a = reinterpret_cast<const float4 *>(at)[i];
+        y[2 * i] = pack2(a.x, a.y);
+        y[2 * i + 1] = pack2(a.z, a.w);
     }
 }
-// (u, z) turned by the angle whose cosine and sine are (c, s).
-__device__ __forceinline__ void turn(float &u, float &z, float c, float s)
+__device__ __forceinline__ unsigned long long add_squares(const float *x, unsigned long long sum)
 {
-    const float x = u;
-    u = x * c - z * s;
-    z = z * c + x * s;
+    unsigned long long y[4];
+    pairs_of(y, x);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) sum = ffma2(y[i], y[i], sum);
+    return sum;
 }
-template <typename C> struct alignas(8 * sizeof(C)) Eight {
-    C x[8];
-};
+// x times unit and eight weights.
+__device__ __forceinline__ void weigh8(float *x, const unsigned long long (&w)[4], float unit)
+{
+    unsigned long long y[4];
+    pairs_of(y, x);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) y[i] = mul2(y[i], mul2(w[i], pack2(unit, unit)));
+    floats_of(x, y);
+}
+// Eight (u, z) turned by the angles whose cosines and sines are (c, s).
+__device__ __forceinline__ void turn8(float *u, float *z, const unsigned long long (&c)[4], const unsigned long long (&s)[4])
+{
+    unsigned long long a[4], b[4];
+    pairs_of(a, u);
+    pairs_of(b, z);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const unsigned long long x = a[i];
+        a[i] = ffma2(mul2(b[i], s[i]), pack2(-1.0f, -1.0f), mul2(x, c[i]));
+        b[i] = ffma2(x, s[i], mul2(b[i], c[i]));
+    }
+    floats_of(u, a);
+    floats_of(z, b);
+}
 template <typename C> __device__ __forceinline__ void narrow8(C *to, const float *y, float div)
 {
-    Eight<C> o;
+    if constexpr (sizeof(C) == 1) {
+        uint32_t o[4];
 #pragma unroll
-    for (int i = 0; i < 8; ++i) o.x[i] = Num<C>::down(sizeof(C) == 1 ? y[i] / div : y[i]);
-    *reinterpret_cast<Eight<C> *>(to) = o;
+        for (int i = 0; i < 4; ++i)
+            o[i] = __nv_cvt_float2_to_fp8x2(make_float2(y[2 * i] / div, y[2 * i + 1] / div), __NV_SATFINITE, __NV_E4M3);
+        *reinterpret_cast<uint2 *>(to) = make_uint2(o[0] | o[1] << 16, o[2] | o[3] << 16);
+    } else {
+        *reinterpret_cast<uint4 *>(to) = make_uint4(pack_mma<C>(y[0], y[1]), pack_mma<C>(y[2], y[3]), pack_mma<C>(y[4], y[5]), pack_mma<C>(y[6], y[7]));
+    }
 }
 
 template <int MODE, int TOKENS, typename T, typename C>
-__global__ void __launch_bounds__(NORM_THREADS) norm_rope_kernel(const NormRopeParams p, const int width)
+__global__ void __launch_bounds__(NORM_THREADS, 2) norm_rope_kernel(const NormRopeParams p, const int width)
 {
     extern __shared__ __align__(16) float shared[];
-    __shared__ int pages[TOKENS];  // of the tokens; -1: not written
-    const int D = p.D, half = p.half;
-    float2 *cs = reinterpret_cast<float2 *>(shared);             // [token][pair], padded to 16 bytes
-    const int cs_row = (half + 1) & ~1;
-    float *weights = shared + 2 * TOKENS * cs_row;               // [q, k][D]
-    float *odd = weights + 2 * D;                                // NORM_ODD: a head of each group
+    __shared__ int64_t rows[2][TOKENS];  // bytes from a head's first slot to the token's, of K and V; -1: not written
+    const int D = p.D, half = p.half, kv_heads = p.c.kv_heads;
     const int tid = threadIdx.x, blocks = (p.T + TOKENS - 1) / TOKENS, b = blockIdx.x / blocks;
-    const int t0 = (blockIdx.x - b * blocks) * TOKENS, tokens = min(TOKENS, p.T - t0);
-    const int n0 = b * p.T + t0, kv_heads = p.c.kv_heads, heads = p.q_heads + 2 * kv_heads;
-    const T *q0 = static_cast<const T *>(p.q) + b * p.stride[0] + t0 * p.stride[1];
-    const T *k0 = static_cast<const T *>(p.k) + b * p.stride[2] + t0 * p.stride[3];
-    const T *v0 = static_cast<const T *>(p.v) + b * p.stride[4] + t0 * p.stride[5];
-    // this lane's place in its group and in a head: 8 elements from d on, and their partners from `other` on
+    const int t0 = (blockIdx.x - b * blocks) * TOKENS, tokens = min(TOKENS, p.T - t0), n0 = b * p.T + t0;
     const int lane = tid & (width - 1), group = tid / width, groups = NORM_THREADS / width;
+    float *cs = shared;                         // [token]: pairs (cosine, sine), of NORM_HALVES all cosines before the sines
+    const int cs_row = norm_angles(half);
+    float *weights = shared + TOKENS * cs_row;  // [q, k][D]
+    float *odd = weights + 2 * D;               // NORM_ODD: a head of each group
+    // this lane's place in a head: 8 elements from d on, and their partners from `other` on
     const bool works = lane < norm_tasks<MODE>(D, half);
-    const bool turns = MODE == NORM_HALVES ? lane < half >> 3 : 8 * lane < 2 * half;
+    const bool turns = MODE == NORM_HALVES ? lane < half >> 3 : 8 * lane < 2 * half, pair = MODE == NORM_HALVES && turns;
     const int d = MODE == NORM_HALVES && !turns ? 8 * lane + half : 8 * lane, other = d + half;
+    // a group has one token, and every so many heads of it
+    const int token = group % TOKENS, my_first = group / TOKENS, apart = groups / TOKENS;
     struct Data {
         uint4 x, y;
     };
-    struct Where {
-        int token, head;
+    auto row_of = [&](const void *x, int64_t of_b, int64_t of_t) { return static_cast<const T *>(x) + b * of_b + (t0 + token) * of_t + my_first * D; };
+    auto get = [&](bool there, Data &to, const T *row) {
+        if (there && works) to.x = *reinterpret_cast<const uint4 *>(row + d);
+        if (there && pair) to.y = *reinterpret_cast<const uint4 *>(row + other);
     };
-    // a group's heads are `groups` apart in the row of work
-    const int step = TOKENS == 1 ? 0 : groups / heads, step_heads = groups - step * heads;
-    auto after = [&](Where w) {
-        w.token += step;
-        w.head += step_heads;
-        if (TOKENS > 1 && w.head >= heads) ++w.token, w.head -= heads;
-        return w;
+    // v has no partners: 8 elements at 8 lane, and where a group has fewer lanes than that, 8 more behind
+    const int v0 = 8 * lane, v1 = 8 * (lane + width);
+    auto get_v = [&](bool there, Data &to, const T *row) {
+        if (there && v0 < D) to.x = *reinterpret_cast<const uint4 *>(row + v0);
+        if (there && v1 < D) to.y = *reinterpret_cast<const uint4 *>(row + v1);
     };
-    // v has no partners: its lanes take 8 elements at 8 lane, and where a group has fewer lanes than that, 8 more behind
-    auto v_at = [&](int i) { return 8 * (lane + i * width); };
-    auto fetch = [&](Where w, Data &to) {
-        if (w.token >= tokens || w.head >= heads) return;
-        if (w.head >= p.q_heads + kv_heads) {
-            const T *row = v0 + w.token * p.stride[5] + (w.head - p.q_heads - kv_heads) * D;
-            if (v_at(0) < D) to.x = *reinterpret_cast<const uint4 *>(row + v_at(0));
-            if (v_at(1) < D) to.y = *reinterpret_cast<const uint4 *>(row + v_at(1));
-            return;
-        }
-        const T *row = w.head < p.q_heads ? q0 + w.token * p.stride[1] + w.head * D
-                                          : k0 + w.token * p.stride[3] + (w.head - p.q_heads) * D;
-        if (works) to.x = *reinterpret_cast<const uint4 *>(row + d);
-        if (MODE == NORM_HALVES && works && turns) to.y = *reinterpret_cast<const uint4 *>(row + other);
-    };
-    Data now{}, next{};
+    const T *q_row = row_of(p.q, p.stride[0], p.stride[1]), *k_row = row_of(p.k, p.stride[2], p.stride[3]), *v_row = row_of(p.v, p.stride[4], p.stride[5]);
+    Data q_now{}, k_now{}, v_now{};
     chain_begin();
-    Where w{TOKENS == 1 ? 0 : group / heads, 0};
-    w.head = group - w.token * heads;
-    fetch(w, now);
+    get(token < tokens && my_first < p.q_heads, q_now, q_row);
+    get(token < tokens && my_first < kv_heads, k_now, k_row);
+    get_v(token < tokens && my_first < kv_heads, v_now, v_row);
     const SeqLens s = seq_lens(p.ctx_lens, p.new_lens, b, p.T, p.c);
+    auto position = [&](int tk, int axis) {
+        return p.positions ? __ldg(p.positions + static_cast<int64_t>(n0 + tk) * p.num_axes + axis) : s.ctx + t0 + tk;
+    };
+    const int live = s.bad ? 0 : max(0, min(tokens, s.fresh - t0));
+    for (int i = tid; i < live * half; i += NORM_THREADS) {
+        const int tk = TOKENS == 1 ? 0 : i / half, e = i - tk * half;
+        const int axis = p.axes ? min(max(__ldg(p.axes + e), 0), p.num_axes - 1) : 0;
+        const unsigned long long turn = static_cast<unsigned long long>(static_cast<long long>(position(tk, axis))) * __ldg(p.freqs + e);
+        // the top 32 bits, signed: half a turn either way, at most 2^-33 turns off
+        float sn, cn;
+        sincospif(static_cast<float>(static_cast<int>((turn + (1ull << 31)) >> 32)) * 0x1p-31f, &sn, &cn);
+        cn *= p.mscale, sn *= p.mscale;
+        float *at = cs + tk * cs_row;
+        if (MODE == NORM_HALVES)
+            at[e] = cn, at[half + e] = sn;
+        else
+            reinterpret_cast<float2 *>(at)[e] = make_float2(cn, sn);
+    }
+    for (int i = tid; i < 2 * D; i += NORM_THREADS) {
+        const float *w = i < D ? p.q_weight : p.k_weight;
+        weights[i] = w ? __ldg(w + (i < D ? i : i - D)) : 1.0f;
+    }
     const int32_t *table = p.c.table + static_cast<int64_t>(b) * p.c.max_pages;
     if (t0 == 0 && p.row_status) {  // all pages that the sequence's new tokens touch
         int bad = s.bad;
@@ -147,130 +200,120 @@ __global__ void __launch_bounds__(NORM_THREADS) norm_rope_kernel(const NormRopeP
         bad = __syncthreads_or(bad);
         if (tid == 0) p.row_status[b] = bad ? KV_STATUS_BAD : 0;
     }
-    const int live = s.bad ? 0 : max(0, min(tokens, s.fresh - t0));
-    auto position = [&](int tk, int axis) {
-        return p.positions ? __ldg(p.positions + static_cast<int64_t>(n0 + tk) * p.num_axes + axis) : s.ctx + t0 + tk;
-    };
-    for (int i = tid; i < live * half; i += NORM_THREADS) {
-        const int tk = TOKENS == 1 ? 0 : i / half, e = i - tk * half;
-        const int axis = p.axes ? min(max(__ldg(p.axes + e), 0), p.num_axes - 1) : 0;
-        const unsigned long long turn = static_cast<unsigned long long>(static_cast<long long>(position(tk, axis))) * __ldg(p.freqs + e);
-        // the top 32 bits, signed: half a turn either way, at most 2^-33 turns off
-        float sn, cn;
-        sincospif(static_cast<float>(static_cast<int>((turn + (1ull << 31)) >> 32)) * 0x1p-31f, &sn, &cn);
-        cs[tk * cs_row + e] = make_float2(cn * p.mscale, sn * p.mscale);
+    if (tid < live) {
+        const int slot = s.ctx + t0 + tid, page = page_of(p.c, table, slot), in_page = slot & ((1 << p.c.page_shift) - 1);
+        rows[0][tid] = page < 0 ? -1 : page * p.c.k.page_stride + in_page * p.c.k.slot_stride;
+        rows[1][tid] = page < 0 ? -1 : page * p.c.v.page_stride + in_page * p.c.v.slot_stride;
     }
-    for (int i = tid; i < 2 * D; i += NORM_THREADS) {
-        const float *w = i < D ? p.q_weight : p.k_weight;
-        weights[i] = w ? __ldg(w + (i < D ? i : i - D)) : 1.0f;
-    }
-    if (tid < live) pages[tid] = page_of(p.c, table, s.ctx + t0 + tid);
     if (p.slot_pos)
         for (int i = tid; i < live * kv_heads; i += NORM_THREADS) {
             const int tk = i / kv_heads, h = i - tk * kv_heads, slot = s.ctx + t0 + tk;
             if (slot < p.pos_stride) p.slot_pos[(static_cast<int64_t>(b) * kv_heads + h) * p.pos_stride + slot] = position(tk, 0);
         }
-    __syncthreads();
     T *q_out = static_cast<T *>(p.q_out) + static_cast<int64_t>(n0) * p.q_heads * D;
-    for (int i = live * p.q_heads * (D >> 3) + tid; i < tokens * p.q_heads * (D >> 3); i += NORM_THREADS)
-        reinterpret_cast<uint4 *>(q_out)[i] = uint4{};
-    const int todo = live * heads;
-    const int rounds = (todo + groups - 1) / groups;  // of every group: shuffles need whole warps
-    for (int round = 0; round < rounds; ++round) {
-        const Where then = after(w);
-        fetch(then, next);
-        const bool here = round * groups + group < todo;
-        if (!here) w = Where{0, 0};
-        const bool is_q = w.head < p.q_heads, is_v = w.head >= p.q_heads + kv_heads;
-        const int h = is_q ? w.head : is_v ? w.head - p.q_heads - kv_heads : w.head - p.q_heads;  // in its tensor
-        const bool pair = MODE == NORM_HALVES && turns;
-        float x[8], y[8];
-        widen8<T>(x, now.x);
-        widen8<T>(y, now.y);
-        float sum = 0.0f;
-        if (works) {
-#pragma unroll
-            for (int e = 0; e < 8; ++e) sum += x[e] * x[e];
-            if (pair) {
-#pragma unroll
-                for (int e = 0; e < 8; ++e) sum += y[e] * y[e];
-            }
+    for (int i = live * p.q_heads * D + 8 * tid; i < tokens * p.q_heads * D; i += 8 * NORM_THREADS) *reinterpret_cast<uint4 *>(q_out + i) = uint4{};
+    __syncthreads();
+    if (live == 0) return;
+    const bool there = token < live;
+    const float *angles = cs + token * cs_row;
+    unsigned long long cosines[4], sines[4];  // NORM_PAIRS: `cosines` has both
+    if (pair) {
+        pairs_at(cosines, angles + d);
+        pairs_at(sines, angles + half + d);
+    } else if (MODE == NORM_PAIRS && turns) {
+        pairs_at(cosines, angles + d);
+    }
+    const float by_d = 1.0f / static_cast<float>(D);
+    // now: this group's first head, which is at `row`; to: where head 0 goes; apart_by: from head to head
+    auto turn_heads = [&](bool there, int count, Data now, const T *row, const float *weight, const float *in_shared, auto *to, int64_t apart_by, const float *scale) {
+        unsigned long long wx[4], wy[4];
+        if (weight && works) {
+            pairs_at(wx, in_shared + d);
+            if (pair) pairs_at(wy, in_shared + other);
         }
-        for (int o = width >> 1; o; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-        if (!is_v) {
-            if (is_q ? p.q_weight != nullptr : p.k_weight != nullptr) {
-                const float unit = 1.0f / sqrtf(sum / static_cast<float>(D) + p.eps);
-                const float *wt = weights + (is_q ? 0 : D);
+#pragma unroll 1
+        for (int at = my_first, round = 0; round < count; round += apart, at += apart) {  // whole warps: shuffles need them
+            const bool here = there && at < count;
+            Data next;
+            row += apart * D;
+            get(there && at + apart < count, next, row);
+            float x[8], y[8];
+            widen8<T>(x, now.x);
+            widen8<T>(y, now.y);
+            now = next;
+            if (weight) {
+                float sum = 0.0f;
                 if (works) {
-                    weigh8(x, wt + d, unit);
-                    if (pair) weigh8(y, wt + other, unit);
+                    unsigned long long squares = add_squares(x, 0);
+                    if (pair) squares = add_squares(y, squares);
+                    float more;
+                    unpack2(squares, sum, more);
+                    sum += more;
                 }
+                for (int o = width >> 1; o; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+                const float unit = rsqrtf(fmaf(sum, by_d, p.eps));
+                if (works) weigh8(x, wx, unit);
+                if (works && pair) weigh8(y, wy, unit);
             }
-            const float2 *mine = cs + w.token * cs_row;
             if (pair) {
-#pragma unroll
-                for (int e = 0; e < 8; e += 2) {
-                    const float4 a = *reinterpret_cast<const float4 *>(mine + d + e);
-                    turn(x[e], y[e], a.x, a.y);
-                    turn(x[e + 1], y[e + 1], a.z, a.w);
-                }
+                turn8(x, y, cosines, sines);
             } else if (MODE == NORM_PAIRS && turns) {
 #pragma unroll
-                for (int e = 0; e < 8; e += 4) {
+                for (int e = 0; e < 8; e += 2) {
                     if (d + e >= 2 * half) continue;
-                    const float4 a = *reinterpret_cast<const float4 *>(mine + ((d + e) >> 1));
-                    turn(x[e], x[e + 1], a.x, a.y);
-                    if (d + e + 2 < 2 * half) turn(x[e + 2], x[e + 3], a.z, a.w);
+                    float c, sn;
+                    unpack2(cosines[e >> 1], c, sn);
+                    const float u = x[e], z = x[e + 1];
+                    x[e] = u * c - z * sn;
+                    x[e + 1] = z * c + u * sn;
                 }
             }
-        }
-        if (MODE == NORM_ODD) {  // a lane's partners are in other lanes, at other places of their 8
-            float *head = odd + group * D;
-            if (works)
+            if (MODE == NORM_ODD) {  // a lane's partners are in other lanes, at other places of their 8
+                float *head = odd + group * D;
+                if (works)
 #pragma unroll
-                for (int e = 0; e < 8; ++e) head[d + e] = x[e];
-            __syncwarp();
-            if (works && !is_v) {
-                const float2 *mine = cs + w.token * cs_row;
+                    for (int e = 0; e < 8; ++e) head[d + e] = x[e];
+                __syncwarp();
+                if (works)
 #pragma unroll
-                for (int e = 0; e < 8; ++e) {
-                    const int at = d + e;
-                    if (at >= 2 * half) continue;
-                    const float2 a = mine[at < half ? at : at - half];
-                    x[e] = at < half ? x[e] * a.x - head[at + half] * a.y : x[e] * a.x + head[at - half] * a.y;
-                }
-            }
-            __syncwarp();
-        }
-        if (here) {
-            if (is_q) {
-                T *row = q_out + (static_cast<int64_t>(w.token) * p.q_heads + h) * D;
-                if (works) narrow8(row + d, x, 1.0f);
-                if (works && pair) narrow8(row + other, y, 1.0f);
-            } else {
-                const int slot = s.ctx + t0 + w.token, page = pages[w.token];
-                if (page >= 0) {
-                    const PoolView &pool = is_v ? p.c.v : p.c.k;
-                    C *row = reinterpret_cast<C *>(const_cast<char *>(row_ptr(p.c, pool, page, slot, h)));
-                    const float *scale = is_v ? p.c.v_scale : p.c.k_scale;
-                    const float div = sizeof(C) == 1 && scale ? __ldg(scale + h) : 1.0f;
-                    if (is_v) {
-                        if constexpr (std::is_same<T, C>::value) {
-                            if (v_at(0) < D) *reinterpret_cast<uint4 *>(row + v_at(0)) = now.x;
-                            if (v_at(1) < D) *reinterpret_cast<uint4 *>(row + v_at(1)) = now.y;
-                        } else {
-                            if (v_at(0) < D) narrow8(row + v_at(0), x, div);
-                            if (v_at(1) < D) narrow8(row + v_at(1), y, div);
-                        }
-                    } else {
-                        if (works) narrow8(row + d, x, div);
-                        if (works && pair) narrow8(row + other, y, div);
+                    for (int e = 0; e < 8; ++e) {
+                        const int i = d + e;
+                        if (i >= 2 * half) continue;
+                        const float2 a = reinterpret_cast<const float2 *>(angles)[i < half ? i : i - half];
+                        x[e] = i < half ? x[e] * a.x - head[i + half] * a.y : x[e] * a.x + head[i - half] * a.y;
                     }
-                }
+                __syncwarp();
+            }
+            if (here && works) {
+                const float div = sizeof(*to) == 1 && scale ? __ldg(scale + at) : 1.0f;
+                narrow8(to + at * apart_by + d, x, div);
+                if (pair) narrow8(to + at * apart_by + other, y, div);
             }
         }
-        now = next;
-        w = then;
+    };
+    turn_heads(there, p.q_heads, q_now, q_row, p.q_weight, weights, q_out + static_cast<int64_t>(token) * p.q_heads * D, D, nullptr);
+    const int64_t k_at = there ? rows[0][token] : -1, v_at = there ? rows[1][token] : -1;
+    auto head_0 = [&](const PoolView &pool, int64_t at) { return reinterpret_cast<C *>(const_cast<char *>(pool.base) + at); };
+    const int64_t element = sizeof(C);
+    turn_heads(k_at >= 0, kv_heads, k_now, k_row, p.k_weight, weights + D, head_0(p.c.k, k_at), p.c.k.head_stride / element, p.c.k_scale);
+    if (v_at < 0) return;
+    for (int at = my_first; at < kv_heads; at += apart) {
+        C *to = head_0(p.c.v, v_at) + at * (p.c.v.head_stride / element);
+        Data next;
+        v_row += apart * D;
+        get_v(at + apart < kv_heads, next, v_row);
+        if constexpr (std::is_same<T, C>::value) {
+            if (v0 < D) *reinterpret_cast<uint4 *>(to + v0) = v_now.x;
+            if (v1 < D) *reinterpret_cast<uint4 *>(to + v1) = v_now.y;
+        } else {
+            const float div = p.c.v_scale ? __ldg(p.c.v_scale + at) : 1.0f;
+            float x[8];
+            widen8<T>(x, v_now.x);
+            if (v0 < D) narrow8(to + v0, x, div);
+            widen8<T>(x, v_now.y);
+            if (v1 < D) narrow8(to + v1, x, div);
+        }
+        v_now = next;
     }
 }
 
@@ -278,13 +321,16 @@ template <int MODE, typename T, typename C> static cudaError_t launch_mode(const
 {
     int width = 1;
     while (width < norm_tasks<MODE>(p.D, p.half)) width *= 2;
-    const int pairs = (p.half + 1) & ~1, odd = MODE == NORM_ODD ? NORM_THREADS / width * p.D : 0;
-    auto bytes = [&](int tokens) { return (2 * tokens * pairs + 2 * p.D + odd) * static_cast<int>(sizeof(float)); };
-    // four tokens a block once that still gives every SM eight blocks
-    if (static_cast<int64_t>(p.B) * p.T >= 8 * 152 * NORM_TOKENS)
-        return launch_chained(norm_rope_kernel<MODE, NORM_TOKENS, T, C>, dim3(p.B * ((p.T + NORM_TOKENS - 1) / NORM_TOKENS)),
-                              NORM_THREADS, bytes(NORM_TOKENS), st, p, width);
-    return launch_chained(norm_rope_kernel<MODE, 1, T, C>, dim3(p.B * p.T), NORM_THREADS, bytes(1), st, p, width);
+    auto go = [&](auto kernel, int tokens) {
+        const int floats = tokens * norm_angles(p.half) + 2 * p.D + (MODE == NORM_ODD ? NORM_THREADS / width * p.D : 0);
+        return launch_chained(kernel, dim3(p.B * ((p.T + tokens - 1) / tokens)), NORM_THREADS, floats * static_cast<int>(sizeof(float)), st, p, width);
+    };
+    // More tokens a block once that still gives every SM three blocks: 4,800 tokens take 30 us by eight, 33 by four and 61 by one,
+    // 2,400 take 15 us by four and 29 by one.
+    const int64_t blocks = static_cast<int64_t>(p.B) * p.T / (3 * 152);
+    if (blocks >= 8) return go(norm_rope_kernel<MODE, 8, T, C>, 8);
+    if (blocks >= 4) return go(norm_rope_kernel<MODE, 4, T, C>, 4);
+    return go(norm_rope_kernel<MODE, 1, T, C>, 1);
 }
 template <typename T, typename C> static cudaError_t launch(const NormRopeParams &p, bool interleaved, cudaStream_t st)
 {
