@@ -19,8 +19,10 @@
 // tokens 88 us, 4.5 TB/s, 74 us where a quarter of them is padding; 4,800 tokens
 // 30 us, 2,400 (in L2) 15 us; one token 6.3 us.  Instructions and their waits are
 // half of it: with no arithmetic 62 us are left of 77.  Rows by way of shared
-// memory, all at once (77 us) or an item ahead in blocks that stay (102 us), one
-// token a block (158 us) and more blocks of fewer registers (78 us) were slower.
+// memory, all at once (77 us) or an item ahead in blocks that stay (102 us), two
+// heads asked for ahead (76 us), positions and pages before the lengths are used
+// (77 us), one token a block (158 us) and more blocks of fewer registers (78 us)
+// were no faster.
 #include "spv_mma.cuh"
 
 namespace spv {
@@ -211,7 +213,8 @@ __global__ void __launch_bounds__(NORM_THREADS, 2) norm_rope_kernel(const NormRo
             if (slot < p.pos_stride) p.slot_pos[(static_cast<int64_t>(b) * kv_heads + h) * p.pos_stride + slot] = position(tk, 0);
         }
     T *q_out = static_cast<T *>(p.q_out) + static_cast<int64_t>(n0) * p.q_heads * D;
-    for (int i = live * p.q_heads * D + 8 * tid; i < tokens * p.q_heads * D; i += 8 * NORM_THREADS) *reinterpret_cast<uint4 *>(q_out + i) = uint4{};
+    const int64_t token_q = static_cast<int64_t>(p.q_heads) * D;
+    for (int64_t i = live * token_q + 8 * tid; i < tokens * token_q; i += 8 * NORM_THREADS) *reinterpret_cast<uint4 *>(q_out + i) = uint4{};
     __syncthreads();
     if (live == 0) return;
     const bool there = token < live;

@@ -1,5 +1,7 @@
 // spv_scored.cu -- spv_paged_attention_scored for few rows a key head, and the
 // statuses of scored calls.
+#include <algorithm>
+
 #include "spv_attention_warps.cuh"
 
 namespace spv {
@@ -78,7 +80,7 @@ cudaError_t launch_attention_scored(const AttentionLaunch &L, cudaStream_t st)
     // through shared memory twice there, never (64 x 2,000 of 128: 169 and 90).  How long the caches are the host does not know:
     // what the page table has room for counts, or the window.
     int64_t slots = static_cast<int64_t>(k.max_pages) << log2_of(k.cache.page_size);
-    if (p.sc.window > 0 && !p.sc.slot_pos && p.sc.window + k.T < slots) slots = p.sc.window + k.T;
+    if (p.sc.window > 0 && !p.sc.slot_pos) slots = std::min<int64_t>(slots, static_cast<int64_t>(p.sc.window) + k.T);
     const double bytes = 4.0 * D * k.cache.kv_heads * k.B * static_cast<double>(slots);
     const bool large = !eight && (D == 256 ? bytes >= 64e6 : D == 128 && bytes >= 1e9);
     if (large || p.rows > (eight && D <= 128 ? 32 : 16)) return launch_tiles(p, k, false, st);

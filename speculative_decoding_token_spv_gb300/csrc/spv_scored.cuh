@@ -25,6 +25,6 @@ __host__ __device__ __forceinline__ ScoredWork work_of(const ScoredParams &p)
 // rows at a time (head_dim up to 128; the workspace has to have room for pieces
 // of so many).
 cudaError_t launch_tiles(const ScoredParams &p, const KvLaunch &L, bool pairs, cudaStream_t st);
-constexpr int TILES_PAIR_ROWS = 256;
+constexpr int TILES_PAIR_ROWS = 256;  // of a piece then
 
 }  // namespace spv
