@@ -22,10 +22,10 @@
 //
 // The same kernel serves calls with scores and masks (spv_scores): tiles before
 // the first slot that is seen only pass their old weights on.  The batch above
-// with capped scores takes 191 us: about 1,900 cycles a tile of 40 rows in each
-// of the two groups that sum, of which the cap is 450, exponentials and sums 450,
-// the rows' constants 180, the tile's old and new weights 250; K's bytes would
-// take 1,000.
+// with capped scores takes 191 us: of 3,800 cycles that a tile of 40 rows takes a
+// group (two groups are at work) the cap is 900, exponentials and sums 900, the
+// rows' constants 400, the tile's old and new weights 500, waits 500; the bytes of
+// two tiles would take 2,900.
 //
 // Every wait is bounded; one that gives up ends the block in order: the weights
 // that it still had to write become NaN, and the row_status of their sequences

@@ -35,8 +35,8 @@
 // thread's scores take 1,500 cycles (loads 240, maximum 400, exponentials and
 // weights 450, waits for products 470).  Capped scores, bound by the polynomials:
 // 906 us.  Distance biases 616, documents of some 1,000 tokens 199, a window of
-// 1,024 192, heads of 64 498, 16 heads of 256 574 us.  e4m3 888 us: widening K and
-// V, four warps.  An item's beginning and end take some 14,000 cycles (its rows'
+// 1,024 192, heads of 64 498, 16 heads of 256 574 us.  e4m3 769 us (heads of 64 639): widening K
+// and V, four warps.  An item's beginning and end take some 14,000 cycles (its rows'
 // intervals and q 5,500, the outputs 4,600, agreeing on the end 2,000).
 //
 // O is only rescaled when a maximum has grown by more than 2^8 (2^7 for f16).
@@ -71,6 +71,7 @@ struct TilesParams : ScoredParams {
 template <typename C, int D, int COPIES> struct TilesShape {
     static constexpr bool PAIR = COPIES == 0;
     static constexpr bool WIDEN = sizeof(C) == 1;
+    static constexpr bool ROWS_WIDEN = WIDEN && PAIR;            // the rows' threads bring q into f16's range, each its row
     static constexpr int PLACE = PAIR ? 64 : 128;                // columns from one place of scores to the next
     static constexpr int SUBS = PAIR ? 2 : 1, ROWS = PAIR ? 256 : 128 / (PAIR ? 1 : COPIES);
     static constexpr int KEYS = PAIR || D == 256 ? 64 : 128;     // of a tile
@@ -124,7 +125,7 @@ template <typename S> struct TilesCtl {
                 signed char depth[S::Q_PLACES][S::SUBS == 1 ? 64 : 1];  // else, of trees: per place of q the depth of each new token
             };
             float top[2][S::SUBS == 1 ? 256 : 1];                // maxima of the two halves, of a tile and the next; sums
-            signed char q_power[S::WIDEN ? S::Q_PLACES * S::ROWS : 1];  // e4m3: the rows of q are stored times 2^q_power
+            signed char q_power[S::WIDEN && !S::ROWS_WIDEN ? S::Q_PLACES * S::ROWS : 1];  // e4m3: the rows of q are stored times 2^q_power
         } at;
     };
 };
@@ -387,6 +388,16 @@ template <typename S> __device__ void tiles_items(const TilesParams &p, TileCurs
         if (end) return;
     }
 }
+// Whether the phase of `parity` is complete, without a wait.
+__device__ __forceinline__ bool mbar_done(uint64_t *bar, uint32_t parity)
+{
+    uint32_t done;
+    asm volatile("{\n\t.reg .pred p;\n\tmbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\tselp.u32 %0, 1, 0, p;\n\t}"
+                 : "=r"(done)
+                 : "r"(smem_u32(bar)), "r"(parity)
+                 : "memory");
+    return done != 0;
+}
 // The block's item k, for a whole warp; false at the end, or after a wait gave up.
 constexpr int TILES_TAKERS = 8 + 1 + 2 + 4;  // warps that take every item
 template <typename Ctl> __device__ __forceinline__ bool take_item(Ctl *ctl, int k, TileItem *it, unsigned *err, int lane)
@@ -471,7 +482,11 @@ __device__ void tiles_load(const TilesParams &p, char *smem, TilesCtl<S> *ctl, u
 
     TileItem it;
     int item = 0;
-    for (int k = 0; ok && take_item(ctl, k, &it, err, lane); ++k) {
+    for (int k = 0; ok; ++k) {
+        // The next item may come only when the rows have ended one whose tiles are still raw here: these go first.
+        if (S::WIDEN)
+            while (ok && waiting > 0 && !__all_sync(0xffffffffu, mbar_done(&ctl->item_full[k & 1], (k >> 1) & 1))) ok = widen();
+        if (!ok || !take_item(ctl, k, &it, err, lane)) break;
         const int t0 = it.t0, t1 = it.t1;
         if (t0 == t1) continue;
         const int32_t *table = p.c.table + static_cast<int64_t>(it.b) * p.c.max_pages;
@@ -669,7 +684,8 @@ __device__ void tiles_multiply(char *smem, TilesCtl<S> *ctl, unsigned *err, int 
 // the depths of the new tokens.  The copy engine brings it where a tile's rows
 // are whole tokens (the threads, some 20 instructions for 16 bytes, took 18,000
 // cycles for 256 rows); e4m3 caches: it is then multiplied into f16's range where
-// it lies.
+// it lies, in pairs of tiles by the rows' threads, a row each (889 us for 8,192
+// tokens when these two warps did it, 769 since).
 template <typename C, int D, int COPIES, typename S = TilesShape<C, D, COPIES>>
 __device__ void tiles_prepare(const TilesParams &p, char *smem, TilesCtl<S> *ctl, unsigned *err, int lt, const CUtensorMap *map_q)
 {
@@ -711,6 +727,10 @@ __device__ void tiles_prepare(const TilesParams &p, char *smem, TilesCtl<S> *ctl
                         (row0 + (S::PAIR ? part * 128 : 0)) / p.group, it.b, bar);
             }
             __syncwarp();
+            if (S::ROWS_WIDEN) {  // the rows wait for it
+                ++item;
+                continue;
+            }
             if (S::WIDEN) {
                 if (!tiles_wait(ctl, bar, (item / S::Q_PLACES) & 1, err)) break;
             } else if (lt != 0) {
@@ -732,7 +752,12 @@ __device__ void tiles_prepare(const TilesParams &p, char *smem, TilesCtl<S> *ctl
             }
             asm volatile("cp.async.wait_all;" ::: "memory");
         }
-        if constexpr (S::WIDEN) {
+        if constexpr (S::ROWS_WIDEN) {
+            mbar_arrive(&ctl->q_raw[place]);
+            ++item;
+            continue;
+        }
+        if constexpr (S::WIDEN && !S::ROWS_WIDEN) {
 #pragma unroll 2
             for (int r = first; r < S::ROWS; r += STEP) {  // every thread the same number of times
                 char *at = to + (r >> 7) * S::Q_SUB;
@@ -771,6 +796,35 @@ __device__ void tiles_prepare(const TilesParams &p, char *smem, TilesCtl<S> *ctl
 }
 
 // ------------------------------------------------------------------ rows
+// Multiplies row r of q, where it lies, into f16's range by a power of two, and returns that power's inverse.
+template <typename T, int D> __device__ __forceinline__ float widen_row(char *rows, int r)
+{
+    constexpr uint32_t INF = std::is_same<T, __half>::value ? 0x7c007c00u : 0x7f807f80u;
+    uint32_t top = 0;  // of two columns of elements, as bits: finite ones are ordered as their bits
+#pragma unroll 4
+    for (int c = 0; c < D / 8; ++c) {
+        const uint4 x = *reinterpret_cast<const uint4 *>(rows + tile_at<128>(r, c));
+        const uint32_t w[4] = {x.x & 0x7fff7fffu, x.y & 0x7fff7fffu, x.z & 0x7fff7fffu, x.w & 0x7fff7fffu};
+#pragma unroll
+        for (int i = 0; i < 4; ++i) top = __vmaxu2(top, w[i] & __vcmpltu2(w[i], INF));
+    }
+    const uint16_t most = static_cast<uint16_t>(max(top & 0xffffu, top >> 16));
+    const float largest = Num<T>::up(*reinterpret_cast<const T *>(&most));
+    // the largest below 2^15 (the exponent of a number that is not normal counts as the smallest's)
+    const int e2 = largest > 0.0f ? max(-120, min(120, 14 - (static_cast<int>(__float_as_uint(largest) >> 23) - 127))) : 0;
+    const float up = __uint_as_float(static_cast<uint32_t>(e2 + 127) << 23);
+#pragma unroll 2
+    for (int c = 0; c < D / 8; ++c) {
+        uint4 *at = reinterpret_cast<uint4 *>(rows + tile_at<128>(r, c));
+        const uint4 x = *at;
+        const T *y = reinterpret_cast<const T *>(&x);
+        uint32_t w[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) w[i] = pack_mma<__half>(Num<T>::up(y[2 * i]) * up, Num<T>::up(y[2 * i + 1]) * up);
+        *at = make_uint4(w[0], w[1], w[2], w[3]);
+    }
+    return __uint_as_float(static_cast<uint32_t>(127 - e2) << 23);
+}
 // All threads that have rows of the same tile of rows.
 template <int N> __device__ __forceinline__ void group_sync(int group) { asm volatile("bar.sync %0, %1;" ::"r"(1 + group), "n"(N) : "memory"); }
 // The two warps that share rows.
@@ -1068,8 +1122,18 @@ __device__ void tiles_rows(const TilesParams &p, char *smem, TilesCtl<S> *ctl, u
             const int origin = moved ? __ldg(pos + it.ctx) : 0;  // the first new token's position
             const float slope = there && v.slopes ? __ldg(v.slopes + it.h * p.group + (row0 + r) - token * p.group) * LOG2E : 0.0f;
             float factor = p.scale_log2 * (p.c.k_scale ? __ldg(p.c.k_scale + it.h) : 1.0f);
-            ok = tiles_wait(ctl, &ctl->q_full[place], (item / S::Q_PLACES) & 1, err);
-            if (S::WIDEN) factor *= exp2f(-static_cast<float>(ctl->at.q_power[place * S::ROWS + r]));
+            if constexpr (S::ROWS_WIDEN) {
+                ok = tiles_wait(ctl, &ctl->q_raw[place], (item / S::Q_PLACES) & 1, err);
+                if (ok) {
+                    char *row = smem + place * S::Q + group * S::Q_SUB;
+                    factor *= p.q_bf16 ? widen_row<__nv_bfloat16, D>(row, lane_row) : widen_row<__half, D>(row, lane_row);
+                }
+                fence_async_shared();
+                mbar_arrive(&ctl->q_full[place]);
+            } else {
+                ok = tiles_wait(ctl, &ctl->q_full[place], (item / S::Q_PLACES) & 1, err);
+                if (S::WIDEN) factor *= exp2f(-static_cast<float>(ctl->at.q_power[place * S::ROWS + r]));
+            }
             if (OF_ROW == 1) {
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&ctl->q_empty[place]);
@@ -1377,13 +1441,13 @@ __global__ void __launch_bounds__(TILES_THREADS, 1)
         for (int i = 0; i < 2; ++i) {
             mbar_init(&ctl->item_full[i], 1);
             mbar_init(&ctl->item_empty[i], TILES_TAKERS);
-            mbar_init(&ctl->q_full[i], TILES_PREPARE);
+            mbar_init(&ctl->q_full[i], S::ROWS_WIDEN ? 256 : TILES_PREPARE);
             mbar_init(&ctl->q_empty[i], 1 + 8);  // the products' end, and the row warps, who have read what lies beside q
             ctl->stop[i] = ctl->lost[i] = 0;
             for (int k = 0; k < S::ITEMS; ++k) ctl->bad[i][k] = 0;
         }
         mbar_init(&ctl->spare, 1);
-        for (int i = 0; i < S::Q_PLACES; ++i) mbar_init(&ctl->q_raw[i], 1);
+        for (int i = 0; i < S::Q_PLACES; ++i) mbar_init(&ctl->q_raw[i], S::ROWS_WIDEN && !q_map ? TILES_PREPARE : 1);
         if (S::WIDEN)
             for (int i = 0; i < 4; ++i)
                 for (int k = 0; k < S::RAW_STAGES; ++k) mbar_init(&ctl->raw_full[S::WIDEN ? i : 0][k], 1);

@@ -189,3 +189,20 @@ def test_two_streams_with_their_own_workspaces(spv):
     got = [c.attend(prompt=True, stream=s)["out"] for s in streams]
     torch.cuda.synchronize()
     assert all(torch.equal(g, want) for g in got)
+
+
+@pytest.mark.parametrize("kv", ["bf16", "e4m3"])
+@pytest.mark.parametrize("D,T,B", [(64, 70, 90), (128, 66, 70), (256, 34, 40)])
+def test_blocks_of_many_items_of_a_tile_or_two(spv, D, T, B, kv):
+    """A block's copies run ahead of its rows by several whole items."""
+    c = sr.Case(spv, 71, [(3 * b) % 7 for b in range(B)], None, T, 8 if D == 256 else 16, 4, D, 16, "nhd", "bf16", kv)
+    c.check(c.attend(prompt=True))
+
+
+@pytest.mark.parametrize("kv", ["bf16", "e4m3"])
+@pytest.mark.parametrize("D", [64, 128, 256])
+def test_blocks_of_many_items_without_tiles(spv, D, kv):
+    """Most rows are padding: items that see nothing lie between those that do, and behind them."""
+    new = [(0, 1, 300, 0, 2, 70)[b % 6] for b in range(30)]
+    c = sr.Case(spv, 72, [(11 * b) % 90 for b in range(30)], new, 300, 8, 2, D, 16, "nhd", "bf16", kv)
+    c.check(c.attend(prompt=True))

@@ -363,3 +363,12 @@ def test_mass_skips_what_no_token_sees(spv):
     assert got["row_status"].item() == 0
     assert (m[48:64] == -3.0).all() and (m[:48] == 1.0).all() and (m[64:340] == 1.0).all()
     assert (m[360:402] != 1.0).any() and (m[402:] == -3.0).all()
+
+
+@pytest.mark.parametrize("kv", ["bf16", "e4m3"])
+@pytest.mark.parametrize("D", [64, 128, 256])
+def test_many_idle_sequences_in_tiles(spv, D, kv):
+    """Sequences without new tokens, and short ones, between those of a batch whose rows go in tiles."""
+    new = [(0, 9, 0, 1, 0, 0, 5, 0)[b % 8] for b in range(160)]
+    c = sr.Case(spv, 73, [(13 * b) % 200 for b in range(160)], new, 9, 16, 2, D, 16, "nhd", "bf16", kv, cap=30.0)
+    c.check(c.attend())
