@@ -121,3 +121,57 @@ def test_a_prompt_in_pieces_decodes_the_same_keys(loop):
         # the projection's products may be summed in another order: two roundings apart before the norm, one after
         assert ((a - b).abs() <= 3 * 2.0 ** -8 * a.abs() + 2.0 ** -7 * a.square().mean(-1, keepdim=True).sqrt()).all()
         assert torch.equal(whole.pos[0][0, :, slot], pieces.pos[0][0, :, slot])
+
+
+def test_a_step_captured_and_replayed(loop):
+    """Append, attention and weights of a step in one graph: replayed after the lengths and the inputs have changed, it gives
+    what the calls give."""
+    spv, m = loop.spv, loop.ToyModel(layers=1, shaped=True)
+    gen = torch.Generator(device="cuda").manual_seed(9)
+    B, T, Hq, Hkv, D, pages = 3, 5, m.heads, m.kv_heads, m.head_dim, 20
+    pools = [torch.randn(B * pages, 16, Hkv, D, generator=gen, device="cuda").bfloat16() for _ in range(2)]
+    table = torch.arange(B * pages, dtype=torch.int32, device="cuda").reshape(B, pages)
+    qkv = torch.empty(B, T, Hq + 2 * Hkv, D, dtype=torch.bfloat16, device="cuda")
+    ctx, accept = (torch.zeros(B, dtype=torch.int32, device="cuda") for _ in range(2))
+    pos = torch.arange(pages * 16, dtype=torch.int32, device="cuda").expand(B, Hkv, -1).contiguous()
+    mass = torch.zeros(B, Hkv, pages * 16, device="cuda")
+    workspace = spv.new_workspace(spv.spv_attention_workspace_bytes(B, T, Hq, Hkv, D), "cuda")
+    outs = [dict(q=torch.empty(B, T, Hq, D, dtype=torch.bfloat16, device="cuda")),
+            dict(out=torch.empty(B, T, Hq, D, dtype=torch.bfloat16, device="cuda"), lse=torch.empty(B, T, Hq, device="cuda")),
+            dict(mass=mass)]
+
+    def step():
+        cache = spv.KVCache(*pools)
+        q, k, v = qkv.split([Hq, Hkv, Hkv], dim=2)
+        q = spv.spv_norm_rope_append(q, k, v, cache, table, ctx, m.freqs, q_weight=m.norms[0][0], k_weight=m.norms[0][1], slot_pos=pos,
+                                     out=outs[0], want_status=False)["q"]
+        scores = m.scores(1, pos)
+        got = spv.spv_paged_attention_scored(q, cache, table, ctx, scores, workspace=workspace, out=outs[1], want_lse=True,
+                                             want_status=False)
+        spv.spv_attention_mass_scored(q, got["lse"], cache, table, ctx, accept, scores, mass_in=mass, out=outs[2], want_status=False)
+
+    def state():
+        return [x.clone() for x in (*pools, pos, mass)]
+
+    def restore(saved):
+        for x, y in zip((*pools, pos, mass), saved):
+            x.copy_(y)
+
+    qkv.normal_(generator=gen)
+    step()  # as a user would before a capture
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        step()
+    for lens, counts in (([0, 17, 200], [0, 4, 2]), ([90, 300, 5], [4, 4, 0]), ([315, 64, 16], [1, 0, 3])):
+        qkv.normal_(generator=gen)
+        ctx.copy_(torch.tensor(lens, dtype=torch.int32))
+        accept.copy_(torch.tensor(counts, dtype=torch.int32))
+        before = state()
+        step()
+        want = [x.clone() for x in (*state(), outs[0]["q"], outs[1]["out"], outs[1]["lse"])]
+        restore(before)
+        for x in (outs[0]["q"], outs[1]["out"], outs[1]["lse"]):
+            x.zero_()
+        graph.replay()
+        for a, b in zip((*state(), outs[0]["q"], outs[1]["out"], outs[1]["lse"]), want):
+            assert torch.equal(a, b)
