@@ -1081,15 +1081,15 @@ __device__ void tiles_rows(const TilesParams &p, char *smem, TilesCtl<S> *ctl, u
     TileItem it;
     int k = 0;
     bool ok = true;
-    // The next item, for the whole group: a warp that a wait has given up stops all.
-    auto take = [&]() {
-        const bool some = take_item(ctl, k, &it, err, lane);
-        if (!some && !(it.flags & ITEM_END) && lane == 0) *reinterpret_cast<volatile int *>(&ctl->stop[group]) = 1;
-        group_sync<GROUP>(group);  // and all have read the last item's sums and flags
-        return some && !*reinterpret_cast<volatile int *>(&ctl->stop[group]);
-    };
     it.flags = 0;
-    for (; take(); ++k) {
+    for (;; ++k) {
+        // The next item, for the whole group: a warp that a wait has given up stops all.
+        const bool some = take_item(ctl, k, &it, err, lane);
+        if (!some) {
+            if (!(it.flags & ITEM_END) && lane == 0) *reinterpret_cast<volatile int *>(&ctl->stop[group]) = 1;
+            group_sync<GROUP>(group);
+            break;
+        }
         const int t0 = it.t0, t1 = it.t1, row0 = it.row_tile * S::ROWS, live = min(S::ROWS, p.rows - row0);
         const int s0 = PAIR ? max(t0, group ? it.lo1 : it.lo0) : t0, s1 = max(s0, PAIR ? min(t1, group ? it.hi1 : it.hi0) : t1);
         const float v_scale = p.c.v_scale ? __ldg(p.c.v_scale + it.h) : 1.0f;
@@ -1099,29 +1099,32 @@ __device__ void tiles_rows(const TilesParams &p, char *smem, TilesCtl<S> *ctl, u
         float m = -CUDART_INF_F, l = 0.0f;  // a maximum so far less UP: what l and O are sums against
         bool any_bad = it.flags & ITEM_BAD;
         const int place = item % S::Q_PLACES;
+        // What the row sees, asked for before the others are waited for: the last warp then finds it in the L1.
+        const bool there = mine && token < it.fresh && t0 < t1;
+        const SeqLens lens{it.ctx, it.fresh, it.total, false};
+        Interval see{0, 0};
+        unsigned long long bits = 0;
+        int own = 0;
+        const int32_t *pos = v.slot_pos ? v.slot_pos + (static_cast<int64_t>(it.b) * p.c.kv_heads + it.h) * v.pos_stride : nullptr;
+        if (there && !p.parent) {
+            see = token_interval(p, lens, it.b, token);
+            own = moved ? __ldg(pos + it.ctx + token) : it.ctx + token;
+        }
+        if constexpr (!PAIR) {
+            if (there && p.parent) {
+                const TokenView view = token_view(v, p.parent + static_cast<int64_t>(it.b) * p.w.T, lens, it.b, p.w.T, token);
+                bits = view.bits;
+                own = moved ? __ldg(pos + it.ctx + token) : it.ctx + view.depth;
+                see.hi = bits ? it.ctx : 0;
+                see.lo = view.lo;
+            }
+        }
+        const int origin = moved && t0 < t1 ? __ldg(pos + it.ctx) : 0;  // the first new token's position
+        const float slope = there && v.slopes ? __ldg(v.slopes + it.h * p.group + (row0 + r) - token * p.group) * LOG2E : 0.0f;
+        float factor = p.scale_log2 * (p.c.k_scale ? __ldg(p.c.k_scale + it.h) : 1.0f);
+        group_sync<GROUP>(group);  // all have read the last item's sums and flags
+        if (*reinterpret_cast<volatile int *>(&ctl->stop[group])) break;
         if (t0 < t1) {
-            const bool there = mine && token < it.fresh;
-            const SeqLens lens{it.ctx, it.fresh, it.total, false};
-            Interval see{0, 0};
-            unsigned long long bits = 0;
-            int own = 0;
-            const int32_t *pos = v.slot_pos ? v.slot_pos + (static_cast<int64_t>(it.b) * p.c.kv_heads + it.h) * v.pos_stride : nullptr;
-            if (there && !p.parent) {
-                see = token_interval(p, lens, it.b, token);
-                own = moved ? __ldg(pos + it.ctx + token) : it.ctx + token;
-            }
-            if constexpr (!PAIR) {
-                if (there && p.parent) {
-                    const TokenView view = token_view(v, p.parent + static_cast<int64_t>(it.b) * p.w.T, lens, it.b, p.w.T, token);
-                    bits = view.bits;
-                    own = moved ? __ldg(pos + it.ctx + token) : it.ctx + view.depth;
-                    see.hi = bits ? it.ctx : 0;
-                    see.lo = view.lo;
-                }
-            }
-            const int origin = moved ? __ldg(pos + it.ctx) : 0;  // the first new token's position
-            const float slope = there && v.slopes ? __ldg(v.slopes + it.h * p.group + (row0 + r) - token * p.group) * LOG2E : 0.0f;
-            float factor = p.scale_log2 * (p.c.k_scale ? __ldg(p.c.k_scale + it.h) : 1.0f);
             if constexpr (S::ROWS_WIDEN) {
                 ok = tiles_wait(ctl, &ctl->q_raw[place], (item / S::Q_PLACES) & 1, err);
                 if (ok) {
