@@ -34,10 +34,11 @@
 // PFLOP/s of the 1.9 that the products alone could have: for a tile of 64 keys a
 // thread's scores take 1,500 cycles (loads 240, maximum 400, exponentials and
 // weights 450, waits for products 470).  Capped scores, bound by the polynomials:
-// 906 us.  Distance biases 616, documents of some 1,000 tokens 199, a window of
-// 1,024 192, heads of 64 498, 16 heads of 256 574 us.  e4m3 769 us (heads of 64 639): widening K
-// and V, four warps.  An item's beginning and end take some 14,000 cycles (its rows'
-// intervals and q 5,500, the outputs 4,600, agreeing on the end 2,000).
+// 872 us.  Distance biases 600, documents of some 1,000 tokens 197, a window of
+// 1,024 187, heads of 64 470, 16 heads of 256 558 us.  e4m3 766 us (heads of 64
+// 633): widening K and V, four warps.  An item's beginning and end take some
+// 12,000 cycles: the outputs 4,600, agreeing on the end 2,000, the next rows'
+// intervals and q.
 //
 // O is only rescaled when a maximum has grown by more than 2^8 (2^7 for f16).
 // The blocks' pieces of an item that they share are joined by a dependent
