@@ -589,12 +589,13 @@ typedef struct {
  * spv_paged_attention_scored -- spv_paged_attention with the scores and masks
  * of `scores` (HOST struct of device pointers).  All else as there, the
  * workspace (spv_attention_workspace_bytes) too, but for this:
- * Pages that lie wholly before the first slot that a sequence's tokens can see
- * (first, window without slot_pos) are not read and may be gone.  A page id
- * outside the pool among the others makes row_status[b] SPV_ERR_BAD_ROW and
- * the rows that see one of its slots NaN; other rows of that sequence may be
- * NaN too.  Bad sequences also: ctx + new > pos_stride.  With row_status a
- * small kernel of its own goes before the others.
+* Pages that lie wholly before the first slot that a sequence's tokens can see
+ * -- the larger of ctx_lens[b] - window + 1 (a window without slot_pos) and the
+ * least `first` of its new tokens, its last slot at most -- do not matter and
+ * may be gone.  A page id outside the pool among the others makes
+ * row_status[b] SPV_ERR_BAD_ROW and the rows that see one of its slots NaN;
+ * other rows of that sequence may be NaN too.  Bad sequences also: ctx + new >
+ * pos_stride.  With row_status a small kernel of its own goes before the others.
  */
 spv_status spv_paged_attention_scored(const void *q, spv_dtype dtype, int B, int T, int q_heads,
                                       const spv_kv_cache *cache, const int32_t *page_table, int max_pages,

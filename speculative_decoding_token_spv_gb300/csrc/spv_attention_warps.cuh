@@ -100,14 +100,14 @@ __global__ void __launch_bounds__(ATT_THREADS, AttShape<C, D, MT>::BLOCKS_PER_SM
         const int skip = skipped_tiles(work, c.s);  // tiles are counted from the first that is seen
 
         // the first slices, as early as the page table allows
-        SliceSource src = find_slice(p.c, table, (t0 + skip) * ATT_KEYS + warp * 16, t0 < t1 ? c.s.total : 0, lane, &bad);
+        SliceSource src = find_slice(p.c, table, (t0 + skip) * ATT_KEYS + warp * 16, t0 < t1 ? c.s.total : 0, first_seen(c.s), lane, &bad);
         auto issue = [&](int tile) {
             if (tile < t1) {
                 const int j0 = (tile + skip) * ATT_KEYS + warp * 16;
                 const uint32_t dst = ring + ((tile - t0) % NST) * (2 * S::SLICE);
                 copy_slice<S::ROW_BYTES>(p.c, p.c.k, src, j0, c.h, dst, lane);
                 copy_slice<S::ROW_BYTES>(p.c, p.c.v, src, j0, c.h, dst + S::SLICE, lane);
-                src = find_slice(p.c, table, j0 + ATT_KEYS, tile + 1 < t1 ? c.s.total : 0, lane, &bad);
+                src = find_slice(p.c, table, j0 + ATT_KEYS, tile + 1 < t1 ? c.s.total : 0, first_seen(c.s), lane, &bad);
             }
             cp_async_commit();
         };

@@ -97,6 +97,8 @@ __device__ __forceinline__ SeqLens lens_of(const Work &w, int b, const PagedView
 }
 // Tiles at a sequence's beginning that its new tokens do not see at all.
 __device__ __forceinline__ int skipped_tiles(const Work &, const SeqLens &) { return 0; }
+// The first slot that any of them sees; pages that end before it may be missing.
+__device__ __forceinline__ int first_seen(const SeqLens &) { return 0; }
 
 // A block's range [at, end) and the item that it is in: `first` is the number
 // of the item's first tile, `tiles` how many it has.

@@ -86,13 +86,14 @@ __device__ __forceinline__ void cp_async16_zfill(uint32_t dst, const void *src, 
 
 // Sixteen keys of one head on their way to shared memory: where they are.
 // Pages of at least 16 slots hold a slice whole (slices start at multiples of
-// 16); smaller ones are looked up row by row.
+// 16); smaller ones are looked up row by row.  Pages that end before slot `from`
+// may be missing: nobody sees them.
 struct SliceSource {
     int page;  // of the whole slice, or of row `lane` (lane < 16); -1: none, or bad
     int keys;  // rows that exist
 };
-__device__ __forceinline__ SliceSource find_slice(const PagedView &c, const int32_t *table, int j0, int total, int lane,
-                                                  bool *bad)
+__device__ __forceinline__ SliceSource find_slice(const PagedView &c, const int32_t *table, int j0, int total, int from,
+                                                  int lane, bool *bad)
 {
     SliceSource s;
     s.keys = min(16, total - j0);
@@ -100,10 +101,10 @@ __device__ __forceinline__ SliceSource find_slice(const PagedView &c, const int3
     if (s.keys <= 0) return s;
     if (c.page_shift >= 4) {
         s.page = page_of(c, table, j0);
-        *bad |= s.page < 0;
+        *bad |= s.page < 0 && j0 >> c.page_shift >= from >> c.page_shift;
     } else if (lane < s.keys) {
         s.page = page_of(c, table, j0 + lane);
-        *bad |= s.page < 0;
+        *bad |= s.page < 0 && (j0 + lane) >> c.page_shift >= from >> c.page_shift;
     }
     return s;
 }

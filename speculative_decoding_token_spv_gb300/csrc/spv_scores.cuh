@@ -168,6 +168,7 @@ __device__ __forceinline__ SpanLens lens_of(const ScoredWork &w, int b, const Pa
     return s;
 }
 __device__ __forceinline__ int skipped_tiles(const ScoredWork &w, const SpanLens &s) { return s.from / w.tile; }
+__device__ __forceinline__ int first_seen(const SpanLens &s) { return s.from; }
 
 // What new token t of sequence b sees, t < 64: of the new tokens those in the
 // bits, of the cached slots those from `lo` on (of a token without bits none).

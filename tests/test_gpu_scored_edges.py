@@ -1,0 +1,57 @@
+"""GPU tests of the calls with scores where they went wrong or nearly: pages that
+were given back, pages outside the pool beside other items, masks near the ends
+of 32 bits, rows of q next to nothing, trees of many short sequences."""
+import pytest
+import torch
+
+import scored_reference as sr
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module")
+def spv():
+    if not torch.cuda.is_available():
+        pytest.skip("no CUDA device")
+    import __graft_entry__
+    __graft_entry__.build()
+    import speculative_decoding_token_spv_gb300 as m
+    return m
+
+
+# ------------------------------------------------------------------ pages that were given back
+def without_passed_pages(c, page):
+    """The page table with every page that ends before the first slot that its sequence's tokens can see outside the pool."""
+    table = c.table.clone()
+    for b in range(c.B):
+        if c.new[b] == 0:
+            continue
+        lowest = c.ctx[b] - c.window + 1 if c.window else 0
+        if c.first is not None:
+            lowest = max(lowest, int(c.first[b, : c.new[b]].min()))
+        gone = max(0, min(lowest, c.ctx[b] + c.new[b] - 1)) // page
+        table[b, :gone] = torch.tensor([-1, c.k.shape[0] + 5])[torch.arange(gone) % 2].to(torch.int32)
+    return table
+
+
+def check_without_passed_pages(c, page, prompt=False):
+    table, whole = without_passed_pages(c, page), c.table
+    assert (table != whole).any()
+    c.table = table
+    got = c.attend(prompt=prompt)
+    c.table = whole
+    c.check(got)
+
+
+GONE = [((300, 5, 131, 448, 64), None, 64), ((1000, 777, 12), None, 100), ((700, 333), [[650, 651], [201, 333]], 0),
+        ((700, 333), [[600, 702], [50, 0]], 77)]
+
+
+@pytest.mark.parametrize("page", [1, 8, 16, 32])
+@pytest.mark.parametrize("D,kv", [(64, "bf16"), (128, "f16"), (128, "e4m3"), (256, "bf16"), (256, "e4m3")])
+@pytest.mark.parametrize("ctx,first,window", GONE, ids=["64", "100", "first", "both"])
+def test_pages_before_the_first_slot_that_is_seen_few_rows(spv, ctx, first, window, D, kv, page):
+    check_without_passed_pages(sr.Case(spv, 51, ctx, None, 2, 4, 2, D, page, "nhd", "f16" if kv == "f16" else "bf16", kv, first=first,
+                                       window=window, cap=30.0), page)
+
+
