@@ -589,7 +589,7 @@ typedef struct {
  * spv_paged_attention_scored -- spv_paged_attention with the scores and masks
  * of `scores` (HOST struct of device pointers).  All else as there, the
  * workspace (spv_attention_workspace_bytes) too, but for this:
-* Pages that lie wholly before the first slot that a sequence's tokens can see
+ * Pages that lie wholly before the first slot that a sequence's tokens can see
  * -- the larger of ctx_lens[b] - window + 1 (a window without slot_pos) and the
  * least `first` of its new tokens, its last slot at most -- do not matter and
  * may be gone.  A page id outside the pool among the others makes

@@ -90,9 +90,10 @@ template <typename C, int D, int COPIES> struct TilesShape {
     static constexpr int GROUP = PAIR ? 128 : 256;               // threads that belong to the same rows
 };
 
-// An item's tiles of keys: [from, to), and of each tile of rows.
+// An item's tiles of keys: [from, to), and of each tile of rows; `seen`: the
+// first slot that any of its rows sees.
 struct TileLens : SeqLens {
-    int from, to, lo[2], hi[2];
+    int from, to, lo[2], hi[2], seen;
 };
 using TileCursor = CursorOf<TileLens>;
 
@@ -101,7 +102,7 @@ struct alignas(16) TileItem {
     int b, row_tile, h, flags;
     int ctx, fresh, total, t0;
     int t1, lo0, hi0, lo1;
-    int hi1, pad[3];
+    int hi1, seen, pad[2];
 };
 enum TileFlags { ITEM_BAD = 1, ITEM_WHOLE = 2, ITEM_SECOND = 4, ITEM_END = 8 };  // ITEM_SECOND: a piece goes to the block's second place
 
@@ -180,7 +181,7 @@ template <typename S> __device__ __forceinline__ TileLens item_tiles(const Tiles
 {
     TileLens r;
     static_cast<SeqLens &>(r) = s;
-    r.from = 0x7fffffff;
+    r.from = r.seen = 0x7fffffff;
     r.to = 0;
     const bool sliding = p.sc.window > 0 && !p.sc.slot_pos;
 #pragma unroll
@@ -217,6 +218,7 @@ template <typename S> __device__ __forceinline__ TileLens item_tiles(const Tiles
         r.lo[k] = lo / S::KEYS;
         r.hi[k] = (hi + S::KEYS - 1) / S::KEYS;
         r.from = min(r.from, r.lo[k]);
+        r.seen = min(r.seen, lo);
         r.to = max(r.to, r.hi[k]);
     }
     if (r.to == 0) r.from = 0;
@@ -381,6 +383,7 @@ template <typename S> __device__ void tiles_items(const TilesParams &p, TileCurs
             it.ctx = c.s.ctx, it.fresh = c.s.fresh, it.total = c.s.total;
             it.t0 = tiles_first(c), it.t1 = tiles_last(c);
             it.lo0 = c.s.lo[0], it.hi0 = c.s.hi[0], it.lo1 = c.s.lo[1], it.hi1 = c.s.hi[1];
+            it.seen = c.s.seen;
             mbar_arrive(&ctl->item_full[k & 1]);
             if (!end && !item_whole(c))
                 note_split(p, c, AttRows{c.b, c.h, c.row_tile * S::ROWS, min(S::ROWS, p.rows - c.row_tile * S::ROWS)}, begin, 0);
@@ -411,6 +414,7 @@ template <typename Ctl> __device__ __forceinline__ bool take_item(Ctl *ctl, int 
     it->ctx = same_in_warp(y.x), it->fresh = same_in_warp(y.y), it->total = same_in_warp(y.z), it->t0 = same_in_warp(y.w);
     it->t1 = same_in_warp(z.x), it->lo0 = same_in_warp(z.y), it->hi0 = same_in_warp(z.z), it->lo1 = same_in_warp(z.w);
     it->hi1 = same_in_warp(from[3].x);
+    it->seen = from[3].y;
     __syncwarp();
     if (lane == 0) mbar_arrive(&ctl->item_empty[k & 1]);
     return !(it->flags & ITEM_END);
@@ -431,9 +435,6 @@ __device__ void tiles_load(const TilesParams &p, char *smem, TilesCtl<S> *ctl, u
     int raw = 0, waiting = 0;          // e4m3: the place of the next raw tile; raw tiles not widened yet
     int rows[RST];          // e4m3: slots of this warp that exist, of the raw tiles in turn
     bool ok = true;
-    auto flag = [&](int flags) {
-        *reinterpret_cast<volatile char *>(&ctl->bad[0][flags]) = *reinterpret_cast<volatile char *>(&ctl->bad[1][flags]) = 1;
-    };
     auto free_place = [&]() { return tiles_wait(ctl, &ctl->empty[st], pass, err); };
     auto step = [&]() {
         if (++st == NST) st = 0, pass ^= 1;
@@ -491,8 +492,12 @@ __device__ void tiles_load(const TilesParams &p, char *smem, TilesCtl<S> *ctl, u
         const int t0 = it.t0, t1 = it.t1;
         if (t0 == t1) continue;
         const int32_t *table = p.c.table + static_cast<int64_t>(it.b) * p.c.max_pages;
-        const int flags = item;
+        const int flags = item, needed = it.seen >> p.c.page_shift;
         if (++item == S::ITEMS) item = 0;
+        auto flag = [&](int slot) {  // the page of this slot is outside the pool: that matters from the first that is seen on
+            if (slot >> p.c.page_shift < needed) return;
+            *reinterpret_cast<volatile char *>(&ctl->bad[0][flags]) = *reinterpret_cast<volatile char *>(&ctl->bad[1][flags]) = 1;
+        };
         // With maps each warp asks the copy engine for its slots: a box a page (or what the warp has of a larger one), of 64
         // elements, or e4m3's whole rows; a lane each.  (A lane's takes 80 to 100 cycles: from one warp, 16 of a tile of K
         // and 16 of V took longer than the tile's products.)
@@ -517,7 +522,7 @@ __device__ void tiles_load(const TilesParams &p, char *smem, TilesCtl<S> *ctl, u
                 if (S::WIDEN && waiting == RST && !(ok = widen())) break;
                 if (map_k && (S::WIDEN || !kv || j0 + KEYS <= it.total)) {
                     const int slot = j0 + box_slot;
-                    if (asks && slot < it.total && static_cast<unsigned>(page) >= static_cast<unsigned>(p.c.num_pages)) flag(flags);
+                    if (asks && slot < it.total && static_cast<unsigned>(page) >= static_cast<unsigned>(p.c.num_pages)) flag(slot);
                     uint64_t *bar;
                     uint32_t to;
                     if constexpr (S::WIDEN) {
@@ -541,7 +546,7 @@ __device__ void tiles_load(const TilesParams &p, char *smem, TilesCtl<S> *ctl, u
                         pg = lane < WARP_ROWS && j < it.total ? __ldg(table + (j >> p.c.page_shift)) : -1;
                     }
                     if (static_cast<unsigned>(pg) >= static_cast<unsigned>(p.c.num_pages)) {
-                        if (lane < WARP_ROWS && j0 + WARP_ROWS * w + lane < it.total) flag(flags);
+                        if (lane < WARP_ROWS && j0 + WARP_ROWS * w + lane < it.total) flag(j0 + WARP_ROWS * w + lane);
                         pg = -1;
                     }
                     const int64_t mine = pg < 0 ? -1 : pg * pool.page_stride + ((j0 + WARP_ROWS * w + lane) & mask) * pool.slot_stride;

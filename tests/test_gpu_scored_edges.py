@@ -55,3 +55,24 @@ def test_pages_before_the_first_slot_that_is_seen_few_rows(spv, ctx, first, wind
                                        window=window, cap=30.0), page)
 
 
+@pytest.mark.parametrize("page", [1, 8, 16, 128])
+@pytest.mark.parametrize("Hq,D,kv", [(2, 64, "bf16"), (4, 128, "f16"), (8, 128, "bf16"), (8, 128, "e4m3"), (4, 256, "bf16"), (4, 256, "e4m3")])
+@pytest.mark.parametrize("first", [False, True])
+def test_pages_before_the_first_slot_that_is_seen_many_rows(spv, first, Hq, D, kv, page):
+    """20, 40 and 80 rows a key head: a row stands in tensor memory four times, twice, once."""
+    ctx, T = (300, 5, 131, 1000, 517), 20 if D < 256 else 40
+    begins = [[max(0, n - 40 + t) for t in range(T)] for n in ctx] if first else None
+    check_without_passed_pages(sr.Case(spv, 52, ctx, None, T, Hq, 2, D, page, "nhd", "f16" if kv == "f16" else "bf16", kv,
+                                       first=begins, window=0 if first else 64, slopes=True), page)
+
+
+@pytest.mark.parametrize("page", [4, 16, 64])
+@pytest.mark.parametrize("T,D,kv", [(1, 128, "bf16"), (70, 64, "f16"), (100, 128, "bf16"), (200, 128, "e4m3"), (70, 256, "bf16")])
+@pytest.mark.parametrize("first", [False, True])
+def test_pages_before_the_first_slot_that_is_seen_prompts(spv, first, T, D, kv, page):
+    ctx = (300, 45, 1000, 517)
+    begins = [[max(0, n - 31 + t // 2) for t in range(T)] for n in ctx] if first else None
+    check_without_passed_pages(sr.Case(spv, 53, ctx, [T, 1, T - T // 3, T], T, 6, 2, D, page, "nhd", "f16" if kv == "f16" else "bf16", kv,
+                                       first=begins, window=0 if first else 40), page, prompt=True)
+
+
