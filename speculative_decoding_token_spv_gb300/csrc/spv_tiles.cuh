@@ -494,9 +494,12 @@ __device__ void tiles_load(const TilesParams &p, char *smem, TilesCtl<S> *ctl, u
         const int32_t *table = p.c.table + static_cast<int64_t>(it.b) * p.c.max_pages;
         const int flags = item, needed = it.seen >> p.c.page_shift;
         if (++item == S::ITEMS) item = 0;
-        auto flag = [&](int slot) {  // the page of this slot is outside the pool: that matters from the first that is seen on
+        // The page of this slot, in this tile, is outside the pool: that matters from the first slot that is seen on, and to the
+        // groups of row warps that see the tile.  (One that does not may be done with the item, and its flag another item's.)
+        auto flag = [&](int slot, int tile) {
             if (slot >> p.c.page_shift < needed) return;
-            *reinterpret_cast<volatile char *>(&ctl->bad[0][flags]) = *reinterpret_cast<volatile char *>(&ctl->bad[1][flags]) = 1;
+            if (!S::PAIR || (tile >= it.lo0 && tile < it.hi0)) *reinterpret_cast<volatile char *>(&ctl->bad[0][flags]) = 1;
+            if (S::PAIR && tile >= it.lo1 && tile < it.hi1) *reinterpret_cast<volatile char *>(&ctl->bad[1][flags]) = 1;
         };
         // With maps each warp asks the copy engine for its slots: a box a page (or what the warp has of a larger one), of 64
         // elements, or e4m3's whole rows; a lane each.  (A lane's takes 80 to 100 cycles: from one warp, 16 of a tile of K
@@ -522,7 +525,7 @@ __device__ void tiles_load(const TilesParams &p, char *smem, TilesCtl<S> *ctl, u
                 if (S::WIDEN && waiting == RST && !(ok = widen())) break;
                 if (map_k && (S::WIDEN || !kv || j0 + KEYS <= it.total)) {
                     const int slot = j0 + box_slot;
-                    if (asks && slot < it.total && static_cast<unsigned>(page) >= static_cast<unsigned>(p.c.num_pages)) flag(slot);
+                    if (asks && slot < it.total && static_cast<unsigned>(page) >= static_cast<unsigned>(p.c.num_pages)) flag(slot, tile);
                     uint64_t *bar;
                     uint32_t to;
                     if constexpr (S::WIDEN) {
@@ -546,7 +549,7 @@ __device__ void tiles_load(const TilesParams &p, char *smem, TilesCtl<S> *ctl, u
                         pg = lane < WARP_ROWS && j < it.total ? __ldg(table + (j >> p.c.page_shift)) : -1;
                     }
                     if (static_cast<unsigned>(pg) >= static_cast<unsigned>(p.c.num_pages)) {
-                        if (lane < WARP_ROWS && j0 + WARP_ROWS * w + lane < it.total) flag(j0 + WARP_ROWS * w + lane);
+                        if (lane < WARP_ROWS && j0 + WARP_ROWS * w + lane < it.total) flag(j0 + WARP_ROWS * w + lane, tile);
                         pg = -1;
                     }
                     const int64_t mine = pg < 0 ? -1 : pg * pool.page_stride + ((j0 + WARP_ROWS * w + lane) & mask) * pool.slot_stride;

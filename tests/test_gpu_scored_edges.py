@@ -76,3 +76,28 @@ def test_pages_before_the_first_slot_that_is_seen_prompts(spv, first, T, D, kv, 
                                        first=begins, window=0 if first else 40), page, prompt=True)
 
 
+@pytest.mark.parametrize("D", [64, 128])
+def test_a_page_outside_the_pool_ends_with_its_item(spv, D):
+    """The second tile of rows of the first sequence begins its document late: it is done before the page outside the pool,
+    at the first's beginning, is asked for.  The items that its block goes on with have nothing to do with that page."""
+    B, T, ctx, page = 2500, 256, 4000, 16
+    gen = torch.Generator(device="cuda").manual_seed(54)
+    q = torch.randn(B, T, 1, D, generator=gen, device="cuda").bfloat16()
+    lens = torch.zeros(B, dtype=torch.int32, device="cuda")
+    lens[0] = ctx
+    pages = (ctx + T) // page
+    k, v = (torch.randn(pages + B * 16, page, 1, D, generator=gen, device="cuda").bfloat16() for _ in range(2))
+    table = torch.full((B, pages), -1, dtype=torch.int32, device="cuda")
+    table[0] = torch.arange(pages, device="cuda")
+    table[1:, :16] = pages + torch.arange((B - 1) * 16, device="cuda", dtype=torch.int32).reshape(B - 1, 16)
+    first = torch.zeros(B, T, dtype=torch.int32, device="cuda")
+    first[0, 128:] = ctx + 128
+    scores = spv.Scores(first=first)
+    want = spv.spv_prompt_attention(q, spv.KVCache(k, v), table, lens, scores, want_lse=True)
+    table[0, 1] = -1
+    got = spv.spv_prompt_attention(q, spv.KVCache(k, v), table, lens, scores, want_lse=True)
+    assert want["row_status"].sum() == 0 and got["row_status"][0] == 4 and got["row_status"][1:].sum() == 0
+    assert torch.isnan(got["out"][0, :128]).all()
+    assert torch.equal(got["out"][1:], want["out"][1:]) and torch.equal(got["lse"][1:], want["lse"][1:])
+
+
