@@ -1086,6 +1086,7 @@ __device__ void tiles_rows(const TilesParams &p, char *smem, TilesCtl<S> *ctl, u
     const uint32_t tm_o = ctl->tmem + quarter + 256 + group * 128;
     const ScoresView &v = p.sc;
     const bool moved = moved_slots(v);
+    const bool by_depth = !PAIR && p.parent && v.slopes && !v.slot_pos;  // the depths beside q are read in every tile
     int n = 0, item = 0;  // tiles of this group; items with tiles
     TileItem it;
     int k = 0;
@@ -1146,7 +1147,7 @@ __device__ void tiles_rows(const TilesParams &p, char *smem, TilesCtl<S> *ctl, u
                 ok = tiles_wait(ctl, &ctl->q_full[place], (item / S::Q_PLACES) & 1, err);
                 if (S::WIDEN) factor *= exp2f(-static_cast<float>(ctl->at.q_power[place * S::ROWS + r]));
             }
-            if (OF_ROW == 1) {
+            if (OF_ROW == 1 && !by_depth) {
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&ctl->q_empty[place]);
             }
@@ -1306,6 +1307,10 @@ __device__ void tiles_rows(const TilesParams &p, char *smem, TilesCtl<S> *ctl, u
             }
             if (s0 < s1) ok = ok && tiles_wait(ctl, &ctl->o_done[group * 2 + ((n - 1) & 1)], ((n - 1) >> 1) & 1, err);
             tc_fence_after();
+            if (OF_ROW == 1 && by_depth) {
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&ctl->q_empty[place]);
+            }
             any_bad |= *reinterpret_cast<volatile char *>(&ctl->bad[group][item % S::ITEMS]) != 0;
             ++item;
         }
@@ -1454,7 +1459,7 @@ __global__ void __launch_bounds__(TILES_THREADS, 1)
             mbar_init(&ctl->item_full[i], 1);
             mbar_init(&ctl->item_empty[i], TILES_TAKERS);
             mbar_init(&ctl->q_full[i], S::ROWS_WIDEN ? 256 : TILES_PREPARE);
-            mbar_init(&ctl->q_empty[i], 1 + 8);  // the products' end, and the row warps, who have read what lies beside q
+            mbar_init(&ctl->q_empty[i], 1 + 8);  // the products' end, and the row warps, when they need what lies beside q no more
             ctl->stop[i] = ctl->lost[i] = 0;
             for (int k = 0; k < S::ITEMS; ++k) ctl->bad[i][k] = 0;
         }

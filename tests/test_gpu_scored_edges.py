@@ -101,3 +101,15 @@ def test_a_page_outside_the_pool_ends_with_its_item(spv, D):
     assert torch.equal(got["out"][1:], want["out"][1:]) and torch.equal(got["lse"][1:], want["lse"][1:])
 
 
+# ------------------------------------------------------------------ trees of many short sequences
+@pytest.mark.parametrize("T,Hq,D", [(64, 6, 128), (64, 6, 64), (40, 8, 256), (20, 4, 256)])
+@pytest.mark.parametrize("seed", range(2))
+def test_every_short_sequence_has_its_own_tree(spv, T, Hq, D, seed):
+    """Items of a tile or two: the depths of the next items' trees are on their way while a row still needs its own."""
+    ctx = [(17 * b) % 40 for b in range(160)]
+    c = sr.Case(spv, 60 + seed, ctx, None, T, Hq, 2, D, 16, tree=True, slopes=True, cap=20.0, poison=False)
+    a, b = c.attend(), c.attend()
+    assert torch.equal(a["out"], b["out"]) and torch.equal(a["lse"], b["lse"])
+    c.check(a)
+
+
