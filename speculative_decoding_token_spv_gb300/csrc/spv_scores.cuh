@@ -199,8 +199,8 @@ __device__ __forceinline__ TokenView token_view(const ScoresView &v, const int32
         r.bits = (2ull << t) - 1ull;
         r.depth = t;
         if (v.last) {
-            const int n = __ldg(v.last + static_cast<int64_t>(b) * T + t) - s.ctx;
-            if (n > 0) r.bits |= n >= 64 ? ~0ull : (1ull << n) - 1ull;
+            const int end = __ldg(v.last + static_cast<int64_t>(b) * T + t);  // any value: compared before it is a difference
+            if (end > s.ctx) r.bits |= end - s.ctx >= 64 ? ~0ull : (1ull << (end - s.ctx)) - 1ull;
         }
         if (sliding && t >= v.window) r.bits &= ~((1ull << (t - v.window + 1)) - 1ull);
     }
@@ -208,8 +208,7 @@ __device__ __forceinline__ TokenView token_view(const ScoresView &v, const int32
     if (v.first) {
         const int f = __ldg(v.first + static_cast<int64_t>(b) * T + t);
         r.lo = max(r.lo, f);
-        const int n = f - s.ctx;
-        if (n > 0) r.bits = n >= 64 ? 0ull : r.bits & ~((1ull << n) - 1ull);
+        if (f > s.ctx) r.bits = f - s.ctx >= 64 ? 0ull : r.bits & ~((1ull << (f - s.ctx)) - 1ull);
     }
     return r;
 }

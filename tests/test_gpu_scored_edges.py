@@ -101,6 +101,32 @@ def test_a_page_outside_the_pool_ends_with_its_item(spv, D):
     assert torch.equal(got["out"][1:], want["out"][1:]) and torch.equal(got["lse"][1:], want["lse"][1:])
 
 
+# ------------------------------------------------------------------ masks near the ends of 32 bits
+LEAST, MOST = -2 ** 31, 2 ** 31 - 1
+
+
+@pytest.mark.parametrize("T,D", [(3, 64), (30, 64), (30, 256)])
+def test_documents_and_prefixes_at_the_ends_of_32_bits(spv, T, D):
+    """`last` at its least is no prefix, `first` at its least the sequence's beginning; at their most, all and nothing."""
+    ends = [LEAST, LEAST + 1, -1, 0, MOST]
+    last = [[ends[(t + b) % 5] for t in range(T)] for b in range(2)]
+    first = [[ends[(t + b) % 4] for t in range(T)] for b in range(2)]
+    first[1][T - 1] = MOST
+    c = sr.Case(spv, 55, [150, 70], None, T, 4, 2, D, 16, first=first, last=last)
+    c.check(c.attend())
+
+
+def test_weights_of_keys_of_documents_at_the_ends_of_32_bits(spv):
+    T = 4
+    c = sr.Case(spv, 56, [150, 70], None, T, 4, 2, 64, 16, first=[[LEAST, 0, 5, LEAST + 3]] * 2, last=[[LEAST, LEAST + 9, -1, MOST]] * 2)
+    lse, W = c.attention()[1].float().cuda(), 160
+    out = {"mass": torch.zeros(2, 2, W, device="cuda")}
+    got = spv.spv_attention_mass_scored(c.q.cuda(), lse, c.cache(), c.table.cuda(), c.i32(c.ctx), c.i32([T - 1] * 2), c.scores(), out=out)
+    want, bound = c.mass([list(range(T))] * 2, 1.0, torch.zeros(2, 2, W))
+    there = ~torch.isnan(want)
+    assert ((got["mass"].cpu().double() - want).abs() <= bound + 2.0 ** -24 * want.abs())[there].all()
+
+
 # ------------------------------------------------------------------ trees of many short sequences
 @pytest.mark.parametrize("T,Hq,D", [(64, 6, 128), (64, 6, 64), (40, 8, 256), (20, 4, 256)])
 @pytest.mark.parametrize("seed", range(2))
