@@ -204,7 +204,7 @@ __device__ __forceinline__ TokenView token_view(const ScoresView &v, const int32
         }
         if (sliding && t >= v.window) r.bits &= ~((1ull << (t - v.window + 1)) - 1ull);
     }
-    if (sliding) r.lo = s.ctx + r.depth - v.window + 1;
+    if (sliding) r.lo = max(0, s.ctx + r.depth - v.window + 1);  // (far below 0 a slot's distance to it would not fit 32 bits)
     if (v.first) {
         const int f = __ldg(v.first + static_cast<int64_t>(b) * T + t);
         r.lo = max(r.lo, f);

@@ -127,6 +127,16 @@ def test_weights_of_keys_of_documents_at_the_ends_of_32_bits(spv):
     assert ((got["mass"].cpu().double() - want).abs() <= bound + 2.0 ** -24 * want.abs())[there].all()
 
 
+@pytest.mark.parametrize("window", [MOST, MOST - 17, 2 ** 30])
+@pytest.mark.parametrize("T,Hq,D,kv", [(3, 4, 64, "bf16"), (60, 4, 64, "bf16"), (60, 4, 128, "e4m3"), (33, 8, 256, "bf16")])
+def test_trees_under_a_window_as_wide_as_32_bits(spv, T, Hq, D, kv, window):
+    """Nodes next to the root that stand far behind it: a window that reaches further than any slot takes nothing away."""
+    c = sr.Case(spv, 57, [64, 31, 500], None, T, Hq, 2, D, 16, "nhd", "bf16", kv, tree=True, window=window)
+    c.parent[0, 1:] = 0
+    c.seen = [c._seen(b) for b in range(c.B)]
+    c.check(c.attend())
+
+
 # ------------------------------------------------------------------ trees of many short sequences
 @pytest.mark.parametrize("T,Hq,D", [(64, 6, 128), (64, 6, 64), (40, 8, 256), (20, 4, 256)])
 @pytest.mark.parametrize("seed", range(2))
