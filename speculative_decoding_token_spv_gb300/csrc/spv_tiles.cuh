@@ -997,6 +997,10 @@ __device__ __noinline__ void tiles_finish(const TilesParams &p, bool again, int 
     }
 }
 
+// Whether a row's products become scores before the bias is taken off them: where the largest product is not the largest
+// score (no factor above 0), and where the bias, times 31 bits of distance, would not be finite in units of the products.
+__device__ __forceinline__ bool products_first(float factor, float slope) { return !(fabsf(slope) < factor * 0x1p90f); }
+
 // Cap, bias and a window over moved slots of a row's MINE scores of a tile whose
 // first key is jb: the true scores are then x f - off.  slope_in: the slope in
 // units of x.
@@ -1008,7 +1012,7 @@ __device__ __forceinline__ void tile_shape(const TilesParams &p, unsigned long l
     if (v.cap2 != 0.0f) {
         cap_pairs(v, x, *f);
         *f = 1.0f;
-    } else if (!(*f > 0.0f)) {  // the largest product has to be the largest score
+    } else if (products_first(*f, slope)) {
         const unsigned long long f2 = pack2(*f, *f);
 #pragma unroll
         for (int i = 0; i < MINE / 2; ++i) x[i] = mul2(x[i], f2);
@@ -1151,8 +1155,8 @@ __device__ void tiles_rows(const TilesParams &p, char *smem, TilesCtl<S> *ctl, u
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&ctl->q_empty[place]);
             }
-            const float slope_in = v.cap2 != 0.0f || !(factor > 0.0f) ? slope : slope / factor;
-            const bool shaped = v.cap2 != 0.0f || v.slopes || moved || __any_sync(0xffffffffu, !(factor > 0.0f));
+            const float slope_in = v.cap2 != 0.0f || products_first(factor, slope) ? slope : slope / factor;
+            const bool shaped = v.cap2 != 0.0f || v.slopes || moved || __any_sync(0xffffffffu, products_first(factor, slope));
             const bool works = __any_sync(0xffffffffu, there);
             // the slots that all rows of the warp see (votes of each tile took hundreds of cycles)
             const int all_lo = __reduce_max_sync(0xffffffffu, see.lo), all_hi = __reduce_min_sync(0xffffffffu, see.hi);

@@ -137,6 +137,26 @@ def test_trees_under_a_window_as_wide_as_32_bits(spv, T, Hq, D, kv, window):
     c.check(c.attend())
 
 
+# ------------------------------------------------------------------ rows of q next to nothing
+@pytest.mark.parametrize("prompt", [False, True])
+@pytest.mark.parametrize("moved", [False, True])
+@pytest.mark.parametrize("D,kv,size", [(128, "e4m3", 1e-33), (64, "e4m3", 1e-37), (256, "e4m3", 1e-33), (128, "bf16", 1e-33)])
+def test_a_bias_beside_rows_of_q_next_to_nothing(spv, moved, prompt, D, kv, size):
+    """All that tells keys apart is then the bias, and keys far away still count."""
+    c = sr.Case(spv, 58, [700, 90], None, 66 if prompt else 40, 4, 2, D, 16, "nhd", "bf16", kv, slopes=True, moved=moved)
+    c.slopes = torch.exp2(-6.0 - torch.arange(4.0))
+    c.q[:, ::2] *= size
+    c.check(c.attend(prompt=prompt))
+
+
+@pytest.mark.parametrize("T", [2, 40])
+@pytest.mark.parametrize("moved", [False, True])
+def test_a_bias_beside_a_scale_next_to_nothing(spv, moved, T):
+    c = sr.Case(spv, 59, [700, 90], None, T, 4, 2, 128, 16, slopes=True, moved=moved, scale=1e-39)
+    c.slopes = torch.exp2(-6.0 - torch.arange(4.0))
+    c.check(c.attend())
+
+
 # ------------------------------------------------------------------ trees of many short sequences
 @pytest.mark.parametrize("T,Hq,D", [(64, 6, 128), (64, 6, 64), (40, 8, 256), (20, 4, 256)])
 @pytest.mark.parametrize("seed", range(2))
