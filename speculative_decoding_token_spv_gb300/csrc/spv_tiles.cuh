@@ -102,7 +102,7 @@ struct alignas(16) TileItem {
     int b, row_tile, h, flags;
     int ctx, fresh, total, t0;
     int t1, lo0, hi0, lo1;
-    int hi1, seen, pad[2];
+    int hi1, pad[3];
 };
 enum TileFlags { ITEM_BAD = 1, ITEM_WHOLE = 2, ITEM_SECOND = 4, ITEM_END = 8 };  // ITEM_SECOND: a piece goes to the block's second place
 
@@ -112,6 +112,9 @@ template <typename S> struct TilesCtl {
     uint64_t full[S::STAGES], empty[S::STAGES], s_full[4], p_full[4], o_done[4], q_full[2], q_empty[2], spare;
     uint64_t q_raw[S::Q_PLACES];
     uint64_t raw_full[S::WIDEN ? 4 : 1][S::WIDEN ? S::RAW_STAGES : 1];  // of each loader warp's rows
+    // what makes a missing page of an item matter, of items in turn (they are worked out two ahead): the first slot that any of
+    // its rows sees, and the tiles that each tile of rows sees
+    int seen[4], spans[S::PAIR ? 4 : 1][4];
     char bad[2][S::ITEMS];                                       // a page id outside the pool, for each group of row warps
     int stop[2], lost[2];
     uint32_t tmem;
@@ -383,7 +386,11 @@ template <typename S> __device__ void tiles_items(const TilesParams &p, TileCurs
             it.ctx = c.s.ctx, it.fresh = c.s.fresh, it.total = c.s.total;
             it.t0 = tiles_first(c), it.t1 = tiles_last(c);
             it.lo0 = c.s.lo[0], it.hi0 = c.s.hi[0], it.lo1 = c.s.lo[1], it.hi1 = c.s.hi[1];
-            it.seen = c.s.seen;
+            ctl->seen[k & 3] = c.s.seen;
+            if (S::PAIR) {
+                int(&span)[4] = ctl->spans[S::PAIR ? k & 3 : 0];
+                span[0] = c.s.lo[0], span[1] = c.s.hi[0], span[2] = c.s.lo[1], span[3] = c.s.hi[1];
+            }
             mbar_arrive(&ctl->item_full[k & 1]);
             if (!end && !item_whole(c))
                 note_split(p, c, AttRows{c.b, c.h, c.row_tile * S::ROWS, min(S::ROWS, p.rows - c.row_tile * S::ROWS)}, begin, 0);
@@ -414,7 +421,6 @@ template <typename Ctl> __device__ __forceinline__ bool take_item(Ctl *ctl, int 
     it->ctx = same_in_warp(y.x), it->fresh = same_in_warp(y.y), it->total = same_in_warp(y.z), it->t0 = same_in_warp(y.w);
     it->t1 = same_in_warp(z.x), it->lo0 = same_in_warp(z.y), it->hi0 = same_in_warp(z.z), it->lo1 = same_in_warp(z.w);
     it->hi1 = same_in_warp(from[3].x);
-    it->seen = from[3].y;
     __syncwarp();
     if (lane == 0) mbar_arrive(&ctl->item_empty[k & 1]);
     return !(it->flags & ITEM_END);
@@ -492,14 +498,15 @@ __device__ void tiles_load(const TilesParams &p, char *smem, TilesCtl<S> *ctl, u
         const int t0 = it.t0, t1 = it.t1;
         if (t0 == t1) continue;
         const int32_t *table = p.c.table + static_cast<int64_t>(it.b) * p.c.max_pages;
-        const int flags = item, needed = it.seen >> p.c.page_shift;
+        const int flags = item;
         if (++item == S::ITEMS) item = 0;
         // The page of this slot, in this tile, is outside the pool: that matters from the first slot that is seen on, and to the
         // groups of row warps that see the tile.  (One that does not may be done with the item, and its flag another item's.)
         auto flag = [&](int slot, int tile) {
-            if (slot >> p.c.page_shift < needed) return;
-            if (!S::PAIR || (tile >= it.lo0 && tile < it.hi0)) *reinterpret_cast<volatile char *>(&ctl->bad[0][flags]) = 1;
-            if (S::PAIR && tile >= it.lo1 && tile < it.hi1) *reinterpret_cast<volatile char *>(&ctl->bad[1][flags]) = 1;
+            if (slot >> p.c.page_shift < ctl->seen[k & 3] >> p.c.page_shift) return;
+            const int(&span)[4] = ctl->spans[S::PAIR ? k & 3 : 0];
+            if (!S::PAIR || (tile >= span[0] && tile < span[1])) *reinterpret_cast<volatile char *>(&ctl->bad[0][flags]) = 1;
+            if (S::PAIR && tile >= span[2] && tile < span[3]) *reinterpret_cast<volatile char *>(&ctl->bad[1][flags]) = 1;
         };
         // With maps each warp asks the copy engine for its slots: a box a page (or what the warp has of a larger one), of 64
         // elements, or e4m3's whole rows; a lane each.  (A lane's takes 80 to 100 cycles: from one warp, 16 of a tile of K
@@ -1002,17 +1009,17 @@ __device__ __noinline__ void tiles_finish(const TilesParams &p, bool again, int 
 __device__ __forceinline__ bool products_first(float factor, float slope) { return !(fabsf(slope) < factor * 0x1p90f); }
 
 // Cap, bias and a window over moved slots of a row's MINE scores of a tile whose
-// first key is jb: the true scores are then x f - off.  slope_in: the slope in
-// units of x.
+// first key is jb: the true scores are then x f - off.  products: some row of the
+// warp has products_first, so all do; slope_in: the slope in units of x.
 template <int MINE, bool PAIR, typename Ctl>
 __device__ __forceinline__ void tile_shape(const TilesParams &p, unsigned long long (&x)[MINE / 2], float *f, float *off, int ctx, int total,
-                                           Ctl *ctl, int place, int jb, int own, int all_own, float slope, float slope_in, int origin, const int *positions)
+                                           Ctl *ctl, int place, int jb, int own, int all_own, bool products, float slope, float slope_in, int origin, const int *positions)
 {
     const ScoresView &v = p.sc;
     if (v.cap2 != 0.0f) {
         cap_pairs(v, x, *f);
         *f = 1.0f;
-    } else if (products_first(*f, slope)) {
+    } else if (products) {
         const unsigned long long f2 = pack2(*f, *f);
 #pragma unroll
         for (int i = 0; i < MINE / 2; ++i) x[i] = mul2(x[i], f2);
@@ -1155,8 +1162,8 @@ __device__ void tiles_rows(const TilesParams &p, char *smem, TilesCtl<S> *ctl, u
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&ctl->q_empty[place]);
             }
-            const float slope_in = v.cap2 != 0.0f || products_first(factor, slope) ? slope : slope / factor;
-            const bool shaped = v.cap2 != 0.0f || v.slopes || moved || __any_sync(0xffffffffu, products_first(factor, slope));
+            const bool products = __any_sync(0xffffffffu, products_first(factor, slope)), shaped = v.cap2 != 0.0f || v.slopes || moved || products;
+            const float slope_in = v.cap2 != 0.0f || products ? slope : slope / factor;
             const bool works = __any_sync(0xffffffffu, there);
             // the slots that all rows of the warp see (votes of each tile took hundreds of cycles)
             const int all_lo = __reduce_max_sync(0xffffffffu, see.lo), all_hi = __reduce_min_sync(0xffffffffu, see.hi);
@@ -1202,7 +1209,7 @@ __device__ void tiles_rows(const TilesParams &p, char *smem, TilesCtl<S> *ctl, u
                     }
                     // The true scores are x f - off.
                     float f = factor, off = 0.0f;
-                    if (shaped) tile_shape<MINE, PAIR>(p, x, &f, &off, it.ctx, it.total, ctl, place, jb, own, all_own, slope, slope_in, origin, ctl->at.positions[group] + of_tile);
+                    if (shaped) tile_shape<MINE, PAIR>(p, x, &f, &off, it.ctx, it.total, ctl, place, jb, own, all_own, products, slope, slope_in, origin, ctl->at.positions[group] + of_tile);
                     if (all_lo > jb || all_hi < jb + MINE) {
 #pragma unroll
                         for (int i = 0; i < MINE; i += 32) {
