@@ -328,11 +328,13 @@ template <int MODE, typename T, typename C> static cudaError_t launch_mode(const
         const int floats = tokens * norm_angles(p.half) + 2 * p.D + (MODE == NORM_ODD ? NORM_THREADS / width * p.D : 0);
         return launch_chained(kernel, dim3(p.B * ((p.T + tokens - 1) / tokens)), NORM_THREADS, floats * static_cast<int>(sizeof(float)), st, p, width);
     };
-    // More tokens a block once that still gives every SM three blocks: 4,800 tokens take 30 us by eight, 33 by four and 61 by one,
-    // 2,400 take 15 us by four and 29 by one.
-    const int64_t blocks = static_cast<int64_t>(p.B) * p.T / (3 * 152);
-    if (blocks >= 8) return go(norm_rope_kernel<MODE, 8, T, C>, 8);
-    if (blocks >= 4) return go(norm_rope_kernel<MODE, 4, T, C>, 4);
+    // More tokens a block once that still gives every SM three blocks: 16 x 300 tokens take 27 us by eight, 28 by four, 53 by one,
+    // 2,400 take 15 us by four and 29 by one.  A block's tokens are one sequence's, and places that it has no tokens for take as
+    // long: by eight only where that pads T by no more than a twentieth over four (300 x 17 tokens 36 us by eight, 34 by four,
+    // 1,300 x 3: 45 and 30), by four not for single tokens (4,096: 117 us by eight, 77 by four, 51 by one; 2,000 x 2: 62, 41, 49).
+    const int64_t blocks = static_cast<int64_t>(p.B) * p.T / (3 * 152), by_eight = (p.T + 7ll) / 8 * 8, by_four = (p.T + 3ll) / 4 * 4;
+    if (blocks >= 8 && 20 * by_eight <= 21 * by_four) return go(norm_rope_kernel<MODE, 8, T, C>, 8);
+    if (blocks >= 4 && p.T > 1) return go(norm_rope_kernel<MODE, 4, T, C>, 4);
     return go(norm_rope_kernel<MODE, 1, T, C>, 1);
 }
 template <typename T, typename C> static cudaError_t launch(const NormRopeParams &p, bool interleaved, cudaStream_t st)

@@ -169,3 +169,27 @@ def test_every_short_sequence_has_its_own_tree(spv, T, Hq, D, seed):
     c.check(a)
 
 
+
+
+# ------------------------------------------------------------------ norms and rotation of many short sequences
+@pytest.mark.parametrize("B,T,rotary,interleaved", [(4100, 1, 128, False), (2000, 2, 128, True), (1300, 3, 36, False), (950, 5, 64, False), (500, 9, 128, False)])
+def test_many_short_sequences_are_appended_as_each_by_itself(spv, B, T, rotary, interleaved):
+    """Whatever number of tokens a block takes: the same bits as from calls of a few sequences."""
+    Hq, Hkv, D, page = 6, 2, 128, 4
+    gen = torch.Generator(device="cuda").manual_seed(67)
+    draw = lambda *shape: torch.randn(*shape, generator=gen, device="cuda").bfloat16()  # noqa: E731
+    q, k, v = draw(B, T, Hq + 2 * Hkv, D).split([Hq, Hkv, Hkv], dim=2)
+    per = (T + 8) // page + 1
+    table = torch.randperm(B * per, generator=gen, device="cuda").to(torch.int32).reshape(B, per)
+    ctx = torch.randint(0, 8, (B,), generator=gen, device="cuda", dtype=torch.int32)
+    new = torch.randint(0, T + 1, (B,), generator=gen, device="cuda", dtype=torch.int32)
+    qw, kw = (1 + torch.rand(D, generator=gen, device="cuda") for _ in range(2))
+    freqs = spv.spv_rope_frequencies(rotary)
+    got = []
+    for step in (B, 100):
+        cache = spv.KVCache(*(torch.zeros(B * per, page, Hkv, D, dtype=torch.bfloat16, device="cuda") for _ in range(2)))
+        out = [spv.spv_norm_rope_append(q[i:i + step], k[i:i + step], v[i:i + step], cache, table[i:i + step], ctx[i:i + step], freqs, q_weight=qw,
+                                        k_weight=kw, interleaved=interleaved, new_lens=new[i:i + step]) for i in range(0, B, step)]
+        got.append((torch.cat([x["q"] for x in out]), torch.cat([x["row_status"] for x in out]), cache.k, cache.v))
+    assert all(torch.equal(a, b) for a, b in zip(*got))
+    assert (got[0][1] == 0).all() and (got[0][0][new > 0][:, 0] != 0).any(-1).all()
