@@ -193,3 +193,24 @@ def test_many_short_sequences_are_appended_as_each_by_itself(spv, B, T, rotary, 
         got.append((torch.cat([x["q"] for x in out]), torch.cat([x["row_status"] for x in out]), cache.k, cache.v))
     assert all(torch.equal(a, b) for a, b in zip(*got))
     assert (got[0][1] == 0).all() and (got[0][0][new > 0][:, 0] != 0).any(-1).all()
+
+
+# ------------------------------------------------------------------ few rows in tiles
+@pytest.mark.parametrize("D,width", [(256, 600), (128, 32000)])
+@pytest.mark.parametrize("T,Hq,tree,kw", [(1, 4, False, dict(cap=30.0)), (1, 16, False, dict(slopes=True)), (7, 4, True, dict(slopes=True)),
+                                          (5, 6, False, dict(window=2 ** 30, cap=30.0, first=[[3 * t for t in range(5)]] * 4)),
+                                          (8, 4, True, dict(moved=True, window=90, slopes=True))])
+def test_few_rows_of_a_table_with_room_for_large_caches(spv, D, width, T, Hq, tree, kw):
+    """How long the caches are only the page table's width tells the host: few rows go in tiles from 64 MB (heads of 256) or
+    1 GB (heads of 128) of room on, whatever lies in them."""
+    c = sr.Case(spv, 65, [300, 0, 41, 1000], [T, T, 0, T - T // 3], T, Hq, 2, D, 16, tree=tree, **kw)
+    assert 4.0 * D * 2 * 4 * 16 * width > (64e6 if D == 256 else 1e9)
+    table = torch.full((4, width), -1, dtype=torch.int32)
+    table[:, : c.table.shape[1]] = c.table
+    c.table = table
+    ws = spv.new_workspace(spv.spv_attention_workspace_bytes(4, T, Hq, 2, D), "cuda")
+    got = c.attend(workspace=ws)
+    c.check(got)
+    e = sr.Case(spv, 66, [300, 0, 41, 1000], [T, T, 0, T - T // 3], T, Hq, 2, D, 16, "nhd", "bf16", "e4m3", tree=tree, **kw)
+    e.table = torch.cat([e.table, torch.full((4, width - e.table.shape[1]), -1, dtype=torch.int32)], 1)
+    e.check(e.attend(workspace=ws))  # which stays where it was
