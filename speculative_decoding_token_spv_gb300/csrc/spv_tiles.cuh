@@ -1063,12 +1063,14 @@ __device__ __forceinline__ void tile_shape(const TilesParams &p, unsigned long l
                 }
                 x[i] = pack2(z[0], z[1]);
             }
-        } else if (all_own >= jb + MINE - 1) {  // no key is ahead: the distance is own - jb less the key's place
-            *off = slope * static_cast<float>(own - jb);
+        } else if (all_own >= jb + MINE - 1) {
+            // no key is ahead: the distance is that of the place behind the last key and the places before it (the nearest keys,
+            // which count most, so have the smallest terms and roundings)
+            *off = slope * static_cast<float>(own - (jb + MINE));
 #pragma unroll
             for (int i = 0; i < MINE / 2; ++i) {
                 const float2 y = unpair(x[i]);
-                x[i] = pack2(fmaf(s, static_cast<float>(2 * i), y.x), fmaf(s, static_cast<float>(2 * i + 1), y.y));
+                x[i] = pack2(fmaf(-s, static_cast<float>(MINE - 2 * i), y.x), fmaf(-s, static_cast<float>(MINE - 1 - 2 * i), y.y));
             }
         } else {
             const float far = static_cast<float>(own - jb);

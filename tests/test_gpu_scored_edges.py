@@ -157,6 +157,16 @@ def test_a_bias_beside_a_scale_next_to_nothing(spv, moved, T):
     c.check(c.attend())
 
 
+@pytest.mark.parametrize("T,Hq,D,kv", [(30, 2, 64, "f16"), (60, 2, 128, "bf16"), (60, 4, 128, "e4m3"), (40, 8, 256, "bf16"), (200, 4, 128, "bf16")])
+def test_the_bias_of_near_keys_has_their_size(spv, T, Hq, D, kv):
+    """Rows that see themselves or few keys before them, scores next to nothing: what is off is off by the bias of those
+    keys, not of a tile's."""
+    c = sr.Case(spv, 68, [191, 64, 500], None, T, Hq, 2, D, 16, "nhd", "f16" if kv == "f16" else "bf16", kv, window=1 + T % 7 // 3, slopes=True,
+                spread=0.01)
+    c.slopes = 1.0 - 0.11 * torch.rand(Hq, generator=c.gen)
+    c.check(c.attend(prompt=T > 64))
+
+
 # ------------------------------------------------------------------ trees of many short sequences
 @pytest.mark.parametrize("T,Hq,D", [(64, 6, 128), (64, 6, 64), (40, 8, 256), (20, 4, 256)])
 @pytest.mark.parametrize("seed", range(2))
