@@ -353,6 +353,8 @@ def spv_paged_attention_scored(q, cache: KVCache, page_table, ctx_lens, scores: 
                                stream=None) -> dict:
     """:func:`spv_paged_attention` with the scores and masks of ``scores`` (see
     spv_paged_attention_scored in spv.h)."""
+    if not isinstance(scores, Scores):
+        raise ValueError("scores must be a Scores")
     pack, dev, (_, _, Hkv, D) = cache.packed()
     shape, code, address = _queries(q, D, dev)
     B, T, Hq, _ = shape
@@ -383,6 +385,8 @@ def spv_prompt_attention(q, cache: KVCache, page_table, ctx_lens, scores: Scores
     """Attention of prompts: any number of new tokens q [B, T, q_heads, D] over
     the paged cache that holds their keys and values, causal, with the scores
     and masks of ``scores`` (see spv_prompt_attention in spv.h)."""
+    if scores is not None and not isinstance(scores, Scores):
+        raise ValueError("scores must be a Scores or None")
     pack, dev, (_, _, Hkv, D) = cache.packed()
     shape, code, address = _queries(q, D, dev)
     B, T, Hq, _ = shape
@@ -449,6 +453,8 @@ def spv_attention_mass_scored(q, lse, cache: KVCache, page_table, ctx_lens, acce
                               want_status: bool = True, stream=None) -> dict:
     """:func:`spv_attention_mass` after :func:`spv_paged_attention_scored`, with
     the same ``scores`` (see spv_attention_mass_scored in spv.h)."""
+    if not isinstance(scores, Scores):
+        raise ValueError("scores must be a Scores")
     return _mass("spv_attention_mass_scored", q, lse, cache, page_table, ctx_lens, accept_count, scores, nodes, new_lens, parent,
                  scale, decay, mass_in, out, want_status, stream)
 
