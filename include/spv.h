@@ -574,6 +574,9 @@ spv_status spv_attention_mass(const void *q, spv_dtype dtype, int B, int T, int 
  * slot_pos those of each slot and key head, the new tokens' among them
  * (spv_rope_append and spv_norm_rope_append write them, spv_kv_evict moves
  * them): after an eviction a slot is not a position.
+ * first and last are slots, any 32-bit value, one for all key heads.  An
+ * eviction moves each head's slots by itself, so that no slot marks a document
+ * or a prefix in what it has moved: they do not serve over such a cache.
  */
 typedef struct {
     float cap;               /* > 0, or 0: none */

@@ -20,15 +20,15 @@
 // = 128, bf16, 1.36 GB: 214 us, 6.3 TB/s, 94% of a copy's rate.  Two sequences of
 // 131,001 slots in e4m3, 32 rows a key head, 537 MB: 163 us, bound by issuing the
 // conversions and products, about 600 instructions for 16 keys.  One token of
-// one sequence of 777 slots: 10.2 us, the chain from lengths to page ids to keys,
-// the join's launch and its loads.
+// one sequence of 777 slots, captured: 10.0 us, the chain from lengths to page ids
+// to keys, the join's launch and its loads.
 //
 // The same kernel serves calls with scores and masks (spv_scores): these are
 // then made from the products, in powers of two, before the running maximum,
-// and masks are looked at in the slices where some row may not see a slot.  One
-// token of one sequence of 777 slots, capped, with its status: 14.6 us (12.6
-// plain); 64 sequences of up to 8,191 slots, 16 heads on 8 of 256, capped: 484 us
-// (441 plain), which spv_scored.cu gives to tiles.
+// and masks are looked at in the slices where some row may not see a slot.  That
+// one token, capped and captured: 11.7 us, with its status 13.0; 64 sequences of
+// up to 8,191 slots, 16 heads on 8 of 256, capped: 484 us (441 plain), which
+// spv_scored.cu gives to tiles.
 #pragma once
 
 #include "spv_scored.cuh"

@@ -30,13 +30,13 @@
 //     (small pages; a sequence's last tile of V, whose slots past the end become
 //     zero).  e4m3 lands as it is and is widened to f16 by the warp that asked for
 //     it.
-// Measured: a prompt of 8,192 tokens, 32 heads on 8 of 128, bf16: 546 us, 1.0
-// PFLOP/s of the 1.9 that the products alone could have: for a tile of 64 keys a
-// thread's scores take 1,500 cycles (loads 240, maximum 400, exponentials and
-// weights 450, waits for products 470).  Capped scores, bound by the polynomials:
-// 872 us.  Distance biases 600, documents of some 1,000 tokens 197, a window of
-// 1,024 187, heads of 64 470, 16 heads of 256 558 us.  e4m3 766 us (heads of 64
-// 633): widening K and V, four warps.  An item's beginning and end take some
+// Measured: a prompt of 8,192 tokens, 32 heads on 8 of 128, bf16, pages of 16: 538
+// us, 1.0 PFLOP/s of the 1.9 that the products alone could have: for a tile of 64
+// keys a thread's scores take 1,500 cycles (loads 240, maximum 400, exponentials
+// and weights 450, waits for products 470).  Capped scores, bound by the
+// polynomials: 883 us.  Distance biases 586, documents of 1,000 tokens 156, a
+// window of 1,024 182, heads of 64 474, 16 heads of 256 536 us.  e4m3 772 us (heads
+// of 64 640): widening K and V, four warps.  An item's beginning and end take some
 // 12,000 cycles: the outputs 4,600, agreeing on the end 2,000, the next rows'
 // intervals and q.
 //

@@ -291,8 +291,9 @@ class Scores:
     ``cap`` tanh(s / cap); ``slopes`` [q_heads] float32 times the distance off
     them; a ``window`` of positions; ``first`` [B, T] int32, the slot where a
     token's document begins; ``last`` [B, T] int32, the slot where the prefix
-    ends that a token sees whole; ``slot_pos`` [B, kv_heads, slots] int32, the
-    positions of the slots where an eviction has moved them."""
+    ends that a token sees whole (both mean nothing over slots that an eviction
+    has moved); ``slot_pos`` [B, kv_heads, slots] int32, the positions of the
+    slots where an eviction has moved them."""
     cap: float = 0.0
     slopes: torch.Tensor | None = None
     window: int = 0
